@@ -71,7 +71,8 @@ typedef enum {
     FA_ERR_INVALID_ARG = 1, /* null pointer, bad alignment, negative size, ... */
     FA_ERR_UNSUPPORTED = 2, /* valid request outside the supported sizes/types */
     FA_ERR_CUDA = 3,        /* a CUDA runtime call or launch failed */
-    FA_ERR_TIMEOUT = 4      /* a device-side bounded wait gave up */
+    FA_ERR_TIMEOUT = 4,     /* a device-side bounded wait gave up */
+    FA_ERR_NO_BLOCKS = 5    /* fa_cache_plan: the free list ran out (reported by fa_get_status) */
 } fa_status;
 
 typedef enum { FA_BF16 = 0, FA_FP32 = 1 } fa_dtype;
@@ -158,6 +159,116 @@ size_t fa_decode_workspace_size(int B, int H, int Nq, int Nk, int d, int num_spl
 fa_status fa_decode(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int Nq, int Nk,
                     int d, float scale, const int32_t* cache_len, int num_splits, fa_dtype dtype, void* workspace,
                     size_t ws_bytes, void* stream);
+
+/*
+ * Paged 8-bit key/value cache: three calls for one serving step.
+ * fa_cache_plan hands out blocks and says where each new token goes,
+ * fa_cache_append writes the new keys and values there, and fa_fwd_paged
+ * attends from the new tokens over everything cached. The host needs no
+ * length for any of them, so a step can be captured in a CUDA graph.
+ *
+ * The cache is two arrays [num_blocks, Hkv, block_size, d] of E4M3 numbers
+ * and two float32 arrays [num_blocks, Hkv] of scales: the cached value is the
+ * E4M3 number times the scale of its block and head. block_size is 16, 32,
+ * 64, 128 or 256. Request b's token p lives in row p % block_size of block
+ * block_table[b][p / block_size]; slot = block * block_size + row.
+ *
+ * Free blocks stand in a ring: free_blocks [num_blocks], free_state = {head,
+ * count}; the free ones are entries head, head + 1, ... (count of them,
+ * modulo num_blocks). An empty cache has free_blocks = 0 .. num_blocks - 1
+ * and free_state = {0, num_blocks}.
+ */
+
+/*
+ * Block tables and slot maps from the lengths. Request b has cache_len[b]
+ * tokens cached and brings new_len[b] more; new_len[b] < 0 releases it (its
+ * blocks go to the back of the ring, its length becomes 0).
+ *   new_len        in,  device, int32 [B]
+ *   cache_len      in,  device, int32 [B], tokens cached
+ *   cache_len_out  out, device, int32 [B], tokens cached with the new ones;
+ *                  may be cache_len itself
+ *   block_table    in/out, device, int32 [B, max_blocks]: entries of new
+ *                  blocks are written, all others stay
+ *   free_blocks    in/out, device, int32 [num_blocks]
+ *   free_state     in,  device, int32 [2]
+ *   free_state_out out, device, int32 [2]; may be free_state itself
+ *   cu_seqlens     out, device, int32 [B + 1]: offsets of the requests' new
+ *                  tokens in the packed batch
+ *   slots          out, device, int32 [total]: slot of each new token, -1 for
+ *                  tokens of a refused request and past the last request
+ *   total          size of slots, at least the sum of the positive new_len
+ *   workspace      256 bytes (the status word)
+ * Blocks are handed out in the order of the requests: one that needs blocks is
+ * refused when the needs up to and with its own exceed the free count (so
+ * every later one that needs blocks is refused as well). A refused request
+ * keeps its length and blocks, and fa_get_status returns FA_ERR_NO_BLOCKS.
+ * Blocks released by a call can be handed out from the next call on. Lengths
+ * that do not fit (negative or above max_blocks * block_size, together more
+ * than total, a table or ring entry that is no block) are refused on the
+ * device and reported as FA_ERR_INVALID_ARG.
+ * With separate outputs a call may be repeated with the same result.
+ * B <= 16384, total <= 2^30. Runs one kernel.
+ */
+fa_status fa_cache_plan(const int32_t* new_len, const int32_t* cache_len, int32_t* cache_len_out,
+                        int32_t* block_table, int32_t* free_blocks, const int32_t* free_state,
+                        int32_t* free_state_out, int32_t* cu_seqlens, int32_t* slots, int B, int max_blocks,
+                        int num_blocks, int block_size, int total, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Writes new keys and values into their slots. The new rows of one block and
+ * head share the scale 2^e, e = max(-126, ceil(log2(amax / 448))) over their
+ * finite values, or the block's scale so far (rounded up to a power of two)
+ * where that is larger; a run of new rows that starts in the block's row 0
+ * ignores the scale so far. Rows in front of the run are moved to the new
+ * scale (exact but for numbers below the smallest normal E4M3 number, 2^-6 of
+ * the new scale); rows behind it are left as they are. Values are divided by the scale
+ * (exactly) and rounded to E4M3 (nearest even); infinities become +-448 times
+ * the scale, NaN stays NaN.
+ *   k, v              in,  device, token-major [total, H, d] bf16
+ *   k_cache, v_cache  in/out, device, E4M3 [num_blocks, H, block_size, d]
+ *   k_scale, v_scale  in/out, device, float32 [num_blocks, H]
+ *   slots             in,  device, int32 [total]; tokens whose slot is not in
+ *                     [0, num_blocks * block_size) are skipped
+ * The tokens of one block stand next to each other in ascending order (as
+ * fa_cache_plan lists them); a block that appears in two places of the list,
+ * or one slot given twice, holds one of the two writes.
+ * d in {64, 128}. Runs one kernel; no workspace.
+ */
+fa_status fa_cache_append(const void* k, const void* v, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                          const int32_t* slots, int total, int H, int d, int num_blocks, int block_size,
+                          void* stream);
+
+/*
+ * Attention of a packed batch of new tokens over the paged cache, which holds
+ * the new tokens as well. Request b's tokens are cu_seqlens[b] ..
+ * cu_seqlens[b+1] - 1 and its cache holds cache_len[b] tokens, the new ones
+ * last. With causal = 1, new token i of n sees the first cache_len - n + i + 1
+ * tokens; with causal = 0 all of them. Query head h reads key head
+ * h / (Hq / Hkv).
+ *   q            in,  device, [total, Hq, d] bf16
+ *   k_cache, v_cache, k_scale, v_scale, block_table  in, device, as above
+ *                (block_table [B, max_blocks]; scales finite and >= 0)
+ *   o            out, device, [total, Hq, d] bf16
+ *   lse          out, device, float32 [Hq, total] (natural log; -inf for a
+ *                row that sees no token, whose o row is 0)
+ *   cu_seqlens   in,  device, int32 [B + 1]
+ *   cache_len    in,  device, int32 [B]
+ *   max_new      host, the most new tokens of a request, <= total
+ *   workspace    fa_fwd_paged_workspace_size bytes
+ * Rows of q outside every request are not read, and their o and lse are left
+ * as they are. What the cache holds behind a request's last token has no
+ * influence, NaN included. Offsets outside [0, total], requests of more than
+ * max_new tokens (cut to max_new), lengths above max_blocks * block_size (cut)
+ * and table entries that are no block are reported as FA_ERR_INVALID_ARG by
+ * fa_get_status; the rows they touch are then invalid. Hq a multiple of Hkv,
+ * d in {64, 128}, num_blocks * Hkv * block_size < 2^31.
+ */
+size_t fa_fwd_paged_workspace_size(int B, int Hq, int Hkv, int total, int max_new, int d);
+fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                       const float* v_scale, void* o, float* lse, const int32_t* cu_seqlens, const int32_t* cache_len,
+                       const int32_t* block_table, int B, int Hq, int Hkv, int total, int max_new, int max_blocks,
+                       int num_blocks, int block_size, int d, float scale, int causal, void* workspace,
+                       size_t ws_bytes, void* stream);
 
 /*
  * FP8 forward pass ("FlashAttention: making attention IO-aware", section
@@ -290,7 +401,8 @@ fa_status fa_bwd_noalloc_get_status(void* stream);
 /* Synchronises `stream`, then reads and clears the device status word of
  * `workspace` (of the fa_fwd or fa_bwd call that used it). Returns FA_OK or
  * FA_ERR_TIMEOUT (a device-side wait gave up; the outputs are then invalid),
- * or FA_ERR_CUDA if the stream reported an error. */
+ * FA_ERR_INVALID_ARG or FA_ERR_NO_BLOCKS where the entry point says so, or
+ * FA_ERR_CUDA if the stream reported an error. */
 fa_status fa_get_status(void* workspace, void* stream);
 
 /* Static, human-readable name of a status code. */
@@ -298,8 +410,8 @@ const char* fa_status_string(fa_status s);
 
 /* Number of kernels that the last successful call made by this host thread
  * to an entry point that launches work (fa_fwd, fa_bwd, their packed,
- * decoding, FP8 and dropout forms, fa_bwd_noalloc) launched, for accounting
- * in benchmarks. */
+ * decoding, FP8, paged and dropout forms, the cache calls, fa_bwd_noalloc)
+ * launched, for accounting in benchmarks. */
 int fa_last_launch_count(void);
 
 /* Profiling hook: for the following calls made by this host thread to the

@@ -11,6 +11,12 @@ from .binding import (  # noqa: F401
     forward_varlen,
     backward_varlen,
     decode,
+    PagedCache,
+    paged_cache,
+    cache_plan,
+    cache_append,
+    forward_paged,
+    fwd_paged_workspace_size,
     forward_fp8,
     forward_dropout,
     backward_dropout,

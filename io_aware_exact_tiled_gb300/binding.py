@@ -13,7 +13,7 @@ import ctypes
 import math
 import os
 import re
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -21,7 +21,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libfa.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "fa.h")
 
-FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT = range(5)
+FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT, FA_ERR_NO_BLOCKS = range(6)
 FA_BF16, FA_FP32 = 0, 1
 
 
@@ -68,6 +68,14 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fa_fwd_fp8_workspace_size.restype = sz
     lib.fa_fwd_fp8.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, f, i, vp, vp, vp, sz, vp]
     lib.fa_fwd_fp8.restype = i
+    lib.fa_cache_plan.argtypes = [vp] * 9 + [i] * 5 + [vp, sz, vp]
+    lib.fa_cache_plan.restype = i
+    lib.fa_cache_append.argtypes = [vp] * 7 + [i] * 5 + [vp]
+    lib.fa_cache_append.restype = i
+    lib.fa_fwd_paged_workspace_size.argtypes = [i] * 6
+    lib.fa_fwd_paged_workspace_size.restype = sz
+    lib.fa_fwd_paged.argtypes = [vp] * 10 + [i] * 9 + [f, i, vp, sz, vp]
+    lib.fa_fwd_paged.restype = i
     u64 = ctypes.c_ulonglong
     lib.fa_fwd_dropout.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, f, i, vp, f, u64, vp, sz, vp]
     lib.fa_fwd_dropout.restype = i
@@ -201,6 +209,10 @@ def decode_workspace_size(B, H, Nq, Nk, d, num_splits: int = 0) -> int:
 
 def fwd_fp8_workspace_size(B, H, N, d) -> int:
     return load().fa_fwd_fp8_workspace_size(B, H, N, d)
+
+
+def fwd_paged_workspace_size(B, Hq, Hkv, total, max_new, d) -> int:
+    return load().fa_fwd_paged_workspace_size(B, Hq, Hkv, total, max_new, d)
 
 
 def workspace(nbytes: int, device) -> torch.Tensor:
@@ -383,6 +395,129 @@ def decode(q, k_cache, v_cache, cache_len=None, scale: Optional[float] = None, n
     return o, L
 
 
+class PagedCache(NamedTuple):
+    """The buffers of a paged 8-bit cache and of the requests it serves, as
+    cache_plan, cache_append and forward_paged take them."""
+    k: torch.Tensor            # float8_e4m3fn [num_blocks, Hkv, block_size, d]
+    v: torch.Tensor
+    k_scale: torch.Tensor      # float32 [num_blocks, Hkv]
+    v_scale: torch.Tensor
+    block_table: torch.Tensor  # int32 [B, max_blocks]
+    cache_len: torch.Tensor    # int32 [B]
+    free_blocks: torch.Tensor  # int32 [num_blocks], a ring
+    free_state: torch.Tensor   # int32 [2]: its head and count
+
+
+def paged_cache(num_blocks: int, Hkv: int, block_size: int, d: int, B: int, max_blocks: int,
+                device="cuda") -> PagedCache:
+    """An empty cache of num_blocks blocks for up to B requests of at most
+    max_blocks blocks each. The other layers of a model have k, v, k_scale and
+    v_scale of their own and share the tables."""
+    i32 = dict(dtype=torch.int32, device=device)
+    k, v = (torch.zeros((num_blocks, Hkv, block_size, d), dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+            for _ in range(2))
+    ks, vs = (torch.zeros((num_blocks, Hkv), dtype=torch.float32, device=device) for _ in range(2))
+    return PagedCache(k, v, ks, vs, torch.full((B, max_blocks), -1, **i32), torch.zeros(B, **i32),
+                      torch.arange(num_blocks, **i32), torch.tensor([0, num_blocks], **i32))
+
+
+def cache_plan(new_len, cache_len, block_table, free_blocks, free_state, block_size: int,
+               total: Optional[int] = None, cache_len_out=None, free_state_out=None, cu_seqlens=None, slots=None,
+               ws=None, stream=None):
+    """cu_seqlens, slots = fa_cache_plan(...): blocks for each request's
+    new_len tokens (-1 releases the request) and their slots. new_len,
+    cache_len: int32 [B]; block_table: int32 [B, max_blocks]; free_blocks:
+    int32 [num_blocks]; free_state: int32 [2]. cache_len and free_state are
+    updated in place unless cache_len_out or free_state_out is given. total
+    (the size of the packed batch) is needed when slots is not passed in.
+    Returns (cu_seqlens int32 [B + 1], slots int32 [total])."""
+    lib = load()
+    _check_device(new_len)
+    dev, i32 = new_len.device, torch.int32
+    if new_len.dim() != 1 or block_table.dim() != 2 or free_blocks.dim() != 1:
+        raise ValueError("expected new_len [B], block_table [B, max_blocks] and free_blocks [num_blocks]")
+    B, max_blocks, num_blocks = new_len.numel(), block_table.shape[1], free_blocks.numel()
+    _in(new_len, (B,), i32, dev, "new_len")
+    _in(cache_len, (B,), i32, dev, "cache_len")
+    _in(block_table, (B, max_blocks), i32, dev, "block_table")
+    _in(free_blocks, (num_blocks,), i32, dev, "free_blocks")
+    _in(free_state, (2,), i32, dev, "free_state")
+    cache_len_out = cache_len if cache_len_out is None else _in(cache_len_out, (B,), i32, dev, "cache_len_out")
+    free_state_out = free_state if free_state_out is None else _in(free_state_out, (2,), i32, dev, "free_state_out")
+    if slots is None and total is None:
+        raise ValueError("pass slots, or total, the size of the packed batch")
+    total = slots.numel() if total is None else int(total)
+    cu = _out(cu_seqlens, (B + 1,), i32, dev, "cu_seqlens")
+    slots = _out(slots, (total,), i32, dev, "slots")
+    ws = _ws(ws, 256, dev)
+    rc = lib.fa_cache_plan(_ptr(new_len), _ptr(cache_len), _ptr(cache_len_out), _ptr(block_table), _ptr(free_blocks),
+                           _ptr(free_state), _ptr(free_state_out), _ptr(cu), _ptr(slots), B, max_blocks, num_blocks,
+                           int(block_size), total, _ptr(ws), _nbytes(ws), _stream_handle(stream))
+    if rc != FA_OK:
+        raise FAError(rc, "fa_cache_plan")
+    return cu, slots
+
+
+def _check_paged(k_cache, v_cache, k_scale, v_scale, device):
+    if k_cache.dim() != 4:
+        raise ValueError("the cache must be [num_blocks, Hkv, block_size, d]")
+    shape = tuple(k_cache.shape)
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _in(t, shape, torch.float8_e4m3fn, device, name)
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        _in(t, shape[:2], torch.float32, device, name)
+    return shape
+
+
+def cache_append(k, v, k_cache, v_cache, k_scale, v_scale, slots, stream=None):
+    """fa_cache_append(...): quantises k, v [total, Hkv, d] bf16 into the rows
+    `slots` (int32 [total], from cache_plan) of the caches (float8_e4m3fn
+    [num_blocks, Hkv, block_size, d]; scales float32 [num_blocks, Hkv])."""
+    lib = load()
+    _check_device(k)
+    num_blocks, H, bs, d = _check_paged(k_cache, v_cache, k_scale, v_scale, k.device)
+    if k.dim() != 3:
+        raise ValueError("k and v must be [total, Hkv, d]")
+    total = k.shape[0]
+    for t, name in ((k, "k"), (v, "v")):
+        _in(t, (total, H, d), torch.bfloat16, k.device, name)
+    _in(slots, (total,), torch.int32, k.device, "slots")
+    rc = lib.fa_cache_append(_ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                             _ptr(slots), total, H, d, num_blocks, bs, _stream_handle(stream))
+    if rc != FA_OK:
+        raise FAError(rc, "fa_cache_append")
+
+
+def forward_paged(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens, cache_len, block_table, max_new: int,
+                  scale: Optional[float] = None, causal: bool = True, out=None, lse=None, ws=None, stream=None):
+    """O, L = fa_fwd_paged(...): attention of the packed new tokens q
+    [total, Hq, d] bf16 over the paged cache, which holds them as well
+    (cache_len counts them). max_new: the most new tokens of a request.
+    Returns (o [total, Hq, d], lse fp32 [Hq, total])."""
+    lib = load()
+    _check_device(q)
+    num_blocks, Hkv, bs, d = _check_paged(k_cache, v_cache, k_scale, v_scale, q.device)
+    if q.dim() != 3 or block_table.dim() != 2 or cache_len.dim() != 1:
+        raise ValueError("expected q [total, Hq, d], block_table [B, max_blocks] and cache_len [B]")
+    total, Hq, _ = q.shape
+    B, max_blocks = block_table.shape
+    _in(q, (total, Hq, d), torch.bfloat16, q.device, "q")
+    _in(cu_seqlens, (B + 1,), torch.int32, q.device, "cu_seqlens")
+    _in(cache_len, (B,), torch.int32, q.device, "cache_len")
+    _in(block_table, (B, max_blocks), torch.int32, q.device, "block_table")
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    o = _out(out, q.shape, q.dtype, q.device, "out")
+    L = _out(lse, (Hq, total), torch.float32, q.device, "lse")
+    ws = _ws(ws, lambda: lib.fa_fwd_paged_workspace_size(B, Hq, Hkv, total, int(max_new), d), q.device)
+    rc = lib.fa_fwd_paged(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(o), _ptr(L),
+                          _ptr(cu_seqlens), _ptr(cache_len), _ptr(block_table), B, Hq, Hkv, total, int(max_new),
+                          max_blocks, num_blocks, bs, d, scale, int(bool(causal)), _ptr(ws), _nbytes(ws),
+                          _stream_handle(stream))
+    if rc != FA_OK:
+        raise FAError(rc, "fa_fwd_paged")
+    return o, L
+
+
 def backward(q, k, v, o, lse, do, scale: Optional[float] = None, causal: bool = False, blockmask=None,
              kv_len=None, dq=None, dk=None, dv=None, ws=None, stream=None):
     """dQ, dK, dV = fa_bwd(...). Returns (dq, dk, dv)."""
@@ -463,6 +598,10 @@ C_NAMES = {
     "fa_bwd_varlen_workspace_size": bwd_varlen_workspace_size,
     "fa_decode": decode,
     "fa_decode_workspace_size": decode_workspace_size,
+    "fa_cache_plan": cache_plan,
+    "fa_cache_append": cache_append,
+    "fa_fwd_paged": forward_paged,
+    "fa_fwd_paged_workspace_size": fwd_paged_workspace_size,
     "fa_fwd_fp8": forward_fp8,
     "fa_fwd_fp8_workspace_size": fwd_fp8_workspace_size,
     "fa_fwd_dropout": forward_dropout,

@@ -9,6 +9,7 @@
 #include "fa_decode.h"
 #include "fa_fp8.h"
 #include "fa_launch.h"
+#include "fa_paged.h"
 
 namespace {
 
@@ -501,6 +502,167 @@ fa_status fa_bwd(const void* q, const void* k, const void* v, const void* o, con
     return st;
 }
 
+// Block sizes of the paged cache: powers of two from 16 to 256.
+static bool paged_block_ok(int block_size) {
+    return block_size == 16 || block_size == 32 || block_size == 64 || block_size == 128 || block_size == 256;
+}
+
+fa_status fa_cache_plan(const int32_t* new_len, const int32_t* cache_len, int32_t* cache_len_out,
+                        int32_t* block_table, int32_t* free_blocks, const int32_t* free_state,
+                        int32_t* free_state_out, int32_t* cu_seqlens, int32_t* slots, int B, int max_blocks,
+                        int num_blocks, int block_size, int total, void* workspace, size_t ws_bytes, void* stream) {
+    if (!new_len || !cache_len || !cache_len_out || !block_table || !free_blocks || !free_state || !free_state_out ||
+        !cu_seqlens || (total > 0 && !slots) || !workspace)
+        return FA_ERR_INVALID_ARG;
+    if (B <= 0 || max_blocks <= 0 || num_blocks <= 0 || block_size <= 0 || total < 0) return FA_ERR_INVALID_ARG;
+    if (!paged_block_ok(block_size) || B > fa::kPlanMaxB || total > (1 << 30)) return FA_ERR_UNSUPPORTED;
+    if (static_cast<long long>(max_blocks) * block_size >= (1LL << 31) ||
+        static_cast<long long>(num_blocks) * block_size >= (1LL << 31))
+        return FA_ERR_UNSUPPORTED;
+    if (!aligned(new_len, 4) || !aligned(cache_len, 4) || !aligned(cache_len_out, 4) || !aligned(block_table, 4) ||
+        !aligned(free_blocks, 4) || !aligned(free_state, 4) || !aligned(free_state_out, 4) ||
+        !aligned(cu_seqlens, 4) || !aligned(slots, 4) || !aligned(workspace, 256))
+        return FA_ERR_INVALID_ARG;
+    if (ws_bytes < kStatusBytes) return FA_ERR_INVALID_ARG;
+    fa::PlanArgs a{};
+    a.new_len = new_len;
+    a.cache_len = cache_len;
+    a.cache_len_out = cache_len_out;
+    a.block_table = block_table;
+    a.free_blocks = free_blocks;
+    a.free_state = free_state;
+    a.free_state_out = free_state_out;
+    a.cu_seqlens = cu_seqlens;
+    a.slots = slots;
+    a.B = B;
+    a.max_blocks = max_blocks;
+    a.num_blocks = num_blocks;
+    a.block_size = block_size;
+    a.total = total;
+    a.status = static_cast<int*>(workspace);
+    int n = 0;
+    const fa_status st = map_cuda(fa::launch_cache_plan(a, static_cast<cudaStream_t>(stream), &n));
+    if (st == FA_OK) g_last_launches = n;
+    return st;
+}
+
+fa_status fa_cache_append(const void* k, const void* v, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                          const int32_t* slots, int total, int H, int d, int num_blocks, int block_size,
+                          void* stream) {
+    if (!k_cache || !v_cache || !k_scale || !v_scale) return FA_ERR_INVALID_ARG;
+    if (total < 0 || H <= 0 || d <= 0 || num_blocks <= 0 || block_size <= 0) return FA_ERR_INVALID_ARG;
+    if (total > 0 && (!k || !v || !slots)) return FA_ERR_INVALID_ARG;
+    if ((d != 64 && d != 128) || !paged_block_ok(block_size)) return FA_ERR_UNSUPPORTED;
+    if (static_cast<long long>(num_blocks) * H * block_size >= (1LL << 31) ||
+        static_cast<long long>(total) * H >= (1LL << 31))
+        return FA_ERR_UNSUPPORTED;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(slots, 4))
+        return FA_ERR_INVALID_ARG;
+    int n = 0;
+    if (total > 0) {
+        fa::AppendArgs a{};
+        a.k = k;
+        a.v = v;
+        a.k_cache = static_cast<uint8_t*>(k_cache);
+        a.v_cache = static_cast<uint8_t*>(v_cache);
+        a.k_scale = k_scale;
+        a.v_scale = v_scale;
+        a.slots = slots;
+        a.total = total;
+        a.H = H;
+        a.d = d;
+        a.num_blocks = num_blocks;
+        a.block_size = block_size;
+        const fa_status st = map_cuda(fa::launch_cache_append(a, static_cast<cudaStream_t>(stream), &n));
+        if (st != FA_OK) return st;
+    }
+    g_last_launches = n;
+    return FA_OK;
+}
+
+// Workspace of fa_fwd_paged: the status word and the units' counters (zeroed
+// together), then the partial maxima, sums and outputs of the CTAs.
+static size_t paged_zeroed_bytes(int B, int Hq, int Hkv, int total, int max_new) {
+    return kStatusBytes + align256(static_cast<size_t>(fa::paged_max_units(B, Hq, Hkv, total, max_new)) * sizeof(int));
+}
+
+size_t fa_fwd_paged_workspace_size(int B, int Hq, int Hkv, int total, int max_new, int d) {
+    if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || total < 0 || max_new < 0 || d <= 0) return 0;
+    const size_t rows = 2 * static_cast<size_t>(fa::kPagedCtas) * fa::kPagedMaxRows;
+    return paged_zeroed_bytes(B, Hq, Hkv, total, max_new) + 2 * align256(rows * sizeof(float)) +
+           align256(rows * d * sizeof(float));
+}
+
+fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                       const float* v_scale, void* o, float* lse, const int32_t* cu_seqlens, const int32_t* cache_len,
+                       const int32_t* block_table, int B, int Hq, int Hkv, int total, int max_new, int max_blocks,
+                       int num_blocks, int block_size, int d, float scale, int causal, void* workspace,
+                       size_t ws_bytes, void* stream) {
+    if (!k_cache || !v_cache || !k_scale || !v_scale || !cu_seqlens || !cache_len || !block_table || !workspace)
+        return FA_ERR_INVALID_ARG;
+    if (total > 0 && (!q || !o || !lse)) return FA_ERR_INVALID_ARG;
+    if (B <= 0 || Hq <= 0 || Hkv <= 0 || total < 0 || max_new < 0 || max_new > total || max_blocks <= 0 ||
+        num_blocks <= 0 || block_size <= 0 || d <= 0)
+        return FA_ERR_INVALID_ARG;
+    if (Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
+    if (causal != 0 && causal != 1) return FA_ERR_INVALID_ARG;
+    if (!(scale > 0.f) || !isfinite(scale)) return FA_ERR_INVALID_ARG;
+    if ((d != 64 && d != 128) || !paged_block_ok(block_size)) return FA_ERR_UNSUPPORTED;
+    if (B > 65535 || Hq > 65535 || static_cast<long long>(total) * Hq >= (1LL << 31) ||
+        static_cast<long long>(max_blocks) * block_size >= (1LL << 31) ||
+        static_cast<long long>(num_blocks) * Hkv * block_size >= (1LL << 31) ||
+        fa::paged_max_units(B, Hq, Hkv, total, max_new) >= (1LL << 30))
+        return FA_ERR_UNSUPPORTED;
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
+        !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(cu_seqlens, 4) || !aligned(cache_len, 4) ||
+        !aligned(block_table, 4) || !aligned(workspace, 256))
+        return FA_ERR_INVALID_ARG;
+    if (ws_bytes < fa_fwd_paged_workspace_size(B, Hq, Hkv, total, max_new, d)) return FA_ERR_INVALID_ARG;
+    const size_t rows = 2 * static_cast<size_t>(fa::kPagedCtas) * fa::kPagedMaxRows;
+    const size_t zeroed = paged_zeroed_bytes(B, Hq, Hkv, total, max_new);
+    char* ws = static_cast<char*>(workspace);
+    fa::PagedArgs a{};
+    a.q = q;
+    a.k_cache = static_cast<const uint8_t*>(k_cache);
+    a.v_cache = static_cast<const uint8_t*>(v_cache);
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.o = o;
+    a.lse = lse;
+    a.cu_seqlens = cu_seqlens;
+    a.cache_len = cache_len;
+    a.block_table = block_table;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.total = total;
+    a.max_new = max_new;
+    a.max_blocks = max_blocks;
+    a.num_blocks = num_blocks;
+    a.block_size = block_size;
+    a.d = d;
+    a.scale = scale;
+    a.causal = causal;
+    a.status = reinterpret_cast<int*>(ws);
+    a.counters = reinterpret_cast<int*>(ws + kStatusBytes);
+    a.max_units = static_cast<int>(fa::paged_max_units(B, Hq, Hkv, total, max_new));
+    a.pm = reinterpret_cast<float*>(ws + zeroed);
+    a.pl = reinterpret_cast<float*>(ws + zeroed + align256(rows * sizeof(float)));
+    a.po = reinterpret_cast<float*>(ws + zeroed + 2 * align256(rows * sizeof(float)));
+    a.ev_begin = g_ev_begin;
+    a.ev_end = g_ev_end;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (cudaMemsetAsync(ws, 0, zeroed, s) != cudaSuccess) return FA_ERR_CUDA;
+    int n = 0;
+    if (total > 0 && max_new > 0) {
+        const fa_status st = map_cuda(fa::launch_fwd_paged(a, s, &n));
+        if (st != FA_OK) return st;
+    }
+    g_last_launches = n;
+    return FA_OK;
+}
+
 fa_status fa_get_status(void* workspace, void* stream) {
     if (!workspace) return FA_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -511,6 +673,7 @@ fa_status fa_get_status(void* workspace, void* stream) {
     if (cudaMemset(workspace, 0, sizeof(int)) != cudaSuccess) return FA_ERR_CUDA;
     if ((word & 0xFF) == FA_ERR_TIMEOUT) return FA_ERR_TIMEOUT;
     if ((word & 0xFF) == FA_ERR_INVALID_ARG) return FA_ERR_INVALID_ARG;
+    if ((word & 0xFF) == FA_ERR_NO_BLOCKS) return FA_ERR_NO_BLOCKS;
     return FA_ERR_CUDA;
 }
 
@@ -521,6 +684,7 @@ const char* fa_status_string(fa_status s) {
         case FA_ERR_UNSUPPORTED: return "FA_ERR_UNSUPPORTED: unsupported size or type";
         case FA_ERR_CUDA: return "FA_ERR_CUDA: CUDA runtime or launch error";
         case FA_ERR_TIMEOUT: return "FA_ERR_TIMEOUT: a device-side wait gave up";
+        case FA_ERR_NO_BLOCKS: return "FA_ERR_NO_BLOCKS: the free list ran out";
     }
     return "unknown fa_status";
 }

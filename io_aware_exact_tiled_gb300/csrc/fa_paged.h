@@ -1,0 +1,76 @@
+// Internal interface of the paged 8-bit key/value cache: the block plan and
+// the quantising append (fa_cache.cu) and attention over the cache
+// (fa_paged.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace fa {
+
+// Status code a kernel leaves when the free list ran out (FA_ERR_NO_BLOCKS).
+enum : int { FA_DEV_NO_BLOCKS = 5 };
+
+constexpr int kPlanMaxB = 16384;      // requests of one plan (offsets of all of them sit in shared memory)
+constexpr int kPagedCtas = 152;       // one persistent CTA per SM
+constexpr int kPagedMaxRows = 32;     // query rows of the largest row tile of the split-key kernel
+
+struct PlanArgs {
+    const int32_t *new_len, *cache_len;
+    int32_t* cache_len_out;
+    int32_t* block_table;  // [B][max_blocks]
+    int32_t* free_blocks;  // ring [num_blocks]
+    const int32_t* free_state;  // {head, count}
+    int32_t* free_state_out;
+    int32_t* cu_seqlens;  // [B + 1]
+    int32_t* slots;       // [total]
+    int B, max_blocks, num_blocks, block_size, total;
+    int* status;
+};
+
+struct AppendArgs {
+    const void *k, *v;  // [total][H][d] bf16
+    uint8_t *k_cache, *v_cache;  // [num_blocks][H][block_size][d] E4M3
+    float *k_scale, *v_scale;    // [num_blocks][H]
+    const int32_t* slots;        // [total]
+    int total, H, d, num_blocks, block_size;
+};
+
+struct PagedArgs {
+    const void* q;  // [total][Hq][d] bf16
+    const uint8_t *k_cache, *v_cache;
+    const float *k_scale, *v_scale;
+    void* o;     // [total][Hq][d] bf16
+    float* lse;  // [Hq][total]
+    const int32_t *cu_seqlens, *cache_len, *block_table;
+    int B, Hq, Hkv, total, max_new, max_blocks, num_blocks, block_size, d;
+    float scale;
+    int causal;
+    // workspace
+    int* status;
+    int* counters;     // [max_units] finished pieces of each unit, zero at the start
+    int max_units;
+    float *pm, *pl;    // [2 * kPagedCtas][kPagedMaxRows]
+    float* po;         // [2 * kPagedCtas][kPagedMaxRows][d]
+    cudaEvent_t ev_begin, ev_end;  // optional, recorded around the attention kernel
+};
+
+// Rows of the split-key kernel's row tile for requests of at most max_new
+// new tokens and `group` query heads per key head.
+inline int paged_row_tile(int max_new, int group) {
+    const long long rows = static_cast<long long>(max_new) * group;
+    return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+}
+
+// Units (row tile and key head of a request) that B requests of together
+// `total` tokens can have.
+inline long long paged_max_units(int B, int Hq, int Hkv, int total, int max_new) {
+    const long long group = Hq / Hkv, rt = paged_row_tile(max_new, static_cast<int>(group));
+    return Hkv * (B + total * group / rt);
+}
+
+cudaError_t launch_cache_plan(const PlanArgs& a, cudaStream_t stream, int* nlaunch);
+cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t stream, int* nlaunch);
+cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t stream, int* nlaunch);
+
+}  // namespace fa
