@@ -581,17 +581,34 @@ fa_status fa_cache_append(const void* k, const void* v, void* k_cache, void* v_c
     return FA_OK;
 }
 
-// Workspace of fa_fwd_paged: the status word and the units' counters (zeroed
-// together), then the partial maxima, sums and outputs of the CTAs.
-static size_t paged_zeroed_bytes(int B, int Hq, int Hkv, int total, int max_new) {
-    return kStatusBytes + align256(static_cast<size_t>(fa::paged_max_units(B, Hq, Hkv, total, max_new)) * sizeof(int));
+// Workspace of fa_fwd_paged: the status word and the counters of both kernels
+// (zeroed together), then the partial maxima, sums and outputs of the CTAs.
+struct PagedWs {
+    size_t counters, tile_counters, zeroed;  // offsets; bytes to zero
+    size_t pm, pl, po, tile_pm, tile_pl, tile_po, bytes;
+};
+
+static PagedWs paged_ws(int B, int Hq, int Hkv, int total, int max_new, int d) {
+    PagedWs w;
+    const size_t rows = 2 * static_cast<size_t>(fa::kPagedCtas) * fa::kPagedMaxRows;
+    const size_t units = static_cast<size_t>(fa::paged_max_tile_units(B, Hq, Hkv, total, max_new));
+    const size_t tile_rows = units ? 2 * static_cast<size_t>(fa::kPagedCtas) * fa::kPagedTileRows : 0;
+    w.counters = kStatusBytes;
+    w.tile_counters = w.counters + align256(static_cast<size_t>(B) * Hkv * sizeof(int));
+    w.zeroed = w.tile_counters + align256(2 * units * sizeof(int));
+    w.pm = w.zeroed;
+    w.pl = w.pm + align256(rows * sizeof(float));
+    w.po = w.pl + align256(rows * sizeof(float));
+    w.tile_pm = w.po + align256(rows * d * sizeof(float));
+    w.tile_pl = w.tile_pm + align256(tile_rows * sizeof(float));
+    w.tile_po = w.tile_pl + align256(tile_rows * sizeof(float));
+    w.bytes = w.tile_po + align256(tile_rows * d * sizeof(float));
+    return w;
 }
 
 size_t fa_fwd_paged_workspace_size(int B, int Hq, int Hkv, int total, int max_new, int d) {
     if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || total < 0 || max_new < 0 || d <= 0) return 0;
-    const size_t rows = 2 * static_cast<size_t>(fa::kPagedCtas) * fa::kPagedMaxRows;
-    return paged_zeroed_bytes(B, Hq, Hkv, total, max_new) + 2 * align256(rows * sizeof(float)) +
-           align256(rows * d * sizeof(float));
+    return paged_ws(B, Hq, Hkv, total, max_new, d).bytes;
 }
 
 fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
@@ -612,15 +629,15 @@ fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
     if (B > 65535 || Hq > 65535 || static_cast<long long>(total) * Hq >= (1LL << 31) ||
         static_cast<long long>(max_blocks) * block_size >= (1LL << 31) ||
         static_cast<long long>(num_blocks) * Hkv * block_size >= (1LL << 31) ||
-        fa::paged_max_units(B, Hq, Hkv, total, max_new) >= (1LL << 30))
+        static_cast<long long>(B) * Hkv >= (1LL << 30) ||
+        fa::paged_max_tile_units(B, Hq, Hkv, total, max_new) >= (1LL << 29))
         return FA_ERR_UNSUPPORTED;
     if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
         !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(cu_seqlens, 4) || !aligned(cache_len, 4) ||
         !aligned(block_table, 4) || !aligned(workspace, 256))
         return FA_ERR_INVALID_ARG;
-    if (ws_bytes < fa_fwd_paged_workspace_size(B, Hq, Hkv, total, max_new, d)) return FA_ERR_INVALID_ARG;
-    const size_t rows = 2 * static_cast<size_t>(fa::kPagedCtas) * fa::kPagedMaxRows;
-    const size_t zeroed = paged_zeroed_bytes(B, Hq, Hkv, total, max_new);
+    const PagedWs w = paged_ws(B, Hq, Hkv, total, max_new, d);
+    if (ws_bytes < w.bytes) return FA_ERR_INVALID_ARG;
     char* ws = static_cast<char*>(workspace);
     fa::PagedArgs a{};
     a.q = q;
@@ -645,15 +662,19 @@ fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
     a.scale = scale;
     a.causal = causal;
     a.status = reinterpret_cast<int*>(ws);
-    a.counters = reinterpret_cast<int*>(ws + kStatusBytes);
-    a.max_units = static_cast<int>(fa::paged_max_units(B, Hq, Hkv, total, max_new));
-    a.pm = reinterpret_cast<float*>(ws + zeroed);
-    a.pl = reinterpret_cast<float*>(ws + zeroed + align256(rows * sizeof(float)));
-    a.po = reinterpret_cast<float*>(ws + zeroed + 2 * align256(rows * sizeof(float)));
+    a.counters = reinterpret_cast<int*>(ws + w.counters);
+    a.pm = reinterpret_cast<float*>(ws + w.pm);
+    a.pl = reinterpret_cast<float*>(ws + w.pl);
+    a.po = reinterpret_cast<float*>(ws + w.po);
+    a.tile_counters = reinterpret_cast<int*>(ws + w.tile_counters);
+    a.max_tile_units = static_cast<int>(fa::paged_max_tile_units(B, Hq, Hkv, total, max_new));
+    a.tile_pm = reinterpret_cast<float*>(ws + w.tile_pm);
+    a.tile_pl = reinterpret_cast<float*>(ws + w.tile_pl);
+    a.tile_po = reinterpret_cast<float*>(ws + w.tile_po);
     a.ev_begin = g_ev_begin;
     a.ev_end = g_ev_end;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (cudaMemsetAsync(ws, 0, zeroed, s) != cudaSuccess) return FA_ERR_CUDA;
+    if (cudaMemsetAsync(ws, 0, w.zeroed, s) != cudaSuccess) return FA_ERR_CUDA;
     int n = 0;
     if (total > 0 && max_new > 0) {
         const fa_status st = map_cuda(fa::launch_fwd_paged(a, s, &n));

@@ -13,8 +13,9 @@
 // wait for the block table in front of each copy.
 //
 // Design:
-//   * Work is counted in chunks of 32 keys. A unit is (request, key head, row
-//     tile of RT rows); the units' chunks form one line that is cut into
+//   * Work is counted in chunks of 32 keys. A unit is (request, key head), with
+//     at most RT = 8, 16 or 32 query rows (fa_paged_tile.cu takes requests of
+//     more); the units' chunks form one line that is cut into
 //     equal quotas, one for each persistent CTA, so ragged lengths balance by
 //     themselves and one long request spreads over the whole GPU. A unit that
 //     was cut leaves partial (m, l, O) in the workspace and the CTA that
@@ -87,7 +88,6 @@ struct PagedParams {
     float scale_log2;
     int causal;
     int *status, *counters;
-    int max_units;  // counters
     float *pm, *pl, *po;
 };
 
@@ -141,25 +141,21 @@ __device__ __forceinline__ uint32_t pg_off(int j, int c) {
 
 // One unit's piece of a CTA's quota.
 struct PgSeg {
-    int b, unit;        // request; unit within the request: hk * ntile + rt
-    int hk, rt;
-    int n, len, tok0;   // new tokens, length, first token
-    int ntile;          // row tiles of the request
-    int nchunk;         // chunks of each of the request's units
+    int b, hk;          // request, key head
+    int n, len, tok0;   // new tokens (0: none, or the row-tile kernel's), length, first token
+    int nchunk;         // chunks of each of the request's units; 0 without rows
     int c0, c1;         // this piece's chunks
     long long line0;    // position of the unit's first chunk on the line of all chunks
-    int unit0;          // units of the earlier requests
 };
 
 // Loads request b (sizes clamped to what the tables can hold).
-template <int RT>
 __device__ __forceinline__ void pg_request(const PagedParams& p, int b, PgSeg& s) {
     const int t0 = min(max(p.cu_seqlens[b], 0), p.total), t1 = min(max(p.cu_seqlens[b + 1], t0), p.total);
     s.tok0 = t0;
     s.n = min(t1 - t0, p.max_new);
+    if (static_cast<long long>(s.n) * p.G > kPagedMaxRows) s.n = 0;
     s.len = min(max(p.cache_len[b], 0), p.max_blocks << p.bs_log2);
-    s.ntile = static_cast<int>((static_cast<long long>(s.n) * p.G + RT - 1) / RT);
-    s.nchunk = max(1, (s.len + kPgChunk - 1) / kPgChunk);
+    s.nchunk = s.n > 0 ? max(1, (s.len + kPgChunk - 1) / kPgChunk) : 0;
 }
 
 template <int D, int NT, bool B16>
@@ -170,8 +166,8 @@ __global__ void __launch_bounds__(256, 1)
     constexpr int RT = C::RT;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    __shared__ long long scan_w[kPgWarps], scan_u[kPgWarps];
-    __shared__ int start_b, start_units, last_s;
+    __shared__ long long scan_w[kPgWarps];
+    __shared__ int start_b, last_s;
     __shared__ long long start_line;
     __shared__ int nan_seen, abort_s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
@@ -179,31 +175,23 @@ __global__ void __launch_bounds__(256, 1)
     // ---- the line of chunks: total length, and the request at this CTA's start
     const int per = (p.B + 255) / 256;
     const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-    long long mw = 0, mu = 0;
+    long long mw = 0;
     bool bad = false;
     for (int b = b0; b < b1; ++b) {
         PgSeg s;
-        pg_request<RT>(p, b, s);
-        const long long u = static_cast<long long>(s.ntile) * p.Hkv;
-        mu += u;
-        mw += u * s.nchunk;
+        pg_request(p, b, s);
+        mw += static_cast<long long>(p.Hkv) * s.nchunk;
         const int raw = p.cu_seqlens[b], nxt = p.cu_seqlens[b + 1], len = p.cache_len[b];
         bad |= raw < 0 || nxt < raw || nxt > p.total || nxt - raw > p.max_new || len != s.len;
     }
     if (bad && blockIdx.x == 0) atomicCAS(p.status, 0, FA_DEV_INVALID | (90 << 8));
-    long long iw = mw, iu = mu;
+    long long iw = mw;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const long long a = __shfl_up_sync(0xffffffffu, iw, off), c = __shfl_up_sync(0xffffffffu, iu, off);
-        if (lane >= off) {
-            iw += a;
-            iu += c;
-        }
+        const long long a = __shfl_up_sync(0xffffffffu, iw, off);
+        if (lane >= off) iw += a;
     }
-    if (lane == 31) {
-        scan_w[warp] = iw;
-        scan_u[warp] = iu;
-    }
+    if (lane == 31) scan_w[warp] = iw;
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::BAR_OFF) + warp * C::STAGES;
     if (tid == 0) {
         abort_s = 0;
@@ -214,19 +202,10 @@ __global__ void __launch_bounds__(256, 1)
     int* first_nan = reinterpret_cast<int*>(sm + C::NAN_OFF);
     for (int i = tid; i < D; i += 256) first_nan[i] = INT_MAX;
     __syncthreads();
-    long long W = 0, U = 0, bw = 0, bu = 0;
+    long long W = 0, bw = 0;
     for (int w = 0; w < kPgWarps; ++w) {
-        if (w < warp) {
-            bw += scan_w[w];
-            bu += scan_u[w];
-        }
+        if (w < warp) bw += scan_w[w];
         W += scan_w[w];
-        U += scan_u[w];
-    }
-    // offsets that overlap (more rows than total): nothing is computed
-    if (U > p.max_units) {
-        if (tid == 0) atomicCAS(p.status, 0, FA_DEV_INVALID | (93 << 8));
-        return;
     }
     // equal quotas, at least one chunk for each warp
     long long quota = (W + gridDim.x - 1) / gridDim.x;
@@ -234,50 +213,42 @@ __global__ void __launch_bounds__(256, 1)
     const long long x0 = quota * blockIdx.x, x1 = min(x0 + quota, W);
     if (x0 >= x1) return;  // uniform over the CTA
     bw += iw - mw;
-    bu += iu - mu;
     if (x0 >= bw && x0 < bw + mw) {
         for (int b = b0; b < b1; ++b) {
             PgSeg s;
-            pg_request<RT>(p, b, s);
-            const long long u = static_cast<long long>(s.ntile) * p.Hkv, w = u * s.nchunk;
+            pg_request(p, b, s);
+            const long long w = static_cast<long long>(p.Hkv) * s.nchunk;
             if (x0 < bw + w) {
                 start_b = b;
                 start_line = bw;
-                start_units = static_cast<int>(bu);
                 break;
             }
             bw += w;
-            bu += u;
         }
     }
     __syncthreads();
 
-    // the piece that starts at position x of the line, given a request at or before it
-    long long seg_line = start_line;  // where the current request starts
+    // the piece that starts at position x of the line, given a request at or
+    // before it (which starts at rline)
     auto place = [&](PgSeg& s, long long& rline, long long x) {
-        // advance to the request that holds x (requests without rows take no room)
         for (;;) {
-            const long long w = static_cast<long long>(s.ntile) * p.Hkv * s.nchunk;
+            const long long w = static_cast<long long>(p.Hkv) * s.nchunk;
             if (x < rline + w) break;
             rline += w;
-            s.unit0 += s.ntile * p.Hkv;
             ++s.b;
-            pg_request<RT>(p, s.b, s);
+            pg_request(p, s.b, s);
         }
         const long long r = x - rline;
-        s.unit = static_cast<int>(r / s.nchunk);
-        s.c0 = static_cast<int>(r - static_cast<long long>(s.unit) * s.nchunk);
+        s.hk = static_cast<int>(r / s.nchunk);
+        s.c0 = static_cast<int>(r - static_cast<long long>(s.hk) * s.nchunk);
         s.line0 = x - s.c0;
         s.c1 = static_cast<int>(min(static_cast<long long>(s.nchunk), x1 - s.line0));
-        s.hk = s.unit / s.ntile;
-        s.rt = s.unit - s.hk * s.ntile;
     };
     PgSeg cs, is;  // pieces being consumed and being requested
-    long long crl = seg_line, irl = seg_line;
+    long long crl = start_line, irl = start_line;
     cs.b = is.b = start_b;
-    cs.unit0 = is.unit0 = start_units;
-    pg_request<RT>(p, cs.b, cs);
-    pg_request<RT>(p, is.b, is);
+    pg_request(p, cs.b, cs);
+    pg_request(p, is.b, is);
     place(cs, crl, x0);
     place(is, irl, x0);
 
@@ -353,18 +324,17 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll 1
     for (;;) {
         // ---------------------------------------------------- the piece's rows
-        const int row_base = cs.rt * RT;                    // rows of the request: token * G + head of the group
-        const int nrow = min(RT, cs.n * p.G - row_base);
+        const int nrow = cs.n * p.G;  // rows of the request: token * G + head of the group
         // visible keys of the first and the last row
         auto visible = [&](int tok) { return p.causal ? min(max(cs.len - cs.n + tok + 1, 0), cs.len) : cs.len; };
-        const int vis_min = visible(row_base / p.G), vis_max = visible((row_base + nrow - 1) / p.G);
+        const int vis_min = visible(0), vis_max = visible(cs.n - 1);
         for (int r = warp; r < RT; r += kPgWarps) {
             // four values per lane; the row's power of two goes to its score factor
             uint2 x = make_uint2(0u, 0u);
-            const int rr = row_base + r, tok = rr / p.G;
+            const int tok = r / p.G;
             if (r < nrow && lane < D / 4)
                 x = *reinterpret_cast<const uint2*>(
-                    p.q + (static_cast<size_t>(cs.tok0 + tok) * p.Hq + cs.hk * p.G + (rr - tok * p.G)) * D + lane * 4);
+                    p.q + (static_cast<size_t>(cs.tok0 + tok) * p.Hq + cs.hk * p.G + (r - tok * p.G)) * D + lane * 4);
             const uint32_t h4[4] = {x.x & 0xFFFFu, x.x >> 16, x.y & 0xFFFFu, x.y >> 16};
             uint32_t top = 0;
 #pragma unroll
@@ -643,7 +613,7 @@ __global__ void __launch_bounds__(256, 1)
                 if (nan_seen && first_nan[col] < __float_as_int(rowc[r].y)) sum = CUDART_NAN_F;
                 if (whole) {
                     if (r < nrow) {
-                        const int rr = row_base + r, tok = rr / p.G, hq = cs.hk * p.G + rr - tok * p.G;
+                        const int tok = r / p.G, hq = cs.hk * p.G + r - tok * p.G;
                         const float out = L == 0.f ? 0.f : sum / L;
                         p.o[(static_cast<size_t>(cs.tok0 + tok) * p.Hq + hq) * D + col] =
                             static_cast<uint16_t>(pack_bf16x2(out, 0.f) & 0xFFFFu);
@@ -669,7 +639,7 @@ __global__ void __launch_bounds__(256, 1)
             const int f = static_cast<int>(cs.line0 / quota), e = static_cast<int>((cs.line0 + cs.nchunk - 1) / quota);
             __threadfence();
             __syncthreads();
-            if (tid == 0) last_s = atomicAdd(&p.counters[cs.unit0 + cs.unit], 1) == e - f;
+            if (tid == 0) last_s = atomicAdd(&p.counters[cs.b * p.Hkv + cs.hk], 1) == e - f;
             __syncthreads();
             if (last_s) {
                 __threadfence();
@@ -687,7 +657,7 @@ __global__ void __launch_bounds__(256, 1)
                         L = fmaf(w, __ldcg(&p.pl[sl * kPagedMaxRows + r]), L);
                         acc = fmaf(w, __ldcg(&p.po[(static_cast<size_t>(sl) * kPagedMaxRows + r) * D + col]), acc);
                     }
-                    const int rr = row_base + r, tok = rr / p.G, hq = cs.hk * p.G + rr - tok * p.G;
+                    const int tok = r / p.G, hq = cs.hk * p.G + r - tok * p.G;
                     const float out = L == 0.f ? 0.f : acc / L;
                     p.o[(static_cast<size_t>(cs.tok0 + tok) * p.Hq + hq) * D + col] =
                         static_cast<uint16_t>(pack_bf16x2(out, 0.f) & 0xFFFFu);
@@ -720,20 +690,17 @@ static cudaError_t launch_split(const PagedArgs& a, const PagedParams& p, cudaSt
     cudaError_t e =
         cudaFuncSetAttribute(fa_paged_split_kernel<D, NT, B16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    if (a.ev_begin) cudaEventRecord(a.ev_begin, stream);
     fa_paged_split_kernel<D, NT, B16><<<kPagedCtas, 256, C::SMEM, stream>>>(tk, tv, p);
-    if (a.ev_end) cudaEventRecord(a.ev_end, stream);
     return cudaGetLastError();
 }
 
 template <int D>
 static cudaError_t launch_split_d(const PagedArgs& a, const PagedParams& p, cudaStream_t stream) {
     const bool b16 = a.block_size == 16;
-    switch (paged_row_tile(a.max_new, p.G)) {
-        case 8: return b16 ? launch_split<D, 1, true>(a, p, stream) : launch_split<D, 1, false>(a, p, stream);
-        case 16: return b16 ? launch_split<D, 2, true>(a, p, stream) : launch_split<D, 2, false>(a, p, stream);
-        default: return b16 ? launch_split<D, 4, true>(a, p, stream) : launch_split<D, 4, false>(a, p, stream);
-    }
+    const long long rows = static_cast<long long>(a.max_new) * p.G;
+    if (rows <= 8) return b16 ? launch_split<D, 1, true>(a, p, stream) : launch_split<D, 1, false>(a, p, stream);
+    if (rows <= 16) return b16 ? launch_split<D, 2, true>(a, p, stream) : launch_split<D, 2, false>(a, p, stream);
+    return b16 ? launch_split<D, 4, true>(a, p, stream) : launch_split<D, 4, false>(a, p, stream);
 }
 
 cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t stream, int* nlaunch) {
@@ -760,12 +727,17 @@ cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t stream, int* nlaun
     p.causal = a.causal;
     p.status = a.status;
     p.counters = a.counters;
-    p.max_units = a.max_units;
     p.pm = a.pm;
     p.pl = a.pl;
     p.po = a.po;
-    const cudaError_t e = a.d == 64 ? launch_split_d<64>(a, p, stream) : launch_split_d<128>(a, p, stream);
+    if (a.ev_begin) cudaEventRecord(a.ev_begin, stream);
+    cudaError_t e = a.d == 64 ? launch_split_d<64>(a, p, stream) : launch_split_d<128>(a, p, stream);
     *nlaunch = 1;
+    if (e == cudaSuccess && paged_has_tiles(a.max_new, p.G)) {
+        e = launch_paged_tile(a, stream);
+        *nlaunch = 2;
+    }
+    if (a.ev_end) cudaEventRecord(a.ev_end, stream);
     return e;
 }
 

@@ -13,7 +13,9 @@ enum : int { FA_DEV_NO_BLOCKS = 5 };
 
 constexpr int kPlanMaxB = 16384;      // requests of one plan (offsets of all of them sit in shared memory)
 constexpr int kPagedCtas = 152;       // one persistent CTA per SM
-constexpr int kPagedMaxRows = 32;     // query rows of the largest row tile of the split-key kernel
+constexpr int kPagedMaxRows = 32;     // query rows (new tokens x heads of a group) up to which a request is the
+                                      // split-key kernel's; the row-tile kernel takes the others
+constexpr int kPagedTileRows = 256;   // query rows of a unit of the row-tile kernel
 
 struct PlanArgs {
     const int32_t *new_len, *cache_len;
@@ -46,31 +48,33 @@ struct PagedArgs {
     int B, Hq, Hkv, total, max_new, max_blocks, num_blocks, block_size, d;
     float scale;
     int causal;
-    // workspace
+    // workspace; the counters are zero at the start
     int* status;
-    int* counters;     // [max_units] finished pieces of each unit, zero at the start
-    int max_units;
-    float *pm, *pl;    // [2 * kPagedCtas][kPagedMaxRows]
-    float* po;         // [2 * kPagedCtas][kPagedMaxRows][d]
-    cudaEvent_t ev_begin, ev_end;  // optional, recorded around the attention kernel
+    int* counters;       // [B * Hkv] finished pieces of the split-key kernel's units
+    float *pm, *pl;      // [2 * kPagedCtas][kPagedMaxRows]
+    float* po;           // [2 * kPagedCtas][kPagedMaxRows][d]
+    int* tile_counters;  // [2 * max_tile_units], of the row-tile kernel's row tiles
+    int max_tile_units;
+    float *tile_pm, *tile_pl;  // [2 * kPagedCtas][kPagedTileRows]
+    float* tile_po;            // [2 * kPagedCtas][kPagedTileRows][d]
+    cudaEvent_t ev_begin, ev_end;  // optional, recorded around the attention kernels
 };
 
-// Rows of the split-key kernel's row tile for requests of at most max_new
-// new tokens and `group` query heads per key head.
-inline int paged_row_tile(int max_new, int group) {
-    const long long rows = static_cast<long long>(max_new) * group;
-    return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+// Whether a request of max_new new tokens goes to the row-tile kernel.
+inline bool paged_has_tiles(int max_new, int group) {
+    return static_cast<long long>(max_new) * group > kPagedMaxRows;
 }
-
-// Units (row tile and key head of a request) that B requests of together
-// `total` tokens can have.
-inline long long paged_max_units(int B, int Hq, int Hkv, int total, int max_new) {
-    const long long group = Hq / Hkv, rt = paged_row_tile(max_new, static_cast<int>(group));
-    return Hkv * (B + total * group / rt);
+// Units of the row-tile kernel that B requests of together `total` tokens can
+// have (none if no request can be that long).
+inline long long paged_max_tile_units(int B, int Hq, int Hkv, int total, int max_new) {
+    const long long group = Hq / Hkv;
+    if (!paged_has_tiles(max_new, static_cast<int>(group))) return 0;
+    return Hkv * (B + total * group / kPagedTileRows);
 }
 
 cudaError_t launch_cache_plan(const PlanArgs& a, cudaStream_t stream, int* nlaunch);
 cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t stream, int* nlaunch);
+cudaError_t launch_paged_tile(const PagedArgs& a, cudaStream_t stream);
 cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t stream, int* nlaunch);
 
 }  // namespace fa

@@ -1,0 +1,858 @@
+// Attention over the paged 8-bit cache for requests with many query rows
+// (prompts and pieces of prompts): tcgen05 products on tiles of 128 rows.
+//
+// Same computation as fa_paged.cu. With hundreds of rows for each cached key
+// the time is that of the two products, 4 n len d flops for each query head.
+//
+// Work: a unit is (request, key head, pair of row tiles); a row is (new token,
+// query head of the group), token-major, so that a tile of 128 rows sees
+// nearly the same keys in all of them. The units' key tiles (128 keys, only
+// those that some row sees) form one line that is cut into equal quotas for
+// the persistent CTAs, as in the split-key kernel; the rows of a unit that was
+// cut are merged by whoever finishes last.
+//
+// A CTA holds two row tiles so that each V tile is converted once for 256
+// rows. Warps:
+//   0      copies K tiles by TMA, E4M3 as they lie, and their block scales
+//   1, 2   issue the products of row tile 0, 1 (independent of each other)
+//   3      allocates TMEM
+//   4-7    softmax of row tile 0: thread = row
+//   8-11   softmax of row tile 1
+//   12-15  convert V to f16: thread = key
+//
+// S = Q K^T runs on E4M3 operands, two products instead of one of f16: each
+// row of Q, divided by a power of two, is the sum of two E4M3 numbers (four
+// bits each of bfloat16's eight; exact down to 2^-10 of the row's maximum,
+// within 2^-17 of it below). Two E4M3 products cost what one f16 product costs, and K needs no
+// conversion and half the shared memory.
+// O += P V runs on f16: V's numbers convert exactly, P keeps 11 bits.
+// Block scales: ks multiplies the exponent's slope and log2(vs) is added to
+// the exponent, so P holds 2^(s - mu) vs; mu follows the largest of these
+// products, and P's rounding is relative to it whatever the scales are. The
+// row sum takes vs out again, for each group of 16 keys (the smallest block).
+#include <math_constants.h>
+
+#include "fa_common.cuh"
+#include "fa_paged.h"
+#include "tmap.h"
+
+namespace fa {
+
+constexpr float kPtLn2 = 0.69314718055994530942f;
+constexpr float kPtRescale = 8.0f;  // log2 units
+constexpr float kPtOffset = 6.0f;   // log2 of the factor on P before its rounding to f16
+constexpr float kPtSpan = 60.0f;    // log2 of the largest ratio of V's block scales that is kept apart
+constexpr int kPtScaleSlots = 8;
+constexpr int kPtNanSlots = 4;
+
+template <int D>
+struct PtCfg {
+    static constexpr int KS = D == 128 ? 4 : 6;   // K stages
+    static constexpr int VS = 2;                  // V stages
+    static constexpr int NREG = D / 64;           // 128-byte-wide regions of an f16 row
+    static constexpr int Q_BYTES = D == 128 ? 32768 : 16384;  // high and low parts of a row tile
+    static constexpr int K_BYTES = 128 * D;
+    static constexpr int V_BYTES = 128 * D * 2;
+    static constexpr int Q_OFF = 0;
+    static constexpr int K_OFF = Q_OFF + 2 * Q_BYTES;
+    static constexpr int V_OFF = K_OFF + KS * K_BYTES;
+    static constexpr int SC_OFF = V_OFF + VS * V_BYTES;       // float [slots][24]: ks, log2 vs, 1 / vs of 8 groups
+    static constexpr int NAN_OFF = SC_OFF + kPtScaleSlots * 96;  // int [slots][D + 4]: first key with a NaN value
+    static constexpr int NAN_STRIDE = (D + 4) * 4;
+    static constexpr int BAR_OFF = NAN_OFF + kPtNanSlots * NAN_STRIDE;
+    static constexpr int USED = BAR_OFF + 512;
+    static constexpr int SMEM = USED + 1024;
+    static constexpr int COL_S = 0, COL_O = 256;  // TMEM: S of tile i at 128 i, O at 256 + 128 i
+    static constexpr uint32_t ID_S = idesc_make(128, 128, kFmtE4M3, false, false);
+    static constexpr uint32_t ID_PV = idesc_make(128, D, 0 /* f16 */, false, true);
+    static_assert(SMEM <= 232448 - 2048, "shared memory");
+};
+
+struct PtParams {
+    const uint16_t* q;
+    const uint8_t* v_cache;
+    const float *k_scale, *v_scale;
+    uint16_t* o;
+    float* lse;
+    const int32_t *cu_seqlens, *cache_len, *block_table;
+    int B, Hq, Hkv, G, total, max_new, max_blocks, num_blocks, bs_log2;
+    float scale_log2;
+    int causal;
+    int *status, *counters;
+    int max_units;
+    float *pm, *pl, *po;
+};
+
+__device__ __forceinline__ void named_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ uint32_t pt_f16x2_from_e4m3x2(uint32_t x) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pt_pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t sbo) {
+    return (sdesc_sw128(saddr, 16, sbo) & ~(7ull << 61)) | (4ull << 61);
+}
+
+struct PtReq {
+    int b, n, len, tok0;
+    int npair;        // pairs of row tiles
+    long long tiles;  // key tiles of all pairs of one key head
+};
+struct PtSeg {
+    PtReq r;
+    int hk, pair;
+    int ntile;        // key tiles of the unit
+    int c0, c1;       // this piece's tiles
+    long long line0;  // position of the unit's first tile on the line
+    int unit;         // index of the unit among all
+};
+
+// Keys that new token `tok` of a request sees.
+__device__ __forceinline__ int pt_visible(const PtParams& p, const PtReq& r, int tok) {
+    return p.causal ? min(max(r.len - r.n + tok + 1, 0), r.len) : r.len;
+}
+// Key tiles that rows [.., last] of a request need (at least one, so that
+// rows that see nothing get their zero output).
+__device__ __forceinline__ int pt_tiles(const PtParams& p, const PtReq& r, int pair) {
+    const int last = min(pair * 256 + 255, r.n * p.G - 1);
+    return max(1, (pt_visible(p, r, last / p.G) + 127) >> 7);
+}
+__device__ __forceinline__ void pt_request(const PtParams& p, int b, PtReq& r) {
+    const int t0 = min(max(p.cu_seqlens[b], 0), p.total), t1 = min(max(p.cu_seqlens[b + 1], t0), p.total);
+    r.b = b;
+    r.tok0 = t0;
+    r.n = min(t1 - t0, p.max_new);
+    if (static_cast<long long>(r.n) * p.G <= kPagedMaxRows) r.n = 0;  // the split-key kernel's
+    r.len = min(max(p.cache_len[b], 0), p.max_blocks << p.bs_log2);
+    r.npair = static_cast<int>((static_cast<long long>(r.n) * p.G + 255) >> 8);
+    r.tiles = 0;
+    for (int i = 0; i < r.npair; ++i) r.tiles += pt_tiles(p, r, i);
+}
+
+template <int D>
+__global__ void __launch_bounds__(512, 1)
+    fa_paged_tile_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ PtParams p) {
+    using C = PtCfg<D>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    __shared__ long long scan_w[16], scan_u[16];
+    __shared__ long long start_line;
+    __shared__ int start_b, start_units, abort_s, last_s[2];
+    __shared__ uint32_t tmem_slot;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    // ---- the line of key tiles: total length, and the request at this CTA's start
+    const int per = (p.B + 511) / 512;
+    const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+    long long mw = 0, mu = 0;
+    for (int b = b0; b < b1; ++b) {
+        PtReq r;
+        pt_request(p, b, r);
+        mu += static_cast<long long>(r.npair) * p.Hkv;
+        mw += r.tiles * p.Hkv;
+    }
+    long long iw = mw, iu = mu;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long a = __shfl_up_sync(0xffffffffu, iw, off), c = __shfl_up_sync(0xffffffffu, iu, off);
+        if (lane >= off) {
+            iw += a;
+            iu += c;
+        }
+    }
+    if (lane == 31) {
+        scan_w[warp] = iw;
+        scan_u[warp] = iu;
+    }
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::BAR_OFF);
+    uint64_t* q_full = bars;                   // [2] Q parts of a row tile stored
+    uint64_t* s_full = q_full + 2;             // [2] S ready
+    uint64_t* p_full = s_full + 2;             // [2] P stored, O rescaled
+    uint64_t* o_done = p_full + 2;             // [2] O of a piece final
+    uint64_t* drain = o_done + 2;              // [2]
+    uint64_t* nan_full = drain + 2;            // [4] a piece's V has been looked over
+    uint64_t* sc_full = nan_full + kPtNanSlots;          // [8] scales stored
+    uint64_t* k_full = sc_full + kPtScaleSlots;  // [KS]
+    uint64_t* k_empty = k_full + C::KS;        // [KS] both row tiles' S done
+    uint64_t* v_full = k_empty + C::KS;        // [VS]
+    uint64_t* v_empty = v_full + C::VS;        // [VS]
+    if (tid == 0) {
+        abort_s = 0;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], 128);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 128);
+            mbar_init(&o_done[i], 1);
+            mbar_init(&drain[i], 1);
+        }
+        for (int i = 0; i < kPtNanSlots; ++i) mbar_init(&nan_full[i], 128);
+        for (int i = 0; i < kPtScaleSlots; ++i) mbar_init(&sc_full[i], 1);
+        for (int i = 0; i < C::KS; ++i) {
+            mbar_init(&k_full[i], 1);
+            mbar_init(&k_empty[i], 2);
+        }
+        for (int i = 0; i < C::VS; ++i) {
+            mbar_init(&v_full[i], 128);
+            mbar_init(&v_empty[i], 2);
+        }
+        fence_barrier_init();
+    }
+    int* nan_first = reinterpret_cast<int*>(sm + C::NAN_OFF);  // [slot][D], then a flag
+    for (int i = tid; i < kPtNanSlots * (D + 4); i += 512) nan_first[i] = i % (D + 4) == D ? 0 : INT_MAX;
+    __syncthreads();
+    long long W = 0, U = 0, bw = 0, bu = 0;
+    for (int w = 0; w < 16; ++w) {
+        if (w < warp) {
+            bw += scan_w[w];
+            bu += scan_u[w];
+        }
+        W += scan_w[w];
+        U += scan_u[w];
+    }
+    if (U > p.max_units) return;  // overlapping offsets: reported by the split-key kernel
+    const long long quota = max((W + gridDim.x - 1) / static_cast<long long>(gridDim.x), 2ll);
+    const long long x0 = quota * blockIdx.x, x1 = min(x0 + quota, W);
+    if (x0 >= x1) return;  // uniform over the CTA, before any TMEM use
+    bw += iw - mw;
+    bu += iu - mu;
+    if (x0 >= bw && x0 < bw + mw) {
+        for (int b = b0; b < b1; ++b) {
+            PtReq r;
+            pt_request(p, b, r);
+            if (x0 < bw + r.tiles * p.Hkv) {
+                start_b = b;
+                start_line = bw;
+                start_units = static_cast<int>(bu);
+                break;
+            }
+            bw += r.tiles * p.Hkv;
+            bu += static_cast<long long>(r.npair) * p.Hkv;
+        }
+    }
+    if (warp == 3) {
+        tmem_alloc(&tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = tmem_slot;
+
+    // Every role walks the same pieces.
+    long long rline = start_line;
+    int runits = start_units;
+    auto find = [&](PtSeg& s, long long x) {  // the piece that starts at x, in the current request or a later one
+        while (x >= rline + s.r.tiles * p.Hkv) {
+            rline += s.r.tiles * p.Hkv;
+            runits += s.r.npair * p.Hkv;
+            pt_request(p, s.r.b + 1, s.r);
+        }
+        const long long off = x - rline;
+        s.hk = static_cast<int>(off / s.r.tiles);
+        long long rest = off - s.hk * s.r.tiles;
+        s.pair = 0;
+        for (;;) {
+            s.ntile = pt_tiles(p, s.r, s.pair);
+            if (rest < s.ntile) break;
+            rest -= s.ntile;
+            ++s.pair;
+        }
+        s.c0 = static_cast<int>(rest);
+        s.line0 = x - s.c0;
+        s.c1 = static_cast<int>(min(static_cast<long long>(s.ntile), x1 - s.line0));
+        s.unit = runits + s.hk * s.r.npair + s.pair;
+    };
+    auto first = [&](PtSeg& s) {
+        pt_request(p, start_b, s.r);
+        find(s, x0);
+    };
+    auto next = [&](PtSeg& s) -> bool {
+        const long long x = s.line0 + s.c1;
+        if (x >= x1) return false;
+        if (s.pair + 1 < s.r.npair) {  // the usual step: the next pair of the same head
+            ++s.pair;
+            ++s.unit;
+            s.ntile = pt_tiles(p, s.r, s.pair);
+            s.c0 = 0;
+            s.line0 = x;
+            s.c1 = static_cast<int>(min(static_cast<long long>(s.ntile), x1 - x));
+            return true;
+        }
+        find(s, x);
+        return true;
+    };
+    // key tiles that row tile i of a piece takes part in: [c0, end)
+    auto half_end = [&](const PtSeg& s, int i) {
+        const int rows = s.r.n * p.G, base = s.pair * 256 + i * 128;
+        if (base >= rows) return s.c0;
+        const int last = min(base + 127, rows - 1);
+        return max(s.c0, min(s.c1, (pt_visible(p, s.r, last / p.G) + 127) >> 7));
+    };
+    const WaitCtx cx{reinterpret_cast<volatile int*>(&abort_s), p.status};
+    PtSeg s;
+    first(s);
+
+    if (warp < 4) {
+        regs_dec<56>();
+        if (warp == 0) {
+            // ------------------------------------------------------ K tiles and scales
+            const int bs = 1 << p.bs_log2, box = min(bs, 128);
+            int u = 0;
+            bool ok = true;
+            float* sc = reinterpret_cast<float*>(sm + C::SC_OFF);
+            do {
+                float vref = 0.f;  // largest V scale met so far in this piece
+                for (int t = s.c0; ok && t < s.c1; ++t, ++u) {
+                    const int st = u % C::KS, slot = u % kPtScaleSlots;
+                    // lane i < 8: the group of 16 keys from 16 i on
+                    int id = 0;
+                    float ks = 0.f, vs = 0.f;
+                    const int key = t * 128 + lane * 16;
+                    if (lane < 8 && key < s.r.len) {
+                        id = p.block_table[static_cast<size_t>(s.r.b) * p.max_blocks + (key >> p.bs_log2)];
+                        if (id < 0 || id >= p.num_blocks) {
+                            atomicCAS(p.status, 0, FA_DEV_INVALID | (94 << 8));
+                            id = 0;
+                        } else {
+                            ks = p.k_scale[static_cast<size_t>(id) * p.Hkv + s.hk];
+                            vs = p.v_scale[static_cast<size_t>(id) * p.Hkv + s.hk];
+                        }
+                    }
+                    if (!(ok = mbar_wait_warp(&k_empty[st], ((u / C::KS) & 1) ^ 1, cx, 95))) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&k_full[st], C::K_BYTES);
+                    __syncwarp();
+                    // box b covers the groups from b * box / 16 on; its first lane requests it
+                    const int gpb = box >> 4;
+                    if (lane < 8 && lane % gpb == 0) {
+                        const int in = (t * 128 + lane * 16) & (bs - 1);
+                        const long long row = ((static_cast<long long>(id) * p.Hkv + s.hk) << p.bs_log2) + in;
+                        tma_load_2d(sm + C::K_OFF + st * C::K_BYTES + lane * 16 * D, &tmK, 0, static_cast<int>(row),
+                                    &k_full[st]);
+                    }
+                    float top = vs;
+#pragma unroll
+                    for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    vref = fmaxf(vref, top);
+                    if (lane < 8) {
+                        // groups whose scale is below 2^-60 of the largest (blocks of
+                        // zeros have 2^-126) count as if it were that
+                        const float lv = fmaxf(fmaxf(log2f(vs), log2f(vref) - kPtSpan), -100.f);
+                        sc[slot * 24 + lane] = ks;
+                        sc[slot * 24 + 8 + lane] = lv;
+                        sc[slot * 24 + 16 + lane] = exp2f(-lv);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sc_full[slot]);
+                }
+            } while (ok && next(s));
+            // let every copy in flight land before the CTA can exit
+            if (lane == 0)
+                for (int i = 0; i < C::KS && i < u; ++i) {
+                    const int last = i + ((u - 1 - i) / C::KS) * C::KS;
+                    mbar_wait_teardown(&k_full[i], (last / C::KS) & 1, 200000000ull);
+                }
+        } else if (warp < 3) {
+            // ------------------------------------------------------ products of row tile i
+            const int i = warp - 1;
+            const uint32_t leader = elect_one_sync();
+            const uint32_t tS = tm + C::COL_S + i * 128, tO = tm + C::COL_O + i * 128;
+            const uint64_t dQ = sdesc_sw128(smem_u32(sm + C::Q_OFF + i * C::Q_BYTES), 16, 1024);
+            const uint64_t dK = D == 128 ? sdesc_sw128(smem_u32(sm + C::K_OFF), 16, 1024)
+                                         : sdesc_sw64(smem_u32(sm + C::K_OFF), 512);
+            const uint64_t dV = sdesc_sw128(smem_u32(sm + C::V_OFF), 16384, 1024);
+            int u = 0, nseg = 0, np = 0;  // tiles walked, pieces with work, tiles of P multiplied
+            bool ok = true;
+            do {
+                const int end = half_end(s, i);
+                auto issue_pv = [&](int uu, bool fresh) -> bool {
+                    const int vs = uu % C::VS;
+                    if (!mbar_wait_warp(&p_full[i], np & 1, cx, 96)) return false;
+                    if (!mbar_wait_warp(&v_full[vs], (uu / C::VS) & 1, cx, 97)) return false;
+                    tc_fence_after();
+                    const uint64_t vd = sdesc_advance(dV, vs * C::V_BYTES);
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        umma_ts<false>(leader, tO, tS + kk * 8, sdesc_advance(vd, kk * 2048), C::ID_PV,
+                                       !fresh || kk > 0 ? 1u : 0u);
+                    umma_commit(leader, &v_empty[vs]);
+                    ++np;
+                    return true;
+                };
+                if (end > s.c0 && !(ok = mbar_wait_warp(&q_full[i], nseg & 1, cx, 98))) break;
+                for (int t = s.c0; t < s.c1; ++t, ++u) {
+                    const int st = u % C::KS;
+                    if (t < end) {
+                        // the previous tile's P V first: S below overwrites its P
+                        if (t > s.c0 && !(ok = issue_pv(u - 1, t - 1 == s.c0))) break;
+                        if (!(ok = mbar_wait_warp(&k_full[st], (u / C::KS) & 1, cx, 99))) break;
+                        tc_fence_after();
+                        const uint64_t kd = sdesc_advance(dK, st * C::K_BYTES);
+#pragma unroll
+                        for (int part = 0; part < 2; ++part)
+#pragma unroll
+                            for (int kk = 0; kk < D / 32; ++kk)
+                                umma_ss_f8(leader, tS,
+                                           sdesc_advance(dQ, (D == 128 ? part * 16384 : part * 64) + kk * 32),
+                                           sdesc_advance(kd, kk * 32), C::ID_S, part || kk ? 1u : 0u);
+                        umma_commit(leader, &s_full[i]);
+                        umma_commit(leader, &k_empty[st]);
+                    } else {
+                        // tiles that only the other row tile needs
+                        if (t == end && t > s.c0 && !(ok = issue_pv(u - 1, t - 1 == s.c0))) break;
+                        const int vs = u % C::VS;
+                        if (!(ok = mbar_wait_warp(&k_full[st], (u / C::KS) & 1, cx, 100))) break;
+                        if (lane == 0) mbar_arrive(&k_empty[st]);
+                        if (!(ok = mbar_wait_warp(&v_full[vs], (u / C::VS) & 1, cx, 101))) break;
+                        if (lane == 0) mbar_arrive(&v_empty[vs]);
+                    }
+                }
+                if (ok && end == s.c1 && end > s.c0) ok = issue_pv(u - 1, end - 1 == s.c0);
+                if (!ok) break;
+                if (end > s.c0) {
+                    umma_commit(leader, &o_done[i]);
+                    ++nseg;
+                }
+            } while (next(s));
+            // every MMA issued so far must be complete before TMEM is released
+            umma_commit(leader, &drain[i]);
+            mbar_wait_teardown(&drain[i], 0, 200000000ull);
+        }
+    } else if (warp < 12) {
+        // ---------------------------------------------------------- softmax of row tile i
+        regs_inc<184>();
+        const int i = (warp - 4) >> 2, wq = warp & 3, r = wq * 32 + lane;
+        const uint32_t tl = tm + (static_cast<uint32_t>(wq * 32) << 16);
+        const uint32_t tS = tl + C::COL_S + i * 128, tO = tl + C::COL_O + i * 128;
+        uint8_t* qb = sm + C::Q_OFF + i * C::Q_BYTES;
+        int u = 0, ns = 0, nseg = 0, seg = 0;
+        bool ok = true;
+        do {
+            const int end = half_end(s, i);
+            const int rows = s.r.n * p.G, base = s.pair * 256 + i * 128, row = base + r;
+            const bool row_ok = row < rows;
+            const int tok = row_ok ? row / p.G : 0, hq = s.hk * p.G + (row_ok ? row - tok * p.G : 0);
+            const int limit = row_ok ? pt_visible(p, s.r, tok) : 0;
+            const size_t qrow = (static_cast<size_t>(s.r.tok0 + tok) * p.Hq + hq) * D;
+            float rc = 0.f, mu = -CUDART_INF_F, l = 0.f;
+            if (end > s.c0) {
+                // ---- Q: the row's power of two, then its high and low E4M3 parts
+                uint4 x[D / 8];
+#pragma unroll
+                for (int j = 0; j < D / 8; ++j)
+                    x[j] = row_ok ? reinterpret_cast<const uint4*>(p.q + qrow)[j] : make_uint4(0u, 0u, 0u, 0u);
+                uint32_t top = 0;
+                bool wild = false;  // an infinity or a NaN
+#pragma unroll
+                for (int j = 0; j < D / 8; ++j) {
+                    const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const uint32_t a = w[y] & 0x7FFFu, b = (w[y] >> 16) & 0x7FFFu;
+                        wild |= a >= 0x7F80u || b >= 0x7F80u;
+                        top = max(top, max(a, b));
+                    }
+                }
+                // largest magnitude to [2^7, 2^8): high parts up to 256, low parts up to 8
+                const int e = top >> 7 && !wild ? min(max(static_cast<int>(top >> 7) - 134, -120), 120) : 0;
+                const float f = exp2i(-e);
+                rc = wild ? CUDART_NAN_F : p.scale_log2 * exp2i(e);  // such a row has no finite result
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) {
+                    const uint32_t w[8] = {x[2 * j].x,     x[2 * j].y,     x[2 * j].z,     x[2 * j].w,
+                                           x[2 * j + 1].x, x[2 * j + 1].y, x[2 * j + 1].z, x[2 * j + 1].w};
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        hi[y] = lo[y] = 0u;
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            const float a = __uint_as_float(w[2 * y + z] << 16) * f;
+                            const float b = __uint_as_float(w[2 * y + z] & 0xFFFF0000u) * f;
+                            const uint32_t h2 = pack_e4m3x2(a, b);
+                            float ha, hb;
+                            f2_split(f2_from_e4m3x2(h2), ha, hb);
+                            hi[y] |= h2 << (16 * z);
+                            lo[y] |= pack_e4m3x2(a - ha, b - hb) << (16 * z);
+                        }
+                    }
+                    if constexpr (D == 128) {
+                        const uint32_t at = r * 128 + ((j ^ (r & 7)) << 4);
+                        sts128(smem_u32(qb + at), hi[0], hi[1], hi[2], hi[3]);
+                        sts128(smem_u32(qb + 16384 + at), lo[0], lo[1], lo[2], lo[3]);
+                    } else {
+                        sts128(smem_u32(qb + r * 128 + ((j ^ (r & 7)) << 4)), hi[0], hi[1], hi[2], hi[3]);
+                        sts128(smem_u32(qb + r * 128 + (((j + 4) ^ (r & 7)) << 4)), lo[0], lo[1], lo[2], lo[3]);
+                    }
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(&q_full[i]);
+            }
+            // rows that the first row's keys bound: tiles below need no mask
+            const int vis_min = pt_visible(p, s.r, min(base, rows - 1) / p.G);
+            for (int t = s.c0; t < end; ++t) {
+                const int us = u + (t - s.c0), slot = us % kPtScaleSlots;
+                ok = mbar_wait(&sc_full[slot], (us / kPtScaleSlots) & 1, cx, 102);
+                ok = ok && mbar_wait(&s_full[i], ns & 1, cx, 103);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t sr[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, sr[c]);
+                const float4* sc4 = reinterpret_cast<const float4*>(sm + C::SC_OFF + slot * 96);
+                float c2[8], lv[8];
+                {
+                    const float4 a = sc4[0], b = sc4[1], c = sc4[2], d = sc4[3];
+                    c2[0] = a.x; c2[1] = a.y; c2[2] = a.z; c2[3] = a.w;
+                    c2[4] = b.x; c2[5] = b.y; c2[6] = b.z; c2[7] = b.w;
+                    lv[0] = c.x; lv[1] = c.y; lv[2] = c.z; lv[3] = c.w;
+                    lv[4] = d.x; lv[5] = d.y; lv[6] = d.z; lv[7] = d.w;
+                }
+#pragma unroll
+                for (int gr = 0; gr < 8; ++gr) c2[gr] = c2[gr] * rc;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld_wait(sr[c]);
+                if (t * 128 + 128 > vis_min) {
+                    const int lim = limit - t * 128;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (c * 32 + k >= lim) sr[c][k] = __float_as_uint(-CUDART_INF_F);
+                }
+                float m_new = mu;
+#pragma unroll
+                for (int gr = 0; gr < 8; ++gr) {
+                    const uint32_t* v = &sr[gr >> 1][(gr & 1) * 16];
+                    float a = -CUDART_INF_F, b = -CUDART_INF_F;
+#pragma unroll
+                    for (int k = 0; k < 16; k += 4) {
+                        a = fmax3(a, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+                        b = fmax3(b, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
+                    }
+                    a = fmaxf(a, b);
+                    // a slope of zero (a block of zeros) would turn masked scores into NaN
+                    c2[gr] = c2[gr] < 1e-37f || a == -CUDART_INF_F ? 1e-37f : c2[gr];
+                    m_new = fmaxf(m_new, fmaf(a, c2[gr], lv[gr]));
+                }
+                const bool resc = m_new - mu > kPtRescale;
+                float alpha = 1.f;
+                if (resc) {
+                    alpha = ex2_approx(mu - m_new);
+                    mu = m_new;
+                    l *= alpha;
+                }
+                const bool resc_any = __any_sync(0xffffffffu, resc) && t > s.c0;
+                const float sub = mu == -CUDART_INF_F ? 0.f : mu - kPtOffset;
+                const float* il = reinterpret_cast<const float*>(sc4) + 16;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const int gr = 2 * c + hf;
+                        const float add = lv[gr] - sub;
+                        const uint64_t cc = f2_make(c2[gr], c2[gr]), aa = f2_make(add, add);
+                        uint64_t sum = 0ull;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int at = hf * 16 + 2 * k;
+                            float y0, y1;
+                            f2_split(f2_fma(f2_make(__uint_as_float(sr[c][at]), __uint_as_float(sr[c][at + 1])), cc, aa),
+                                     y0, y1);
+                            const float e0 = ex2_approx(y0), e1 = ex2_approx(y1);
+                            pk[hf * 8 + k] = pt_pack_f16x2(e0, e1);
+                            sum = f2_add(sum, f2_make(e0, e1));
+                        }
+                        float a, b;
+                        f2_split(sum, a, b);
+                        l = fmaf(a + b, il[gr], l);
+                    }
+                    tmem_st16(tS + c * 16, pk);
+                }
+                if (resc_any) {
+                    // the previous tiles' P V were issued before this tile's S
+                    // and MMAs complete in order: O is final, and rescaled here
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t ov[32];
+                        tmem_ld32(tO + c * 32, ov);
+                        tmem_ld_wait(ov);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * alpha);
+                        tmem_st32(tO + c * 32, ov);
+                    }
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&p_full[i]);
+                ++ns;
+            }
+            if (!ok) break;
+            u += s.c1 - s.c0;
+            // ---------------------------------------------------- the piece's rows
+            if (end > s.c0) {
+                ok = mbar_wait(&o_done[i], nseg & 1, cx, 104);
+                ++nseg;
+            }
+            ok = ok && mbar_wait(&nan_full[seg % kPtNanSlots], (seg / kPtNanSlots) & 1, cx, 105);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            int* nf = nan_first + (seg % kPtNanSlots) * (D + 4);
+            const bool nan_seen = nf[D] != 0;
+            ++seg;
+            const bool whole = s.c0 == 0 && s.c1 == s.ntile;
+            const int slot = 2 * static_cast<int>(blockIdx.x) + (s.line0 <= x0 ? 0 : 1);
+            const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+            float* po = p.po + (static_cast<size_t>(slot) * kPagedTileRows + i * 128 + r) * D;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t ov[32];
+                if (end > s.c0) {
+                    tmem_ld32(tO + c * 32, ov);
+                    tmem_ld_wait(ov);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) ov[k] = 0u;
+                }
+                if (nan_seen) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (nf[c * 32 + k] < limit) ov[k] = __float_as_uint(CUDART_NAN_F);
+                }
+                if (whole) {
+                    if (row_ok) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint4 w;
+                            w.x = pack_bf16x2(__uint_as_float(ov[8 * k + 0]) * inv, __uint_as_float(ov[8 * k + 1]) * inv);
+                            w.y = pack_bf16x2(__uint_as_float(ov[8 * k + 2]) * inv, __uint_as_float(ov[8 * k + 3]) * inv);
+                            w.z = pack_bf16x2(__uint_as_float(ov[8 * k + 4]) * inv, __uint_as_float(ov[8 * k + 5]) * inv);
+                            w.w = pack_bf16x2(__uint_as_float(ov[8 * k + 6]) * inv, __uint_as_float(ov[8 * k + 7]) * inv);
+                            reinterpret_cast<uint4*>(p.o + qrow + c * 32)[k] = w;
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        reinterpret_cast<uint4*>(po + c * 32)[k] =
+                            make_uint4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
+                }
+            }
+            tc_fence_before();  // O has been read: the next piece's products may overwrite it
+            const float lse_off = kPtOffset;
+            if (whole) {
+                if (row_ok)
+                    p.lse[static_cast<size_t>(hq) * p.total + s.r.tok0 + tok] =
+                        l == 0.f ? -CUDART_INF_F : (mu - lse_off + log2f(l)) * kPtLn2;
+            } else {
+                p.pm[slot * kPagedTileRows + i * 128 + r] = mu;
+                p.pl[slot * kPagedTileRows + i * 128 + r] = l;
+                // pieces of a unit lie in consecutive CTAs; whoever finishes last
+                // merges them in order
+                const int f = static_cast<int>(s.line0 / quota), e = static_cast<int>((s.line0 + s.ntile - 1) / quota);
+                __threadfence();
+                named_sync(1 + i, 128);
+                if (r == 0) last_s[i] = atomicAdd(&p.counters[2 * s.unit + i], 1) == e - f;
+                named_sync(1 + i, 128);
+                if (last_s[i]) {
+                    __threadfence();
+                    // a warp per row, lanes over the columns
+                    for (int rr = wq; rr < 128 && base + rr < rows; rr += 4) {
+                        float M = -CUDART_INF_F, L = 0.f, acc[D / 32];
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k) acc[k] = 0.f;
+                        for (int cta = f; cta <= e; ++cta) {
+                            const int sl = 2 * cta + (s.line0 <= quota * cta ? 0 : 1);
+                            M = fmaxf(M, __ldcg(&p.pm[sl * kPagedTileRows + i * 128 + rr]));
+                        }
+                        for (int cta = f; cta <= e; ++cta) {
+                            const int sl = 2 * cta + (s.line0 <= quota * cta ? 0 : 1);
+                            const size_t at = static_cast<size_t>(sl) * kPagedTileRows + i * 128 + rr;
+                            const float mc = __ldcg(&p.pm[at]);
+                            const float w = mc == -CUDART_INF_F ? 0.f : ex2_approx(mc - M);
+                            L = fmaf(w, __ldcg(&p.pl[at]), L);
+#pragma unroll
+                            for (int k = 0; k < D / 32; ++k)
+                                acc[k] = fmaf(w, __ldcg(&p.po[at * D + k * 32 + lane]), acc[k]);
+                        }
+                        const int tk = (base + rr) / p.G, hh = s.hk * p.G + (base + rr) - tk * p.G;
+                        const size_t at = (static_cast<size_t>(s.r.tok0 + tk) * p.Hq + hh) * D;
+                        const float iL = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k)
+                            p.o[at + k * 32 + lane] =
+                                static_cast<uint16_t>(pack_bf16x2(acc[k] * iL, 0.f) & 0xFFFFu);
+                        if (lane == 0)
+                            p.lse[static_cast<size_t>(hh) * p.total + s.r.tok0 + tk] =
+                                L == 0.f ? -CUDART_INF_F : (M - lse_off + log2f(L)) * kPtLn2;
+                    }
+                }
+            }
+            if (nan_seen) {
+                // both row tiles have looked at the list: clean it for a later piece
+                named_sync(3, 256);
+                if (i == 0 && r < D) nf[r] = INT_MAX;
+                if (i == 0 && r == 0) nf[D] = 0;
+            }
+        } while (next(s));
+    } else {
+        // ---------------------------------------------------------- V to f16, thread = key
+        regs_dec<88>();
+        const int r = (warp - 12) * 32 + lane;
+        int u = 0, seg = 0;
+        bool ok = true;
+        uint4 x[D / 16];
+        auto load = [&](const PtSeg& q, int t) {
+            const int key = t * 128 + r;
+            int id = -1;
+            if (key < q.r.len) id = p.block_table[static_cast<size_t>(q.r.b) * p.max_blocks + (key >> p.bs_log2)];
+            const bool in = id >= 0 && id < p.num_blocks;
+            const uint8_t* src =
+                p.v_cache + ((((static_cast<size_t>(in ? id : 0) * p.Hkv + q.hk) << p.bs_log2) +
+                              (key & ((1 << p.bs_log2) - 1))) * D);
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j)
+                x[j] = in ? __ldg(reinterpret_cast<const uint4*>(src) + j) : make_uint4(0u, 0u, 0u, 0u);
+        };
+        load(s, s.c0);
+        do {
+            const int rows = s.r.n * p.G;
+            const int vis_min = pt_visible(p, s.r, s.pair * 256 / p.G);
+            const int vis_max = pt_visible(p, s.r, min(s.pair * 256 + 255, rows - 1) / p.G);
+            int* nf = nan_first + (seg % kPtNanSlots) * (D + 4);
+            PtSeg n = s;
+            bool more = true;
+            for (int t = s.c0; t < s.c1; ++t, ++u) {
+                const int vs = u % C::VS;
+                ok = mbar_wait_warp(&v_empty[vs], ((u / C::VS) & 1) ^ 1, cx, 106);
+                if (!ok) break;
+                if (t * 128 + 128 > vis_min) {
+                    // rows that no query sees count as zero; a NaN that only
+                    // some see is noted and taken out, the softmax warps give
+                    // it back to the rows that see it
+                    const int key = t * 128 + r;
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) {
+                        uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            if (key >= vis_max) w[y] = 0u;
+                            const uint32_t nb = ((w[y] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                            if (nb) {
+                                nf[D] = 1;
+#pragma unroll
+                                for (int z = 0; z < 4; ++z)
+                                    if ((nb >> (8 * z)) & 0x80u) {
+                                        atomicMin(&nf[j * 16 + y * 4 + z], key);
+                                        w[y] &= ~(0xFFu << (8 * z));
+                                    }
+                            }
+                        }
+                        x[j] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                // row r of the [128 keys x 64 columns] swizzled regions
+                uint8_t* vb = sm + C::V_OFF + vs * C::V_BYTES + r * 128;
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) {
+                    const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+                    uint32_t h[8];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        h[2 * y] = pt_f16x2_from_e4m3x2(w[y]);
+                        h[2 * y + 1] = pt_f16x2_from_e4m3x2(w[y] >> 16);
+                    }
+                    uint8_t* reg = vb + (j >> 2) * 16384;
+                    const int c = (j & 3) * 2;
+                    sts128(smem_u32(reg + ((c ^ (r & 7)) << 4)), h[0], h[1], h[2], h[3]);
+                    sts128(smem_u32(reg + (((c + 1) ^ (r & 7)) << 4)), h[4], h[5], h[6], h[7]);
+                }
+                // the next tile's row is on its way while this one is multiplied
+                if (t + 1 < s.c1) load(s, t + 1);
+                else if ((more = next(n))) load(n, n.c0);
+                fence_proxy_async_smem();
+                mbar_arrive(&v_full[vs]);
+            }
+            if (!ok) break;
+            mbar_arrive(&nan_full[seg % kPtNanSlots]);
+            ++seg;
+            if (!more) break;
+            s = n;
+        } while (true);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 3) {
+        tc_fence_after();
+        tmem_dealloc(tm, 512);
+    }
+}
+
+// K as [num_blocks * Hkv * block_size rows, d] in boxes of a block (at most
+// 128 rows), with the swizzle of its row length.
+static bool make_tmap_k(CUtensorMap* map, const void* base, uint64_t rows, int d, uint32_t box_rows) {
+    EncodeTiledFn fn = encode_tiled_fn();
+    if (!fn) return false;
+    cuuint64_t gdim[2] = {static_cast<cuuint64_t>(d), rows};
+    cuuint64_t gstride[1] = {static_cast<cuuint64_t>(d)};
+    cuuint32_t box[2] = {static_cast<cuuint32_t>(d), box_rows};
+    cuuint32_t estride[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), gdim, gstride, box, estride,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+static cudaError_t launch_tile(const PagedArgs& a, const PtParams& p, cudaStream_t stream) {
+    using C = PtCfg<D>;
+    CUtensorMap tk;
+    const uint64_t rows = static_cast<uint64_t>(a.num_blocks) * a.Hkv * a.block_size;
+    if (!make_tmap_k(&tk, a.k_cache, rows, D, a.block_size < 128 ? a.block_size : 128)) return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(fa_paged_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    fa_paged_tile_kernel<D><<<kPagedCtas, 512, C::SMEM, stream>>>(tk, p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_paged_tile(const PagedArgs& a, cudaStream_t stream) {
+    PtParams p;
+    p.q = static_cast<const uint16_t*>(a.q);
+    p.v_cache = a.v_cache;
+    p.k_scale = a.k_scale;
+    p.v_scale = a.v_scale;
+    p.o = static_cast<uint16_t*>(a.o);
+    p.lse = a.lse;
+    p.cu_seqlens = a.cu_seqlens;
+    p.cache_len = a.cache_len;
+    p.block_table = a.block_table;
+    p.B = a.B;
+    p.Hq = a.Hq;
+    p.Hkv = a.Hkv;
+    p.G = a.Hq / a.Hkv;
+    p.total = a.total;
+    p.max_new = a.max_new;
+    p.max_blocks = a.max_blocks;
+    p.num_blocks = a.num_blocks;
+    p.bs_log2 = 0;
+    while ((1 << p.bs_log2) < a.block_size) ++p.bs_log2;
+    p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.causal = a.causal;
+    p.status = a.status;
+    p.counters = a.tile_counters;
+    p.max_units = a.max_tile_units;
+    p.pm = a.tile_pm;
+    p.pl = a.tile_pl;
+    p.po = a.tile_po;
+    return a.d == 64 ? launch_tile<64>(a, p, stream) : launch_tile<128>(a, p, stream);
+}
+
+}  // namespace fa

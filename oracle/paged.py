@@ -132,14 +132,15 @@ def append(x, cache, scale, slots):
 
 def attend(q, k_bytes, v_bytes, k_scale, v_scale, cu_seqlens, cache_len, block_table, scale, causal=True):
     """O [total, Hq, d], L [Hq, total] and, for tolerances, the weighted
-    absolute values A = sum_j P_j |v_j| and the score magnitudes
-    X = max_j scale |q| . |k_j| of each row."""
+    absolute values A = sum_j P_j |v_j|, the score magnitudes
+    X = max_j scale |q| . |k_j| of each row and their bound
+    Y = max_j scale max|q| sum|k_j|."""
     q = np.asarray(q, dtype=np.float64)
     total, Hq, d = q.shape
     nb, Hkv, bs, _ = k_bytes.shape
     G = Hq // Hkv
     O, A = np.zeros((total, Hq, d)), np.zeros((total, Hq, d))
-    L, X = np.full((Hq, total), -np.inf), np.zeros((Hq, total))
+    L, X, Y = np.full((Hq, total), -np.inf), np.zeros((Hq, total)), np.zeros((Hq, total))
     for b in range(len(cache_len)):
         t0, n, length = int(cu_seqlens[b]), int(cu_seqlens[b + 1] - cu_seqlens[b]), int(cache_len[b])
         if n == 0 or length == 0:
@@ -162,4 +163,5 @@ def attend(q, k_bytes, v_bytes, k_scale, v_scale, cu_seqlens, cache_len, block_t
                     A[t0 + i, g] = p @ np.abs(v[:seen]) / l
                     L[g, t0 + i] = m + math.log(l) if l > 0 else math.nan
                     X[g, t0 + i] = (scale * (np.abs(k[:seen]) @ np.abs(q[t0 + i, g]))).max()
-    return O, L, A, X
+                    Y[g, t0 + i] = scale * np.abs(q[t0 + i, g]).max() * np.abs(k[:seen]).sum(1).max()
+    return O, L, A, X, Y

@@ -82,7 +82,7 @@ def test_attend_equals_contiguous_decoding():
     table = np.array([[4, 0, 7], [2, 5, 8]])
     lens, n = [37, 48], 1
     q = rng.normal(size=(2, Hkv * G, d))
-    O, L, _, _ = P.attend(q, kb, vb, ks, vs, [0, 1, 2], lens, table, 0.125)
+    O, L, *_ = P.attend(q, kb, vb, ks, vs, [0, 1, 2], lens, table, 0.125)
     k = (P.e4m3_decode(kb) * ks[..., None, None])[table].transpose(0, 2, 1, 3, 4).reshape(2, Hkv, -1, d)
     v = (P.e4m3_decode(vb) * vs[..., None, None])[table].transpose(0, 2, 1, 3, 4).reshape(2, Hkv, -1, d)
     k, v = np.repeat(k, G, 1), np.repeat(v, G, 1)
@@ -97,10 +97,10 @@ def test_attend_causal_rows_see_their_prefix():
     one = np.full((2, 1), 0.004)
     q = rng.normal(size=(5, 2, 64))
     table = np.array([[1, 0]])
-    O, L, _, _ = P.attend(q, kb, vb, one, one, [0, 5], [20], table, 0.1)
+    O, L, *_ = P.attend(q, kb, vb, one, one, [0, 5], [20], table, 0.1)
     for i in range(5):
-        Oi, Li, _, _ = P.attend(q[i:i + 1], kb, vb, one, one, [0, 1], [16 + i], table, 0.1, causal=False)
+        Oi, Li, *_ = P.attend(q[i:i + 1], kb, vb, one, one, [0, 1], [16 + i], table, 0.1, causal=False)
         np.testing.assert_allclose(O[i], Oi[0], rtol=1e-13)
         np.testing.assert_allclose(L[:, i], Li[:, 0], rtol=1e-13)
-    O, L, _, _ = P.attend(q, kb, vb, one, one, [0, 5], [3], table, 0.1)   # two rows before the first token
+    O, L, *_ = P.attend(q, kb, vb, one, one, [0, 5], [3], table, 0.1)   # two rows before the first token
     assert (O[:2] == 0).all() and np.isneginf(L[:, :2]).all() and np.isfinite(L[:, 2:]).all()

@@ -255,14 +255,17 @@ def run_attend(q, c, cu, lens, max_new, causal, dev, scale, junk=7.0):
     return o.double().cpu().numpy(), lse.double().cpu().numpy()
 
 
-def check(o, lse, O, L, A, X, rows, visible, d):
+def check(o, lse, ref, cu, G, rows, visible, d):
     """Bounds. Scores: d products and sums in fp32 (d 2^-24 of sum |q k|), the
     two scale factors and the exponent's argument (4 roundings of 2^-24), Q's
     f16 parts (2^-25 of the row's largest): together below (d + 16) 2^-24 X.
-    Weights: f16 (2^-11), exp2 (2^-22) and twice the score error; weights below
+    Requests of more than 32 rows (new tokens x heads of a group) take Q as two
+    E4M3 parts: 2^-17 of the row's largest, hence 2^-17 Y more. Weights: f16 (2^-11), exp2 (2^-22) and twice the score error; weights below
     2^-31 of the largest vanish. O: that on A = sum P |v|, fp32 sums (2^-20 A),
     and bf16 (2^-8 |O|)."""
-    ds = (d + 16) * 2.0 ** -24 * X[:, rows]
+    O, L, A, X, Y = ref
+    n = np.repeat(np.diff(cu), np.diff(cu))[rows]
+    ds = (d + 16) * 2.0 ** -24 * X[:, rows] + np.where(n * G > 32, 2.0 ** -17, 0.0) * Y[:, rows]
     L, lse = L[:, rows], lse[:, rows]
     empty = np.isneginf(L)
     assert np.array_equal(empty, np.isneginf(lse))
@@ -304,8 +307,8 @@ def test_attend_within_bounds(cuda_device, d, bs, Hkv, G, which):
     scale = 1 / math.sqrt(d)
     for causal in (True, False):
         o, lse = run_attend(q, c, cu, lens, max(n for _, n in pairs), causal, cuda_device, scale)
-        O, L, A, X = P.attend(q.double().cpu().numpy(), *c[:4], cu, lens, c[4], scale, causal)
-        check(o, lse, O, L, A, X, slice(0, total), max(lens), d)
+        ref = P.attend(q.double().cpu().numpy(), *c[:4], cu, lens, c[4], scale, causal)
+        check(o, lse, ref, cu, G, slice(0, total), max(lens), d)
         assert (o[total:] == 7).all() and (lse[:, total:] == 7).all()   # rows behind the last request
 
 
@@ -320,8 +323,8 @@ def test_attend_peaked_and_flat_rows(cuda_device, d):
     q[1] = 0
     q = bf16(q, cuda_device)
     o, lse = run_attend(q, c, cu, lens, 2, True, cuda_device, 0.1)
-    O, L, A, X = P.attend(q.double().cpu().numpy(), *c[:4], cu, lens, c[4], 0.1)
-    check(o, lse, O, L, A, X, slice(0, 4), 1500, d)
+    ref = P.attend(q.double().cpu().numpy(), *c[:4], cu, lens, c[4], 0.1)
+    check(o, lse, ref, cu, 2, slice(0, 4), 1500, d)
 
 
 def test_attend_long_cache_of_one_request(cuda_device):
@@ -331,8 +334,8 @@ def test_attend_long_cache_of_one_request(cuda_device):
     c = make_cache(lens, 64, 1, d, seed=2)
     q = bf16(rng.normal(size=(1, 8, d)), cuda_device)
     o, lse = run_attend(q, c, cu, lens, 1, True, cuda_device, 0.09)
-    O, L, A, X = P.attend(q.double().cpu().numpy(), *c[:4], cu, lens, c[4], 0.09)
-    check(o, lse, O, L, A, X, slice(0, 1), 40000, d)
+    ref = P.attend(q.double().cpu().numpy(), *c[:4], cu, lens, c[4], 0.09)
+    check(o, lse, ref, cu, 8, slice(0, 1), 40000, d)
 
 
 def test_attend_many_requests(cuda_device):
@@ -343,8 +346,71 @@ def test_attend_many_requests(cuda_device):
     c = make_cache(lens, 16, 2, 64, seed=3)
     q = bf16(rng.normal(size=(int(cu[-1]), 4, 64)), cuda_device)
     o, lse = run_attend(q, c, cu, lens, 2, True, cuda_device, 0.125)
-    O, L, A, X = P.attend(q.double().cpu().numpy(), *c[:4], cu, lens, c[4], 0.125)
-    check(o, lse, O, L, A, X, slice(0, int(cu[-1])), 100, 64)
+    ref = P.attend(q.double().cpu().numpy(), *c[:4], cu, lens, c[4], 0.125)
+    check(o, lse, ref, cu, 2, slice(0, int(cu[-1])), 100, 64)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bs", [16, 32, 128, 256])
+@pytest.mark.parametrize("Hkv,G,pairs", [
+    (1, 1, [(0, 33)]), (2, 1, [(0, 300), (7, 1), (1000, 129)]), (1, 8, [(5, 5), (130, 32), (600, 1), (0, 33)]),
+    (1, 5, [(100, 52), (0, 0), (127, 26), (128, 26)]), (1, 40, [(300, 1), (77, 2)])])
+def test_attend_many_rows(cuda_device, d, bs, Hkv, G, pairs):
+    """Prompts and pieces of prompts beside requests of a few rows."""
+    lens = [c + n for c, n in pairs]
+    cu = np.concatenate([[0], np.cumsum([n for _, n in pairs])])
+    total = int(cu[-1])
+    rng = np.random.default_rng(d + bs + G)
+    q = bf16(rng.normal(size=(total + 3, Hkv * G, d)), cuda_device)
+    c = make_cache(lens, bs, Hkv, d, seed=bs + G)
+    scale = 1 / math.sqrt(d)
+    for causal in (True, False):
+        o, lse = run_attend(q, c, cu, lens, max(n for _, n in pairs), causal, cuda_device, scale)
+        ref = P.attend(q.double().cpu().numpy(), *c[:4], cu, lens, c[4], scale, causal)
+        check(o, lse, ref, cu, G, slice(0, total), max(lens), d)
+        assert (o[total:] == 7).all() and (lse[:, total:] == 7).all()
+
+
+def test_attend_many_rows_over_a_long_cache(cuda_device):
+    """One piece of a prompt, its keys split over every CTA."""
+    lens, cu, d = [20000], [0, 40], 128
+    rng = np.random.default_rng(1)
+    c = make_cache(lens, 64, 1, d, seed=2)
+    q = bf16(rng.normal(size=(40, 2, d)), cuda_device)
+    o, lse = run_attend(q, c, cu, lens, 40, True, cuda_device, 0.09)
+    ref = P.attend(q.double().cpu().numpy(), *c[:4], cu, lens, c[4], 0.09)
+    check(o, lse, ref, cu, 2, slice(0, 40), 20000, d)
+    again = run_attend(q, c, cu, lens, 40, True, cuda_device, 0.09)
+    np.testing.assert_array_equal(o, again[0])
+    np.testing.assert_array_equal(lse, again[1])
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_attend_block_scales_far_apart(cuda_device, n):
+    """Blocks of zeros (scale 2^-126 or 0), values 2^20 apart, key scales from
+    none to large, and weights that lie on the small values."""
+    lens, cu, d, bs = [333], [0, n], 64, 16
+    rng = np.random.default_rng(6)
+    kb, vb, ks, vs, table = make_cache(lens, bs, 1, d, seed=2)
+    blocks = table[0]
+    vs[blocks, 0] = (2.0 ** rng.integers(-12, 9, len(blocks))).astype(np.float32)
+    for i, z in ((0, 2.0 ** -126), (3, 0.0), (20, 2.0 ** -126)):
+        vs[blocks[i], 0] = z
+        vb[blocks[i]] = 0
+    ks[blocks, 0] = (rng.uniform(0, 0.2, len(blocks))).astype(np.float32)
+    ks[blocks[5], 0] = 0.0
+    ks[blocks[0], 0] = 2.0 ** -126
+    kb[blocks[0]] = 0
+    q = bf16(rng.normal(size=(n, 2, d)), cuda_device)
+    c = (kb, vb, ks, vs, table)
+    o, lse = run_attend(q, c, cu, lens, n, True, cuda_device, 0.1)
+    ref = P.attend(q.double().cpu().numpy(), *c[:4], cu, lens, table, 0.1)
+    check(o, lse, ref, cu, 2, slice(0, n), 333, d)
+    vb[blocks] = 0                                   # nothing but zeros
+    vs[blocks, 0] = 2.0 ** -126
+    o, lse2 = run_attend(q, c, cu, lens, n, True, cuda_device, 0.1)
+    assert (o == 0).all()
+    np.testing.assert_allclose(lse2, lse, rtol=1e-5)
 
 
 def test_attend_refused_request_and_rows_that_see_nothing(cuda_device):
@@ -355,8 +421,8 @@ def test_attend_refused_request_and_rows_that_see_nothing(cuda_device):
     q = bf16(rng.normal(size=(8, 2, 64)), cuda_device)
     for causal in (True, False):
         o, lse = run_attend(q, c, cu, lens, 5, causal, cuda_device, 0.125)
-        O, L, A, X = P.attend(q.double().cpu().numpy(), *c[:4], cu, lens, c[4], 0.125, causal)
-        check(o, lse, O, L, A, X, slice(0, 8), 20, 64)
+        ref = P.attend(q.double().cpu().numpy(), *c[:4], cu, lens, c[4], 0.125, causal)
+        check(o, lse, ref, cu, 2, slice(0, 8), 20, 64)
 
 
 @pytest.mark.parametrize("d,G,n", [(128, 2, 4), (64, 4, 8), (128, 8, 70), (64, 1, 130)])
@@ -390,8 +456,8 @@ def test_attend_nan_reaches_only_the_rows_that_see_it(cuda_device, d, G, n, old)
         assert (np.isnan(o[i]) == nan).all(), i
         assert (np.isnan(lse[:, i]) == (pos >= first_k)).all()
     rows = slice(0, n // 2)                    # before the first NaN: exact as ever
-    O, L, A, X = P.attend(q.double().cpu().numpy()[rows], *c[:4], [0, n // 2], [old + n // 2], table, 0.125)
-    check(o, lse, O, L, A, X, rows, old + n, d)
+    ref = P.attend(q.double().cpu().numpy()[rows], *c[:4], [0, n // 2], [old + n // 2], table, 0.125)
+    check(o, lse, ref, cu, G, rows, old + n, d)
 
 
 def test_attend_infinite_and_nan_queries_stay_in_their_rows(cuda_device):
@@ -497,7 +563,7 @@ def test_serving_steps(cuda_device):
         fa.cache_append(k, v, c.k, c.v, c.k_scale, c.v_scale, slots)
         o, lse = fa.forward_paged(q, c.k, c.v, c.k_scale, c.v_scale, cu, c.cache_len, c.block_table,
                                   max(max(new), 0), scale=0.125)
-        r, (O, L, A, X) = oracle_step(s, new, *(x.double().cpu().numpy() for x in (k, v, q)), bs, total, 0.125)
+        r, ref = oracle_step(s, new, *(x.double().cpu().numpy() for x in (k, v, q)), bs, total, 0.125)
         for name, t in (("slots", slots), ("cu_seqlens", cu), ("cache_len", c.cache_len),
                         ("block_table", c.block_table), ("free_blocks", c.free_blocks), ("free_state", c.free_state)):
             np.testing.assert_array_equal(t.cpu().numpy(), r[name], err_msg=name)
@@ -506,7 +572,8 @@ def test_serving_steps(cuda_device):
         same_bytes(c.k.view(torch.uint8).cpu().numpy(), s["kb"])
         same_bytes(c.v.view(torch.uint8).cpu().numpy(), s["vb"])
         np.testing.assert_array_equal(c.k_scale.cpu().numpy(), s["ks"].astype(np.float32))
-        check(o.double().cpu().numpy(), lse.double().cpu().numpy(), O, L, A, X, slice(0, total - 1), 400, d)
+        check(o.double().cpu().numpy(), lse.double().cpu().numpy(), ref, r["cu_seqlens"], G,
+              slice(0, total - 1), 400, d)
     assert refused > 0
 
 
