@@ -13,7 +13,7 @@
 //
 // A CTA holds two row tiles so that each V tile is converted once for 256
 // rows. Warps:
-//   0      copies K tiles by TMA, E4M3 as they lie, and their block scales
+//   0      copies K and V tiles by TMA, E4M3 as they lie, and their block scales
 //   1, 2   issue the products of row tile 0, 1 (independent of each other)
 //   3      allocates TMEM
 //   4-7    softmax of row tile 0: thread = row
@@ -47,15 +47,17 @@ constexpr int kPtNanSlots = 4;
 
 template <int D>
 struct PtCfg {
-    static constexpr int KS = D == 128 ? 4 : 6;   // K stages
-    static constexpr int VS = 2;                  // V stages
+    static constexpr int KS = D == 128 ? 3 : 6;   // K stages
+    static constexpr int RS = D == 128 ? 2 : 4;   // stages of V as it lies in the cache
+    static constexpr int VS = 2;                  // stages of converted V
     static constexpr int NREG = D / 64;           // 128-byte-wide regions of an f16 row
     static constexpr int Q_BYTES = D == 128 ? 32768 : 16384;  // high and low parts of a row tile
     static constexpr int K_BYTES = 128 * D;
     static constexpr int V_BYTES = 128 * D * 2;
     static constexpr int Q_OFF = 0;
     static constexpr int K_OFF = Q_OFF + 2 * Q_BYTES;
-    static constexpr int V_OFF = K_OFF + KS * K_BYTES;
+    static constexpr int R_OFF = K_OFF + KS * K_BYTES;
+    static constexpr int V_OFF = R_OFF + RS * K_BYTES;
     static constexpr int SC_OFF = V_OFF + VS * V_BYTES;       // float [slots][24]: ks, log2 vs, 1 / vs of 8 groups
     static constexpr int NAN_OFF = SC_OFF + kPtScaleSlots * 96;  // int [slots][D + 4]: first key with a NaN value
     static constexpr int NAN_STRIDE = (D + 4) * 4;
@@ -70,7 +72,6 @@ struct PtCfg {
 
 struct PtParams {
     const uint16_t* q;
-    const uint8_t* v_cache;
     const float *k_scale, *v_scale;
     uint16_t* o;
     float* lse;
@@ -138,7 +139,8 @@ __device__ __forceinline__ void pt_request(const PtParams& p, int b, PtReq& r) {
 
 template <int D>
 __global__ void __launch_bounds__(512, 1)
-    fa_paged_tile_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ PtParams p) {
+    fa_paged_tile_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                         const __grid_constant__ PtParams p) {
     using C = PtCfg<D>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -181,8 +183,10 @@ __global__ void __launch_bounds__(512, 1)
     uint64_t* sc_full = nan_full + kPtNanSlots;          // [8] scales stored
     uint64_t* k_full = sc_full + kPtScaleSlots;  // [KS]
     uint64_t* k_empty = k_full + C::KS;        // [KS] both row tiles' S done
-    uint64_t* v_full = k_empty + C::KS;        // [VS]
-    uint64_t* v_empty = v_full + C::VS;        // [VS]
+    uint64_t* r_full = k_empty + C::KS;        // [RS] V landed
+    uint64_t* r_empty = r_full + C::RS;        // [RS] V read
+    uint64_t* v_full = r_empty + C::RS;        // [VS] V converted
+    uint64_t* v_empty = v_full + C::VS;        // [VS] both row tiles' P V done
     if (tid == 0) {
         abort_s = 0;
         for (int i = 0; i < 2; ++i) {
@@ -197,6 +201,10 @@ __global__ void __launch_bounds__(512, 1)
         for (int i = 0; i < C::KS; ++i) {
             mbar_init(&k_full[i], 1);
             mbar_init(&k_empty[i], 2);
+        }
+        for (int i = 0; i < C::RS; ++i) {
+            mbar_init(&r_full[i], 1);
+            mbar_init(&r_empty[i], 128);
         }
         for (int i = 0; i < C::VS; ++i) {
             mbar_init(&v_full[i], 128);
@@ -304,7 +312,7 @@ __global__ void __launch_bounds__(512, 1)
         if (warp == 0) {
             // ------------------------------------------------------ K tiles and scales
             const int bs = 1 << p.bs_log2, box = min(bs, 128);
-            int u = 0;
+            int u = 0, klast = -1;
             bool ok = true;
             float* sc = reinterpret_cast<float*>(sm + C::SC_OFF);
             do {
@@ -328,14 +336,12 @@ __global__ void __launch_bounds__(512, 1)
                     if (!(ok = mbar_wait_warp(&k_empty[st], ((u / C::KS) & 1) ^ 1, cx, 95))) break;
                     if (lane == 0) mbar_arrive_expect_tx(&k_full[st], C::K_BYTES);
                     __syncwarp();
-                    // box b covers the groups from b * box / 16 on; its first lane requests it
-                    const int gpb = box >> 4;
-                    if (lane < 8 && lane % gpb == 0) {
-                        const int in = (t * 128 + lane * 16) & (bs - 1);
-                        const long long row = ((static_cast<long long>(id) * p.Hkv + s.hk) << p.bs_log2) + in;
-                        tma_load_2d(sm + C::K_OFF + st * C::K_BYTES + lane * 16 * D, &tmK, 0, static_cast<int>(row),
-                                    &k_full[st]);
-                    }
+                    // the first lane of each box of min(block, 128) rows requests it
+                    const bool asks = lane < 8 && lane % (box >> 4) == 0;
+                    const int row = static_cast<int>(((static_cast<long long>(id) * p.Hkv + s.hk) << p.bs_log2) +
+                                                     ((t * 128 + lane * 16) & (bs - 1)));
+                    if (asks)
+                        tma_load_2d(sm + C::K_OFF + st * C::K_BYTES + lane * 16 * D, &tmK, 0, row, &k_full[st]);
                     float top = vs;
 #pragma unroll
                     for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -350,14 +356,29 @@ __global__ void __launch_bounds__(512, 1)
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sc_full[slot]);
+                    const int rs = u % C::RS;
+                    if (!(ok = mbar_wait_warp(&r_empty[rs], ((u / C::RS) & 1) ^ 1, cx, 107))) {
+                        klast = u + 1;
+                        break;
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(&r_full[rs], C::K_BYTES);
+                    __syncwarp();
+                    if (asks)
+                        tma_load_2d(sm + C::R_OFF + rs * C::K_BYTES + lane * 16 * D, &tmV, 0, row, &r_full[rs]);
                 }
             } while (ok && next(s));
             // let every copy in flight land before the CTA can exit
-            if (lane == 0)
-                for (int i = 0; i < C::KS && i < u; ++i) {
-                    const int last = i + ((u - 1 - i) / C::KS) * C::KS;
+            if (lane == 0) {
+                const int nk = max(u, klast);
+                for (int i = 0; i < C::KS && i < nk; ++i) {
+                    const int last = i + ((nk - 1 - i) / C::KS) * C::KS;
                     mbar_wait_teardown(&k_full[i], (last / C::KS) & 1, 200000000ull);
                 }
+                for (int i = 0; i < C::RS && i < u; ++i) {
+                    const int last = i + ((u - 1 - i) / C::RS) * C::RS;
+                    mbar_wait_teardown(&r_full[i], (last / C::RS) & 1, 200000000ull);
+                }
+            }
         } else if (warp < 3) {
             // ------------------------------------------------------ products of row tile i
             const int i = warp - 1;
@@ -612,7 +633,8 @@ __global__ void __launch_bounds__(512, 1)
             const bool whole = s.c0 == 0 && s.c1 == s.ntile;
             const int slot = 2 * static_cast<int>(blockIdx.x) + (s.line0 <= x0 ? 0 : 1);
             const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-            float* po = p.po + (static_cast<size_t>(slot) * kPagedTileRows + i * 128 + r) * D;
+            // partial outputs lie as [d / 4][128 rows] float4, coalesced over the rows
+            float4* po = reinterpret_cast<float4*>(p.po) + (static_cast<size_t>(2 * slot + i) * (D / 4)) * 128 + r;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t ov[32];
@@ -643,8 +665,9 @@ __global__ void __launch_bounds__(512, 1)
                 } else {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        reinterpret_cast<uint4*>(po + c * 32)[k] =
-                            make_uint4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
+                        po[(c * 8 + k) * 128] =
+                            make_float4(__uint_as_float(ov[4 * k]), __uint_as_float(ov[4 * k + 1]),
+                                        __uint_as_float(ov[4 * k + 2]), __uint_as_float(ov[4 * k + 3]));
                 }
             }
             tc_fence_before();  // O has been read: the next piece's products may overwrite it
@@ -665,36 +688,48 @@ __global__ void __launch_bounds__(512, 1)
                 named_sync(1 + i, 128);
                 if (last_s[i]) {
                     __threadfence();
-                    // a warp per row, lanes over the columns
-                    for (int rr = wq; rr < 128 && base + rr < rows; rr += 4) {
-                        float M = -CUDART_INF_F, L = 0.f, acc[D / 32];
+                    auto piece = [&](int cta) { return 2 * cta + (s.line0 <= quota * cta ? 0 : 1); };
+                    float M = -CUDART_INF_F, L = 0.f;
+                    for (int cta = f; cta <= e; ++cta)
+                        M = fmaxf(M, __ldcg(&p.pm[piece(cta) * kPagedTileRows + i * 128 + r]));
 #pragma unroll
-                        for (int k = 0; k < D / 32; ++k) acc[k] = 0.f;
+                    for (int c = 0; c < D / 32; ++c) {
+                        float4 acc[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        L = 0.f;
                         for (int cta = f; cta <= e; ++cta) {
-                            const int sl = 2 * cta + (s.line0 <= quota * cta ? 0 : 1);
-                            M = fmaxf(M, __ldcg(&p.pm[sl * kPagedTileRows + i * 128 + rr]));
-                        }
-                        for (int cta = f; cta <= e; ++cta) {
-                            const int sl = 2 * cta + (s.line0 <= quota * cta ? 0 : 1);
-                            const size_t at = static_cast<size_t>(sl) * kPagedTileRows + i * 128 + rr;
+                            const int sl = piece(cta), at = sl * kPagedTileRows + i * 128 + r;
                             const float mc = __ldcg(&p.pm[at]);
                             const float w = mc == -CUDART_INF_F ? 0.f : ex2_approx(mc - M);
                             L = fmaf(w, __ldcg(&p.pl[at]), L);
+                            const float4* src = reinterpret_cast<const float4*>(p.po) +
+                                                (static_cast<size_t>(2 * sl + i) * (D / 4) + c * 8) * 128 + r;
 #pragma unroll
-                            for (int k = 0; k < D / 32; ++k)
-                                acc[k] = fmaf(w, __ldcg(&p.po[at * D + k * 32 + lane]), acc[k]);
+                            for (int k = 0; k < 8; ++k) {
+                                const float4 v = __ldcg(src + k * 128);
+                                acc[k].x = fmaf(w, v.x, acc[k].x);
+                                acc[k].y = fmaf(w, v.y, acc[k].y);
+                                acc[k].z = fmaf(w, v.z, acc[k].z);
+                                acc[k].w = fmaf(w, v.w, acc[k].w);
+                            }
                         }
-                        const int tk = (base + rr) / p.G, hh = s.hk * p.G + (base + rr) - tk * p.G;
-                        const size_t at = (static_cast<size_t>(s.r.tok0 + tk) * p.Hq + hh) * D;
                         const float iL = L == 0.f ? 0.f : 1.f / L;
+                        if (row_ok) {
 #pragma unroll
-                        for (int k = 0; k < D / 32; ++k)
-                            p.o[at + k * 32 + lane] =
-                                static_cast<uint16_t>(pack_bf16x2(acc[k] * iL, 0.f) & 0xFFFFu);
-                        if (lane == 0)
-                            p.lse[static_cast<size_t>(hh) * p.total + s.r.tok0 + tk] =
-                                L == 0.f ? -CUDART_INF_F : (M - lse_off + log2f(L)) * kPtLn2;
+                            for (int k = 0; k < 4; ++k) {
+                                uint4 w;
+                                w.x = pack_bf16x2(acc[2 * k].x * iL, acc[2 * k].y * iL);
+                                w.y = pack_bf16x2(acc[2 * k].z * iL, acc[2 * k].w * iL);
+                                w.z = pack_bf16x2(acc[2 * k + 1].x * iL, acc[2 * k + 1].y * iL);
+                                w.w = pack_bf16x2(acc[2 * k + 1].z * iL, acc[2 * k + 1].w * iL);
+                                reinterpret_cast<uint4*>(p.o + qrow + c * 32)[k] = w;
+                            }
+                        }
                     }
+                    if (row_ok)
+                        p.lse[static_cast<size_t>(hq) * p.total + s.r.tok0 + tok] =
+                            L == 0.f ? -CUDART_INF_F : (M - lse_off + log2f(L)) * kPtLn2;
                 }
             }
             if (nan_seen) {
@@ -710,29 +745,23 @@ __global__ void __launch_bounds__(512, 1)
         const int r = (warp - 12) * 32 + lane;
         int u = 0, seg = 0;
         bool ok = true;
-        uint4 x[D / 16];
-        auto load = [&](const PtSeg& q, int t) {
-            const int key = t * 128 + r;
-            int id = -1;
-            if (key < q.r.len) id = p.block_table[static_cast<size_t>(q.r.b) * p.max_blocks + (key >> p.bs_log2)];
-            const bool in = id >= 0 && id < p.num_blocks;
-            const uint8_t* src =
-                p.v_cache + ((((static_cast<size_t>(in ? id : 0) * p.Hkv + q.hk) << p.bs_log2) +
-                              (key & ((1 << p.bs_log2) - 1))) * D);
-#pragma unroll
-            for (int j = 0; j < D / 16; ++j)
-                x[j] = in ? __ldg(reinterpret_cast<const uint4*>(src) + j) : make_uint4(0u, 0u, 0u, 0u);
-        };
-        load(s, s.c0);
         do {
             const int rows = s.r.n * p.G;
             const int vis_min = pt_visible(p, s.r, s.pair * 256 / p.G);
             const int vis_max = pt_visible(p, s.r, min(s.pair * 256 + 255, rows - 1) / p.G);
             int* nf = nan_first + (seg % kPtNanSlots) * (D + 4);
-            PtSeg n = s;
-            bool more = true;
             for (int t = s.c0; t < s.c1; ++t, ++u) {
-                const int vs = u % C::VS;
+                const int vs = u % C::VS, rs = u % C::RS;
+                ok = mbar_wait_warp(&r_full[rs], (u / C::RS) & 1, cx, 108);
+                if (!ok) break;
+                // row r as TMA swizzled it (d = 64: two bits of the row index
+                // above its 64-byte pair)
+                uint4 x[D / 16];
+                const uint32_t rb = smem_u32(sm + C::R_OFF + rs * C::K_BYTES) + r * D;
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j)
+                    x[j] = lds128_u4(rb + ((D == 128 ? j ^ (r & 7) : j ^ ((r >> 1) & 3)) << 4));
+                mbar_arrive(&r_empty[rs]);
                 ok = mbar_wait_warp(&v_empty[vs], ((u / C::VS) & 1) ^ 1, cx, 106);
                 if (!ok) break;
                 if (t * 128 + 128 > vis_min) {
@@ -776,18 +805,13 @@ __global__ void __launch_bounds__(512, 1)
                     sts128(smem_u32(reg + ((c ^ (r & 7)) << 4)), h[0], h[1], h[2], h[3]);
                     sts128(smem_u32(reg + (((c + 1) ^ (r & 7)) << 4)), h[4], h[5], h[6], h[7]);
                 }
-                // the next tile's row is on its way while this one is multiplied
-                if (t + 1 < s.c1) load(s, t + 1);
-                else if ((more = next(n))) load(n, n.c0);
                 fence_proxy_async_smem();
                 mbar_arrive(&v_full[vs]);
             }
             if (!ok) break;
             mbar_arrive(&nan_full[seg % kPtNanSlots]);
             ++seg;
-            if (!more) break;
-            s = n;
-        } while (true);
+        } while (next(s));
     }
     tc_fence_before();
     __syncthreads();
@@ -797,9 +821,9 @@ __global__ void __launch_bounds__(512, 1)
     }
 }
 
-// K as [num_blocks * Hkv * block_size rows, d] in boxes of a block (at most
+// K or V as [num_blocks * Hkv * block_size rows, d] in boxes of a block (at most
 // 128 rows), with the swizzle of its row length.
-static bool make_tmap_k(CUtensorMap* map, const void* base, uint64_t rows, int d, uint32_t box_rows) {
+static bool make_tmap_rows(CUtensorMap* map, const void* base, uint64_t rows, int d, uint32_t box_rows) {
     EncodeTiledFn fn = encode_tiled_fn();
     if (!fn) return false;
     cuuint64_t gdim[2] = {static_cast<cuuint64_t>(d), rows};
@@ -814,19 +838,20 @@ static bool make_tmap_k(CUtensorMap* map, const void* base, uint64_t rows, int d
 template <int D>
 static cudaError_t launch_tile(const PagedArgs& a, const PtParams& p, cudaStream_t stream) {
     using C = PtCfg<D>;
-    CUtensorMap tk;
+    CUtensorMap tk, tv;
     const uint64_t rows = static_cast<uint64_t>(a.num_blocks) * a.Hkv * a.block_size;
-    if (!make_tmap_k(&tk, a.k_cache, rows, D, a.block_size < 128 ? a.block_size : 128)) return cudaErrorInvalidValue;
+    const uint32_t box = a.block_size < 128 ? a.block_size : 128;
+    if (!make_tmap_rows(&tk, a.k_cache, rows, D, box) || !make_tmap_rows(&tv, a.v_cache, rows, D, box))
+        return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(fa_paged_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    fa_paged_tile_kernel<D><<<kPagedCtas, 512, C::SMEM, stream>>>(tk, p);
+    fa_paged_tile_kernel<D><<<kPagedCtas, 512, C::SMEM, stream>>>(tk, tv, p);
     return cudaGetLastError();
 }
 
 cudaError_t launch_paged_tile(const PagedArgs& a, cudaStream_t stream) {
     PtParams p;
     p.q = static_cast<const uint16_t*>(a.q);
-    p.v_cache = a.v_cache;
     p.k_scale = a.k_scale;
     p.v_scale = a.v_scale;
     p.o = static_cast<uint16_t*>(a.o);
