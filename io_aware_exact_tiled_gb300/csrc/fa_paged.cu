@@ -15,16 +15,18 @@
 // Design:
 //   * Work is counted in chunks of 32 keys. A unit is (request, key head), with
 //     at most RT = 8, 16 or 32 query rows (fa_paged_tile.cu takes requests of
-//     more); the units' chunks form one line that is cut into
-//     equal quotas, one for each persistent CTA, so ragged lengths balance by
+//     more). The chunks of the long units form one line that is cut into equal
+//     quotas, one for each persistent CTA, so ragged lengths balance by
 //     themselves and one long request spreads over the whole GPU. A unit that
 //     was cut leaves partial (m, l, O) in the workspace and the CTA that
 //     finishes last merges them, in the order of the CTAs (the same result
-//     every time).
-//   * Each of a CTA's eight warps streams its own chunks (every eighth one)
-//     through its own ring of TMA boxes with its own mbarriers: no barrier
-//     between warps before a unit ends. Block ids and scales are fetched for
-//     32 chunks at once, a lane for each.
+//     every time). Short units (no longer than a warp's even share of all
+//     chunks) are not worth a CTA's barriers: each is one warp's, from its Q
+//     to its output.
+//   * Each of a CTA's eight warps streams its own chunks (of a long unit every
+//     eighth one) through its own ring of TMA boxes with its own mbarriers:
+//     no barrier between warps before a long unit ends. Block ids are fetched
+//     three chunks ahead of the copies that need them.
 //   * S^T = K Q^T and O^T = V^T P^T as m16n8k16 products with f16 operands
 //     and fp32 sums, keys respectively head columns along M, the query rows
 //     along N: eight rows cost no more than one. E4M3 converts to f16 exactly,
@@ -39,6 +41,7 @@
 //     11 bits down to 2^-20 of the maximum and vanish below 2^-30.
 //   * ks multiplies S, vs the product of each chunk: neither scale is folded
 //     into an 8- or 16-bit number.
+#include <limits.h>
 #include <math_constants.h>
 
 #include "fa_paged.h"
@@ -52,30 +55,34 @@ constexpr float kPgRescale = 8.0f;  // log2 units
 constexpr float kPgOffset = 6.0f;   // log2 of the factor on P before its rounding to f16
 constexpr int kPgChunk = 32;        // keys of a chunk
 constexpr int kPgWarps = 8;
+constexpr int kPgAhead = 3;         // chunks between the fetch of a block id and its use
 
 template <int D, int NT, bool B16>
 struct PgCfg {
-    static constexpr int RT = 8 * NT;                     // query rows of a tile
-    static constexpr int STAGES = NT == 4 ? 2 : (D == 64 ? 5 : 3);
+    static constexpr int RT = 8 * NT;                     // query rows of a unit
+    static constexpr int STAGES = D == 64 ? (NT == 4 ? 4 : 5) : (NT == 1 ? 3 : 2);
     static constexpr int TILE = kPgChunk * D;             // bytes of a chunk's K (or V)
     static constexpr int SUBS = B16 ? 2 : 1;              // boxes of a tile
     static constexpr int BOX = TILE / SUBS;
     static constexpr int KK = D / 16;                     // k steps of S
     static constexpr int MI = D / 16;                     // m tiles of O^T
     static constexpr int RED_F = 4 * NT * 32;             // floats of one m tile of a warp's O^T
-    static constexpr int RED_M = 4 / NT > 0 ? 4 / NT : 1; // m tiles merged at a time
+    static constexpr int RED_M = 4;                       // m tiles merged at a time
     static constexpr int RING_OFF = 0;
     static constexpr int RING = kPgWarps * STAGES * 2 * TILE;
-    static constexpr int RED_OFF = RING_OFF + RING;       // fp32 [8 warps][RED_M][RED_F]
-    static constexpr int Q_OFF = RED_OFF + kPgWarps * RED_M * RED_F * 4;  // f16 fragments of Q
-    static constexpr int ML_OFF = Q_OFF + RT * D * 2;     // fp32 [8 warps][RT][2]
-    static constexpr int ROW_OFF = ML_OFF + kPgWarps * RT * 8;  // {score factor, visible keys} of each row
-    static constexpr int META_OFF = ROW_OFF + RT * 8;     // float4 [8 warps][STAGES]: ks0, ks1, vs0, vs1
-    static constexpr int NAN_OFF = META_OFF + kPgWarps * STAGES * 16;  // int [D] first key with a NaN value
-    static constexpr int BAR_OFF = NAN_OFF + D * 4;
-    static constexpr int USED = BAR_OFF + kPgWarps * STAGES * 8 + 64;
+    static constexpr int RED_OFF = RING_OFF + RING;       // fp32 [8 warps][RED_M][RED_F] or f16 Q of each warp's unit
+    static constexpr int Q_BYTES = RT * D * 2;            // f16 fragments of Q
+    static constexpr int Q_OFF = RED_OFF + kPgWarps * RED_M * RED_F * 4;  // of a long unit
+    static constexpr int ML_OFF = Q_OFF + Q_BYTES;        // fp32 [8 warps + 1][RT][2]
+    static constexpr int ROW_OFF = ML_OFF + (kPgWarps + 1) * RT * 8;  // [8] {score factor, visible keys} of each row
+    static constexpr int META_OFF = ROW_OFF + kPgWarps * RT * 8;  // float4 [8][STAGES]: ks0, ks1, vs0, vs1
+    static constexpr int NAN_OFF = META_OFF + kPgWarps * STAGES * 16;  // int [8][D] first key with a NaN value
+    static constexpr int ID_OFF = NAN_OFF + kPgWarps * D * 4;  // int [8][4][2] block ids on their way
+    static constexpr int BAR_OFF = ID_OFF + kPgWarps * 32;
+    static constexpr int USED = BAR_OFF + kPgWarps * STAGES * 8;
     static constexpr int SMEM = USED + 1024;
-    static_assert(SMEM <= 232448 - 2048, "shared memory");
+    static_assert(kPgWarps * RED_M * RED_F * 4 >= kPgWarps * Q_BYTES, "Q of the warps' units");
+    static_assert(SMEM <= 232448 - 4096, "shared memory");
 };
 
 struct PagedParams {
@@ -120,6 +127,15 @@ __device__ __forceinline__ uint2 lds64(uint32_t saddr) {
     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(saddr));
     return v;
 }
+// Asynchronous copy of four bytes to shared memory, in groups.
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>  // all but the newest N groups of this thread have landed
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 // Bytes of x that are E4M3 NaN (0x7F or 0xFF) as 0x80 bits.
 __device__ __forceinline__ uint32_t e4m3_nan_bits(uint32_t x) { return ((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
@@ -145,7 +161,9 @@ struct PgSeg {
     int n, len, tok0;   // new tokens (0: none, or the row-tile kernel's), length, first token
     int nchunk;         // chunks of each of the request's units; 0 without rows
     int c0, c1;         // this piece's chunks
-    long long line0;    // position of the unit's first chunk on the line of all chunks
+    bool alone;         // a short unit, one warp's
+    long long rline;    // position of the request's first chunk on its line
+    long long line0;    // position of a long unit's first chunk
 };
 
 // Loads request b (sizes clamped to what the tables can hold).
@@ -166,13 +184,14 @@ __global__ void __launch_bounds__(256, 1)
     constexpr int RT = C::RT;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    __shared__ long long scan_w[kPgWarps];
+    __shared__ long long scan_w[2][kPgWarps];
+    __shared__ long long short_base[257];  // chunks of short units in front of each thread's requests
     __shared__ int start_b, last_s;
     __shared__ long long start_line;
     __shared__ int nan_seen, abort_s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
 
-    // ---- the line of chunks: total length, and the request at this CTA's start
+    // ---- all chunks, then the lines of long and of short units
     const int per = (p.B + 255) / 256;
     const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
     long long mw = 0;
@@ -185,13 +204,6 @@ __global__ void __launch_bounds__(256, 1)
         bad |= raw < 0 || nxt < raw || nxt > p.total || nxt - raw > p.max_new || len != s.len;
     }
     if (bad && blockIdx.x == 0) atomicCAS(p.status, 0, FA_DEV_INVALID | (90 << 8));
-    long long iw = mw;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const long long a = __shfl_up_sync(0xffffffffu, iw, off);
-        if (lane >= off) iw += a;
-    }
-    if (lane == 31) scan_w[warp] = iw;
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::BAR_OFF) + warp * C::STAGES;
     if (tid == 0) {
         abort_s = 0;
@@ -200,24 +212,69 @@ __global__ void __launch_bounds__(256, 1)
         fence_barrier_init();
     }
     int* first_nan = reinterpret_cast<int*>(sm + C::NAN_OFF);
-    for (int i = tid; i < D; i += 256) first_nan[i] = INT_MAX;
+    for (int i = tid; i < kPgWarps * D; i += 256) first_nan[i] = INT_MAX;
+    long long sum = mw;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (lane == 0) scan_w[0][warp] = sum;
     __syncthreads();
-    long long W = 0, bw = 0;
-    for (int w = 0; w < kPgWarps; ++w) {
-        if (w < warp) bw += scan_w[w];
-        W += scan_w[w];
+    long long W = 0;
+    for (int w = 0; w < kPgWarps; ++w) W += scan_w[0][w];
+    // A unit of up to a third of a warp's even share of all chunks is short,
+    // and one of up to twelve chunks always: a long unit costs its CTA some
+    // microseconds of barriers and merging, a short one keeps one warp busy for
+    // about 1.3 us a chunk while other warps may have nothing left.
+    const long long share = W / (static_cast<long long>(gridDim.x) * kPgWarps);
+    const int T = static_cast<int>(min(max(share / 3, 12ll), 1ll << 30));
+    auto line_long = [&](const PgSeg& s) { return s.nchunk > T ? static_cast<long long>(p.Hkv) * s.nchunk : 0ll; };
+    auto line_short = [&](const PgSeg& s) { return s.nchunk <= T ? static_cast<long long>(p.Hkv) * s.nchunk : 0ll; };
+    long long ml_ = 0, ms = 0;
+    for (int b = b0; b < b1; ++b) {
+        PgSeg s;
+        pg_request(p, b, s);
+        ml_ += line_long(s);
+        ms += line_short(s);
     }
-    // equal quotas, at least one chunk for each warp
-    long long quota = (W + gridDim.x - 1) / gridDim.x;
-    quota = quota < kPgWarps ? kPgWarps : quota;
-    const long long x0 = quota * blockIdx.x, x1 = min(x0 + quota, W);
-    if (x0 >= x1) return;  // uniform over the CTA
-    bw += iw - mw;
-    if (x0 >= bw && x0 < bw + mw) {
+    long long il = ml_, is_ = ms;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long a = __shfl_up_sync(0xffffffffu, il, off), c = __shfl_up_sync(0xffffffffu, is_, off);
+        if (lane >= off) {
+            il += a;
+            is_ += c;
+        }
+    }
+    __syncthreads();
+    if (lane == 31) {
+        scan_w[0][warp] = il;
+        scan_w[1][warp] = is_;
+    }
+    __syncthreads();
+    long long Wl = 0, Ws = 0, bw = il - ml_, bs = is_ - ms;
+    for (int w = 0; w < kPgWarps; ++w) {
+        if (w < warp) {
+            bw += scan_w[0][w];
+            bs += scan_w[1][w];
+        }
+        Wl += scan_w[0][w];
+        Ws += scan_w[1][w];
+    }
+    // equal quotas of the long line, at least one chunk for each warp
+    const long long quota = max((Wl + gridDim.x - 1) / static_cast<long long>(gridDim.x),
+                                static_cast<long long>(kPgWarps));
+    const long long x0 = quota * blockIdx.x, x1 = min(x0 + quota, Wl);
+    // the short units that start in this warp's part of their line; parts that
+    // follow one another lie in different CTAs
+    const long long nwarp = static_cast<long long>(gridDim.x) * kPgWarps;
+    const long long part = (Ws + nwarp - 1) / nwarp;
+    const long long y0 = part * (static_cast<long long>(warp) * gridDim.x + blockIdx.x), y1 = min(y0 + part, Ws);
+    short_base[tid] = bs;
+    if (tid == 255) short_base[256] = Ws;
+    if (x0 < x1 && x0 >= bw && x0 < bw + ml_) {
         for (int b = b0; b < b1; ++b) {
             PgSeg s;
             pg_request(p, b, s);
-            const long long w = static_cast<long long>(p.Hkv) * s.nchunk;
+            const long long w = line_long(s);
             if (x0 < bw + w) {
                 start_b = b;
                 start_line = bw;
@@ -228,107 +285,179 @@ __global__ void __launch_bounds__(256, 1)
     }
     __syncthreads();
 
-    // the piece that starts at position x of the line, given a request at or
-    // before it (which starts at rline)
-    auto place = [&](PgSeg& s, long long& rline, long long x) {
+    // ---- the pieces of this warp: first its share of the CTA's pieces of long
+    // units, then its short units
+    auto place = [&](PgSeg& s, long long x) {  // long: the piece that starts at x, here or in a later request
         for (;;) {
-            const long long w = static_cast<long long>(p.Hkv) * s.nchunk;
-            if (x < rline + w) break;
-            rline += w;
+            const long long w = line_long(s);
+            if (x < s.rline + w) break;
+            s.rline += w;
             ++s.b;
             pg_request(p, s.b, s);
         }
-        const long long r = x - rline;
+        const long long r = x - s.rline;
         s.hk = static_cast<int>(r / s.nchunk);
         s.c0 = static_cast<int>(r - static_cast<long long>(s.hk) * s.nchunk);
         s.line0 = x - s.c0;
         s.c1 = static_cast<int>(min(static_cast<long long>(s.nchunk), x1 - s.line0));
     };
+    auto settle = [&](PgSeg& s) -> bool {  // short: hk names the wanted unit of request b, or one past its last
+        while (s.hk >= p.Hkv || s.nchunk == 0 || s.nchunk > T) {
+            s.rline += line_short(s);
+            if (s.rline >= y1) return false;
+            ++s.b;
+            s.hk = 0;
+            pg_request(p, s.b, s);
+        }
+        s.c0 = 0;
+        s.c1 = s.nchunk;
+        return s.rline + static_cast<long long>(s.hk) * s.nchunk < y1;
+    };
+    auto first_short = [&](PgSeg& s) -> bool {
+        if (y0 >= y1) return false;
+        s.alone = true;
+        // the thread whose requests hold position y0
+        int lo = 0;
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t in = __ballot_sync(0xffffffffu, short_base[i * 32 + lane] <= y0);
+            if (in) lo = i * 32 + 31 - __clz(in);
+        }
+        s.b = lo * per;
+        s.rline = short_base[lo];
+        pg_request(p, s.b, s);
+        for (;;) {
+            const long long w = line_short(s);
+            if (y0 < s.rline + w) break;
+            s.rline += w;
+            ++s.b;
+            pg_request(p, s.b, s);
+        }
+        s.hk = static_cast<int>((y0 - s.rline + s.nchunk - 1) / s.nchunk);
+        return settle(s);
+    };
+    auto next = [&](PgSeg& s) -> bool {
+        if (s.alone) {
+            ++s.hk;
+            return settle(s);
+        }
+        const long long x = s.line0 + s.c1;
+        if (x >= x1) return first_short(s);
+        place(s, x);
+        return true;
+    };
     PgSeg cs, is;  // pieces being consumed and being requested
-    long long crl = start_line, irl = start_line;
-    cs.b = is.b = start_b;
-    pg_request(p, cs.b, cs);
-    pg_request(p, is.b, is);
-    place(cs, crl, x0);
-    place(is, irl, x0);
+    bool work = true, iwork = true;
+    if (x0 < x1) {
+        cs.alone = false;
+        cs.b = start_b;
+        cs.rline = start_line;
+        pg_request(p, cs.b, cs);
+        place(cs, x0);
+    } else {
+        work = iwork = first_short(cs);
+    }
+    is = cs;
 
     const WaitCtx cx{reinterpret_cast<volatile int*>(&abort_s), p.status};
     uint8_t* ring = sm + C::RING_OFF + warp * C::STAGES * 2 * C::TILE;
     float4* meta = reinterpret_cast<float4*>(sm + C::META_OFF) + warp * C::STAGES;
-    // ---- requests of this warp: chunk c0 + warp + 8 k of each piece
-    int ik = 0, issued = 0, consumed = 0;
-    bool idone = false;
-    float bks[C::SUBS], bvs[C::SUBS];  // batch of 32 of them: block ids and scales, a lane each
-    int bid[C::SUBS];
-    auto fetch = [&]() {
-        const int c = is.c0 + warp + kPgWarps * (ik + lane);
-#pragma unroll
-        for (int u = 0; u < C::SUBS; ++u) {
-            bid[u] = 0;
-            bks[u] = bvs[u] = 0.f;
-            const int key = c * kPgChunk + u * 16;
-            if (c < is.c1 && key < is.len) {
-                const int id = p.block_table[static_cast<size_t>(is.b) * p.max_blocks + (key >> p.bs_log2)];
-                if (id >= 0 && id < p.num_blocks) {
-                    bid[u] = id;
-                    bks[u] = p.k_scale[static_cast<size_t>(id) * p.Hkv + is.hk];
-                    bvs[u] = p.v_scale[static_cast<size_t>(id) * p.Hkv + is.hk];
-                } else {
-                    atomicCAS(p.status, 0, FA_DEV_INVALID | (91 << 8));
-                }
-            }
-        }
-    };
-    fetch();
-    auto issue = [&]() {
-        // the next chunk, if this warp has one
-        while (!idone && is.c0 + warp + kPgWarps * ik >= is.c1) {
-            const long long x = is.line0 + is.c1;
-            if (x >= x1) {
-                idone = true;
-                break;
-            }
-            place(is, irl, x);
+    // ---- requests of this warp: chunk c0 + warp + 8 k of a long piece, c0 + k
+    // of a short unit. A chunk's loads depend on one another (block id, then
+    // the copies and the scales), so the ids come three chunks ahead of the
+    // copies, and both they and the scales go to shared memory by asynchronous
+    // copies. Step j commits one group: the ids of chunk j + 3 and the scales
+    // of chunk j.
+    auto chunk_of = [&](const PgSeg& s, int k) { return s.alone ? s.c0 + k : s.c0 + warp + kPgWarps * k; };
+    int* idq = reinterpret_cast<int*>(sm + C::ID_OFF) + warp * 8;  // [4][2] block ids
+    int ik = 0, issued = 0, consumed = 0, fetched = 0;
+    int hk_in[kPgAhead] = {};  // (key head << bs_log2) + first row; -1: no chunk
+    int in_len[kPgAhead] = {};  // boxes with keys in front of the last token's end
+    auto fetch = [&](int at) {
+        while (iwork && chunk_of(is, ik) >= is.c1) {
+            iwork = next(is);
             ik = 0;
-            fetch();
-        }
-        if (idone) return;
-        const int c = is.c0 + warp + kPgWarps * ik, st = issued % C::STAGES;
-        if (lane == (ik & 31)) {
-            meta[st] = make_float4(bks[0], bks[C::SUBS - 1], bvs[0], bvs[C::SUBS - 1]);
-            mbar_arrive_expect_tx(&bars[st], 2 * C::TILE);
-#pragma unroll
-            for (int u = 0; u < C::SUBS; ++u) {
-                // rows of the [num_blocks * Hkv * block_size * d / 128, 128] matrix
-                const int in = B16 ? 0 : (c * kPgChunk) & ((1 << p.bs_log2) - 1);
-                const long long key = (static_cast<long long>(bid[u]) * p.Hkv + is.hk << p.bs_log2) + in;
-                const int row = static_cast<int>(D == 128 ? key : key >> 1);
-                tma_load_2d(ring + (2 * st) * C::TILE + u * C::BOX, &tmK, 0, row, &bars[st]);
-                tma_load_2d(ring + (2 * st + 1) * C::TILE + u * C::BOX, &tmV, 0, row, &bars[st]);
+            if (iwork && lane < is.n * p.G) {  // its query rows will be wanted soon
+                const int tok = lane / p.G;
+                const uint16_t* row =
+                    p.q + (static_cast<size_t>(is.tok0 + tok) * p.Hq + is.hk * p.G + (lane - tok * p.G)) * D;
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(row));
+                if (D == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + 64));
             }
         }
-        __syncwarp();
-        ++issued;
+        hk_in[at] = -1;
+        if (!iwork) return;
+        const int key0 = chunk_of(is, ik) * kPgChunk, key = key0 + 16 * lane;
+        hk_in[at] = (is.hk << p.bs_log2) + (B16 ? 0 : key0 & ((1 << p.bs_log2) - 1));
+        in_len[at] = key0 >= is.len ? 0 : key0 + 16 < is.len ? 2 : 1;
+        if (lane < C::SUBS && key < is.len)
+            cp_async4(&idq[(fetched & 3) * 2 + lane],
+                      &p.block_table[static_cast<size_t>(is.b) * p.max_blocks + (key >> p.bs_log2)]);
+        ++fetched;
         ++ik;
-        if ((ik & 31) == 0) fetch();
     };
+    auto issue = [&]() {
+        cp_async_wait<2>();
+        __syncwarp();
+        const int hi = hk_in[0];
+        if (hi >= 0) {
+            const int st = issued % C::STAGES;
+            if (lane == 0) mbar_arrive_expect_tx(&bars[st], 2 * C::TILE);
+            __syncwarp();
+            // lane 0 (and 1, for a second box) requests the copies, lanes 0..3 the scales
+            const int sub = C::SUBS == 2 ? lane & 1 : 0, raw = idq[(issued & 3) * 2 + sub];
+            const bool named = sub < in_len[0], good = named && raw >= 0 && raw < p.num_blocks;
+            const int id = good ? raw : 0;
+            if (lane < C::SUBS) {
+                if (named && !good) atomicCAS(p.status, 0, FA_DEV_INVALID | (91 << 8));
+                // rows of the [num_blocks * Hkv * block_size * d / 128, 128] matrix
+                const long long key = ((static_cast<long long>(id) * p.Hkv) << p.bs_log2) + hi;
+                const int row = static_cast<int>(D == 128 ? key : key >> 1);
+                tma_load_2d(ring + (2 * st) * C::TILE + sub * C::BOX, &tmK, 0, row, &bars[st]);
+                tma_load_2d(ring + (2 * st + 1) * C::TILE + sub * C::BOX, &tmV, 0, row, &bars[st]);
+            }
+            if (lane < 4) {
+                float* dst = reinterpret_cast<float*>(&meta[st]) + lane;
+                if (good)
+                    cp_async4(dst, (lane < 2 ? p.k_scale : p.v_scale) + static_cast<size_t>(id) * p.Hkv +
+                                       (hi >> p.bs_log2));
+                else
+                    *dst = 0.f;
+            }
+            ++issued;
+        }
+#pragma unroll
+        for (int i = 0; i + 1 < kPgAhead; ++i) {
+            hk_in[i] = hk_in[i + 1];
+            in_len[i] = in_len[i + 1];
+        }
+        fetch(kPgAhead - 1);
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kPgAhead; ++i) {
+        fetch(i);
+        cp_async_commit();
+    }
 #pragma unroll 1
     for (int i = 0; i < C::STAGES; ++i) issue();
 
-    uint8_t* qs = sm + C::Q_OFF;
-    float2* rowc = reinterpret_cast<float2*>(sm + C::ROW_OFF);
     float2* ml = reinterpret_cast<float2*>(sm + C::ML_OFF);
     float* red = reinterpret_cast<float*>(sm + C::RED_OFF);
     bool ok = true;
 
 #pragma unroll 1
-    for (;;) {
+    while (work) {
         // ---------------------------------------------------- the piece's rows
         const int nrow = cs.n * p.G;  // rows of the request: token * G + head of the group
+        uint8_t* qs = cs.alone ? sm + C::RED_OFF + warp * C::Q_BYTES : sm + C::Q_OFF;
+        float2* rowc = reinterpret_cast<float2*>(sm + C::ROW_OFF) + (cs.alone ? warp * RT : 0);
+        int* nan_at = first_nan + (cs.alone ? warp * D : 0);
         // visible keys of the first and the last row
         auto visible = [&](int tok) { return p.causal ? min(max(cs.len - cs.n + tok + 1, 0), cs.len) : cs.len; };
         const int vis_min = visible(0), vis_max = visible(cs.n - 1);
-        for (int r = warp; r < RT; r += kPgWarps) {
+        const int r0 = cs.alone ? 0 : warp, rstep = cs.alone ? 1 : kPgWarps;
+#pragma unroll 4
+        for (int r = r0; r < RT; r += rstep) {
             // four values per lane; the row's power of two goes to its score factor
             uint2 x = make_uint2(0u, 0u);
             const int tok = r / p.G;
@@ -355,7 +484,8 @@ __global__ void __launch_bounds__(256, 1)
             }
             if (lane == 0) rowc[r] = make_float2(p.scale_log2 * exp2i(e), __int_as_float(r < nrow ? visible(tok) : cs.len));
         }
-        __syncthreads();
+        if (cs.alone) __syncwarp();
+        else __syncthreads();
         float rc[NT][2], m[NT][2], l[NT][2];
         int lim[NT][2];
         float o[C::MI][NT][4];
@@ -377,11 +507,14 @@ __global__ void __launch_bounds__(256, 1)
                 for (int e = 0; e < 4; ++e) o[i][nt][e] = 0.f;
 
         // ---------------------------------------------------- its chunks
+        uint32_t nan_bits = 0u;
 #pragma unroll 1
-        for (int c = cs.c0 + warp; c < cs.c1; c += kPgWarps) {
+        for (int c = chunk_of(cs, 0), cstep = chunk_of(cs, 1) - c; c < cs.c1; c += cstep) {
             const int st = consumed % C::STAGES;
             ok = mbar_wait_warp(&bars[st], (consumed / C::STAGES) & 1, cx, 92);
             if (!ok) break;
+            cp_async_wait<C::STAGES - 1>();
+            __syncwarp();
             const float4 mt4 = meta[st];
             const uint32_t kb = smem_u32(ring + 2 * st * C::TILE), vb = kb + C::TILE;
             const int key0 = c * kPgChunk;
@@ -516,11 +649,11 @@ __global__ void __launch_bounds__(256, 1)
                             if (key >= vis_max) vw[ks][r][w] = 0u;
                             const uint32_t nb = e4m3_nan_bits(vw[ks][r][w]);
                             if (nb) {
-                                nan_seen = 1;
+                                nan_bits = 1u;
 #pragma unroll
                                 for (int y = 0; y < 4; ++y)
                                     if ((nb >> (8 * y)) & 0x80u) {
-                                        atomicMin(&first_nan[g * (D / 8) + w * 4 + y], key);
+                                        atomicMin(&nan_at[g * (D / 8) + w * 4 + y], key);
                                         vw[ks][r][w] &= ~(0xFFu << (8 * y));
                                     }
                             }
@@ -560,7 +693,6 @@ __global__ void __launch_bounds__(256, 1)
             issue();
         }
 
-        // ---------------------------------------------------- merge of the warps
         // row sums over the key lanes
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -570,8 +702,56 @@ __global__ void __launch_bounds__(256, 1)
                 x += __shfl_xor_sync(0xffffffffu, x, 4);
                 x += __shfl_xor_sync(0xffffffffu, x, 8);
                 x += __shfl_xor_sync(0xffffffffu, x, 16);
-                if (g == 0) ml[warp * RT + nt * 8 + 2 * t4 + e] = make_float2(m[nt][e], x);
+                l[nt][e] = x;
             }
+        auto lse_of = [&](float mm, float ll) {
+            return ll == 0.f ? -CUDART_INF_F : (mm - kPgOffset + log2f(ll)) * kPgLn2;
+        };
+        if (cs.alone) {
+            // ------------------------------------------------ a short unit: its rows are this warp's
+            if (!ok) break;
+            const bool nans = __any_sync(0xffffffffu, nan_bits != 0u);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = nt * 8 + 2 * t4 + e, tok = r / p.G, hq = cs.hk * p.G + r - tok * p.G;
+                    if (r >= nrow) continue;
+                    const float inv = l[nt][e] == 0.f ? 0.f : 1.f / l[nt][e];
+                    // columns g D/8 .. + D/8 of row r
+                    uint32_t w[C::MI];
+#pragma unroll
+                    for (int i = 0; i < C::MI; ++i) {
+                        float a = o[i][nt][e] * inv, b = o[i][nt][2 + e] * inv;
+                        if (nans) {
+                            a = nan_at[g * (D / 8) + 2 * i] < lim[nt][e] ? CUDART_NAN_F : a;
+                            b = nan_at[g * (D / 8) + 2 * i + 1] < lim[nt][e] ? CUDART_NAN_F : b;
+                        }
+                        w[i] = pack_bf16x2(a, b);
+                    }
+                    uint4* dst = reinterpret_cast<uint4*>(
+                        p.o + (static_cast<size_t>(cs.tok0 + tok) * p.Hq + hq) * D + g * (D / 8));
+#pragma unroll
+                    for (int i = 0; i < C::MI / 4; ++i)
+                        dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                    if (g == 0)
+                        p.lse[static_cast<size_t>(hq) * p.total + cs.tok0 + tok] = lse_of(m[nt][e], l[nt][e]);
+                }
+            __syncwarp();
+            if (nans) {
+                for (int i = lane; i < D; i += 32) nan_at[i] = INT_MAX;
+                __syncwarp();
+            }
+            work = next(cs);
+            continue;
+        }
+        // ---------------------------------------------------- merge of the warps
+        if (nan_bits) nan_seen = 1;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (g == 0) ml[warp * RT + nt * 8 + 2 * t4 + e] = make_float2(m[nt][e], l[nt][e]);
         if (__syncthreads_or(!ok)) break;
         float fac[NT][2];
 #pragma unroll
@@ -579,11 +759,31 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float M = -CUDART_INF_F;
+#pragma unroll
                 for (int w = 0; w < kPgWarps; ++w) M = fmaxf(M, ml[w * RT + nt * 8 + 2 * t4 + e].x);
                 fac[nt][e] = m[nt][e] == -CUDART_INF_F ? 0.f : ex2_approx(m[nt][e] - M);
             }
         const bool whole = cs.c0 == 0 && cs.c1 == cs.nchunk;
         const int slot = 2 * static_cast<int>(blockIdx.x) + (cs.line0 <= x0 ? 0 : 1);
+        if (tid < RT) {
+            // the row's maximum and sum over the warps
+            float M = -CUDART_INF_F, L = 0.f;
+#pragma unroll
+            for (int w = 0; w < kPgWarps; ++w) M = fmaxf(M, ml[w * RT + tid].x);
+#pragma unroll
+            for (int w = 0; w < kPgWarps; ++w) {
+                const float2 v = ml[w * RT + tid];
+                L += v.y * (v.x == -CUDART_INF_F ? 0.f : ex2_approx(v.x - M));
+            }
+            ml[kPgWarps * RT + tid] = make_float2(M, L == 0.f ? 0.f : 1.f / L);
+            if (!whole) {
+                p.pm[slot * kPagedMaxRows + tid] = M;
+                p.pl[slot * kPagedMaxRows + tid] = L;
+            } else if (tid < nrow) {
+                const int tok = tid / p.G, hq = cs.hk * p.G + tid - tok * p.G;
+                p.lse[static_cast<size_t>(hq) * p.total + cs.tok0 + tok] = lse_of(M, L);
+            }
+        }
         // m tiles in turn: the warps' parts of RED_M tiles at a time
 #pragma unroll
         for (int i0 = 0; i0 < C::MI; i0 += C::RED_M) {
@@ -597,6 +797,7 @@ __global__ void __launch_bounds__(256, 1)
                         red[((warp * C::RED_M + i - i0) * 4 * NT + nt * 4 + e) * 32 + lane] =
                             o[i][nt][e] * fac[nt][e & 1];
             __syncthreads();
+#pragma unroll
             for (int x = tid; x < C::RED_M * C::RED_F; x += 256) {
                 float sum = 0.f;
 #pragma unroll
@@ -604,34 +805,18 @@ __global__ void __launch_bounds__(256, 1)
                 const int ln = x & 31, q = x >> 5, e = q & 3, nt = (q >> 2) % NT, i = i0 + q / (4 * NT);
                 const int r = nt * 8 + 2 * (ln & 3) + (e & 1);
                 const int col = (ln >> 2) * (D / 8) + 2 * i + (e >> 1);
-                float M = -CUDART_INF_F, L = 0.f;
-                for (int w = 0; w < kPgWarps; ++w) M = fmaxf(M, ml[w * RT + r].x);
-                for (int w = 0; w < kPgWarps; ++w) {
-                    const float2 v = ml[w * RT + r];
-                    L += v.y * (v.x == -CUDART_INF_F ? 0.f : ex2_approx(v.x - M));
-                }
-                if (nan_seen && first_nan[col] < __float_as_int(rowc[r].y)) sum = CUDART_NAN_F;
-                if (whole) {
-                    if (r < nrow) {
-                        const int tok = r / p.G, hq = cs.hk * p.G + r - tok * p.G;
-                        const float out = L == 0.f ? 0.f : sum / L;
-                        p.o[(static_cast<size_t>(cs.tok0 + tok) * p.Hq + hq) * D + col] =
-                            static_cast<uint16_t>(pack_bf16x2(out, 0.f) & 0xFFFFu);
-                        if (col == 0)
-                            p.lse[static_cast<size_t>(hq) * p.total + cs.tok0 + tok] =
-                                L == 0.f ? -CUDART_INF_F : (M - kPgOffset + log2f(L)) * kPgLn2;
-                    }
-                } else {
+                if (nan_seen && nan_at[col] < __float_as_int(rowc[r].y)) sum = CUDART_NAN_F;
+                if (!whole) {
                     p.po[(static_cast<size_t>(slot) * kPagedMaxRows + r) * D + col] = sum;
-                    if (col == 0) {
-                        p.pm[slot * kPagedMaxRows + r] = M;
-                        p.pl[slot * kPagedMaxRows + r] = L;
-                    }
+                } else if (r < nrow) {
+                    const int tok = r / p.G, hq = cs.hk * p.G + r - tok * p.G;
+                    p.o[(static_cast<size_t>(cs.tok0 + tok) * p.Hq + hq) * D + col] =
+                        static_cast<uint16_t>(pack_bf16x2(sum * ml[kPgWarps * RT + r].y, 0.f) & 0xFFFFu);
                 }
             }
             __syncthreads();
         }
-        if (tid < D) first_nan[tid] = INT_MAX;
+        if (tid < D) nan_at[tid] = INT_MAX;
         if (tid == 0) nan_seen = 0;
         if (!whole) {
             // the CTAs that hold pieces of this unit are consecutive; the last
@@ -643,35 +828,56 @@ __global__ void __launch_bounds__(256, 1)
             __syncthreads();
             if (last_s) {
                 __threadfence();
-                for (int x = tid; x < nrow * D; x += 256) {
-                    const int r = x / D, col = x - r * D;
-                    float M = -CUDART_INF_F, L = 0.f, acc = 0.f;
-                    for (int cta = f; cta <= e; ++cta) {
-                        const int sl = 2 * cta + (cs.line0 <= quota * cta ? 0 : 1);
-                        M = fmaxf(M, __ldcg(&p.pm[sl * kPagedMaxRows + r]));
+                auto piece = [&](int cta) { return 2 * cta + (cs.line0 <= quota * cta ? 0 : 1); };
+                // maxima and sums: a warp for each row, a lane for each piece
+                for (int r = warp; r < nrow; r += kPgWarps) {
+                    float M = -CUDART_INF_F, L = 0.f;
+                    for (int cta = f + lane; cta <= e; cta += 32)
+                        M = fmaxf(M, __ldcg(&p.pm[piece(cta) * kPagedMaxRows + r]));
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+                    for (int cta = f + lane; cta <= e; cta += 32) {
+                        const float mc = __ldcg(&p.pm[piece(cta) * kPagedMaxRows + r]);
+                        L = fmaf(mc == -CUDART_INF_F ? 0.f : ex2_approx(mc - M),
+                                 __ldcg(&p.pl[piece(cta) * kPagedMaxRows + r]), L);
                     }
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+                    if (lane == 0) {
+                        ml[r] = make_float2(M, L == 0.f ? 0.f : 1.f / L);
+                        const int tok = r / p.G, hq = cs.hk * p.G + r - tok * p.G;
+                        p.lse[static_cast<size_t>(hq) * p.total + cs.tok0 + tok] = lse_of(M, L);
+                    }
+                }
+                __syncthreads();
+                // outputs: a thread for four columns of a row
+                for (int x = tid; x < nrow * (D / 4); x += 256) {
+                    const int r = x / (D / 4), c4 = x - r * (D / 4);
+                    const float M = ml[r].x;
+                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
                     for (int cta = f; cta <= e; ++cta) {
-                        const int sl = 2 * cta + (cs.line0 <= quota * cta ? 0 : 1);
+                        const int sl = piece(cta);
                         const float mc = __ldcg(&p.pm[sl * kPagedMaxRows + r]);
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(
+                                                    p.po + (static_cast<size_t>(sl) * kPagedMaxRows + r) * D) + c4);
                         const float w = mc == -CUDART_INF_F ? 0.f : ex2_approx(mc - M);
-                        L = fmaf(w, __ldcg(&p.pl[sl * kPagedMaxRows + r]), L);
-                        acc = fmaf(w, __ldcg(&p.po[(static_cast<size_t>(sl) * kPagedMaxRows + r) * D + col]), acc);
+                        acc.x = fmaf(w, v.x, acc.x);
+                        acc.y = fmaf(w, v.y, acc.y);
+                        acc.z = fmaf(w, v.z, acc.z);
+                        acc.w = fmaf(w, v.w, acc.w);
                     }
                     const int tok = r / p.G, hq = cs.hk * p.G + r - tok * p.G;
-                    const float out = L == 0.f ? 0.f : acc / L;
-                    p.o[(static_cast<size_t>(cs.tok0 + tok) * p.Hq + hq) * D + col] =
-                        static_cast<uint16_t>(pack_bf16x2(out, 0.f) & 0xFFFFu);
-                    if (col == 0)
-                        p.lse[static_cast<size_t>(hq) * p.total + cs.tok0 + tok] =
-                            L == 0.f ? -CUDART_INF_F : (M - kPgOffset + log2f(L)) * kPgLn2;
+                    const float iL = ml[r].y;
+                    *reinterpret_cast<uint2*>(p.o + (static_cast<size_t>(cs.tok0 + tok) * p.Hq + hq) * D + c4 * 4) =
+                        make_uint2(pack_bf16x2(acc.x * iL, acc.y * iL), pack_bf16x2(acc.z * iL, acc.w * iL));
                 }
             }
         }
-        const long long x = cs.line0 + cs.c1;
-        if (x >= x1) break;
-        place(cs, crl, x);
+        work = next(cs);
         __syncthreads();
     }
+    cp_async_wait<0>();
     // after a wait that gave up: let the copies still in flight land before
     // leaving (otherwise every copy requested has been consumed)
     for (int u = consumed; u < issued; ++u)
