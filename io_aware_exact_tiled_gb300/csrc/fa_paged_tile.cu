@@ -14,7 +14,7 @@
 // A CTA holds two row tiles so that each V tile is converted once for 256
 // rows. Warps:
 //   0      copies K and V tiles by TMA, E4M3 as they lie, and their block scales
-//   1, 2   issue the products of row tile 0, 1 (independent of each other)
+//   1      issues the products
 //   3      allocates TMEM
 //   4-7    softmax of row tile 0: thread = row
 //   8-11   softmax of row tile 1
@@ -65,7 +65,7 @@ struct PtCfg {
     static constexpr int USED = BAR_OFF + 512;
     static constexpr int SMEM = USED + 1024;
     static constexpr int COL_S = 0, COL_O = 256;  // TMEM: S of tile i at 128 i, O at 256 + 128 i
-    static constexpr uint32_t ID_S = idesc_make(128, 128, kFmtE4M3, false, false);
+    static constexpr uint32_t ID_S = idesc_make(128, 64, kFmtE4M3, false, false);
     static constexpr uint32_t ID_PV = idesc_make(128, D, 0 /* f16 */, false, true);
     static_assert(SMEM <= 232448 - 2048, "shared memory");
 };
@@ -97,6 +97,37 @@ __device__ __forceinline__ uint32_t pt_pack_f16x2(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+__device__ __forceinline__ uint32_t pt_e4m3x2_from_f16x2(uint32_t x) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pt_sub_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// Bounded wait of a whole warp, in few instructions (the five roles' loops
+// compete for the instruction cache). False after FA_WAIT_LIMIT_NS or once
+// the CTA is aborting; the role then leaves its loop and reports (pt_gave_up).
+__device__ __forceinline__ bool pt_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    uint64_t t0 = 0;
+    for (uint32_t it = 1; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity)); ++it) {
+        if ((it & 255u) == 0) {
+            if (it == 256u) t0 = globaltimer_ns();
+            if (*abort_flag || globaltimer_ns() - t0 > FA_WAIT_LIMIT_NS) return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ void pt_gave_up(volatile int* abort_flag, int* status, int role) {
+    if (!*abort_flag) {
+        *abort_flag = 1;
+        atomicCAS(status, 0, FA_DEV_TIMEOUT | (role << 8));
+    }
+}
+// A value that all lanes of a warp share.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 __device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t sbo) {
     return (sdesc_sw128(saddr, 16, sbo) & ~(7ull << 61)) | (4ull << 61);
 }
@@ -175,11 +206,11 @@ __global__ void __launch_bounds__(512, 1)
     }
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::BAR_OFF);
     uint64_t* q_full = bars;                   // [2] Q parts of a row tile stored
-    uint64_t* s_full = q_full + 2;             // [2] S ready
-    uint64_t* p_full = s_full + 2;             // [2] P stored, O rescaled
-    uint64_t* o_done = p_full + 2;             // [2] O of a piece final
-    uint64_t* drain = o_done + 2;              // [2]
-    uint64_t* nan_full = drain + 2;            // [4] a piece's V has been looked over
+    uint64_t* s_full = q_full + 2;             // [2][2] S of a row tile and half of the keys ready
+    uint64_t* p_full = s_full + 4;             // [2][2] its P stored, O rescaled
+    uint64_t* pv_done = p_full + 4;            // [2][2] its P V done
+    uint64_t* drain = pv_done + 4;
+    uint64_t* nan_full = drain + 1;            // [4] a piece's V has been looked over
     uint64_t* sc_full = nan_full + kPtNanSlots;          // [8] scales stored
     uint64_t* k_full = sc_full + kPtScaleSlots;  // [KS]
     uint64_t* k_empty = k_full + C::KS;        // [KS] both row tiles' S done
@@ -191,16 +222,18 @@ __global__ void __launch_bounds__(512, 1)
         abort_s = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 128);
-            mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 128);
-            mbar_init(&o_done[i], 1);
-            mbar_init(&drain[i], 1);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(&s_full[2 * i + h], 1);
+                mbar_init(&p_full[2 * i + h], 128);
+                mbar_init(&pv_done[2 * i + h], 1);
+            }
         }
+        mbar_init(drain, 1);
         for (int i = 0; i < kPtNanSlots; ++i) mbar_init(&nan_full[i], 128);
         for (int i = 0; i < kPtScaleSlots; ++i) mbar_init(&sc_full[i], 1);
         for (int i = 0; i < C::KS; ++i) {
             mbar_init(&k_full[i], 1);
-            mbar_init(&k_empty[i], 2);
+            mbar_init(&k_empty[i], 1);
         }
         for (int i = 0; i < C::RS; ++i) {
             mbar_init(&r_full[i], 1);
@@ -208,7 +241,7 @@ __global__ void __launch_bounds__(512, 1)
         }
         for (int i = 0; i < C::VS; ++i) {
             mbar_init(&v_full[i], 128);
-            mbar_init(&v_empty[i], 2);
+            mbar_init(&v_empty[i], 1);
         }
         fence_barrier_init();
     }
@@ -303,12 +336,12 @@ __global__ void __launch_bounds__(512, 1)
         const int last = min(base + 127, rows - 1);
         return max(s.c0, min(s.c1, (pt_visible(p, s.r, last / p.G) + 127) >> 7));
     };
-    const WaitCtx cx{reinterpret_cast<volatile int*>(&abort_s), p.status};
+    auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return pt_wait(bar, parity, &abort_s); };
     PtSeg s;
     first(s);
 
     if (warp < 4) {
-        regs_dec<56>();
+        regs_dec<96>();
         if (warp == 0) {
             // ------------------------------------------------------ K tiles and scales
             const int bs = 1 << p.bs_log2, box = min(bs, 128);
@@ -333,7 +366,7 @@ __global__ void __launch_bounds__(512, 1)
                             vs = p.v_scale[static_cast<size_t>(id) * p.Hkv + s.hk];
                         }
                     }
-                    if (!(ok = mbar_wait_warp(&k_empty[st], ((u / C::KS) & 1) ^ 1, cx, 95))) break;
+                    if (!(ok = wait_warp(&k_empty[st], ((u / C::KS) & 1) ^ 1))) break;
                     if (lane == 0) mbar_arrive_expect_tx(&k_full[st], C::K_BYTES);
                     __syncwarp();
                     // the first lane of each box of min(block, 128) rows requests it
@@ -357,7 +390,7 @@ __global__ void __launch_bounds__(512, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sc_full[slot]);
                     const int rs = u % C::RS;
-                    if (!(ok = mbar_wait_warp(&r_empty[rs], ((u / C::RS) & 1) ^ 1, cx, 107))) {
+                    if (!(ok = wait_warp(&r_empty[rs], ((u / C::RS) & 1) ^ 1))) {
                         klast = u + 1;
                         break;
                     }
@@ -367,6 +400,7 @@ __global__ void __launch_bounds__(512, 1)
                         tma_load_2d(sm + C::R_OFF + rs * C::K_BYTES + lane * 16 * D, &tmV, 0, row, &r_full[rs]);
                 }
             } while (ok && next(s));
+            if (!ok) pt_gave_up(&abort_s, p.status, 95);
             // let every copy in flight land before the CTA can exit
             if (lane == 0) {
                 const int nk = max(u, klast);
@@ -379,80 +413,90 @@ __global__ void __launch_bounds__(512, 1)
                     mbar_wait_teardown(&r_full[i], (last / C::RS) & 1, 200000000ull);
                 }
             }
-        } else if (warp < 3) {
-            // ------------------------------------------------------ products of row tile i
-            const int i = warp - 1;
+        } else if (warp == 1) {
+            // ------------------------------------------------------ products
+            // A key tile's two halves of 64 keys have S columns of their own:
+            // while the softmax warps of a row tile work on one half, P V and
+            // the next tile's S of the other half run. In turn: half 0 of row
+            // tile 0 and 1, half 1 of row tile 0 and 1.
             const uint32_t leader = elect_one_sync();
-            const uint32_t tS = tm + C::COL_S + i * 128, tO = tm + C::COL_O + i * 128;
-            const uint64_t dQ = sdesc_sw128(smem_u32(sm + C::Q_OFF + i * C::Q_BYTES), 16, 1024);
+            const uint64_t dQ0 = sdesc_sw128(smem_u32(sm + C::Q_OFF), 16, 1024);
             const uint64_t dK = D == 128 ? sdesc_sw128(smem_u32(sm + C::K_OFF), 16, 1024)
                                          : sdesc_sw64(smem_u32(sm + C::K_OFF), 512);
             const uint64_t dV = sdesc_sw128(smem_u32(sm + C::V_OFF), 16384, 1024);
-            int u = 0, nseg = 0, np = 0;  // tiles walked, pieces with work, tiles of P multiplied
+            const uint32_t tm0 = __shfl_sync(0xffffffffu, tm, 0);
+            int u = 0;                             // tiles walked
+            int nseg[2] = {0, 0}, np[2] = {0, 0};  // pieces with work, tiles of P multiplied
             bool ok = true;
             do {
-                const int end = half_end(s, i);
-                auto issue_pv = [&](int uu, bool fresh) -> bool {
-                    const int vs = uu % C::VS;
-                    if (!mbar_wait_warp(&p_full[i], np & 1, cx, 96)) return false;
-                    if (!mbar_wait_warp(&v_full[vs], (uu / C::VS) & 1, cx, 97)) return false;
-                    tc_fence_after();
-                    const uint64_t vd = sdesc_advance(dV, vs * C::V_BYTES);
+                // warp-uniform in the compiler's eyes too, so that descriptors and
+                // TMEM addresses stay in uniform registers
+                const int c0 = uniform(s.c0), c1 = uniform(s.c1);
+                const int end[2] = {uniform(half_end(s, 0)), uniform(half_end(s, 1))};
+                for (int t = c0; t <= c1; ++t, ++u) {
+                    const int st = u % C::KS, vs = (u - 1) % C::VS;
+                    const uint64_t vd0 = sdesc_advance(dV, vs * C::V_BYTES), kd0 = sdesc_advance(dK, st * C::K_BYTES);
+                    if (t < c1 && !(ok = wait_warp(&k_full[st], (u / C::KS) & 1))) break;
+                    if (t > c0 && !(ok = wait_warp(&v_full[vs], ((u - 1) / C::VS) & 1))) break;
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        umma_ts<false>(leader, tO, tS + kk * 8, sdesc_advance(vd, kk * 2048), C::ID_PV,
-                                       !fresh || kk > 0 ? 1u : 0u);
-                    umma_commit(leader, &v_empty[vs]);
-                    ++np;
-                    return true;
-                };
-                if (end > s.c0 && !(ok = mbar_wait_warp(&q_full[i], nseg & 1, cx, 98))) break;
-                for (int t = s.c0; t < s.c1; ++t, ++u) {
-                    const int st = u % C::KS;
-                    if (t < end) {
-                        // the previous tile's P V first: S below overwrites its P
-                        if (t > s.c0 && !(ok = issue_pv(u - 1, t - 1 == s.c0))) break;
-                        if (!(ok = mbar_wait_warp(&k_full[st], (u / C::KS) & 1, cx, 99))) break;
-                        tc_fence_after();
-                        const uint64_t kd = sdesc_advance(dK, st * C::K_BYTES);
+                    for (int step = 0; step < 4; ++step) {
+                        const int h = step >> 1, i = step & 1;
+                        const int e = end[i], bar = 2 * i + h;
+                        const uint32_t tS = tm0 + C::COL_S + i * 128 + h * 64, tO = tm0 + C::COL_O + i * 128;
+                        if (t > c0 && t <= e) {
+                            if (!(ok = wait_warp(&p_full[bar], np[i] & 1))) break;
+                            tc_fence_after();
+                            const uint64_t vd = sdesc_advance(vd0, h * 8192);
+                            const uint32_t more = !(t - 1 == c0 && h == 0);
 #pragma unroll
-                        for (int part = 0; part < 2; ++part)
+                            for (int kk = 0; kk < 4; ++kk)
+                                umma_ts<false>(leader, tO, tS + kk * 8, sdesc_advance(vd, kk * 2048), C::ID_PV,
+                                               kk > 0 ? 1u : more);
+                            umma_commit(leader, &pv_done[bar]);
+                        }
+                        if (t < e) {
+                            if (t == c0 && h == 0 && !(ok = wait_warp(&q_full[i], nseg[i] & 1)))
+                                break;
+                            tc_fence_after();
+                            const uint64_t kd = sdesc_advance(kd0, h * (C::K_BYTES / 2));
+                            const uint64_t qd = sdesc_advance(dQ0, i * C::Q_BYTES);
 #pragma unroll
-                            for (int kk = 0; kk < D / 32; ++kk)
-                                umma_ss_f8(leader, tS,
-                                           sdesc_advance(dQ, (D == 128 ? part * 16384 : part * 64) + kk * 32),
-                                           sdesc_advance(kd, kk * 32), C::ID_S, part || kk ? 1u : 0u);
-                        umma_commit(leader, &s_full[i]);
-                        umma_commit(leader, &k_empty[st]);
-                    } else {
-                        // tiles that only the other row tile needs
-                        if (t == end && t > s.c0 && !(ok = issue_pv(u - 1, t - 1 == s.c0))) break;
-                        const int vs = u % C::VS;
-                        if (!(ok = mbar_wait_warp(&k_full[st], (u / C::KS) & 1, cx, 100))) break;
-                        if (lane == 0) mbar_arrive(&k_empty[st]);
-                        if (!(ok = mbar_wait_warp(&v_full[vs], (u / C::VS) & 1, cx, 101))) break;
-                        if (lane == 0) mbar_arrive(&v_empty[vs]);
+                            for (int part = 0; part < 2; ++part)
+#pragma unroll
+                                for (int kk = 0; kk < D / 32; ++kk)
+                                    umma_ss_f8(leader, tS,
+                                               sdesc_advance(qd, (D == 128 ? part * 16384 : part * 64) + kk * 32),
+                                               sdesc_advance(kd, kk * 32), C::ID_S, part || kk ? 1u : 0u);
+                            umma_commit(leader, &s_full[bar]);
+                        }
+                    }
+                    if (!ok) break;
+                    // both row tiles have read K of tile t and V of tile t - 1
+                    if (t < c1) umma_commit(leader, &k_empty[st]);
+                    if (t > c0) {
+                        umma_commit(leader, &v_empty[vs]);
+                        np[0] += t <= end[0];
+                        np[1] += t <= end[1];
                     }
                 }
-                if (ok && end == s.c1 && end > s.c0) ok = issue_pv(u - 1, end - 1 == s.c0);
+                --u;  // the last round had no tile of its own
                 if (!ok) break;
-                if (end > s.c0) {
-                    umma_commit(leader, &o_done[i]);
-                    ++nseg;
-                }
-            } while (next(s));
+                nseg[0] += end[0] > c0;
+                nseg[1] += end[1] > c0;
+            } while (__any_sync(0xffffffffu, next(s)));
+            if (!ok) pt_gave_up(&abort_s, p.status, 96);
             // every MMA issued so far must be complete before TMEM is released
-            umma_commit(leader, &drain[i]);
-            mbar_wait_teardown(&drain[i], 0, 200000000ull);
+            umma_commit(leader, drain);
+            mbar_wait_teardown(drain, 0, 200000000ull);
         }
     } else if (warp < 12) {
         // ---------------------------------------------------------- softmax of row tile i
-        regs_inc<184>();
+        regs_inc<152>();
         const int i = (warp - 4) >> 2, wq = warp & 3, r = wq * 32 + lane;
         const uint32_t tl = tm + (static_cast<uint32_t>(wq * 32) << 16);
         const uint32_t tS = tl + C::COL_S + i * 128, tO = tl + C::COL_O + i * 128;
         uint8_t* qb = sm + C::Q_OFF + i * C::Q_BYTES;
-        int u = 0, ns = 0, nseg = 0, seg = 0;
+        int u = 0, ns = 0, seg = 0;  // tiles walked, halves of them multiplied, pieces
         bool ok = true;
         do {
             const int end = half_end(s, i);
@@ -491,17 +535,18 @@ __global__ void __launch_bounds__(512, 1)
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
-                        hi[y] = lo[y] = 0u;
+                        uint32_t h[2], l[2];
 #pragma unroll
                         for (int z = 0; z < 2; ++z) {
-                            const float a = __uint_as_float(w[2 * y + z] << 16) * f;
-                            const float b = __uint_as_float(w[2 * y + z] & 0xFFFF0000u) * f;
-                            const uint32_t h2 = pack_e4m3x2(a, b);
-                            float ha, hb;
-                            f2_split(f2_from_e4m3x2(h2), ha, hb);
-                            hi[y] |= h2 << (16 * z);
-                            lo[y] |= pack_e4m3x2(a - ha, b - hb) << (16 * z);
+                            const uint32_t v = w[2 * y + z];
+                            // exact in f16 down to 2^-24
+                            const uint32_t a = pt_pack_f16x2(__uint_as_float(v << 16) * f,
+                                                             __uint_as_float(v & 0xFFFF0000u) * f);
+                            h[z] = pt_e4m3x2_from_f16x2(a);
+                            l[z] = pt_e4m3x2_from_f16x2(pt_sub_f16x2(a, pt_f16x2_from_e4m3x2(h[z])));
                         }
+                        hi[y] = __byte_perm(h[0], h[1], 0x5410);
+                        lo[y] = __byte_perm(l[0], l[1], 0x5410);
                     }
                     if constexpr (D == 128) {
                         const uint32_t at = r * 128 + ((j ^ (r & 7)) << 4);
@@ -517,40 +562,34 @@ __global__ void __launch_bounds__(512, 1)
             }
             // rows that the first row's keys bound: tiles below need no mask
             const int vis_min = pt_visible(p, s.r, min(base, rows - 1) / p.G);
-            for (int t = s.c0; t < end; ++t) {
+#pragma unroll 1
+            for (int th = 2 * s.c0; th < 2 * end; ++th) {
+                const int t = th >> 1, h = th & 1;  // key tile and half of it
                 const int us = u + (t - s.c0), slot = us % kPtScaleSlots;
-                ok = mbar_wait(&sc_full[slot], (us / kPtScaleSlots) & 1, cx, 102);
-                ok = ok && mbar_wait(&s_full[i], ns & 1, cx, 103);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
+                if (h == 0 && !(ok = wait_warp(&sc_full[slot], (us / kPtScaleSlots) & 1))) break;
+                if (!(ok = wait_warp(&s_full[2 * i + h], (ns >> 1) & 1))) break;
                 tc_fence_after();
-                uint32_t sr[4][32];
+                const uint32_t tSh = tS + h * 64;
+                uint32_t sr[2][32];
+                tmem_ld32(tSh, sr[0]);
+                tmem_ld32(tSh + 32, sr[1]);
+                const float4* sc4 = reinterpret_cast<const float4*>(sm + C::SC_OFF + slot * 96) + h;
+                const float4 ks4 = sc4[0], lv4 = sc4[2], il4 = sc4[4];
+                float c2[4] = {ks4.x * rc, ks4.y * rc, ks4.z * rc, ks4.w * rc};
+                const float lv[4] = {lv4.x, lv4.y, lv4.z, lv4.w}, il[4] = {il4.x, il4.y, il4.z, il4.w};
+                tmem_ld_wait(sr[0]);
+                tmem_ld_wait(sr[1]);
+                if (t * 128 + h * 64 + 64 > vis_min) {
+                    const int lim = limit - t * 128 - h * 64;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, sr[c]);
-                const float4* sc4 = reinterpret_cast<const float4*>(sm + C::SC_OFF + slot * 96);
-                float c2[8], lv[8];
-                {
-                    const float4 a = sc4[0], b = sc4[1], c = sc4[2], d = sc4[3];
-                    c2[0] = a.x; c2[1] = a.y; c2[2] = a.z; c2[3] = a.w;
-                    c2[4] = b.x; c2[5] = b.y; c2[6] = b.z; c2[7] = b.w;
-                    lv[0] = c.x; lv[1] = c.y; lv[2] = c.z; lv[3] = c.w;
-                    lv[4] = d.x; lv[5] = d.y; lv[6] = d.z; lv[7] = d.w;
-                }
-#pragma unroll
-                for (int gr = 0; gr < 8; ++gr) c2[gr] = c2[gr] * rc;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld_wait(sr[c]);
-                if (t * 128 + 128 > vis_min) {
-                    const int lim = limit - t * 128;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < 2; ++c)
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
                             if (c * 32 + k >= lim) sr[c][k] = __float_as_uint(-CUDART_INF_F);
                 }
                 float m_new = mu;
 #pragma unroll
-                for (int gr = 0; gr < 8; ++gr) {
+                for (int gr = 0; gr < 4; ++gr) {
                     const uint32_t* v = &sr[gr >> 1][(gr & 1) * 16];
                     float a = -CUDART_INF_F, b = -CUDART_INF_F;
 #pragma unroll
@@ -570,37 +609,33 @@ __global__ void __launch_bounds__(512, 1)
                     mu = m_new;
                     l *= alpha;
                 }
-                const bool resc_any = __any_sync(0xffffffffu, resc) && t > s.c0;
                 const float sub = mu == -CUDART_INF_F ? 0.f : mu - kPtOffset;
-                const float* il = reinterpret_cast<const float*>(sc4) + 16;
+                uint32_t pk[32];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t pk[16];
+                for (int gr = 0; gr < 4; ++gr) {
+                    const float add = lv[gr] - sub;
+                    const uint64_t cc = f2_make(c2[gr], c2[gr]), aa = f2_make(add, add);
+                    uint64_t sum = 0ull;
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        const int gr = 2 * c + hf;
-                        const float add = lv[gr] - sub;
-                        const uint64_t cc = f2_make(c2[gr], c2[gr]), aa = f2_make(add, add);
-                        uint64_t sum = 0ull;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int at = hf * 16 + 2 * k;
-                            float y0, y1;
-                            f2_split(f2_fma(f2_make(__uint_as_float(sr[c][at]), __uint_as_float(sr[c][at + 1])), cc, aa),
-                                     y0, y1);
-                            const float e0 = ex2_approx(y0), e1 = ex2_approx(y1);
-                            pk[hf * 8 + k] = pt_pack_f16x2(e0, e1);
-                            sum = f2_add(sum, f2_make(e0, e1));
-                        }
-                        float a, b;
-                        f2_split(sum, a, b);
-                        l = fmaf(a + b, il[gr], l);
+                    for (int k = 0; k < 8; ++k) {
+                        const uint32_t* v = &sr[gr >> 1][(gr & 1) * 16 + 2 * k];
+                        float y0, y1;
+                        f2_split(f2_fma(f2_make(__uint_as_float(v[0]), __uint_as_float(v[1])), cc, aa), y0, y1);
+                        const float e0 = ex2_approx(y0), e1 = ex2_approx(y1);
+                        pk[gr * 8 + k] = pt_pack_f16x2(e0, e1);
+                        sum = f2_add(sum, f2_make(e0, e1));
                     }
-                    tmem_st16(tS + c * 16, pk);
+                    float a, b;
+                    f2_split(sum, a, b);
+                    l = fmaf(a + b, il[gr], l);
                 }
-                if (resc_any) {
-                    // the previous tiles' P V were issued before this tile's S
-                    // and MMAs complete in order: O is final, and rescaled here
+                tmem_st32(tSh, pk);
+                if (__any_sync(0xffffffffu, resc) && th > 2 * s.c0) {
+                    // O of the halves so far is final once the last one's P V
+                    // is (the ones before it were issued ahead of this S; the
+                    // next one waits for this half's P)
+                    if (!(ok = wait_warp(&pv_done[2 * i + (h ^ 1)], ((ns - 1) >> 1) & 1))) break;
+                    tc_fence_after();
 #pragma unroll
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t ov[32];
@@ -613,18 +648,16 @@ __global__ void __launch_bounds__(512, 1)
                 }
                 tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(&p_full[i]);
+                mbar_arrive(&p_full[2 * i + h]);
                 ++ns;
             }
             if (!ok) break;
             u += s.c1 - s.c0;
             // ---------------------------------------------------- the piece's rows
             if (end > s.c0) {
-                ok = mbar_wait(&o_done[i], nseg & 1, cx, 104);
-                ++nseg;
+                ok = wait_warp(&pv_done[2 * i + 1], ((ns - 1) >> 1) & 1);
             }
-            ok = ok && mbar_wait(&nan_full[seg % kPtNanSlots], (seg / kPtNanSlots) & 1, cx, 105);
-            ok = __all_sync(0xffffffffu, ok);
+            ok = ok && wait_warp(&nan_full[seg % kPtNanSlots], (seg / kPtNanSlots) & 1);
             if (!ok) break;
             tc_fence_after();
             int* nf = nan_first + (seg % kPtNanSlots) * (D + 4);
@@ -739,9 +772,10 @@ __global__ void __launch_bounds__(512, 1)
                 if (i == 0 && r == 0) nf[D] = 0;
             }
         } while (next(s));
+        if (!ok) pt_gave_up(&abort_s, p.status, 97);
     } else {
         // ---------------------------------------------------------- V to f16, thread = key
-        regs_dec<88>();
+        regs_dec<112>();
         const int r = (warp - 12) * 32 + lane;
         int u = 0, seg = 0;
         bool ok = true;
@@ -752,7 +786,7 @@ __global__ void __launch_bounds__(512, 1)
             int* nf = nan_first + (seg % kPtNanSlots) * (D + 4);
             for (int t = s.c0; t < s.c1; ++t, ++u) {
                 const int vs = u % C::VS, rs = u % C::RS;
-                ok = mbar_wait_warp(&r_full[rs], (u / C::RS) & 1, cx, 108);
+                ok = wait_warp(&r_full[rs], (u / C::RS) & 1);
                 if (!ok) break;
                 // row r as TMA swizzled it (d = 64: two bits of the row index
                 // above its 64-byte pair)
@@ -762,7 +796,7 @@ __global__ void __launch_bounds__(512, 1)
                 for (int j = 0; j < D / 16; ++j)
                     x[j] = lds128_u4(rb + ((D == 128 ? j ^ (r & 7) : j ^ ((r >> 1) & 3)) << 4));
                 mbar_arrive(&r_empty[rs]);
-                ok = mbar_wait_warp(&v_empty[vs], ((u / C::VS) & 1) ^ 1, cx, 106);
+                ok = wait_warp(&v_empty[vs], ((u / C::VS) & 1) ^ 1);
                 if (!ok) break;
                 if (t * 128 + 128 > vis_min) {
                     // rows that no query sees count as zero; a NaN that only
@@ -812,6 +846,7 @@ __global__ void __launch_bounds__(512, 1)
             mbar_arrive(&nan_full[seg % kPtNanSlots]);
             ++seg;
         } while (next(s));
+        if (!ok) pt_gave_up(&abort_s, p.status, 98);
     }
     tc_fence_before();
     __syncthreads();
