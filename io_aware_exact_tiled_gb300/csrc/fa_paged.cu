@@ -94,6 +94,7 @@ struct PagedParams {
     int B, Hq, Hkv, G, total, max_new, max_blocks, num_blocks, bs_log2;
     float scale_log2;
     int causal;
+    FastDiv by_g;  // division by G
     int *status, *counters;
     float *pm, *pl, *po;
 };
@@ -190,6 +191,8 @@ __global__ void __launch_bounds__(256, 1)
     __shared__ long long start_line;
     __shared__ int nan_seen, abort_s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+    // the row-tile kernel behind this one, if there is one, works on other rows
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // ---- all chunks, then the lines of long and of short units
     const int per = (p.B + 255) / 256;
@@ -377,7 +380,7 @@ __global__ void __launch_bounds__(256, 1)
             iwork = next(is);
             ik = 0;
             if (iwork && lane < is.n * p.G) {  // its query rows will be wanted soon
-                const int tok = lane / p.G;
+                const int tok = p.by_g.div(lane);
                 const uint16_t* row =
                     p.q + (static_cast<size_t>(is.tok0 + tok) * p.Hq + is.hk * p.G + (lane - tok * p.G)) * D;
                 asm volatile("prefetch.global.L2 [%0];" ::"l"(row));
@@ -460,7 +463,7 @@ __global__ void __launch_bounds__(256, 1)
         for (int r = r0; r < RT; r += rstep) {
             // four values per lane; the row's power of two goes to its score factor
             uint2 x = make_uint2(0u, 0u);
-            const int tok = r / p.G;
+            const int tok = p.by_g.div(r);
             if (r < nrow && lane < D / 4)
                 x = *reinterpret_cast<const uint2*>(
                     p.q + (static_cast<size_t>(cs.tok0 + tok) * p.Hq + cs.hk * p.G + (r - tok * p.G)) * D + lane * 4);
@@ -715,7 +718,7 @@ __global__ void __launch_bounds__(256, 1)
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int r = nt * 8 + 2 * t4 + e, tok = r / p.G, hq = cs.hk * p.G + r - tok * p.G;
+                    const int r = nt * 8 + 2 * t4 + e, tok = p.by_g.div(r), hq = cs.hk * p.G + r - tok * p.G;
                     if (r >= nrow) continue;
                     const float inv = l[nt][e] == 0.f ? 0.f : 1.f / l[nt][e];
                     // columns g D/8 .. + D/8 of row r
@@ -780,7 +783,7 @@ __global__ void __launch_bounds__(256, 1)
                 p.pm[slot * kPagedMaxRows + tid] = M;
                 p.pl[slot * kPagedMaxRows + tid] = L;
             } else if (tid < nrow) {
-                const int tok = tid / p.G, hq = cs.hk * p.G + tid - tok * p.G;
+                const int tok = p.by_g.div(tid), hq = cs.hk * p.G + tid - tok * p.G;
                 p.lse[static_cast<size_t>(hq) * p.total + cs.tok0 + tok] = lse_of(M, L);
             }
         }
@@ -809,7 +812,7 @@ __global__ void __launch_bounds__(256, 1)
                 if (!whole) {
                     p.po[(static_cast<size_t>(slot) * kPagedMaxRows + r) * D + col] = sum;
                 } else if (r < nrow) {
-                    const int tok = r / p.G, hq = cs.hk * p.G + r - tok * p.G;
+                    const int tok = p.by_g.div(r), hq = cs.hk * p.G + r - tok * p.G;
                     p.o[(static_cast<size_t>(cs.tok0 + tok) * p.Hq + hq) * D + col] =
                         static_cast<uint16_t>(pack_bf16x2(sum * ml[kPgWarps * RT + r].y, 0.f) & 0xFFFFu);
                 }
@@ -845,7 +848,7 @@ __global__ void __launch_bounds__(256, 1)
                     for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
                     if (lane == 0) {
                         ml[r] = make_float2(M, L == 0.f ? 0.f : 1.f / L);
-                        const int tok = r / p.G, hq = cs.hk * p.G + r - tok * p.G;
+                        const int tok = p.by_g.div(r), hq = cs.hk * p.G + r - tok * p.G;
                         p.lse[static_cast<size_t>(hq) * p.total + cs.tok0 + tok] = lse_of(M, L);
                     }
                 }
@@ -867,7 +870,7 @@ __global__ void __launch_bounds__(256, 1)
                         acc.z = fmaf(w, v.z, acc.z);
                         acc.w = fmaf(w, v.w, acc.w);
                     }
-                    const int tok = r / p.G, hq = cs.hk * p.G + r - tok * p.G;
+                    const int tok = p.by_g.div(r), hq = cs.hk * p.G + r - tok * p.G;
                     const float iL = ml[r].y;
                     *reinterpret_cast<uint2*>(p.o + (static_cast<size_t>(cs.tok0 + tok) * p.Hq + hq) * D + c4 * 4) =
                         make_uint2(pack_bf16x2(acc.x * iL, acc.y * iL), pack_bf16x2(acc.z * iL, acc.w * iL));
@@ -923,6 +926,7 @@ cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t stream, int* nlaun
     p.Hq = a.Hq;
     p.Hkv = a.Hkv;
     p.G = a.Hq / a.Hkv;
+    p.by_g = make_fast_div(p.G);
     p.total = a.total;
     p.max_new = a.max_new;
     p.max_blocks = a.max_blocks;

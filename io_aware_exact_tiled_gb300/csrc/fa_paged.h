@@ -72,6 +72,24 @@ inline long long paged_max_tile_units(int B, int Hq, int Hkv, int total, int max
     return Hkv * (B + total * group / kPagedTileRows);
 }
 
+// Division of 0 <= x < 2^31 by a divisor that the host knows: with
+// l = ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1 the quotient is
+// (umulhi(m, x) + x) >> l (Granlund and Montgomery, PLDI 1994).
+struct FastDiv {
+    uint32_t d, m, l;
+#ifdef __CUDACC__
+    __device__ __forceinline__ int div(int x) const {
+        return static_cast<int>((__umulhi(m, static_cast<uint32_t>(x)) + static_cast<uint32_t>(x)) >> l);
+    }
+#endif
+};
+inline FastDiv make_fast_div(int d) {
+    uint32_t l = 0;
+    while ((1ull << l) < static_cast<uint64_t>(d)) ++l;
+    const uint64_t m = ((((1ull << l) - d) << 32) / d) + 1;
+    return {static_cast<uint32_t>(d), static_cast<uint32_t>(m), l};
+}
+
 cudaError_t launch_cache_plan(const PlanArgs& a, cudaStream_t stream, int* nlaunch);
 cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t stream, int* nlaunch);
 cudaError_t launch_paged_tile(const PagedArgs& a, cudaStream_t stream);

@@ -9,12 +9,13 @@
 // nearly the same keys in all of them. The units' key tiles (128 keys, only
 // those that some row sees) form one line that is cut into equal quotas for
 // the persistent CTAs, as in the split-key kernel; the rows of a unit that was
-// cut are merged by whoever finishes last.
+// cut are merged by whoever finishes last. Each unit takes kPtUnitCost more
+// places on the line than it has tiles: what its start and end cost.
 //
 // A CTA holds two row tiles so that each V tile is converted once for 256
 // rows. Warps:
 //   0      copies K and V tiles by TMA, E4M3 as they lie, and their block scales
-//   1      issues the products
+//   1, 2   issue the products of row tile 0, 1
 //   3      allocates TMEM
 //   4-7    softmax of row tile 0: thread = row
 //   8-11   softmax of row tile 1
@@ -42,6 +43,7 @@ constexpr float kPtLn2 = 0.69314718055994530942f;
 constexpr float kPtRescale = 8.0f;  // log2 units
 constexpr float kPtOffset = 6.0f;   // log2 of the factor on P before its rounding to f16
 constexpr float kPtSpan = 60.0f;    // log2 of the largest ratio of V's block scales that is kept apart
+constexpr int kPtUnitCost = 4;       // key tiles' time that a unit's Q, first S and output take
 constexpr int kPtScaleSlots = 8;
 constexpr int kPtNanSlots = 4;
 
@@ -79,6 +81,7 @@ struct PtParams {
     int B, Hq, Hkv, G, total, max_new, max_blocks, num_blocks, bs_log2;
     float scale_log2;
     int causal;
+    FastDiv by_g;  // division by G
     int *status, *counters;
     int max_units;
     float *pm, *pl, *po;
@@ -135,14 +138,14 @@ __device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t sbo) {
 struct PtReq {
     int b, n, len, tok0;
     int npair;        // pairs of row tiles
-    long long tiles;  // key tiles of all pairs of one key head
+    long long tiles;  // key tiles of all pairs of one key head, each with its unit's cost
 };
 struct PtSeg {
     PtReq r;
     int hk, pair;
     int ntile;        // key tiles of the unit
     int c0, c1;       // this piece's tiles
-    long long line0;  // position of the unit's first tile on the line
+    long long line0;  // position of the unit's first tile on the line (its cost lies in front of it)
     int unit;         // index of the unit among all
 };
 
@@ -154,7 +157,7 @@ __device__ __forceinline__ int pt_visible(const PtParams& p, const PtReq& r, int
 // rows that see nothing get their zero output).
 __device__ __forceinline__ int pt_tiles(const PtParams& p, const PtReq& r, int pair) {
     const int last = min(pair * 256 + 255, r.n * p.G - 1);
-    return max(1, (pt_visible(p, r, last / p.G) + 127) >> 7);
+    return max(1, (pt_visible(p, r, p.by_g.div(last)) + 127) >> 7);
 }
 __device__ __forceinline__ void pt_request(const PtParams& p, int b, PtReq& r) {
     const int t0 = min(max(p.cu_seqlens[b], 0), p.total), t1 = min(max(p.cu_seqlens[b + 1], t0), p.total);
@@ -165,7 +168,7 @@ __device__ __forceinline__ void pt_request(const PtParams& p, int b, PtReq& r) {
     r.len = min(max(p.cache_len[b], 0), p.max_blocks << p.bs_log2);
     r.npair = static_cast<int>((static_cast<long long>(r.n) * p.G + 255) >> 8);
     r.tiles = 0;
-    for (int i = 0; i < r.npair; ++i) r.tiles += pt_tiles(p, r, i);
+    for (int i = 0; i < r.npair; ++i) r.tiles += pt_tiles(p, r, i) + kPtUnitCost;
 }
 
 template <int D>
@@ -209,8 +212,8 @@ __global__ void __launch_bounds__(512, 1)
     uint64_t* s_full = q_full + 2;             // [2][2] S of a row tile and half of the keys ready
     uint64_t* p_full = s_full + 4;             // [2][2] its P stored, O rescaled
     uint64_t* pv_done = p_full + 4;            // [2][2] its P V done
-    uint64_t* drain = pv_done + 4;
-    uint64_t* nan_full = drain + 1;            // [4] a piece's V has been looked over
+    uint64_t* drain = pv_done + 4;             // [2]
+    uint64_t* nan_full = drain + 2;            // [4] a piece's V has been looked over
     uint64_t* sc_full = nan_full + kPtNanSlots;          // [8] scales stored
     uint64_t* k_full = sc_full + kPtScaleSlots;  // [KS]
     uint64_t* k_empty = k_full + C::KS;        // [KS] both row tiles' S done
@@ -222,18 +225,18 @@ __global__ void __launch_bounds__(512, 1)
         abort_s = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 128);
+            mbar_init(&drain[i], 1);
             for (int h = 0; h < 2; ++h) {
                 mbar_init(&s_full[2 * i + h], 1);
                 mbar_init(&p_full[2 * i + h], 128);
                 mbar_init(&pv_done[2 * i + h], 1);
             }
         }
-        mbar_init(drain, 1);
         for (int i = 0; i < kPtNanSlots; ++i) mbar_init(&nan_full[i], 128);
         for (int i = 0; i < kPtScaleSlots; ++i) mbar_init(&sc_full[i], 1);
         for (int i = 0; i < C::KS; ++i) {
             mbar_init(&k_full[i], 1);
-            mbar_init(&k_empty[i], 1);
+            mbar_init(&k_empty[i], 2);
         }
         for (int i = 0; i < C::RS; ++i) {
             mbar_init(&r_full[i], 1);
@@ -241,7 +244,7 @@ __global__ void __launch_bounds__(512, 1)
         }
         for (int i = 0; i < C::VS; ++i) {
             mbar_init(&v_full[i], 128);
-            mbar_init(&v_empty[i], 1);
+            mbar_init(&v_empty[i], 2);
         }
         fence_barrier_init();
     }
@@ -257,10 +260,12 @@ __global__ void __launch_bounds__(512, 1)
         W += scan_w[w];
         U += scan_u[w];
     }
-    if (U > p.max_units) return;  // overlapping offsets: reported by the split-key kernel
     const long long quota = max((W + gridDim.x - 1) / static_cast<long long>(gridDim.x), 2ll);
     const long long x0 = quota * blockIdx.x, x1 = min(x0 + quota, W);
-    if (x0 >= x1) return;  // uniform over the CTA, before any TMEM use
+    if (U > p.max_units || x0 >= x1) {  // uniform over the CTA, before any TMEM use
+        // (too many units: overlapping offsets, which the split-key kernel reports)
+        return;
+    }
     bw += iw - mw;
     bu += iu - mu;
     if (x0 >= bw && x0 < bw + mw) {
@@ -301,20 +306,16 @@ __global__ void __launch_bounds__(512, 1)
         s.pair = 0;
         for (;;) {
             s.ntile = pt_tiles(p, s.r, s.pair);
-            if (rest < s.ntile) break;
-            rest -= s.ntile;
+            if (rest < s.ntile + kPtUnitCost) break;
+            rest -= s.ntile + kPtUnitCost;
             ++s.pair;
         }
-        s.c0 = static_cast<int>(rest);
-        s.line0 = x - s.c0;
+        s.line0 = x - rest + kPtUnitCost;
+        s.c0 = max(static_cast<int>(rest) - kPtUnitCost, 0);
         s.c1 = static_cast<int>(min(static_cast<long long>(s.ntile), x1 - s.line0));
         s.unit = runits + s.hk * s.r.npair + s.pair;
     };
-    auto first = [&](PtSeg& s) {
-        pt_request(p, start_b, s.r);
-        find(s, x0);
-    };
-    auto next = [&](PtSeg& s) -> bool {
+    auto next = [&](PtSeg& s) -> bool {  // false if what is left is no tile, or only the cost in front of one
         const long long x = s.line0 + s.c1;
         if (x >= x1) return false;
         if (s.pair + 1 < s.r.npair) {  // the usual step: the next pair of the same head
@@ -322,25 +323,29 @@ __global__ void __launch_bounds__(512, 1)
             ++s.unit;
             s.ntile = pt_tiles(p, s.r, s.pair);
             s.c0 = 0;
-            s.line0 = x;
-            s.c1 = static_cast<int>(min(static_cast<long long>(s.ntile), x1 - x));
-            return true;
+            s.line0 = x + kPtUnitCost;
+            s.c1 = static_cast<int>(min(static_cast<long long>(s.ntile), x1 - s.line0));
+        } else {
+            find(s, x);
         }
-        find(s, x);
-        return true;
+        return s.c1 > 0;
     };
     // key tiles that row tile i of a piece takes part in: [c0, end)
     auto half_end = [&](const PtSeg& s, int i) {
         const int rows = s.r.n * p.G, base = s.pair * 256 + i * 128;
         if (base >= rows) return s.c0;
         const int last = min(base + 127, rows - 1);
-        return max(s.c0, min(s.c1, (pt_visible(p, s.r, last / p.G) + 127) >> 7));
+        return max(s.c0, min(s.c1, (pt_visible(p, s.r, p.by_g.div(last)) + 127) >> 7));
     };
     auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return pt_wait(bar, parity, &abort_s); };
     PtSeg s;
-    first(s);
+    pt_request(p, start_b, s.r);
+    find(s, x0);
+    const bool any = s.c1 > s.c0;  // uniform over the CTA: not only the cost in front of a tile
 
-    if (warp < 4) {
+    if (!any) {
+        // nothing but TMEM to give back
+    } else if (warp < 4) {
         regs_dec<96>();
         if (warp == 0) {
             // ------------------------------------------------------ K tiles and scales
@@ -413,81 +418,72 @@ __global__ void __launch_bounds__(512, 1)
                     mbar_wait_teardown(&r_full[i], (last / C::RS) & 1, 200000000ull);
                 }
             }
-        } else if (warp == 1) {
-            // ------------------------------------------------------ products
+        } else if (warp < 3) {
+            // ------------------------------------------------------ products of row tile i
             // A key tile's two halves of 64 keys have S columns of their own:
-            // while the softmax warps of a row tile work on one half, P V and
-            // the next tile's S of the other half run. In turn: half 0 of row
-            // tile 0 and 1, half 1 of row tile 0 and 1.
+            // while the softmax warps work on one half, P V and the next
+            // tile's S of the other half run. One issuer for each row tile: a
+            // half's wait, twelve products and two commits take a warp about
+            // 450 cycles to issue, which one warp for both could not hide.
+            const int i = warp - 1;
             const uint32_t leader = elect_one_sync();
-            const uint64_t dQ0 = sdesc_sw128(smem_u32(sm + C::Q_OFF), 16, 1024);
+            const uint64_t dQ = sdesc_sw128(smem_u32(sm + C::Q_OFF) + i * C::Q_BYTES, 16, 1024);
             const uint64_t dK = D == 128 ? sdesc_sw128(smem_u32(sm + C::K_OFF), 16, 1024)
                                          : sdesc_sw64(smem_u32(sm + C::K_OFF), 512);
             const uint64_t dV = sdesc_sw128(smem_u32(sm + C::V_OFF), 16384, 1024);
-            const uint32_t tm0 = __shfl_sync(0xffffffffu, tm, 0);
-            int u = 0;                             // tiles walked
-            int nseg[2] = {0, 0}, np[2] = {0, 0};  // pieces with work, tiles of P multiplied
+            const uint32_t tm0 = uniform(tm) + i * 128;
+            int u = 0, nseg = 0, np = 0;  // tiles walked, pieces with work, tiles of P multiplied
             bool ok = true;
             do {
                 // warp-uniform in the compiler's eyes too, so that descriptors and
                 // TMEM addresses stay in uniform registers
-                const int c0 = uniform(s.c0), c1 = uniform(s.c1);
-                const int end[2] = {uniform(half_end(s, 0)), uniform(half_end(s, 1))};
+                const int c0 = uniform(s.c0), c1 = uniform(s.c1), end = uniform(half_end(s, i));
                 for (int t = c0; t <= c1; ++t, ++u) {
                     const int st = u % C::KS, vs = (u - 1) % C::VS;
-                    const uint64_t vd0 = sdesc_advance(dV, vs * C::V_BYTES), kd0 = sdesc_advance(dK, st * C::K_BYTES);
+                    const uint64_t vd = sdesc_advance(dV, vs * C::V_BYTES), kd = sdesc_advance(dK, st * C::K_BYTES);
                     if (t < c1 && !(ok = wait_warp(&k_full[st], (u / C::KS) & 1))) break;
                     if (t > c0 && !(ok = wait_warp(&v_full[vs], ((u - 1) / C::VS) & 1))) break;
+                    if (t == c0 && t < end && !(ok = wait_warp(&q_full[i], nseg & 1))) break;
 #pragma unroll
-                    for (int step = 0; step < 4; ++step) {
-                        const int h = step >> 1, i = step & 1;
-                        const int e = end[i], bar = 2 * i + h;
-                        const uint32_t tS = tm0 + C::COL_S + i * 128 + h * 64, tO = tm0 + C::COL_O + i * 128;
-                        if (t > c0 && t <= e) {
-                            if (!(ok = wait_warp(&p_full[bar], np[i] & 1))) break;
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t tS = tm0 + C::COL_S + h * 64, tO = tm0 + C::COL_O;
+                        if (t > c0 && t <= end) {
+                            if (!(ok = wait_warp(&p_full[2 * i + h], np & 1))) break;
                             tc_fence_after();
-                            const uint64_t vd = sdesc_advance(vd0, h * 8192);
                             const uint32_t more = !(t - 1 == c0 && h == 0);
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                umma_ts<false>(leader, tO, tS + kk * 8, sdesc_advance(vd, kk * 2048), C::ID_PV,
-                                               kk > 0 ? 1u : more);
-                            umma_commit(leader, &pv_done[bar]);
+                                umma_ts<false>(leader, tO, tS + kk * 8, sdesc_advance(vd, h * 8192 + kk * 2048),
+                                               C::ID_PV, kk > 0 ? 1u : more);
+                            umma_commit(leader, &pv_done[2 * i + h]);
                         }
-                        if (t < e) {
-                            if (t == c0 && h == 0 && !(ok = wait_warp(&q_full[i], nseg[i] & 1)))
-                                break;
+                        if (t < end) {
                             tc_fence_after();
-                            const uint64_t kd = sdesc_advance(kd0, h * (C::K_BYTES / 2));
-                            const uint64_t qd = sdesc_advance(dQ0, i * C::Q_BYTES);
 #pragma unroll
                             for (int part = 0; part < 2; ++part)
 #pragma unroll
                                 for (int kk = 0; kk < D / 32; ++kk)
                                     umma_ss_f8(leader, tS,
-                                               sdesc_advance(qd, (D == 128 ? part * 16384 : part * 64) + kk * 32),
-                                               sdesc_advance(kd, kk * 32), C::ID_S, part || kk ? 1u : 0u);
-                            umma_commit(leader, &s_full[bar]);
+                                               sdesc_advance(dQ, (D == 128 ? part * 16384 : part * 64) + kk * 32),
+                                               sdesc_advance(kd, h * (C::K_BYTES / 2) + kk * 32), C::ID_S,
+                                               part || kk ? 1u : 0u);
+                            umma_commit(leader, &s_full[2 * i + h]);
                         }
                     }
                     if (!ok) break;
-                    // both row tiles have read K of tile t and V of tile t - 1
+                    // this row tile has read K of tile t and V of tile t - 1
                     if (t < c1) umma_commit(leader, &k_empty[st]);
-                    if (t > c0) {
-                        umma_commit(leader, &v_empty[vs]);
-                        np[0] += t <= end[0];
-                        np[1] += t <= end[1];
-                    }
+                    if (t > c0) umma_commit(leader, &v_empty[vs]);
+                    np += t > c0 && t <= end;
                 }
                 --u;  // the last round had no tile of its own
                 if (!ok) break;
-                nseg[0] += end[0] > c0;
-                nseg[1] += end[1] > c0;
+                nseg += end > c0;
             } while (__any_sync(0xffffffffu, next(s)));
             if (!ok) pt_gave_up(&abort_s, p.status, 96);
             // every MMA issued so far must be complete before TMEM is released
-            umma_commit(leader, drain);
-            mbar_wait_teardown(drain, 0, 200000000ull);
+            umma_commit(leader, &drain[i]);
+            mbar_wait_teardown(&drain[i], 0, 200000000ull);
         }
     } else if (warp < 12) {
         // ---------------------------------------------------------- softmax of row tile i
@@ -502,7 +498,7 @@ __global__ void __launch_bounds__(512, 1)
             const int end = half_end(s, i);
             const int rows = s.r.n * p.G, base = s.pair * 256 + i * 128, row = base + r;
             const bool row_ok = row < rows;
-            const int tok = row_ok ? row / p.G : 0, hq = s.hk * p.G + (row_ok ? row - tok * p.G : 0);
+            const int tok = row_ok ? p.by_g.div(row) : 0, hq = s.hk * p.G + (row_ok ? row - tok * p.G : 0);
             const int limit = row_ok ? pt_visible(p, s.r, tok) : 0;
             const size_t qrow = (static_cast<size_t>(s.r.tok0 + tok) * p.Hq + hq) * D;
             float rc = 0.f, mu = -CUDART_INF_F, l = 0.f;
@@ -561,7 +557,7 @@ __global__ void __launch_bounds__(512, 1)
                 mbar_arrive(&q_full[i]);
             }
             // rows that the first row's keys bound: tiles below need no mask
-            const int vis_min = pt_visible(p, s.r, min(base, rows - 1) / p.G);
+            const int vis_min = pt_visible(p, s.r, p.by_g.div(min(base, rows - 1)));
 #pragma unroll 1
             for (int th = 2 * s.c0; th < 2 * end; ++th) {
                 const int t = th >> 1, h = th & 1;  // key tile and half of it
@@ -781,8 +777,8 @@ __global__ void __launch_bounds__(512, 1)
         bool ok = true;
         do {
             const int rows = s.r.n * p.G;
-            const int vis_min = pt_visible(p, s.r, s.pair * 256 / p.G);
-            const int vis_max = pt_visible(p, s.r, min(s.pair * 256 + 255, rows - 1) / p.G);
+            const int vis_min = pt_visible(p, s.r, p.by_g.div(s.pair * 256));
+            const int vis_max = pt_visible(p, s.r, p.by_g.div(min(s.pair * 256 + 255, rows - 1)));
             int* nf = nan_first + (seg % kPtNanSlots) * (D + 4);
             for (int t = s.c0; t < s.c1; ++t, ++u) {
                 const int vs = u % C::VS, rs = u % C::RS;
@@ -898,6 +894,7 @@ cudaError_t launch_paged_tile(const PagedArgs& a, cudaStream_t stream) {
     p.Hq = a.Hq;
     p.Hkv = a.Hkv;
     p.G = a.Hq / a.Hkv;
+    p.by_g = make_fast_div(p.G);
     p.total = a.total;
     p.max_new = a.max_new;
     p.max_blocks = a.max_blocks;
