@@ -15,9 +15,10 @@
 // Design:
 //   * Work is counted in chunks of 32 keys. A unit is (request, key head), with
 //     at most RT = 8, 16 or 32 query rows (fa_paged_tile.cu takes requests of
-//     more). The chunks of the long units form one line that is cut into equal
-//     quotas, one for each persistent CTA, so ragged lengths balance by
-//     themselves and one long request spreads over the whole GPU. A unit that
+//     more). The chunks of the long units form one line (with room in front of
+//     each unit for what its start and end cost) that is cut into equal quotas,
+//     one for each persistent CTA, so ragged lengths balance by themselves and
+//     one long request spreads over the whole GPU. A unit that
 //     was cut leaves partial (m, l, O) in the workspace and the CTA that
 //     finishes last merges them, in the order of the CTAs (the same result
 //     every time). Short units (no longer than a warp's even share of all
@@ -55,6 +56,7 @@ constexpr float kPgRescale = 8.0f;  // log2 units
 constexpr float kPgOffset = 6.0f;   // log2 of the factor on P before its rounding to f16
 constexpr int kPgChunk = 32;        // keys of a chunk
 constexpr int kPgWarps = 8;
+constexpr int kPgUnitCost = 24;     // chunks' time that a long unit's rows, barriers and merge take
 constexpr int kPgAhead = 3;         // chunks between the fetch of a block id and its use
 
 template <int D, int NT, bool B16>
@@ -164,7 +166,7 @@ struct PgSeg {
     int c0, c1;         // this piece's chunks
     bool alone;         // a short unit, one warp's
     long long rline;    // position of the request's first chunk on its line
-    long long line0;    // position of a long unit's first chunk
+    long long line0;    // position of a long unit's first chunk on its line
 };
 
 // Loads request b (sizes clamped to what the tables can hold).
@@ -223,13 +225,15 @@ __global__ void __launch_bounds__(256, 1)
     __syncthreads();
     long long W = 0;
     for (int w = 0; w < kPgWarps; ++w) W += scan_w[0][w];
-    // A unit of up to a third of a warp's even share of all chunks is short,
+    // A unit of up to a sixth of a warp's even share of all chunks is short,
     // and one of up to twelve chunks always: a long unit costs its CTA some
     // microseconds of barriers and merging, a short one keeps one warp busy for
     // about 1.3 us a chunk while other warps may have nothing left.
     const long long share = W / (static_cast<long long>(gridDim.x) * kPgWarps);
-    const int T = static_cast<int>(min(max(share / 3, 12ll), 1ll << 30));
-    auto line_long = [&](const PgSeg& s) { return s.nchunk > T ? static_cast<long long>(p.Hkv) * s.nchunk : 0ll; };
+    const int T = static_cast<int>(min(max(share / 6, 12ll), 1ll << 30));
+    auto line_long = [&](const PgSeg& s) {
+        return s.nchunk > T ? static_cast<long long>(p.Hkv) * (s.nchunk + kPgUnitCost) : 0ll;
+    };
     auto line_short = [&](const PgSeg& s) { return s.nchunk <= T ? static_cast<long long>(p.Hkv) * s.nchunk : 0ll; };
     long long ml_ = 0, ms = 0;
     for (int b = b0; b < b1; ++b) {
@@ -290,7 +294,7 @@ __global__ void __launch_bounds__(256, 1)
 
     // ---- the pieces of this warp: first its share of the CTA's pieces of long
     // units, then its short units
-    auto place = [&](PgSeg& s, long long x) {  // long: the piece that starts at x, here or in a later request
+    auto place = [&](PgSeg& s, long long x) -> bool {  // long: the piece that starts at x, here or in a later request
         for (;;) {
             const long long w = line_long(s);
             if (x < s.rline + w) break;
@@ -299,10 +303,12 @@ __global__ void __launch_bounds__(256, 1)
             pg_request(p, s.b, s);
         }
         const long long r = x - s.rline;
-        s.hk = static_cast<int>(r / s.nchunk);
-        s.c0 = static_cast<int>(r - static_cast<long long>(s.hk) * s.nchunk);
-        s.line0 = x - s.c0;
+        s.hk = static_cast<int>(r / (s.nchunk + kPgUnitCost));
+        const int rest = static_cast<int>(r - static_cast<long long>(s.hk) * (s.nchunk + kPgUnitCost));
+        s.line0 = x - rest + kPgUnitCost;
+        s.c0 = max(rest - kPgUnitCost, 0);
         s.c1 = static_cast<int>(min(static_cast<long long>(s.nchunk), x1 - s.line0));
+        return s.c1 > s.c0;  // not only the room in front of a unit
     };
     auto settle = [&](PgSeg& s) -> bool {  // short: hk names the wanted unit of request b, or one past its last
         while (s.hk >= p.Hkv || s.nchunk == 0 || s.nchunk > T) {
@@ -344,22 +350,20 @@ __global__ void __launch_bounds__(256, 1)
             return settle(s);
         }
         const long long x = s.line0 + s.c1;
-        if (x >= x1) return first_short(s);
-        place(s, x);
-        return true;
+        return (x < x1 && place(s, x)) || first_short(s);
     };
     PgSeg cs, is;  // pieces being consumed and being requested
-    bool work = true, iwork = true;
+    cs.alone = false;
+    bool work = false;
     if (x0 < x1) {
-        cs.alone = false;
         cs.b = start_b;
         cs.rline = start_line;
         pg_request(p, cs.b, cs);
-        place(cs, x0);
-    } else {
-        work = iwork = first_short(cs);
+        work = place(cs, x0);
     }
+    work = work || first_short(cs);
     is = cs;
+    bool iwork = work;
 
     const WaitCtx cx{reinterpret_cast<volatile int*>(&abort_s), p.status};
     uint8_t* ring = sm + C::RING_OFF + warp * C::STAGES * 2 * C::TILE;
