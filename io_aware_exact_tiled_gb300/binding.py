@@ -109,19 +109,27 @@ def status_string(code: int) -> str:
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# the current stream's handle without a Stream object (a microsecond or two of
+# a decoding call's host time)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream_handle(stream: Optional[torch.cuda.Stream]):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _check_device(q: torch.Tensor):
     """The kernels run on the current CUDA device: q must live there."""
-    if q.device.type != "cuda":
+    if not q.is_cuda:
         raise ValueError("tensors must be on a CUDA device")
-    if q.device.index != torch.cuda.current_device():
+    if q.get_device() != torch.cuda.current_device():
         raise ValueError(f"tensors are on {q.device} but the current device is cuda:{torch.cuda.current_device()}:"
                          " call under torch.cuda.device(q.device)")
 
@@ -129,7 +137,7 @@ def _check_device(q: torch.Tensor):
 def _in(t: torch.Tensor, shape, dtype, device, name: str) -> torch.Tensor:
     """Check a buffer the kernels read or write as exactly `shape` contiguous
     elements of `dtype` on `device` (the library cannot see its size)."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != tuple(shape) or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on {device}")
     return t
 

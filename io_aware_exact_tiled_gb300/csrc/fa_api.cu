@@ -537,7 +537,7 @@ fa_status fa_cache_plan(const int32_t* new_len, const int32_t* cache_len, int32_
     a.B = B;
     a.max_blocks = max_blocks;
     a.num_blocks = num_blocks;
-    a.block_size = block_size;
+    while ((1 << a.bs_log2) < block_size) ++a.bs_log2;
     a.total = total;
     a.status = static_cast<int*>(workspace);
     int n = 0;

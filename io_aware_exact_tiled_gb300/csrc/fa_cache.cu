@@ -34,6 +34,8 @@ __device__ __forceinline__ uint32_t cluster_size() {
 // into its own shared memory, then takes its share of the tokens. The scan is
 // the only reader of cache_len and free_state, so after the cluster barrier
 // CTA 0 may write their new values, in place if the caller wants that.
+constexpr int kPlanKeep = 4;
+
 struct PlanSum {
     long long tok, need, freed;
 };
@@ -52,18 +54,21 @@ struct PlanItem {
     bool bad;    // a length out of range
 };
 
-__device__ __forceinline__ PlanItem plan_item(const PlanArgs& p, int b) {
+__device__ __forceinline__ int plan_blocks(const PlanArgs& p, int len) {  // len < 2^31 - 256
+    return (len + (1 << p.bs_log2) - 1) >> p.bs_log2;
+}
+
+__device__ __forceinline__ PlanItem plan_item(const PlanArgs& p, int raw, int len) {
     PlanItem it;
-    const int cap = p.max_blocks * p.block_size;  // < 2^31, checked on the host
-    const int raw = p.new_len[b], len = p.cache_len[b];
+    const int cap = p.max_blocks << p.bs_log2;  // < 2^31, checked on the host
     it.len = min(max(len, 0), cap);
     it.bad = len != it.len;
     it.drop = raw < 0;
     it.n = max(raw, 0);
     it.fits = static_cast<long long>(it.len) + it.n <= cap;
-    it.had = (it.len + p.block_size - 1) / p.block_size;
+    it.had = plan_blocks(p, it.len);
     it.need = 0;
-    if (!it.drop && it.fits) it.need = (it.len + it.n + p.block_size - 1) / p.block_size - it.had;
+    if (!it.drop && it.fits) it.need = plan_blocks(p, it.len + it.n) - it.had;
     return it;
 }
 
@@ -90,11 +95,21 @@ __global__ void __launch_bounds__(1024) fa_cache_plan_kernel(const __grid_consta
     // prefix sums over the requests, `per` consecutive ones for each thread
     const int per = (p.B + nth - 1) / nth;
     const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-    PlanSum mine{0, 0, 0};
-    for (int b = b0; b < b1; ++b) {
-        const PlanItem it = plan_item(p, b);
-        mine = plan_add(mine, {it.n, it.need, it.drop ? it.had : 0});
+    // the first few of them stay in registers, their loads in flight together
+    int raw[kPlanKeep], len0[kPlanKeep];
+#pragma unroll
+    for (int k = 0; k < kPlanKeep; ++k) {
+        raw[k] = b0 + k < b1 ? p.new_len[b0 + k] : 0;
+        len0[k] = b0 + k < b1 ? p.cache_len[b0 + k] : 0;
     }
+    auto each = [&](auto&& f) {
+#pragma unroll
+        for (int k = 0; k < kPlanKeep; ++k)
+            if (b0 + k < b1) f(b0 + k, plan_item(p, raw[k], len0[k]));
+        for (int b = b0 + kPlanKeep; b < b1; ++b) f(b, plan_item(p, p.new_len[b], p.cache_len[b]));
+    };
+    PlanSum mine{0, 0, 0};
+    each([&](int, const PlanItem& it) { mine = plan_add(mine, {it.n, it.need, it.drop ? it.had : 0}); });
     PlanSum inc = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -112,8 +127,7 @@ __global__ void __launch_bounds__(1024) fa_cache_plan_kernel(const __grid_consta
     PlanSum run{base.tok + inc.tok - mine.tok, base.need + inc.need - mine.need, base.freed + inc.freed - mine.freed};
     bool invalid = all.tok > p.total, refused = false;
     int granted = 0;
-    for (int b = b0; b < b1; ++b) {
-        const PlanItem it = plan_item(p, b);
+    each([&](int b, const PlanItem& it) {
         const bool room = it.need == 0 || run.need + it.need <= count;
         // tokens past the slot array (the lengths add up to more than total)
         const bool listed = run.tok + it.n <= p.total;
@@ -132,7 +146,7 @@ __global__ void __launch_bounds__(1024) fa_cache_plan_kernel(const __grid_consta
         }
         invalid |= it.bad || !it.fits;
         run = plan_add(run, {it.n, it.need, it.drop ? it.had : 0});
-    }
+    });
     if (tid == nth - 1) tok_off[p.B] = static_cast<int>(min(all.tok, static_cast<long long>(p.total)));
     if (granted) atomicMax(&granted_s, granted);
     if (invalid) invalid_s = 1;
@@ -148,7 +162,7 @@ __global__ void __launch_bounds__(1024) fa_cache_plan_kernel(const __grid_consta
             const int mid = (lo + hi) >> 1;
             if (tok_off[mid] <= t0) lo = mid; else hi = mid;
         }
-        int b = lo;
+        int b = lo, blk = -1, blk_b = -1, blk_j = 0;  // the block looked up last
         const int t1 = min(t0 + 4, p.total);
         for (int t = t0; t < t1; ++t) {
             int slot = -1;
@@ -156,19 +170,22 @@ __global__ void __launch_bounds__(1024) fa_cache_plan_kernel(const __grid_consta
                 while (t >= tok_off[b + 1]) ++b;
                 const int len = lens[b];
                 if (len >= 0) {
-                    const int pos = len + t - tok_off[b], j = pos / p.block_size, r = pos - j * p.block_size;
-                    const int had = (len + p.block_size - 1) / p.block_size;
-                    int32_t* row = p.block_table + static_cast<size_t>(b) * p.max_blocks;
-                    int blk;
-                    if (j < had) {
-                        blk = row[j];
-                    } else {
-                        long long at = static_cast<long long>(head) + blk_off[b] + (j - had);
-                        at = at >= cap ? at - cap : at;
-                        blk = p.free_blocks[at];
-                        if (r == 0) row[j] = blk;
+                    const int pos = len + t - tok_off[b], j = pos >> p.bs_log2, r = pos & ((1 << p.bs_log2) - 1);
+                    if (b != blk_b || j != blk_j) {
+                        const int had = plan_blocks(p, len);
+                        int32_t* row = p.block_table + static_cast<size_t>(b) * p.max_blocks;
+                        blk_b = b;
+                        blk_j = j;
+                        if (j < had) {
+                            blk = row[j];
+                        } else {
+                            long long at = static_cast<long long>(head) + blk_off[b] + (j - had);
+                            at = at >= cap ? at - cap : at;
+                            blk = p.free_blocks[at];
+                            if (r == 0) row[j] = blk;  // the thread that has the block's first token
+                        }
                     }
-                    if (blk >= 0 && blk < cap) slot = blk * p.block_size + r;
+                    if (blk >= 0 && blk < cap) slot = (blk << p.bs_log2) + r;
                     else invalid = true;
                 }
             }
@@ -181,14 +198,16 @@ __global__ void __launch_bounds__(1024) fa_cache_plan_kernel(const __grid_consta
     if (all.freed > room) invalid = true;
     for (int b = static_cast<int>(rank) * nw + warp; b < p.B && all.freed; b += static_cast<int>(ranks) * nw) {
         if (lens[b] > -2) continue;
-        const int len = -2 - lens[b], had = (len + p.block_size - 1) / p.block_size;
+        const int len = -2 - lens[b], had = plan_blocks(p, len);
         const int32_t* row = p.block_table + static_cast<size_t>(b) * p.max_blocks;
         for (int j = lane; j < had; j += 32) {
             const int blk = row[j];
             const bool ok = blk >= 0 && blk < cap;
             if (!ok) invalid = true;
             const long long k = static_cast<long long>(blk_off[b]) + j;
-            if (k < room) p.free_blocks[(static_cast<long long>(head) + count + k) % cap] = ok ? blk : -1;
+            long long at = static_cast<long long>(head) + count + k;
+            at = at >= cap ? at - cap : at;
+            if (k < room) p.free_blocks[at] = ok ? blk : -1;
         }
     }
     if (rank == 0) {
@@ -215,16 +234,25 @@ __global__ void __launch_bounds__(1024) fa_cache_plan_kernel(const __grid_consta
 
 cudaError_t launch_cache_plan(const PlanArgs& a, cudaStream_t stream, int* nlaunch) {
     const size_t smem = (static_cast<size_t>(a.B) * 3 + 1) * sizeof(int);
-    cudaError_t e = cudaFuncSetAttribute(fa_cache_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (3 * kPlanMaxB + 4) * sizeof(int));
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = once_per_device(done, [] {
+        cudaError_t r = cudaFuncSetAttribute(fa_cache_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (3 * kPlanMaxB + 4) * sizeof(int));
+        if (r == cudaSuccess)
+            r = cudaFuncSetAttribute(fa_cache_plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        return r;
+    });
     if (e != cudaSuccess) return e;
+    // One CTA where latency is all there is (16 requests of a token each: 4.3 us),
+    // a cluster of 16 where there are many requests or tokens (4096 requests,
+    // 117K tokens: 22 us with eight CTAs, 17 with sixteen).
     const bool big = a.B > 1024 || a.total > 4096;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = big ? 8 : 1;
+    at[0].val.clusterDim.x = big ? 16 : 1;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(big ? 8 : 1);
+    cfg.gridDim = dim3(big ? 16 : 1);
     cfg.blockDim = dim3(big ? 1024 : 256);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -244,104 +272,203 @@ cudaError_t launch_cache_plan(const PlanArgs& a, cudaStream_t stream, int* nlaun
 // rows the block holds already are then moved to the new scale. With powers
 // of two x / scale is exact before its one rounding to E4M3, and a move only
 // rounds what falls below the smallest normal number.
-template <int D>
-__global__ void __launch_bounds__(256) fa_cache_append_kernel(const __grid_constant__ AppendArgs p) {
-    constexpr int LPR = D / 8;      // lanes per row, eight values (16 bytes) each
-    constexpr int RPW = 32 / LPR;   // rows of one warp-wide load
-    const int lane = threadIdx.x & 31;
-    const long long w = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int t = static_cast<int>(w / (2 * p.H));
-    if (t >= p.total) return;
-    const int rest = static_cast<int>(w - static_cast<long long>(t) * (2 * p.H));
-    const int h = rest >> 1;
-    const int bs = p.block_size, nslots = p.num_blocks * bs;
-    const int slot = p.slots[t];
-    if (slot < 0 || slot >= nslots) return;
-    const int blk = slot / bs;
-    if (t > 0) {
-        const int before = p.slots[t - 1];
-        if (before >= 0 && before < nslots && before / bs == blk) return;  // an earlier token's warp takes the block
-    }
-    // the run: the following tokens whose slots lie in the same block
-    int end = t + 1;
-    for (;;) {
-        const int u = end + lane;
-        const int s = u < p.total ? p.slots[u] : -1;
-        const uint32_t in = __ballot_sync(0xffffffffu, s >= 0 && s / bs == blk);
-        if (in != 0xffffffffu) {
-            end += __ffs(~in) - 1;
-            break;
-        }
-        end += 32;
-    }
-    const uint16_t* src = static_cast<const uint16_t*>(rest & 1 ? p.v : p.k);
-    uint8_t* cache = (rest & 1 ? p.v_cache : p.k_cache) + (static_cast<size_t>(blk) * p.H + h) * bs * D;
-    float* scale = (rest & 1 ? p.v_scale : p.k_scale) + static_cast<size_t>(blk) * p.H + h;
-    const int sub = lane / LPR, col = (lane % LPR) * 8;
-    // largest finite magnitude, as bf16 bits (ordered like the values)
-    uint32_t top = 0;
-    for (int u = t + sub; u < end; u += RPW) {
-        const uint4 x = *reinterpret_cast<const uint4*>(src + (static_cast<size_t>(u) * p.H + h) * D + col);
-        const uint32_t wds[4] = {x.x, x.y, x.z, x.w};
+//
+// A CTA takes the runs (consecutive tokens whose slots lie in one block) that
+// start among its `span` tokens, for one head and one of K and V. One or two
+// runs, as in a prompt, are each the whole CTA's: a thread holds 16 bytes of L
+// rows, so the data are read once and the scale found on the way. More runs, as
+// in a decoding batch, go to a warp each, which reads its rows twice (they stay
+// in the L1 cache).
+struct AppendRun {
+    const uint16_t* src;  // this head's first row: token t is src + t * H * D
+    uint8_t* cache;       // the block's rows of this head
+    float* scale;
+    size_t stride;        // H * D
+};
+
+// Largest finite magnitude of eight bf16 values, as bf16 bits (ordered like
+// the values).
+__device__ __forceinline__ uint32_t append_amax(uint4 x, uint32_t top) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t lo = wds[i] & 0x7FFFu, hi = (wds[i] >> 16) & 0x7FFFu;
-            top = max(top, lo < 0x7F80u ? lo : 0u);
-            top = max(top, hi < 0x7F80u ? hi : 0u);
-        }
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
+        top = max(top, lo < 0x7F80u ? lo : 0u);
+        top = max(top, hi < 0x7F80u ? hi : 0u);
     }
-    top = __reduce_max_sync(0xffffffffu, top);
+    return top;
+}
+__device__ __forceinline__ uint2 append_quantise(uint4 x, float inv) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t y[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t a = w[2 * i], b = w[2 * i + 1];
+        y[i] = pack_e4m3x2(__uint_as_float(a << 16) * inv, __uint_as_float(a & 0xFFFF0000u) * inv) |
+               (pack_e4m3x2(__uint_as_float(b << 16) * inv, __uint_as_float(b & 0xFFFF0000u) * inv) << 16);
+    }
+    return make_uint2(y[0], y[1]);
+}
+// The scale of a run whose largest magnitude is `top`, given the block's scale
+// so far (0: none).
+__device__ __forceinline__ float append_scale(uint32_t top, float old) {
     // amax / 448 = (1.m / 1.75) 2^(E - 135)
     const int e = max(static_cast<int>(top >> 7) - 135 + ((top & 127u) > 96u ? 1 : 0), -126);
-    float s_new = exp2i(e), s_old = 0.f;
-    const int first = slot - blk * bs;
-    if (first > 0) {
-        s_old = *scale;
-        s_old = s_old > 0.f && s_old < CUDART_INF_F ? s_old : 0.f;
-        const float up = __uint_as_float((__float_as_uint(s_old) + 0x7FFFFFu) & 0x7F800000u);
-        if (up < CUDART_INF_F) s_new = fmaxf(s_new, up);
-    }
-    __syncwarp();
-    if (first > 0 && s_new != s_old) {
-        const float f = s_old / s_new;
-        for (int i = lane * 16; i < first * D; i += 512) {
-            uint4* at = reinterpret_cast<uint4*>(cache + i);
-            const uint4 x = *at;
-            uint32_t y[4] = {x.x, x.y, x.z, x.w};
+    const float s = exp2i(e), up = __uint_as_float((__float_as_uint(old) + 0x7FFFFFu) & 0x7F800000u);
+    return up < CUDART_INF_F ? fmaxf(s, up) : s;
+}
+__device__ __forceinline__ float append_old_scale(const float* scale) {
+    const float s = *scale;
+    return s > 0.f && s < CUDART_INF_F ? s : 0.f;
+}
+// Rows in front of the run to a new scale: factor f, 16 bytes a step.
+__device__ __forceinline__ void append_move(uint8_t* cache, int bytes, float f, int i, int step) {
+    for (i *= 16; i < bytes; i += step * 16) {
+        uint4* at = reinterpret_cast<uint4*>(cache + i);
+        const uint4 x = *at;
+        uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float a, b, c, d;
-                f2_split(f2_from_e4m3x2(y[k] & 0xFFFFu), a, b);
-                f2_split(f2_from_e4m3x2(y[k] >> 16), c, d);
-                y[k] = pack_e4m3x2(a * f, b * f) | (pack_e4m3x2(c * f, d * f) << 16);
-            }
-            *at = make_uint4(y[0], y[1], y[2], y[3]);
+        for (int k = 0; k < 4; ++k) {
+            float a, b, c, d;
+            f2_split(f2_from_e4m3x2(y[k] & 0xFFFFu), a, b);
+            f2_split(f2_from_e4m3x2(y[k] >> 16), c, d);
+            y[k] = pack_e4m3x2(a * f, b * f) | (pack_e4m3x2(c * f, d * f) << 16);
         }
-    }
-    if (lane == 0) *scale = s_new;
-    const float inv = 1.f / s_new;  // a power of two: exact
-    for (int u = t + sub; u < end; u += RPW) {
-        const uint4 x = *reinterpret_cast<const uint4*>(src + (static_cast<size_t>(u) * p.H + h) * D + col);
-        const uint32_t wds[4] = {x.x, x.y, x.z, x.w};
-        uint32_t y[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t a = wds[2 * i], b = wds[2 * i + 1];
-            y[i] = pack_e4m3x2(__uint_as_float(a << 16) * inv, __uint_as_float(a & 0xFFFF0000u) * inv) |
-                   (pack_e4m3x2(__uint_as_float(b << 16) * inv, __uint_as_float(b & 0xFFFF0000u) * inv) << 16);
-        }
-        *reinterpret_cast<uint2*>(cache + static_cast<size_t>(p.slots[u] - blk * bs) * D + col) =
-            make_uint2(y[0], y[1]);
+        *at = make_uint4(y[0], y[1], y[2], y[3]);
     }
 }
 
+template <int D, int L>
+__global__ void __launch_bounds__(256) fa_cache_append_kernel(const __grid_constant__ AppendArgs p, int span) {
+    constexpr int LPR = D / 8;         // lanes per row, eight values (16 bytes) each
+    constexpr int ROWS = 256 / LPR;    // rows of a CTA-wide load
+    __shared__ int blk_of[512];        // block of tokens t0 .. (-1: none)
+    __shared__ int leads[256], nlead;
+    __shared__ uint32_t warp_top[8];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // the heads of a span follow one another: they share its rows' DRAM pages
+    const int part = static_cast<int>(blockIdx.x / (2u * p.H)), hv = static_cast<int>(blockIdx.x - part * (2u * p.H));
+    const int h = hv >> 1, bs = p.block_size, nslots = p.num_blocks * bs;
+    const bool is_v = hv & 1;
+    const long long t0 = static_cast<long long>(part) * span;
+    auto block_at = [&](long long t) {
+        if (t < 0 || t >= p.total) return -1;
+        const int s = p.slots[t];
+        return s >= 0 && s < nslots ? s / bs : -1;
+    };
+    // blocks of the span's tokens and of those that its last run may reach
+    for (int i = tid; i < span + bs; i += 256) blk_of[i] = block_at(t0 + i);
+    if (tid == 0) nlead = 0;
+    __syncthreads();
+    if (tid < span && blk_of[tid] >= 0 && blk_of[tid] != (tid ? blk_of[tid - 1] : block_at(t0 - 1)))
+        leads[atomicAdd(&nlead, 1)] = tid;
+    __syncthreads();
+    const int n = nlead;
+    if (n == 0) return;
+    AppendRun r;
+    r.src = static_cast<const uint16_t*>(is_v ? p.v : p.k) + static_cast<size_t>(h) * D;
+    r.stride = static_cast<size_t>(p.H) * D;
+    auto open = [&](int lead) {  // returns the run's first row in its block
+        const size_t at = static_cast<size_t>(blk_of[lead]) * p.H + h;
+        r.cache = (is_v ? p.v_cache : p.k_cache) + at * bs * D;
+        r.scale = (is_v ? p.v_scale : p.k_scale) + at;
+        return p.slots[t0 + lead] - blk_of[lead] * bs;
+    };
+    auto run_end = [&](int lead) {  // first token behind the run, as far as blk_of reaches (block_size tokens)
+        const int blk = blk_of[lead];
+        for (int e = lead + 1;; e += 32) {
+            const int i = e + lane;
+            const uint32_t in = __ballot_sync(0xffffffffu, i < min(lead + bs, span + bs) && blk_of[i] == blk);
+            if (in != 0xffffffffu) return e + __ffs(~in) - 1;
+        }
+    };
+    if (n <= 2) {
+        // ------------------------------------------------ the CTA takes the runs in turn
+        const int row = tid / LPR, col = (tid % LPR) * 8;
+        for (int k = 0; k < n; ++k) {
+            const int lead = leads[k], end = run_end(lead), first = open(lead);
+            uint4 x[L];
+            int at[L];
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                const int t = lead + i * ROWS + row;
+                x[i] = make_uint4(0u, 0u, 0u, 0u);
+                at[i] = -1;
+                if (t < end) {
+                    x[i] = *reinterpret_cast<const uint4*>(r.src + (t0 + t) * r.stride + col);
+                    at[i] = p.slots[t0 + t];
+                }
+            }
+            const float old = first > 0 ? append_old_scale(r.scale) : 0.f;
+#pragma unroll
+            for (int i = 0; i < L; ++i) top = append_amax(x[i], top);
+            top = __reduce_max_sync(0xffffffffu, top);
+            if (lane == 0) warp_top[warp] = top;
+            __syncthreads();  // every thread has read the scale so far, too
+#pragma unroll
+            for (int w = 0; w < 8; ++w) top = max(top, warp_top[w]);
+            const float s = append_scale(top, old), inv = 1.f / s;  // a power of two: exact
+            if (first > 0 && s != old) append_move(r.cache, first * D, old / s, tid, 256);
+            if (tid == 0) *r.scale = s;
+            const int base = blk_of[lead] * bs;
+            // the run's own rows, after the moved ones of a slot that it writes again
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < L; ++i)
+                if (at[i] >= 0)
+                    *reinterpret_cast<uint2*>(r.cache + static_cast<size_t>(at[i] - base) * D + col) =
+                        append_quantise(x[i], inv);
+        }
+        return;
+    }
+    // ---------------------------------------------------- a warp for each run
+    constexpr int RPW = 32 / LPR;
+    const int sub = lane / LPR, col = (lane % LPR) * 8;
+    for (int k = warp; k < n; k += 8) {
+        const int lead = leads[k], end = run_end(lead), first = open(lead);
+        const float old = first > 0 ? append_old_scale(r.scale) : 0.f;
+        uint32_t top = 0;
+        for (int t = lead + sub; t < end; t += RPW)
+            top = append_amax(*reinterpret_cast<const uint4*>(r.src + (t0 + t) * r.stride + col), top);
+        top = __reduce_max_sync(0xffffffffu, top);
+        const float s = append_scale(top, old), inv = 1.f / s;
+        if (first > 0 && s != old) append_move(r.cache, first * D, old / s, lane, 32);
+        __syncwarp();
+        if (lane == 0) *r.scale = s;
+        const int base = blk_of[lead] * bs;
+        for (int t = lead + sub; t < end; t += RPW) {
+            const uint4 x = *reinterpret_cast<const uint4*>(r.src + (t0 + t) * r.stride + col);
+            *reinterpret_cast<uint2*>(r.cache + static_cast<size_t>(p.slots[t0 + t] - base) * D + col) =
+                append_quantise(x, inv);
+        }
+    }
+}
+
+template <int D, int L>
+static void launch_append(const AppendArgs& a, cudaStream_t stream) {
+    // Tokens of a CTA: a block's in a large batch (most likely prompts, a run or
+    // two in each span), sixteen in a small one, so that the many runs of a
+    // decoding batch spread over the GPU.
+    const int span = a.total > 1024 ? min(a.block_size, 64) : 16;
+    const unsigned grid = static_cast<unsigned>((a.total + span - 1) / span) * 2u * a.H;
+    fa_cache_append_kernel<D, L><<<grid, 256, 0, stream>>>(a, span);
+}
+
 cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t stream, int* nlaunch) {
-    const long long warps = static_cast<long long>(a.total) * a.H * 2;
-    const unsigned grid = static_cast<unsigned>((warps + 7) / 8);
-    if (a.d == 64)
-        fa_cache_append_kernel<64><<<grid, 256, 0, stream>>>(a);
-    else
-        fa_cache_append_kernel<128><<<grid, 256, 0, stream>>>(a);
+    const int rows = a.d == 64 ? 32 : 16, l = (a.block_size + rows - 1) / rows;
+    if (a.d == 64) {
+        if (l == 1) launch_append<64, 1>(a, stream);
+        else if (l == 2) launch_append<64, 2>(a, stream);
+        else if (l == 4) launch_append<64, 4>(a, stream);
+        else launch_append<64, 8>(a, stream);
+    } else {
+        if (l == 1) launch_append<128, 1>(a, stream);
+        else if (l == 2) launch_append<128, 2>(a, stream);
+        else if (l == 4) launch_append<128, 4>(a, stream);
+        else if (l == 8) launch_append<128, 8>(a, stream);
+        else launch_append<128, 16>(a, stream);
+    }
     *nlaunch = 1;
     return cudaGetLastError();
 }

@@ -193,8 +193,6 @@ __global__ void __launch_bounds__(256, 1)
     __shared__ long long start_line;
     __shared__ int nan_seen, abort_s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
-    // the row-tile kernel behind this one, if there is one, works on other rows
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // ---- all chunks, then the lines of long and of short units
     const int per = (p.B + 255) / 256;
@@ -900,8 +898,11 @@ static cudaError_t launch_split(const PagedArgs& a, const PagedParams& p, cudaSt
     if (!make_tmap_2d_sw128(&tk, a.k_cache, rows, 128, 1, box, 128) ||
         !make_tmap_2d_sw128(&tv, a.v_cache, rows, 128, 1, box, 128))
         return cudaErrorInvalidValue;
-    cudaError_t e =
-        cudaFuncSetAttribute(fa_paged_split_kernel<D, NT, B16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = once_per_device(done, [] {
+        return cudaFuncSetAttribute(fa_paged_split_kernel<D, NT, B16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    C::SMEM);
+    });
     if (e != cudaSuccess) return e;
     fa_paged_split_kernel<D, NT, B16><<<kPagedCtas, 256, C::SMEM, stream>>>(tk, tv, p);
     return cudaGetLastError();

@@ -3,6 +3,8 @@
 // (fa_paged.cu).
 #pragma once
 
+#include <atomic>
+
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -26,7 +28,7 @@ struct PlanArgs {
     int32_t* free_state_out;
     int32_t* cu_seqlens;  // [B + 1]
     int32_t* slots;       // [total]
-    int B, max_blocks, num_blocks, block_size, total;
+    int B, max_blocks, num_blocks, bs_log2, total;
     int* status;
 };
 
@@ -70,6 +72,20 @@ inline long long paged_max_tile_units(int B, int Hq, int Hkv, int total, int max
     const long long group = Hq / Hkv;
     if (!paged_has_tiles(max_new, static_cast<int>(group))) return 0;
     return Hkv * (B + total * group / kPagedTileRows);
+}
+
+// Runs `set` (function attributes) once for each device; `done` remembers
+// which, for up to 64 devices.
+template <typename F>
+inline cudaError_t once_per_device(std::atomic<uint64_t>& done, F&& set) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = set();
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
 }
 
 // Division of 0 <= x < 2^31 by a divisor that the host knows: with

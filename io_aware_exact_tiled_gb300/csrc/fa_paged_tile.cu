@@ -874,7 +874,10 @@ static cudaError_t launch_tile(const PagedArgs& a, const PtParams& p, cudaStream
     const uint32_t box = a.block_size < 128 ? a.block_size : 128;
     if (!make_tmap_rows(&tk, a.k_cache, rows, D, box) || !make_tmap_rows(&tv, a.v_cache, rows, D, box))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(fa_paged_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = once_per_device(done, [] {
+        return cudaFuncSetAttribute(fa_paged_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    });
     if (e != cudaSuccess) return e;
     fa_paged_tile_kernel<D><<<kPagedCtas, 512, C::SMEM, stream>>>(tk, tv, p);
     return cudaGetLastError();
