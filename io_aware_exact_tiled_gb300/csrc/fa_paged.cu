@@ -14,7 +14,7 @@
 //
 // Design:
 //   * Work is counted in chunks of 32 keys. A unit is (request, key head), with
-//     at most RT = 8, 16 or 32 query rows (fa_paged_tile.cu takes requests of
+//     at most RT = 8, 16, 24 or 32 query rows (fa_paged_tile.cu takes requests of
 //     more). The chunks of the long units form one line (with room in front of
 //     each unit for what its start and end cost) that is cut into equal quotas,
 //     one for each persistent CTA, so ragged lengths balance by themselves and
@@ -62,7 +62,7 @@ constexpr int kPgAhead = 3;         // chunks between the fetch of a block id an
 template <int D, int NT, bool B16>
 struct PgCfg {
     static constexpr int RT = 8 * NT;                     // query rows of a unit
-    static constexpr int STAGES = D == 64 ? (NT == 4 ? 4 : 5) : (NT == 1 ? 3 : 2);
+    static constexpr int STAGES = D == 64 ? (NT >= 3 ? 4 : 5) : (NT == 1 ? 3 : 2);
     static constexpr int TILE = kPgChunk * D;             // bytes of a chunk's K (or V)
     static constexpr int SUBS = B16 ? 2 : 1;              // boxes of a tile
     static constexpr int BOX = TILE / SUBS;
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(256, 1)
     constexpr int RT = C::RT;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    __shared__ long long scan_w[2][kPgWarps];
+    __shared__ long long scan_w[3][kPgWarps];
     __shared__ long long short_base[257];  // chunks of short units in front of each thread's requests
     __shared__ int start_b, last_s;
     __shared__ long long start_line;
@@ -211,9 +211,9 @@ __global__ void __launch_bounds__(256, 1)
     if (tid == 0) {
         abort_s = 0;
         nan_seen = 0;
-        for (int i = 0; i < kPgWarps * C::STAGES; ++i) mbar_init(reinterpret_cast<uint64_t*>(sm + C::BAR_OFF) + i, 1);
-        fence_barrier_init();
     }
+    if (lane < C::STAGES) mbar_init(&bars[lane], 1);
+    fence_barrier_init();
     int* first_nan = reinterpret_cast<int*>(sm + C::NAN_OFF);
     for (int i = tid; i < kPgWarps * D; i += 256) first_nan[i] = INT_MAX;
     long long sum = mw;
@@ -227,52 +227,67 @@ __global__ void __launch_bounds__(256, 1)
     // and one of up to twelve chunks always: a long unit costs its CTA some
     // microseconds of barriers and merging, a short one keeps one warp busy for
     // about 1.3 us a chunk while other warps may have nothing left.
-    const long long share = W / (static_cast<long long>(gridDim.x) * kPgWarps);
-    const int T = static_cast<int>(min(max(share / 6, 12ll), 1ll << 30));
+    const long long share = W / (kPagedCtas * kPgWarps);
+    int T = static_cast<int>(min(max(share / 6, 12ll), 1ll << 30));
     auto line_long = [&](const PgSeg& s) {
         return s.nchunk > T ? static_cast<long long>(p.Hkv) * (s.nchunk + kPgUnitCost) : 0ll;
     };
     auto line_short = [&](const PgSeg& s) { return s.nchunk <= T ? static_cast<long long>(p.Hkv) * s.nchunk : 0ll; };
-    long long ml_ = 0, ms = 0;
+    long long ml_ = 0, ms = 0, ma = 0;  // long, short, all as long ones
     for (int b = b0; b < b1; ++b) {
         PgSeg s;
         pg_request(p, b, s);
         ml_ += line_long(s);
         ms += line_short(s);
+        if (s.nchunk > 0) ma += static_cast<long long>(p.Hkv) * (s.nchunk + kPgUnitCost);
     }
-    long long il = ml_, is_ = ms;
+    long long il = ml_, is_ = ms, ia = ma;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const long long a = __shfl_up_sync(0xffffffffu, il, off), c = __shfl_up_sync(0xffffffffu, is_, off);
+        const long long d = __shfl_up_sync(0xffffffffu, ia, off);
         if (lane >= off) {
             il += a;
             is_ += c;
+            ia += d;
         }
     }
     __syncthreads();
     if (lane == 31) {
         scan_w[0][warp] = il;
         scan_w[1][warp] = is_;
+        scan_w[2][warp] = ia;
     }
     __syncthreads();
-    long long Wl = 0, Ws = 0, bw = il - ml_, bs = is_ - ms;
+    long long Wl = 0, Ws = 0, Wa = 0, bw = il - ml_, bs = is_ - ms, ba = ia - ma;
+#pragma unroll
     for (int w = 0; w < kPgWarps; ++w) {
         if (w < warp) {
             bw += scan_w[0][w];
             bs += scan_w[1][w];
+            ba += scan_w[2][w];
         }
         Wl += scan_w[0][w];
         Ws += scan_w[1][w];
+        Wa += scan_w[2][w];
+    }
+    // A few short units among long ones would only come after everything else:
+    // they are taken as long ones.
+    if (Ws * 8 < W) {
+        T = 0;
+        Wl = Wa;
+        Ws = 0;
+        bw = ba;
+        ml_ = ma;
+        bs = 0;
     }
     // equal quotas of the long line, at least one chunk for each warp
-    const long long quota = max((Wl + gridDim.x - 1) / static_cast<long long>(gridDim.x),
-                                static_cast<long long>(kPgWarps));
+    const long long quota = max((Wl + kPagedCtas - 1) / kPagedCtas, static_cast<long long>(kPgWarps));
     const long long x0 = quota * blockIdx.x, x1 = min(x0 + quota, Wl);
     // the short units that start in this warp's part of their line; parts that
     // follow one another lie in different CTAs
-    const long long nwarp = static_cast<long long>(gridDim.x) * kPgWarps;
-    const long long part = (Ws + nwarp - 1) / nwarp;
-    const long long y0 = part * (static_cast<long long>(warp) * gridDim.x + blockIdx.x), y1 = min(y0 + part, Ws);
+    const long long part = (Ws + kPagedCtas * kPgWarps - 1) / (kPagedCtas * kPgWarps);
+    const long long y0 = part * (warp * kPagedCtas + static_cast<int>(blockIdx.x)), y1 = min(y0 + part, Ws);
     short_base[tid] = bs;
     if (tid == 255) short_base[256] = Ws;
     if (x0 < x1 && x0 >= bw && x0 < bw + ml_) {
@@ -301,7 +316,7 @@ __global__ void __launch_bounds__(256, 1)
             pg_request(p, s.b, s);
         }
         const long long r = x - s.rline;
-        s.hk = static_cast<int>(r / (s.nchunk + kPgUnitCost));
+        s.hk = static_cast<int>(div_short(r, s.nchunk + kPgUnitCost));
         const int rest = static_cast<int>(r - static_cast<long long>(s.hk) * (s.nchunk + kPgUnitCost));
         s.line0 = x - rest + kPgUnitCost;
         s.c0 = max(rest - kPgUnitCost, 0);
@@ -339,7 +354,7 @@ __global__ void __launch_bounds__(256, 1)
             ++s.b;
             pg_request(p, s.b, s);
         }
-        s.hk = static_cast<int>((y0 - s.rline + s.nchunk - 1) / s.nchunk);
+        s.hk = static_cast<int>(div_short(y0 - s.rline + s.nchunk - 1, s.nchunk));
         return settle(s);
     };
     auto next = [&](PgSeg& s) -> bool {
@@ -375,19 +390,21 @@ __global__ void __launch_bounds__(256, 1)
     auto chunk_of = [&](const PgSeg& s, int k) { return s.alone ? s.c0 + k : s.c0 + warp + kPgWarps * k; };
     int* idq = reinterpret_cast<int*>(sm + C::ID_OFF) + warp * 8;  // [4][2] block ids
     int ik = 0, issued = 0, consumed = 0, fetched = 0;
+    auto prefetch_q = [&](const PgSeg& s) {  // a unit's query rows, wanted soon
+        if (lane >= s.n * p.G) return;
+        const int tok = p.by_g.div(lane);
+        const uint16_t* row = p.q + (static_cast<size_t>(s.tok0 + tok) * p.Hq + s.hk * p.G + (lane - tok * p.G)) * D;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(row));
+        if (D == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + 64));
+    };
+    if (work) prefetch_q(cs);
     int hk_in[kPgAhead] = {};  // (key head << bs_log2) + first row; -1: no chunk
     int in_len[kPgAhead] = {};  // boxes with keys in front of the last token's end
     auto fetch = [&](int at) {
         while (iwork && chunk_of(is, ik) >= is.c1) {
             iwork = next(is);
             ik = 0;
-            if (iwork && lane < is.n * p.G) {  // its query rows will be wanted soon
-                const int tok = p.by_g.div(lane);
-                const uint16_t* row =
-                    p.q + (static_cast<size_t>(is.tok0 + tok) * p.Hq + is.hk * p.G + (lane - tok * p.G)) * D;
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(row));
-                if (D == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + 64));
-            }
+            if (iwork) prefetch_q(is);
         }
         hk_in[at] = -1;
         if (!iwork) return;
@@ -826,7 +843,8 @@ __global__ void __launch_bounds__(256, 1)
         if (!whole) {
             // the CTAs that hold pieces of this unit are consecutive; the last
             // one to get here merges them in order
-            const int f = static_cast<int>(cs.line0 / quota), e = static_cast<int>((cs.line0 + cs.nchunk - 1) / quota);
+            const int f = static_cast<int>(div_short(cs.line0, quota));
+            const int e = static_cast<int>(div_short(cs.line0 + cs.nchunk - 1, quota));
             __threadfence();
             __syncthreads();
             if (tid == 0) last_s = atomicAdd(&p.counters[cs.b * p.Hkv + cs.hk], 1) == e - f;
@@ -914,6 +932,7 @@ static cudaError_t launch_split_d(const PagedArgs& a, const PagedParams& p, cuda
     const long long rows = static_cast<long long>(a.max_new) * p.G;
     if (rows <= 8) return b16 ? launch_split<D, 1, true>(a, p, stream) : launch_split<D, 1, false>(a, p, stream);
     if (rows <= 16) return b16 ? launch_split<D, 2, true>(a, p, stream) : launch_split<D, 2, false>(a, p, stream);
+    if (rows <= 24) return b16 ? launch_split<D, 3, true>(a, p, stream) : launch_split<D, 3, false>(a, p, stream);
     return b16 ? launch_split<D, 4, true>(a, p, stream) : launch_split<D, 4, false>(a, p, stream);
 }
 

@@ -88,6 +88,14 @@ inline cudaError_t once_per_device(std::atomic<uint64_t>& done, F&& set) {
     return e;
 }
 
+#ifdef __CUDACC__
+// x / d for 0 <= x, 0 < d: in 32 bits where x has no more.
+__device__ __forceinline__ long long div_short(long long x, long long d) {
+    if (((x | d) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(d);
+    return x / d;
+}
+#endif
+
 // Division of 0 <= x < 2^31 by a divisor that the host knows: with
 // l = ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1 the quotient is
 // (umulhi(m, x) + x) >> l (Granlund and Montgomery, PLDI 1994).

@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(512, 1)
         W += scan_w[w];
         U += scan_u[w];
     }
-    const long long quota = max((W + gridDim.x - 1) / static_cast<long long>(gridDim.x), 2ll);
+    const long long quota = max((W + kPagedCtas - 1) / kPagedCtas, 2ll);
     const long long x0 = quota * blockIdx.x, x1 = min(x0 + quota, W);
     if (U > p.max_units || x0 >= x1) {  // uniform over the CTA, before any TMEM use
         // (too many units: overlapping offsets, which the split-key kernel reports)
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(512, 1)
             pt_request(p, s.r.b + 1, s.r);
         }
         const long long off = x - rline;
-        s.hk = static_cast<int>(off / s.r.tiles);
+        s.hk = static_cast<int>(div_short(off, s.r.tiles));
         long long rest = off - s.hk * s.r.tiles;
         s.pair = 0;
         for (;;) {
@@ -710,7 +710,8 @@ __global__ void __launch_bounds__(512, 1)
                 p.pl[slot * kPagedTileRows + i * 128 + r] = l;
                 // pieces of a unit lie in consecutive CTAs; whoever finishes last
                 // merges them in order
-                const int f = static_cast<int>(s.line0 / quota), e = static_cast<int>((s.line0 + s.ntile - 1) / quota);
+                const int f = static_cast<int>(div_short(s.line0, quota));
+                const int e = static_cast<int>(div_short(s.line0 + s.ntile - 1, quota));
                 __threadfence();
                 named_sync(1 + i, 128);
                 if (r == 0) last_s[i] = atomicAdd(&p.counters[2 * s.unit + i], 1) == e - f;
