@@ -516,7 +516,7 @@ fa_status fa_cache_plan(const int32_t* new_len, const int32_t* cache_len, int32_
         return FA_ERR_INVALID_ARG;
     if (B <= 0 || max_blocks <= 0 || num_blocks <= 0 || block_size <= 0 || total < 0) return FA_ERR_INVALID_ARG;
     if (!paged_block_ok(block_size) || B > fa::kPlanMaxB || total > (1 << 30)) return FA_ERR_UNSUPPORTED;
-    if (static_cast<long long>(max_blocks) * block_size >= (1LL << 31) ||
+    if (static_cast<long long>(max_blocks) * block_size >= (1LL << 31) - 256 ||
         static_cast<long long>(num_blocks) * block_size >= (1LL << 31))
         return FA_ERR_UNSUPPORTED;
     if (!aligned(new_len, 4) || !aligned(cache_len, 4) || !aligned(cache_len_out, 4) || !aligned(block_table, 4) ||
@@ -627,7 +627,7 @@ fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
     if (!(scale > 0.f) || !isfinite(scale)) return FA_ERR_INVALID_ARG;
     if ((d != 64 && d != 128) || !paged_block_ok(block_size)) return FA_ERR_UNSUPPORTED;
     if (B > 65535 || Hq > 65535 || static_cast<long long>(total) * Hq >= (1LL << 31) ||
-        static_cast<long long>(max_blocks) * block_size >= (1LL << 31) ||
+        static_cast<long long>(max_blocks) * block_size >= (1LL << 31) - 256 ||
         static_cast<long long>(num_blocks) * Hkv * block_size >= (1LL << 31) ||
         static_cast<long long>(B) * Hkv >= (1LL << 30) ||
         fa::paged_max_tile_units(B, Hq, Hkv, total, max_new) >= (1LL << 29))

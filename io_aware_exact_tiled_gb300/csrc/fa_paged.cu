@@ -96,7 +96,8 @@ struct PagedParams {
     int B, Hq, Hkv, G, total, max_new, max_blocks, num_blocks, bs_log2;
     float scale_log2;
     int causal;
-    FastDiv by_g;  // division by G
+    int split_rows;  // requests of more rows are the row-tile kernel's
+    FastDiv by_g;    // division by G
     int *status, *counters;
     float *pm, *pl, *po;
 };
@@ -174,7 +175,7 @@ __device__ __forceinline__ void pg_request(const PagedParams& p, int b, PgSeg& s
     const int t0 = min(max(p.cu_seqlens[b], 0), p.total), t1 = min(max(p.cu_seqlens[b + 1], t0), p.total);
     s.tok0 = t0;
     s.n = min(t1 - t0, p.max_new);
-    if (static_cast<long long>(s.n) * p.G > kPagedMaxRows) s.n = 0;
+    if (static_cast<long long>(s.n) * p.G > p.split_rows) s.n = 0;
     s.len = min(max(p.cache_len[b], 0), p.max_blocks << p.bs_log2);
     s.nchunk = s.n > 0 ? max(1, (s.len + kPgChunk - 1) / kPgChunk) : 0;
 }
@@ -929,7 +930,7 @@ static cudaError_t launch_split(const PagedArgs& a, const PagedParams& p, cudaSt
 template <int D>
 static cudaError_t launch_split_d(const PagedArgs& a, const PagedParams& p, cudaStream_t stream) {
     const bool b16 = a.block_size == 16;
-    const long long rows = static_cast<long long>(a.max_new) * p.G;
+    const int rows = p.split_rows;
     if (rows <= 8) return b16 ? launch_split<D, 1, true>(a, p, stream) : launch_split<D, 1, false>(a, p, stream);
     if (rows <= 16) return b16 ? launch_split<D, 2, true>(a, p, stream) : launch_split<D, 2, false>(a, p, stream);
     if (rows <= 24) return b16 ? launch_split<D, 3, true>(a, p, stream) : launch_split<D, 3, false>(a, p, stream);
@@ -951,6 +952,7 @@ cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t stream, int* nlaun
     p.Hkv = a.Hkv;
     p.G = a.Hq / a.Hkv;
     p.by_g = make_fast_div(p.G);
+    p.split_rows = paged_split_rows(a.max_new, p.G);
     p.total = a.total;
     p.max_new = a.max_new;
     p.max_blocks = a.max_blocks;

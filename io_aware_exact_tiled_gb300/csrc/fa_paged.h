@@ -15,8 +15,8 @@ enum : int { FA_DEV_NO_BLOCKS = 5 };
 
 constexpr int kPlanMaxB = 16384;      // requests of one plan (offsets of all of them sit in shared memory)
 constexpr int kPagedCtas = 152;       // one persistent CTA per SM
-constexpr int kPagedMaxRows = 32;     // query rows (new tokens x heads of a group) up to which a request is the
-                                      // split-key kernel's; the row-tile kernel takes the others
+constexpr int kPagedMaxRows = 32;     // most query rows (new tokens x heads of a group) of a request that the
+                                      // split-key kernel takes; the row-tile kernel takes the others
 constexpr int kPagedTileRows = 256;   // query rows of a unit of the row-tile kernel
 
 struct PlanArgs {
@@ -62,6 +62,17 @@ struct PagedArgs {
     cudaEvent_t ev_begin, ev_end;  // optional, recorded around the attention kernels
 };
 
+// Query rows up to which a request is the split-key kernel's, the height of its
+// tile: what the longest request has, or, where that one is the row-tile
+// kernel's, what one new token has: a batch with a prompt in it is mostly
+// decoding otherwise, and a taller tile than their rows need slows those
+// requests down (64 requests of 8,000 tokens, 4 rows each: 137 us in a tile of
+// eight rows, 223 in one of 32 at d = 64; 173 and 492 at d = 128).
+inline int paged_split_rows(int max_new, int group) {
+    const long long rows = static_cast<long long>(max_new) * group;
+    const int r = rows <= kPagedMaxRows ? static_cast<int>(rows) : group <= kPagedMaxRows ? group : kPagedMaxRows;
+    return (r + 7) / 8 * 8;
+}
 // Whether a request of max_new new tokens goes to the row-tile kernel.
 inline bool paged_has_tiles(int max_new, int group) {
     return static_cast<long long>(max_new) * group > kPagedMaxRows;

@@ -43,7 +43,7 @@ constexpr float kPtLn2 = 0.69314718055994530942f;
 constexpr float kPtRescale = 8.0f;  // log2 units
 constexpr float kPtOffset = 6.0f;   // log2 of the factor on P before its rounding to f16
 constexpr float kPtSpan = 60.0f;    // log2 of the largest ratio of V's block scales that is kept apart
-constexpr int kPtUnitCost = 4;       // key tiles' time that a unit's Q, first S and output take
+constexpr int kPtUnitCost = 6;       // key tiles' time that a unit's Q, first S and output take
 constexpr int kPtScaleSlots = 8;
 constexpr int kPtNanSlots = 4;
 
@@ -61,12 +61,15 @@ struct PtCfg {
     static constexpr int R_OFF = K_OFF + KS * K_BYTES;
     static constexpr int V_OFF = R_OFF + RS * K_BYTES;
     static constexpr int SC_OFF = V_OFF + VS * V_BYTES;       // float [slots][24]: ks, log2 vs, 1 / vs of 8 groups
-    static constexpr int NAN_OFF = SC_OFF + kPtScaleSlots * 96;  // int [slots][D + 4]: first key with a NaN value
-    static constexpr int NAN_STRIDE = (D + 4) * 4;
-    static constexpr int BAR_OFF = NAN_OFF + kPtNanSlots * NAN_STRIDE;
+    static constexpr int NAN_OFF = SC_OFF + kPtScaleSlots * 96;  // u64 [slots][D]: {tag, first key with a NaN value}
+    static constexpr int BAR_OFF = NAN_OFF + kPtNanSlots * D * 8;
     static constexpr int USED = BAR_OFF + 512;
     static constexpr int SMEM = USED + 1024;
-    static constexpr int COL_S = 0, COL_O = 256;  // TMEM: S of tile i at 128 i, O at 256 + 128 i
+    // TMEM: S of row tile i and half h of the keys at 128 i + 64 h, O at 256 +
+    // 128 i. P of a half: d = 64 behind O, d = 128 (no room) over its S.
+    static constexpr int COL_S = 0, COL_O = 256;
+    static constexpr bool P_OVER_S = D == 128;
+    static constexpr int COL_P = P_OVER_S ? COL_S : COL_O + 64, P_STRIDE = P_OVER_S ? 64 : 32;
     static constexpr uint32_t ID_S = idesc_make(128, 64, kFmtE4M3, false, false);
     static constexpr uint32_t ID_PV = idesc_make(128, D, 0 /* f16 */, false, true);
     static_assert(SMEM <= 232448 - 2048, "shared memory");
@@ -81,7 +84,8 @@ struct PtParams {
     int B, Hq, Hkv, G, total, max_new, max_blocks, num_blocks, bs_log2;
     float scale_log2;
     int causal;
-    FastDiv by_g;  // division by G
+    int split_rows;  // requests of no more rows are the split-key kernel's
+    FastDiv by_g;    // division by G
     int *status, *counters;
     int max_units;
     float *pm, *pl, *po;
@@ -89,6 +93,19 @@ struct PtParams {
 
 __device__ __forceinline__ void named_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// The tag of piece `seg` in the list of NaN values: later pieces' are smaller,
+// and none is that of an entry nobody has written.
+__device__ __forceinline__ uint32_t pt_nan_tag(int seg) { return ~static_cast<uint32_t>(seg + 1); }
+// Whether `v` holds in all `threads` threads that meet at the barrier.
+__device__ __forceinline__ bool named_all(int id, int threads, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %3, 0;\n\tbar.red.and.pred p, %1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(v))
+        : "memory");
+    return r != 0;
 }
 __device__ __forceinline__ uint32_t pt_f16x2_from_e4m3x2(uint32_t x) {
     uint32_t r;
@@ -164,7 +181,7 @@ __device__ __forceinline__ void pt_request(const PtParams& p, int b, PtReq& r) {
     r.b = b;
     r.tok0 = t0;
     r.n = min(t1 - t0, p.max_new);
-    if (static_cast<long long>(r.n) * p.G <= kPagedMaxRows) r.n = 0;  // the split-key kernel's
+    if (static_cast<long long>(r.n) * p.G <= p.split_rows) r.n = 0;
     r.len = min(max(p.cache_len[b], 0), p.max_blocks << p.bs_log2);
     r.npair = static_cast<int>((static_cast<long long>(r.n) * p.G + 255) >> 8);
     r.tiles = 0;
@@ -180,7 +197,7 @@ __global__ void __launch_bounds__(512, 1)
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ long long scan_w[16], scan_u[16];
     __shared__ long long start_line;
-    __shared__ int start_b, start_units, abort_s, last_s[2];
+    __shared__ int start_b, start_units, abort_s, last_s[2], nan_piece[kPtNanSlots];
     __shared__ uint32_t tmem_slot;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -248,8 +265,14 @@ __global__ void __launch_bounds__(512, 1)
         }
         fence_barrier_init();
     }
-    int* nan_first = reinterpret_cast<int*>(sm + C::NAN_OFF);  // [slot][D], then a flag
-    for (int i = tid; i < kPtNanSlots * (D + 4); i += 512) nan_first[i] = i % (D + 4) == D ? 0 : INT_MAX;
+    // NaN values that only some rows see: for each column the piece's tag
+    // (a later piece's entry replaces an earlier one's) and the first key;
+    // and the piece that noted one last. A piece's slot is used again four
+    // pieces on: by then both row tiles have read it, as the conversion of V is
+    // at most two tiles ahead of the products.
+    unsigned long long* nan_first = reinterpret_cast<unsigned long long*>(sm + C::NAN_OFF);
+    for (int i = tid; i < kPtNanSlots * D; i += 512) nan_first[i] = ~0ull;
+    if (tid < kPtNanSlots) nan_piece[tid] = -1;
     __syncthreads();
     long long W = 0, U = 0, bw = 0, bu = 0;
     for (int w = 0; w < 16; ++w) {
@@ -447,17 +470,22 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t tS = tm0 + C::COL_S + h * 64, tO = tm0 + C::COL_O;
+                        const uint32_t tP = tm0 + C::COL_P + h * C::P_STRIDE;
                         if (t > c0 && t <= end) {
                             if (!(ok = wait_warp(&p_full[2 * i + h], np & 1))) break;
                             tc_fence_after();
                             const uint32_t more = !(t - 1 == c0 && h == 0);
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                umma_ts<false>(leader, tO, tS + kk * 8, sdesc_advance(vd, h * 8192 + kk * 2048),
+                                umma_ts<false>(leader, tO, tP + kk * 8, sdesc_advance(vd, h * 8192 + kk * 2048),
                                                C::ID_PV, kk > 0 ? 1u : more);
                             umma_commit(leader, &pv_done[2 * i + h]);
                         }
                         if (t < end) {
+                            // Only products with the same accumulator are bound to
+                            // the order of their issue: where S takes P's place,
+                            // P V has to be done.
+                            if (C::P_OVER_S && t > c0 && !(ok = wait_warp(&pv_done[2 * i + h], np & 1))) break;
                             tc_fence_after();
 #pragma unroll
                             for (int part = 0; part < 2; ++part)
@@ -490,7 +518,7 @@ __global__ void __launch_bounds__(512, 1)
         regs_inc<152>();
         const int i = (warp - 4) >> 2, wq = warp & 3, r = wq * 32 + lane;
         const uint32_t tl = tm + (static_cast<uint32_t>(wq * 32) << 16);
-        const uint32_t tS = tl + C::COL_S + i * 128, tO = tl + C::COL_O + i * 128;
+        const uint32_t tS = tl + C::COL_S + i * 128, tO = tl + C::COL_O + i * 128, tP = tl + C::COL_P + i * 128;
         uint8_t* qb = sm + C::Q_OFF + i * C::Q_BYTES;
         int u = 0, ns = 0, seg = 0;  // tiles walked, halves of them multiplied, pieces
         bool ok = true;
@@ -625,7 +653,7 @@ __global__ void __launch_bounds__(512, 1)
                     f2_split(sum, a, b);
                     l = fmaf(a + b, il[gr], l);
                 }
-                tmem_st32(tSh, pk);
+                tmem_st32(tP + h * C::P_STRIDE, pk);
                 if (__any_sync(0xffffffffu, resc) && th > 2 * s.c0) {
                     // O of the halves so far is final once the last one's P V
                     // is (the ones before it were issued ahead of this S; the
@@ -644,20 +672,19 @@ __global__ void __launch_bounds__(512, 1)
                 }
                 tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(&p_full[2 * i + h]);
+                if (!FA_DROP_THIS_ARRIVE(ns == 0)) mbar_arrive(&p_full[2 * i + h]);
                 ++ns;
             }
-            if (!ok) break;
             u += s.c1 - s.c0;
             // ---------------------------------------------------- the piece's rows
-            if (end > s.c0) {
-                ok = wait_warp(&pv_done[2 * i + 1], ((ns - 1) >> 1) & 1);
-            }
-            ok = ok && wait_warp(&nan_full[seg % kPtNanSlots], (seg / kPtNanSlots) & 1);
-            if (!ok) break;
+            if (ok && end > s.c0) ok = wait_warp(&pv_done[2 * i + 1], ((ns - 1) >> 1) & 1);
+            if (ok) ok = wait_warp(&nan_full[seg % kPtNanSlots], (seg / kPtNanSlots) & 1);
+            // the row tile's warps leave together, so that none waits for the others below
+            if (!(ok = named_all(1 + i, 128, ok))) break;
             tc_fence_after();
-            int* nf = nan_first + (seg % kPtNanSlots) * (D + 4);
-            const bool nan_seen = nf[D] != 0;
+            const unsigned long long* nf = nan_first + (seg % kPtNanSlots) * D;
+            const uint32_t nan_tag = pt_nan_tag(seg);
+            const bool nan_seen = nan_piece[seg % kPtNanSlots] == seg;
             ++seg;
             const bool whole = s.c0 == 0 && s.c1 == s.ntile;
             const int slot = 2 * static_cast<int>(blockIdx.x) + (s.line0 <= x0 ? 0 : 1);
@@ -677,7 +704,9 @@ __global__ void __launch_bounds__(512, 1)
                 if (nan_seen) {
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
-                        if (nf[c * 32 + k] < limit) ov[k] = __float_as_uint(CUDART_NAN_F);
+                        if (static_cast<uint32_t>(nf[c * 32 + k] >> 32) == nan_tag &&
+                            static_cast<int>(nf[c * 32 + k] & 0xFFFFFFFFu) < limit)
+                            ov[k] = __float_as_uint(CUDART_NAN_F);
                 }
                 if (whole) {
                     if (row_ok) {
@@ -762,12 +791,6 @@ __global__ void __launch_bounds__(512, 1)
                             L == 0.f ? -CUDART_INF_F : (M - lse_off + log2f(L)) * kPtLn2;
                 }
             }
-            if (nan_seen) {
-                // both row tiles have looked at the list: clean it for a later piece
-                named_sync(3, 256);
-                if (i == 0 && r < D) nf[r] = INT_MAX;
-                if (i == 0 && r == 0) nf[D] = 0;
-            }
         } while (next(s));
         if (!ok) pt_gave_up(&abort_s, p.status, 97);
     } else {
@@ -780,7 +803,7 @@ __global__ void __launch_bounds__(512, 1)
             const int rows = s.r.n * p.G;
             const int vis_min = pt_visible(p, s.r, p.by_g.div(s.pair * 256));
             const int vis_max = pt_visible(p, s.r, p.by_g.div(min(s.pair * 256 + 255, rows - 1)));
-            int* nf = nan_first + (seg % kPtNanSlots) * (D + 4);
+            unsigned long long* nf = nan_first + (seg % kPtNanSlots) * D;
             for (int t = s.c0; t < s.c1; ++t, ++u) {
                 const int vs = u % C::VS, rs = u % C::RS;
                 ok = wait_warp(&r_full[rs], (u / C::RS) & 1);
@@ -792,7 +815,6 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j)
                     x[j] = lds128_u4(rb + ((D == 128 ? j ^ (r & 7) : j ^ ((r >> 1) & 3)) << 4));
-                mbar_arrive(&r_empty[rs]);
                 ok = wait_warp(&v_empty[vs], ((u / C::VS) & 1) ^ 1);
                 if (!ok) break;
                 if (t * 128 + 128 > vis_min) {
@@ -808,11 +830,13 @@ __global__ void __launch_bounds__(512, 1)
                             if (key >= vis_max) w[y] = 0u;
                             const uint32_t nb = ((w[y] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
                             if (nb) {
-                                nf[D] = 1;
+                                nan_piece[seg % kPtNanSlots] = seg;
 #pragma unroll
                                 for (int z = 0; z < 4; ++z)
                                     if ((nb >> (8 * z)) & 0x80u) {
-                                        atomicMin(&nf[j * 16 + y * 4 + z], key);
+                                        atomicMin(&nf[j * 16 + y * 4 + z],
+                                                  (static_cast<unsigned long long>(pt_nan_tag(seg)) << 32) |
+                                                      static_cast<uint32_t>(key));
                                         w[y] &= ~(0xFFu << (8 * z));
                                     }
                             }
@@ -836,6 +860,12 @@ __global__ void __launch_bounds__(512, 1)
                     sts128(smem_u32(reg + ((c ^ (r & 7)) << 4)), h[0], h[1], h[2], h[3]);
                     sts128(smem_u32(reg + (((c + 1) ^ (r & 7)) << 4)), h[4], h[5], h[6], h[7]);
                 }
+                // Only here, with every loaded value used, may the copy of a later
+                // tile take the row's place: the arrival does not wait for loads
+                // whose values are still on their way (released right behind the
+                // loads, the row was overwritten under them about once in 10^4
+                // tiles).
+                mbar_arrive(&r_empty[rs]);
                 fence_proxy_async_smem();
                 mbar_arrive(&v_full[vs]);
             }
@@ -899,6 +929,7 @@ cudaError_t launch_paged_tile(const PagedArgs& a, cudaStream_t stream) {
     p.Hkv = a.Hkv;
     p.G = a.Hq / a.Hkv;
     p.by_g = make_fast_div(p.G);
+    p.split_rows = paged_split_rows(a.max_new, p.G);
     p.total = a.total;
     p.max_new = a.max_new;
     p.max_blocks = a.max_blocks;

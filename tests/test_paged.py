@@ -259,13 +259,14 @@ def check(o, lse, ref, cu, G, rows, visible, d):
     """Bounds. Scores: d products and sums in fp32 (d 2^-24 of sum |q k|), the
     two scale factors and the exponent's argument (4 roundings of 2^-24), Q's
     f16 parts (2^-25 of the row's largest): together below (d + 16) 2^-24 X.
-    Requests of more than 32 rows (new tokens x heads of a group) take Q as two
-    E4M3 parts: 2^-17 of the row's largest, hence 2^-17 Y more. Weights: f16 (2^-11), exp2 (2^-22) and twice the score error; weights below
+    Requests of more than 32 rows (new tokens x heads of a group; beside one of
+    those, of more rows than a token has) take Q as two E4M3 parts: 2^-17 of the row's largest, hence 2^-17 Y more. Weights: f16 (2^-11), exp2 (2^-22) and twice the score error; weights below
     2^-31 of the largest vanish. O: that on A = sum P |v|, fp32 sums (2^-20 A),
     and bf16 (2^-8 |O|)."""
     O, L, A, X, Y = ref
-    n = np.repeat(np.diff(cu), np.diff(cu))[rows]
-    ds = (d + 16) * 2.0 ** -24 * X[:, rows] + np.where(n * G > 32, 2.0 ** -17, 0.0) * Y[:, rows]
+    n, most = np.repeat(np.diff(cu), np.diff(cu))[rows], int(np.diff(cu).max()) * G
+    split = 8 * -(-(most if most <= 32 else min(G, 32)) // 8)   # rows up to which Q is f16
+    ds = (d + 16) * 2.0 ** -24 * X[:, rows] + np.where(n * G > split, 2.0 ** -17, 0.0) * Y[:, rows]
     L, lse = L[:, rows], lse[:, rows]
     empty = np.isneginf(L)
     assert np.array_equal(empty, np.isneginf(lse))
@@ -369,6 +370,48 @@ def test_attend_many_rows(cuda_device, d, bs, Hkv, G, pairs):
         ref = P.attend(q.double().cpu().numpy(), *c[:4], cu, lens, c[4], scale, causal)
         check(o, lse, ref, cu, G, slice(0, total), max(lens), d)
         assert (o[total:] == 7).all() and (lse[:, total:] == 7).all()
+
+
+@pytest.mark.parametrize("d,Hkv,G,pairs", [
+    (64, 16, 1, [(0, 1871), (0, 685), (0, 448), (0, 1255), (0, 314), (0, 1967), (0, 1054), (0, 1142)]),
+    (128, 8, 4, [(3000, 700), (0, 900), (515, 333)])])
+def test_attend_prompts_again_and_again(cuda_device, d, Hkv, G, pairs):
+    """Many row tiles in every CTA, twenty times: the same bits each time, and
+    within the sum of the bounds (here 2^-7 of a row's largest value, bf16's
+    2^-8 and as much for P and the scores) of a float64 computation."""
+    lens = [c + n for c, n in pairs]
+    cu = np.concatenate([[0], np.cumsum([n for _, n in pairs])])
+    total, bs, scale = int(cu[-1]), 64, 1 / math.sqrt(d)
+    gen = torch.Generator(device=cuda_device).manual_seed(3)
+    used = [-(-x // bs) for x in lens]
+    perm = torch.randperm(sum(used), generator=gen, device=cuda_device).to(torch.int32)
+    table = torch.full((len(lens), max(used)), -1, dtype=torch.int32, device=cuda_device)
+    at = 0
+    for b, u in enumerate(used):
+        table[b, :u] = perm[at:at + u]
+        at += u
+    kc, vc = ((torch.randn((at, Hkv, bs, d), generator=gen, device=cuda_device) * 60).to(torch.float8_e4m3fn)
+              for _ in range(2))
+    ks, vs = (torch.ldexp(torch.ones((at, Hkv), device=cuda_device),
+                          torch.randint(-7, -4, (at, Hkv), generator=gen, device=cuda_device)) for _ in range(2))
+    q = torch.randn((total, Hkv * G, d), generator=gen, device=cuda_device).to(torch.bfloat16)
+    args = (q, kc, vc, ks, vs, dev_i32(cu, cuda_device), dev_i32(lens, cuda_device), table,
+            max(n for _, n in pairs))
+    o, lse = fa.forward_paged(*args, scale=scale)
+    for _ in range(20):
+        again = fa.forward_paged(*args, scale=scale)
+        assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+    for b, (c, n) in enumerate(pairs):
+        t = table[b, :used[b]].long()
+        seen = torch.arange(lens[b], device=cuda_device) <= c + torch.arange(n, device=cuda_device)[:, None]
+        for h in range(Hkv):
+            k, v = ((x[t, h].double() * s[t, h].double()[:, None, None]).reshape(-1, d)[:lens[b]]
+                    for x, s in ((kc, ks), (vc, vs)))
+            for g in range(h * G, (h + 1) * G):
+                x = torch.where(seen, (q[cu[b]:cu[b + 1], g].double() @ k.T) * scale, -math.inf)
+                want = torch.softmax(x, -1) @ v
+                err = (o[cu[b]:cu[b + 1], g].double() - want).abs()
+                assert (err <= 2.0 ** -7 * v.abs().max(0).values).all(), (b, g)
 
 
 def test_attend_many_rows_over_a_long_cache(cuda_device):
