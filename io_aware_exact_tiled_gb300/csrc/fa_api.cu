@@ -591,7 +591,7 @@ struct PagedWs {
 static PagedWs paged_ws(int B, int Hq, int Hkv, int total, int max_new, int d) {
     PagedWs w;
     const size_t rows = 2 * static_cast<size_t>(fa::kPagedCtas) * fa::kPagedMaxRows;
-    const size_t units = static_cast<size_t>(fa::paged_max_tile_units(B, Hq, Hkv, total, max_new));
+    const size_t units = static_cast<size_t>(fa::paged_max_tile_units(B, Hq, Hkv, total, max_new, d));
     const size_t tile_rows = units ? 2 * static_cast<size_t>(fa::kPagedCtas) * fa::kPagedTileRows : 0;
     w.counters = kStatusBytes;
     w.tile_counters = w.counters + align256(static_cast<size_t>(B) * Hkv * sizeof(int));
@@ -630,7 +630,7 @@ fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
         static_cast<long long>(max_blocks) * block_size >= (1LL << 31) - 256 ||
         static_cast<long long>(num_blocks) * Hkv * block_size >= (1LL << 31) ||
         static_cast<long long>(B) * Hkv >= (1LL << 30) ||
-        fa::paged_max_tile_units(B, Hq, Hkv, total, max_new) >= (1LL << 29))
+        fa::paged_max_tile_units(B, Hq, Hkv, total, max_new, d) >= (1LL << 29))
         return FA_ERR_UNSUPPORTED;
     if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
         !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(cu_seqlens, 4) || !aligned(cache_len, 4) ||
@@ -667,7 +667,7 @@ fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
     a.pl = reinterpret_cast<float*>(ws + w.pl);
     a.po = reinterpret_cast<float*>(ws + w.po);
     a.tile_counters = reinterpret_cast<int*>(ws + w.tile_counters);
-    a.max_tile_units = static_cast<int>(fa::paged_max_tile_units(B, Hq, Hkv, total, max_new));
+    a.max_tile_units = static_cast<int>(fa::paged_max_tile_units(B, Hq, Hkv, total, max_new, d));
     a.tile_pm = reinterpret_cast<float*>(ws + w.tile_pm);
     a.tile_pl = reinterpret_cast<float*>(ws + w.tile_pl);
     a.tile_po = reinterpret_cast<float*>(ws + w.tile_po);

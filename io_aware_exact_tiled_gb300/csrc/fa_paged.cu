@@ -14,7 +14,7 @@
 //
 // Design:
 //   * Work is counted in chunks of 32 keys. A unit is (request, key head), with
-//     at most RT = 8, 16, 24 or 32 query rows (fa_paged_tile.cu takes requests of
+//     at most RT = 8, 16, 24 or (d = 64) 32 query rows (fa_paged_tile.cu takes requests of
 //     more). The chunks of the long units form one line (with room in front of
 //     each unit for what its start and end cost) that is cut into equal quotas,
 //     one for each persistent CTA, so ragged lengths balance by themselves and
@@ -55,13 +55,14 @@ constexpr float kPgLn2 = 0.69314718055994530942f;
 constexpr float kPgRescale = 8.0f;  // log2 units
 constexpr float kPgOffset = 6.0f;   // log2 of the factor on P before its rounding to f16
 constexpr int kPgChunk = 32;        // keys of a chunk
-constexpr int kPgWarps = 8;
 constexpr int kPgUnitCost = 24;     // chunks' time that a long unit's rows, barriers and merge take
 constexpr int kPgAhead = 3;         // chunks between the fetch of a block id and its use
 
 template <int D, int NT, bool B16>
 struct PgCfg {
     static constexpr int RT = 8 * NT;                     // query rows of a unit
+    static constexpr int W = 8;                           // warps
+    static constexpr int THREADS = 32 * W;
     static constexpr int STAGES = D == 64 ? (NT >= 3 ? 4 : 5) : (NT == 1 ? 3 : 2);
     static constexpr int TILE = kPgChunk * D;             // bytes of a chunk's K (or V)
     static constexpr int SUBS = B16 ? 2 : 1;              // boxes of a tile
@@ -71,19 +72,19 @@ struct PgCfg {
     static constexpr int RED_F = 4 * NT * 32;             // floats of one m tile of a warp's O^T
     static constexpr int RED_M = 4;                       // m tiles merged at a time
     static constexpr int RING_OFF = 0;
-    static constexpr int RING = kPgWarps * STAGES * 2 * TILE;
-    static constexpr int RED_OFF = RING_OFF + RING;       // fp32 [8 warps][RED_M][RED_F] or f16 Q of each warp's unit
+    static constexpr int RING = W * STAGES * 2 * TILE;
+    static constexpr int RED_OFF = RING_OFF + RING;       // fp32 [W][RED_M][RED_F] or f16 Q of each warp's unit
     static constexpr int Q_BYTES = RT * D * 2;            // f16 fragments of Q
-    static constexpr int Q_OFF = RED_OFF + kPgWarps * RED_M * RED_F * 4;  // of a long unit
-    static constexpr int ML_OFF = Q_OFF + Q_BYTES;        // fp32 [8 warps + 1][RT][2]
-    static constexpr int ROW_OFF = ML_OFF + (kPgWarps + 1) * RT * 8;  // [8] {score factor, visible keys} of each row
-    static constexpr int META_OFF = ROW_OFF + kPgWarps * RT * 8;  // float4 [8][STAGES]: ks0, ks1, vs0, vs1
-    static constexpr int NAN_OFF = META_OFF + kPgWarps * STAGES * 16;  // int [8][D] first key with a NaN value
-    static constexpr int ID_OFF = NAN_OFF + kPgWarps * D * 4;  // int [8][4][2] block ids on their way
-    static constexpr int BAR_OFF = ID_OFF + kPgWarps * 32;
-    static constexpr int USED = BAR_OFF + kPgWarps * STAGES * 8;
+    static constexpr int Q_OFF = RED_OFF + W * RED_M * RED_F * 4;  // of a long unit
+    static constexpr int ML_OFF = Q_OFF + Q_BYTES;        // fp32 [W + 1][RT][2]
+    static constexpr int ROW_OFF = ML_OFF + (W + 1) * RT * 8;  // [W] {score factor, visible keys} of each row
+    static constexpr int META_OFF = ROW_OFF + W * RT * 8;  // float4 [W][STAGES]: ks0, ks1, vs0, vs1
+    static constexpr int NAN_OFF = META_OFF + W * STAGES * 16;  // int [W][D] first key with a NaN value
+    static constexpr int ID_OFF = NAN_OFF + W * D * 4;  // int [W][4][2] block ids on their way
+    static constexpr int BAR_OFF = ID_OFF + W * 32;
+    static constexpr int USED = BAR_OFF + W * STAGES * 8;
     static constexpr int SMEM = USED + 1024;
-    static_assert(kPgWarps * RED_M * RED_F * 4 >= kPgWarps * Q_BYTES, "Q of the warps' units");
+    static_assert(W * RED_M * RED_F * 4 >= W * Q_BYTES, "Q of the warps' units");
     static_assert(SMEM <= 232448 - 4096, "shared memory");
 };
 
@@ -181,22 +182,22 @@ __device__ __forceinline__ void pg_request(const PagedParams& p, int b, PgSeg& s
 }
 
 template <int D, int NT, bool B16>
-__global__ void __launch_bounds__(256, 1)
+__global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
     fa_paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                           const __grid_constant__ PagedParams p) {
     using C = PgCfg<D, NT, B16>;
     constexpr int RT = C::RT;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    __shared__ long long scan_w[3][kPgWarps];
-    __shared__ long long short_base[257];  // chunks of short units in front of each thread's requests
+    __shared__ long long scan_w[3][C::W];
+    __shared__ long long short_base[C::THREADS + 1];  // chunks of short units in front of each thread's requests
     __shared__ int start_b, last_s;
     __shared__ long long start_line;
     __shared__ int nan_seen, abort_s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
 
     // ---- all chunks, then the lines of long and of short units
-    const int per = (p.B + 255) / 256;
+    const int per = (p.B + C::THREADS - 1) / C::THREADS;
     const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
     long long mw = 0;
     bool bad = false;
@@ -216,19 +217,19 @@ __global__ void __launch_bounds__(256, 1)
     if (lane < C::STAGES) mbar_init(&bars[lane], 1);
     fence_barrier_init();
     int* first_nan = reinterpret_cast<int*>(sm + C::NAN_OFF);
-    for (int i = tid; i < kPgWarps * D; i += 256) first_nan[i] = INT_MAX;
+    for (int i = tid; i < C::W * D; i += C::THREADS) first_nan[i] = INT_MAX;
     long long sum = mw;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     if (lane == 0) scan_w[0][warp] = sum;
     __syncthreads();
     long long W = 0;
-    for (int w = 0; w < kPgWarps; ++w) W += scan_w[0][w];
+    for (int w = 0; w < C::W; ++w) W += scan_w[0][w];
     // A unit of up to a sixth of a warp's even share of all chunks is short,
     // and one of up to twelve chunks always: a long unit costs its CTA some
     // microseconds of barriers and merging, a short one keeps one warp busy for
     // about 1.3 us a chunk while other warps may have nothing left.
-    const long long share = W / (kPagedCtas * kPgWarps);
+    const long long share = W / (kPagedCtas * C::W);
     int T = static_cast<int>(min(max(share / 6, 12ll), 1ll << 30));
     auto line_long = [&](const PgSeg& s) {
         return s.nchunk > T ? static_cast<long long>(p.Hkv) * (s.nchunk + kPgUnitCost) : 0ll;
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(256, 1)
     __syncthreads();
     long long Wl = 0, Ws = 0, Wa = 0, bw = il - ml_, bs = is_ - ms, ba = ia - ma;
 #pragma unroll
-    for (int w = 0; w < kPgWarps; ++w) {
+    for (int w = 0; w < C::W; ++w) {
         if (w < warp) {
             bw += scan_w[0][w];
             bs += scan_w[1][w];
@@ -283,14 +284,14 @@ __global__ void __launch_bounds__(256, 1)
         bs = 0;
     }
     // equal quotas of the long line, at least one chunk for each warp
-    const long long quota = max((Wl + kPagedCtas - 1) / kPagedCtas, static_cast<long long>(kPgWarps));
+    const long long quota = max((Wl + kPagedCtas - 1) / kPagedCtas, static_cast<long long>(C::W));
     const long long x0 = quota * blockIdx.x, x1 = min(x0 + quota, Wl);
     // the short units that start in this warp's part of their line; parts that
     // follow one another lie in different CTAs
-    const long long part = (Ws + kPagedCtas * kPgWarps - 1) / (kPagedCtas * kPgWarps);
+    const long long part = (Ws + kPagedCtas * C::W - 1) / (kPagedCtas * C::W);
     const long long y0 = part * (warp * kPagedCtas + static_cast<int>(blockIdx.x)), y1 = min(y0 + part, Ws);
     short_base[tid] = bs;
-    if (tid == 255) short_base[256] = Ws;
+    if (tid == C::THREADS - 1) short_base[C::THREADS] = Ws;
     if (x0 < x1 && x0 >= bw && x0 < bw + ml_) {
         for (int b = b0; b < b1; ++b) {
             PgSeg s;
@@ -341,7 +342,7 @@ __global__ void __launch_bounds__(256, 1)
         s.alone = true;
         // the thread whose requests hold position y0
         int lo = 0;
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < C::W; ++i) {
             const uint32_t in = __ballot_sync(0xffffffffu, short_base[i * 32 + lane] <= y0);
             if (in) lo = i * 32 + 31 - __clz(in);
         }
@@ -382,13 +383,13 @@ __global__ void __launch_bounds__(256, 1)
     const WaitCtx cx{reinterpret_cast<volatile int*>(&abort_s), p.status};
     uint8_t* ring = sm + C::RING_OFF + warp * C::STAGES * 2 * C::TILE;
     float4* meta = reinterpret_cast<float4*>(sm + C::META_OFF) + warp * C::STAGES;
-    // ---- requests of this warp: chunk c0 + warp + 8 k of a long piece, c0 + k
+    // ---- requests of this warp: chunk c0 + warp + W k of a long piece, c0 + k
     // of a short unit. A chunk's loads depend on one another (block id, then
     // the copies and the scales), so the ids come three chunks ahead of the
     // copies, and both they and the scales go to shared memory by asynchronous
     // copies. Step j commits one group: the ids of chunk j + 3 and the scales
     // of chunk j.
-    auto chunk_of = [&](const PgSeg& s, int k) { return s.alone ? s.c0 + k : s.c0 + warp + kPgWarps * k; };
+    auto chunk_of = [&](const PgSeg& s, int k) { return s.alone ? s.c0 + k : s.c0 + warp + C::W * k; };
     int* idq = reinterpret_cast<int*>(sm + C::ID_OFF) + warp * 8;  // [4][2] block ids
     int ik = 0, issued = 0, consumed = 0, fetched = 0;
     auto prefetch_q = [&](const PgSeg& s) {  // a unit's query rows, wanted soon
@@ -478,7 +479,7 @@ __global__ void __launch_bounds__(256, 1)
         // visible keys of the first and the last row
         auto visible = [&](int tok) { return p.causal ? min(max(cs.len - cs.n + tok + 1, 0), cs.len) : cs.len; };
         const int vis_min = visible(0), vis_max = visible(cs.n - 1);
-        const int r0 = cs.alone ? 0 : warp, rstep = cs.alone ? 1 : kPgWarps;
+        const int r0 = cs.alone ? 0 : warp, rstep = cs.alone ? 1 : C::W;
 #pragma unroll 4
         for (int r = r0; r < RT; r += rstep) {
             // four values per lane; the row's power of two goes to its score factor
@@ -640,74 +641,83 @@ __global__ void __launch_bounds__(256, 1)
                     }
             }
             // ---- O^T += vs V^T P^T
-            uint32_t vw[2][4][D / 32];
+            // (with many rows and d = 128, in two parts of the columns: the registers
+            // hold no more)
+            constexpr int VH = D == 128 && NT >= 3 ? 2 : 1, VW = D / 32 / VH;
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int j = ks * 16 + (r >> 1) * 8 + pg_key<D>(2 * t4 + (r & 1));
-                    if constexpr (D == 128) {
-                        const uint4 x = lds128_u4(vb + pg_off<D>(j, g));
-                        vw[ks][r][0] = x.x;
-                        vw[ks][r][1] = x.y;
-                        vw[ks][r][2] = x.z;
-                        vw[ks][r][3] = x.w;
-                    } else {
-                        const uint2 x = lds64(vb + pg_off<D>(j, g >> 1) + (g & 1) * 8);
-                        vw[ks][r][0] = x.x;
-                        vw[ks][r][1] = x.y;
-                    }
-                }
-            if (edge) {
-                // keys that no row sees count as zero whatever their bytes are;
-                // a NaN that only some rows see is taken out here and given
-                // back to those rows at the end
+            for (int vh = 0; vh < VH; ++vh) {
+                uint32_t vw[2][4][VW];
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const int key = key0 + ks * 16 + (r >> 1) * 8 + pg_key<D>(2 * t4 + (r & 1));
-#pragma unroll
-                        for (int w = 0; w < D / 32; ++w) {
-                            if (key >= vis_max) vw[ks][r][w] = 0u;
-                            const uint32_t nb = e4m3_nan_bits(vw[ks][r][w]);
-                            if (nb) {
-                                nan_bits = 1u;
-#pragma unroll
-                                for (int y = 0; y < 4; ++y)
-                                    if ((nb >> (8 * y)) & 0x80u) {
-                                        atomicMin(&nan_at[g * (D / 8) + w * 4 + y], key);
-                                        vw[ks][r][w] &= ~(0xFFu << (8 * y));
-                                    }
-                            }
+                        const int j = ks * 16 + (r >> 1) * 8 + pg_key<D>(2 * t4 + (r & 1));
+                        if constexpr (VW == 4) {
+                            const uint4 x = lds128_u4(vb + pg_off<D>(j, g));
+                            vw[ks][r][0] = x.x;
+                            vw[ks][r][1] = x.y;
+                            vw[ks][r][2] = x.z;
+                            vw[ks][r][3] = x.w;
+                        } else {
+                            const uint2 x = D == 128 ? lds64(vb + pg_off<D>(j, g) + vh * 8)
+                                                     : lds64(vb + pg_off<D>(j, g >> 1) + (g & 1) * 8);
+                            vw[ks][r][0] = x.x;
+                            vw[ks][r][1] = x.y;
                         }
                     }
-            }
+                if (edge) {
+                    // keys that no row sees count as zero whatever their bytes are;
+                    // a NaN that only some rows see is taken out here and given
+                    // back to those rows at the end
 #pragma unroll
-            for (int i = 0; i < C::MI; ++i) {
-                float acc[NT][4];
+                    for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                        for (int r = 0; r < 4; ++r) {
+                            const int key = key0 + ks * 16 + (r >> 1) * 8 + pg_key<D>(2 * t4 + (r & 1));
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
+                            for (int w = 0; w < VW; ++w) {
+                                if (key >= vis_max) vw[ks][r][w] = 0u;
+                                const uint32_t nb = e4m3_nan_bits(vw[ks][r][w]);
+                                if (nb) {
+                                    nan_bits = 1u;
 #pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {
-                    const uint32_t sel = i & 1 ? 0x7362u : 0x5140u;
-                    const uint32_t x = __byte_perm(vw[ks][0][i >> 1], vw[ks][1][i >> 1], sel);
-                    const uint32_t y = __byte_perm(vw[ks][2][i >> 1], vw[ks][3][i >> 1], sel);
-                    const uint32_t a0 = f16x2_from_e4m3x2(x), a1 = f16x2_from_e4m3x2(x >> 16);
-                    const uint32_t a2 = f16x2_from_e4m3x2(y), a3 = f16x2_from_e4m3x2(y >> 16);
+                                    for (int y = 0; y < 4; ++y)
+                                        if ((nb >> (8 * y)) & 0x80u) {
+                                            atomicMin(&nan_at[g * (D / 8) + (vh * VW + w) * 4 + y], key);
+                                            vw[ks][r][w] &= ~(0xFFu << (8 * y));
+                                        }
+                                }
+                            }
+                        }
+                }
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt], a0, a1, a2, a3, pb[ks][nt][0], pb[ks][nt][1]);
-                    if (B16 || ks == 1) {
-                        const float vs = ks ? mt4.w : mt4.z;
+                for (int k = 0; k < 2 * VW; ++k) {
+                    const int i = vh * 2 * VW + k;
+                    float acc[NT][4];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
+#pragma unroll
+                    for (int ks = 0; ks < 2; ++ks) {
+                        const uint32_t sel = k & 1 ? 0x7362u : 0x5140u;
+                        const uint32_t x = __byte_perm(vw[ks][0][k >> 1], vw[ks][1][k >> 1], sel);
+                        const uint32_t y = __byte_perm(vw[ks][2][k >> 1], vw[ks][3][k >> 1], sel);
+                        const uint32_t a0 = f16x2_from_e4m3x2(x), a1 = f16x2_from_e4m3x2(x >> 16);
+                        const uint32_t a2 = f16x2_from_e4m3x2(y), a3 = f16x2_from_e4m3x2(y >> 16);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
+                            mma_f16(acc[nt], a0, a1, a2, a3, pb[ks][nt][0], pb[ks][nt][1]);
+                        if (B16 || ks == 1) {
+                            const float vs = ks ? mt4.w : mt4.z;
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                o[i][nt][e] = fmaf(vs, acc[nt][e], o[i][nt][e]);
-                                if (B16) acc[nt][e] = 0.f;
-                            }
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    o[i][nt][e] = fmaf(vs, acc[nt][e], o[i][nt][e]);
+                                    if (B16) acc[nt][e] = 0.f;
+                                }
+                        }
                     }
                 }
             }
@@ -783,7 +793,7 @@ __global__ void __launch_bounds__(256, 1)
             for (int e = 0; e < 2; ++e) {
                 float M = -CUDART_INF_F;
 #pragma unroll
-                for (int w = 0; w < kPgWarps; ++w) M = fmaxf(M, ml[w * RT + nt * 8 + 2 * t4 + e].x);
+                for (int w = 0; w < C::W; ++w) M = fmaxf(M, ml[w * RT + nt * 8 + 2 * t4 + e].x);
                 fac[nt][e] = m[nt][e] == -CUDART_INF_F ? 0.f : ex2_approx(m[nt][e] - M);
             }
         const bool whole = cs.c0 == 0 && cs.c1 == cs.nchunk;
@@ -792,13 +802,13 @@ __global__ void __launch_bounds__(256, 1)
             // the row's maximum and sum over the warps
             float M = -CUDART_INF_F, L = 0.f;
 #pragma unroll
-            for (int w = 0; w < kPgWarps; ++w) M = fmaxf(M, ml[w * RT + tid].x);
+            for (int w = 0; w < C::W; ++w) M = fmaxf(M, ml[w * RT + tid].x);
 #pragma unroll
-            for (int w = 0; w < kPgWarps; ++w) {
+            for (int w = 0; w < C::W; ++w) {
                 const float2 v = ml[w * RT + tid];
                 L += v.y * (v.x == -CUDART_INF_F ? 0.f : ex2_approx(v.x - M));
             }
-            ml[kPgWarps * RT + tid] = make_float2(M, L == 0.f ? 0.f : 1.f / L);
+            ml[C::W * RT + tid] = make_float2(M, L == 0.f ? 0.f : 1.f / L);
             if (!whole) {
                 p.pm[slot * kPagedMaxRows + tid] = M;
                 p.pl[slot * kPagedMaxRows + tid] = L;
@@ -821,10 +831,10 @@ __global__ void __launch_bounds__(256, 1)
                             o[i][nt][e] * fac[nt][e & 1];
             __syncthreads();
 #pragma unroll
-            for (int x = tid; x < C::RED_M * C::RED_F; x += 256) {
+            for (int x = tid; x < C::RED_M * C::RED_F; x += C::THREADS) {
                 float sum = 0.f;
 #pragma unroll
-                for (int w = 0; w < kPgWarps; ++w) sum += red[w * C::RED_M * C::RED_F + x];
+                for (int w = 0; w < C::W; ++w) sum += red[w * C::RED_M * C::RED_F + x];
                 const int ln = x & 31, q = x >> 5, e = q & 3, nt = (q >> 2) % NT, i = i0 + q / (4 * NT);
                 const int r = nt * 8 + 2 * (ln & 3) + (e & 1);
                 const int col = (ln >> 2) * (D / 8) + 2 * i + (e >> 1);
@@ -834,7 +844,7 @@ __global__ void __launch_bounds__(256, 1)
                 } else if (r < nrow) {
                     const int tok = p.by_g.div(r), hq = cs.hk * p.G + r - tok * p.G;
                     p.o[(static_cast<size_t>(cs.tok0 + tok) * p.Hq + hq) * D + col] =
-                        static_cast<uint16_t>(pack_bf16x2(sum * ml[kPgWarps * RT + r].y, 0.f) & 0xFFFFu);
+                        static_cast<uint16_t>(pack_bf16x2(sum * ml[C::W * RT + r].y, 0.f) & 0xFFFFu);
                 }
             }
             __syncthreads();
@@ -854,7 +864,7 @@ __global__ void __launch_bounds__(256, 1)
                 __threadfence();
                 auto piece = [&](int cta) { return 2 * cta + (cs.line0 <= quota * cta ? 0 : 1); };
                 // maxima and sums: a warp for each row, a lane for each piece
-                for (int r = warp; r < nrow; r += kPgWarps) {
+                for (int r = warp; r < nrow; r += C::W) {
                     float M = -CUDART_INF_F, L = 0.f;
                     for (int cta = f + lane; cta <= e; cta += 32)
                         M = fmaxf(M, __ldcg(&p.pm[piece(cta) * kPagedMaxRows + r]));
@@ -875,7 +885,7 @@ __global__ void __launch_bounds__(256, 1)
                 }
                 __syncthreads();
                 // outputs: a thread for four columns of a row
-                for (int x = tid; x < nrow * (D / 4); x += 256) {
+                for (int x = tid; x < nrow * (D / 4); x += C::THREADS) {
                     const int r = x / (D / 4), c4 = x - r * (D / 4);
                     const float M = ml[r].x;
                     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -923,7 +933,7 @@ static cudaError_t launch_split(const PagedArgs& a, const PagedParams& p, cudaSt
                                     C::SMEM);
     });
     if (e != cudaSuccess) return e;
-    fa_paged_split_kernel<D, NT, B16><<<kPagedCtas, 256, C::SMEM, stream>>>(tk, tv, p);
+    fa_paged_split_kernel<D, NT, B16><<<kPagedCtas, C::THREADS, C::SMEM, stream>>>(tk, tv, p);
     return cudaGetLastError();
 }
 
@@ -933,8 +943,9 @@ static cudaError_t launch_split_d(const PagedArgs& a, const PagedParams& p, cuda
     const int rows = p.split_rows;
     if (rows <= 8) return b16 ? launch_split<D, 1, true>(a, p, stream) : launch_split<D, 1, false>(a, p, stream);
     if (rows <= 16) return b16 ? launch_split<D, 2, true>(a, p, stream) : launch_split<D, 2, false>(a, p, stream);
-    if (rows <= 24) return b16 ? launch_split<D, 3, true>(a, p, stream) : launch_split<D, 3, false>(a, p, stream);
-    return b16 ? launch_split<D, 4, true>(a, p, stream) : launch_split<D, 4, false>(a, p, stream);
+    if constexpr (D == 64)
+        if (rows > 24) return b16 ? launch_split<D, 4, true>(a, p, stream) : launch_split<D, 4, false>(a, p, stream);
+    return b16 ? launch_split<D, 3, true>(a, p, stream) : launch_split<D, 3, false>(a, p, stream);
 }
 
 cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t stream, int* nlaunch) {
@@ -952,7 +963,7 @@ cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t stream, int* nlaun
     p.Hkv = a.Hkv;
     p.G = a.Hq / a.Hkv;
     p.by_g = make_fast_div(p.G);
-    p.split_rows = paged_split_rows(a.max_new, p.G);
+    p.split_rows = paged_split_rows(a.max_new, p.G, a.d);
     p.total = a.total;
     p.max_new = a.max_new;
     p.max_blocks = a.max_blocks;
@@ -969,7 +980,7 @@ cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t stream, int* nlaun
     if (a.ev_begin) cudaEventRecord(a.ev_begin, stream);
     cudaError_t e = a.d == 64 ? launch_split_d<64>(a, p, stream) : launch_split_d<128>(a, p, stream);
     *nlaunch = 1;
-    if (e == cudaSuccess && paged_has_tiles(a.max_new, p.G)) {
+    if (e == cudaSuccess && paged_has_tiles(a.max_new, p.G, a.d)) {
         e = launch_paged_tile(a, stream);
         *nlaunch = 2;
     }

@@ -15,8 +15,7 @@ enum : int { FA_DEV_NO_BLOCKS = 5 };
 
 constexpr int kPlanMaxB = 16384;      // requests of one plan (offsets of all of them sit in shared memory)
 constexpr int kPagedCtas = 152;       // one persistent CTA per SM
-constexpr int kPagedMaxRows = 32;     // most query rows (new tokens x heads of a group) of a request that the
-                                      // split-key kernel takes; the row-tile kernel takes the others
+constexpr int kPagedMaxRows = 32;     // tallest row tile of the split-key kernel
 constexpr int kPagedTileRows = 256;   // query rows of a unit of the row-tile kernel
 
 struct PlanArgs {
@@ -62,26 +61,30 @@ struct PagedArgs {
     cudaEvent_t ev_begin, ev_end;  // optional, recorded around the attention kernels
 };
 
-// Query rows up to which a request is the split-key kernel's, the height of its
-// tile: what the longest request has, or, where that one is the row-tile
-// kernel's, what one new token has: a batch with a prompt in it is mostly
+// Query rows (new tokens x heads of a group) up to which a request can be the
+// split-key kernel's. Above 24 rows of d = 128 its registers do not hold O (64
+// requests of 8,000 tokens: 479 us with 32 rows, 374 with 64 rows in the
+// row-tile kernel); at d = 64 they do (232 us and 290).
+inline int paged_max_rows(int d) { return d == 64 ? 32 : 24; }
+// Whether a request of max_new new tokens goes to the row-tile kernel.
+inline bool paged_has_tiles(int max_new, int group, int d) {
+    return static_cast<long long>(max_new) * group > paged_max_rows(d);
+}
+// Rows up to which a request of this call is the split-key kernel's, the height
+// of its tile: what the longest request has, or, where that one is the row-tile
+// kernel's, what one new token has. A batch with a prompt in it is mostly
 // decoding otherwise, and a taller tile than their rows need slows those
 // requests down (64 requests of 8,000 tokens, 4 rows each: 137 us in a tile of
-// eight rows, 223 in one of 32 at d = 64; 173 and 492 at d = 128).
-inline int paged_split_rows(int max_new, int group) {
-    const long long rows = static_cast<long long>(max_new) * group;
-    const int r = rows <= kPagedMaxRows ? static_cast<int>(rows) : group <= kPagedMaxRows ? group : kPagedMaxRows;
-    return (r + 7) / 8 * 8;
-}
-// Whether a request of max_new new tokens goes to the row-tile kernel.
-inline bool paged_has_tiles(int max_new, int group) {
-    return static_cast<long long>(max_new) * group > kPagedMaxRows;
+// eight rows, 223 in one of 32 at d = 64).
+inline int paged_split_rows(int max_new, int group, int d) {
+    const int rows = paged_has_tiles(max_new, group, d) ? group : max_new * group;
+    return ((rows < paged_max_rows(d) ? rows : paged_max_rows(d)) + 7) / 8 * 8;
 }
 // Units of the row-tile kernel that B requests of together `total` tokens can
 // have (none if no request can be that long).
-inline long long paged_max_tile_units(int B, int Hq, int Hkv, int total, int max_new) {
+inline long long paged_max_tile_units(int B, int Hq, int Hkv, int total, int max_new, int d) {
     const long long group = Hq / Hkv;
-    if (!paged_has_tiles(max_new, static_cast<int>(group))) return 0;
+    if (!paged_has_tiles(max_new, static_cast<int>(group), d)) return 0;
     return Hkv * (B + total * group / kPagedTileRows);
 }
 

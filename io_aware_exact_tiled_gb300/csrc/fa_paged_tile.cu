@@ -929,7 +929,7 @@ cudaError_t launch_paged_tile(const PagedArgs& a, cudaStream_t stream) {
     p.Hkv = a.Hkv;
     p.G = a.Hq / a.Hkv;
     p.by_g = make_fast_div(p.G);
-    p.split_rows = paged_split_rows(a.max_new, p.G);
+    p.split_rows = paged_split_rows(a.max_new, p.G, a.d);
     p.total = a.total;
     p.max_new = a.max_new;
     p.max_blocks = a.max_blocks;

@@ -12,8 +12,6 @@ bias 7, 3 fraction bits, no infinities, 0x7F and 0xFF are NaN, largest 448).
 
 from __future__ import annotations
 
-import math
-
 import numpy as np
 
 E4M3_MAX = 448.0
@@ -26,7 +24,7 @@ def _table():
         e, f = (b >> 3) & 15, b & 7
         x = f / 8 * 2.0 ** -6 if e == 0 else (1 + f / 8) * 2.0 ** (e - 7)
         if e == 15 and f == 7:
-            x = math.nan
+            x = np.nan
         t[b] = -x if b & 128 else x
     return t
 
@@ -93,7 +91,7 @@ def scale_exponent(amax):
     """e with 2^e the scale of a run whose largest finite magnitude is amax."""
     if amax == 0:
         return EXP_MIN
-    f, x = math.frexp(amax)                            # amax = f 2^x, 0.5 <= f < 1; 448 = 0.875 2^9
+    f, x = np.frexp(amax)                            # amax = f 2^x, 0.5 <= f < 1; 448 = 0.875 2^9
     return max(x - 9 + (1 if f > 0.875 else 0), EXP_MIN)
 
 
@@ -119,7 +117,7 @@ def append(x, cache, scale, slots):
             s = 2.0 ** scale_exponent(fin.max() if fin.size else 0.0)
             old = scale[blk, h] if first > 0 else 0.0
             if old > 0:
-                f, e = math.frexp(old)
+                f, e = np.frexp(old)
                 s = max(s, 2.0 ** (e - 1 if f == 0.5 else e))
             if first > 0 and s != old:
                 cache[blk, h, :first] = e4m3_encode(e4m3_decode(cache[blk, h, :first]) * (old / s))
@@ -161,7 +159,7 @@ def attend(q, k_bytes, v_bytes, k_scale, v_scale, cu_seqlens, cache_len, block_t
                     l = p.sum()
                     O[t0 + i, g] = p @ v[:seen] / l
                     A[t0 + i, g] = p @ np.abs(v[:seen]) / l
-                    L[g, t0 + i] = m + math.log(l) if l > 0 else math.nan
+                    L[g, t0 + i] = m + np.log(l) if l > 0 else np.nan
                     X[g, t0 + i] = (scale * (np.abs(k[:seen]) @ np.abs(q[t0 + i, g]))).max()
                     Y[g, t0 + i] = scale * np.abs(q[t0 + i, g]).max() * np.abs(k[:seen]).sum(1).max()
     return O, L, A, X, Y

@@ -265,7 +265,8 @@ def check(o, lse, ref, cu, G, rows, visible, d):
     and bf16 (2^-8 |O|)."""
     O, L, A, X, Y = ref
     n, most = np.repeat(np.diff(cu), np.diff(cu))[rows], int(np.diff(cu).max()) * G
-    split = 8 * -(-(most if most <= 32 else min(G, 32)) // 8)   # rows up to which Q is f16
+    cap = 32 if d == 64 else 24
+    split = 8 * -(-(most if most <= cap else min(G, cap)) // 8)   # rows up to which Q is f16
     ds = (d + 16) * 2.0 ** -24 * X[:, rows] + np.where(n * G > split, 2.0 ** -17, 0.0) * Y[:, rows]
     L, lse = L[:, rows], lse[:, rows]
     empty = np.isneginf(L)
