@@ -24,8 +24,8 @@
 //     every time). Short units (no longer than a warp's even share of all
 //     chunks) are not worth a CTA's barriers: each is one warp's, from its Q
 //     to its output.
-//   * Each of a CTA's eight warps streams its own chunks (of a long unit every
-//     eighth one) through its own ring of TMA boxes with its own mbarriers:
+//   * Each of a CTA's eight or sixteen warps streams its own chunks (of a long unit every
+//     eighth or sixteenth) through its own ring of TMA boxes with its own mbarriers:
 //     no barrier between warps before a long unit ends. Block ids are fetched
 //     three chunks ahead of the copies that need them.
 //   * S^T = K Q^T and O^T = V^T P^T as m16n8k16 products with f16 operands
@@ -55,15 +55,22 @@ constexpr float kPgLn2 = 0.69314718055994530942f;
 constexpr float kPgRescale = 8.0f;  // log2 units
 constexpr float kPgOffset = 6.0f;   // log2 of the factor on P before its rounding to f16
 constexpr int kPgChunk = 32;        // keys of a chunk
-constexpr int kPgUnitCost = 24;     // chunks' time that a long unit's rows, barriers and merge take
 constexpr int kPgAhead = 3;         // chunks between the fetch of a block id and its use
 
 template <int D, int NT, bool B16>
 struct PgCfg {
     static constexpr int RT = 8 * NT;                     // query rows of a unit
-    static constexpr int W = 8;                           // warps
+    // Warps: what hides a chunk's chain of loads, products, exponentials and
+    // shuffles is other warps, as many as the registers allow without spills (64
+    // requests of 8,000 tokens, d = 64: 8 rows 137 us with 8 warps, 118 with 12,
+    // 115 with 16; 16 rows 165 with 8, 212 with 16).
+    static constexpr int W = D == 64 && NT == 1 ? 16 : 8;
     static constexpr int THREADS = 32 * W;
-    static constexpr int STAGES = D == 64 ? (NT >= 3 ? 4 : 5) : (NT == 1 ? 3 : 2);
+    static constexpr int STAGES = D == 64 ? (NT >= 3 ? 4 : NT == 2 ? 5 : 2) : (NT == 1 ? 3 : 2);
+    // chunks' time that a long unit's rows, barriers and merge take (64 requests
+    // of 1 to 16,384 tokens: d = 128 307 us with 1, 196 with 24, 197 with 48; d = 64
+    // 226, 143, 127, and 131 with 72)
+    static constexpr int COST = D == 64 ? 48 : 24;
     static constexpr int TILE = kPgChunk * D;             // bytes of a chunk's K (or V)
     static constexpr int SUBS = B16 ? 2 : 1;              // boxes of a tile
     static constexpr int BOX = TILE / SUBS;
@@ -225,14 +232,16 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
     __syncthreads();
     long long W = 0;
     for (int w = 0; w < C::W; ++w) W += scan_w[0][w];
-    // A unit of up to a sixth of a warp's even share of all chunks is short,
-    // and one of up to twelve chunks always: a long unit costs its CTA some
-    // microseconds of barriers and merging, a short one keeps one warp busy for
-    // about 1.3 us a chunk while other warps may have nothing left.
+    // A unit of up to a third of a warp's even share of all chunks is short, and
+    // one of up to twelve chunks always: a long unit costs its CTA barriers and a
+    // merge, a short one keeps a single warp busy, at the end while others have
+    // nothing left. d = 128, one token, 8 heads of keys: 1,024 requests of 1 to
+    // 600 tokens 235 us (a sixth: 306; none short: 371), 256 requests of 1 to
+    // 2,000 tokens 158 us (half: 183; up to the whole share: 180).
     const long long share = W / (kPagedCtas * C::W);
-    int T = static_cast<int>(min(max(share / 6, 12ll), 1ll << 30));
+    int T = static_cast<int>(min(max(share / 3, 12ll), 1ll << 30));
     auto line_long = [&](const PgSeg& s) {
-        return s.nchunk > T ? static_cast<long long>(p.Hkv) * (s.nchunk + kPgUnitCost) : 0ll;
+        return s.nchunk > T ? static_cast<long long>(p.Hkv) * (s.nchunk + C::COST) : 0ll;
     };
     auto line_short = [&](const PgSeg& s) { return s.nchunk <= T ? static_cast<long long>(p.Hkv) * s.nchunk : 0ll; };
     long long ml_ = 0, ms = 0, ma = 0;  // long, short, all as long ones
@@ -241,7 +250,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
         pg_request(p, b, s);
         ml_ += line_long(s);
         ms += line_short(s);
-        if (s.nchunk > 0) ma += static_cast<long long>(p.Hkv) * (s.nchunk + kPgUnitCost);
+        if (s.nchunk > 0) ma += static_cast<long long>(p.Hkv) * (s.nchunk + C::COST);
     }
     long long il = ml_, is_ = ms, ia = ma;
 #pragma unroll
@@ -274,7 +283,8 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
         Wa += scan_w[2][w];
     }
     // A few short units among long ones would only come after everything else:
-    // they are taken as long ones.
+    // they are taken as long ones (64 requests of 1 to 16,384 tokens: 196 us, 209
+    // with a warp each for the short ones).
     if (Ws * 8 < W) {
         T = 0;
         Wl = Wa;
@@ -318,10 +328,10 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
             pg_request(p, s.b, s);
         }
         const long long r = x - s.rline;
-        s.hk = static_cast<int>(div_short(r, s.nchunk + kPgUnitCost));
-        const int rest = static_cast<int>(r - static_cast<long long>(s.hk) * (s.nchunk + kPgUnitCost));
-        s.line0 = x - rest + kPgUnitCost;
-        s.c0 = max(rest - kPgUnitCost, 0);
+        s.hk = static_cast<int>(div_short(r, s.nchunk + C::COST));
+        const int rest = static_cast<int>(r - static_cast<long long>(s.hk) * (s.nchunk + C::COST));
+        s.line0 = x - rest + C::COST;
+        s.c0 = max(rest - C::COST, 0);
         s.c1 = static_cast<int>(min(static_cast<long long>(s.nchunk), x1 - s.line0));
         return s.c1 > s.c0;  // not only the room in front of a unit
     };
