@@ -229,10 +229,9 @@ fa_status fa_cache_plan(const int32_t* new_len, const int32_t* cache_len, int32_
  *   k_scale, v_scale  in/out, device, float32 [num_blocks, H]
  *   slots             in,  device, int32 [total]; tokens whose slot is not in
  *                     [0, num_blocks * block_size) are skipped
- * The tokens of one block stand next to each other in ascending order, as
- * fa_cache_plan lists them (of a slot given twice in a row of tokens of one
- * block either write stays; what a block holds that appears in two places of
- * the list is undefined).
+ * The tokens of one block stand next to each other, their slots ascending, as
+ * fa_cache_plan lists them. A slot given twice, or a block that appears in two
+ * places of the list, leaves what that block holds undefined, other blocks not.
  * d in {64, 128}. Runs one kernel; no workspace.
  */
 fa_status fa_cache_append(const void* k, const void* v, void* k_cache, void* v_cache, float* k_scale, float* v_scale,

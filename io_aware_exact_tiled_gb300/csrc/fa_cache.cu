@@ -34,6 +34,9 @@ __device__ __forceinline__ uint32_t cluster_size() {
 // into its own shared memory, then takes its share of the tokens. The scan is
 // the only reader of cache_len and free_state, so after the cluster barrier
 // CTA 0 may write their new values, in place if the caller wants that.
+// Bound: latency. 16 requests of a token each take 4.6 us (a launch alone 2),
+// 4,096 requests with 117K tokens, a tenth of them released, 17 us: the scan 4,
+// the tokens 6, released blocks 3.
 constexpr int kPlanKeep = 4;
 
 struct PlanSum {
@@ -243,7 +246,7 @@ cudaError_t launch_cache_plan(const PlanArgs& a, cudaStream_t stream, int* nlaun
         return r;
     });
     if (e != cudaSuccess) return e;
-    // One CTA where latency is all there is (16 requests of a token each: 4.3 us),
+    // One CTA where latency is all there is (16 requests of a token each: 4.6 us),
     // a cluster of 16 where there are many requests or tokens (4096 requests,
     // 117K tokens: 22 us with eight CTAs, 17 with sixteen).
     const bool big = a.B > 1024 || a.total > 4096;
@@ -286,17 +289,30 @@ struct AppendRun {
     size_t stride;        // H * D
 };
 
-// Largest finite magnitude of eight bf16 values, as bf16 bits (ordered like
-// the values).
-__device__ __forceinline__ uint32_t append_amax(uint4 x, uint32_t top) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+// Largest finite magnitude of N x eight bf16 values, as bf16 bits (ordered like
+// the values): of both halves of the words at once, again without the infinities
+// and NaN if there were any.
+template <int N>
+__device__ __forceinline__ uint32_t append_amax(const uint4 (&x)[N], uint32_t top) {
+    uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
-        top = max(top, lo < 0x7F80u ? lo : 0u);
-        top = max(top, hi < 0x7F80u ? hi : 0u);
+    for (int i = 0; i < N; ++i)
+        m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu),
+                                 __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu)));
+    uint32_t t = max(m & 0xFFFFu, m >> 16);
+    if (t >= 0x7F80u) {
+        t = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t lo = w[k] & 0x7FFFu, hi = (w[k] >> 16) & 0x7FFFu;
+                t = max(t, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+            }
+        }
     }
-    return top;
+    return max(top, t);
 }
 __device__ __forceinline__ uint2 append_quantise(uint4 x, float inv) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -338,29 +354,33 @@ __device__ __forceinline__ void append_move(uint8_t* cache, int bytes, float f, 
     }
 }
 
+// As many CTAs of an SM as their rows in registers allow with few spills (d =
+// 128, prompts of 20,000 tokens, blocks of 64 / 128 / 256: 97 / 94 / 134 us with
+// five, four and two, 83 / 89 / 116 with eight, five and three).
 template <int D, int L>
-__global__ void __launch_bounds__(256) fa_cache_append_kernel(const __grid_constant__ AppendArgs p, int span) {
+__global__ void __launch_bounds__(256, L <= 4 ? 8 : L == 8 ? 5 : 3) fa_cache_append_kernel(const __grid_constant__ AppendArgs p, int span) {
     constexpr int LPR = D / 8;         // lanes per row, eight values (16 bytes) each
     constexpr int ROWS = 256 / LPR;    // rows of a CTA-wide load
-    __shared__ int blk_of[512];        // block of tokens t0 .. (-1: none)
+    __shared__ int slot_of[512];       // slot of tokens t0 .. (-1: none)
     __shared__ int leads[256], nlead;
     __shared__ uint32_t warp_top[8];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // the heads of a span follow one another: they share its rows' DRAM pages
     const int part = static_cast<int>(blockIdx.x / (2u * p.H)), hv = static_cast<int>(blockIdx.x - part * (2u * p.H));
-    const int h = hv >> 1, bs = p.block_size, nslots = p.num_blocks * bs;
+    const int h = hv >> 1, bs = p.block_size, nslots = p.num_blocks * bs, bs_log2 = 31 - __clz(bs);
     const bool is_v = hv & 1;
     const long long t0 = static_cast<long long>(part) * span;
-    auto block_at = [&](long long t) {
+    auto slot_at = [&](long long t) {
         if (t < 0 || t >= p.total) return -1;
         const int s = p.slots[t];
-        return s >= 0 && s < nslots ? s / bs : -1;
+        return s >= 0 && s < nslots ? s : -1;
     };
-    // blocks of the span's tokens and of those that its last run may reach
-    for (int i = tid; i < span + bs; i += 256) blk_of[i] = block_at(t0 + i);
+    auto blk_of = [&](int i) { return slot_of[i] >> bs_log2; };
+    // slots of the span's tokens and of those that its last run may reach
+    for (int i = tid; i < span + bs; i += 256) slot_of[i] = slot_at(t0 + i);
     if (tid == 0) nlead = 0;
     __syncthreads();
-    if (tid < span && blk_of[tid] >= 0 && blk_of[tid] != (tid ? blk_of[tid - 1] : block_at(t0 - 1)))
+    if (tid < span && slot_of[tid] >= 0 && blk_of(tid) != (tid ? blk_of(tid - 1) : slot_at(t0 - 1) >> bs_log2))
         leads[atomicAdd(&nlead, 1)] = tid;
     __syncthreads();
     const int n = nlead;
@@ -369,16 +389,16 @@ __global__ void __launch_bounds__(256) fa_cache_append_kernel(const __grid_const
     r.src = static_cast<const uint16_t*>(is_v ? p.v : p.k) + static_cast<size_t>(h) * D;
     r.stride = static_cast<size_t>(p.H) * D;
     auto open = [&](int lead) {  // returns the run's first row in its block
-        const size_t at = static_cast<size_t>(blk_of[lead]) * p.H + h;
+        const size_t at = static_cast<size_t>(blk_of(lead)) * p.H + h;
         r.cache = (is_v ? p.v_cache : p.k_cache) + at * bs * D;
         r.scale = (is_v ? p.v_scale : p.k_scale) + at;
-        return p.slots[t0 + lead] - blk_of[lead] * bs;
+        return slot_of[lead] & (bs - 1);
     };
-    auto run_end = [&](int lead) {  // first token behind the run, as far as blk_of reaches (block_size tokens)
-        const int blk = blk_of[lead];
+    auto run_end = [&](int lead) {  // first token behind the run, as far as slot_of reaches (block_size tokens)
+        const int blk = blk_of(lead);
         for (int e = lead + 1;; e += 32) {
             const int i = e + lane;
-            const uint32_t in = __ballot_sync(0xffffffffu, i < min(lead + bs, span + bs) && blk_of[i] == blk);
+            const uint32_t in = __ballot_sync(0xffffffffu, i < min(lead + bs, span + bs) && blk_of(i) == blk);
             if (in != 0xffffffffu) return e + __ffs(~in) - 1;
         }
     };
@@ -388,21 +408,15 @@ __global__ void __launch_bounds__(256) fa_cache_append_kernel(const __grid_const
         for (int k = 0; k < n; ++k) {
             const int lead = leads[k], end = run_end(lead), first = open(lead);
             uint4 x[L];
-            int at[L];
             uint32_t top = 0;
 #pragma unroll
             for (int i = 0; i < L; ++i) {
                 const int t = lead + i * ROWS + row;
                 x[i] = make_uint4(0u, 0u, 0u, 0u);
-                at[i] = -1;
-                if (t < end) {
-                    x[i] = *reinterpret_cast<const uint4*>(r.src + (t0 + t) * r.stride + col);
-                    at[i] = p.slots[t0 + t];
-                }
+                if (t < end) x[i] = *reinterpret_cast<const uint4*>(r.src + (t0 + t) * r.stride + col);
             }
             const float old = first > 0 ? append_old_scale(r.scale) : 0.f;
-#pragma unroll
-            for (int i = 0; i < L; ++i) top = append_amax(x[i], top);
+            top = append_amax(x, top);
             top = __reduce_max_sync(0xffffffffu, top);
             if (lane == 0) warp_top[warp] = top;
             __syncthreads();  // every thread has read the scale so far, too
@@ -411,14 +425,14 @@ __global__ void __launch_bounds__(256) fa_cache_append_kernel(const __grid_const
             const float s = append_scale(top, old), inv = 1.f / s;  // a power of two: exact
             if (first > 0 && s != old) append_move(r.cache, first * D, old / s, tid, 256);
             if (tid == 0) *r.scale = s;
-            const int base = blk_of[lead] * bs;
             // the run's own rows, after the moved ones of a slot that it writes again
             __syncthreads();
 #pragma unroll
-            for (int i = 0; i < L; ++i)
-                if (at[i] >= 0)
-                    *reinterpret_cast<uint2*>(r.cache + static_cast<size_t>(at[i] - base) * D + col) =
-                        append_quantise(x[i], inv);
+            for (int i = 0; i < L; ++i) {
+                const int t = lead + i * ROWS + row;
+                if (t < end)
+                    *reinterpret_cast<uint2*>(r.cache + (slot_of[t] & (bs - 1)) * D + col) = append_quantise(x[i], inv);
+            }
         }
         return;
     }
@@ -429,18 +443,18 @@ __global__ void __launch_bounds__(256) fa_cache_append_kernel(const __grid_const
         const int lead = leads[k], end = run_end(lead), first = open(lead);
         const float old = first > 0 ? append_old_scale(r.scale) : 0.f;
         uint32_t top = 0;
-        for (int t = lead + sub; t < end; t += RPW)
-            top = append_amax(*reinterpret_cast<const uint4*>(r.src + (t0 + t) * r.stride + col), top);
+        for (int t = lead + sub; t < end; t += RPW) {
+            const uint4 x[1] = {*reinterpret_cast<const uint4*>(r.src + (t0 + t) * r.stride + col)};
+            top = append_amax(x, top);
+        }
         top = __reduce_max_sync(0xffffffffu, top);
         const float s = append_scale(top, old), inv = 1.f / s;
         if (first > 0 && s != old) append_move(r.cache, first * D, old / s, lane, 32);
         __syncwarp();
         if (lane == 0) *r.scale = s;
-        const int base = blk_of[lead] * bs;
         for (int t = lead + sub; t < end; t += RPW) {
             const uint4 x = *reinterpret_cast<const uint4*>(r.src + (t0 + t) * r.stride + col);
-            *reinterpret_cast<uint2*>(r.cache + static_cast<size_t>(p.slots[t0 + t] - base) * D + col) =
-                append_quantise(x, inv);
+            *reinterpret_cast<uint2*>(r.cache + (slot_of[t] & (bs - 1)) * D + col) = append_quantise(x, inv);
         }
     }
 }
@@ -449,7 +463,8 @@ template <int D, int L>
 static void launch_append(const AppendArgs& a, cudaStream_t stream) {
     // Tokens of a CTA: a block's in a large batch (most likely prompts, a run or
     // two in each span), sixteen in a small one, so that the many runs of a
-    // decoding batch spread over the GPU.
+    // decoding batch spread over the GPU. Before other changes, prompts of 19,900
+    // tokens: 116 us, 203 with sixteen; 1,700 tokens: 6.7 and 7.8.
     const int span = a.total > 1024 ? min(a.block_size, 64) : 16;
     const unsigned grid = static_cast<unsigned>((a.total + span - 1) / span) * 2u * a.H;
     fa_cache_append_kernel<D, L><<<grid, 256, 0, stream>>>(a, span);

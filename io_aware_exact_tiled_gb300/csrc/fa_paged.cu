@@ -10,23 +10,29 @@
 // Bound: every cached byte is read once and serves the n * G query rows of
 // its head, so with few rows the time is the cache's bytes over HBM's rate.
 // What has to be kept off that path is the conversion of the bytes and the
-// wait for the block table in front of each copy.
+// wait for the block table in front of each copy. Measured, d = 128, one token
+// for each request, against a copy's 6,766 GB/s: 16 requests of 8,192 to 16,383
+// tokens, 32 key heads, 255 us = 6,560 GB/s of cache; 64 requests of 1 to 16,384
+// tokens, 8 key heads, 196 us = 5,860; one request of 262,001 tokens, 98 us =
+// 5,480. At d = 64, or with more rows, the issue slots bound it: 64 requests of
+// 8,000 tokens, 8 key heads, 8 / 16 / 24 / 32 rows: 115 / 165 / 191 / 232 us
+// (bytes alone: 77), d = 128 175 / 221 / 275 us (155).
 //
 // Design:
 //   * Work is counted in chunks of 32 keys. A unit is (request, key head), with
-//     at most RT = 8, 16, 24 or (d = 64) 32 query rows (fa_paged_tile.cu takes requests of
-//     more). The chunks of the long units form one line (with room in front of
+//     at most RT = 8, 16, 24 or (d = 64) 32 query rows (fa_paged_tile.cu takes
+//     requests of more). The chunks of the long units form one line (with room in front of
 //     each unit for what its start and end cost) that is cut into equal quotas,
 //     one for each persistent CTA, so ragged lengths balance by themselves and
 //     one long request spreads over the whole GPU. A unit that
 //     was cut leaves partial (m, l, O) in the workspace and the CTA that
 //     finishes last merges them, in the order of the CTAs (the same result
-//     every time). Short units (no longer than a warp's even share of all
+//     every time). Short units (up to a third of a warp's even share of all
 //     chunks) are not worth a CTA's barriers: each is one warp's, from its Q
 //     to its output.
-//   * Each of a CTA's eight or sixteen warps streams its own chunks (of a long unit every
-//     eighth or sixteenth) through its own ring of TMA boxes with its own mbarriers:
-//     no barrier between warps before a long unit ends. Block ids are fetched
+//   * Each of a CTA's eight or sixteen warps streams its own chunks (of a long
+//     unit every eighth or sixteenth) through its own ring of TMA boxes with its
+//     own mbarriers: no barrier between warps before a long unit ends. Block ids are fetched
 //     three chunks ahead of the copies that need them.
 //   * S^T = K Q^T and O^T = V^T P^T as m16n8k16 products with f16 operands
 //     and fp32 sums, keys respectively head columns along M, the query rows
@@ -68,9 +74,9 @@ struct PgCfg {
     static constexpr int THREADS = 32 * W;
     static constexpr int STAGES = D == 64 ? (NT >= 3 ? 4 : NT == 2 ? 5 : 2) : (NT == 1 ? 3 : 2);
     // chunks' time that a long unit's rows, barriers and merge take (64 requests
-    // of 1 to 16,384 tokens: d = 128 307 us with 1, 196 with 24, 197 with 48; d = 64
-    // 226, 143, 127, and 131 with 72)
-    static constexpr int COST = D == 64 ? 48 : 24;
+    // of 1 to 16,384 tokens: d = 128 307 us with 1, 195 with 32, 197 with 48; d = 64
+    // 226, 127 with 48, 131 with 72)
+    static constexpr int COST = D == 64 ? 48 : 32;
     static constexpr int TILE = kPgChunk * D;             // bytes of a chunk's K (or V)
     static constexpr int SUBS = B16 ? 2 : 1;              // boxes of a tile
     static constexpr int BOX = TILE / SUBS;

@@ -3,6 +3,11 @@
 //
 // Same computation as fa_paged.cu. With hundreds of rows for each cached key
 // the time is that of the two products, 4 n len d flops for each query head.
+// Measured against 1,871 TFLOP/s of bf16 products: d = 128, two requests of
+// about 2,000 new tokens behind 15,000 to 16,384, 32 query heads, 803 us = 1,320
+// TFLOP/s (the softmax warps share the issue slots with the products); d = 64,
+// eight prompts of 314 to 1,967 tokens, 16 heads, 93 us = 267 TFLOP/s (a unit's
+// start and end, and three times the products' time for the softmax).
 //
 // Work: a unit is (request, key head, pair of row tiles); a row is (new token,
 // query head of the group), token-major, so that a tile of 128 rows sees
@@ -24,8 +29,8 @@
 // S = Q K^T runs on E4M3 operands, two products instead of one of f16: each
 // row of Q, divided by a power of two, is the sum of two E4M3 numbers (four
 // bits each of bfloat16's eight; exact down to 2^-10 of the row's maximum,
-// within 2^-17 of it below). Two E4M3 products cost what one f16 product costs, and K needs no
-// conversion and half the shared memory.
+// within 2^-17 of it below). Two E4M3 products cost what one f16 product costs,
+// and K needs no conversion and half the shared memory.
 // O += P V runs on f16: V's numbers convert exactly, P keeps 11 bits.
 // Block scales: ks multiplies the exponent's slope and log2(vs) is added to
 // the exponent, so P holds 2^(s - mu) vs; mu follows the largest of these
