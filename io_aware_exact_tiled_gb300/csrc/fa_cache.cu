@@ -461,11 +461,14 @@ __global__ void __launch_bounds__(256, L <= 4 ? 8 : L == 8 ? 5 : 3) fa_cache_app
 
 template <int D, int L>
 static void launch_append(const AppendArgs& a, cudaStream_t stream) {
-    // Tokens of a CTA: a block's in a large batch (most likely prompts, a run or
-    // two in each span), sixteen in a small one, so that the many runs of a
-    // decoding batch spread over the GPU. Before other changes, prompts of 19,900
-    // tokens: 116 us, 203 with sixteen; 1,700 tokens: 6.7 and 7.8.
-    const int span = a.total > 1024 ? min(a.block_size, 64) : 16;
+    // Tokens of a CTA: sixteen in a small batch, so that the many runs of a
+    // decoding batch spread over the GPU (128 requests of a token 3.9 us; prompts
+    // of 19,900 tokens 203 us with sixteen, 116 with 64, before other changes), 64
+    // in a large one (64 in blocks of 16, 20,000 tokens of prompts, d = 128: 118
+    // us, 184 with one block), 128 where blocks are so small that each warp should
+    // have one (the same prompts: 104 us, d = 64 60 and 74; 2,048 requests of a
+    // token, d = 128: 16 us, 11 with 64).
+    const int span = a.total > 8192 && a.block_size * D <= 2048 ? 128 : a.total > 1024 ? 64 : 16;
     const unsigned grid = static_cast<unsigned>((a.total + span - 1) / span) * 2u * a.H;
     fa_cache_append_kernel<D, L><<<grid, 256, 0, stream>>>(a, span);
 }

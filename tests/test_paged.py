@@ -173,6 +173,31 @@ def test_append_equals_the_definition(cuda_device, d, bs, H, runs):
         same_bytes(gb, wb)
 
 
+@pytest.mark.parametrize("d,bs,total", [(64, 16, 1500), (64, 16, 8500), (64, 32, 8500), (64, 64, 2000), (128, 16, 8500),
+                                        (128, 32, 1100), (128, 128, 1300), (128, 256, 1500)])
+def test_append_large_batches(cuda_device, d, bs, total):
+    """Whole blocks, parts of blocks and single tokens in a batch that is taken
+    in larger spans, with padding between them; values over many magnitudes."""
+    rng = np.random.default_rng(total + d + bs)
+    runs, left = [], total
+    while left > 0:
+        n = min(left, int(rng.choice([1, 2, bs // 2, bs - 1, bs, bs, bs])))
+        runs.append((int(rng.integers(0, bs - n + 1)), n))
+        left -= n
+    nb = len(runs) + 1
+    slots = np.concatenate([blk * bs + r + np.arange(n) if i % 11 else np.full(n, -1)
+                            for i, (blk, (r, n)) in enumerate(zip(rng.permutation(nb), runs))])
+    kb, vb = (rng.integers(0, 127, (nb, 1, bs, d)).astype(np.uint8) for _ in range(2))
+    ks, vs = (2.0 ** rng.integers(-12, 3, (nb, 1)) for _ in range(2))
+    kt, vt = (bf16(rng.normal(size=(total, 1, d)) * 2.0 ** rng.integers(-9, 9, (total, 1, 1)), cuda_device)
+              for _ in range(2))
+    got = run_append(kt, vt, kb, vb, ks, vs, slots, cuda_device)
+    for x, b0, s0, gb, gs in ((kt, kb, ks, got[0], got[2]), (vt, vb, vs, got[1], got[3])):
+        wb, ws = P.append(x.double().cpu().numpy(), b0, s0, slots)
+        np.testing.assert_array_equal(gs, ws.astype(np.float32))
+        same_bytes(gb, wb)
+
+
 def test_append_special_values(cuda_device):
     """Zeros, subnormal and huge values, infinities and NaN; scales so far that
     are no powers of two, zero, or not finite; padding and slots out of range."""
