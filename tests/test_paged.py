@@ -284,7 +284,7 @@ def check(o, lse, ref, cu, G, rows, visible, d):
     """Bounds. Scores: d products and sums in fp32 (d 2^-24 of sum |q k|), the
     two scale factors and the exponent's argument (4 roundings of 2^-24), Q's
     f16 parts (2^-25 of the row's largest): together below (d + 16) 2^-24 X.
-    Requests of more than 32 rows (new tokens x heads of a group; beside one of
+    Requests of more than 32 rows (24 at d = 128; new tokens x heads of a group; beside one of
     those, of more rows than a token has) take Q as two E4M3 parts: 2^-17 of the row's largest, hence 2^-17 Y more. Weights: f16 (2^-11), exp2 (2^-22) and twice the score error; weights below
     2^-31 of the largest vanish. O: that on A = sum P |v|, fp32 sums (2^-20 A),
     and bf16 (2^-8 |O|)."""
@@ -352,6 +352,20 @@ def test_attend_peaked_and_flat_rows(cuda_device, d):
     o, lse = run_attend(q, c, cu, lens, 2, True, cuda_device, 0.1)
     ref = P.attend(q.double().cpu().numpy(), *c[:4], cu, lens, c[4], 0.1)
     check(o, lse, ref, cu, 2, slice(0, 4), 1500, d)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,G", [(2, 8), (17, 1), (3, 8), (1, 24), (1, 25), (5, 5), (4, 8), (1, 32), (3, 11), (1, 33)])
+def test_attend_rows_at_the_borders(cuda_device, d, n, G):
+    """Requests of just as many rows as a tile of either kernel takes, one more,
+    and fewer beside them."""
+    lens, cu = [n + 40, n + 900, 31, n, 500], np.concatenate([[0], np.cumsum([n, n, 1, n, 0])])
+    rng = np.random.default_rng(d + n + G)
+    c = make_cache(lens, 32, 2, d, seed=n + G)
+    q = bf16(rng.normal(size=(int(cu[-1]), 2 * G, d)), cuda_device)
+    o, lse = run_attend(q, c, cu, lens, n, True, cuda_device, 0.1)
+    ref = P.attend(q.double().cpu().numpy(), *c[:4], cu, lens, c[4], 0.1)
+    check(o, lse, ref, cu, G, slice(0, int(cu[-1])), max(lens), d)
 
 
 def test_attend_long_cache_of_one_request(cuda_device):
