@@ -48,7 +48,11 @@ constexpr float kPtLn2 = 0.69314718055994530942f;
 constexpr float kPtRescale = 8.0f;  // log2 units
 constexpr float kPtOffset = 6.0f;   // log2 of the factor on P before its rounding to f16
 constexpr float kPtSpan = 60.0f;    // log2 of the largest ratio of V's block scales that is kept apart
-constexpr int kPtUnitCost = 6;       // key tiles' time that a unit's Q, first S and output take
+// key tiles' time that a unit's Q, first S and output take (eight prompts of 256
+// to 1,999 tokens, 16 heads: d = 64 105 us with 1, 94 with 6, 99 with 12; d = 128
+// 177, 160 with 6, 155 with 8 and with 12)
+template <int D>
+constexpr int kPtUnitCost = D == 64 ? 6 : 8;
 constexpr int kPtScaleSlots = 8;
 constexpr int kPtNanSlots = 4;
 
@@ -181,6 +185,7 @@ __device__ __forceinline__ int pt_tiles(const PtParams& p, const PtReq& r, int p
     const int last = min(pair * 256 + 255, r.n * p.G - 1);
     return max(1, (pt_visible(p, r, p.by_g.div(last)) + 127) >> 7);
 }
+template <int D>
 __device__ __forceinline__ void pt_request(const PtParams& p, int b, PtReq& r) {
     const int t0 = min(max(p.cu_seqlens[b], 0), p.total), t1 = min(max(p.cu_seqlens[b + 1], t0), p.total);
     r.b = b;
@@ -190,7 +195,7 @@ __device__ __forceinline__ void pt_request(const PtParams& p, int b, PtReq& r) {
     r.len = min(max(p.cache_len[b], 0), p.max_blocks << p.bs_log2);
     r.npair = static_cast<int>((static_cast<long long>(r.n) * p.G + 255) >> 8);
     r.tiles = 0;
-    for (int i = 0; i < r.npair; ++i) r.tiles += pt_tiles(p, r, i) + kPtUnitCost;
+    for (int i = 0; i < r.npair; ++i) r.tiles += pt_tiles(p, r, i) + kPtUnitCost<D>;
 }
 
 template <int D>
@@ -212,7 +217,7 @@ __global__ void __launch_bounds__(512, 1)
     long long mw = 0, mu = 0;
     for (int b = b0; b < b1; ++b) {
         PtReq r;
-        pt_request(p, b, r);
+        pt_request<D>(p, b, r);
         mu += static_cast<long long>(r.npair) * p.Hkv;
         mw += r.tiles * p.Hkv;
     }
@@ -299,7 +304,7 @@ __global__ void __launch_bounds__(512, 1)
     if (x0 >= bw && x0 < bw + mw) {
         for (int b = b0; b < b1; ++b) {
             PtReq r;
-            pt_request(p, b, r);
+            pt_request<D>(p, b, r);
             if (x0 < bw + r.tiles * p.Hkv) {
                 start_b = b;
                 start_line = bw;
@@ -326,7 +331,7 @@ __global__ void __launch_bounds__(512, 1)
         while (x >= rline + s.r.tiles * p.Hkv) {
             rline += s.r.tiles * p.Hkv;
             runits += s.r.npair * p.Hkv;
-            pt_request(p, s.r.b + 1, s.r);
+            pt_request<D>(p, s.r.b + 1, s.r);
         }
         const long long off = x - rline;
         s.hk = static_cast<int>(div_short(off, s.r.tiles));
@@ -334,12 +339,12 @@ __global__ void __launch_bounds__(512, 1)
         s.pair = 0;
         for (;;) {
             s.ntile = pt_tiles(p, s.r, s.pair);
-            if (rest < s.ntile + kPtUnitCost) break;
-            rest -= s.ntile + kPtUnitCost;
+            if (rest < s.ntile + kPtUnitCost<D>) break;
+            rest -= s.ntile + kPtUnitCost<D>;
             ++s.pair;
         }
-        s.line0 = x - rest + kPtUnitCost;
-        s.c0 = max(static_cast<int>(rest) - kPtUnitCost, 0);
+        s.line0 = x - rest + kPtUnitCost<D>;
+        s.c0 = max(static_cast<int>(rest) - kPtUnitCost<D>, 0);
         s.c1 = static_cast<int>(min(static_cast<long long>(s.ntile), x1 - s.line0));
         s.unit = runits + s.hk * s.r.npair + s.pair;
     };
@@ -351,7 +356,7 @@ __global__ void __launch_bounds__(512, 1)
             ++s.unit;
             s.ntile = pt_tiles(p, s.r, s.pair);
             s.c0 = 0;
-            s.line0 = x + kPtUnitCost;
+            s.line0 = x + kPtUnitCost<D>;
             s.c1 = static_cast<int>(min(static_cast<long long>(s.ntile), x1 - s.line0));
         } else {
             find(s, x);
@@ -367,7 +372,7 @@ __global__ void __launch_bounds__(512, 1)
     };
     auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return pt_wait(bar, parity, &abort_s); };
     PtSeg s;
-    pt_request(p, start_b, s.r);
+    pt_request<D>(p, start_b, s.r);
     find(s, x0);
     const bool any = s.c1 > s.c0;  // uniform over the CTA: not only the cost in front of a tile
 
