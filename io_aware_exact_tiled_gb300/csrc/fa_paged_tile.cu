@@ -5,7 +5,8 @@
 // the time is that of the two products, 4 n len d flops for each query head.
 // Measured against 1,871 TFLOP/s of bf16 products: d = 128, two requests of
 // about 2,000 new tokens behind 15,000 to 16,384, 32 query heads, 803 us = 1,320
-// TFLOP/s (the softmax warps share the issue slots with the products); d = 64,
+// TFLOP/s (the chain of S, softmax and P V of two row tiles: the tensor pipe is
+// active 55 % of the time); d = 64,
 // eight prompts of 314 to 1,967 tokens, 16 heads, 95 us = 262 TFLOP/s (a unit's
 // start and end, and three times the products' time for the softmax).
 //
