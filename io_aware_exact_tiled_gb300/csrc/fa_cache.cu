@@ -358,7 +358,8 @@ __device__ __forceinline__ void append_move(uint8_t* cache, int bytes, float f, 
 // 128, prompts of 20,000 tokens, blocks of 64 / 128 / 256: 97 / 94 / 134 us with
 // five, four and two, 83 / 89 / 116 with eight, five and three).
 template <int D, int L>
-__global__ void __launch_bounds__(256, L <= 4 ? 8 : L == 8 ? 5 : 3) fa_cache_append_kernel(const __grid_constant__ AppendArgs p, int span) {
+__global__ void __launch_bounds__(256, L <= 4 ? 8 : L == 8 ? 5 : 3)
+    fa_cache_append_kernel(const __grid_constant__ AppendArgs p, int span) {
     constexpr int LPR = D / 8;         // lanes per row, eight values (16 bytes) each
     constexpr int ROWS = 256 / LPR;    // rows of a CTA-wide load
     __shared__ int slot_of[512];       // slot of tokens t0 .. (-1: none)

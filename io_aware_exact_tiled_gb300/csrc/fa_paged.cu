@@ -98,7 +98,7 @@ struct PgCfg {
     static constexpr int USED = BAR_OFF + W * STAGES * 8;
     static constexpr int SMEM = USED + 1024;
     static_assert(W * RED_M * RED_F * 4 >= W * Q_BYTES, "Q of the warps' units");
-    static_assert(SMEM <= 232448 - 4096, "shared memory");
+    static_assert(SMEM <= 232448 - 6144, "shared memory, beside the static arrays");
 };
 
 struct PagedParams {

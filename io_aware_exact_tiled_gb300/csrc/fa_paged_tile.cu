@@ -6,9 +6,9 @@
 // Measured against 1,871 TFLOP/s of bf16 products: d = 128, two requests of
 // about 2,000 new tokens behind 15,000 to 16,384, 32 query heads, 803 us = 1,320
 // TFLOP/s (the chain of S, softmax and P V of two row tiles: the tensor pipe is
-// active 55 % of the time); d = 64,
-// eight prompts of 314 to 1,967 tokens, 16 heads, 95 us = 262 TFLOP/s (a unit's
-// start and end, and three times the products' time for the softmax).
+// active 55 % of the time); d = 64, eight prompts of 314 to 1,967 tokens, 16
+// heads, 95 us = 262 TFLOP/s (a unit's start and end, and three times the
+// products' time for the softmax).
 //
 // Work: a unit is (request, key head, pair of row tiles); a row is (new token,
 // query head of the group), token-major, so that a tile of 128 rows sees
