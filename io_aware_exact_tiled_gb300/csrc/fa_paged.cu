@@ -15,7 +15,7 @@
 // tokens, 32 key heads, 254 us = 6,590 GB/s of cache; 64 requests of 1 to 16,384
 // tokens, 8 key heads, 193 us = 5,950; one request of 262,001 tokens, 96 us =
 // 5,590. At d = 64, or with more rows, the issue slots bound it: 64 requests of
-// 8,000 tokens, 8 key heads, 8 / 16 / 24 / 32 rows: 115 / 165 / 191 / 232 us
+// 8,000 tokens, 8 key heads, 8 / 16 / 24 / 32 rows: 115 / 146 / 191 / 232 us
 // (bytes alone: 77), d = 128 171 / 211 / 267 us (155).
 //
 // Design:
@@ -30,8 +30,8 @@
 //     every time). Short units (up to a third of a warp's even share of all
 //     chunks) are not worth a CTA's barriers: each is one warp's, from its Q
 //     to its output.
-//   * Each of a CTA's eight or sixteen warps streams its own chunks (of a long
-//     unit every eighth or sixteenth) through its own ring of TMA boxes with its
+//   * Each of a CTA's eight to sixteen warps streams its own chunks (of a long
+//     unit every eighth to sixteenth) through its own ring of TMA boxes with its
 //     own mbarriers: no barrier between warps before a long unit ends. Block ids are fetched
 //     three chunks ahead of the copies that need them.
 //   * S^T = K Q^T and O^T = V^T P^T as m16n8k16 products with f16 operands
@@ -67,12 +67,13 @@ template <int D, int NT, bool B16>
 struct PgCfg {
     static constexpr int RT = 8 * NT;                     // query rows of a unit
     // Warps: what hides a chunk's chain of loads, products, exponentials and
-    // shuffles is other warps, as many as the registers allow without spills (64
-    // requests of 8,000 tokens, d = 64: 8 rows 137 us with 8 warps, 118 with 12,
-    // 115 with 16; 16 rows 165 with 8, 212 with 16).
-    static constexpr int W = D == 64 && NT == 1 ? 16 : 8;
+    // shuffles is other warps, as many as the registers allow with few spills,
+    // and as many on each scheduler (64 requests of 8,000 tokens, d = 64: 8 rows
+    // 137 us with 8 warps, 118 with 12, 115 with 16; 16 rows 165 with 8, 174 with
+    // 10, 146 with 12, 212 with 16).
+    static constexpr int W = D == 64 && NT <= 2 ? (NT == 1 ? 16 : 12) : 8;
     static constexpr int THREADS = 32 * W;
-    static constexpr int STAGES = D == 64 ? (NT >= 3 ? 4 : NT == 2 ? 5 : 2) : (NT == 1 ? 3 : 2);
+    static constexpr int STAGES = D == 64 ? (NT >= 3 ? 4 : NT == 2 ? 3 : 2) : (NT == 1 ? 3 : 2);
     // chunks' time that a long unit's rows, barriers and merge take (64 requests
     // of 1 to 16,384 tokens: d = 128 307 us with 1, 195 with 32, 197 with 48; d = 64
     // 226, 127 with 48, 131 with 72)
