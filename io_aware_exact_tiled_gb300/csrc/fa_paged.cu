@@ -75,8 +75,8 @@ struct PgCfg {
     static constexpr int THREADS = 32 * W;
     static constexpr int STAGES = D == 64 ? (NT >= 3 ? 4 : NT == 2 ? 3 : 2) : (NT == 1 ? 3 : 2);
     // chunks' time that a long unit's rows, barriers and merge take (64 requests
-    // of 1 to 16,384 tokens: d = 128 307 us with 1, 195 with 32, 197 with 48; d = 64
-    // 226, 127 with 48, 131 with 72)
+    // of 1 to 16,384 tokens: d = 128 271 us with 1, 192 with 32, 196 with 48; d = 64
+    // 212 with 1, 126 with 48, 129 with 72)
     static constexpr int COST = D == 64 ? 48 : 32;
     static constexpr int TILE = kPgChunk * D;             // bytes of a chunk's K (or V)
     static constexpr int SUBS = B16 ? 2 : 1;              // boxes of a tile
@@ -243,8 +243,8 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
     // one of up to twelve chunks always: a long unit costs its CTA barriers and a
     // merge, a short one keeps a single warp busy, at the end while others have
     // nothing left. d = 128, one token, 8 heads of keys: 1,024 requests of 1 to
-    // 600 tokens 235 us (a sixth: 306; none short: 371), 256 requests of 1 to
-    // 2,000 tokens 158 us (half: 183; up to the whole share: 180).
+    // 600 tokens 197 us (up to a sixth: 251; none short: 302), 256 requests of 1 to
+    // 2,000 tokens 143 us (up to a half: 160; to the whole share: 172).
     const long long share = W / (kPagedCtas * C::W);
     int T = static_cast<int>(min(max(share / 3, 12ll), 1ll << 30));
     auto line_long = [&](const PgSeg& s) {
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
         Wa += scan_w[2][w];
     }
     // A few short units among long ones would only come after everything else:
-    // they are taken as long ones (64 requests of 1 to 16,384 tokens: 196 us, 209
+    // they are taken as long ones (64 requests of 1 to 16,384 tokens: 192 us, 232
     // with a warp each for the short ones).
     if (Ws * 8 < W) {
         T = 0;
