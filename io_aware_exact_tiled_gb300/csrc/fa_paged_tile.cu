@@ -242,7 +242,8 @@ __global__ void __launch_bounds__(512, 1)
     uint64_t* pv_done = p_full + 4;            // [2][2] its P V done
     uint64_t* drain = pv_done + 4;             // [2]
     uint64_t* nan_full = drain + 2;            // [4] a piece's V has been looked over
-    uint64_t* sc_full = nan_full + kPtNanSlots;          // [8] scales stored
+    uint64_t* nan_empty = nan_full + kPtNanSlots;  // [4] both row tiles' softmax warps are through with that piece
+    uint64_t* sc_full = nan_empty + kPtNanSlots;   // [8] scales stored
     uint64_t* k_full = sc_full + kPtScaleSlots;  // [KS]
     uint64_t* k_empty = k_full + C::KS;        // [KS] both row tiles' S done
     uint64_t* r_full = k_empty + C::KS;        // [RS] V landed
@@ -260,7 +261,10 @@ __global__ void __launch_bounds__(512, 1)
                 mbar_init(&pv_done[2 * i + h], 1);
             }
         }
-        for (int i = 0; i < kPtNanSlots; ++i) mbar_init(&nan_full[i], 128);
+        for (int i = 0; i < kPtNanSlots; ++i) {
+            mbar_init(&nan_full[i], 128);
+            mbar_init(&nan_empty[i], 256);
+        }
         for (int i = 0; i < kPtScaleSlots; ++i) mbar_init(&sc_full[i], 1);
         for (int i = 0; i < C::KS; ++i) {
             mbar_init(&k_full[i], 1);
@@ -279,8 +283,10 @@ __global__ void __launch_bounds__(512, 1)
     // NaN values that only some rows see: for each column the piece's tag
     // (a later piece's entry replaces an earlier one's) and the first key;
     // and the piece that noted one last. A piece's slot is used again four
-    // pieces on: by then both row tiles have read it, as the conversion of V is
-    // at most two tiles ahead of the products.
+    // pieces on, once all softmax warps have said that they are through with it
+    // (nan_empty): a row tile without rows, or whose rows see none of a piece's
+    // keys, has no products that would hold the conversion of V back for them.
+    // So nan_full is at most one phase ahead of those that wait for it.
     unsigned long long* nan_first = reinterpret_cast<unsigned long long*>(sm + C::NAN_OFF);
     for (int i = tid; i < kPtNanSlots * D; i += 512) nan_first[i] = ~0ull;
     if (tid < kPtNanSlots) nan_piece[tid] = -1;
@@ -740,6 +746,7 @@ __global__ void __launch_bounds__(512, 1)
                 }
             }
             tc_fence_before();  // O has been read: the next piece's products may overwrite it
+            mbar_arrive(&nan_empty[(seg - 1) % kPtNanSlots]);
             const float lse_off = kPtOffset;
             if (whole) {
                 if (row_ok)
@@ -815,6 +822,7 @@ __global__ void __launch_bounds__(512, 1)
             const int vis_min = pt_visible(p, s.r, p.by_g.div(s.pair * 256));
             const int vis_max = pt_visible(p, s.r, p.by_g.div(min(s.pair * 256 + 255, rows - 1)));
             unsigned long long* nf = nan_first + (seg % kPtNanSlots) * D;
+            if (!(ok = wait_warp(&nan_empty[seg % kPtNanSlots], ((seg / kPtNanSlots) & 1) ^ 1))) break;
             for (int t = s.c0; t < s.c1; ++t, ++u) {
                 const int vs = u % C::VS, rs = u % C::RS;
                 ok = wait_warp(&r_full[rs], (u / C::RS) & 1);
