@@ -752,7 +752,16 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
                 }
             }
             ++consumed;
-            __syncwarp();  // the stage has been read
+            // The stage has been read: the copy that issue() requests into it
+            // must find every lane's loads done, and a barrier alone does not
+            // wait for loads whose values are still on their way. A vote on a
+            // sum that took a word of each load of V does, with the branch on it
+            // (to a fence, which changes nothing); the loads of K were done at
+            // the vote on the maxima above.
+            bool odd = __float_as_uint(o[0][0][0]) == 0x7F7F7F7Fu;
+            if constexpr (VH == 2) odd |= __float_as_uint(o[2 * VW][0][0]) == 0x7F7F7F7Fu;
+            if (__any_sync(0xffffffffu, odd)) __threadfence_block();
+            __syncwarp();
             issue();
         }
 

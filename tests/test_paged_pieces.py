@@ -1,6 +1,6 @@
-"""GPU checks of how the row-tile kernel of fa_fwd_paged walks many short
-pieces: row tiles without rows or without keys fall behind the roles that feed
-them, and what those roles reuse has to wait for them."""
+"""GPU checks of what the kernels of fa_fwd_paged reuse while they run: the
+row-tile kernel over many short pieces, whose row tiles without rows or keys
+fall behind the roles that feed them, and the rings of the split-key kernel."""
 
 import math
 
@@ -8,6 +8,7 @@ import numpy as np
 import pytest
 import torch
 
+import io_aware_exact_tiled_gb300 as fa
 from oracle import paged as P
 from test_paged import bf16, check, make_cache, run_attend
 
@@ -61,3 +62,35 @@ def test_many_row_tiles_that_see_nothing(cuda_device, d, G, Hkv):
         o, lse = run_attend(q, c, cu, lens, max(n), True, cuda_device, 0.1)
         check(o, lse, ref, cu, G, slice(0, total), max(lens), d)
     assert torch.isfinite(torch.from_numpy(o)).all()
+
+
+@pytest.mark.parametrize("d,G,n", [(64, 4, 1), (64, 4, 3), (64, 8, 4), (128, 4, 1), (128, 7, 2), (128, 8, 3)])
+@pytest.mark.parametrize("bs", [16, 64])
+def test_split_key_rings_again_and_again(cuda_device, d, G, n, bs):
+    """The split-key kernel's rings turn over thousands of times while another
+    stream keeps the memory busy: the same bits each time, and within the
+    bounds (long requests, cut, and short ones, a warp each)."""
+    rng = np.random.default_rng(d + G + n)
+    for lens in ([9000, 40, 5000, 17, 2500], rng.integers(n, 300, 400).tolist()):
+        cu = n * np.arange(len(lens) + 1)
+        total = int(cu[-1])
+        c = make_cache(lens, bs, 2, d, seed=bs)
+        q = bf16(rng.normal(size=(total, 2 * G, d)), cuda_device)
+        ref = P.attend(q.double().cpu().numpy(), *c[:4], cu, lens, c[4], 0.1)
+        o, lse = run_attend(q, c, cu, lens, n, True, cuda_device, 0.1)
+        check(o, lse, ref, cu, G, slice(0, total), max(lens), d)
+        kb, vb, ks, vs, table = c
+        args = [torch.tensor(x, device=cuda_device).view(torch.float8_e4m3fn) for x in (kb, vb)]
+        args += [torch.tensor(x, device=cuda_device) for x in (ks, vs)]
+        args += [torch.tensor(np.asarray(x), dtype=torch.int32, device=cuda_device) for x in (cu, lens, table)]
+        side, busy = torch.cuda.Stream(), torch.empty(1 << 26, device=cuda_device)
+        side.wait_stream(torch.cuda.current_stream())
+        first = fa.forward_paged(q, *args, n, scale=0.1)
+        for i in range(60):
+            if i % 3 == 0:
+                with torch.cuda.stream(side):
+                    busy.add_(1.0)
+            again = fa.forward_paged(q, *args, n, scale=0.1)
+            assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1]), i
+        torch.cuda.synchronize()
+        np.testing.assert_array_equal(first[0].double().cpu().numpy(), o)
