@@ -63,6 +63,15 @@ constexpr float kPgOffset = 6.0f;   // log2 of the factor on P before its roundi
 constexpr int kPgChunk = 32;        // keys of a chunk
 constexpr int kPgAhead = 3;         // chunks between the fetch of a block id and its use
 
+// FA_DEBUG_DROP_ARRIVE (debug builds only): the first chunk's V is not
+// requested in the first warp of each CTA, so that this warp's bounded wait
+// runs out; a test checks that every warp gives up cleanly.
+#ifdef FA_DEBUG_DROP_ARRIVE
+#define FA_DROP_THIS_COPY(first_chunk) ((first_chunk) && threadIdx.x < 32)
+#else
+#define FA_DROP_THIS_COPY(first_chunk) false
+#endif
+
 template <int D, int NT, bool B16>
 struct PgCfg {
     static constexpr int RT = 8 * NT;                     // query rows of a unit
@@ -454,7 +463,8 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
                 const long long key = ((static_cast<long long>(id) * p.Hkv) << p.bs_log2) + hi;
                 const int row = static_cast<int>(D == 128 ? key : key >> 1);
                 tma_load_2d(ring + (2 * st) * C::TILE + sub * C::BOX, &tmK, 0, row, &bars[st]);
-                tma_load_2d(ring + (2 * st + 1) * C::TILE + sub * C::BOX, &tmV, 0, row, &bars[st]);
+                if (!FA_DROP_THIS_COPY(issued == 0))
+                    tma_load_2d(ring + (2 * st + 1) * C::TILE + sub * C::BOX, &tmV, 0, row, &bars[st]);
             }
             if (lane < 4) {
                 float* dst = reinterpret_cast<float*>(&meta[st]) + lane;
