@@ -202,10 +202,13 @@ fa_status fa_decode(const void* q, const void* k, const void* v, void* o, float*
  * refused when the needs up to and with its own exceed the free count (so
  * every later one that needs blocks is refused as well). A refused request
  * keeps its length and blocks, and fa_get_status returns FA_ERR_NO_BLOCKS.
- * Blocks released by a call can be handed out from the next call on. Lengths
- * that do not fit (negative or above max_blocks * block_size, together more
- * than total, a table or ring entry that is no block) are refused on the
- * device and reported as FA_ERR_INVALID_ARG.
+ * Blocks released by a call can be handed out from the next call on. Requests
+ * whose lengths do not fit (cached or new ones negative or above max_blocks *
+ * block_size, new ones that end behind total) are refused in the same way,
+ * released ones too, and reported as FA_ERR_INVALID_ARG. So is a table or ring
+ * entry that is no block: tokens that would go there get slot -1, but the
+ * entry, the length and the list are carried on as if it were one (fa_fwd_paged
+ * then reports the request as well), so after that the lists want rebuilding.
  * With separate outputs a call may be repeated with the same result.
  * B <= 16384, total <= 2^30. Runs one kernel.
  */

@@ -51,10 +51,9 @@ struct PlanItem {
     int n;       // new tokens (0 for a released request)
     int len;     // tokens cached, clamped to the table's capacity
     int had;     // blocks they take
-    int need;    // further blocks (0 if the request is released or too long)
+    int need;    // further blocks (0 if the request is released or does not fit)
     bool drop;   // released
-    bool fits;   // the new length is within the block table
-    bool bad;    // a length out of range
+    bool fits;   // both lengths are within the block table
 };
 
 __device__ __forceinline__ int plan_blocks(const PlanArgs& p, int len) {  // len < 2^31 - 256
@@ -65,10 +64,9 @@ __device__ __forceinline__ PlanItem plan_item(const PlanArgs& p, int raw, int le
     PlanItem it;
     const int cap = p.max_blocks << p.bs_log2;  // < 2^31, checked on the host
     it.len = min(max(len, 0), cap);
-    it.bad = len != it.len;
-    it.drop = raw < 0;
     it.n = max(raw, 0);
-    it.fits = static_cast<long long>(it.len) + it.n <= cap;
+    it.fits = len == it.len && static_cast<long long>(it.len) + it.n <= cap;
+    it.drop = raw < 0 && it.fits;  // of a length out of range nobody knows which blocks are the request's
     it.had = plan_blocks(p, it.len);
     it.need = 0;
     if (!it.drop && it.fits) it.need = plan_blocks(p, it.len + it.n) - it.had;
@@ -147,7 +145,7 @@ __global__ void __launch_bounds__(1024) fa_cache_plan_kernel(const __grid_consta
             lens[b] = -1;
             refused |= !room;
         }
-        invalid |= it.bad || !it.fits;
+        invalid |= !it.fits;
         run = plan_add(run, {it.n, it.need, it.drop ? it.had : 0});
     });
     if (tid == nth - 1) tok_off[p.B] = static_cast<int>(min(all.tok, static_cast<long long>(p.total)));
