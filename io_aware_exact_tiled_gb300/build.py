@@ -65,10 +65,12 @@ DEBUG_LIB = os.path.join(PKG, "libfa_debug.so")
 
 
 def build_debug(force: bool = False) -> str:
-    """Debug variant for the give-up test: short (0.2 s) device wait limit and
-    one withheld "P ready" arrival per kernel (FA_DEBUG_DROP_ARRIVE)."""
-    return build(force, ("-DFA_DEBUG_DROP_ARRIVE", "-DFA_WAIT_LIMIT_NS=200000000ull"), DEBUG_LIB,
-                 os.path.join(PKG, "_build_debug"))
+    """Debug variant for the give-up tests: short (0.2 s) device wait limit and
+    one withheld "P ready" arrival (or copy) per kernel (FA_DEBUG_DROP_ARRIVE);
+    and plans in clusters of two CTAs, as on a device that holds no larger
+    ones."""
+    return build(force, ("-DFA_DEBUG_DROP_ARRIVE", "-DFA_WAIT_LIMIT_NS=200000000ull", "-DFA_PLAN_MAX_CLUSTER=2"),
+                 DEBUG_LIB, os.path.join(PKG, "_build_debug"))
 
 
 if __name__ == "__main__":

@@ -38,6 +38,7 @@ __device__ __forceinline__ uint32_t cluster_size() {
 // 4,096 requests with 117K tokens, a tenth of them released, 17 us: the scan 4,
 // the tokens 6, released blocks 3.
 constexpr int kPlanKeep = 4;
+constexpr int kPlanMaxSmem = (3 * kPlanMaxB + 4) * sizeof(int);
 
 struct PlanSum {
     long long tok, need, freed;
@@ -233,12 +234,54 @@ __global__ void __launch_bounds__(1024) fa_cache_plan_kernel(const __grid_consta
     if (invalid) atomicExch(p.status, FA_DEV_INVALID);
 }
 
+// The largest cluster that a plan asks for (a debug build sets it lower, so that
+// a test runs a smaller one).
+#ifndef FA_PLAN_MAX_CLUSTER
+#define FA_PLAN_MAX_CLUSTER 16
+#endif
+
+static cudaLaunchConfig_t plan_config(cudaLaunchAttribute* at, int ctas, int threads, size_t smem) {
+    at->id = cudaLaunchAttributeClusterDimension;
+    at->val.clusterDim.x = ctas;
+    at->val.clusterDim.y = at->val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+// CTAs of the largest cluster that fits the current device with the most shared
+// memory a plan takes (a part of a GPU may have no sixteen SMs together; one CTA
+// always fits). Asked once for each device.
+static cudaError_t plan_cluster(int* ctas) {
+    static std::atomic<int> known[64];  // 0: not asked yet
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+        for (n = FA_PLAN_MAX_CLUSTER; n > 1; n /= 2) {
+            cudaLaunchAttribute at;
+            const cudaLaunchConfig_t cfg = plan_config(&at, n, 1024, kPlanMaxSmem);
+            int fit = 0;
+            if (cudaOccupancyMaxActiveClusters(&fit, fa_cache_plan_kernel, &cfg) == cudaSuccess && fit > 0) break;
+            cudaGetLastError();  // a size that the device does not know is one that does not fit
+        }
+        if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    }
+    *ctas = n;
+    return cudaSuccess;
+}
+
 cudaError_t launch_cache_plan(const PlanArgs& a, cudaStream_t stream, int* nlaunch) {
     const size_t smem = (static_cast<size_t>(a.B) * 3 + 1) * sizeof(int);
     static std::atomic<uint64_t> done{0};
     cudaError_t e = once_per_device(done, [] {
-        cudaError_t r = cudaFuncSetAttribute(fa_cache_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (3 * kPlanMaxB + 4) * sizeof(int));
+        cudaError_t r =
+            cudaFuncSetAttribute(fa_cache_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanMaxSmem);
         if (r == cudaSuccess)
             r = cudaFuncSetAttribute(fa_cache_plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         return r;
@@ -248,17 +291,11 @@ cudaError_t launch_cache_plan(const PlanArgs& a, cudaStream_t stream, int* nlaun
     // a cluster of 16 where there are many requests or tokens (4096 requests,
     // 117K tokens: 22 us with eight CTAs, 17 with sixteen).
     const bool big = a.B > 1024 || a.total > 4096;
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = big ? 16 : 1;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(big ? 16 : 1);
-    cfg.blockDim = dim3(big ? 1024 : 256);
-    cfg.dynamicSmemBytes = smem;
+    int ctas = 1;
+    if (big && (e = plan_cluster(&ctas)) != cudaSuccess) return e;
+    cudaLaunchAttribute at;
+    cudaLaunchConfig_t cfg = plan_config(&at, ctas, big ? 1024 : 256, smem);
     cfg.stream = stream;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, fa_cache_plan_kernel, a);
     *nlaunch = 1;
     return e != cudaSuccess ? e : cudaGetLastError();

@@ -1,10 +1,13 @@
 """GPU checks of fa_cache_plan where a batch holds something that does not fit
 or has no room: that request keeps what it has, and the others are served."""
 
+import ctypes
+
 import numpy as np
 import pytest
 
 from io_aware_exact_tiled_gb300 import binding as fb
+from io_aware_exact_tiled_gb300 import build as fbuild
 from oracle import paged as P
 from test_paged import PLAN_KEYS, make_plan, run_plan
 
@@ -87,3 +90,23 @@ def test_entries_that_are_no_blocks_get_no_slots(cuda_device):
     bad = (want["slots"] < 0) | (want["slots"] >= nb * 16)
     assert 0 < bad.sum() < 73
     np.testing.assert_array_equal(got["slots"], np.where(bad, -1, want["slots"]))
+
+
+@pytest.mark.parametrize("B,bs,len_hi,new_hi,release,room", [
+    (1025, 64, 500, 9, 0.1, 0.9), (5000, 16, 64, 40, 0.2, 0.6), (16384, 16, 20, 2, 0.1, 0.99),
+    (2, 64, 70, 40000, 0.0, 1.0)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_large_plans_in_a_smaller_cluster(cuda_device, B, bs, len_hi, new_hi, release, room, in_place, monkeypatch):
+    """Where the device cannot hold a cluster of sixteen CTAs (here: a build
+    that asks for two at most) a large plan is the same."""
+    dbg, regular = ctypes.CDLL(fbuild.build_debug()), fb.load()
+    for name in ("fa_cache_plan", "fa_get_status"):
+        getattr(dbg, name).argtypes = getattr(regular, name).argtypes
+        getattr(dbg, name).restype = getattr(regular, name).restype
+    x = make_plan(B, bs, len_hi, new_hi, release, room, seed=B + bs)
+    want = P.plan(**x)
+    monkeypatch.setattr(fb, "_lib", dbg)
+    got, status = run_plan(x, cuda_device, in_place)
+    for k in PLAN_KEYS:
+        np.testing.assert_array_equal(got[k], want[k], err_msg=k)
+    assert status == (fb.FA_ERR_NO_BLOCKS if want["refused"] else fb.FA_OK)
