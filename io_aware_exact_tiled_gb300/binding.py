@@ -5,11 +5,17 @@ this module checks tensor properties, allocates outputs and workspace with
 PyTorch when the caller does not pass them, and forwards raw device pointers
 and the current CUDA stream. There is no fallback: if the library is missing
 or a call fails, an exception is raised.
+
+``stream`` names another stream to run on: the call is then the same as one
+inside ``with torch.cuda.stream(stream)``, buffers that it allocates included
+(they are that stream's for the allocator, so memory is not handed on while the
+kernels on it still run).
 """
 
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import re
@@ -125,6 +131,23 @@ def _stream_handle(stream: Optional[torch.cuda.Stream]):
     return _raw_stream(torch.cuda.current_device())
 
 
+def _on_stream(call):
+    """Entry points with `stream` as their last argument: a given stream is
+    made the current one, so that outputs and workspaces allocated in the call
+    come from that stream's memory."""
+    nargs = call.__code__.co_argcount
+
+    @functools.wraps(call)
+    def run(*args, stream=None, **kw):
+        if len(args) == nargs:
+            stream, args = args[-1], args[:-1]
+        if stream is None:
+            return call(*args, **kw)
+        with torch.cuda.stream(stream):
+            return call(*args, **kw)
+    return run
+
+
 def _check_device(q: torch.Tensor):
     """The kernels run on the current CUDA device: q must live there."""
     if not q.is_cuda:
@@ -228,6 +251,7 @@ def workspace(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(256, nbytes), dtype=torch.uint8, device=device)
 
 
+@_on_stream
 def forward(q, k, v, scale: Optional[float] = None, causal: bool = False, blockmask=None, kv_len=None,
             out=None, lse=None, ws=None, stream=None):
     """O, L = fa_fwd(...). Returns (o [B,H,N,d], lse fp32 [B,H,N])."""
@@ -264,6 +288,7 @@ def _check_packed(cu_seqlens, *ts: torch.Tensor):
     return FA_BF16
 
 
+@_on_stream
 def forward_varlen(q, k, v, cu_seqlens, max_seqlen: int, scale: Optional[float] = None, causal: bool = False,
                    out=None, lse=None, ws=None, stream=None):
     """O, L = fa_fwd_varlen(...) on a packed batch. q, k, v: [total, H, d]
@@ -285,6 +310,7 @@ def forward_varlen(q, k, v, cu_seqlens, max_seqlen: int, scale: Optional[float] 
     return o, L
 
 
+@_on_stream
 def backward_varlen(q, k, v, o, lse, do, cu_seqlens, max_seqlen: int, scale: Optional[float] = None,
                     causal: bool = False, dq=None, dk=None, dv=None, ws=None, stream=None):
     """dQ, dK, dV = fa_bwd_varlen(...) on a packed batch ([total, H, d] bf16;
@@ -307,6 +333,7 @@ def backward_varlen(q, k, v, o, lse, do, cu_seqlens, max_seqlen: int, scale: Opt
     return dq, dk, dv
 
 
+@_on_stream
 def forward_fp8(q, k, v, signs, scale: Optional[float] = None, causal: bool = False, kv_len=None, out=None,
                 lse=None, ws=None, stream=None):
     """O, L = fa_fwd_fp8(...): the FP8 forward pass with a Hadamard rotation
@@ -332,6 +359,7 @@ def forward_fp8(q, k, v, signs, scale: Optional[float] = None, causal: bool = Fa
     return o, L
 
 
+@_on_stream
 def forward_dropout(q, k, v, dropout_p: float, seed: int, scale: Optional[float] = None, causal: bool = False,
                     kv_len=None, out=None, lse=None, ws=None, stream=None):
     """O, L = fa_fwd_dropout(...): attention with dropout on the
@@ -353,6 +381,7 @@ def forward_dropout(q, k, v, dropout_p: float, seed: int, scale: Optional[float]
     return o, L
 
 
+@_on_stream
 def backward_dropout(q, k, v, o, lse, do, dropout_p: float, seed: int, scale: Optional[float] = None,
                      causal: bool = False, kv_len=None, dq=None, dk=None, dv=None, ws=None, stream=None):
     """dQ, dK, dV = fa_bwd_dropout(...) for forward_dropout's outputs."""
@@ -375,6 +404,7 @@ def backward_dropout(q, k, v, o, lse, do, dropout_p: float, seed: int, scale: Op
     return dq, dk, dv
 
 
+@_on_stream
 def decode(q, k_cache, v_cache, cache_len=None, scale: Optional[float] = None, num_splits: int = 0, out=None,
            lse=None, ws=None, stream=None):
     """O, L = fa_decode(...): Nq (1..8) query rows per (b, h) against a
@@ -429,6 +459,7 @@ def paged_cache(num_blocks: int, Hkv: int, block_size: int, d: int, B: int, max_
                       torch.arange(num_blocks, **i32), torch.tensor([0, num_blocks], **i32))
 
 
+@_on_stream
 def cache_plan(new_len, cache_len, block_table, free_blocks, free_state, block_size: int,
                total: Optional[int] = None, cache_len_out=None, free_state_out=None, cu_seqlens=None, slots=None,
                ws=None, stream=None):
@@ -477,6 +508,7 @@ def _check_paged(k_cache, v_cache, k_scale, v_scale, device):
     return shape
 
 
+@_on_stream
 def cache_append(k, v, k_cache, v_cache, k_scale, v_scale, slots, stream=None):
     """fa_cache_append(...): quantises k, v [total, Hkv, d] bf16 into the rows
     `slots` (int32 [total], from cache_plan) of the caches (float8_e4m3fn
@@ -496,6 +528,7 @@ def cache_append(k, v, k_cache, v_cache, k_scale, v_scale, slots, stream=None):
         raise FAError(rc, "fa_cache_append")
 
 
+@_on_stream
 def forward_paged(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens, cache_len, block_table, max_new: int,
                   scale: Optional[float] = None, causal: bool = True, out=None, lse=None, ws=None, stream=None):
     """O, L = fa_fwd_paged(...): attention of the packed new tokens q
@@ -526,6 +559,7 @@ def forward_paged(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens, cache_len, 
     return o, L
 
 
+@_on_stream
 def backward(q, k, v, o, lse, do, scale: Optional[float] = None, causal: bool = False, blockmask=None,
              kv_len=None, dq=None, dk=None, dv=None, ws=None, stream=None):
     """dQ, dK, dV = fa_bwd(...). Returns (dq, dk, dv)."""
@@ -566,6 +600,7 @@ def set_timing_events(begin=None, end=None):
         raise FAError(rc, "fa_set_timing_events")
 
 
+@_on_stream
 def backward_noalloc(q, k, v, o, lse, do, scale: Optional[float] = None, causal: bool = False, blockmask=None,
                      kv_len=None, dq=None, dk=None, dv=None, stream=None):
     """dQ, dK, dV = fa_bwd_noalloc(...): the backward pass with the library's
