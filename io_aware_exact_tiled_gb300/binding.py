@@ -6,16 +6,15 @@ PyTorch when the caller does not pass them, and forwards raw device pointers
 and the current CUDA stream. There is no fallback: if the library is missing
 or a call fails, an exception is raised.
 
-``stream`` names another stream to run on: the call is then the same as one
-inside ``with torch.cuda.stream(stream)``, buffers that it allocates included
-(they are that stream's for the allocator, so memory is not handed on while the
-kernels on it still run).
+``stream`` names another stream (of the current device) to run on. Outputs and
+workspaces that the call allocates are then that stream's for the allocator, as
+inside ``with torch.cuda.stream(stream)``: their memory is not handed on while
+kernels on it still run.
 """
 
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 import os
 import re
@@ -125,27 +124,13 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _stream_handle(stream: Optional[torch.cuda.Stream]):
     if stream is not None:
+        if stream.device_index != torch.cuda.current_device():
+            raise ValueError(f"the stream is on {stream.device} but the current device is"
+                             f" cuda:{torch.cuda.current_device()}")
         return stream.cuda_stream
     if _raw_stream is None:
         return torch.cuda.current_stream().cuda_stream
     return _raw_stream(torch.cuda.current_device())
-
-
-def _on_stream(call):
-    """Entry points with `stream` as their last argument: a given stream is
-    made the current one, so that outputs and workspaces allocated in the call
-    come from that stream's memory."""
-    nargs = call.__code__.co_argcount
-
-    @functools.wraps(call)
-    def run(*args, stream=None, **kw):
-        if len(args) == nargs:
-            stream, args = args[-1], args[:-1]
-        if stream is None:
-            return call(*args, **kw)
-        with torch.cuda.stream(stream):
-            return call(*args, **kw)
-    return run
 
 
 def _check_device(q: torch.Tensor):
@@ -165,18 +150,25 @@ def _in(t: torch.Tensor, shape, dtype, device, name: str) -> torch.Tensor:
     return t
 
 
-def _out(t: Optional[torch.Tensor], shape, dtype, device, name: str) -> torch.Tensor:
-    """A caller-supplied output, checked as in _in, or a new one."""
+def _out(t: Optional[torch.Tensor], shape, dtype, device, name: str, stream=None) -> torch.Tensor:
+    """A caller-supplied output, checked as in _in, or a new one of `stream`."""
     if t is None:
-        return torch.empty(tuple(shape), dtype=dtype, device=device)
+        if stream is None:
+            return torch.empty(tuple(shape), dtype=dtype, device=device)
+        with torch.cuda.stream(stream):
+            return torch.empty(tuple(shape), dtype=dtype, device=device)
     return _in(t, shape, dtype, device, name)
 
 
-def _ws(ws: Optional[torch.Tensor], nbytes, device) -> torch.Tensor:
+def _ws(ws: Optional[torch.Tensor], nbytes, device, stream=None) -> torch.Tensor:
     """A caller-supplied workspace (on the device, contiguous; its size is
-    checked by the library) or a new one of `nbytes`."""
+    checked by the library) or a new one of `nbytes`, of `stream`."""
     if ws is None:
-        return workspace(nbytes() if callable(nbytes) else nbytes, device)
+        nbytes = nbytes() if callable(nbytes) else nbytes
+        if stream is None:
+            return workspace(nbytes, device)
+        with torch.cuda.stream(stream):
+            return workspace(nbytes, device)
     if ws.device != device or not ws.is_contiguous():
         raise ValueError(f"the workspace must be a contiguous tensor on {device}")
     return ws
@@ -251,7 +243,6 @@ def workspace(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(256, nbytes), dtype=torch.uint8, device=device)
 
 
-@_on_stream
 def forward(q, k, v, scale: Optional[float] = None, causal: bool = False, blockmask=None, kv_len=None,
             out=None, lse=None, ws=None, stream=None):
     """O, L = fa_fwd(...). Returns (o [B,H,N,d], lse fp32 [B,H,N])."""
@@ -259,9 +250,9 @@ def forward(q, k, v, scale: Optional[float] = None, causal: bool = False, blockm
     dtype = _check_qkv(q, k, v)
     B, H, N, d = q.shape
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    o = _out(out, q.shape, q.dtype, q.device, "out")
-    L = _out(lse, (B, H, N), torch.float32, q.device, "lse")
-    ws = _ws(ws, lambda: lib.fa_fwd_workspace_size(B, H, N, d) if dtype == FA_FP32 else 256, q.device)
+    o = _out(out, q.shape, q.dtype, q.device, "out", stream)
+    L = _out(lse, (B, H, N), torch.float32, q.device, "lse", stream)
+    ws = _ws(ws, lambda: lib.fa_fwd_workspace_size(B, H, N, d) if dtype == FA_FP32 else 256, q.device, stream)
     bm, kl = _mask_ptrs(blockmask, kv_len, q)
     rc = lib.fa_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(L), B, H, N, d, scale, int(bool(causal)), bm, kl,
                     dtype, _ptr(ws), _nbytes(ws), _stream_handle(stream))
@@ -288,7 +279,6 @@ def _check_packed(cu_seqlens, *ts: torch.Tensor):
     return FA_BF16
 
 
-@_on_stream
 def forward_varlen(q, k, v, cu_seqlens, max_seqlen: int, scale: Optional[float] = None, causal: bool = False,
                    out=None, lse=None, ws=None, stream=None):
     """O, L = fa_fwd_varlen(...) on a packed batch. q, k, v: [total, H, d]
@@ -299,9 +289,9 @@ def forward_varlen(q, k, v, cu_seqlens, max_seqlen: int, scale: Optional[float] 
     total, H, d = q.shape
     B = cu_seqlens.numel() - 1
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    o = _out(out, q.shape, q.dtype, q.device, "out")
-    L = _out(lse, (H, total), torch.float32, q.device, "lse")
-    ws = _ws(ws, lambda: lib.fa_fwd_varlen_workspace_size(H, total, d), q.device)
+    o = _out(out, q.shape, q.dtype, q.device, "out", stream)
+    L = _out(lse, (H, total), torch.float32, q.device, "lse", stream)
+    ws = _ws(ws, lambda: lib.fa_fwd_varlen_workspace_size(H, total, d), q.device, stream)
     rc = lib.fa_fwd_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(L), _ptr(cu_seqlens), B, H, total,
                            int(max_seqlen), d, scale, int(bool(causal)), dtype, _ptr(ws), _nbytes(ws),
                            _stream_handle(stream))
@@ -310,7 +300,6 @@ def forward_varlen(q, k, v, cu_seqlens, max_seqlen: int, scale: Optional[float] 
     return o, L
 
 
-@_on_stream
 def backward_varlen(q, k, v, o, lse, do, cu_seqlens, max_seqlen: int, scale: Optional[float] = None,
                     causal: bool = False, dq=None, dk=None, dv=None, ws=None, stream=None):
     """dQ, dK, dV = fa_bwd_varlen(...) on a packed batch ([total, H, d] bf16;
@@ -321,10 +310,10 @@ def backward_varlen(q, k, v, o, lse, do, cu_seqlens, max_seqlen: int, scale: Opt
     B = cu_seqlens.numel() - 1
     _in(lse, (H, total), torch.float32, q.device, "lse")
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    dq = _out(dq, q.shape, q.dtype, q.device, "dq")
-    dk = _out(dk, q.shape, q.dtype, q.device, "dk")
-    dv = _out(dv, q.shape, q.dtype, q.device, "dv")
-    ws = _ws(ws, lambda: lib.fa_bwd_varlen_workspace_size(B, H, total, d), q.device)
+    dq = _out(dq, q.shape, q.dtype, q.device, "dq", stream)
+    dk = _out(dk, q.shape, q.dtype, q.device, "dk", stream)
+    dv = _out(dv, q.shape, q.dtype, q.device, "dv", stream)
+    ws = _ws(ws, lambda: lib.fa_bwd_varlen_workspace_size(B, H, total, d), q.device, stream)
     rc = lib.fa_bwd_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(do), _ptr(dq), _ptr(dk), _ptr(dv),
                            _ptr(cu_seqlens), B, H, total, int(max_seqlen), d, scale, int(bool(causal)), dtype,
                            _ptr(ws), _nbytes(ws), _stream_handle(stream))
@@ -333,7 +322,6 @@ def backward_varlen(q, k, v, o, lse, do, cu_seqlens, max_seqlen: int, scale: Opt
     return dq, dk, dv
 
 
-@_on_stream
 def forward_fp8(q, k, v, signs, scale: Optional[float] = None, causal: bool = False, kv_len=None, out=None,
                 lse=None, ws=None, stream=None):
     """O, L = fa_fwd_fp8(...): the FP8 forward pass with a Hadamard rotation
@@ -348,9 +336,9 @@ def forward_fp8(q, k, v, signs, scale: Optional[float] = None, causal: bool = Fa
     if signs is not None and (signs.dtype != torch.float32 or signs.shape != (d,) or signs.device != q.device):
         raise ValueError("signs must be None or a float32 [d] tensor on the same device")
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    o = _out(out, q.shape, q.dtype, q.device, "out")
-    L = _out(lse, (B, H, N), torch.float32, q.device, "lse")
-    ws = _ws(ws, lambda: lib.fa_fwd_fp8_workspace_size(B, H, N, d), q.device)
+    o = _out(out, q.shape, q.dtype, q.device, "out", stream)
+    L = _out(lse, (B, H, N), torch.float32, q.device, "lse", stream)
+    ws = _ws(ws, lambda: lib.fa_fwd_fp8_workspace_size(B, H, N, d), q.device, stream)
     _, kl = _mask_ptrs(None, kv_len, q)
     rc = lib.fa_fwd_fp8(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(L), B, H, N, d, scale, int(bool(causal)), kl,
                         _ptr(signs), _ptr(ws), _nbytes(ws), _stream_handle(stream))
@@ -359,7 +347,6 @@ def forward_fp8(q, k, v, signs, scale: Optional[float] = None, causal: bool = Fa
     return o, L
 
 
-@_on_stream
 def forward_dropout(q, k, v, dropout_p: float, seed: int, scale: Optional[float] = None, causal: bool = False,
                     kv_len=None, out=None, lse=None, ws=None, stream=None):
     """O, L = fa_fwd_dropout(...): attention with dropout on the
@@ -369,9 +356,9 @@ def forward_dropout(q, k, v, dropout_p: float, seed: int, scale: Optional[float]
         raise ValueError("dropout takes bfloat16 inputs")
     B, H, N, d = q.shape
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    o = _out(out, q.shape, q.dtype, q.device, "out")
-    L = _out(lse, (B, H, N), torch.float32, q.device, "lse")
-    ws = _ws(ws, 256, q.device)
+    o = _out(out, q.shape, q.dtype, q.device, "out", stream)
+    L = _out(lse, (B, H, N), torch.float32, q.device, "lse", stream)
+    ws = _ws(ws, 256, q.device, stream)
     _, kl = _mask_ptrs(None, kv_len, q)
     rc = lib.fa_fwd_dropout(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(L), B, H, N, d, scale, int(bool(causal)), kl,
                             float(dropout_p), int(seed) & 0xFFFFFFFFFFFFFFFF, _ptr(ws), _nbytes(ws),
@@ -381,7 +368,6 @@ def forward_dropout(q, k, v, dropout_p: float, seed: int, scale: Optional[float]
     return o, L
 
 
-@_on_stream
 def backward_dropout(q, k, v, o, lse, do, dropout_p: float, seed: int, scale: Optional[float] = None,
                      causal: bool = False, kv_len=None, dq=None, dk=None, dv=None, ws=None, stream=None):
     """dQ, dK, dV = fa_bwd_dropout(...) for forward_dropout's outputs."""
@@ -391,10 +377,10 @@ def backward_dropout(q, k, v, o, lse, do, dropout_p: float, seed: int, scale: Op
     B, H, N, d = q.shape
     _in(lse, (B, H, N), torch.float32, q.device, "lse")
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    dq = _out(dq, q.shape, q.dtype, q.device, "dq")
-    dk = _out(dk, q.shape, q.dtype, q.device, "dk")
-    dv = _out(dv, q.shape, q.dtype, q.device, "dv")
-    ws = _ws(ws, lambda: lib.fa_bwd_workspace_size(B, H, N, d), q.device)
+    dq = _out(dq, q.shape, q.dtype, q.device, "dq", stream)
+    dk = _out(dk, q.shape, q.dtype, q.device, "dk", stream)
+    dv = _out(dv, q.shape, q.dtype, q.device, "dv", stream)
+    ws = _ws(ws, lambda: lib.fa_bwd_workspace_size(B, H, N, d), q.device, stream)
     _, kl = _mask_ptrs(None, kv_len, q)
     rc = lib.fa_bwd_dropout(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(do), _ptr(dq), _ptr(dk), _ptr(dv),
                             B, H, N, d, scale, int(bool(causal)), kl, float(dropout_p),
@@ -404,7 +390,6 @@ def backward_dropout(q, k, v, o, lse, do, dropout_p: float, seed: int, scale: Op
     return dq, dk, dv
 
 
-@_on_stream
 def decode(q, k_cache, v_cache, cache_len=None, scale: Optional[float] = None, num_splits: int = 0, out=None,
            lse=None, ws=None, stream=None):
     """O, L = fa_decode(...): Nq (1..8) query rows per (b, h) against a
@@ -423,9 +408,9 @@ def decode(q, k_cache, v_cache, cache_len=None, scale: Optional[float] = None, n
                                   or cache_len.device != q.device):
         raise ValueError("cache_len must be an int32 [B] tensor on the same device")
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    o = _out(out, q.shape, q.dtype, q.device, "out")
-    L = _out(lse, (B, H, Nq), torch.float32, q.device, "lse")
-    ws = _ws(ws, lambda: lib.fa_decode_workspace_size(B, H, Nq, Nk, d, num_splits), q.device)
+    o = _out(out, q.shape, q.dtype, q.device, "out", stream)
+    L = _out(lse, (B, H, Nq), torch.float32, q.device, "lse", stream)
+    ws = _ws(ws, lambda: lib.fa_decode_workspace_size(B, H, Nq, Nk, d, num_splits), q.device, stream)
     rc = lib.fa_decode(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(o), _ptr(L), B, H, Nq, Nk, d, scale,
                        _ptr(cache_len), int(num_splits), FA_BF16, _ptr(ws), _nbytes(ws), _stream_handle(stream))
     if rc != FA_OK:
@@ -459,7 +444,6 @@ def paged_cache(num_blocks: int, Hkv: int, block_size: int, d: int, B: int, max_
                       torch.arange(num_blocks, **i32), torch.tensor([0, num_blocks], **i32))
 
 
-@_on_stream
 def cache_plan(new_len, cache_len, block_table, free_blocks, free_state, block_size: int,
                total: Optional[int] = None, cache_len_out=None, free_state_out=None, cu_seqlens=None, slots=None,
                ws=None, stream=None):
@@ -486,9 +470,9 @@ def cache_plan(new_len, cache_len, block_table, free_blocks, free_state, block_s
     if slots is None and total is None:
         raise ValueError("pass slots, or total, the size of the packed batch")
     total = slots.numel() if total is None else int(total)
-    cu = _out(cu_seqlens, (B + 1,), i32, dev, "cu_seqlens")
-    slots = _out(slots, (total,), i32, dev, "slots")
-    ws = _ws(ws, 256, dev)
+    cu = _out(cu_seqlens, (B + 1,), i32, dev, "cu_seqlens", stream)
+    slots = _out(slots, (total,), i32, dev, "slots", stream)
+    ws = _ws(ws, 256, dev, stream)
     rc = lib.fa_cache_plan(_ptr(new_len), _ptr(cache_len), _ptr(cache_len_out), _ptr(block_table), _ptr(free_blocks),
                            _ptr(free_state), _ptr(free_state_out), _ptr(cu), _ptr(slots), B, max_blocks, num_blocks,
                            int(block_size), total, _ptr(ws), _nbytes(ws), _stream_handle(stream))
@@ -508,7 +492,6 @@ def _check_paged(k_cache, v_cache, k_scale, v_scale, device):
     return shape
 
 
-@_on_stream
 def cache_append(k, v, k_cache, v_cache, k_scale, v_scale, slots, stream=None):
     """fa_cache_append(...): quantises k, v [total, Hkv, d] bf16 into the rows
     `slots` (int32 [total], from cache_plan) of the caches (float8_e4m3fn
@@ -528,7 +511,6 @@ def cache_append(k, v, k_cache, v_cache, k_scale, v_scale, slots, stream=None):
         raise FAError(rc, "fa_cache_append")
 
 
-@_on_stream
 def forward_paged(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens, cache_len, block_table, max_new: int,
                   scale: Optional[float] = None, causal: bool = True, out=None, lse=None, ws=None, stream=None):
     """O, L = fa_fwd_paged(...): attention of the packed new tokens q
@@ -547,9 +529,9 @@ def forward_paged(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens, cache_len, 
     _in(cache_len, (B,), torch.int32, q.device, "cache_len")
     _in(block_table, (B, max_blocks), torch.int32, q.device, "block_table")
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    o = _out(out, q.shape, q.dtype, q.device, "out")
-    L = _out(lse, (Hq, total), torch.float32, q.device, "lse")
-    ws = _ws(ws, lambda: lib.fa_fwd_paged_workspace_size(B, Hq, Hkv, total, int(max_new), d), q.device)
+    o = _out(out, q.shape, q.dtype, q.device, "out", stream)
+    L = _out(lse, (Hq, total), torch.float32, q.device, "lse", stream)
+    ws = _ws(ws, lambda: lib.fa_fwd_paged_workspace_size(B, Hq, Hkv, total, int(max_new), d), q.device, stream)
     rc = lib.fa_fwd_paged(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(o), _ptr(L),
                           _ptr(cu_seqlens), _ptr(cache_len), _ptr(block_table), B, Hq, Hkv, total, int(max_new),
                           max_blocks, num_blocks, bs, d, scale, int(bool(causal)), _ptr(ws), _nbytes(ws),
@@ -559,7 +541,6 @@ def forward_paged(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens, cache_len, 
     return o, L
 
 
-@_on_stream
 def backward(q, k, v, o, lse, do, scale: Optional[float] = None, causal: bool = False, blockmask=None,
              kv_len=None, dq=None, dk=None, dv=None, ws=None, stream=None):
     """dQ, dK, dV = fa_bwd(...). Returns (dq, dk, dv)."""
@@ -568,10 +549,10 @@ def backward(q, k, v, o, lse, do, scale: Optional[float] = None, causal: bool = 
     B, H, N, d = q.shape
     _in(lse, (B, H, N), torch.float32, q.device, "lse")
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    dq = _out(dq, q.shape, q.dtype, q.device, "dq")
-    dk = _out(dk, q.shape, q.dtype, q.device, "dk")
-    dv = _out(dv, q.shape, q.dtype, q.device, "dv")
-    ws = _ws(ws, lambda: lib.fa_bwd_workspace_size(B, H, N, d), q.device)
+    dq = _out(dq, q.shape, q.dtype, q.device, "dq", stream)
+    dk = _out(dk, q.shape, q.dtype, q.device, "dk", stream)
+    dv = _out(dv, q.shape, q.dtype, q.device, "dv", stream)
+    ws = _ws(ws, lambda: lib.fa_bwd_workspace_size(B, H, N, d), q.device, stream)
     bm, kl = _mask_ptrs(blockmask, kv_len, q)
     rc = lib.fa_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(do), _ptr(dq), _ptr(dk), _ptr(dv),
                     B, H, N, d, scale, int(bool(causal)), bm, kl, dtype, _ptr(ws), _nbytes(ws),
@@ -600,7 +581,6 @@ def set_timing_events(begin=None, end=None):
         raise FAError(rc, "fa_set_timing_events")
 
 
-@_on_stream
 def backward_noalloc(q, k, v, o, lse, do, scale: Optional[float] = None, causal: bool = False, blockmask=None,
                      kv_len=None, dq=None, dk=None, dv=None, stream=None):
     """dQ, dK, dV = fa_bwd_noalloc(...): the backward pass with the library's
@@ -611,9 +591,9 @@ def backward_noalloc(q, k, v, o, lse, do, scale: Optional[float] = None, causal:
     B, H, N, d = q.shape
     _in(lse, (B, H, N), torch.float32, q.device, "lse")
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    dq = _out(dq, q.shape, q.dtype, q.device, "dq")
-    dk = _out(dk, q.shape, q.dtype, q.device, "dk")
-    dv = _out(dv, q.shape, q.dtype, q.device, "dv")
+    dq = _out(dq, q.shape, q.dtype, q.device, "dq", stream)
+    dk = _out(dk, q.shape, q.dtype, q.device, "dk", stream)
+    dv = _out(dv, q.shape, q.dtype, q.device, "dv", stream)
     bm, kl = _mask_ptrs(blockmask, kv_len, q)
     rc = fn(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(do), _ptr(dq), _ptr(dk), _ptr(dv), B, H, N, d,
             scale, int(bool(causal)), bm, kl, dtype, _stream_handle(stream))

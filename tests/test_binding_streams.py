@@ -3,6 +3,7 @@ belongs to the stream that it runs on."""
 
 import contextlib
 import inspect
+import types
 
 import pytest
 import torch
@@ -89,3 +90,12 @@ def test_outputs_belong_to_the_given_stream(cuda_device, name):
     assert set(owner.values()) == {side.cuda_stream} and len(owner) == 2
     want = getattr(fa, name)(*args[name])
     assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    other = types.SimpleNamespace(device_index=1, device="cuda:1", cuda_stream=7)
+    with pytest.raises(ValueError, match="stream"):
+        fb._stream_handle(other)
+    other.device_index = 0
+    assert fb._stream_handle(other) == 7
