@@ -201,7 +201,10 @@ fa_status fa_decode(const void* q, const void* k, const void* v, void* o, float*
  * Blocks are handed out in the order of the requests: one that needs blocks is
  * refused when the needs up to and with its own exceed the free count (so
  * every later one that needs blocks is refused as well). A refused request
- * keeps its length and blocks, and fa_get_status returns FA_ERR_NO_BLOCKS.
+ * keeps its length and blocks, and fa_get_status returns FA_ERR_NO_BLOCKS. Its
+ * new tokens stay in the packed batch, with slot -1: fa_cache_append skips
+ * them, and what fa_fwd_paged computes in their rows (it takes them for the
+ * last tokens that the cache holds) is to be dropped.
  * Blocks released by a call can be handed out from the next call on. Requests
  * whose lengths do not fit (cached or new ones negative or above max_blocks *
  * block_size, new ones that end behind total) are refused in the same way,

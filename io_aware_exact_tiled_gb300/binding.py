@@ -429,6 +429,7 @@ class PagedCache(NamedTuple):
     cache_len: torch.Tensor    # int32 [B]
     free_blocks: torch.Tensor  # int32 [num_blocks], a ring
     free_state: torch.Tensor   # int32 [2]: its head and count
+    status: torch.Tensor       # uint8 [256]: cache_plan's workspace, read by get_status
 
 
 def paged_cache(num_blocks: int, Hkv: int, block_size: int, d: int, B: int, max_blocks: int,
@@ -441,7 +442,8 @@ def paged_cache(num_blocks: int, Hkv: int, block_size: int, d: int, B: int, max_
             for _ in range(2))
     ks, vs = (torch.zeros((num_blocks, Hkv), dtype=torch.float32, device=device) for _ in range(2))
     return PagedCache(k, v, ks, vs, torch.full((B, max_blocks), -1, **i32), torch.zeros(B, **i32),
-                      torch.arange(num_blocks, **i32), torch.tensor([0, num_blocks], **i32))
+                      torch.arange(num_blocks, **i32), torch.tensor([0, num_blocks], **i32),
+                      torch.zeros(256, dtype=torch.uint8, device=device))
 
 
 def cache_plan(new_len, cache_len, block_table, free_blocks, free_state, block_size: int,
@@ -453,6 +455,12 @@ def cache_plan(new_len, cache_len, block_table, free_blocks, free_state, block_s
     int32 [num_blocks]; free_state: int32 [2]. cache_len and free_state are
     updated in place unless cache_len_out or free_state_out is given. total
     (the size of the packed batch) is needed when slots is not passed in.
+    Whether every request got its blocks (FA_OK, FA_ERR_NO_BLOCKS or
+    FA_ERR_INVALID_ARG) is read by get_status(ws), which waits for the stream:
+    pass ws (a cache's `status`), as nothing reads a workspace of the call's
+    own. On the device a refused request's tokens have slot -1; cu_seqlens
+    lists them all the same, and forward_paged takes them for the last tokens
+    that the cache holds.
     Returns (cu_seqlens int32 [B + 1], slots int32 [total])."""
     lib = load()
     _check_device(new_len)
