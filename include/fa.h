@@ -212,6 +212,13 @@ fa_status fa_decode(const void* q, const void* k, const void* v, void* o, float*
  * entry that is no block: tokens that would go there get slot -1, but the
  * entry, the length and the list are carried on as if it were one (fa_fwd_paged
  * then reports the request as well), so after that the lists want rebuilding.
+ * A request's blocks are known by its length alone, ceil(cache_len /
+ * block_size) entries of its row. To take tokens back (rejected drafts), lower
+ * cache_len between calls; where that number of blocks falls, first put the
+ * entries behind it at the back of the ring, or they are lost to it:
+ * free_blocks[(head + count) % num_blocks] = entry, count + 1, for each. The
+ * rows taken back are written again by later appends; a block's scale stays
+ * what its taken-back rows made it until a run starts the block anew.
  * With separate outputs a call may be repeated with the same result.
  * B <= 16384, total <= 2^30. Runs one kernel.
  */
