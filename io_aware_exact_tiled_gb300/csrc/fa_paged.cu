@@ -37,8 +37,8 @@
 //   * S^T = K Q^T and O^T = V^T P^T as m16n8k16 products with f16 operands
 //     and fp32 sums, keys respectively head columns along M, the query rows
 //     along N: eight rows cost no more than one. E4M3 converts to f16 exactly,
-//     and Q does up to 2^-25 of its row's maximum after a power of two is
-//     taken out of each row. The k index of either product may be permuted
+//     and so does Q down to 2^-31 of its row's maximum (within 2^-39 of it
+//     below) after a power of two is taken out of each row. The k index of either product may be permuted
 //     freely: K rows are read sixteen bytes a lane as they lie, and V's bytes
 //     of two keys are interleaved by a byte permute; the permutations are
 //     chosen so that no read of the 128-byte-swizzled tiles meets a bank
@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
                 top = max(top, a < 0x7F80u ? a : 0u);
             }
             top = __reduce_max_sync(0xffffffffu, top);
-            const int e = top >> 7 ? min(max(static_cast<int>(top >> 7) - 127, -120), 120) : 0;
+            const int e = top >> 7 ? min(max(static_cast<int>(top >> 7) - 141, -120), 120) : 0;
             const float f = exp2i(-e);
             if (lane < D / 4) {
                 const int half = lane >> 4, tq = (lane >> 2) & 3, kk = half * 4 + (lane & 3);

@@ -27,11 +27,17 @@
 //   8-11   softmax of row tile 1
 //   12-15  convert V to f16: thread = key
 //
-// S = Q K^T runs on E4M3 operands, two products instead of one of f16: each
-// row of Q, divided by a power of two, is the sum of two E4M3 numbers (four
-// bits each of bfloat16's eight; exact down to 2^-10 of the row's maximum,
-// within 2^-17 of it below). Two E4M3 products cost what one f16 product costs,
-// and K needs no conversion and half the shared memory.
+// S = Q K^T runs on 8-bit operands: each row of Q, divided by a power of two,
+// is the sum of two numbers, in E5M2 (three of bfloat16's eight bits) and E4M3
+// (the other five, one of them by its sign). Both hold an element exactly down
+// to 2^-13 of the row's largest (E4M3 ends there); a row with more than an eighth
+// of its elements below that, or that leaves out more than 2^-20 of its largest,
+// summed over its elements, makes its row tile wide: then Q is three numbers in E5M2, exact down to 2^-23 and within 2^-31 of the
+// largest below. Two 8-bit products cost what one f16 product costs, and K needs
+// no conversion and half the shared memory; three cost a third more tensor time
+// in S. Measured, rows of normal values and the same with a channel 4,096 times
+// larger: pieces of prompts 789 and 891 us at d = 128, 690 and 714 at d = 64;
+// prompts 152 and 211, 97 and 125 us (a wide row is split twice).
 // O += P V runs on f16: V's numbers convert exactly, P keeps 11 bits.
 // Block scales: ks multiplies the exponent's slope and log2(vs) is added to
 // the exponent, so P holds 2^(s - mu) vs; mu follows the largest of these
@@ -55,15 +61,22 @@ constexpr float kPtSpan = 60.0f;    // log2 of the largest ratio of V's block sc
 template <int D>
 constexpr int kPtUnitCost = D == 64 ? 6 : 8;
 constexpr int kPtScaleSlots = 8;
+constexpr uint32_t kFmtE5M2 = 1;  // kind::f8f6f4 operand format code
 constexpr int kPtNanSlots = 4;
 
 template <int D>
 struct PtCfg {
-    static constexpr int KS = D == 128 ? 3 : 6;   // K stages
-    static constexpr int RS = D == 128 ? 2 : 4;   // stages of V as it lies in the cache
+    // K stages, and stages of V as it lies in the cache (d = 128, where the third
+    // part of Q takes their room: 795 us for pieces of prompts with three and two
+    // stages and Q's two parts alone, 793 with these)
+    static constexpr int KS = D == 128 ? 2 : 6;
+    static constexpr int RS = D == 128 ? 1 : 4;
     static constexpr int VS = 2;                  // stages of converted V
     static constexpr int NREG = D / 64;           // 128-byte-wide regions of an f16 row
-    static constexpr int Q_BYTES = D == 128 ? 32768 : 16384;  // high and low parts of a row tile
+    // the three parts of a row tile's Q: rows of 128 bytes, d = 64: the first
+    // two parts side by side, the third in rows of its own
+    static constexpr int Q_BYTES = D == 128 ? 49152 : 32768;
+    __host__ __device__ static constexpr int q_part(int part) { return D == 128 ? part * 16384 : part == 2 ? 16384 : part * 64; }
     static constexpr int K_BYTES = 128 * D;
     static constexpr int V_BYTES = 128 * D * 2;
     static constexpr int Q_OFF = 0;
@@ -80,7 +93,10 @@ struct PtCfg {
     static constexpr int COL_S = 0, COL_O = 256;
     static constexpr bool P_OVER_S = D == 128;
     static constexpr int COL_P = P_OVER_S ? COL_S : COL_O + 64, P_STRIDE = P_OVER_S ? 64 : 32;
-    static constexpr uint32_t ID_S = idesc_make(128, 64, kFmtE4M3, false, false);
+    // S = Q K^T of a part of Q in E5M2 or E4M3, and K in E4M3
+    __host__ __device__ static constexpr uint32_t id_s(bool e5m2) {
+        return idesc_make(128, 64, kFmtE4M3, false, false) | (e5m2 ? kFmtE5M2 << 7 : 0u);
+    }
     static constexpr uint32_t ID_PV = idesc_make(128, D, 0 /* f16 */, false, true);
     static_assert(SMEM <= 232448 - 2048, "shared memory");
 };
@@ -127,10 +143,40 @@ __device__ __forceinline__ uint32_t pt_pack_f16x2(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+__device__ __forceinline__ uint32_t pt_e5m2x2_from_f16x2(uint32_t x) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
+    return r;
+}
+// An E5M2 number is the upper byte of the f16 number of the same value.
+__device__ __forceinline__ uint32_t pt_f16x2_from_e5m2x2(uint32_t x) { return __byte_perm(x, 0u, 0x1404); }
 __device__ __forceinline__ uint32_t pt_e4m3x2_from_f16x2(uint32_t x) {
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
     return r;
+}
+__device__ __forceinline__ uint32_t pt_add_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// 1 or 0 for each half of |a| < b.
+__device__ __forceinline__ uint32_t pt_below_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("{\n\t.reg .b32 t;\n\tabs.f16x2 t, %1;\n\tset.lt.f16x2.f16x2 %0, t, %2;\n\t}" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// Two bf16 numbers times f, as an f16 pair.
+__device__ __forceinline__ uint32_t pt_scaled_f16x2(uint32_t v, float f) {
+    return pt_pack_f16x2(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xFFFF0000u) * f);
+}
+// Sum of the two halves of an f16 pair.
+__device__ __forceinline__ float pt_sum_f16x2(uint32_t x) {
+    float r, t;
+    asm("{\n\t.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+        : "=f"(r), "=f"(t)
+        : "r"(x));
+    return r + t;
 }
 __device__ __forceinline__ uint32_t pt_sub_f16x2(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -161,6 +207,89 @@ __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, 
 __device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t sbo) {
     return (sdesc_sw128(saddr, 16, sbo) & ~(7ull << 61)) | (4ull << 61);
 }
+
+// Q's row r, times f, as parts whose sum it is, into a row tile's buffer: two
+// (E5M2, E4M3), or in a wide row tile three (E5M2 each). Returns how many
+// elements are below 2^-2, the only ones that two parts may not hold exactly.
+template <int D, bool WIDE>
+__device__ __forceinline__ float pt_split_q(const uint4 (&x)[D / 8], float f, uint8_t* qb, int r) {
+    using C = PtCfg<D>;
+    uint32_t small = 0u;  // f16 pair
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) {
+        const uint32_t w[8] = {x[2 * j].x,     x[2 * j].y,     x[2 * j].z,     x[2 * j].w,
+                               x[2 * j + 1].x, x[2 * j + 1].y, x[2 * j + 1].z, x[2 * j + 1].w};
+        uint32_t part[3][4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            uint32_t b[3][2];
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                // exact in f16 down to 2^-24
+                uint32_t a = pt_scaled_f16x2(w[2 * y + z], f);
+                if constexpr (!WIDE) small = pt_add_f16x2(small, pt_below_f16x2(a, 0x34003400u));
+                b[0][z] = pt_e5m2x2_from_f16x2(a);
+                a = pt_sub_f16x2(a, pt_f16x2_from_e5m2x2(b[0][z]));
+                if constexpr (WIDE) {
+                    b[1][z] = pt_e5m2x2_from_f16x2(a);
+                    b[2][z] = pt_e5m2x2_from_f16x2(pt_sub_f16x2(a, pt_f16x2_from_e5m2x2(b[1][z])));
+                } else {
+                    b[1][z] = pt_e4m3x2_from_f16x2(a);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < (WIDE ? 3 : 2); ++k) part[k][y] = __byte_perm(b[k][0], b[k][1], 0x5410);
+        }
+#pragma unroll
+        for (int k = 0; k < (WIDE ? 3 : 2); ++k) {
+            const int c = D == 64 && k == 1 ? j + 4 : j;  // 16-byte piece of the row
+            const int at = (D == 128 || k == 2 ? C::q_part(k) : 0) + r * 128 + ((c ^ (r & 7)) << 4);
+            sts128(smem_u32(qb + at), part[k][0], part[k][1], part[k][2], part[k][3]);
+        }
+    }
+    return pt_sum_f16x2(small);
+}
+
+// Whether two parts hold a row of Q, times f: what they leave out is 2^-9 at
+// most, summed over the elements, and no more than an eighth of these is small
+// (where a few large elements stand above the others, all may hang on those).
+template <int D>
+__device__ __noinline__ bool pt_two_parts_hold(const uint16_t* row, float f) {
+    float left = 0.f;
+    int small = 0;
+#pragma unroll 4
+    for (int j = 0; j < D / 8; ++j) {
+        const uint4 x = reinterpret_cast<const uint4*>(row)[j];
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            const uint32_t a = pt_scaled_f16x2(w[y], f);
+            const uint32_t b = pt_sub_f16x2(a, pt_f16x2_from_e5m2x2(pt_e5m2x2_from_f16x2(a)));
+            const uint32_t lo = w[y] & 0x7FFFu, hi = (w[y] >> 16) & 0x7FFFu;
+            const uint32_t less = pt_below_f16x2(a, 0x34003400u);  // 1 is 0x3C00
+            small += (lo && (less & 0xFFFFu)) + (hi && (less >> 16));
+            left += pt_sum_f16x2(pt_sub_f16x2(b, pt_f16x2_from_e4m3x2(pt_e4m3x2_from_f16x2(b))) & 0x7FFF7FFFu);
+        }
+    }
+    return left <= 0x1p-9f && small <= D / 8;
+}
+
+// A function of its own: few row tiles take it, and the roles' loops compete
+// for the instruction cache.
+template <int D>
+__device__ __noinline__ void pt_split_q_wide(const uint16_t* row, float f, uint8_t* qb, int r) {
+    uint4 x[D / 8];
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j) x[j] = row ? reinterpret_cast<const uint4*>(row)[j] : make_uint4(0u, 0u, 0u, 0u);
+    pt_split_q<D, true>(x, f, qb, r);
+}
+
+struct PtWide {
+    static constexpr bool value = true;
+};
+struct PtNarrow {
+    static constexpr bool value = false;
+};
 
 struct PtReq {
     int b, n, len, tok0;
@@ -208,7 +337,7 @@ __global__ void __launch_bounds__(512, 1)
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ long long scan_w[16], scan_u[16];
     __shared__ long long start_line;
-    __shared__ int start_b, start_units, abort_s, last_s[2], nan_piece[kPtNanSlots];
+    __shared__ int start_b, start_units, abort_s, last_s[2], nan_piece[kPtNanSlots], wide_s[2];
     __shared__ uint32_t tmem_slot;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -474,16 +603,16 @@ __global__ void __launch_bounds__(512, 1)
             const uint32_t tm0 = uniform(tm) + i * 128;
             int u = 0, nseg = 0, np = 0;  // tiles walked, pieces with work, tiles of P multiplied
             bool ok = true;
-            do {
-                // warp-uniform in the compiler's eyes too, so that descriptors and
-                // TMEM addresses stay in uniform registers
-                const int c0 = uniform(s.c0), c1 = uniform(s.c1), end = uniform(half_end(s, i));
+            // The tiles [c0, c1) of a piece, of which row tile i takes part in
+            // those up to `end`; one loop for each form of Q, so that neither
+            // tests it between its products.
+            auto walk = [&](auto form, int c0, int c1, int end) {
+                constexpr bool kWide = decltype(form)::value;
                 for (int t = c0; t <= c1; ++t, ++u) {
                     const int st = u % C::KS, vs = (u - 1) % C::VS;
                     const uint64_t vd = sdesc_advance(dV, vs * C::V_BYTES), kd = sdesc_advance(dK, st * C::K_BYTES);
                     if (t < c1 && !(ok = wait_warp(&k_full[st], (u / C::KS) & 1))) break;
                     if (t > c0 && !(ok = wait_warp(&v_full[vs], ((u - 1) / C::VS) & 1))) break;
-                    if (t == c0 && t < end && !(ok = wait_warp(&q_full[i], nseg & 1))) break;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t tS = tm0 + C::COL_S + h * 64, tO = tm0 + C::COL_O;
@@ -505,13 +634,12 @@ __global__ void __launch_bounds__(512, 1)
                             if (C::P_OVER_S && t > c0 && !(ok = wait_warp(&pv_done[2 * i + h], np & 1))) break;
                             tc_fence_after();
 #pragma unroll
-                            for (int part = 0; part < 2; ++part)
+                            for (int part = 0; part < (kWide ? 3 : 2); ++part)
 #pragma unroll
                                 for (int kk = 0; kk < D / 32; ++kk)
-                                    umma_ss_f8(leader, tS,
-                                               sdesc_advance(dQ, (D == 128 ? part * 16384 : part * 64) + kk * 32),
-                                               sdesc_advance(kd, h * (C::K_BYTES / 2) + kk * 32), C::ID_S,
-                                               part || kk ? 1u : 0u);
+                                    umma_ss_f8(leader, tS, sdesc_advance(dQ, C::q_part(part) + kk * 32),
+                                               sdesc_advance(kd, h * (C::K_BYTES / 2) + kk * 32),
+                                               C::id_s(kWide || part == 0), part || kk ? 1u : 0u);
                             umma_commit(leader, &s_full[2 * i + h]);
                         }
                     }
@@ -522,6 +650,14 @@ __global__ void __launch_bounds__(512, 1)
                     np += t > c0 && t <= end;
                 }
                 --u;  // the last round had no tile of its own
+            };
+            do {
+                // warp-uniform in the compiler's eyes too, so that descriptors and
+                // TMEM addresses stay in uniform registers
+                const int c0 = uniform(s.c0), c1 = uniform(s.c1), end = uniform(half_end(s, i));
+                if (end > c0 && !(ok = wait_warp(&q_full[i], nseg & 1))) break;
+                if (end > c0 && uniform(wide_s[i])) walk(PtWide{}, c0, c1, end);
+                else walk(PtNarrow{}, c0, c1, end);
                 if (!ok) break;
                 nseg += end > c0;
             } while (__any_sync(0xffffffffu, next(s)));
@@ -548,56 +684,35 @@ __global__ void __launch_bounds__(512, 1)
             const size_t qrow = (static_cast<size_t>(s.r.tok0 + tok) * p.Hq + hq) * D;
             float rc = 0.f, mu = -CUDART_INF_F, l = 0.f;
             if (end > s.c0) {
-                // ---- Q: the row's power of two, then its high and low E4M3 parts
+                // ---- Q: the row's power of two, then its parts
                 uint4 x[D / 8];
 #pragma unroll
                 for (int j = 0; j < D / 8; ++j)
                     x[j] = row_ok ? reinterpret_cast<const uint4*>(p.q + qrow)[j] : make_uint4(0u, 0u, 0u, 0u);
-                uint32_t top = 0;
-                bool wild = false;  // an infinity or a NaN
+                uint32_t m2 = 0;  // bf16 bits, ordered like the magnitudes, both halves of a word at once
 #pragma unroll
-                for (int j = 0; j < D / 8; ++j) {
-                    const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const uint32_t a = w[y] & 0x7FFFu, b = (w[y] >> 16) & 0x7FFFu;
-                        wild |= a >= 0x7F80u || b >= 0x7F80u;
-                        top = max(top, max(a, b));
-                    }
-                }
-                // largest magnitude to [2^7, 2^8): high parts up to 256, low parts up to 8
-                const int e = top >> 7 && !wild ? min(max(static_cast<int>(top >> 7) - 134, -120), 120) : 0;
+                for (int j = 0; j < D / 8; ++j)
+                    m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(x[j].x & 0x7FFF7FFFu, x[j].y & 0x7FFF7FFFu),
+                                               __vmaxu2(x[j].z & 0x7FFF7FFFu, x[j].w & 0x7FFF7FFFu)));
+                const uint32_t top = max(m2 & 0xFFFFu, m2 >> 16);
+                const bool wild = top >= 0x7F80u;  // an infinity or a NaN
+                // largest magnitude to [2^11, 2^12), two parts: what is not below
+                // 2^-2 is exact, what is leaves out 2^-10 at most
+                const int e0 = top >> 7 && !wild ? static_cast<int>(top >> 7) - 138 : 0;
+                int e = min(max(e0, -120), 120);
                 const float f = exp2i(-e);
-                rc = wild ? CUDART_NAN_F : p.scale_log2 * exp2i(e);  // such a row has no finite result
-#pragma unroll
-                for (int j = 0; j < D / 16; ++j) {
-                    const uint32_t w[8] = {x[2 * j].x,     x[2 * j].y,     x[2 * j].z,     x[2 * j].w,
-                                           x[2 * j + 1].x, x[2 * j + 1].y, x[2 * j + 1].z, x[2 * j + 1].w};
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        uint32_t h[2], l[2];
-#pragma unroll
-                        for (int z = 0; z < 2; ++z) {
-                            const uint32_t v = w[2 * y + z];
-                            // exact in f16 down to 2^-24
-                            const uint32_t a = pt_pack_f16x2(__uint_as_float(v << 16) * f,
-                                                             __uint_as_float(v & 0xFFFF0000u) * f);
-                            h[z] = pt_e4m3x2_from_f16x2(a);
-                            l[z] = pt_e4m3x2_from_f16x2(pt_sub_f16x2(a, pt_f16x2_from_e4m3x2(h[z])));
-                        }
-                        hi[y] = __byte_perm(h[0], h[1], 0x5410);
-                        lo[y] = __byte_perm(l[0], l[1], 0x5410);
-                    }
-                    if constexpr (D == 128) {
-                        const uint32_t at = r * 128 + ((j ^ (r & 7)) << 4);
-                        sts128(smem_u32(qb + at), hi[0], hi[1], hi[2], hi[3]);
-                        sts128(smem_u32(qb + 16384 + at), lo[0], lo[1], lo[2], lo[3]);
-                    } else {
-                        sts128(smem_u32(qb + r * 128 + ((j ^ (r & 7)) << 4)), hi[0], hi[1], hi[2], hi[3]);
-                        sts128(smem_u32(qb + r * 128 + (((j + 4) ^ (r & 7)) << 4)), lo[0], lo[1], lo[2], lo[3]);
-                    }
+                // a row of few small elements leaves out little for certain
+                // (zeros count as small here)
+                const bool few = pt_split_q<D, false>(x, f, qb, r) <= 2.f || !row_ok || wild;
+                const bool fits = few || pt_two_parts_hold<D>(p.q + qrow, f);
+                __syncwarp();
+                const bool wide = !named_all(1 + i, 128, fits);
+                if (wide) {  // [2^14, 2^15), three
+                    e = min(max(e0 - 3, -120), 120);
+                    pt_split_q_wide<D>(row_ok ? p.q + qrow : nullptr, exp2i(-e), qb, r);
                 }
+                if (r == 0) wide_s[i] = wide;
+                rc = wild ? CUDART_NAN_F : p.scale_log2 * exp2i(e);  // such a row has no finite result
                 fence_proxy_async_smem();
                 mbar_arrive(&q_full[i]);
             }
