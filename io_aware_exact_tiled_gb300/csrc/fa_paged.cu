@@ -518,12 +518,10 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
             const uint32_t h4[4] = {x.x & 0xFFFFu, x.x >> 16, x.y & 0xFFFFu, x.y >> 16};
             uint32_t top = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t a = h4[i] & 0x7FFFu;
-                top = max(top, a < 0x7F80u ? a : 0u);
-            }
+            for (int i = 0; i < 4; ++i) top = max(top, h4[i] & 0x7FFFu);
             top = __reduce_max_sync(0xffffffffu, top);
-            const int e = top >> 7 ? min(max(static_cast<int>(top >> 7) - 141, -120), 120) : 0;
+            const bool wild = top >= 0x7F80u;  // an infinity or a NaN: the row has no finite result
+            const int e = top >> 7 && !wild ? min(max(static_cast<int>(top >> 7) - 141, -120), 120) : 0;
             const float f = exp2i(-e);
             if (lane < D / 4) {
                 const int half = lane >> 4, tq = (lane >> 2) & 3, kk = half * 4 + (lane & 3);
@@ -533,7 +531,9 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
                 *reinterpret_cast<uint2*>(qs + (((r >> 3) * (C::KK / 2) + (kk >> 1)) * 32 + 4 * (r & 7) + tq) * 16 +
                                           (kk & 1) * 8) = y;
             }
-            if (lane == 0) rowc[r] = make_float2(p.scale_log2 * exp2i(e), __int_as_float(r < nrow ? visible(tok) : cs.len));
+            if (lane == 0)
+                rowc[r] = make_float2(wild ? CUDART_NAN_F : p.scale_log2 * exp2i(e),
+                                      __int_as_float(r < nrow ? visible(tok) : cs.len));
         }
         if (cs.alone) __syncwarp();
         else __syncthreads();
