@@ -275,15 +275,17 @@ fa_status fa_cache_append(const void* k, const void* v, void* k_cache, void* v_c
  * and table entries that are no block are reported as FA_ERR_INVALID_ARG by
  * fa_get_status; the rows they touch are then invalid. Hq a multiple of Hkv,
  * d in {64, 128}, num_blocks * Hkv * block_size < 2^31.
+ * Requests that bring a few tokens each (drafts) run faster in a call of their
+ * own than beside a prompt; single tokens do not mind.
  * Numerics: scores, maxima, sums and outputs are kept in fp32. Q enters the
  * scores exactly down to 2^-13 of its row's maximum; of what is smaller, 2^-20
  * of the maximum may be left out of a row in all, or 2^-31 of it of an element
- * where more than an eighth of the row is smaller. The
- * weights are rounded to fp16 (2^-11) before they meet V; one below 2^-30 of
- * its row's largest vanishes, where weights of more rows than a tile of few
- * rows takes (32 at d = 64, 24 at d = 128) are compared with their blocks'
- * v_scale in them. v_scale of the tokens that a row sees should lie within
- * 2^20 of one another, and above 2^-100, for that to be out of sight.
+ * where more than an eighth of the row is smaller. Weights are rounded to fp16
+ * before they meet V, relative to the row's largest: 2^-11 down to 2^-20 of it,
+ * and nothing is left below 2^-30. Requests of more rows (new tokens x heads of
+ * a group; 32 at d = 64, 24 at d = 128) have v_scale in the weights then. So the
+ * v_scale of the tokens that a row sees should lie within 2^20 of one another
+ * and above 2^-100; blocks of zeros may have any.
  */
 size_t fa_fwd_paged_workspace_size(int B, int Hq, int Hkv, int total, int max_new, int d);
 fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,

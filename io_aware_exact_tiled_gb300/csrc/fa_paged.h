@@ -72,10 +72,13 @@ inline bool paged_has_tiles(int max_new, int group, int d) {
 }
 // Rows up to which a request of this call is the split-key kernel's, the height
 // of its tile: what the longest request has, or, where that one is the row-tile
-// kernel's, what one new token has. A batch with a prompt in it is mostly
-// decoding otherwise, and a taller tile than their rows need slows those
-// requests down (64 requests of 8,000 tokens, 4 rows each: 115 us in a tile of
-// eight rows, 223 in one of 32 at d = 64).
+// kernel's, what one new token has, as the host knows no more. A batch with a
+// prompt in it is mostly decoding otherwise, and a taller tile than their rows
+// need slows those requests down (a prompt of 2,000 tokens beside 63 requests of
+// 8,000 tokens, one new token each, 4 rows: 170 us in a tile of eight rows, 274
+// in one of 32 at d = 64; 254 and 334 at d = 128). Requests of a few tokens
+// beside a prompt pay for it (three each, 12 rows: 351 us in the row-tile kernel,
+// 276 in a tile of 32; 437 and 341): they are better off in a call of their own.
 inline int paged_split_rows(int max_new, int group, int d) {
     const int rows = paged_has_tiles(max_new, group, d) ? group : max_new * group;
     return ((rows < paged_max_rows(d) ? rows : paged_max_rows(d)) + 7) / 8 * 8;
@@ -107,6 +110,17 @@ inline cudaError_t once_per_device(std::atomic<uint64_t>& done, F&& set) {
 __device__ __forceinline__ long long div_short(long long x, long long d) {
     if (((x | d) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(d);
     return x / d;
+}
+// Two E4M3 numbers (low 16 bits) to an f16 pair, exactly.
+__device__ __forceinline__ uint32_t f16x2_from_e4m3x2(uint32_t x) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 #endif
 

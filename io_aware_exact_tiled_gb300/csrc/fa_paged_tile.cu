@@ -133,16 +133,6 @@ __device__ __forceinline__ bool named_all(int id, int threads, bool v) {
         : "memory");
     return r != 0;
 }
-__device__ __forceinline__ uint32_t pt_f16x2_from_e4m3x2(uint32_t x) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(x));
-    return r;
-}
-__device__ __forceinline__ uint32_t pt_pack_f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 __device__ __forceinline__ uint32_t pt_e5m2x2_from_f16x2(uint32_t x) {
     uint16_t r;
     asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
@@ -168,7 +158,7 @@ __device__ __forceinline__ uint32_t pt_below_f16x2(uint32_t a, uint32_t b) {
 }
 // Two bf16 numbers times f, as an f16 pair.
 __device__ __forceinline__ uint32_t pt_scaled_f16x2(uint32_t v, float f) {
-    return pt_pack_f16x2(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xFFFF0000u) * f);
+    return pack_f16x2(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xFFFF0000u) * f);
 }
 // Sum of the two halves of an f16 pair.
 __device__ __forceinline__ float pt_sum_f16x2(uint32_t x) {
@@ -268,7 +258,7 @@ __device__ __noinline__ bool pt_two_parts_hold(const uint16_t* row, float f) {
             const uint32_t lo = w[y] & 0x7FFFu, hi = (w[y] >> 16) & 0x7FFFu;
             const uint32_t less = pt_below_f16x2(a, 0x34003400u);  // 1 is 0x3C00
             small += (lo && (less & 0xFFFFu)) + (hi && (less >> 16));
-            left += pt_sum_f16x2(pt_sub_f16x2(b, pt_f16x2_from_e4m3x2(pt_e4m3x2_from_f16x2(b))) & 0x7FFF7FFFu);
+            left += pt_sum_f16x2(pt_sub_f16x2(b, f16x2_from_e4m3x2(pt_e4m3x2_from_f16x2(b))) & 0x7FFF7FFFu);
         }
     }
     return left <= 0x1p-9f && small <= D / 8;
@@ -703,7 +693,7 @@ __global__ void __launch_bounds__(512, 1)
                 const float f = exp2i(-e);
                 // a row of few small elements leaves out little for certain
                 // (zeros count as small here)
-                const bool few = pt_split_q<D, false>(x, f, qb, r) <= 2.f || !row_ok || wild;
+                const bool few = pt_split_q<D, false>(x, f, qb, r) <= 2.f || top == 0 || wild;
                 const bool fits = few || pt_two_parts_hold<D>(p.q + qrow, f);
                 __syncwarp();
                 const bool wide = !named_all(1 + i, 128, fits);
@@ -778,7 +768,7 @@ __global__ void __launch_bounds__(512, 1)
                         float y0, y1;
                         f2_split(f2_fma(f2_make(__uint_as_float(v[0]), __uint_as_float(v[1])), cc, aa), y0, y1);
                         const float e0 = ex2_approx(y0), e1 = ex2_approx(y1);
-                        pk[gr * 8 + k] = pt_pack_f16x2(e0, e1);
+                        pk[gr * 8 + k] = pack_f16x2(e0, e1);
                         sum = f2_add(sum, f2_make(e0, e1));
                     }
                     float a, b;
@@ -986,8 +976,8 @@ __global__ void __launch_bounds__(512, 1)
                     uint32_t h[8];
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
-                        h[2 * y] = pt_f16x2_from_e4m3x2(w[y]);
-                        h[2 * y + 1] = pt_f16x2_from_e4m3x2(w[y] >> 16);
+                        h[2 * y] = f16x2_from_e4m3x2(w[y]);
+                        h[2 * y + 1] = f16x2_from_e4m3x2(w[y] >> 16);
                     }
                     uint8_t* reg = vb + (j >> 2) * 16384;
                     const int c = (j & 3) * 2;
