@@ -234,7 +234,8 @@ fa_status fa_cache_plan(const int32_t* new_len, const int32_t* cache_len, int32_
  * where that is larger; a run of new rows that starts in the block's row 0
  * ignores the scale so far. Rows in front of the run are moved to the new
  * scale (exact but for numbers below the smallest normal E4M3 number, 2^-6 of
- * the new scale); rows behind it are left as they are. Values are divided by the scale
+ * the new scale; from a scale of the caller's that is no power of two, fp32
+ * products are rounded); rows behind it are left as they are. Values are divided by the scale
  * (exactly) and rounded to E4M3 (nearest even); infinities become +-448 times
  * the scale, NaN stays NaN.
  *   k, v              in,  device, token-major [total, H, d] bf16

@@ -803,6 +803,11 @@ __global__ void __launch_bounds__(512, 1)
             if (ok) ok = wait_warp(&nan_full[seg % kPtNanSlots], (seg / kPtNanSlots) & 1);
             // the row tile's warps leave together, so that none waits for the others below
             if (!(ok = named_all(1 + i, 128, ok))) break;
+            if (base >= rows) {  // no rows: nothing to write or to merge, in no piece of the unit
+                mbar_arrive(&nan_empty[seg % kPtNanSlots]);
+                ++seg;
+                continue;
+            }
             tc_fence_after();
             const unsigned long long* nf = nan_first + (seg % kPtNanSlots) * D;
             const uint32_t nan_tag = pt_nan_tag(seg);
