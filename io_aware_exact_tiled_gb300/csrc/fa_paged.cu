@@ -12,11 +12,11 @@
 // What has to be kept off that path is the conversion of the bytes and the
 // wait for the block table in front of each copy. Measured, d = 128, one token
 // for each request, against a copy's 6,766 GB/s: 16 requests of 8,192 to 16,383
-// tokens, 32 key heads, 254 us = 6,590 GB/s of cache; 64 requests of 1 to 16,384
-// tokens, 8 key heads, 193 us = 5,950; one request of 262,001 tokens, 98 us =
-// 5,480. At d = 64, or with more rows, the issue slots bound it: 64 requests of
-// 8,000 tokens, 8 key heads, 8 / 16 / 24 / 32 rows: 115 / 146 / 191 / 232 us
-// (bytes alone: 77), d = 128 171 / 211 / 267 us (155).
+// tokens, 32 key heads, 252 us = 6,630 GB/s of cache; 64 requests of 1 to 16,384
+// tokens, 8 key heads, 193 us = 5,950; one request of 262,001 tokens, 96 us =
+// 5,590. At d = 64, or with more rows, the issue slots bound it: 64 requests of
+// 8,000 tokens, 8 key heads, 8 / 16 / 24 / 32 rows: 115 / 148 / 191 / 231 us
+// (bytes alone: 77), d = 128 170 / 215 / 266 us (155).
 //
 // Design:
 //   * Work is counted in chunks of 32 keys. A unit is (request, key head), with

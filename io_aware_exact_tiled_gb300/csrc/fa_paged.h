@@ -63,7 +63,7 @@ struct PagedArgs {
 
 // Query rows (new tokens x heads of a group) up to which a request can be the
 // split-key kernel's. Above 24 rows of d = 128 its registers do not hold O (64
-// requests of 8,000 tokens: 479 us with 32 rows, 374 with 64 rows in the
+// requests of 8,000 tokens, 32 rows: 479 us there, 332 to 342 in the
 // row-tile kernel); at d = 64 they do (232 us and 290).
 inline int paged_max_rows(int d) { return d == 64 ? 32 : 24; }
 // Whether a request of max_new new tokens goes to the row-tile kernel.

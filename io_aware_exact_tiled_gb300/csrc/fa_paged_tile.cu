@@ -4,10 +4,10 @@
 // Same computation as fa_paged.cu. With hundreds of rows for each cached key
 // the time is that of the two products, 4 n len d flops for each query head.
 // Measured against 1,871 TFLOP/s of bf16 products: d = 128, two requests of
-// about 2,000 new tokens behind 15,000 to 16,384, 32 query heads, 803 us = 1,320
+// about 2,000 new tokens behind 15,000 to 16,384, 32 query heads, 789 us = 1,345
 // TFLOP/s (the chain of S, softmax and P V of two row tiles: the tensor pipe is
-// active 55 % of the time); d = 64, eight prompts of 314 to 1,967 tokens, 16
-// heads, 95 us = 262 TFLOP/s (a unit's start and end, and three times the
+// active 57 % of the time); d = 64, eight prompts of 314 to 1,967 tokens, 16
+// heads, 98 us = 255 TFLOP/s (a unit's start and end, and three times the
 // products' time for the softmax).
 //
 // Work: a unit is (request, key head, pair of row tiles); a row is (new token,
@@ -32,12 +32,13 @@
 // (the other five, one of them by its sign). Both hold an element exactly down
 // to 2^-13 of the row's largest (E4M3 ends there); a row with more than an eighth
 // of its elements below that, or that leaves out more than 2^-20 of its largest,
-// summed over its elements, makes its row tile wide: then Q is three numbers in E5M2, exact down to 2^-23 and within 2^-31 of the
-// largest below. Two 8-bit products cost what one f16 product costs, and K needs
-// no conversion and half the shared memory; three cost a third more tensor time
-// in S. Measured, rows of normal values and the same with a channel 4,096 times
-// larger: pieces of prompts 789 and 891 us at d = 128, 690 and 714 at d = 64;
-// prompts 152 and 211, 97 and 125 us (a wide row is split twice).
+// summed over its elements, makes its row tile wide: then Q is three numbers in
+// E5M2, exact down to 2^-23 and within 2^-31 of the largest below. Two 8-bit
+// products cost what one f16 product costs, and K needs no conversion and half
+// the shared memory; three cost half as much again. Measured, rows of normal
+// values and the same with a channel 4,096 times larger: pieces of prompts 789
+// and 891 us at d = 128, 690 and 714 at d = 64; prompts 152 and 211, 97 and 125
+// us (a wide row is split twice).
 // O += P V runs on f16: V's numbers convert exactly, P keeps 11 bits.
 // Block scales: ks multiplies the exponent's slope and log2(vs) is added to
 // the exponent, so P holds 2^(s - mu) vs; mu follows the largest of these
@@ -76,7 +77,9 @@ struct PtCfg {
     // the three parts of a row tile's Q: rows of 128 bytes, d = 64: the first
     // two parts side by side, the third in rows of its own
     static constexpr int Q_BYTES = D == 128 ? 49152 : 32768;
-    __host__ __device__ static constexpr int q_part(int part) { return D == 128 ? part * 16384 : part == 2 ? 16384 : part * 64; }
+    __host__ __device__ static constexpr int q_part(int part) {
+        return D == 128 ? part * 16384 : part == 2 ? 16384 : part * 64;
+    }
     static constexpr int K_BYTES = 128 * D;
     static constexpr int V_BYTES = 128 * D * 2;
     static constexpr int Q_OFF = 0;

@@ -2,6 +2,9 @@
 or has no room: that request keeps what it has, and the others are served."""
 
 import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -12,6 +15,8 @@ from oracle import paged as P
 from test_paged import PLAN_KEYS, make_plan, run_plan
 
 pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def refuse(x, b):
@@ -110,3 +115,22 @@ def test_large_plans_in_a_smaller_cluster(cuda_device, B, bs, len_hi, new_hi, re
     for k in PLAN_KEYS:
         np.testing.assert_array_equal(got[k], want[k], err_msg=k)
     assert status == (fb.FA_ERR_NO_BLOCKS if want["refused"] else fb.FA_OK)
+
+
+def test_a_large_plan_is_captured_as_a_process_first_call(cuda_device):
+    """What the first large plan asks the device is allowed under capture."""
+    code = """
+import torch, io_aware_exact_tiled_gb300 as fa
+c = fa.paged_cache(9000, 1, 16, 64, 4500, 2)
+new = torch.ones(4500, dtype=torch.int32, device="cuda")
+cu, slots = (torch.empty(n, dtype=torch.int32, device="cuda") for n in (4501, 4500))
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    fa.cache_plan(new, c.cache_len, c.block_table, c.free_blocks, c.free_state, 16, cu_seqlens=cu, slots=slots,
+                  ws=c.status)
+for _ in range(17):
+    g.replay()
+assert fa.get_status(c.status) == 0 and (c.cache_len == 17).all() and c.free_state.tolist() == [0, 0]
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
