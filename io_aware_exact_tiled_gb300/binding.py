@@ -418,9 +418,7 @@ def decode(q, k_cache, v_cache, cache_len=None, scale: Optional[float] = None, n
     return o, L
 
 
-class PagedCache(NamedTuple):
-    """The buffers of a paged 8-bit cache and of the requests it serves, as
-    cache_plan, cache_append and forward_paged take them."""
+class _PagedCacheBuffers(NamedTuple):
     k: torch.Tensor            # float8_e4m3fn [num_blocks, Hkv, block_size, d]
     v: torch.Tensor
     k_scale: torch.Tensor      # float32 [num_blocks, Hkv]
@@ -429,7 +427,13 @@ class PagedCache(NamedTuple):
     cache_len: torch.Tensor    # int32 [B]
     free_blocks: torch.Tensor  # int32 [num_blocks], a ring
     free_state: torch.Tensor   # int32 [2]: its head and count
-    status: torch.Tensor       # uint8 [256]: cache_plan's workspace, read by get_status
+
+
+class PagedCache(_PagedCacheBuffers):
+    """The buffers of a paged 8-bit cache and of the requests it serves, as
+    cache_plan, cache_append and forward_paged take them; and, beside the
+    tuple, `status` (uint8 [256]), cache_plan's workspace, read by get_status."""
+    status: Optional[torch.Tensor] = None
 
 
 def paged_cache(num_blocks: int, Hkv: int, block_size: int, d: int, B: int, max_blocks: int,
@@ -441,9 +445,10 @@ def paged_cache(num_blocks: int, Hkv: int, block_size: int, d: int, B: int, max_
     k, v = (torch.zeros((num_blocks, Hkv, block_size, d), dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
             for _ in range(2))
     ks, vs = (torch.zeros((num_blocks, Hkv), dtype=torch.float32, device=device) for _ in range(2))
-    return PagedCache(k, v, ks, vs, torch.full((B, max_blocks), -1, **i32), torch.zeros(B, **i32),
-                      torch.arange(num_blocks, **i32), torch.tensor([0, num_blocks], **i32),
-                      torch.zeros(256, dtype=torch.uint8, device=device))
+    cache = PagedCache(k, v, ks, vs, torch.full((B, max_blocks), -1, **i32), torch.zeros(B, **i32),
+                       torch.arange(num_blocks, **i32), torch.tensor([0, num_blocks], **i32))
+    cache.status = torch.zeros(256, dtype=torch.uint8, device=device)
+    return cache
 
 
 def cache_plan(new_len, cache_len, block_table, free_blocks, free_state, block_size: int,

@@ -21,6 +21,7 @@ def readme_step():
 def test_a_cache_comes_with_a_status_buffer():
     c = fa.paged_cache(4, 1, 16, 64, 2, 4, device="cpu")
     assert c.status.dtype == torch.uint8 and c.status.numel() == 256 and not c.status.any()
+    assert len(c) == 8 and c._fields[-1] == "free_state" and fa.PagedCache(*c).status is None
     assert "ws=c.status" in readme_step() and "get_status(c.status)" in readme_step()
 
 
