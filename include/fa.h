@@ -296,6 +296,118 @@ fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
                        size_t ws_bytes, void* stream);
 
 /*
+ * fa_fwd_paged for requests in groups, the requests of a group sharing a prefix
+ * that the cache holds once: the same instructions, document or conversation in
+ * front of each, or several answers sampled from one prompt. A request's new
+ * tokens see all of their group's prefix (causal or not), and of the request's
+ * own tokens what fa_fwd_paged lets them see; the softmax is over both.
+ *   prefix_cu     in,  device, int32 [P + 1]: group p is requests prefix_cu[p]
+ *                 .. prefix_cu[p+1] - 1, 0 <= prefix_cu[0] <= .. <=
+ *                 prefix_cu[P] <= B; requests in front of the first group and
+ *                 behind the last have no prefix
+ *   prefix_len    in,  device, int32 [P], tokens of the prefix (0: none)
+ *   prefix_table  in,  device, int32 [P, max_prefix_blocks], its blocks
+ *   workspace     fa_fwd_paged_prefix_workspace_size bytes
+ * cache_len and block_table are the requests' own tokens, without the prefix; a
+ * request may have no token of its own cached (cache_len 0). Blocks may be
+ * shared in any way. All else, what fa_get_status reports and the numerics
+ * included, is as for fa_fwd_paged; offsets, lengths and table entries of the
+ * prefixes are checked as those of the requests are. A prefix and a request's
+ * own tokens are taken apart: the limits on their v_scale are each one's own.
+ * Runs up to four kernels.
+ */
+size_t fa_fwd_paged_prefix_workspace_size(int B, int P, int Hq, int Hkv, int total, int max_new, int d);
+fa_status fa_fwd_paged_prefix(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                              const float* v_scale, void* o, float* lse, const int32_t* cu_seqlens,
+                              const int32_t* cache_len, const int32_t* block_table, const int32_t* prefix_cu,
+                              const int32_t* prefix_len, const int32_t* prefix_table, int B, int P, int Hq, int Hkv,
+                              int total, int max_new, int max_blocks, int max_prefix_blocks, int num_blocks,
+                              int block_size, int d, float scale, int causal, void* workspace, size_t ws_bytes,
+                              void* stream);
+
+/*
+ * Norm of queries and keys for each head, and rotation by position, in one pass
+ * ahead of the attention calls. For a head x of d elements at position s:
+ *
+ *   y = x / sqrt(mean(x^2) + eps) * weight           (no weight: y = x)
+ *   z = y with each pair (u, v) of its first `rot` elements turned by the angle
+ *       s * inv_freq[i]: (u cos - v sin, u sin + v cos)
+ *
+ * Pair i is elements (i, i + rot / 2), or (2 i, 2 i + 1) where `interleaved`.
+ *
+ * Heads are read and written where they lie, as a packed projection leaves
+ * them: fa_rows names rows of d contiguous elements at data + b * batch + h *
+ * head + n * token, strides in elements, the base 16-byte aligned and strides
+ * of dimensions longer than 1 non-negative multiples of 16 bytes. Rows of an
+ * output must not overlap one another; an output may be its own input (the same
+ * base and strides) and must not overlap an input otherwise.
+ *   q, q_out      [B, Hq, N] rows of `dtype` (FA_BF16 or FA_FP32)
+ *   k, k_out      [B, Hkv, N] rows
+ *   q_weight, k_weight  NULL or device [d] of `dtype`; NULL leaves out the norm
+ *                 of that tensor
+ *   eps           > 0
+ *   inv_freq      in,  device, double [rot / 2], finite, below 2^40 in size
+ *   rot           a multiple of 16, at most d
+ *   cu_seqlens    NULL: a dense batch, token n at position n. Else a packed
+ *                 batch: device, int32 [B + 1]; the rows are [heads, N] (batch
+ *                 strides unused, N tokens together), sequence b is tokens
+ *                 cu_seqlens[b] .. cu_seqlens[b+1] - 1, its first at position
+ *                 0. Tokens of no sequence are left as they are.
+ *   ends          NULL, or device, int32 [B]: the last token of sequence b (or
+ *                 of row b of a dense batch) is at position ends[b] - 1 and the
+ *                 others count back from it (cache_len behind fa_cache_plan;
+ *                 with a shared prefix, its length added)
+ * Products, sums and angles are in fp32, positions times frequencies in 64-bit
+ * fixed point (2^-33 of a turn at any position); one rounding to `dtype`. d in
+ * {64, 128}. Runs one kernel; no workspace.
+ */
+typedef struct {
+    void* data;
+    int64_t batch, head, token;
+} fa_rows;
+
+fa_status fa_qk_norm_rope(const fa_rows* q, const fa_rows* k, const fa_rows* q_out, const fa_rows* k_out,
+                          const void* q_weight, const void* k_weight, float eps, const double* inv_freq, int rot,
+                          int interleaved, const int32_t* cu_seqlens, const int32_t* ends, int B, int N, int Hq,
+                          int Hkv, int d, fa_dtype dtype, void* stream);
+
+/*
+ * Gradient of fa_qk_norm_rope: given its inputs and the gradients of its
+ * outputs, those of its inputs and of the weights.
+ *   q, k            in,  as for fa_qk_norm_rope (not read, and NULL allowed,
+ *                   where that tensor has no weight)
+ *   dq_out, dk_out  in,  gradients of q_out and k_out
+ *   dq, dk          out, gradients of q and k; may be dq_out and dk_out
+ *   dq_weight, dk_weight  out, device float32 [d], the sums over all heads and
+ *                   tokens; NULL where the weight is
+ *   workspace       fa_qk_norm_rope_bwd_workspace_size(d) bytes
+ * All else as for fa_qk_norm_rope. Tokens of no sequence have no gradient: their
+ * rows of dq and dk are left as they are. Sums are in fp32 in a fixed order:
+ * repeated calls agree bit by bit. Runs two kernels, one without weights.
+ */
+size_t fa_qk_norm_rope_bwd_workspace_size(int d);
+fa_status fa_qk_norm_rope_bwd(const fa_rows* q, const fa_rows* k, const fa_rows* dq_out, const fa_rows* dk_out,
+                              const fa_rows* dq, const fa_rows* dk, const void* q_weight, const void* k_weight,
+                              float* dq_weight, float* dk_weight, float eps, const double* inv_freq, int rot,
+                              int interleaved, const int32_t* cu_seqlens, const int32_t* ends, int B, int N, int Hq,
+                              int Hkv, int d, fa_dtype dtype, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * fa_qk_norm_rope and fa_cache_append in one pass over the new tokens of a
+ * serving step: q is normalised and rotated into q_out; k as well, rounded to
+ * bf16 and stored into its slots as fa_cache_append stores it; v is stored as
+ * it is. Packed batches of bf16 only ([heads, total] rows; batch strides
+ * unused). Tokens of no sequence are skipped, whatever their slots; tokens
+ * without a slot have their row of q_out all the same. Arguments as for the two
+ * calls, slots and their order included. Runs one kernel; no workspace.
+ */
+fa_status fa_qk_norm_rope_append(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows* q_out,
+                                 void* k_cache, void* v_cache, float* k_scale, float* v_scale, const int32_t* slots,
+                                 const void* q_weight, const void* k_weight, float eps, const double* inv_freq,
+                                 int rot, int interleaved, const int32_t* cu_seqlens, const int32_t* ends, int B,
+                                 int total, int Hq, int Hkv, int d, int num_blocks, int block_size, void* stream);
+
+/*
  * FP8 forward pass ("FlashAttention: making attention IO-aware", section
  * "FlashAttention-3": FP8 doubles the tensor rate but is fragile with
  * outliers, so Q and K are multiplied by a random orthogonal Hadamard matrix

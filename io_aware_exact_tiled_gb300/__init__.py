@@ -17,6 +17,12 @@ from .binding import (  # noqa: F401
     cache_append,
     forward_paged,
     fwd_paged_workspace_size,
+    forward_paged_prefix,
+    fwd_paged_prefix_workspace_size,
+    qk_norm_rope,
+    qk_norm_rope_append,
+    qk_norm_rope_backward,
+    qk_norm_rope_bwd_workspace_size,
     forward_fp8,
     forward_dropout,
     backward_dropout,

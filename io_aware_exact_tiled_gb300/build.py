@@ -19,7 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfa.so")
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd_t1.cu", "fa_bwd.cu", "fa_noalloc.cu", "fa_decode.cu", "fa_fwd_fp8.cu",
-           "fa_cache.cu", "fa_paged.cu", "fa_paged_tile.cu"]
+           "fa_cache.cu", "fa_paged.cu", "fa_paged_tile.cu", "fa_paged_prefix.cu", "fa_norm.cu", "fa_norm_append.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 

@@ -9,6 +9,7 @@
 #include "fa_decode.h"
 #include "fa_fp8.h"
 #include "fa_launch.h"
+#include "fa_norm.h"
 #include "fa_paged.h"
 
 namespace {
@@ -581,28 +582,35 @@ fa_status fa_cache_append(const void* k, const void* v, void* k_cache, void* v_c
     return FA_OK;
 }
 
-// Workspace of fa_fwd_paged: the status word and the counters of both kernels
-// (zeroed together), then the partial maxima, sums and outputs of the CTAs.
+// Workspace of a pass of the paged kernels: the counters of both (zeroed
+// together), then the partial maxima, sums and outputs of the CTAs.
 struct PagedWs {
-    size_t counters, tile_counters, zeroed;  // offsets; bytes to zero
+    size_t counters, tile_counters, zeroed;  // offsets; end of what is to be zeroed
     size_t pm, pl, po, tile_pm, tile_pl, tile_po, bytes;
 };
 
-static PagedWs paged_ws(int B, int Hq, int Hkv, int total, int max_new, int d) {
+static PagedWs paged_ws_counters(size_t at, int B, int Hkv, size_t units) {
     PagedWs w;
-    const size_t rows = 2 * static_cast<size_t>(fa::kPagedCtas) * fa::kPagedMaxRows;
-    const size_t units = static_cast<size_t>(fa::paged_max_tile_units(B, Hq, Hkv, total, max_new, d));
-    const size_t tile_rows = units ? 2 * static_cast<size_t>(fa::kPagedCtas) * fa::kPagedTileRows : 0;
-    w.counters = kStatusBytes;
+    w.counters = at;
     w.tile_counters = w.counters + align256(static_cast<size_t>(B) * Hkv * sizeof(int));
     w.zeroed = w.tile_counters + align256(2 * units * sizeof(int));
-    w.pm = w.zeroed;
+    return w;
+}
+static void paged_ws_partials(PagedWs& w, size_t at, size_t units, int d) {
+    const size_t rows = 2 * static_cast<size_t>(fa::kPagedCtas) * fa::kPagedMaxRows;
+    const size_t tile_rows = units ? 2 * static_cast<size_t>(fa::kPagedCtas) * fa::kPagedTileRows : 0;
+    w.pm = at;
     w.pl = w.pm + align256(rows * sizeof(float));
     w.po = w.pl + align256(rows * sizeof(float));
     w.tile_pm = w.po + align256(rows * d * sizeof(float));
     w.tile_pl = w.tile_pm + align256(tile_rows * sizeof(float));
     w.tile_po = w.tile_pl + align256(tile_rows * sizeof(float));
     w.bytes = w.tile_po + align256(tile_rows * d * sizeof(float));
+}
+static PagedWs paged_ws(int B, int Hq, int Hkv, int total, int max_new, int d) {
+    const size_t units = static_cast<size_t>(fa::paged_max_tile_units(B, Hq, Hkv, total, max_new, d));
+    PagedWs w = paged_ws_counters(kStatusBytes, B, Hkv, units);
+    paged_ws_partials(w, w.zeroed, units, d);
     return w;
 }
 
@@ -611,14 +619,9 @@ size_t fa_fwd_paged_workspace_size(int B, int Hq, int Hkv, int total, int max_ne
     return paged_ws(B, Hq, Hkv, total, max_new, d).bytes;
 }
 
-fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
-                       const float* v_scale, void* o, float* lse, const int32_t* cu_seqlens, const int32_t* cache_len,
-                       const int32_t* block_table, int B, int Hq, int Hkv, int total, int max_new, int max_blocks,
-                       int num_blocks, int block_size, int d, float scale, int causal, void* workspace,
-                       size_t ws_bytes, void* stream) {
-    if (!k_cache || !v_cache || !k_scale || !v_scale || !cu_seqlens || !cache_len || !block_table || !workspace)
-        return FA_ERR_INVALID_ARG;
-    if (total > 0 && (!q || !o || !lse)) return FA_ERR_INVALID_ARG;
+// Sizes of fa_fwd_paged and of either pass of fa_fwd_paged_prefix.
+static fa_status check_paged(int B, int Hq, int Hkv, int total, int max_new, int max_blocks, int num_blocks,
+                             int block_size, int d, float scale, int causal) {
     if (B <= 0 || Hq <= 0 || Hkv <= 0 || total < 0 || max_new < 0 || max_new > total || max_blocks <= 0 ||
         num_blocks <= 0 || block_size <= 0 || d <= 0)
         return FA_ERR_INVALID_ARG;
@@ -632,6 +635,34 @@ fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
         static_cast<long long>(B) * Hkv >= (1LL << 30) ||
         fa::paged_max_tile_units(B, Hq, Hkv, total, max_new, d) >= (1LL << 29))
         return FA_ERR_UNSUPPORTED;
+    return FA_OK;
+}
+
+// The pass's buffers in the workspace.
+static void paged_place(fa::PagedArgs& a, const PagedWs& w, char* ws) {
+    a.status = reinterpret_cast<int*>(ws);
+    a.counters = reinterpret_cast<int*>(ws + w.counters);
+    a.pm = reinterpret_cast<float*>(ws + w.pm);
+    a.pl = reinterpret_cast<float*>(ws + w.pl);
+    a.po = reinterpret_cast<float*>(ws + w.po);
+    a.tile_counters = reinterpret_cast<int*>(ws + w.tile_counters);
+    a.max_tile_units = static_cast<int>(fa::paged_max_tile_units(a.B, a.Hq, a.Hkv, a.total, a.max_new, a.d));
+    a.tile_pm = reinterpret_cast<float*>(ws + w.tile_pm);
+    a.tile_pl = reinterpret_cast<float*>(ws + w.tile_pl);
+    a.tile_po = reinterpret_cast<float*>(ws + w.tile_po);
+}
+
+fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                       const float* v_scale, void* o, float* lse, const int32_t* cu_seqlens, const int32_t* cache_len,
+                       const int32_t* block_table, int B, int Hq, int Hkv, int total, int max_new, int max_blocks,
+                       int num_blocks, int block_size, int d, float scale, int causal, void* workspace,
+                       size_t ws_bytes, void* stream) {
+    if (!k_cache || !v_cache || !k_scale || !v_scale || !cu_seqlens || !cache_len || !block_table || !workspace)
+        return FA_ERR_INVALID_ARG;
+    if (total > 0 && (!q || !o || !lse)) return FA_ERR_INVALID_ARG;
+    const fa_status sizes =
+        check_paged(B, Hq, Hkv, total, max_new, max_blocks, num_blocks, block_size, d, scale, causal);
+    if (sizes != FA_OK) return sizes;
     if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
         !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(cu_seqlens, 4) || !aligned(cache_len, 4) ||
         !aligned(block_table, 4) || !aligned(workspace, 256))
@@ -661,16 +692,8 @@ fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
     a.d = d;
     a.scale = scale;
     a.causal = causal;
-    a.status = reinterpret_cast<int*>(ws);
-    a.counters = reinterpret_cast<int*>(ws + w.counters);
-    a.pm = reinterpret_cast<float*>(ws + w.pm);
-    a.pl = reinterpret_cast<float*>(ws + w.pl);
-    a.po = reinterpret_cast<float*>(ws + w.po);
-    a.tile_counters = reinterpret_cast<int*>(ws + w.tile_counters);
-    a.max_tile_units = static_cast<int>(fa::paged_max_tile_units(B, Hq, Hkv, total, max_new, d));
-    a.tile_pm = reinterpret_cast<float*>(ws + w.tile_pm);
-    a.tile_pl = reinterpret_cast<float*>(ws + w.tile_pl);
-    a.tile_po = reinterpret_cast<float*>(ws + w.tile_po);
+    a.split_rows = fa::paged_split_rows(max_new, Hq / Hkv, d);
+    paged_place(a, w, ws);
     a.ev_begin = g_ev_begin;
     a.ev_end = g_ev_end;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -679,6 +702,292 @@ fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
     if (total > 0 && max_new > 0) {
         const fa_status st = map_cuda(fa::launch_fwd_paged(a, s, &n));
         if (st != FA_OK) return st;
+    }
+    g_last_launches = n;
+    return FA_OK;
+}
+
+// Workspace of fa_fwd_paged_prefix: the status word, the counters of both passes,
+// the results of the prefixes' pass, then both passes' partials.
+struct PrefixWs {
+    PagedWs prefix, own;
+    size_t ml, o, bytes;
+};
+
+static PrefixWs prefix_ws(int B, int P, int Hq, int Hkv, int total, int max_new, int d) {
+    const size_t rows = static_cast<size_t>(total) * Hq;
+    const size_t up = static_cast<size_t>(fa::paged_max_tile_units(P, Hq, Hkv, total, total, d));
+    const size_t uo = static_cast<size_t>(fa::paged_max_tile_units(B, Hq, Hkv, total, max_new, d));
+    PrefixWs w;
+    w.prefix = paged_ws_counters(kStatusBytes, P, Hkv, up);
+    w.own = paged_ws_counters(w.prefix.zeroed, B, Hkv, uo);
+    w.ml = w.own.zeroed;
+    w.o = w.ml + align256(rows * sizeof(float2));
+    paged_ws_partials(w.prefix, w.o + align256(rows * d * sizeof(float)), up, d);
+    paged_ws_partials(w.own, w.prefix.bytes, uo, d);
+    w.bytes = w.own.bytes;
+    return w;
+}
+
+size_t fa_fwd_paged_prefix_workspace_size(int B, int P, int Hq, int Hkv, int total, int max_new, int d) {
+    if (B <= 0 || P <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || total < 0 || max_new < 0 || d <= 0) return 0;
+    return prefix_ws(B, P, Hq, Hkv, total, max_new, d).bytes;
+}
+
+fa_status fa_fwd_paged_prefix(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                              const float* v_scale, void* o, float* lse, const int32_t* cu_seqlens,
+                              const int32_t* cache_len, const int32_t* block_table, const int32_t* prefix_cu,
+                              const int32_t* prefix_len, const int32_t* prefix_table, int B, int P, int Hq, int Hkv,
+                              int total, int max_new, int max_blocks, int max_prefix_blocks, int num_blocks,
+                              int block_size, int d, float scale, int causal, void* workspace, size_t ws_bytes,
+                              void* stream) {
+    if (!k_cache || !v_cache || !k_scale || !v_scale || !cu_seqlens || !cache_len || !block_table || !prefix_cu ||
+        !prefix_len || !prefix_table || !workspace)
+        return FA_ERR_INVALID_ARG;
+    if (total > 0 && (!q || !o || !lse)) return FA_ERR_INVALID_ARG;
+    fa_status st = check_paged(B, Hq, Hkv, total, max_new, max_blocks, num_blocks, block_size, d, scale, causal);
+    if (st != FA_OK) return st;
+    st = check_paged(P, Hq, Hkv, total, total, max_prefix_blocks, num_blocks, block_size, d, scale, 0);
+    if (st != FA_OK) return st;
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
+        !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(cu_seqlens, 4) || !aligned(cache_len, 4) ||
+        !aligned(block_table, 4) || !aligned(prefix_cu, 4) || !aligned(prefix_len, 4) || !aligned(prefix_table, 4) ||
+        !aligned(workspace, 256))
+        return FA_ERR_INVALID_ARG;
+    const PrefixWs w = prefix_ws(B, P, Hq, Hkv, total, max_new, d);
+    if (ws_bytes < w.bytes) return FA_ERR_INVALID_ARG;
+    char* ws = static_cast<char*>(workspace);
+    fa::PagedArgs a{};
+    a.q = q;
+    a.k_cache = static_cast<const uint8_t*>(k_cache);
+    a.v_cache = static_cast<const uint8_t*>(v_cache);
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.o = o;
+    a.lse = lse;
+    a.cu_seqlens = cu_seqlens;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.total = total;
+    a.num_blocks = num_blocks;
+    a.block_size = block_size;
+    a.d = d;
+    a.scale = scale;
+    a.join.ml = reinterpret_cast<float2*>(ws + w.ml);
+    a.join.o = reinterpret_cast<float*>(ws + w.o);
+    a.join.ngroups = P;
+    a.join.requests = B;
+    a.ev_begin = g_ev_begin;
+    a.ev_end = g_ev_end;
+    const int group = Hq / Hkv;
+    fa::PagedArgs pre = a;  // a group of requests as one request, its prefix as its keys
+    pre.B = P;
+    pre.cache_len = prefix_len;
+    pre.block_table = prefix_table;
+    pre.max_blocks = max_prefix_blocks;
+    pre.max_new = total;
+    pre.join.first = prefix_cu;
+    // one group has all rows and none goes to the split-key kernel; of several,
+    // some may be small
+    pre.split_rows = !fa::paged_has_tiles(total, group, d) ? fa::paged_split_rows(total, group, d)
+                     : P == 1                              ? 0
+                                                           : fa::paged_max_rows(d);
+    paged_place(pre, w.prefix, ws);
+    a.B = B;
+    a.cache_len = cache_len;
+    a.block_table = block_table;
+    a.max_blocks = max_blocks;
+    a.max_new = max_new;
+    a.causal = causal;
+    a.join.groups = prefix_cu;
+    a.split_rows = fa::paged_split_rows(max_new, group, d);
+    paged_place(a, w.own, ws);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (cudaMemsetAsync(ws, 0, w.own.zeroed, s) != cudaSuccess) return FA_ERR_CUDA;
+    int n = 0;
+    if (total > 0 && max_new > 0) {
+        st = map_cuda(fa::launch_fwd_paged_prefix(pre, a, s, &n));
+        if (st != FA_OK) return st;
+    }
+    g_last_launches = n;
+    return FA_OK;
+}
+
+// Rows of a [B, H, N, d] or [total, H, d] view: aligned, no negative strides;
+// as an output no two of them overlapping.
+static bool rows_ok(const fa_rows* r, int B, int H, int N, int d, int size, bool out) {
+    if (!r || !r->data || !aligned(r->data, 16)) return false;
+    const long long unit = 16 / size;
+    struct {
+        long long stride, n;
+    } dim[3] = {{r->batch, B}, {r->head, H}, {r->token, N}};
+    for (const auto& x : dim)
+        if (x.n > 1 && (x.stride < 0 || x.stride % unit || x.stride > (1LL << 60) / x.n)) return false;
+    if (!out) return true;
+    for (int i = 0; i < 2; ++i)  // by stride, smallest first
+        for (int j = 0; j + 1 < 3 - i; ++j)
+            if (dim[j].stride > dim[j + 1].stride) {
+                const auto t = dim[j];
+                dim[j] = dim[j + 1];
+                dim[j + 1] = t;
+            }
+    long long extent = d;
+    for (const auto& x : dim) {
+        if (x.n <= 1) continue;
+        if (x.stride < extent) return false;
+        extent += x.stride * (x.n - 1);
+    }
+    return true;
+}
+static fa::NormRows norm_rows(const fa_rows* r, int B, int H, int N) {
+    if (!r) return {};
+    return {r->data, B > 1 ? r->batch : 0, H > 1 ? r->head : 0, N > 1 ? r->token : 0};
+}
+
+// Arguments that the norm's entry points share; a's rows stay to be set.
+static fa_status norm_args(fa::NormArgs& a, const void* q_weight, const void* k_weight, float eps,
+                           const double* inv_freq, int rot, int interleaved, const int32_t* cu_seqlens,
+                           const int32_t* ends, int B, int N, int Hq, int Hkv, int d, fa_dtype dtype) {
+    if (dtype != FA_BF16 && dtype != FA_FP32) return FA_ERR_INVALID_ARG;
+    if (B <= 0 || N < 0 || Hq <= 0 || Hkv <= 0 || d <= 0 || rot <= 0 || !inv_freq) return FA_ERR_INVALID_ARG;
+    if (interleaved != 0 && interleaved != 1) return FA_ERR_INVALID_ARG;
+    if (!(eps > 0.f) || !isfinite(eps)) return FA_ERR_INVALID_ARG;
+    if ((d != 64 && d != 128) || rot % 16 != 0 || rot > d) return FA_ERR_UNSUPPORTED;
+    const long long tokens = cu_seqlens ? N : static_cast<long long>(B) * N;
+    if (Hq > 65535 || Hkv > 65535 || (cu_seqlens && B > 65535) || tokens * (Hq + Hkv) >= (1LL << 31))
+        return FA_ERR_UNSUPPORTED;
+    if (!aligned(q_weight, 4) || !aligned(k_weight, 4) || !aligned(inv_freq, 8) || !aligned(cu_seqlens, 4) ||
+        !aligned(ends, 4))
+        return FA_ERR_INVALID_ARG;
+    a.q_weight = q_weight;
+    a.k_weight = k_weight;
+    a.inv_freq = inv_freq;
+    a.cu_seqlens = cu_seqlens;
+    a.ends = ends;
+    a.B = B;
+    a.N = N;
+    a.tokens = static_cast<int>(tokens);
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.d = d;
+    a.rot = rot;
+    a.interleaved = interleaved;
+    a.fp32 = dtype == FA_FP32;
+    a.eps = eps;
+    a.by_n = fa::make_fast_div(N > 0 ? N : 1);
+    return FA_OK;
+}
+
+fa_status fa_qk_norm_rope(const fa_rows* q, const fa_rows* k, const fa_rows* q_out, const fa_rows* k_out,
+                          const void* q_weight, const void* k_weight, float eps, const double* inv_freq, int rot,
+                          int interleaved, const int32_t* cu_seqlens, const int32_t* ends, int B, int N, int Hq,
+                          int Hkv, int d, fa_dtype dtype, void* stream) {
+    fa::NormArgs a{};
+    const fa_status st = norm_args(a, q_weight, k_weight, eps, inv_freq, rot, interleaved, cu_seqlens, ends, B, N, Hq,
+                                   Hkv, d, dtype);
+    if (st != FA_OK) return st;
+    int n = 0;
+    if (a.tokens > 0) {
+        const int b = cu_seqlens ? 1 : B, size = a.fp32 ? 4 : 2;
+        if (!rows_ok(q, b, Hq, N, d, size, false) || !rows_ok(k, b, Hkv, N, d, size, false) ||
+            !rows_ok(q_out, b, Hq, N, d, size, true) || !rows_ok(k_out, b, Hkv, N, d, size, true))
+            return FA_ERR_INVALID_ARG;
+        a.q = norm_rows(q, b, Hq, N);
+        a.k = norm_rows(k, b, Hkv, N);
+        a.q_out = norm_rows(q_out, b, Hq, N);
+        a.k_out = norm_rows(k_out, b, Hkv, N);
+        const fa_status r = map_cuda(fa::launch_norm(a, static_cast<cudaStream_t>(stream), &n));
+        if (r != FA_OK) return r;
+    }
+    g_last_launches = n;
+    return FA_OK;
+}
+
+size_t fa_qk_norm_rope_bwd_workspace_size(int d) {
+    if (d <= 0) return 0;
+    return kStatusBytes + align256(static_cast<size_t>(fa::kNormBwdCtas) * 2 * d * sizeof(float));
+}
+
+fa_status fa_qk_norm_rope_bwd(const fa_rows* q, const fa_rows* k, const fa_rows* dq_out, const fa_rows* dk_out,
+                              const fa_rows* dq, const fa_rows* dk, const void* q_weight, const void* k_weight,
+                              float* dq_weight, float* dk_weight, float eps, const double* inv_freq, int rot,
+                              int interleaved, const int32_t* cu_seqlens, const int32_t* ends, int B, int N, int Hq,
+                              int Hkv, int d, fa_dtype dtype, void* workspace, size_t ws_bytes, void* stream) {
+    fa::NormArgs a{};
+    const fa_status st = norm_args(a, q_weight, k_weight, eps, inv_freq, rot, interleaved, cu_seqlens, ends, B, N, Hq,
+                                   Hkv, d, dtype);
+    if (st != FA_OK) return st;
+    if (!workspace || !aligned(workspace, 256) || ws_bytes < fa_qk_norm_rope_bwd_workspace_size(d) ||
+        (q_weight != nullptr) != (dq_weight != nullptr) || (k_weight != nullptr) != (dk_weight != nullptr) ||
+        !aligned(dq_weight, 4) || !aligned(dk_weight, 4))
+        return FA_ERR_INVALID_ARG;
+    a.dq_weight = dq_weight;
+    a.dk_weight = dk_weight;
+    a.status = static_cast<int*>(workspace);
+    a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kStatusBytes);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int n = 0;
+    if (a.tokens > 0) {
+        const int b = cu_seqlens ? 1 : B, size = a.fp32 ? 4 : 2;
+        if ((q_weight && !rows_ok(q, b, Hq, N, d, size, false)) || (k_weight && !rows_ok(k, b, Hkv, N, d, size, false)) ||
+            !rows_ok(dq_out, b, Hq, N, d, size, false) || !rows_ok(dk_out, b, Hkv, N, d, size, false) ||
+            !rows_ok(dq, b, Hq, N, d, size, true) || !rows_ok(dk, b, Hkv, N, d, size, true))
+            return FA_ERR_INVALID_ARG;
+        a.q = norm_rows(q, b, Hq, N);
+        a.k = norm_rows(k, b, Hkv, N);
+        a.q_out = norm_rows(dq_out, b, Hq, N);
+        a.k_out = norm_rows(dk_out, b, Hkv, N);
+        a.dq = norm_rows(dq, b, Hq, N);
+        a.dk = norm_rows(dk, b, Hkv, N);
+        const fa_status r = map_cuda(fa::launch_norm_bwd(a, s, &n));
+        if (r != FA_OK) return r;
+    } else {
+        if (cudaMemsetAsync(workspace, 0, sizeof(int), s) != cudaSuccess) return FA_ERR_CUDA;
+        for (float* w : {dq_weight, dk_weight})
+            if (w && cudaMemsetAsync(w, 0, d * sizeof(float), s) != cudaSuccess) return FA_ERR_CUDA;
+    }
+    g_last_launches = n;
+    return FA_OK;
+}
+
+fa_status fa_qk_norm_rope_append(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows* q_out,
+                                 void* k_cache, void* v_cache, float* k_scale, float* v_scale, const int32_t* slots,
+                                 const void* q_weight, const void* k_weight, float eps, const double* inv_freq,
+                                 int rot, int interleaved, const int32_t* cu_seqlens, const int32_t* ends, int B,
+                                 int total, int Hq, int Hkv, int d, int num_blocks, int block_size, void* stream) {
+    if (!k_cache || !v_cache || !k_scale || !v_scale || !cu_seqlens) return FA_ERR_INVALID_ARG;
+    if (num_blocks <= 0 || block_size <= 0) return FA_ERR_INVALID_ARG;
+    fa::NormAppendArgs a{};
+    const fa_status st = norm_args(a.n, q_weight, k_weight, eps, inv_freq, rot, interleaved, cu_seqlens, ends, B,
+                                   total, Hq, Hkv, d, FA_BF16);
+    if (st != FA_OK) return st;
+    if (!paged_block_ok(block_size)) return FA_ERR_UNSUPPORTED;
+    if (static_cast<long long>(num_blocks) * Hkv * block_size >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4) ||
+        !aligned(slots, 4))
+        return FA_ERR_INVALID_ARG;
+    int n = 0;
+    if (total > 0) {
+        if (!slots || !rows_ok(q, 1, Hq, total, d, 2, false) || !rows_ok(k, 1, Hkv, total, d, 2, false) ||
+            !rows_ok(v, 1, Hkv, total, d, 2, false) || !rows_ok(q_out, 1, Hq, total, d, 2, true))
+            return FA_ERR_INVALID_ARG;
+        a.n.q = norm_rows(q, 1, Hq, total);
+        a.n.q_out = norm_rows(q_out, 1, Hq, total);
+        a.n.k = norm_rows(k, 1, Hkv, total);
+        a.v = norm_rows(v, 1, Hkv, total);
+        a.a.k_cache = static_cast<uint8_t*>(k_cache);
+        a.a.v_cache = static_cast<uint8_t*>(v_cache);
+        a.a.k_scale = k_scale;
+        a.a.v_scale = v_scale;
+        a.a.slots = slots;
+        a.a.total = total;
+        a.a.H = Hkv;
+        a.a.d = d;
+        a.a.num_blocks = num_blocks;
+        a.a.block_size = block_size;
+        a.n.Hkv = 0;  // of the rows that go to q_out
+        const fa_status r = map_cuda(fa::launch_norm_append(a, static_cast<cudaStream_t>(stream), &n));
+        if (r != FA_OK) return r;
     }
     g_last_launches = n;
     return FA_OK;

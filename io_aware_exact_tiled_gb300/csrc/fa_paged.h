@@ -7,6 +7,7 @@
 
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include <math.h>
 
 namespace fa {
 
@@ -39,6 +40,15 @@ struct AppendArgs {
     int total, H, d, num_blocks, block_size;
 };
 
+// What a call with shared prefixes adds to its two passes (all zero otherwise).
+struct PagedJoin {
+    const int32_t* first;   // the prefixes' pass: its request b is requests first[b] .. first[b + 1] - 1
+    const int32_t* groups;  // the other pass: requests groups[0] .. groups[ngroups] - 1 have a prefix
+    int ngroups, requests;
+    float2* ml;             // [total][Hq] of the prefixes' pass: maximum and sum
+    float* o;               // [total][Hq][d] of the prefixes' pass, normalised
+};
+
 struct PagedArgs {
     const void* q;  // [total][Hq][d] bf16
     const uint8_t *k_cache, *v_cache;
@@ -49,6 +59,8 @@ struct PagedArgs {
     int B, Hq, Hkv, total, max_new, max_blocks, num_blocks, block_size, d;
     float scale;
     int causal;
+    int split_rows;  // requests of no more rows are the split-key kernel's
+    PagedJoin join;
     // workspace; the counters are zero at the start
     int* status;
     int* counters;       // [B * Hkv] finished pieces of the split-key kernel's units
@@ -117,6 +129,35 @@ __device__ __forceinline__ uint32_t f16x2_from_e4m3x2(uint32_t x) {
     asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(x));
     return r;
 }
+// Of a call with shared prefixes: the requests i0 .. i1 - 1 that request i0 of
+// this pass stands for. False if the offsets are none.
+__device__ __forceinline__ bool paged_members(const PagedJoin& j, int& i0, int& i1) {
+    if (!j.first) return true;
+    const int a = j.first[i0], b = j.first[i1];
+    i0 = min(max(a, 0), j.requests);
+    i1 = min(max(b, i0), j.requests);
+    return i0 == a && i1 == b;
+}
+__device__ __forceinline__ bool paged_joins(const PagedJoin& j, int b) {
+    return b >= j.groups[0] && b < j.groups[j.ngroups];
+}
+// Softmax over two sets of keys with maxima m (log2 units) and sums l (both
+// times 2^6, as the kernels keep them): the weights of the own output (not
+// normalised) and of the prefix's (normalised), and L.
+struct PagedWeights {
+    float own, prefix, lse;
+};
+__device__ __forceinline__ PagedWeights paged_weights(float m, float l, float2 b) {
+    const float la = log2f(l), lb = log2f(b.y), ln2 = 0.69314718055994530942f;
+    const float d = l == 0.f ? -INFINITY : b.y == 0.f ? INFINITY : (m - b.x) + (la - lb);
+    const float e = exp2f(-fabsf(d)), big = 1.f / (1.f + e), small = e * big;
+    PagedWeights w;
+    w.own = l == 0.f ? 0.f : (d >= 0.f ? big : small) / l;
+    w.prefix = b.y == 0.f ? 0.f : d >= 0.f ? small : big;
+    w.lse = ((d >= 0.f ? (m - 6.f) + la : (b.x - 6.f) + lb) + log2f(1.f + e)) * ln2;
+    if (l == 0.f && b.y == 0.f) w.lse = -INFINITY;
+    return w;
+}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -145,6 +186,7 @@ inline FastDiv make_fast_div(int d) {
 cudaError_t launch_cache_plan(const PlanArgs& a, cudaStream_t stream, int* nlaunch);
 cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t stream, int* nlaunch);
 cudaError_t launch_paged_tile(const PagedArgs& a, cudaStream_t stream);
+cudaError_t launch_fwd_paged_prefix(const PagedArgs& prefix, const PagedArgs& own, cudaStream_t stream, int* nlaunch);
 cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t stream, int* nlaunch);
 
 }  // namespace fa

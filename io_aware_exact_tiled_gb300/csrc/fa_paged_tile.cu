@@ -1,7 +1,7 @@
 // Attention over the paged 8-bit cache for requests with many query rows
 // (prompts and pieces of prompts): tcgen05 products on tiles of 128 rows.
 //
-// Same computation as fa_paged.cu. With hundreds of rows for each cached key
+// Same computation as fa_paged_split.cuh. With hundreds of rows for each cached key
 // the time is that of the two products, 4 n len d flops for each query head.
 // Measured against 1,871 TFLOP/s of bf16 products: d = 128, two requests of
 // about 2,000 new tokens behind 15,000 to 16,384, 32 query heads, 789 us = 1,345
@@ -118,6 +118,7 @@ struct PtParams {
     int *status, *counters;
     int max_units;
     float *pm, *pl, *po;
+    PagedJoin join;  // a pass of a call with shared prefixes
 };
 
 __device__ __forceinline__ void named_sync(int id, int threads) {
@@ -308,9 +309,11 @@ __device__ __forceinline__ int pt_tiles(const PtParams& p, const PtReq& r, int p
     const int last = min(pair * 256 + 255, r.n * p.G - 1);
     return max(1, (pt_visible(p, r, p.by_g.div(last)) + 127) >> 7);
 }
-template <int D>
+template <int D, bool PFX>
 __device__ __forceinline__ void pt_request(const PtParams& p, int b, PtReq& r) {
-    const int t0 = min(max(p.cu_seqlens[b], 0), p.total), t1 = min(max(p.cu_seqlens[b + 1], t0), p.total);
+    int i0 = b, i1 = b + 1;
+    if constexpr (PFX) paged_members(p.join, i0, i1);
+    const int t0 = min(max(p.cu_seqlens[i0], 0), p.total), t1 = min(max(p.cu_seqlens[i1], t0), p.total);
     r.b = b;
     r.tok0 = t0;
     r.n = min(t1 - t0, p.max_new);
@@ -321,7 +324,7 @@ __device__ __forceinline__ void pt_request(const PtParams& p, int b, PtReq& r) {
     for (int i = 0; i < r.npair; ++i) r.tiles += pt_tiles(p, r, i) + kPtUnitCost<D>;
 }
 
-template <int D>
+template <int D, bool PFX>
 __global__ void __launch_bounds__(512, 1)
     fa_paged_tile_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                          const __grid_constant__ PtParams p) {
@@ -340,7 +343,7 @@ __global__ void __launch_bounds__(512, 1)
     long long mw = 0, mu = 0;
     for (int b = b0; b < b1; ++b) {
         PtReq r;
-        pt_request<D>(p, b, r);
+        pt_request<D, PFX>(p, b, r);
         mu += static_cast<long long>(r.npair) * p.Hkv;
         mw += r.tiles * p.Hkv;
     }
@@ -433,7 +436,7 @@ __global__ void __launch_bounds__(512, 1)
     if (x0 >= bw && x0 < bw + mw) {
         for (int b = b0; b < b1; ++b) {
             PtReq r;
-            pt_request<D>(p, b, r);
+            pt_request<D, PFX>(p, b, r);
             if (x0 < bw + r.tiles * p.Hkv) {
                 start_b = b;
                 start_line = bw;
@@ -460,7 +463,7 @@ __global__ void __launch_bounds__(512, 1)
         while (x >= rline + s.r.tiles * p.Hkv) {
             rline += s.r.tiles * p.Hkv;
             runits += s.r.npair * p.Hkv;
-            pt_request<D>(p, s.r.b + 1, s.r);
+            pt_request<D, PFX>(p, s.r.b + 1, s.r);
         }
         const long long off = x - rline;
         s.hk = static_cast<int>(div_short(off, s.r.tiles));
@@ -501,7 +504,7 @@ __global__ void __launch_bounds__(512, 1)
     };
     auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return pt_wait(bar, parity, &abort_s); };
     PtSeg s;
-    pt_request<D>(p, start_b, s.r);
+    pt_request<D, PFX>(p, start_b, s.r);
     find(s, x0);
     const bool any = s.c1 > s.c0;  // uniform over the CTA: not only the cost in front of a tile
 
@@ -818,7 +821,46 @@ __global__ void __launch_bounds__(512, 1)
             ++seg;
             const bool whole = s.c0 == 0 && s.c1 == s.ntile;
             const int slot = 2 * static_cast<int>(blockIdx.x) + (s.line0 <= x0 ? 0 : 1);
-            const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+            float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+            // PFX: weight of the prefix in the row's output, and L
+            [[maybe_unused]] float before = 0.f, lse_all = 0.f;
+            [[maybe_unused]] const size_t orow = qrow / D;
+            auto row_weights = [&](float M, float L, float& own) {
+                lse_all = L == 0.f ? -CUDART_INF_F : (M - kPtOffset + log2f(L)) * kPtLn2;
+                if (p.join.first) {
+                    if (row_ok) p.join.ml[orow] = make_float2(M, L);
+                } else if (row_ok && paged_joins(p.join, s.r.b)) {
+                    const PagedWeights w = paged_weights(M, L, __ldcg(&p.join.ml[orow]));
+                    own = w.own;
+                    before = w.prefix;
+                    lse_all = w.lse;
+                }
+            };
+            // columns c .. c + 7 of the row, normalised
+            auto put_row = [&](int c, float (&v)[8]) {
+                float4* at = reinterpret_cast<float4*>(p.join.o + qrow + c);
+                if (p.join.first) {
+                    at[0] = make_float4(v[0], v[1], v[2], v[3]);
+                    at[1] = make_float4(v[4], v[5], v[6], v[7]);
+                    return;
+                }
+                if (before != 0.f) {
+                    const float4 x = __ldcg(at), y = __ldcg(at + 1);
+                    v[0] = fmaf(before, x.x, v[0]);
+                    v[1] = fmaf(before, x.y, v[1]);
+                    v[2] = fmaf(before, x.z, v[2]);
+                    v[3] = fmaf(before, x.w, v[3]);
+                    v[4] = fmaf(before, y.x, v[4]);
+                    v[5] = fmaf(before, y.y, v[5]);
+                    v[6] = fmaf(before, y.z, v[6]);
+                    v[7] = fmaf(before, y.w, v[7]);
+                }
+                *reinterpret_cast<uint4*>(p.o + qrow + c) =
+                    make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                               pack_bf16x2(v[6], v[7]));
+            };
+            if constexpr (PFX)
+                if (whole) row_weights(mu, l, inv);
             // partial outputs lie as [d / 4][128 rows] float4, coalesced over the rows
             float4* po = reinterpret_cast<float4*>(p.po) + (static_cast<size_t>(2 * slot + i) * (D / 4)) * 128 + r;
 #pragma unroll
@@ -839,7 +881,17 @@ __global__ void __launch_bounds__(512, 1)
                             ov[k] = __float_as_uint(CUDART_NAN_F);
                 }
                 if (whole) {
-                    if (row_ok) {
+                    if constexpr (PFX) {
+                        if (row_ok) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                float v[8];
+#pragma unroll
+                                for (int y = 0; y < 8; ++y) v[y] = __uint_as_float(ov[8 * k + y]) * inv;
+                                put_row(c * 32 + k * 8, v);
+                            }
+                        }
+                    } else if (row_ok) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             uint4 w;
@@ -862,7 +914,9 @@ __global__ void __launch_bounds__(512, 1)
             mbar_arrive(&nan_empty[(seg - 1) % kPtNanSlots]);
             const float lse_off = kPtOffset;
             if (whole) {
-                if (row_ok)
+                if constexpr (PFX) {
+                    if (row_ok && !p.join.first) p.lse[static_cast<size_t>(hq) * p.total + s.r.tok0 + tok] = lse_all;
+                } else if (row_ok)
                     p.lse[static_cast<size_t>(hq) * p.total + s.r.tok0 + tok] =
                         l == 0.f ? -CUDART_INF_F : (mu - lse_off + log2f(l)) * kPtLn2;
             } else {
@@ -904,8 +958,19 @@ __global__ void __launch_bounds__(512, 1)
                                 acc[k].w = fmaf(w, v.w, acc[k].w);
                             }
                         }
-                        const float iL = L == 0.f ? 0.f : 1.f / L;
-                        if (row_ok) {
+                        float iL = L == 0.f ? 0.f : 1.f / L;
+                        if constexpr (PFX) {
+                            row_weights(M, L, iL);
+                            if (row_ok) {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    float v[8] = {acc[2 * k].x * iL,     acc[2 * k].y * iL,     acc[2 * k].z * iL,
+                                                  acc[2 * k].w * iL,     acc[2 * k + 1].x * iL, acc[2 * k + 1].y * iL,
+                                                  acc[2 * k + 1].z * iL, acc[2 * k + 1].w * iL};
+                                    put_row(c * 32 + k * 8, v);
+                                }
+                            }
+                        } else if (row_ok) {
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 uint4 w;
@@ -917,7 +982,9 @@ __global__ void __launch_bounds__(512, 1)
                             }
                         }
                     }
-                    if (row_ok)
+                    if constexpr (PFX) {
+                        if (row_ok && !p.join.first) p.lse[static_cast<size_t>(hq) * p.total + s.r.tok0 + tok] = lse_all;
+                    } else if (row_ok)
                         p.lse[static_cast<size_t>(hq) * p.total + s.r.tok0 + tok] =
                             L == 0.f ? -CUDART_INF_F : (M - lse_off + log2f(L)) * kPtLn2;
                 }
@@ -1029,7 +1096,7 @@ static bool make_tmap_rows(CUtensorMap* map, const void* base, uint64_t rows, in
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+template <int D, bool PFX>
 static cudaError_t launch_tile(const PagedArgs& a, const PtParams& p, cudaStream_t stream) {
     using C = PtCfg<D>;
     CUtensorMap tk, tv;
@@ -1039,10 +1106,10 @@ static cudaError_t launch_tile(const PagedArgs& a, const PtParams& p, cudaStream
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = once_per_device(done, [] {
-        return cudaFuncSetAttribute(fa_paged_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        return cudaFuncSetAttribute(fa_paged_tile_kernel<D, PFX>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     });
     if (e != cudaSuccess) return e;
-    fa_paged_tile_kernel<D><<<kPagedCtas, 512, C::SMEM, stream>>>(tk, tv, p);
+    fa_paged_tile_kernel<D, PFX><<<kPagedCtas, 512, C::SMEM, stream>>>(tk, tv, p);
     return cudaGetLastError();
 }
 
@@ -1061,7 +1128,7 @@ cudaError_t launch_paged_tile(const PagedArgs& a, cudaStream_t stream) {
     p.Hkv = a.Hkv;
     p.G = a.Hq / a.Hkv;
     p.by_g = make_fast_div(p.G);
-    p.split_rows = paged_split_rows(a.max_new, p.G, a.d);
+    p.split_rows = a.split_rows;
     p.total = a.total;
     p.max_new = a.max_new;
     p.max_blocks = a.max_blocks;
@@ -1076,7 +1143,9 @@ cudaError_t launch_paged_tile(const PagedArgs& a, cudaStream_t stream) {
     p.pm = a.tile_pm;
     p.pl = a.tile_pl;
     p.po = a.tile_po;
-    return a.d == 64 ? launch_tile<64>(a, p, stream) : launch_tile<128>(a, p, stream);
+    p.join = a.join;
+    if (a.join.ml) return a.d == 64 ? launch_tile<64, true>(a, p, stream) : launch_tile<128, true>(a, p, stream);
+    return a.d == 64 ? launch_tile<64, false>(a, p, stream) : launch_tile<128, false>(a, p, stream);
 }
 
 }  // namespace fa
