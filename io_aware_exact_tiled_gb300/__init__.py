@@ -17,12 +17,6 @@ from .binding import (  # noqa: F401
     cache_append,
     forward_paged,
     fwd_paged_workspace_size,
-    forward_paged_prefix,
-    fwd_paged_prefix_workspace_size,
-    qk_norm_rope,
-    qk_norm_rope_append,
-    qk_norm_rope_backward,
-    qk_norm_rope_bwd_workspace_size,
     forward_fp8,
     forward_dropout,
     backward_dropout,
@@ -35,6 +29,13 @@ from .binding import (  # noqa: F401
     load,
     set_timing_events,
     workspace,
+)
+from .paged_prefix import forward_paged_prefix, fwd_paged_prefix_workspace_size  # noqa: F401
+from .qk_norm import (  # noqa: F401
+    qk_norm_rope,
+    qk_norm_rope_append,
+    qk_norm_rope_backward,
+    qk_norm_rope_bwd_workspace_size,
 )
 from .binding import C_NAMES as _C_NAMES
 

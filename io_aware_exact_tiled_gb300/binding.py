@@ -132,6 +132,8 @@ def _ptr(t: Optional[torch.Tensor]):
 # the current stream's handle without a Stream object (a microsecond or two of
 # a decoding call's host time)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# the current device of a process that has CUDA tensors
+_device_index = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream_handle(stream: Optional[torch.cuda.Stream]):
@@ -142,14 +144,14 @@ def _stream_handle(stream: Optional[torch.cuda.Stream]):
         return stream.cuda_stream
     if _raw_stream is None:
         return torch.cuda.current_stream().cuda_stream
-    return _raw_stream(torch.cuda.current_device())
+    return _raw_stream(_device_index())
 
 
 def _check_device(q: torch.Tensor):
     """The kernels run on the current CUDA device: q must live there."""
     if not q.is_cuda:
         raise ValueError("tensors must be on a CUDA device")
-    if q.get_device() != torch.cuda.current_device():
+    if q.get_device() != _device_index():
         raise ValueError(f"tensors are on {q.device} but the current device is cuda:{torch.cuda.current_device()}:"
                          " call under torch.cuda.device(q.device)")
 
@@ -157,9 +159,9 @@ def _check_device(q: torch.Tensor):
 def _in(t: torch.Tensor, shape, dtype, device, name: str) -> torch.Tensor:
     """Check a buffer the kernels read or write as exactly `shape` contiguous
     elements of `dtype` on `device` (the library cannot see its size)."""
-    if t.dtype != dtype or t.shape != tuple(shape) or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on {device}")
-    return t
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t
+    raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on {device}")
 
 
 def _out(t: Optional[torch.Tensor], shape, dtype, device, name: str, stream=None) -> torch.Tensor:
@@ -248,14 +250,6 @@ def fwd_fp8_workspace_size(B, H, N, d) -> int:
 
 def fwd_paged_workspace_size(B, Hq, Hkv, total, max_new, d) -> int:
     return load().fa_fwd_paged_workspace_size(B, Hq, Hkv, total, max_new, d)
-
-
-def fwd_paged_prefix_workspace_size(B, P, Hq, Hkv, total, max_new, d) -> int:
-    return load().fa_fwd_paged_prefix_workspace_size(B, P, Hq, Hkv, total, max_new, d)
-
-
-def qk_norm_rope_bwd_workspace_size(d) -> int:
-    return load().fa_qk_norm_rope_bwd_workspace_size(d)
 
 
 def workspace(nbytes: int, device) -> torch.Tensor:
@@ -515,13 +509,14 @@ def cache_plan(new_len, cache_len, block_table, free_blocks, free_state, block_s
 
 
 def _check_paged(k_cache, v_cache, k_scale, v_scale, device):
-    if k_cache.dim() != 4:
+    shape = k_cache.shape
+    if len(shape) != 4:
         raise ValueError("the cache must be [num_blocks, Hkv, block_size, d]")
-    shape = tuple(k_cache.shape)
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _in(t, shape, torch.float8_e4m3fn, device, name)
-    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        _in(t, shape[:2], torch.float32, device, name)
+    e4m3, scales = torch.float8_e4m3fn, shape[:2]
+    _in(k_cache, shape, e4m3, device, "k_cache")
+    _in(v_cache, shape, e4m3, device, "v_cache")
+    _in(k_scale, scales, torch.float32, device, "k_scale")
+    _in(v_scale, scales, torch.float32, device, "v_scale")
     return shape
 
 
@@ -572,187 +567,6 @@ def forward_paged(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens, cache_len, 
     if rc != FA_OK:
         raise FAError(rc, "fa_fwd_paged")
     return o, L
-
-
-def forward_paged_prefix(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens, cache_len, block_table, prefix_cu,
-                         prefix_len, prefix_table, max_new: int, scale: Optional[float] = None, causal: bool = True,
-                         out=None, lse=None, ws=None, stream=None):
-    """O, L = fa_fwd_paged_prefix(...): forward_paged for groups of requests
-    that share a prefix of the cache. Group p is requests prefix_cu[p] ..
-    prefix_cu[p + 1] - 1 (int32 [P + 1]); its prefix is prefix_len[p] tokens
-    (int32 [P]) in the blocks prefix_table[p] (int32 [P, max_prefix_blocks]).
-    cache_len and block_table are the requests' own tokens. Returns (o [total,
-    Hq, d], lse fp32 [Hq, total])."""
-    lib = load()
-    _check_device(q)
-    num_blocks, Hkv, bs, d = _check_paged(k_cache, v_cache, k_scale, v_scale, q.device)
-    if q.dim() != 3 or block_table.dim() != 2 or cache_len.dim() != 1 or prefix_table.dim() != 2:
-        raise ValueError("expected q [total, Hq, d], block_table [B, max_blocks], cache_len [B] and prefix_table"
-                         " [P, max_prefix_blocks]")
-    total, Hq, _ = q.shape
-    B, max_blocks = block_table.shape
-    P, max_prefix = prefix_table.shape
-    i32 = torch.int32
-    _in(q, (total, Hq, d), torch.bfloat16, q.device, "q")
-    _in(cu_seqlens, (B + 1,), i32, q.device, "cu_seqlens")
-    _in(cache_len, (B,), i32, q.device, "cache_len")
-    _in(block_table, (B, max_blocks), i32, q.device, "block_table")
-    _in(prefix_cu, (P + 1,), i32, q.device, "prefix_cu")
-    _in(prefix_len, (P,), i32, q.device, "prefix_len")
-    _in(prefix_table, (P, max_prefix), i32, q.device, "prefix_table")
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    o = _out(out, q.shape, q.dtype, q.device, "out", stream)
-    L = _out(lse, (Hq, total), torch.float32, q.device, "lse", stream)
-    ws = _ws(ws, lambda: lib.fa_fwd_paged_prefix_workspace_size(B, P, Hq, Hkv, total, int(max_new), d), q.device,
-             stream)
-    rc = lib.fa_fwd_paged_prefix(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(o), _ptr(L),
-                                 _ptr(cu_seqlens), _ptr(cache_len), _ptr(block_table), _ptr(prefix_cu),
-                                 _ptr(prefix_len), _ptr(prefix_table), B, P, Hq, Hkv, total, int(max_new), max_blocks,
-                                 max_prefix, num_blocks, bs, d, scale, int(bool(causal)), _ptr(ws), _nbytes(ws),
-                                 _stream_handle(stream))
-    if rc != FA_OK:
-        raise FAError(rc, "fa_fwd_paged_prefix")
-    return o, L
-
-
-class _Rows(ctypes.Structure):
-    """fa_rows of include/fa.h."""
-    _fields_ = [("data", ctypes.c_void_p), ("batch", ctypes.c_int64), ("head", ctypes.c_int64),
-                ("token", ctypes.c_int64)]
-
-
-def _rows(t: Optional[torch.Tensor]):
-    """A [B, H, N, d] or [total, H, d] view as the library takes it."""
-    if t is None:
-        return None
-    s = t.stride()
-    if s[-1] != 1:
-        raise ValueError("the elements of a head must be contiguous")
-    return ctypes.byref(_Rows(t.data_ptr(), s[0], s[1], s[2]) if t.dim() == 4 else _Rows(t.data_ptr(), 0, s[1], s[0]))
-
-
-def _like(t, shape, x, name):
-    """Check a tensor of `shape` with x's type and device, any strides."""
-    if t.dtype != x.dtype or t.shape != tuple(shape) or t.device != x.device:
-        raise ValueError(f"{name} must be a {x.dtype} {list(shape)} tensor on {x.device}")
-    return t
-
-
-def _norm_sizes(q, k, inv_freq, q_weight, k_weight, cu_seqlens, ends):
-    """Checks what the norm calls share; returns (B, N, Hq, Hkv, d, rot, dtype)."""
-    _check_device(q)
-    packed = cu_seqlens is not None
-    if q.dim() != (3 if packed else 4) or k.dim() != q.dim():
-        raise ValueError("expected q, k [B, H, N, d], or [total, H, d] with cu_seqlens")
-    if q.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError("dtype must be bfloat16 or float32")
-    dev, d = q.device, q.shape[-1]
-    Hq, Hkv = q.shape[1], k.shape[1]
-    _like(k, (*q.shape[:1], Hkv, *q.shape[2:]), q, "k")
-    if inv_freq.dim() != 1:
-        raise ValueError("inv_freq must be [rot / 2]")
-    _in(inv_freq, inv_freq.shape, torch.float64, dev, "inv_freq")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _in(w, (d,), q.dtype, dev, name)
-    if packed:
-        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
-            raise ValueError("cu_seqlens must be [B + 1]")
-        B, N = cu_seqlens.numel() - 1, q.shape[0]
-        _in(cu_seqlens, (B + 1,), torch.int32, dev, "cu_seqlens")
-    else:
-        B, N = q.shape[0], q.shape[2]
-    if ends is not None:
-        _in(ends, (B,), torch.int32, dev, "ends")
-    return B, N, Hq, Hkv, d, 2 * inv_freq.numel(), FA_BF16 if q.dtype == torch.bfloat16 else FA_FP32
-
-
-def _out_like(t, x, name, stream):
-    """A caller-supplied output of x's shape, or a new contiguous one."""
-    return _out(None, x.shape, x.dtype, x.device, name, stream) if t is None else _like(t, x.shape, x, name)
-
-
-def qk_norm_rope(q, k, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False,
-                 cu_seqlens=None, ends=None, q_out=None, k_out=None, stream=None):
-    """q_out, k_out = fa_qk_norm_rope(...): each head of q and k divided by its
-    root mean square and multiplied by the weight ([d]; None leaves the norm
-    out), its first 2 * len(inv_freq) elements then rotated by the token's
-    position times inv_freq (float64).
-    q [B, Hq, N, d] and k [B, Hkv, N, d], or packed [total, H, d] with
-    cu_seqlens (int32 [B + 1]); bf16 or fp32, any strides with contiguous heads
-    (views of a packed projection). The first token is at position 0, or the
-    last at ends[b] - 1 (int32 [B]). q_out and k_out, of any such strides, may
-    be q and k themselves. Returns (q_out, k_out)."""
-    lib = load()
-    B, N, Hq, Hkv, d, rot, dtype = _norm_sizes(q, k, inv_freq, q_weight, k_weight, cu_seqlens, ends)
-    q_out = _out_like(q_out, q, "q_out", stream)
-    k_out = _out_like(k_out, k, "k_out", stream)
-    rc = lib.fa_qk_norm_rope(_rows(q), _rows(k), _rows(q_out), _rows(k_out), _ptr(q_weight), _ptr(k_weight),
-                             float(eps), _ptr(inv_freq), rot, int(bool(interleaved)), _ptr(cu_seqlens), _ptr(ends), B,
-                             N, Hq, Hkv, d, dtype, _stream_handle(stream))
-    if rc != FA_OK:
-        raise FAError(rc, "fa_qk_norm_rope")
-    return q_out, k_out
-
-
-def qk_norm_rope_backward(q, k, dq_out, dk_out, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6,
-                          interleaved: bool = False, cu_seqlens=None, ends=None, dq=None, dk=None, dq_weight=None,
-                          dk_weight=None, ws=None, stream=None):
-    """dq, dk, dq_weight, dk_weight = fa_qk_norm_rope_bwd(...): the gradients of
-    qk_norm_rope's inputs and weights (float32 [d]; None where there is no
-    weight) from those of its outputs. q and k are qk_norm_rope's inputs; dq
-    and dk, of any strides with contiguous heads, may be dq_out and dk_out."""
-    lib = load()
-    B, N, Hq, Hkv, d, rot, dtype = _norm_sizes(q, k, inv_freq, q_weight, k_weight, cu_seqlens, ends)
-    _like(dq_out, q.shape, q, "dq_out")
-    _like(dk_out, k.shape, q, "dk_out")
-    dq = _out_like(dq, q, "dq", stream)
-    dk = _out_like(dk, k, "dk", stream)
-    for w, g, name in ((q_weight, dq_weight, "dq_weight"), (k_weight, dk_weight, "dk_weight")):
-        if w is None and g is not None:
-            raise ValueError(f"{name} without a weight")
-    if q_weight is not None:
-        dq_weight = _out(dq_weight, (d,), torch.float32, q.device, "dq_weight", stream)
-    if k_weight is not None:
-        dk_weight = _out(dk_weight, (d,), torch.float32, q.device, "dk_weight", stream)
-    ws = _ws(ws, lambda: lib.fa_qk_norm_rope_bwd_workspace_size(d), q.device, stream)
-    rc = lib.fa_qk_norm_rope_bwd(_rows(q), _rows(k), _rows(dq_out), _rows(dk_out), _rows(dq), _rows(dk),
-                                 _ptr(q_weight), _ptr(k_weight), _ptr(dq_weight), _ptr(dk_weight), float(eps),
-                                 _ptr(inv_freq), rot, int(bool(interleaved)), _ptr(cu_seqlens), _ptr(ends), B, N, Hq,
-                                 Hkv, d, dtype, _ptr(ws), _nbytes(ws), _stream_handle(stream))
-    if rc != FA_OK:
-        raise FAError(rc, "fa_qk_norm_rope_bwd")
-    return dq, dk, dq_weight, dk_weight
-
-
-def qk_norm_rope_append(q, k, v, k_cache, v_cache, k_scale, v_scale, slots, inv_freq, cu_seqlens, ends=None,
-                        q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False, q_out=None,
-                        stream=None):
-    """q_out = fa_qk_norm_rope_append(...): qk_norm_rope of a serving step's
-    packed new tokens with the keys, and v, stored into the cache as
-    cache_append does. q [total, Hq, d], k, v [total, Hkv, d] bf16, any strides
-    with contiguous heads; ends: the requests' lengths with the new tokens
-    (cache_len behind cache_plan, a shared prefix added). Returns q_out [total,
-    Hq, d]."""
-    lib = load()
-    if cu_seqlens is None:
-        raise ValueError("cu_seqlens is needed")
-    B, total, Hq, Hkv, d, rot, dtype = _norm_sizes(q, k, inv_freq, q_weight, k_weight, cu_seqlens, ends)
-    if dtype != FA_BF16:
-        raise ValueError("the cache takes bfloat16 inputs")
-    _like(v, k.shape, q, "v")
-    num_blocks, H, bs, dc = _check_paged(k_cache, v_cache, k_scale, v_scale, q.device)
-    if (H, dc) != (Hkv, d):
-        raise ValueError("the cache must have k's heads")
-    _in(slots, (total,), torch.int32, q.device, "slots")
-    q_out = _out_like(q_out, q, "q_out", stream)
-    rc = lib.fa_qk_norm_rope_append(_rows(q), _rows(k), _rows(v), _rows(q_out), _ptr(k_cache), _ptr(v_cache),
-                                    _ptr(k_scale), _ptr(v_scale), _ptr(slots), _ptr(q_weight), _ptr(k_weight),
-                                    float(eps), _ptr(inv_freq), rot, int(bool(interleaved)), _ptr(cu_seqlens),
-                                    _ptr(ends), B, total, Hq, Hkv, d, num_blocks, bs, _stream_handle(stream))
-    if rc != FA_OK:
-        raise FAError(rc, "fa_qk_norm_rope_append")
-    return q_out
 
 
 def backward(q, k, v, o, lse, do, scale: Optional[float] = None, causal: bool = False, blockmask=None,
@@ -822,8 +636,10 @@ def noalloc_status(stream=None) -> int:
     return load().fa_bwd_noalloc_get_status(_stream_handle(stream))
 
 
-# The names of include/fa.h, bound to the wrappers above (same arguments in
-# tensor form; outputs returned rather than passed as pointers).
+from . import paged_prefix as _prefix, qk_norm as _norm  # noqa: E402  (they use what stands above)
+
+# The names of include/fa.h, bound to the wrappers above and in those modules
+# (same arguments in tensor form; outputs returned rather than passed as pointers).
 C_NAMES = {
     "fa_fwd": forward,
     "fa_bwd": backward,
@@ -839,12 +655,12 @@ C_NAMES = {
     "fa_cache_append": cache_append,
     "fa_fwd_paged": forward_paged,
     "fa_fwd_paged_workspace_size": fwd_paged_workspace_size,
-    "fa_fwd_paged_prefix": forward_paged_prefix,
-    "fa_fwd_paged_prefix_workspace_size": fwd_paged_prefix_workspace_size,
-    "fa_qk_norm_rope": qk_norm_rope,
-    "fa_qk_norm_rope_bwd": qk_norm_rope_backward,
-    "fa_qk_norm_rope_bwd_workspace_size": qk_norm_rope_bwd_workspace_size,
-    "fa_qk_norm_rope_append": qk_norm_rope_append,
+    "fa_fwd_paged_prefix": _prefix.forward_paged_prefix,
+    "fa_fwd_paged_prefix_workspace_size": _prefix.fwd_paged_prefix_workspace_size,
+    "fa_qk_norm_rope": _norm.qk_norm_rope,
+    "fa_qk_norm_rope_bwd": _norm.qk_norm_rope_backward,
+    "fa_qk_norm_rope_bwd_workspace_size": _norm.qk_norm_rope_bwd_workspace_size,
+    "fa_qk_norm_rope_append": _norm.qk_norm_rope_append,
     "fa_fwd_fp8": forward_fp8,
     "fa_fwd_fp8_workspace_size": fwd_fp8_workspace_size,
     "fa_fwd_dropout": forward_dropout,

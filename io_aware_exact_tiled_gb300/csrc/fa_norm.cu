@@ -19,110 +19,134 @@
 namespace fa {
 
 template <typename T, int D, bool INTER>
-__global__ void __launch_bounds__(kNormThreads) fa_norm_kernel(const __grid_constant__ NormArgs p, int parts) {
+__global__ void __launch_bounds__(kNormThreads, sizeof(T) == 2 ? 4 : 3)
+    fa_norm_kernel(const __grid_constant__ NormArgs p, int parts) {
+    extern __shared__ __align__(16) uint4 ring[];
     __shared__ uint64_t turns[D / 2];
     __shared__ __align__(16) float weights[2 * D];
     const int tid = threadIdx.x;
-    norm_tables<T, D>(p, turns, weights, tid, kNormThreads);
+    norm_tables<T, D, INTER>(p, turns, weights, tid, kNormThreads);
     __syncthreads();
-    norm_forward<T, D, INTER>(p, turns, weights, blockIdx.x * (kNormThreads / 32) + (tid >> 5),
-                              gridDim.x * (kNormThreads / 32), parts, tid & 31);
+    norm_forward<T, D, INTER>(p, turns, weights, ring, blockIdx.x * (kNormThreads / 32) + (tid >> 5),
+                              gridDim.x * (kNormThreads / 32), parts, tid >> 5, tid & 31);
 }
 
+template <typename T>
+constexpr int kBwdStages = sizeof(T) == 2 ? 5 : 3;
+template <typename T>
+constexpr int kBwdRing = kNormThreads / 32 * kBwdStages<T> * 2 * NormRaw<T>::PIECES * 32 * 16;
+
 template <typename T, int D, bool INTER>
-__global__ void __launch_bounds__(kNormThreads) fa_norm_bwd_kernel(const __grid_constant__ NormArgs p, int parts) {
+__global__ void __launch_bounds__(kNormThreads, 2) fa_norm_bwd_kernel(const __grid_constant__ NormArgs p, int parts) {
     using L = NormLane<D, INTER>;
-    constexpr int WARPS = kNormThreads / 32;
+    constexpr int WARPS = kNormThreads / 32, S = kBwdStages<T>, PIECES = NormRaw<T>::PIECES;
+    extern __shared__ __align__(16) uint4 rings[];
     __shared__ uint64_t turns[D / 2];
     __shared__ __align__(16) float weights[2 * D];
     __shared__ __align__(16) float sums[WARPS][D];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    norm_tables<T, D>(p, turns, weights, tid, kNormThreads);
+    norm_tables<T, D, INTER>(p, turns, weights, tid, kNormThreads);
     if (blockIdx.x == 0 && tid == 0) *p.status = 0;
     __syncthreads();
     const L ln(lane, p.rot);
     uint64_t f[L::OWN];
-#pragma unroll
-    for (int i = 0; i < L::OWN; ++i) {
-        const int at = ln.freq(ln.g * L::OWN + i);
-        f[i] = at < p.rot / 2 ? turns[at] : 0ull;
-    }
+    lane_turns<D, INTER>(ln, turns, p.rot, f);
+    uint4* ring = rings + warp * S * 2 * PIECES * 32 + lane;
     const long long items = static_cast<long long>(p.tokens) * parts;
+    const int w = blockIdx.x * WARPS + warp, nw = gridDim.x * WARPS;
     for (int ten = 0; ten < 2; ++ten) {  // q, then k: one set of sums in registers
         const NormRows rx = ten ? p.k : p.q, ru = ten ? p.k_out : p.q_out, rd = ten ? p.dk : p.dq;
         const int H = ten ? p.Hkv : p.Hq, np = (H + L::RPW - 1) / L::RPW;
         const bool has_w = ten ? p.k_weight : p.q_weight;
-        float acc[16];
+        auto row = [&](const NormRows& r, const NormCursor& c) {
+            return static_cast<T*>(r.data) + c.b * r.batch + (c.pass * L::RPW + ln.g) * r.head + c.n * r.token;
+        };
+        NormVec acc = {};
+        NormCursor in{w}, at{w};
+        bool more = in.open(p, items, parts, np);
+        int slot = 0, next = 0;
+        auto issue = [&] {
+            if (more) {
+                if (in.pass * L::RPW + ln.g < H) {
+                    const T* u = row(ru, in);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-        for (long long it = blockIdx.x * WARPS + warp; it < items; it += gridDim.x * WARPS) {
-            const int t = static_cast<int>(parts == 1 ? it : div_short(it, parts));
-            const int part = static_cast<int>(it - static_cast<long long>(t) * parts);
-            int b = 0, n = t, pos;
-            if (p.cu_seqlens) {
-                const int s = warp_find(p.cu_seqlens, p.B, t, lane);
-                if (t < p.cu_seqlens[s] || t >= p.cu_seqlens[s + 1]) continue;
-                pos = packed_position(p, s, t);
-            } else {
-                b = p.by_n.div(t);
-                n = pos = t - b * p.N;
-                if (p.ends) pos = static_cast<int>(static_cast<uint32_t>(p.ends[b]) - static_cast<uint32_t>(p.N - n));
-            }
-            const int p0 = np * part / parts, p1 = np * (part + 1) / parts;
-            const T* x_at = static_cast<const T*>(rx.data) + b * rx.batch + n * rx.token;
-            const T* u_at = static_cast<const T*>(ru.data) + b * ru.batch + n * ru.token;
-            T* d_at = static_cast<T*>(rd.data) + b * rd.batch + n * rd.token;
-            NormRaw<T> next_u, next_x;
-            auto load = [&](int pass) {
-                next_u.zero();
-                next_x.zero();
-                const int h = pass * L::RPW + ln.g;
-                if (pass < p1 && h < H) {
-                    next_u.load(u_at + h * ru.head, ln.a, ln.b);
-                    if (has_w) next_x.load(x_at + h * rx.head, ln.a, ln.b);
+                    for (int i = 0; i < PIECES; ++i)
+                        cp_async16(ring + (next * 2 * PIECES + i) * 32, u + NormRaw<T>::at(i, ln.a, ln.b));
+                    if (has_w) {
+                        const T* x = row(rx, in);
+#pragma unroll
+                        for (int i = 0; i < PIECES; ++i)
+                            cp_async16(ring + ((next * 2 + 1) * PIECES + i) * 32, x + NormRaw<T>::at(i, ln.a, ln.b));
+                    }
                 }
-            };
-            load(p0);
+                if (++in.pass == in.end) {
+                    in.it += nw;
+                    more = in.open(p, items, parts, np);
+                }
+            }
+            norm_commit();
+            next = next + 1 == S ? 0 : next + 1;
+        };
+#pragma unroll 1
+        for (int i = 0; i < S - 1; ++i) issue();
+        for (; at.open(p, items, parts, np); at.it += nw) {
+            int pos;
+            const bool there = at.position(p, lane, pos);
             NormTurn turn;
             warp_turn<D, INTER>(ln, f, pos, turn);
-            for (int pass = p0; pass < p1; ++pass) {
-                NormRaw<T> raw = next_u;
-                float u[16], x[16];
-                raw.get(u);
-                next_x.get(x);
-                load(pass + 1);
-                rotate_row<INTER, true>(u, turn);
-                if (has_w) {
-                    float sc, y[16];
-                    const float r = row_rms<D, L::TPR>(x, p.eps, sc);
-                    lds_row(y, weights + ten * D, ln.a, ln.b);
-                    float dot = 0.f;
+            for (; at.pass < at.end; ++at.pass) {
+                norm_wait<S - 2>();
+                const bool mine = there && at.pass * L::RPW + ln.g < H;
+                NormRaw<T> raw;
+                NormVec u, x;
+                raw.zero();
+                if (mine && has_w) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        x[i] *= r;
-                        acc[i] = fmaf(u[i], x[i], acc[i]);
-                        u[i] *= y[i];
-                        dot = fmaf(u[i], x[i], dot);
-                    }
-                    dot = row_sum<L::TPR>(dot) * (1.f / D);
-                    const float rs = r * sc;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) u[i] = rs * fmaf(-dot, x[i], u[i]);
+                    for (int i = 0; i < PIECES; ++i) raw.w[i] = ring[((slot * 2 + 1) * PIECES + i) * 32];
                 }
-                raw.set(u);
-                const int h = pass * L::RPW + ln.g;
-                if (h < H) raw.store(d_at + h * rd.head, ln.a, ln.b);
+                raw.template get<INTER>(x);
+                raw.zero();
+                if (mine) {
+#pragma unroll
+                    for (int i = 0; i < PIECES; ++i) raw.w[i] = ring[(slot * 2 * PIECES + i) * 32];
+                }
+                raw.template get<INTER>(u);
+                slot = slot + 1 == S ? 0 : slot + 1;
+                issue();  // into the slot of the step before this one
+                rotate_row<true>(u, turn);
+                if (has_w) {
+                    float sc;
+                    NormVec y;
+                    const float r = row_rms<D, L::TPR>(x, p.eps, sc);
+                    lds_row<INTER>(y, weights + ten * D, ln.a, ln.b);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        x[i] = f2_mul(x[i], f2_all(r));
+                        acc[i] = f2_fma(u[i], x[i], acc[i]);
+                        u[i] = f2_mul(u[i], y[i]);
+                    }
+                    const float dot = row_dot<L::TPR>(u, x) * (-1.f / D), rs = r * sc;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) u[i] = f2_mul(f2_fma(f2_all(dot), x[i], u[i]), f2_all(rs));
+                }
+                raw.template set<INTER>(u);
+                if (mine) raw.store(row(rd, at), ln.a, ln.b);
             }
         }
+        norm_wait<0>();
         if (!has_w) continue;
         // this CTA's sums, in a fixed order
+        float a[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+        for (int i = 0; i < 8; ++i) f2_split(acc[i], a[2 * i], a[2 * i + 1]);
 #pragma unroll
-            for (int off = L::TPR; off < 32; off <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], off);
-        if (ln.g == 0) {
+        for (int i = 0; i < 16; ++i) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) sums[warp][(i < 8 ? ln.a : ln.b) + (i & 7)] = acc[i];
+            for (int off = L::TPR; off < 32; off <<= 1) a[i] += __shfl_xor_sync(0xffffffffu, a[i], off);
+            // element of u (i < 8) or v of pair i & 7
+            const int k = i & 7;
+            const int e = INTER ? (k < 4 ? ln.a : ln.b) + 2 * (k & 3) + (i >> 3) : (i < 8 ? ln.a : ln.b) + k;
+            if (ln.g == 0) sums[warp][e] = a[i];
         }
         __syncthreads();
         if (tid < D) {
@@ -160,21 +184,39 @@ static int norm_parts(const NormArgs& a, int warps, int passes) {
 static int passes_of(int heads, int d) { return (heads * (d / 16) + 31) / 32; }
 
 template <typename T, int D, bool INTER>
-static void launch_fwd(const NormArgs& a, cudaStream_t stream) {
-    const int most = 152 * 4, parts = norm_parts(a, most * 8, passes_of(a.Hq, D) + passes_of(a.Hkv, D));
-    const long long ctas = (static_cast<long long>(a.tokens) * parts + 7) / 8;
-    fa_norm_kernel<T, D, INTER><<<static_cast<unsigned>(ctas < most ? ctas : most), kNormThreads, 0, stream>>>(a, parts);
+static cudaError_t launch_fwd(const NormArgs& a, cudaStream_t stream) {
+    const int most = 152 * (sizeof(T) == 2 ? 4 : 3), warps = kNormThreads / 32;
+    const int parts = norm_parts(a, most * warps, passes_of(a.Hq, D) + passes_of(a.Hkv, D));
+    const long long ctas = (static_cast<long long>(a.tokens) * parts + warps - 1) / warps;
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = once_per_device(done, [] {
+        return cudaFuncSetAttribute(fa_norm_kernel<T, D, INTER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kNormRing<T>);
+    });
+    if (e != cudaSuccess) return e;
+    fa_norm_kernel<T, D, INTER>
+        <<<static_cast<unsigned>(ctas < most ? ctas : most), kNormThreads, kNormRing<T>, stream>>>(a, parts);
+    return cudaGetLastError();
 }
 
 template <typename T, int D, bool INTER>
-static int launch_bwd(const NormArgs& a, cudaStream_t stream) {
-    const int parts = norm_parts(a, kNormBwdCtas * 8, passes_of(a.Hq, D));
-    const long long want = (static_cast<long long>(a.tokens) * parts + 7) / 8;
+static cudaError_t launch_bwd(const NormArgs& a, cudaStream_t stream, int* nlaunch) {
+    const int warps = kNormThreads / 32, parts = norm_parts(a, kNormBwdCtas * warps, passes_of(a.Hq, D));
+    const long long want = (static_cast<long long>(a.tokens) * parts + warps - 1) / warps;
     const int ctas = static_cast<int>(want < kNormBwdCtas ? want : kNormBwdCtas);
-    fa_norm_bwd_kernel<T, D, INTER><<<ctas, kNormThreads, 0, stream>>>(a, parts);
-    if (!a.q_weight && !a.k_weight) return 1;
-    fa_norm_bwd_sum_kernel<<<2 * D / 32, 1024, 0, stream>>>(a, ctas);
-    return 2;
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = once_per_device(done, [] {
+        return cudaFuncSetAttribute(fa_norm_bwd_kernel<T, D, INTER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kBwdRing<T>);
+    });
+    if (e != cudaSuccess) return e;
+    fa_norm_bwd_kernel<T, D, INTER><<<ctas, kNormThreads, kBwdRing<T>, stream>>>(a, parts);
+    *nlaunch = 1;
+    if (a.q_weight || a.k_weight) {
+        fa_norm_bwd_sum_kernel<<<2 * D / 32, 1024, 0, stream>>>(a, ctas);
+        *nlaunch = 2;
+    }
+    return cudaGetLastError();
 }
 
 template <typename F>
@@ -191,18 +233,20 @@ static void dispatch(const NormArgs& a, F&& f) {
 }
 
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream, int* nlaunch) {
-    dispatch(a, [&](auto t, auto d, auto inter) {
-        launch_fwd<decltype(t), decltype(d)::value, decltype(inter)::value>(a, stream);
-    });
+    cudaError_t e = cudaSuccess;
     *nlaunch = 1;
-    return cudaGetLastError();
+    dispatch(a, [&](auto t, auto d, auto inter) {
+        e = launch_fwd<decltype(t), decltype(d)::value, decltype(inter)::value>(a, stream);
+    });
+    return e;
 }
 
 cudaError_t launch_norm_bwd(const NormArgs& a, cudaStream_t stream, int* nlaunch) {
+    cudaError_t e = cudaSuccess;
     dispatch(a, [&](auto t, auto d, auto inter) {
-        *nlaunch = launch_bwd<decltype(t), decltype(d)::value, decltype(inter)::value>(a, stream);
+        e = launch_bwd<decltype(t), decltype(d)::value, decltype(inter)::value>(a, stream, nlaunch);
     });
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace fa

@@ -89,8 +89,9 @@ struct NormLane {
     }
 };
 
+// Cosines and sines of a lane's eight angles, two to a word.
 struct NormTurn {
-    float c[8], s[8];
+    uint64_t c[4], s[4];
 };
 
 // Angles of a token that all rows of the warp share: each lane computes OWN of
@@ -99,26 +100,37 @@ template <int D, bool INTER>
 __device__ __forceinline__ void warp_turn(const NormLane<D, INTER>& ln, const uint64_t (&f)[NormLane<D, INTER>::OWN],
                                           int pos, NormTurn& t) {
     using L = NormLane<D, INTER>;
-    float c[L::OWN], s[L::OWN];
+    float c[L::OWN], s[L::OWN], cc[8], ss[8];
 #pragma unroll
     for (int i = 0; i < L::OWN; ++i) turn_cos_sin(static_cast<uint64_t>(static_cast<int64_t>(pos)) * f[i], c[i], s[i]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int from = (i / L::OWN) * L::TPR + ln.j;
-        t.c[i] = __shfl_sync(0xffffffffu, c[i % L::OWN], from);
-        t.s[i] = __shfl_sync(0xffffffffu, s[i % L::OWN], from);
+        cc[i] = __shfl_sync(0xffffffffu, c[i % L::OWN], from);
+        ss[i] = __shfl_sync(0xffffffffu, s[i % L::OWN], from);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        t.c[i] = f2_make(cc[2 * i], cc[2 * i + 1]);
+        t.s[i] = f2_make(ss[2 * i], ss[2 * i + 1]);
     }
 }
 
-// x[0..7]: chunk a, x[8..15]: chunk b. Rotated by +angle, or by -angle (BACK).
-template <bool INTER, bool BACK>
-__device__ __forceinline__ void rotate_row(float (&x)[16], const NormTurn& t) {
+// A lane's sixteen elements, two to a word: the first elements u of its pairs in
+// x[0..3], the second ones v in x[4..7].
+typedef uint64_t NormVec[8];
+
+__device__ __forceinline__ uint64_t f2_neg(uint64_t x) { return x ^ 0x8000000080000000ull; }
+__device__ __forceinline__ uint64_t f2_all(float x) { return f2_make(x, x); }
+
+// Rotated by +angle, or by -angle (BACK).
+template <bool BACK>
+__device__ __forceinline__ void rotate_row(NormVec& x, const NormTurn& t) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int u = INTER ? 2 * i : i, v = INTER ? 2 * i + 1 : i + 8;
-        const float s = BACK ? -t.s[i] : t.s[i], a = x[u], b = x[v];
-        x[u] = fmaf(a, t.c[i], -(b * s));
-        x[v] = fmaf(a, s, b * t.c[i]);
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t s = BACK ? f2_neg(t.s[i]) : t.s[i], u = x[i], v = x[i + 4];
+        x[i] = f2_fma(u, t.c[i], f2_neg(f2_mul(v, s)));
+        x[i + 4] = f2_fma(u, s, f2_mul(v, t.c[i]));
     }
 }
 
@@ -128,91 +140,103 @@ __device__ __forceinline__ float row_sum(float x) {
     for (int off = 1; off < TPR; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
     return x;
 }
+// Sum over the row of the products of two lanes' elements.
+template <int TPR>
+__device__ __forceinline__ float row_dot(const NormVec& x, const NormVec& y) {
+    uint64_t a = f2_mul(x[0], y[0]), b = f2_mul(x[1], y[1]);
+#pragma unroll
+    for (int i = 2; i < 8; i += 2) {
+        a = f2_fma(x[i], y[i], a);
+        b = f2_fma(x[i + 1], y[i + 1], b);
+    }
+    float lo, hi;
+    f2_split(f2_add(a, b), lo, hi);
+    return row_sum<TPR>(lo + hi);
+}
 
 // r with 1 / sqrt(mean x^2 + eps) = f r, x then being scaled by f: 1 but for a
 // row whose squares leave fp32's range.
 template <int D, int TPR>
-__device__ __forceinline__ float row_rms(float (&x)[16], float eps, float& f) {
-    auto squares = [&] {
-        float a = 0.f, b = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            a = fmaf(x[i], x[i], a);
-            b = fmaf(x[i + 8], x[i + 8], b);
-        }
-        return row_sum<TPR>(a + b);
-    };
-    float ss = squares();
+__device__ __forceinline__ float row_rms(NormVec& x, float eps, float& f) {
+    float ss = row_dot<TPR>(x, x);
     const bool big = ss > 1e38f;
     f = big ? 0x1p-70f : 1.f;
     if (__any_sync(0xffffffffu, big)) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] *= f;
-        ss = squares();
+        for (int i = 0; i < 8; ++i) x[i] = f2_mul(x[i], f2_all(f));
+        ss = row_dot<TPR>(x, x);
+        eps = eps * f * f;
     }
-    return rsqrtf(fmaf(ss, 1.f / D, eps * f * f));
+    return rsqrtf(fmaf(ss, 1.f / D, eps));
 }
 
 // The raw words of a lane's two chunks.
 template <typename T>
-struct NormRaw;
-template <>
-struct NormRaw<uint16_t> {
-    uint4 w[2];
-    __device__ __forceinline__ void zero() { w[0] = w[1] = make_uint4(0u, 0u, 0u, 0u); }
-    __device__ __forceinline__ void load(const uint16_t* row, int a, int b) {
-        w[0] = *reinterpret_cast<const uint4*>(row + a);
-        w[1] = *reinterpret_cast<const uint4*>(row + b);
+struct NormRaw {
+    static constexpr int PIECES = sizeof(T);  // of 16 bytes
+    uint4 w[PIECES];
+    // first element of piece i
+    __device__ __forceinline__ static int at(int i, int a, int b) {
+        return sizeof(T) == 2 ? (i ? b : a) : (i < 2 ? a : b) + 4 * (i & 1);
     }
-    __device__ __forceinline__ void get(float (&x)[16]) const {
+    __device__ __forceinline__ void zero() {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            const uint32_t v[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+        for (int i = 0; i < PIECES; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ void load(const T* row, int a, int b) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[8 * c + 2 * i] = __uint_as_float(v[i] << 16);
-                x[8 * c + 2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+        for (int i = 0; i < PIECES; ++i) w[i] = *reinterpret_cast<const uint4*>(row + at(i, a, b));
+    }
+    __device__ __forceinline__ void store(T* row, int a, int b) const {
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) *reinterpret_cast<uint4*>(row + at(i, a, b)) = w[i];
+    }
+    // Word i of eight (bf16) or sixteen (fp32).
+    __device__ __forceinline__ uint32_t word(int i) const {
+        const uint4& v = w[i >> 2];
+        return (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
+    }
+    template <bool INTER>
+    __device__ __forceinline__ void get(NormVec& x) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 2) {
+                if constexpr (INTER) {
+                    const uint32_t p = word(2 * i), q = word(2 * i + 1);
+                    x[i] = f2_make(__uint_as_float(p << 16), __uint_as_float(q << 16));
+                    x[i + 4] = f2_make(__uint_as_float(p & 0xFFFF0000u), __uint_as_float(q & 0xFFFF0000u));
+                } else {
+                    x[i] = f2_from_bf16x2(word(i));
+                    x[i + 4] = f2_from_bf16x2(word(i + 4));
+                }
+            } else {
+                const int u = INTER ? 4 * i : 2 * i, v = INTER ? 4 * i + 1 : 8 + 2 * i, next = INTER ? 2 : 1;
+                x[i] = f2_make(__uint_as_float(word(u)), __uint_as_float(word(u + next)));
+                x[i + 4] = f2_make(__uint_as_float(word(v)), __uint_as_float(word(v + next)));
             }
         }
     }
-    __device__ __forceinline__ void set(const float (&x)[16]) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-            w[c] = make_uint4(pack_bf16x2(x[8 * c], x[8 * c + 1]), pack_bf16x2(x[8 * c + 2], x[8 * c + 3]),
-                              pack_bf16x2(x[8 * c + 4], x[8 * c + 5]), pack_bf16x2(x[8 * c + 6], x[8 * c + 7]));
-    }
-    __device__ __forceinline__ void store(uint16_t* row, int a, int b) const {
-        *reinterpret_cast<uint4*>(row + a) = w[0];
-        *reinterpret_cast<uint4*>(row + b) = w[1];
-    }
-};
-template <>
-struct NormRaw<float> {
-    float4 w[4];
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    __device__ __forceinline__ void load(const float* row, int a, int b) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(row + (i < 2 ? a : b) + 4 * (i & 1));
-    }
-    __device__ __forceinline__ void get(float (&x)[16]) const {
+    template <bool INTER>
+    __device__ __forceinline__ void set(const NormVec& x) {
+        uint32_t y[4 * PIECES];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            x[4 * i] = w[i].x;
-            x[4 * i + 1] = w[i].y;
-            x[4 * i + 2] = w[i].z;
-            x[4 * i + 3] = w[i].w;
+            float u0, u1, v0, v1;
+            f2_split(x[i], u0, u1);
+            f2_split(x[i + 4], v0, v1);
+            if constexpr (sizeof(T) == 2) {
+                y[INTER ? 2 * i : i] = INTER ? pack_bf16x2(u0, v0) : pack_bf16x2(u0, u1);
+                y[INTER ? 2 * i + 1 : i + 4] = INTER ? pack_bf16x2(u1, v1) : pack_bf16x2(v0, v1);
+            } else {
+                const int u = INTER ? 4 * i : 2 * i, v = INTER ? 4 * i + 1 : 8 + 2 * i, next = INTER ? 2 : 1;
+                y[u] = __float_as_uint(u0);
+                y[u + next] = __float_as_uint(u1);
+                y[v] = __float_as_uint(v0);
+                y[v + next] = __float_as_uint(v1);
+            }
         }
-    }
-    __device__ __forceinline__ void set(const float (&x)[16]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-    }
-    __device__ __forceinline__ void store(float* row, int a, int b) const {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(row + (i < 2 ? a : b) + 4 * (i & 1)) = w[i];
+        for (int i = 0; i < PIECES; ++i) w[i] = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
     }
 };
 
@@ -221,96 +245,165 @@ __device__ __forceinline__ float norm_weight(const T* w, int i) {
     if constexpr (sizeof(T) == 2) return __uint_as_float(static_cast<uint32_t>(w[i]) << 16);
     else return w[i];
 }
-
-// Eight floats at a and eight at b of a row of D floats in shared memory.
-__device__ __forceinline__ void lds_row(float (&y)[16], const float* row, int a, int b) {
+// Where a row of weights in shared memory has element i: in the order of NormVec
+// within each chunk of eight.
+template <bool INTER>
+__device__ __forceinline__ int norm_place(int i) {
+    return INTER ? (i & ~7) | ((i & 1) << 2) | ((i >> 1) & 3) : i;
+}
+template <bool INTER>
+__device__ __forceinline__ void lds_row(NormVec& y, const float* row, int a, int b) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 v = *reinterpret_cast<const float4*>(row + (i < 2 ? a : b) + 4 * (i & 1));
-        y[4 * i] = v.x;
-        y[4 * i + 1] = v.y;
-        y[4 * i + 2] = v.z;
-        y[4 * i + 3] = v.w;
+    for (int i = 0; i < 4; ++i) {  // INTER: u of a, u of b, v of a, v of b
+        const int at = INTER ? (i & 1 ? b : a) + 4 * (i >> 1) : (i < 2 ? a : b) + 4 * (i & 1);
+        const float4 v = *reinterpret_cast<const float4*>(row + at);
+        y[2 * i] = f2_make(v.x, v.y);
+        y[2 * i + 1] = f2_make(v.z, v.w);
     }
 }
 
 // One row of the forward: x / rms(x) * w (w null: x as it is), rotated.
 template <int D, bool INTER>
-__device__ __forceinline__ void norm_row(float (&x)[16], const float* w, const NormLane<D, INTER>& ln, float eps,
+__device__ __forceinline__ void norm_row(NormVec& x, const float* w, const NormLane<D, INTER>& ln, float eps,
                                          const NormTurn& t) {
     if (w) {
-        float f, y[16];
+        float f;
+        NormVec y;
         const float r = row_rms<D, NormLane<D, INTER>::TPR>(x, eps, f);
-        lds_row(y, w, ln.a, ln.b);
+        lds_row<INTER>(y, w, ln.a, ln.b);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = x[i] * r * y[i];
+        for (int i = 0; i < 8; ++i) x[i] = f2_mul(f2_mul(x[i], f2_all(r)), y[i]);
     }
-    rotate_row<INTER, false>(x, t);
+    rotate_row<false>(x, t);
 }
 
-// Tokens' rows [pass * RPW, + RPW) of q and then of k, for warp `w` of `nw`.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void norm_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>  // all but the newest N groups of this thread have landed
+__device__ __forceinline__ void norm_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Where a warp stands among its items: steps [pass, end) of token (b, n).
+struct NormCursor {
+    long long it;
+    int t, b, n, pass, end;
+    __device__ __forceinline__ bool open(const NormArgs& p, long long items, int parts, int np) {
+        if (it >= items) return false;
+        t = static_cast<int>(parts == 1 ? it : div_short(it, parts));
+        const int part = static_cast<int>(it - static_cast<long long>(t) * parts);
+        b = p.cu_seqlens ? 0 : p.by_n.div(t);
+        n = p.cu_seqlens ? t : t - b * p.N;
+        pass = np * part / parts;
+        end = np * (part + 1) / parts;
+        return true;
+    }
+    // Position of the token; false if it is of no sequence.
+    __device__ __forceinline__ bool position(const NormArgs& p, int lane, int& pos) const {
+        if (p.cu_seqlens) {
+            const int s = warp_find(p.cu_seqlens, p.B, t, lane);
+            pos = packed_position(p, s, t);
+            return t >= p.cu_seqlens[s] && t < p.cu_seqlens[s + 1];
+        }
+        pos = p.ends ? static_cast<int>(static_cast<uint32_t>(p.ends[b]) - static_cast<uint32_t>(p.N - n)) : n;
+        return true;
+    }
+};
+
+// A lane's frequencies: the OWN that it computes for its warp.
+template <int D, bool INTER>
+__device__ __forceinline__ void lane_turns(const NormLane<D, INTER>& ln, const uint64_t* turns, int rot,
+                                           uint64_t (&f)[NormLane<D, INTER>::OWN]) {
+    constexpr int OWN = NormLane<D, INTER>::OWN;
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) {
+        const int at = ln.freq(ln.g * OWN + i);
+        f[i] = at < rot / 2 ? turns[at] : 0ull;
+    }
+}
+
+// Stages of a warp's ring in shared memory: the rows of a step each.
+template <typename T>
+constexpr int kNormStages = sizeof(T) == 2 ? 6 : 3;
+template <typename T>
+constexpr int kNormRing = kNormThreads / 32 * kNormStages<T> * NormRaw<T>::PIECES * 32 * 16;  // bytes
+
+// Tokens' rows, RPW heads a step, first q's and then k's, for warp `w` of `nw`.
+// Each lane copies its own pieces of the steps to come into shared memory and
+// reads them back itself: no barriers.
 template <typename T, int D, bool INTER>
-__device__ __forceinline__ void norm_forward(const NormArgs& p, const uint64_t* turns, const float* weights, int w,
-                                             int nw, int parts, int lane) {
+__device__ __forceinline__ void norm_forward(const NormArgs& p, const uint64_t* turns, const float* weights,
+                                             uint4* ring, int w, int nw, int parts, int warp, int lane) {
     using L = NormLane<D, INTER>;
+    constexpr int S = kNormStages<T>, PIECES = NormRaw<T>::PIECES;
     const L ln(lane, p.rot);
     uint64_t f[L::OWN];
-#pragma unroll
-    for (int i = 0; i < L::OWN; ++i) {
-        const int at = ln.freq(ln.g * L::OWN + i);
-        f[i] = at < p.rot / 2 ? turns[at] : 0ull;
-    }
-    const int pq = (p.Hq + L::RPW - 1) / L::RPW, pk = (p.Hkv + L::RPW - 1) / L::RPW, np = pq + pk;
+    lane_turns<D, INTER>(ln, turns, p.rot, f);
+    ring += warp * S * PIECES * 32 + lane;
+    const int pq = (p.Hq + L::RPW - 1) / L::RPW, np = pq + (p.Hkv + L::RPW - 1) / L::RPW;
     const float* wq = p.q_weight ? weights : nullptr;
     const float* wk = p.k_weight ? weights + D : nullptr;
     const long long items = static_cast<long long>(p.tokens) * parts;
-    for (long long it = w; it < items; it += nw) {
-        const int t = static_cast<int>(parts == 1 ? it : div_short(it, parts));
-        const int part = static_cast<int>(it - static_cast<long long>(t) * parts);
-        int b = 0, n = t, pos;
-        if (p.cu_seqlens) {
-            const int s = warp_find(p.cu_seqlens, p.B, t, lane);
-            if (t < p.cu_seqlens[s] || t >= p.cu_seqlens[s + 1]) continue;  // of no sequence: left as it is
-            pos = packed_position(p, s, t);
-        } else {
-            b = p.by_n.div(t);
-            n = pos = t - b * p.N;
-            if (p.ends) pos = static_cast<int>(static_cast<uint32_t>(p.ends[b]) - static_cast<uint32_t>(p.N - n));
+    auto row = [&](const NormRows& q, const NormRows& k, const NormCursor& c, T*& at) {
+        const bool is_k = c.pass >= pq;
+        const int h = (is_k ? c.pass - pq : c.pass) * L::RPW + ln.g;
+        const NormRows& r = is_k ? k : q;
+        at = static_cast<T*>(r.data) + c.b * r.batch + h * r.head + c.n * r.token;
+        return h < (is_k ? p.Hkv : p.Hq);
+    };
+    NormCursor in{w}, at{w};
+    bool more = in.open(p, items, parts, np);
+    int slot = 0, next = 0;
+    auto issue = [&] {
+        T* src;
+        if (more) {
+            if (row(p.q, p.k, in, src)) {
+#pragma unroll
+                for (int i = 0; i < PIECES; ++i)
+                    cp_async16(ring + (next * PIECES + i) * 32, src + NormRaw<T>::at(i, ln.a, ln.b));
+            }
+            if (++in.pass == in.end) {
+                in.it += nw;
+                more = in.open(p, items, parts, np);
+            }
         }
-        const int p0 = np * part / parts, p1 = np * (part + 1) / parts;
-        auto row = [&](const NormRows& q, const NormRows& k, int pass, T*& at) {
-            const bool is_k = pass >= pq;
-            const int h = (is_k ? pass - pq : pass) * L::RPW + ln.g;
-            const NormRows& r = is_k ? k : q;
-            at = static_cast<T*>(r.data) + b * r.batch + h * r.head + n * r.token;
-            return h < (is_k ? p.Hkv : p.Hq);
-        };
-        NormRaw<T> next;
-        T* at;
-        next.zero();
-        if (row(p.q, p.k, p0, at)) next.load(at, ln.a, ln.b);
+        norm_commit();
+        next = next + 1 == S ? 0 : next + 1;
+    };
+#pragma unroll 1
+    for (int i = 0; i < S - 1; ++i) issue();
+    for (; at.open(p, items, parts, np); at.it += nw) {
+        int pos;
+        const bool there = at.position(p, lane, pos);
         NormTurn turn;
         warp_turn<D, INTER>(ln, f, pos, turn);
-        for (int pass = p0; pass < p1; ++pass) {
-            NormRaw<T> raw = next;
-            next.zero();
-            if (pass + 1 < p1 && row(p.q, p.k, pass + 1, at)) next.load(at, ln.a, ln.b);
-            float x[16];
-            raw.get(x);
-            norm_row<D, INTER>(x, pass >= pq ? wk : wq, ln, p.eps, turn);
-            raw.set(x);
-            if (row(p.q_out, p.k_out, pass, at)) raw.store(at, ln.a, ln.b);
+        for (; at.pass < at.end; ++at.pass) {
+            norm_wait<S - 2>();
+            NormRaw<T> raw;
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) raw.w[i] = ring[(slot * PIECES + i) * 32];
+            slot = slot + 1 == S ? 0 : slot + 1;
+            issue();  // into the slot of the step before this one
+            NormVec x;
+            raw.template get<INTER>(x);
+            norm_row<D, INTER>(x, at.pass >= pq ? wk : wq, ln, p.eps, turn);
+            raw.template set<INTER>(x);
+            T* dst;
+            if (row(p.q_out, p.k_out, at, dst) && there) raw.store(dst, ln.a, ln.b);
         }
     }
+    norm_wait<0>();
 }
 
 // Fractions of a turn and the weights in fp32, into shared memory. The caller synchronises.
-template <typename T, int D>
+template <typename T, int D, bool INTER>
 __device__ __forceinline__ void norm_tables(const NormArgs& p, uint64_t* turns, float* weights, int tid, int threads) {
     for (int i = tid; i < p.rot / 2; i += threads) turns[i] = turn_fraction(p.inv_freq[i]);
     for (int i = tid; i < 2 * D; i += threads) {
         const T* w = static_cast<const T*>(i < D ? p.q_weight : p.k_weight);
-        if (w) weights[i] = norm_weight(w, i < D ? i : i - D);
+        if (w) weights[(i & ~(D - 1)) + norm_place<INTER>(i & (D - 1))] = norm_weight(w, i & (D - 1));
     }
 }
 

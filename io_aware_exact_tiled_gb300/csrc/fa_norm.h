@@ -14,7 +14,7 @@ struct NormRows {
 };
 
 constexpr int kNormThreads = 256;
-constexpr int kNormBwdCtas = 3 * 152;  // partial sums of the weights' gradients
+constexpr int kNormBwdCtas = 2 * 152;  // partial sums of the weights' gradients
 
 struct NormArgs {
     NormRows q, k;              // inputs

@@ -21,9 +21,10 @@ constexpr int kNaSeqs = 1024;  // offsets kept in shared memory
 
 template <int D, bool INTER, int L, int HPC>
 __global__ void __launch_bounds__(256)
-    fa_norm_append_kernel(const __grid_constant__ NormAppendArgs args, int span, int kv_ctas, int q_parts) {
+    fa_norm_append_kernel(const __grid_constant__ NormAppendArgs args, int span, int hpc, int kv_ctas, int q_parts) {
     using LN = NormLane<D, INTER>;
     constexpr int ROWS = 256 / LN::TPR;  // rows of a CTA-wide load
+    extern __shared__ __align__(16) uint4 ring[];
     __shared__ uint64_t turns[D / 2];
     __shared__ __align__(16) float weights[2 * D];
     __shared__ int cu_s[kNaSeqs];
@@ -33,17 +34,18 @@ __global__ void __launch_bounds__(256)
     const NormArgs& p = args.n;
     const AppendArgs& a = args.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    norm_tables<uint16_t, D>(p, turns, weights, tid, 256);
+    norm_tables<uint16_t, D, INTER>(p, turns, weights, tid, 256);
     if (static_cast<int>(blockIdx.x) >= kv_ctas) {
         __syncthreads();
-        norm_forward<uint16_t, D, INTER>(p, turns, weights, (blockIdx.x - kv_ctas) * 8 + warp,
-                                         (gridDim.x - kv_ctas) * 8, q_parts, lane);
+        norm_forward<uint16_t, D, INTER>(p, turns, weights, ring, (blockIdx.x - kv_ctas) * 8 + warp,
+                                         (gridDim.x - kv_ctas) * 8, q_parts, warp, lane);
         return;
     }
-    const int groups = (a.H + HPC - 1) / HPC;
+    const int groups = (a.H + hpc - 1) / hpc;
     // the heads of a span follow one another: they share its rows' DRAM pages
-    const int part = static_cast<int>(blockIdx.x / (2u * groups)), gv = static_cast<int>(blockIdx.x - part * (2u * groups));
-    const int h0 = (gv >> 1) * HPC, nh = min(HPC, a.H - h0);
+    const int part = static_cast<int>(blockIdx.x / (2u * groups));
+    const int gv = static_cast<int>(blockIdx.x - part * (2u * groups));
+    const int h0 = (gv >> 1) * hpc, nh = min(hpc, a.H - h0);
     const int bs = a.block_size, nslots = a.num_blocks * bs, bs_log2 = 31 - __clz(bs);
     const bool is_v = gv & 1;
     const long long t0 = static_cast<long long>(part) * span;
@@ -100,16 +102,22 @@ __global__ void __launch_bounds__(256)
     auto turn_of = [&](int t, NormTurn& turn) {  // this lane's angles of token t
         const uint64_t pos = static_cast<uint64_t>(static_cast<int64_t>(pos_s[t]));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int at = ln.freq(i);
-            turn_cos_sin(pos * (at < p.rot / 2 ? turns[at] : 0ull), turn.c[i], turn.s[i]);
+        for (int i = 0; i < 4; ++i) {
+            float c[2], s[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const int at = ln.freq(2 * i + y);
+                turn_cos_sin(pos * (at < p.rot / 2 ? turns[at] : 0ull), c[y], s[y]);
+            }
+            turn.c[i] = f2_make(c[0], c[1]);
+            turn.s[i] = f2_make(s[0], s[1]);
         }
     };
     auto finish = [&](NormRaw<uint16_t>& raw, const NormTurn& turn) {  // a row of K, in bf16
-        float x[16];
-        raw.get(x);
+        NormVec x;
+        raw.get<INTER>(x);
         norm_row<D, INTER>(x, w, ln, p.eps, turn);
-        raw.set(x);
+        raw.set<INTER>(x);
     };
     auto store = [&](uint8_t* row, const NormRaw<uint16_t>& raw, float inv) {
         *reinterpret_cast<uint2*>(row + ln.a) = append_quantise(raw.w[0], inv);
@@ -209,37 +217,44 @@ __global__ void __launch_bounds__(256)
 }
 
 template <int D, bool INTER, int L>
-static void launch(const NormAppendArgs& a, cudaStream_t stream) {
-    constexpr int HPC = 1;
+static cudaError_t launch(const NormAppendArgs& a, cudaStream_t stream) {
+    constexpr int HPC = L >= 8 ? 1 : L == 4 ? 2 : 4;
     const int total = a.a.total, passes = (a.n.Hq * (D / 16) + 31) / 32;
     const int span = total > 8192 && a.a.block_size * D <= 2048 ? 128 : total > 1024 ? 64 : 16;
-    const unsigned kv = static_cast<unsigned>((total + span - 1) / span) * 2u * ((a.a.H + HPC - 1) / HPC);
+    const int hpc = total > 1024 ? HPC : 1;
+    const unsigned kv = static_cast<unsigned>((total + span - 1) / span) * 2u * ((a.a.H + hpc - 1) / hpc);
     int parts = (152 * 16 + total - 1) / total;
     parts = parts > passes ? passes : parts;
     const long long want = (static_cast<long long>(total) * parts + 7) / 8;
     const unsigned qc = static_cast<unsigned>(want < 152 * 8 ? want : 152 * 8);
-    fa_norm_append_kernel<D, INTER, L, HPC><<<kv + qc, 256, 0, stream>>>(a, span, static_cast<int>(kv), parts);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = once_per_device(done, [] {
+        return cudaFuncSetAttribute(fa_norm_append_kernel<D, INTER, L, HPC>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kNormRing<uint16_t>);
+    });
+    if (e != cudaSuccess) return e;
+    fa_norm_append_kernel<D, INTER, L, HPC>
+        <<<kv + qc, 256, kNormRing<uint16_t>, stream>>>(a, span, hpc, static_cast<int>(kv), parts);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_norm_append(const NormAppendArgs& a, cudaStream_t stream, int* nlaunch) {
-    auto rows = [&](auto inter) {
+    auto rows = [&](auto inter) -> cudaError_t {
         constexpr bool INTER = decltype(inter)::value;
         const int bs = a.a.block_size;
         if (a.n.d == 64) {
-            if (bs <= 64) launch<64, INTER, 1>(a, stream);
-            else if (bs == 128) launch<64, INTER, 2>(a, stream);
-            else launch<64, INTER, 4>(a, stream);
+            if (bs <= 64) return launch<64, INTER, 1>(a, stream);
+            if (bs == 128) return launch<64, INTER, 2>(a, stream);
+            return launch<64, INTER, 4>(a, stream);
         } else {
-            if (bs <= 32) launch<128, INTER, 1>(a, stream);
-            else if (bs == 64) launch<128, INTER, 2>(a, stream);
-            else if (bs == 128) launch<128, INTER, 4>(a, stream);
-            else launch<128, INTER, 8>(a, stream);
+            if (bs <= 32) return launch<128, INTER, 1>(a, stream);
+            if (bs == 64) return launch<128, INTER, 2>(a, stream);
+            if (bs == 128) return launch<128, INTER, 4>(a, stream);
+            return launch<128, INTER, 8>(a, stream);
         }
     };
-    if (a.n.interleaved) rows(std::true_type{});
-    else rows(std::false_type{});
     *nlaunch = 1;
-    return cudaGetLastError();
+    return a.n.interleaved ? rows(std::true_type{}) : rows(std::false_type{});
 }
 
 }  // namespace fa

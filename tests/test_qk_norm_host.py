@@ -1,13 +1,17 @@
 """Norm with rotation and attention with shared prefixes on the CPU: refusals of
 the entry points, workspace sizes, and the binding's argument order and checks."""
 
-import ctypes
+import contextlib
+import inspect
+import struct
 
 import pytest
 import torch
 
+import io_aware_exact_tiled_gb300 as fa
 from io_aware_exact_tiled_gb300 import binding as fb
 from io_aware_exact_tiled_gb300 import build as fbuild
+from io_aware_exact_tiled_gb300 import qk_norm
 
 from test_binding import FakeLib, addr, last
 
@@ -22,7 +26,7 @@ def lib():
 
 
 def rows(data=FAKE, batch=8 * 64 * 4, head=64, token=4 * 64):
-    return ctypes.byref(fb._Rows(data, batch, head, token))
+    return qk_norm._pack_rows(data or 0, batch, head, token)
 
 
 NORM = dict(eps=1e-6, inv_freq=FAKE, rot=64, inter=0, cu=None, ends=None, B=2, N=8, Hq=4, Hkv=4, d=64,
@@ -94,7 +98,7 @@ def test_append_refusals(lib):
         assert append(lib, ptrs={i: None}) == BAD and append(lib, ptrs={i: MIS}) == BAD, i
     assert append(lib, cu=None) == BAD and append(lib, cu=MIS) == BAD
     for i in range(4):
-        for bad in [x for x in ROWS if x is None or x._obj.batch in (8 * 64 * 4,)] + (OVERLAPS[:2] if i == 3 else []):
+        for bad in [x for x in ROWS if x is None or row(x)[1] == 8 * 64 * 4] + (OVERLAPS[:2] if i == 3 else []):
             assert append(lib, r=[bad if x == i else rows() for x in range(4)]) == BAD, (i, bad)
     for kw in (dict(bs=8), dict(bs=48), dict(bs=512), dict(nb=1 << 26)):
         assert append(lib, **kw) == NO, kw
@@ -147,8 +151,7 @@ def fake(monkeypatch):
 
 
 def row(a):
-    r = a._obj
-    return r.data, r.batch, r.head, r.token
+    return struct.unpack("@Pqqq", a)
 
 
 def test_norm_argument_order(fake):
@@ -157,12 +160,12 @@ def test_norm_argument_order(fake):
     q, k, _ = (x.transpose(1, 2) for x in qkv.split([Hq, Hkv, Hkv], 2))
     w, f = torch.ones(d, dtype=torch.bfloat16), torch.ones(16, dtype=torch.float64)
     ends = torch.zeros(B, dtype=torch.int32)
-    q_out, k_out = fb.qk_norm_rope(q, k, f, q_weight=w, ends=ends, eps=0.5, interleaved=True)
+    q_out, k_out = fa.qk_norm_rope(q, k, f, q_weight=w, ends=ends, eps=0.5, interleaved=True)
     a = last(fake, "fa_qk_norm_rope")
     assert row(a[0]) == (addr(q), N * 5 * d, d, 5 * d) and row(a[1])[0] == addr(k)
     assert row(a[2]) == (addr(q_out), Hq * N * d, N * d, d) and row(a[3])[0] == addr(k_out)
     assert a[4:] == [addr(w), None, 0.5, addr(f), 32, 1, None, addr(ends), B, N, Hq, Hkv, d, fb.FA_BF16, None]
-    dq, dk, dqw, dkw = fb.qk_norm_rope_backward(q, k, q_out, k_out, f, q_weight=w)
+    dq, dk, dqw, dkw = fa.qk_norm_rope_backward(q, k, q_out, k_out, f, q_weight=w)
     a = last(fake, "fa_qk_norm_rope_bwd")
     assert [row(x)[0] for x in a[:6]] == [addr(x) for x in (q, k, q_out, k_out, dq, dk)]
     assert a[6:10] == [addr(w), None, addr(dqw), None] and dkw is None and dqw.dtype == torch.float32
@@ -171,7 +174,7 @@ def test_norm_argument_order(fake):
     x = torch.zeros(7, 4, d)
     q, k = x[:, :3], x[:, 3:]
     cu = torch.zeros(3, dtype=torch.int32)
-    fb.qk_norm_rope(q, k, f, cu_seqlens=cu, q_out=q, k_out=k)
+    fa.qk_norm_rope(q, k, f, cu_seqlens=cu, q_out=q, k_out=k)
     a = last(fake, "fa_qk_norm_rope")
     assert row(a[0]) == (addr(q), 0, d, 4 * d) == row(a[2]) and a[10] == addr(cu)
     assert a[12:18] == [2, 7, 3, 1, d, fb.FA_FP32]
@@ -184,13 +187,13 @@ def test_append_and_prefix_argument_order(fake):
     f, w = torch.ones(32, dtype=torch.float64), torch.ones(d, dtype=torch.bfloat16)
     i32 = dict(dtype=torch.int32)
     cu, slots, ends = torch.zeros(B + 1, **i32), torch.zeros(total, **i32), torch.zeros(B, **i32)
-    o = fb.qk_norm_rope_append(q, k, v, c.k, c.v, c.k_scale, c.v_scale, slots, f, cu, ends=ends, k_weight=w)
+    o = fa.qk_norm_rope_append(q, k, v, c.k, c.v, c.k_scale, c.v_scale, slots, f, cu, ends=ends, k_weight=w)
     a = last(fake, "fa_qk_norm_rope_append")
     assert [row(x)[0] for x in a[:4]] == [addr(x) for x in (q, k, v, o)]
     assert a[4:9] == [addr(x) for x in (c.k, c.v, c.k_scale, c.v_scale, slots)] and a[9:11] == [None, addr(w)]
     assert a[11:] == [1e-6, addr(f), 64, 0, addr(cu), addr(ends), B, total, Hq, Hkv, d, nb, bs, None]
     pcu, plen, ptab = torch.zeros(P + 1, **i32), torch.zeros(P, **i32), torch.zeros(P, 5, **i32)
-    y, L = fb.forward_paged_prefix(o, c.k, c.v, c.k_scale, c.v_scale, cu, c.cache_len, c.block_table, pcu, plen, ptab,
+    y, L = fa.forward_paged_prefix(o, c.k, c.v, c.k_scale, c.v_scale, cu, c.cache_len, c.block_table, pcu, plen, ptab,
                                    4, scale=0.5)
     a = last(fake, "fa_fwd_paged_prefix")
     assert a[:13] == [addr(x) for x in (o, c.k, c.v, c.k_scale, c.v_scale, y, L, cu, c.cache_len, c.block_table, pcu,
@@ -202,12 +205,12 @@ def test_append_and_prefix_argument_order(fake):
                 dict(prefix_table=ptab.t()), dict(out=y[:3]), dict(cache_len=cu)):
         kw = dict(prefix_cu=pcu, prefix_len=plen, prefix_table=ptab, cache_len=c.cache_len) | bad
         with pytest.raises(ValueError):
-            fb.forward_paged_prefix(o, c.k, c.v, c.k_scale, c.v_scale, cu, block_table=c.block_table, max_new=4, **kw)
+            fa.forward_paged_prefix(o, c.k, c.v, c.k_scale, c.v_scale, cu, block_table=c.block_table, max_new=4, **kw)
     for bad in (dict(cu_seqlens=None), dict(slots=slots[:2]), dict(v=v[:, :1]), dict(q=q.float()), dict(ends=cu),
                 dict(k=k[:, :1], v=v[:, :1])):
         kw = dict(q=q, k=k, v=v, slots=slots, inv_freq=f, cu_seqlens=cu) | bad
         with pytest.raises(ValueError):
-            fb.qk_norm_rope_append(k_cache=c.k, v_cache=c.v, k_scale=c.k_scale, v_scale=c.v_scale, **kw)
+            fa.qk_norm_rope_append(k_cache=c.k, v_cache=c.v, k_scale=c.k_scale, v_scale=c.v_scale, **kw)
     assert len(fake.calls) == i
 
 
@@ -221,11 +224,47 @@ def test_wrong_norm_tensors_are_refused_before_the_call(fake):
                 dict(cu_seqlens=cu), dict(ends=cu), dict(ends=cu[:2].long()), dict(q_out=q[:, :2]),
                 dict(k_out=k.bfloat16()), dict(q=q[0], k=k[0])):
         with pytest.raises(ValueError):
-            fb.qk_norm_rope(**(dict(q=q, k=k, inv_freq=f) | bad))
+            fa.qk_norm_rope(**(dict(q=q, k=k, inv_freq=f) | bad))
         up = {f"d{c}_out": torch.zeros_like((dict(q=q, k=k) | bad)[c]) for c in "qk"}
         bad = {("d" + c[0] if c in ("q_out", "k_out") else c): x for c, x in bad.items()}
         with pytest.raises(ValueError):
-            fb.qk_norm_rope_backward(**(dict(q=q, k=k, inv_freq=f) | up | bad))
+            fa.qk_norm_rope_backward(**(dict(q=q, k=k, inv_freq=f) | up | bad))
     with pytest.raises(ValueError):
-        fb.qk_norm_rope_backward(q, k, q, k, f, dq_weight=w)
+        fa.qk_norm_rope_backward(q, k, q, k, f, dq_weight=w)
     assert not [c for c in fake.calls if not c[0].endswith("_workspace_size")]
+
+
+def stream_calls():
+    """The calls that take a stream, with no outputs or workspace."""
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32)  # noqa: E731
+    q, f, w = bf(1, 1, 4, 64), torch.ones(32, dtype=torch.float64), bf(64)
+    x, c = bf(1, 1, 64), fb.paged_cache(4, 1, 16, 64, 1, 4, "cpu")
+    return {"qk_norm_rope": (q, q, f, w, w), "qk_norm_rope_backward": (q, q, q, q, f, w, w),
+            "qk_norm_rope_append": (x, x, x, c.k, c.v, c.k_scale, c.v_scale, i32(0), f, i32(0, 1)),
+            "forward_paged_prefix": (x, c.k, c.v, c.k_scale, c.v_scale, i32(0, 1), i32(1), i32(0, -1)[None], i32(0, 1),
+                                     i32(3), i32(1)[None], 1)}
+
+
+@pytest.mark.parametrize("name", list(stream_calls()))
+def test_buffers_are_allocated_on_the_given_stream(monkeypatch, fake, name):
+    now, seen = [None], []
+    args = stream_calls()[name]
+    monkeypatch.setattr(fb, "_stream_handle", lambda stream=None: stream or now[0])
+
+    @contextlib.contextmanager
+    def on(s):
+        now[0] = s
+        yield
+        now[0] = None
+
+    real = torch.empty
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: seen.append(now[0]) or real(*a, **kw))
+    f, mine = getattr(fa, name), 1234
+    assert list(inspect.signature(f).parameters)[-1] == "stream"
+    f(*args, stream=mine)
+    assert set(seen) == {mine} and fake.calls[-1][1][-1] == mine and now == [None]
+    seen.clear()
+    f(*args)
+    assert set(seen) == {None} and fake.calls[-1][1][-1] is None
