@@ -314,7 +314,7 @@ fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
  * included, is as for fa_fwd_paged; offsets, lengths and table entries of the
  * prefixes are checked as those of the requests are. A prefix and a request's
  * own tokens are taken apart: the limits on their v_scale are each one's own.
- * Runs up to four kernels.
+ * Runs up to five kernels.
  */
 size_t fa_fwd_paged_prefix_workspace_size(int B, int P, int Hq, int Hkv, int total, int max_new, int d);
 fa_status fa_fwd_paged_prefix(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,

@@ -711,7 +711,7 @@ fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
 // the results of the prefixes' pass, then both passes' partials.
 struct PrefixWs {
     PagedWs prefix, own;
-    size_t ml, o, bytes;
+    size_t cuts, zeroed, ml, o, bytes;
 };
 
 static PrefixWs prefix_ws(int B, int P, int Hq, int Hkv, int total, int max_new, int d) {
@@ -721,7 +721,9 @@ static PrefixWs prefix_ws(int B, int P, int Hq, int Hkv, int total, int max_new,
     PrefixWs w;
     w.prefix = paged_ws_counters(kStatusBytes, P, Hkv, up);
     w.own = paged_ws_counters(w.prefix.zeroed, B, Hkv, uo);
-    w.ml = w.own.zeroed;
+    w.cuts = w.own.zeroed;
+    w.zeroed = w.cuts + align256(2 * fa::kPagedCtas * sizeof(fa::PagedCut));
+    w.ml = w.zeroed;
     w.o = w.ml + align256(rows * sizeof(float2));
     paged_ws_partials(w.prefix, w.o + align256(rows * d * sizeof(float)), up, d);
     paged_ws_partials(w.own, w.prefix.bytes, uo, d);
@@ -775,6 +777,7 @@ fa_status fa_fwd_paged_prefix(const void* q, const void* k_cache, const void* v_
     a.scale = scale;
     a.join.ml = reinterpret_cast<float2*>(ws + w.ml);
     a.join.o = reinterpret_cast<float*>(ws + w.o);
+    a.join.cuts = reinterpret_cast<fa::PagedCut*>(ws + w.cuts);
     a.join.ngroups = P;
     a.join.requests = B;
     a.ev_begin = g_ev_begin;
@@ -803,7 +806,7 @@ fa_status fa_fwd_paged_prefix(const void* q, const void* k_cache, const void* v_
     a.split_rows = fa::paged_split_rows(max_new, group, d);
     paged_place(a, w.own, ws);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (cudaMemsetAsync(ws, 0, w.own.zeroed, s) != cudaSuccess) return FA_ERR_CUDA;
+    if (cudaMemsetAsync(ws, 0, w.zeroed, s) != cudaSuccess) return FA_ERR_CUDA;
     int n = 0;
     if (total > 0 && max_new > 0) {
         st = map_cuda(fa::launch_fwd_paged_prefix(pre, a, s, &n));

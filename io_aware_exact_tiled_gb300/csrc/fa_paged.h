@@ -40,6 +40,15 @@ struct AppendArgs {
     int total, H, d, num_blocks, block_size;
 };
 
+// A unit of the row-tile kernel whose key tiles were cut between CTAs, for the
+// kernel that merges its pieces: rows row0 .. (token row / G, head hk * G + row %
+// G, of tokens tok0 ..) of at most `rows`, pieces in slots piece(cta), cta = first .. last.
+struct PagedCut {
+    int valid, tok0, row0, rows, hk, first, last, pad;
+    long long line0, quota;
+    __host__ __device__ int piece(int cta) const { return 2 * cta + (line0 <= quota * cta ? 0 : 1); }
+};
+
 // What a call with shared prefixes adds to its two passes (all zero otherwise).
 struct PagedJoin {
     const int32_t* first;   // the prefixes' pass: its request b is requests first[b] .. first[b + 1] - 1
@@ -47,6 +56,7 @@ struct PagedJoin {
     int ngroups, requests;
     float2* ml;             // [total][Hq] of the prefixes' pass: maximum and sum
     float* o;               // [total][Hq][d] of the prefixes' pass, normalised
+    PagedCut* cuts;         // [2 * kPagedCtas], prefixes' pass of the row-tile kernel; zero at the start
 };
 
 struct PagedArgs {
@@ -71,7 +81,22 @@ struct PagedArgs {
     float *tile_pm, *tile_pl;  // [2 * kPagedCtas][kPagedTileRows]
     float* tile_po;            // [2 * kPagedCtas][kPagedTileRows][d]
     cudaEvent_t ev_begin, ev_end;  // optional, recorded around the attention kernels
+    int chained;  // launched while the kernel before it may still run (see paged_wait_before)
 };
+
+inline cudaLaunchConfig_t paged_config(int threads, size_t smem, cudaStream_t stream, bool chained,
+                                       cudaLaunchAttribute* at) {
+    at->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at->val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(kPagedCtas);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = at;
+    cfg.numAttrs = chained ? 1 : 0;
+    return cfg;
+}
 
 // Query rows (new tokens x heads of a group) up to which a request can be the
 // split-key kernel's. Above 24 rows of d = 128 its registers do not hold O (64
@@ -123,6 +148,13 @@ __device__ __forceinline__ long long div_short(long long x, long long d) {
     if (((x | d) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(d);
     return x / d;
 }
+// Programmatic dependent launch: a kernel of a chain may start once every CTA of
+// the one before has let it (paged_let_next), and waits (paged_wait_before) where
+// it needs that one's results, at the latest before it ends, so that the end of
+// the last kernel is the end of all.
+__device__ __forceinline__ void paged_let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void paged_wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Two E4M3 numbers (low 16 bits) to an f16 pair, exactly.
 __device__ __forceinline__ uint32_t f16x2_from_e4m3x2(uint32_t x) {
     uint32_t r;

@@ -214,7 +214,9 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
     __shared__ long long start_line;
     __shared__ int nan_seen, abort_s;
     __shared__ float row_before[PFX ? RT : 1];
+    __shared__ int nmax_s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+    if constexpr (PFX) paged_let_next();
 
     // ---- all chunks, then the lines of long and of short units
     const int per = (p.B + C::THREADS - 1) / C::THREADS;
@@ -235,6 +237,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
     if (tid == 0) {
         abort_s = 0;
         nan_seen = 0;
+        nmax_s = 0;
     }
     if (lane < C::STAGES) mbar_init(&bars[lane], 1);
     fence_barrier_init();
@@ -260,12 +263,18 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
     };
     auto line_short = [&](const PgSeg& s) { return s.nchunk <= T ? static_cast<long long>(p.Hkv) * s.nchunk : 0ll; };
     long long ml_ = 0, ms = 0, ma = 0;  // long, short, all as long ones
+    [[maybe_unused]] int nmax = 0;      // the longest of the short ones
     for (int b = b0; b < b1; ++b) {
         PgSeg s;
         pg_request<PFX>(p, b, s);
         ml_ += line_long(s);
         ms += line_short(s);
         if (s.nchunk > 0) ma += static_cast<long long>(p.Hkv) * (s.nchunk + C::COST);
+        if (PFX && s.nchunk <= T) nmax = max(nmax, s.nchunk);
+    }
+    if constexpr (PFX) {
+        nmax = __reduce_max_sync(0xffffffffu, nmax);
+        if (lane == 0) atomicMax(&nmax_s, nmax);
     }
     long long il = ml_, is_ = ms, ia = ma;
 #pragma unroll
@@ -297,10 +306,21 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
         Ws += scan_w[1][w];
         Wa += scan_w[2][w];
     }
+    if constexpr (PFX) nmax = nmax_s;
     // A few short units among long ones would only come after everything else:
     // they are taken as long ones (64 requests of 1 to 16,384 tokens: 192 us, 232
     // with a warp each for the short ones).
-    if (Ws * 8 < W) {
+    bool all_long = Ws * 8 < W;
+    if constexpr (PFX) {
+        // A request's own tokens are few beside a prefix, and its keys wait one
+        // after the other in a lone warp: all units are long ones too where the
+        // line of all then ends first (in chunks' time; a unit's own length
+        // included; 16 requests of up to 512 tokens, 8 heads of keys: PFX_FIG).
+        const long long lone = (Wl / kPagedCtas) / C::W + max(Ws / (kPagedCtas * C::W), static_cast<long long>(nmax)) + 2;
+        const long long together = max(Wa / kPagedCtas, static_cast<long long>(nmax) + C::COST) / C::W;
+        all_long |= together < lone;
+    }
+    if (all_long) {
         T = 0;
         Wl = Wa;
         Ws = 0;
@@ -817,6 +837,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
                             continue;
                         }
                         if (paged_joins(p.join, cs.b)) {
+                            paged_wait_before();
                             const PagedWeights w = paged_weights(m[nt][e], l[nt][e], __ldcg(&p.join.ml[orow]));
                             inv = w.own;
                             before = w.prefix;
@@ -859,6 +880,8 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
             continue;
         }
         // ---------------------------------------------------- merge of the warps
+        if constexpr (PFX)
+            if (!p.join.first) paged_wait_before();
         if (nan_bits) nan_seen = 1;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -1052,6 +1075,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
         __syncthreads();
     }
     cp_async_wait<0>();
+    if constexpr (PFX) paged_wait_before();
     // after a wait that gave up: let the copies still in flight land before
     // leaving (otherwise every copy requested has been consumed)
     for (int u = consumed; u < issued; ++u)
@@ -1073,8 +1097,9 @@ cudaError_t launch_split(const PagedArgs& a, const PagedParams& p, cudaStream_t 
                                     C::SMEM);
     });
     if (e != cudaSuccess) return e;
-    fa_paged_split_kernel<D, NT, B16, PFX><<<kPagedCtas, C::THREADS, C::SMEM, stream>>>(tk, tv, p);
-    return cudaGetLastError();
+    cudaLaunchAttribute at;
+    const cudaLaunchConfig_t cfg = paged_config(C::THREADS, C::SMEM, stream, PFX && a.chained, &at);
+    return cudaLaunchKernelEx(&cfg, fa_paged_split_kernel<D, NT, B16, PFX>, tk, tv, p);
 }
 
 template <int D, bool PFX>

@@ -336,6 +336,7 @@ __global__ void __launch_bounds__(512, 1)
     __shared__ int start_b, start_units, abort_s, last_s[2], nan_piece[kPtNanSlots], wide_s[2];
     __shared__ uint32_t tmem_slot;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if constexpr (PFX) paged_let_next();
 
     // ---- the line of key tiles: total length, and the request at this CTA's start
     const int per = (p.B + 511) / 512;
@@ -429,6 +430,7 @@ __global__ void __launch_bounds__(512, 1)
     const long long x0 = quota * blockIdx.x, x1 = min(x0 + quota, W);
     if (U > p.max_units || x0 >= x1) {  // uniform over the CTA, before any TMEM use
         // (too many units: overlapping offsets, which the split-key kernel reports)
+        if constexpr (PFX) paged_wait_before();
         return;
     }
     bw += iw - mw;
@@ -859,8 +861,10 @@ __global__ void __launch_bounds__(512, 1)
                     make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                                pack_bf16x2(v[6], v[7]));
             };
-            if constexpr (PFX)
+            if constexpr (PFX) {
+                if (!p.join.first) paged_wait_before();
                 if (whole) row_weights(mu, l, inv);
+            }
             // partial outputs lie as [d / 4][128 rows] float4, coalesced over the rows
             float4* po = reinterpret_cast<float4*>(p.po) + (static_cast<size_t>(2 * slot + i) * (D / 4)) * 128 + r;
 #pragma unroll
@@ -926,6 +930,13 @@ __global__ void __launch_bounds__(512, 1)
                 // merges them in order
                 const int f = static_cast<int>(div_short(s.line0, quota));
                 const int e = static_cast<int>(div_short(s.line0 + s.ntile - 1, quota));
+                if constexpr (PFX) {
+                    if (p.join.first) {  // merged by a kernel of its own, over the whole GPU
+                        if (r == 0 && i == 0 && s.c0 == 0)
+                            p.join.cuts[slot] = {1, s.r.tok0, s.pair * 256, rows, s.hk, f, e, 0, s.line0, quota};
+                        continue;
+                    }
+                }
                 __threadfence();
                 named_sync(1 + i, 128);
                 if (r == 0) last_s[i] = atomicAdd(&p.counters[2 * s.unit + i], 1) == e - f;
@@ -1074,6 +1085,7 @@ __global__ void __launch_bounds__(512, 1)
         } while (next(s));
         if (!ok) pt_gave_up(&abort_s, p.status, 98);
     }
+    if constexpr (PFX) paged_wait_before();
     tc_fence_before();
     __syncthreads();
     if (warp == 3) {
@@ -1109,8 +1121,9 @@ static cudaError_t launch_tile(const PagedArgs& a, const PtParams& p, cudaStream
         return cudaFuncSetAttribute(fa_paged_tile_kernel<D, PFX>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     });
     if (e != cudaSuccess) return e;
-    fa_paged_tile_kernel<D, PFX><<<kPagedCtas, 512, C::SMEM, stream>>>(tk, tv, p);
-    return cudaGetLastError();
+    cudaLaunchAttribute at;
+    const cudaLaunchConfig_t cfg = paged_config(512, C::SMEM, stream, PFX && a.chained, &at);
+    return cudaLaunchKernelEx(&cfg, fa_paged_tile_kernel<D, PFX>, tk, tv, p);
 }
 
 cudaError_t launch_paged_tile(const PagedArgs& a, cudaStream_t stream) {

@@ -146,13 +146,12 @@ def test_nan_and_infinite_values(cuda_device, d):
 
 
 def test_no_prefix_is_forward_paged(cuda_device):
-    """Groups without tokens: what forward_paged computes."""
-    b = Batch(BATCHES["groups"][0], [(0, 0), (3, 0)], 32, 2, 4, 128, cuda_device)
+    """Groups without tokens: what forward_paged computes, whose work may be cut
+    elsewhere, so that sums run in another order: both within the bounds."""
+    b = Batch(BATCHES["groups"][0], [(0, 0), (3, 0)], 32, 2, 4, 128, cuda_device, pad=0)
     b.check()
-    o, lse = b.run()
     t = b.tensors()
-    p, pl = fa.forward_paged(b.q[: b.total].contiguous(), *t[:7], max(b.new), scale=b.scale)
-    assert torch.equal(o[: b.total], p) and torch.allclose(lse[:, : b.total], pl, rtol=2.0 ** -22)
+    b.check(got=fa.forward_paged(b.q, *t[:7], max(b.new), scale=b.scale))
 
 
 @pytest.mark.parametrize("which,d", [("many rows", 128), ("prompts", 64), ("groups", 64)])
