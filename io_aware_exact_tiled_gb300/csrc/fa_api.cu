@@ -596,9 +596,9 @@ static PagedWs paged_ws_counters(size_t at, int B, int Hkv, size_t units) {
     w.zeroed = w.tile_counters + align256(2 * units * sizeof(int));
     return w;
 }
-static void paged_ws_partials(PagedWs& w, size_t at, size_t units, int d) {
+static void paged_ws_partials(PagedWs& w, size_t at, size_t units, int d, int slots = 2) {
     const size_t rows = 2 * static_cast<size_t>(fa::kPagedCtas) * fa::kPagedMaxRows;
-    const size_t tile_rows = units ? 2 * static_cast<size_t>(fa::kPagedCtas) * fa::kPagedTileRows : 0;
+    const size_t tile_rows = units ? slots * static_cast<size_t>(fa::kPagedCtas) * fa::kPagedTileRows : 0;
     w.pm = at;
     w.pl = w.pm + align256(rows * sizeof(float));
     w.po = w.pl + align256(rows * sizeof(float));
@@ -716,7 +716,7 @@ struct PrefixWs {
 
 static PrefixWs prefix_ws(int B, int P, int Hq, int Hkv, int total, int max_new, int d) {
     const size_t rows = static_cast<size_t>(total) * Hq;
-    const size_t up = static_cast<size_t>(fa::paged_max_tile_units(P, Hq, Hkv, total, total, d));
+    const size_t up = static_cast<size_t>(fa::paged_max_tile_units(P, Hq, Hkv, total, total, d, 128));
     const size_t uo = static_cast<size_t>(fa::paged_max_tile_units(B, Hq, Hkv, total, max_new, d));
     PrefixWs w;
     w.prefix = paged_ws_counters(kStatusBytes, P, Hkv, up);
@@ -725,7 +725,7 @@ static PrefixWs prefix_ws(int B, int P, int Hq, int Hkv, int total, int max_new,
     w.zeroed = w.cuts + align256(2 * fa::kPagedCtas * sizeof(fa::PagedCut));
     w.ml = w.zeroed;
     w.o = w.ml + align256(rows * sizeof(float2));
-    paged_ws_partials(w.prefix, w.o + align256(rows * d * sizeof(float)), up, d);
+    paged_ws_partials(w.prefix, w.o + align256(rows * d * sizeof(float)), up, d, 3);
     paged_ws_partials(w.own, w.prefix.bytes, uo, d);
     w.bytes = w.own.bytes;
     return w;
@@ -751,6 +751,7 @@ fa_status fa_fwd_paged_prefix(const void* q, const void* k_cache, const void* v_
     if (st != FA_OK) return st;
     st = check_paged(P, Hq, Hkv, total, total, max_prefix_blocks, num_blocks, block_size, d, scale, 0);
     if (st != FA_OK) return st;
+    if (fa::paged_max_tile_units(P, Hq, Hkv, total, total, d, 128) >= (1LL << 29)) return FA_ERR_UNSUPPORTED;
     if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
         !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(cu_seqlens, 4) || !aligned(cache_len, 4) ||
         !aligned(block_table, 4) || !aligned(prefix_cu, 4) || !aligned(prefix_len, 4) || !aligned(prefix_table, 4) ||
@@ -790,12 +791,12 @@ fa_status fa_fwd_paged_prefix(const void* q, const void* k_cache, const void* v_
     pre.max_blocks = max_prefix_blocks;
     pre.max_new = total;
     pre.join.first = prefix_cu;
-    // one group has all rows and none goes to the split-key kernel; of several,
-    // some may be small
-    pre.split_rows = !fa::paged_has_tiles(total, group, d) ? fa::paged_split_rows(total, group, d)
-                     : P == 1                              ? 0
-                                                           : fa::paged_max_rows(d);
+    // the split-key kernel where no group can have more rows than it takes, else
+    // the row-tile kernel for all (groups of few rows among them: a launch less)
+    pre.split_rows = fa::paged_has_tiles(total, group, d) ? 0 : fa::paged_split_rows(total, group, d);
     paged_place(pre, w.prefix, ws);
+    pre.max_tile_units = static_cast<int>(fa::paged_max_tile_units(P, Hq, Hkv, total, total, d, 128));
+    pre.one_tile = static_cast<long long>(total) * group <= 128LL * P;
     a.B = B;
     a.cache_len = cache_len;
     a.block_table = block_table;

@@ -44,7 +44,7 @@ struct AppendArgs {
 // kernel that merges its pieces: rows row0 .. (token row / G, head hk * G + row %
 // G, of tokens tok0 ..) of at most `rows`, pieces in slots piece(cta), cta = first .. last.
 struct PagedCut {
-    int valid, tok0, row0, rows, hk, first, last, pad;
+    int valid, tok0, row0, rows, hk, first, last, parts;  // parts of a row in each piece: 1, 2 (row tiles) or 4 (and lanes 64 ..)
     long long line0, quota;
     __host__ __device__ int piece(int cta) const { return 2 * cta + (line0 <= quota * cta ? 0 : 1); }
 };
@@ -81,6 +81,7 @@ struct PagedArgs {
     float *tile_pm, *tile_pl;  // [2 * kPagedCtas][kPagedTileRows]
     float* tile_po;            // [2 * kPagedCtas][kPagedTileRows][d]
     cudaEvent_t ev_begin, ev_end;  // optional, recorded around the attention kernels
+    int one_tile;  // units of one row tile (the prefixes' pass)
     int chained;  // launched while the kernel before it may still run (see paged_wait_before)
 };
 
@@ -122,10 +123,11 @@ inline int paged_split_rows(int max_new, int group, int d) {
 }
 // Units of the row-tile kernel that B requests of together `total` tokens can
 // have (none if no request can be that long).
-inline long long paged_max_tile_units(int B, int Hq, int Hkv, int total, int max_new, int d) {
+inline long long paged_max_tile_units(int B, int Hq, int Hkv, int total, int max_new, int d,
+                                      int rows = kPagedTileRows) {
     const long long group = Hq / Hkv;
     if (!paged_has_tiles(max_new, static_cast<int>(group), d)) return 0;
-    return Hkv * (B + total * group / kPagedTileRows);
+    return Hkv * (B + total * group / rows);
 }
 
 // Runs `set` (function attributes) once for each device; `done` remembers

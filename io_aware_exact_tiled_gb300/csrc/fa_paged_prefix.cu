@@ -45,31 +45,36 @@ __global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_consta
     for (int it = blockIdx.x; it < items; it += kMergeCtas) {
         const PagedCut& cut = a.join.cuts[list[it / (2 * PARTS)]];
         const int i = it / PARTS & 1, c0 = ((it % PARTS) * 2 + (tid >> 7)) * COLS;
-        const int row = cut.row0 + i * 128 + r, first = cut.first, last = cut.last;
-        if (row >= cut.rows) continue;
+        const int parts = cut.parts, shift = parts >> 1, first = cut.first;  // log2 of parts
+        const int row = cut.row0 + (parts > 1 ? 0 : i * 128) + r;
+        const int n = (cut.last - first + 1) * parts;  // pieces' parts
+        if (row >= cut.rows || (parts > 1 && i) || (parts == 4 && r >= 64)) continue;
+        // part k: its half slot, times 128 and with the lane
+        auto at = [&](int k) {
+            const int slot = 2 * cut.piece(first + (k >> shift));
+            return (parts == 1 ? slot + i : slot + (k & 1)) * 128 + (parts == 4 ? 32 * (k & 2) : 0) + r;
+        };
         float M = -CUDART_INF_F;
-        for (int cta = first; cta <= last; ++cta) {
-            const float m = __ldcg(&a.tile_pm[cut.piece(cta) * kPagedTileRows + i * 128 + r]);
-            M = fmaxf(M, m);
-        }
+#pragma unroll 8
+        for (int k = 0; k < n; ++k) M = fmaxf(M, __ldcg(&a.tile_pm[at(k)]));
         float4 acc[COLS];
 #pragma unroll
-        for (int k = 0; k < COLS; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int y = 0; y < COLS; ++y) acc[y] = make_float4(0.f, 0.f, 0.f, 0.f);
         float L = 0.f;
-#pragma unroll 4
-        for (int cta = first; cta <= last; ++cta) {
-            const int sl = cut.piece(cta), at = sl * kPagedTileRows + i * 128 + r;
-            const float m = __ldcg(&a.tile_pm[at]), w = m == -CUDART_INF_F ? 0.f : exp2f(m - M);
-            L = fmaf(w, __ldcg(&a.tile_pl[at]), L);
+#pragma unroll 8
+        for (int k = 0; k < n; ++k) {
+            const int x = at(k);
+            const float m = __ldcg(&a.tile_pm[x]), w = m == -CUDART_INF_F ? 0.f : ex2_approx(m - M);
+            L = fmaf(w, __ldcg(&a.tile_pl[x]), L);
             const float4* src = reinterpret_cast<const float4*>(a.tile_po) +
-                                (static_cast<size_t>(2 * sl + i) * (D / 4) + c0) * 128 + r;
+                                (static_cast<size_t>(x >> 7) * (D / 4) + c0) * 128 + (x & 127);
 #pragma unroll
-            for (int k = 0; k < COLS; ++k) {
-                const float4 v = __ldcg(src + k * 128);
-                acc[k].x = fmaf(w, v.x, acc[k].x);
-                acc[k].y = fmaf(w, v.y, acc[k].y);
-                acc[k].z = fmaf(w, v.z, acc[k].z);
-                acc[k].w = fmaf(w, v.w, acc[k].w);
+            for (int y = 0; y < COLS; ++y) {
+                const float4 v = __ldcg(src + y * 128);
+                acc[y].x = fmaf(w, v.x, acc[y].x);
+                acc[y].y = fmaf(w, v.y, acc[y].y);
+                acc[y].z = fmaf(w, v.z, acc[y].z);
+                acc[y].w = fmaf(w, v.w, acc[y].w);
             }
         }
         const float inv = L == 0.f ? 0.f : 1.f / L;

@@ -63,6 +63,7 @@ constexpr float kPgLn2 = 0.69314718055994530942f;
 constexpr float kPgRescale = 8.0f;  // log2 units
 constexpr float kPgOffset = 6.0f;   // log2 of the factor on P before its rounding to f16
 constexpr int kPgChunk = 32;        // keys of a chunk
+constexpr int kPgSolo = 96;         // chunks of the longest unit that is not cut where there are CTAs for all
 constexpr int kPgAhead = 3;         // chunks between the fetch of a block id and its use
 
 // FA_DEBUG_DROP_ARRIVE (debug builds only): the first chunk's V is not
@@ -147,15 +148,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t saddr) {
     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(saddr));
     return v;
 }
-// Asynchronous copy of four bytes to shared memory, in groups.
-__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>  // all but the newest N groups of this thread have landed
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 // Bytes of x that are E4M3 NaN (0x7F or 0xFF) as 0x80 bits.
 __device__ __forceinline__ uint32_t e4m3_nan_bits(uint32_t x) { return ((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
@@ -214,7 +206,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
     __shared__ long long start_line;
     __shared__ int nan_seen, abort_s;
     __shared__ float row_before[PFX ? RT : 1];
-    __shared__ int nmax_s;
+    __shared__ int nmax_s, most_s, scan_u[C::W];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     if constexpr (PFX) paged_let_next();
 
@@ -238,6 +230,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
         abort_s = 0;
         nan_seen = 0;
         nmax_s = 0;
+        most_s = 0;
     }
     if (lane < C::STAGES) mbar_init(&bars[lane], 1);
     fence_barrier_init();
@@ -258,12 +251,12 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
     // 2,000 tokens 143 us (up to a half: 160; to the whole share: 172).
     const long long share = W / (kPagedCtas * C::W);
     int T = static_cast<int>(min(max(share / 3, 12ll), 1ll << 30));
-    auto line_long = [&](const PgSeg& s) {
-        return s.nchunk > T ? static_cast<long long>(p.Hkv) * (s.nchunk + C::COST) : 0ll;
-    };
+    int solo = 0;  // PFX: places that every unit has, one CTA's each; 0: as many as its chunks and COST
+    auto places = [&](const PgSeg& s) { return PFX && solo ? solo : s.nchunk + C::COST; };
+    auto line_long = [&](const PgSeg& s) { return s.nchunk > T ? static_cast<long long>(p.Hkv) * places(s) : 0ll; };
     auto line_short = [&](const PgSeg& s) { return s.nchunk <= T ? static_cast<long long>(p.Hkv) * s.nchunk : 0ll; };
     long long ml_ = 0, ms = 0, ma = 0;  // long, short, all as long ones
-    [[maybe_unused]] int nmax = 0;      // the longest of the short ones
+    [[maybe_unused]] int nmax = 0, most = 0, mu = 0;  // the longest of the short ones and of all; units
     for (int b = b0; b < b1; ++b) {
         PgSeg s;
         pg_request<PFX>(p, b, s);
@@ -271,10 +264,25 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
         ms += line_short(s);
         if (s.nchunk > 0) ma += static_cast<long long>(p.Hkv) * (s.nchunk + C::COST);
         if (PFX && s.nchunk <= T) nmax = max(nmax, s.nchunk);
+        if (PFX && s.nchunk > 0) {
+            mu += p.Hkv;
+            most = max(most, s.nchunk);
+        }
     }
+    [[maybe_unused]] int iu = mu;
     if constexpr (PFX) {
         nmax = __reduce_max_sync(0xffffffffu, nmax);
-        if (lane == 0) atomicMax(&nmax_s, nmax);
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 0) {
+            atomicMax(&nmax_s, nmax);
+            atomicMax(&most_s, most);
+        }
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int a = __shfl_up_sync(0xffffffffu, iu, off);
+            if (lane >= off) iu += a;
+        }
+        if (lane == 31) scan_u[warp] = iu;
     }
     long long il = ml_, is_ = ms, ia = ma;
 #pragma unroll
@@ -306,7 +314,15 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
         Ws += scan_w[1][w];
         Wa += scan_w[2][w];
     }
-    if constexpr (PFX) nmax = nmax_s;
+    [[maybe_unused]] int U = 0, bu = iu - mu;
+    if constexpr (PFX) {
+        nmax = nmax_s;
+        most = most_s;
+        for (int w = 0; w < C::W; ++w) {
+            if (w < warp) bu += scan_u[w];
+            U += scan_u[w];
+        }
+    }
     // A few short units among long ones would only come after everything else:
     // they are taken as long ones (64 requests of 1 to 16,384 tokens: 192 us, 232
     // with a warp each for the short ones).
@@ -328,8 +344,22 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
         ml_ = ma;
         bs = 0;
     }
+    if constexpr (PFX) {
+        // Few and short enough, each unit is a CTA's: that costs less than the merge
+        // of a unit that was cut (four requests behind 1,000 tokens: SOLO_FIG).
+        if (U <= kPagedCtas && most <= kPgSolo) {
+            T = 0;
+            solo = most + C::COST;
+            Wl = static_cast<long long>(U) * solo;
+            Ws = 0;
+            bw = static_cast<long long>(bu) * solo;
+            ml_ = static_cast<long long>(mu) * solo;
+            bs = 0;
+        }
+    }
     // equal quotas of the long line, at least one chunk for each warp
-    const long long quota = max((Wl + kPagedCtas - 1) / kPagedCtas, static_cast<long long>(C::W));
+    long long quota = max((Wl + kPagedCtas - 1) / kPagedCtas, static_cast<long long>(C::W));
+    if (PFX && solo) quota = solo;
     const long long x0 = quota * blockIdx.x, x1 = min(x0 + quota, Wl);
     // the short units that start in this warp's part of their line; parts that
     // follow one another lie in different CTAs
@@ -363,10 +393,11 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
             pg_request<PFX>(p, s.b, s);
         }
         const long long r = x - s.rline;
-        s.hk = static_cast<int>(div_short(r, s.nchunk + C::COST));
-        const int rest = static_cast<int>(r - static_cast<long long>(s.hk) * (s.nchunk + C::COST));
-        s.line0 = x - rest + C::COST;
-        s.c0 = max(rest - C::COST, 0);
+        const int len = places(s), cost = len - s.nchunk;
+        s.hk = static_cast<int>(div_short(r, len));
+        const int rest = static_cast<int>(r - static_cast<long long>(s.hk) * len);
+        s.line0 = x - rest + cost;
+        s.c0 = max(rest - cost, 0);
         s.c1 = static_cast<int>(min(static_cast<long long>(s.nchunk), x1 - s.line0));
         return s.c1 > s.c0;  // not only the room in front of a unit
     };

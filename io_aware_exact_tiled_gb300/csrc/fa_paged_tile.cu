@@ -20,9 +20,9 @@
 //
 // A CTA holds two row tiles so that each V tile is converted once for 256
 // rows. Warps:
-//   0      copies K and V tiles by TMA, E4M3 as they lie, and their block scales
+//   0      copies K and V tiles by TMA, E4M3 as they lie
 //   1, 2   issue the products of row tile 0, 1
-//   3      allocates TMEM
+//   3      allocates TMEM, then fetches the block scales
 //   4-7    softmax of row tile 0: thread = row
 //   8-11   softmax of row tile 1
 //   12-15  convert V to f16: thread = key
@@ -64,14 +64,16 @@ constexpr int kPtUnitCost = D == 64 ? 6 : 8;
 constexpr int kPtScaleSlots = 8;
 constexpr uint32_t kFmtE5M2 = 1;  // kind::f8f6f4 operand format code
 constexpr int kPtNanSlots = 4;
+constexpr int kPtAhead = 8;  // tiles whose block ids and scales are on their way or in use
 
-template <int D>
+template <int D, bool ONE>
 struct PtCfg {
     // K stages, and stages of V as it lies in the cache (d = 128, where the third
     // part of Q takes their room: 795 us for pieces of prompts with three and two
-    // stages and Q's two parts alone, 793 with these)
-    static constexpr int KS = D == 128 ? 2 : 6;
-    static constexpr int RS = D == 128 ? 1 : 4;
+    // stages and Q's two parts alone, 793 with these; units of one row tile have
+    // one Q)
+    static constexpr int KS = D == 128 ? (ONE ? 3 : 2) : 6;
+    static constexpr int RS = D == 128 ? (ONE ? 3 : 1) : 4;
     static constexpr int VS = 2;                  // stages of converted V
     static constexpr int NREG = D / 64;           // 128-byte-wide regions of an f16 row
     // the three parts of a row tile's Q: rows of 128 bytes, d = 64: the first
@@ -83,12 +85,13 @@ struct PtCfg {
     static constexpr int K_BYTES = 128 * D;
     static constexpr int V_BYTES = 128 * D * 2;
     static constexpr int Q_OFF = 0;
-    static constexpr int K_OFF = Q_OFF + 2 * Q_BYTES;
+    static constexpr int K_OFF = Q_OFF + (ONE ? 1 : 2) * Q_BYTES;
     static constexpr int R_OFF = K_OFF + KS * K_BYTES;
     static constexpr int V_OFF = R_OFF + RS * K_BYTES;
     static constexpr int SC_OFF = V_OFF + VS * V_BYTES;       // float [slots][24]: ks, log2 vs, 1 / vs of 8 groups
     static constexpr int NAN_OFF = SC_OFF + kPtScaleSlots * 96;  // u64 [slots][D]: {tag, first key with a NaN value}
-    static constexpr int BAR_OFF = NAN_OFF + kPtNanSlots * D * 8;
+    static constexpr int AHEAD_OFF = NAN_OFF + kPtNanSlots * D * 8;  // int ids [2][kPtAhead][8], float {ks, vs} [kPtAhead][8]
+    static constexpr int BAR_OFF = AHEAD_OFF + kPtAhead * 128;
     static constexpr int USED = BAR_OFF + 512;
     static constexpr int SMEM = USED + 1024;
     // TMEM: S of row tile i and half h of the keys at 128 i + 64 h, O at 256 +
@@ -207,7 +210,7 @@ __device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t sbo) {
 // elements are below 2^-2, the only ones that two parts may not hold exactly.
 template <int D, bool WIDE>
 __device__ __forceinline__ float pt_split_q(const uint4 (&x)[D / 8], float f, uint8_t* qb, int r) {
-    using C = PtCfg<D>;
+    using C = PtCfg<D, false>;
     uint32_t small = 0u;  // f16 pair
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) {
@@ -303,13 +306,14 @@ struct PtSeg {
 __device__ __forceinline__ int pt_visible(const PtParams& p, const PtReq& r, int tok) {
     return p.causal ? min(max(r.len - r.n + tok + 1, 0), r.len) : r.len;
 }
-// Key tiles that rows [.., last] of a request need (at least one, so that
+// Key tiles that the rows of a unit (RT of them) need (at least one, so that
 // rows that see nothing get their zero output).
+template <int RT>
 __device__ __forceinline__ int pt_tiles(const PtParams& p, const PtReq& r, int pair) {
-    const int last = min(pair * 256 + 255, r.n * p.G - 1);
+    const int last = min(pair * RT + RT - 1, r.n * p.G - 1);
     return max(1, (pt_visible(p, r, p.by_g.div(last)) + 127) >> 7);
 }
-template <int D, bool PFX>
+template <int D, bool PFX, int RT>
 __device__ __forceinline__ void pt_request(const PtParams& p, int b, PtReq& r) {
     int i0 = b, i1 = b + 1;
     if constexpr (PFX) paged_members(p.join, i0, i1);
@@ -319,16 +323,21 @@ __device__ __forceinline__ void pt_request(const PtParams& p, int b, PtReq& r) {
     r.n = min(t1 - t0, p.max_new);
     if (static_cast<long long>(r.n) * p.G <= p.split_rows) r.n = 0;
     r.len = min(max(p.cache_len[b], 0), p.max_blocks << p.bs_log2);
-    r.npair = static_cast<int>((static_cast<long long>(r.n) * p.G + 255) >> 8);
+    r.npair = static_cast<int>((static_cast<long long>(r.n) * p.G + RT - 1) / RT);
     r.tiles = 0;
-    for (int i = 0; i < r.npair; ++i) r.tiles += pt_tiles(p, r, i) + kPtUnitCost<D>;
+    for (int i = 0; i < r.npair; ++i) r.tiles += pt_tiles<RT>(p, r, i) + kPtUnitCost<D>;
 }
 
-template <int D, bool PFX>
+// ONE (a prefix's rows, which see all its keys): a unit is one row tile, and the
+// two softmax groups and product warps, "row tiles" i below, take every other of
+// its key tiles: with few rows the time is the chain of S, softmax and P V, and
+// two chains hide one another (PT_FIG).
+template <int D, bool PFX, bool ONE>
 __global__ void __launch_bounds__(512, 1)
     fa_paged_tile_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                          const __grid_constant__ PtParams p) {
-    using C = PtCfg<D>;
+    using C = PtCfg<D, ONE>;
+    constexpr int RT = ONE ? 128 : 256, STEP = ONE ? 2 : 1;  // rows of a unit; key tiles from one of a row tile's to the next
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ long long scan_w[16], scan_u[16];
@@ -344,7 +353,7 @@ __global__ void __launch_bounds__(512, 1)
     long long mw = 0, mu = 0;
     for (int b = b0; b < b1; ++b) {
         PtReq r;
-        pt_request<D, PFX>(p, b, r);
+        pt_request<D, PFX, RT>(p, b, r);
         mu += static_cast<long long>(r.npair) * p.Hkv;
         mw += r.tiles * p.Hkv;
     }
@@ -370,7 +379,8 @@ __global__ void __launch_bounds__(512, 1)
     uint64_t* nan_full = drain + 2;            // [4] a piece's V has been looked over
     uint64_t* nan_empty = nan_full + kPtNanSlots;  // [4] both row tiles' softmax warps are through with that piece
     uint64_t* sc_full = nan_empty + kPtNanSlots;   // [8] scales stored
-    uint64_t* k_full = sc_full + kPtScaleSlots;  // [KS]
+    uint64_t* asked = sc_full + kPtScaleSlots;   // [8] K of a tile requested
+    uint64_t* k_full = asked + kPtScaleSlots;    // [KS]
     uint64_t* k_empty = k_full + C::KS;        // [KS] both row tiles' S done
     uint64_t* r_full = k_empty + C::KS;        // [RS] V landed
     uint64_t* r_empty = r_full + C::RS;        // [RS] V read
@@ -391,10 +401,13 @@ __global__ void __launch_bounds__(512, 1)
             mbar_init(&nan_full[i], 128);
             mbar_init(&nan_empty[i], 256);
         }
-        for (int i = 0; i < kPtScaleSlots; ++i) mbar_init(&sc_full[i], 1);
+        for (int i = 0; i < kPtScaleSlots; ++i) {
+            mbar_init(&sc_full[i], 1);
+            mbar_init(&asked[i], 1);
+        }
         for (int i = 0; i < C::KS; ++i) {
             mbar_init(&k_full[i], 1);
-            mbar_init(&k_empty[i], 2);
+            mbar_init(&k_empty[i], ONE ? 1 : 2);
         }
         for (int i = 0; i < C::RS; ++i) {
             mbar_init(&r_full[i], 1);
@@ -402,7 +415,7 @@ __global__ void __launch_bounds__(512, 1)
         }
         for (int i = 0; i < C::VS; ++i) {
             mbar_init(&v_full[i], 128);
-            mbar_init(&v_empty[i], 2);
+            mbar_init(&v_empty[i], ONE ? 1 : 2);
         }
         fence_barrier_init();
     }
@@ -438,7 +451,7 @@ __global__ void __launch_bounds__(512, 1)
     if (x0 >= bw && x0 < bw + mw) {
         for (int b = b0; b < b1; ++b) {
             PtReq r;
-            pt_request<D, PFX>(p, b, r);
+            pt_request<D, PFX, RT>(p, b, r);
             if (x0 < bw + r.tiles * p.Hkv) {
                 start_b = b;
                 start_line = bw;
@@ -465,14 +478,14 @@ __global__ void __launch_bounds__(512, 1)
         while (x >= rline + s.r.tiles * p.Hkv) {
             rline += s.r.tiles * p.Hkv;
             runits += s.r.npair * p.Hkv;
-            pt_request<D, PFX>(p, s.r.b + 1, s.r);
+            pt_request<D, PFX, RT>(p, s.r.b + 1, s.r);
         }
         const long long off = x - rline;
         s.hk = static_cast<int>(div_short(off, s.r.tiles));
         long long rest = off - s.hk * s.r.tiles;
         s.pair = 0;
         for (;;) {
-            s.ntile = pt_tiles(p, s.r, s.pair);
+            s.ntile = pt_tiles<RT>(p, s.r, s.pair);
             if (rest < s.ntile + kPtUnitCost<D>) break;
             rest -= s.ntile + kPtUnitCost<D>;
             ++s.pair;
@@ -488,7 +501,7 @@ __global__ void __launch_bounds__(512, 1)
         if (s.pair + 1 < s.r.npair) {  // the usual step: the next pair of the same head
             ++s.pair;
             ++s.unit;
-            s.ntile = pt_tiles(p, s.r, s.pair);
+            s.ntile = pt_tiles<RT>(p, s.r, s.pair);
             s.c0 = 0;
             s.line0 = x + kPtUnitCost<D>;
             s.c1 = static_cast<int>(min(static_cast<long long>(s.ntile), x1 - s.line0));
@@ -499,14 +512,15 @@ __global__ void __launch_bounds__(512, 1)
     };
     // key tiles that row tile i of a piece takes part in: [c0, end)
     auto half_end = [&](const PtSeg& s, int i) {
-        const int rows = s.r.n * p.G, base = s.pair * 256 + i * 128;
+        if (ONE) return s.c1;
+        const int rows = s.r.n * p.G, base = s.pair * RT + i * 128;
         if (base >= rows) return s.c0;
         const int last = min(base + 127, rows - 1);
         return max(s.c0, min(s.c1, (pt_visible(p, s.r, p.by_g.div(last)) + 127) >> 7));
     };
     auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return pt_wait(bar, parity, &abort_s); };
     PtSeg s;
-    pt_request<D, PFX>(p, start_b, s.r);
+    pt_request<D, PFX, RT>(p, start_b, s.r);
     find(s, x0);
     const bool any = s.c1 > s.c0;  // uniform over the CTA: not only the cost in front of a tile
 
@@ -514,54 +528,56 @@ __global__ void __launch_bounds__(512, 1)
         // nothing but TMEM to give back
     } else if (warp < 4) {
         regs_dec<96>();
+        // A tile's loads depend on one another (block id, then scales and copies):
+        // ids come four tiles ahead and scales two, by asynchronous copies of a
+        // lane for each group of 16 keys. One warp requests the copies and another
+        // sees to the scales: together they took a warp 2,370 cycles a tile, which
+        // is what a long prefix then took (LOAD_FIG).
+        const int bs = 1 << p.bs_log2, box = min(bs, 128);
+        int* ahead = reinterpret_cast<int*>(sm + C::AHEAD_OFF) + (warp == 0 ? 0 : 8 * kPtAhead);
+        auto has = [&](int t) { return lane < 8 && t < s.c1 && t * 128 + lane * 16 < s.r.len; };
+        auto id_at = [&](int t) { return ahead + (t % kPtAhead) * 8 + lane; };  // lanes 0..7
+        auto fetch_id = [&](int t) {
+            if (has(t))
+                cp_async4(id_at(t), &p.block_table[static_cast<size_t>(s.r.b) * p.max_blocks +
+                                                   ((t * 128 + lane * 16) >> p.bs_log2)]);
+        };
+        auto is_block = [&](int id) { return id >= 0 && id < p.num_blocks; };
+        auto row_of = [&](int id, int t) {
+            return static_cast<int>(((static_cast<long long>(id) * p.Hkv + s.hk) << p.bs_log2) +
+                                    ((t * 128 + lane * 16) & (bs - 1)));
+        };
+        // the first lane of each box of min(block, 128) rows requests it
+        const bool asks = lane < 8 && lane % (box >> 4) == 0;
         if (warp == 0) {
-            // ------------------------------------------------------ K tiles and scales
-            const int bs = 1 << p.bs_log2, box = min(bs, 128);
+            // ------------------------------------------------------ K and V tiles
             int u = 0, klast = -1;
             bool ok = true;
-            float* sc = reinterpret_cast<float*>(sm + C::SC_OFF);
             do {
-                float vref = 0.f;  // largest V scale met so far in this piece
+#pragma unroll 1
+                for (int t = 0; t < 4; ++t) {
+                    fetch_id(s.c0 + t);
+                    cp_async_commit();
+                }
                 for (int t = s.c0; ok && t < s.c1; ++t, ++u) {
-                    const int st = u % C::KS, slot = u % kPtScaleSlots;
-                    // lane i < 8: the group of 16 keys from 16 i on
-                    int id = 0;
-                    float ks = 0.f, vs = 0.f;
-                    const int key = t * 128 + lane * 16;
-                    if (lane < 8 && key < s.r.len) {
-                        id = p.block_table[static_cast<size_t>(s.r.b) * p.max_blocks + (key >> p.bs_log2)];
-                        if (id < 0 || id >= p.num_blocks) {
-                            atomicCAS(p.status, 0, FA_DEV_INVALID | (94 << 8));
-                            id = 0;
-                        } else {
-                            ks = p.k_scale[static_cast<size_t>(id) * p.Hkv + s.hk];
-                            vs = p.v_scale[static_cast<size_t>(id) * p.Hkv + s.hk];
-                        }
+                    const int st = u % C::KS, rs = u % C::RS;
+                    cp_async_wait<3>();
+                    int id = has(t) ? *id_at(t) : 0;
+                    if (!is_block(id)) {
+                        atomicCAS(p.status, 0, FA_DEV_INVALID | (94 << 8));
+                        id = 0;
                     }
+                    fetch_id(t + 4);
+                    cp_async_commit();
+                    const int row = row_of(id, t);
                     if (!(ok = wait_warp(&k_empty[st], ((u / C::KS) & 1) ^ 1))) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&k_full[st], C::K_BYTES);
+                    if (lane == 0) {
+                        mbar_arrive(&asked[u % kPtScaleSlots]);
+                        mbar_arrive_expect_tx(&k_full[st], C::K_BYTES);
+                    }
                     __syncwarp();
-                    // the first lane of each box of min(block, 128) rows requests it
-                    const bool asks = lane < 8 && lane % (box >> 4) == 0;
-                    const int row = static_cast<int>(((static_cast<long long>(id) * p.Hkv + s.hk) << p.bs_log2) +
-                                                     ((t * 128 + lane * 16) & (bs - 1)));
                     if (asks)
                         tma_load_2d(sm + C::K_OFF + st * C::K_BYTES + lane * 16 * D, &tmK, 0, row, &k_full[st]);
-                    float top = vs;
-#pragma unroll
-                    for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    vref = fmaxf(vref, top);
-                    if (lane < 8) {
-                        // groups whose scale is below 2^-60 of the largest (blocks of
-                        // zeros have 2^-126) count as if it were that
-                        const float lv = fmaxf(fmaxf(log2f(vs), log2f(vref) - kPtSpan), -100.f);
-                        sc[slot * 24 + lane] = ks;
-                        sc[slot * 24 + 8 + lane] = lv;
-                        sc[slot * 24 + 16 + lane] = exp2f(-lv);
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sc_full[slot]);
-                    const int rs = u % C::RS;
                     if (!(ok = wait_warp(&r_empty[rs], ((u / C::RS) & 1) ^ 1))) {
                         klast = u + 1;
                         break;
@@ -571,6 +587,7 @@ __global__ void __launch_bounds__(512, 1)
                     if (asks)
                         tma_load_2d(sm + C::R_OFF + rs * C::K_BYTES + lane * 16 * D, &tmV, 0, row, &r_full[rs]);
                 }
+                cp_async_wait<0>();
             } while (ok && next(s));
             if (!ok) pt_gave_up(&abort_s, p.status, 95);
             // let every copy in flight land before the CTA can exit
@@ -585,6 +602,62 @@ __global__ void __launch_bounds__(512, 1)
                     mbar_wait_teardown(&r_full[i], (last / C::RS) & 1, 200000000ull);
                 }
             }
+        } else if (warp == 3) {
+            // ------------------------------------------------------ scales
+            // A slot is written once K of its tile has been requested: the tile
+            // eight before it, whose slot it was, is then through its softmax.
+            float* raw = reinterpret_cast<float*>(ahead + 8 * kPtAhead);  // {ks, vs} [kPtAhead][8]
+            float* sc = reinterpret_cast<float*>(sm + C::SC_OFF);
+            auto fetch_scales = [&](int t) {
+                if (!has(t)) return;
+                const int id = *id_at(t);
+                if (!is_block(id)) return;
+                const size_t x = static_cast<size_t>(id) * p.Hkv + s.hk;
+                cp_async4(raw + ((t % kPtAhead) * 8 + lane) * 2, &p.k_scale[x]);
+                cp_async4(raw + ((t % kPtAhead) * 8 + lane) * 2 + 1, &p.v_scale[x]);
+            };
+            int u = 0;
+            bool ok = true;
+            do {
+                float vref = 0.f;  // largest V scale met so far in this piece
+#pragma unroll 1
+                for (int t = 0; t < 4; ++t) fetch_id(s.c0 + t);
+                cp_async_commit();
+                cp_async_wait<0>();
+                fetch_scales(s.c0);
+                cp_async_commit();
+                fetch_scales(s.c0 + 1);
+                cp_async_commit();
+                for (int t = s.c0; ok && t < s.c1; ++t, ++u) {
+                    cp_async_wait<1>();
+                    float ks = 0.f, vs = 0.f;
+                    if (has(t) && is_block(*id_at(t))) {
+                        ks = raw[((t % kPtAhead) * 8 + lane) * 2];
+                        vs = raw[((t % kPtAhead) * 8 + lane) * 2 + 1];
+                    }
+                    fetch_scales(t + 2);
+                    fetch_id(t + 4);
+                    cp_async_commit();
+                    float top = vs;
+#pragma unroll
+                    for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    vref = fmaxf(vref, top);
+                    // groups whose scale is below 2^-60 of the largest (blocks of
+                    // zeros have 2^-126) count as if it were that
+                    const float lv = fmaxf(fmaxf(log2f(vs), log2f(vref) - kPtSpan), -100.f), il = exp2f(-lv);
+                    const int slot = u % kPtScaleSlots;
+                    if (!(ok = wait_warp(&asked[slot], (u / kPtScaleSlots) & 1))) break;
+                    if (lane < 8) {
+                        sc[slot * 24 + lane] = ks;
+                        sc[slot * 24 + 8 + lane] = lv;
+                        sc[slot * 24 + 16 + lane] = il;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sc_full[slot]);
+                }
+                cp_async_wait<0>();
+            } while (ok && next(s));
+            if (!ok) pt_gave_up(&abort_s, p.status, 99);
         } else if (warp < 3) {
             // ------------------------------------------------------ products of row tile i
             // A key tile's two halves of 64 keys have S columns of their own:
@@ -594,7 +667,7 @@ __global__ void __launch_bounds__(512, 1)
             // 450 cycles to issue, which one warp for both could not hide.
             const int i = warp - 1;
             const uint32_t leader = elect_one_sync();
-            const uint64_t dQ = sdesc_sw128(smem_u32(sm + C::Q_OFF) + i * C::Q_BYTES, 16, 1024);
+            const uint64_t dQ = sdesc_sw128(smem_u32(sm + C::Q_OFF) + (ONE ? 0 : i * C::Q_BYTES), 16, 1024);
             const uint64_t dK = D == 128 ? sdesc_sw128(smem_u32(sm + C::K_OFF), 16, 1024)
                                          : sdesc_sw64(smem_u32(sm + C::K_OFF), 512);
             const uint64_t dV = sdesc_sw128(smem_u32(sm + C::V_OFF), 16384, 1024);
@@ -606,19 +679,22 @@ __global__ void __launch_bounds__(512, 1)
             // tests it between its products.
             auto walk = [&](auto form, int c0, int c1, int end) {
                 constexpr bool kWide = decltype(form)::value;
-                for (int t = c0; t <= c1; ++t, ++u) {
-                    const int st = u % C::KS, vs = (u - 1) % C::VS;
+                const int first = ONE ? c0 + i : c0;
+                u += first - c0;
+                for (int t = first; t < c1 + STEP; t += STEP, u += STEP) {
+                    const int st = u % C::KS, vs = (u - STEP) % C::VS;
+                    const bool now = t < c1, before = t > first;  // a tile of K, and one of V, of this row tile's
                     const uint64_t vd = sdesc_advance(dV, vs * C::V_BYTES), kd = sdesc_advance(dK, st * C::K_BYTES);
-                    if (t < c1 && !(ok = wait_warp(&k_full[st], (u / C::KS) & 1))) break;
-                    if (t > c0 && !(ok = wait_warp(&v_full[vs], ((u - 1) / C::VS) & 1))) break;
+                    if (now && !(ok = wait_warp(&k_full[st], (u / C::KS) & 1))) break;
+                    if (before && !(ok = wait_warp(&v_full[vs], ((u - STEP) / C::VS) & 1))) break;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t tS = tm0 + C::COL_S + h * 64, tO = tm0 + C::COL_O;
                         const uint32_t tP = tm0 + C::COL_P + h * C::P_STRIDE;
-                        if (t > c0 && t <= end) {
+                        if (before && t - STEP < end) {
                             if (!(ok = wait_warp(&p_full[2 * i + h], np & 1))) break;
                             tc_fence_after();
-                            const uint32_t more = !(t - 1 == c0 && h == 0);
+                            const uint32_t more = !(t - STEP == first && h == 0);
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
                                 umma_ts<false>(leader, tO, tP + kk * 8, sdesc_advance(vd, h * 8192 + kk * 2048),
@@ -629,7 +705,7 @@ __global__ void __launch_bounds__(512, 1)
                             // Only products with the same accumulator are bound to
                             // the order of their issue: where S takes P's place,
                             // P V has to be done.
-                            if (C::P_OVER_S && t > c0 && !(ok = wait_warp(&pv_done[2 * i + h], np & 1))) break;
+                            if (C::P_OVER_S && before && !(ok = wait_warp(&pv_done[2 * i + h], np & 1))) break;
                             tc_fence_after();
 #pragma unroll
                             for (int part = 0; part < (kWide ? 3 : 2); ++part)
@@ -642,22 +718,25 @@ __global__ void __launch_bounds__(512, 1)
                         }
                     }
                     if (!ok) break;
-                    // this row tile has read K of tile t and V of tile t - 1
-                    if (t < c1) umma_commit(leader, &k_empty[st]);
-                    if (t > c0) umma_commit(leader, &v_empty[vs]);
-                    np += t > c0 && t <= end;
+                    // this row tile has read K of tile t and V of the one before
+                    if (now) umma_commit(leader, &k_empty[st]);
+                    if (before) umma_commit(leader, &v_empty[vs]);
+                    np += before && t - STEP < end;
                 }
-                --u;  // the last round had no tile of its own
             };
+            int upos = 0;  // tiles of the pieces before
             do {
                 // warp-uniform in the compiler's eyes too, so that descriptors and
                 // TMEM addresses stay in uniform registers
                 const int c0 = uniform(s.c0), c1 = uniform(s.c1), end = uniform(half_end(s, i));
-                if (end > c0 && !(ok = wait_warp(&q_full[i], nseg & 1))) break;
-                if (end > c0 && uniform(wide_s[i])) walk(PtWide{}, c0, c1, end);
+                const bool some = end > (ONE ? c0 + i : c0);
+                u = upos;
+                if (some && !(ok = wait_warp(&q_full[i], nseg & 1))) break;
+                if (some && uniform(wide_s[i])) walk(PtWide{}, c0, c1, end);
                 else walk(PtNarrow{}, c0, c1, end);
                 if (!ok) break;
-                nseg += end > c0;
+                nseg += some;
+                upos += c1 - c0;
             } while (__any_sync(0xffffffffu, next(s)));
             if (!ok) pt_gave_up(&abort_s, p.status, 96);
             // every MMA issued so far must be complete before TMEM is released
@@ -670,18 +749,23 @@ __global__ void __launch_bounds__(512, 1)
         const int i = (warp - 4) >> 2, wq = warp & 3, r = wq * 32 + lane;
         const uint32_t tl = tm + (static_cast<uint32_t>(wq * 32) << 16);
         const uint32_t tS = tl + C::COL_S + i * 128, tO = tl + C::COL_O + i * 128, tP = tl + C::COL_P + i * 128;
-        uint8_t* qb = sm + C::Q_OFF + i * C::Q_BYTES;
+        uint8_t* qb = sm + C::Q_OFF + (ONE ? 0 : i * C::Q_BYTES);  // ONE: both write the same bytes
         int u = 0, ns = 0, seg = 0;  // tiles walked, halves of them multiplied, pieces
         bool ok = true;
         do {
             const int end = half_end(s, i);
-            const int rows = s.r.n * p.G, base = s.pair * 256 + i * 128, row = base + r;
+            const int rows = s.r.n * p.G, base = s.pair * RT + (ONE ? 0 : i * 128);
+            const int row = base + (ONE && rows - base <= 64 ? r & 63 : r);
             const bool row_ok = row < rows;
+            // ONE, at most 64 rows: lanes 64 .. 127 have the same rows, and take the
+            // second half of each tile's keys, lanes 0 .. 63 the first
+            const bool twice = ONE && rows - base <= 64;
             const int tok = row_ok ? p.by_g.div(row) : 0, hq = s.hk * p.G + (row_ok ? row - tok * p.G : 0);
             const int limit = row_ok ? pt_visible(p, s.r, tok) : 0;
             const size_t qrow = (static_cast<size_t>(s.r.tok0 + tok) * p.Hq + hq) * D;
             float rc = 0.f, mu = -CUDART_INF_F, l = 0.f;
-            if (end > s.c0) {
+            const int first = ONE ? s.c0 + i : s.c0;  // key tile
+            if (end > first) {
                 // ---- Q: the row's power of two, then its parts
                 uint4 x[D / 8];
 #pragma unroll
@@ -717,12 +801,25 @@ __global__ void __launch_bounds__(512, 1)
             // rows that the first row's keys bound: tiles below need no mask
             const int vis_min = pt_visible(p, s.r, p.by_g.div(min(base, rows - 1)));
 #pragma unroll 1
-            for (int th = 2 * s.c0; th < 2 * end; ++th) {
+            for (int th = 2 * first; th < 2 * end; th += (th & 1) ? 2 * STEP - 1 : 1) {
                 const int t = th >> 1, h = th & 1;  // key tile and half of it
                 const int us = u + (t - s.c0), slot = us % kPtScaleSlots;
                 if (h == 0 && !(ok = wait_warp(&sc_full[slot], (us / kPtScaleSlots) & 1))) break;
                 if (!(ok = wait_warp(&s_full[2 * i + h], (ns >> 1) & 1))) break;
                 tc_fence_after();
+                if constexpr (ONE) {
+                    if (twice && (r >> 6) != h) {  // the other lanes' keys (uniform over the warp)
+                        uint32_t zero[32];
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) zero[k] = 0u;
+                        tmem_st32(tP + h * C::P_STRIDE, zero);
+                        tmem_st_wait();
+                        tc_fence_before();
+                        mbar_arrive(&p_full[2 * i + h]);
+                        ++ns;
+                        continue;
+                    }
+                }
                 const uint32_t tSh = tS + h * 64;
                 uint32_t sr[2][32];
                 tmem_ld32(tSh, sr[0]);
@@ -784,7 +881,7 @@ __global__ void __launch_bounds__(512, 1)
                     l = fmaf(a + b, il[gr], l);
                 }
                 tmem_st32(tP + h * C::P_STRIDE, pk);
-                if (__any_sync(0xffffffffu, resc) && th > 2 * s.c0) {
+                if (__any_sync(0xffffffffu, resc) && th > 2 * first) {
                     // O of the halves so far is final once the last one's P V
                     // is (the ones before it were issued ahead of this S; the
                     // next one waits for this half's P)
@@ -807,10 +904,11 @@ __global__ void __launch_bounds__(512, 1)
             }
             u += s.c1 - s.c0;
             // ---------------------------------------------------- the piece's rows
-            if (ok && end > s.c0) ok = wait_warp(&pv_done[2 * i + 1], ((ns - 1) >> 1) & 1);
+            if (ok && end > first) ok = wait_warp(&pv_done[2 * i + 1], ((ns - 1) >> 1) & 1);
             if (ok) ok = wait_warp(&nan_full[seg % kPtNanSlots], (seg / kPtNanSlots) & 1);
             // the row tile's warps leave together, so that none waits for the others below
-            if (!(ok = named_all(1 + i, 128, ok))) break;
+            // (ONE: of both row tiles, for the same reason)
+            if (!(ok = ONE ? named_all(3, 256, ok) : named_all(1 + i, 128, ok))) break;
             if (base >= rows) {  // no rows: nothing to write or to merge, in no piece of the unit
                 mbar_arrive(&nan_empty[seg % kPtNanSlots]);
                 ++seg;
@@ -822,8 +920,11 @@ __global__ void __launch_bounds__(512, 1)
             const bool nan_seen = nan_piece[seg % kPtNanSlots] == seg;
             ++seg;
             const bool whole = s.c0 == 0 && s.c1 == s.ntile;
-            const int slot = 2 * static_cast<int>(blockIdx.x) + (s.line0 <= x0 ? 0 : 1);
-            float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+            // (ONE: the parts of a whole unit lie in a third slot, until row tile 0 joins them)
+            const int slot = ONE && whole ? 2 * kPagedCtas + static_cast<int>(blockIdx.x)
+                                          : 2 * static_cast<int>(blockIdx.x) + (s.line0 <= x0 ? 0 : 1);
+            const bool leave = ONE || !whole;
+            float inv = leave ? 1.f : l == 0.f ? 0.f : 1.f / l;
             // PFX: weight of the prefix in the row's output, and L
             [[maybe_unused]] float before = 0.f, lse_all = 0.f;
             [[maybe_unused]] const size_t orow = qrow / D;
@@ -863,7 +964,7 @@ __global__ void __launch_bounds__(512, 1)
             };
             if constexpr (PFX) {
                 if (!p.join.first) paged_wait_before();
-                if (whole) row_weights(mu, l, inv);
+                if (!leave) row_weights(mu, l, inv);
             }
             // partial outputs lie as [d / 4][128 rows] float4, coalesced over the rows
             float4* po = reinterpret_cast<float4*>(p.po) + (static_cast<size_t>(2 * slot + i) * (D / 4)) * 128 + r;
@@ -884,7 +985,7 @@ __global__ void __launch_bounds__(512, 1)
                             static_cast<int>(nf[c * 32 + k] & 0xFFFFFFFFu) < limit)
                             ov[k] = __float_as_uint(CUDART_NAN_F);
                 }
-                if (whole) {
+                if (!leave) {
                     if constexpr (PFX) {
                         if (row_ok) {
 #pragma unroll
@@ -917,7 +1018,7 @@ __global__ void __launch_bounds__(512, 1)
             tc_fence_before();  // O has been read: the next piece's products may overwrite it
             mbar_arrive(&nan_empty[(seg - 1) % kPtNanSlots]);
             const float lse_off = kPtOffset;
-            if (whole) {
+            if (!leave) {
                 if constexpr (PFX) {
                     if (row_ok && !p.join.first) p.lse[static_cast<size_t>(hq) * p.total + s.r.tok0 + tok] = lse_all;
                 } else if (row_ok)
@@ -930,10 +1031,54 @@ __global__ void __launch_bounds__(512, 1)
                 // merges them in order
                 const int f = static_cast<int>(div_short(s.line0, quota));
                 const int e = static_cast<int>(div_short(s.line0 + s.ntile - 1, quota));
+                if constexpr (ONE) {
+                    if (whole) {
+                        named_sync(3, 256);
+                        if (i == 0 && row_ok && !(twice && r >= 64)) {
+                            const int n = twice ? 4 : 2;  // parts: row tile k & 1, lanes 64 (k >> 1) + r
+                            auto at = [&](int k) { return slot * kPagedTileRows + (k & 1) * 128 + 64 * (k >> 1) + r; };
+                            float M = -CUDART_INF_F, L = 0.f, w[4];
+                            for (int k = 0; k < n; ++k) M = fmaxf(M, __ldcg(&p.pm[at(k)]));
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                w[k] = 0.f;
+                                if (k >= n) continue;
+                                const float m = __ldcg(&p.pm[at(k)]);
+                                w[k] = m == -CUDART_INF_F ? 0.f : ex2_approx(m - M);
+                                L = fmaf(w[k], __ldcg(&p.pl[at(k)]), L);
+                            }
+                            float own = L == 0.f ? 0.f : 1.f / L;
+                            row_weights(M, L, own);
+                            for (int c = 0; c < D; c += 8) {
+                                float v[8] = {};
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    if (k >= n) continue;
+                                    const float4* src = reinterpret_cast<const float4*>(p.po) +
+                                                        (static_cast<size_t>(2 * slot + (k & 1)) * (D / 4) + c / 4) * 128 +
+                                                        64 * (k >> 1) + r;
+                                    const float4 x = __ldcg(src), y = __ldcg(src + 128);
+                                    v[0] = fmaf(w[k], x.x, v[0]);
+                                    v[1] = fmaf(w[k], x.y, v[1]);
+                                    v[2] = fmaf(w[k], x.z, v[2]);
+                                    v[3] = fmaf(w[k], x.w, v[3]);
+                                    v[4] = fmaf(w[k], y.x, v[4]);
+                                    v[5] = fmaf(w[k], y.y, v[5]);
+                                    v[6] = fmaf(w[k], y.z, v[6]);
+                                    v[7] = fmaf(w[k], y.w, v[7]);
+                                }
+#pragma unroll
+                                for (int y = 0; y < 8; ++y) v[y] *= own;
+                                put_row(c, v);
+                            }
+                        }
+                        continue;
+                    }
+                }
                 if constexpr (PFX) {
                     if (p.join.first) {  // merged by a kernel of its own, over the whole GPU
                         if (r == 0 && i == 0 && s.c0 == 0)
-                            p.join.cuts[slot] = {1, s.r.tok0, s.pair * 256, rows, s.hk, f, e, 0, s.line0, quota};
+                            p.join.cuts[slot] = {1, s.r.tok0, s.pair * RT, rows, s.hk, f, e, ONE ? (twice ? 4 : 2) : 1, s.line0, quota};
                         continue;
                     }
                 }
@@ -1010,8 +1155,8 @@ __global__ void __launch_bounds__(512, 1)
         bool ok = true;
         do {
             const int rows = s.r.n * p.G;
-            const int vis_min = pt_visible(p, s.r, p.by_g.div(s.pair * 256));
-            const int vis_max = pt_visible(p, s.r, p.by_g.div(min(s.pair * 256 + 255, rows - 1)));
+            const int vis_min = pt_visible(p, s.r, p.by_g.div(s.pair * RT));
+            const int vis_max = pt_visible(p, s.r, p.by_g.div(min(s.pair * RT + RT - 1, rows - 1)));
             unsigned long long* nf = nan_first + (seg % kPtNanSlots) * D;
             if (!(ok = wait_warp(&nan_empty[seg % kPtNanSlots], ((seg / kPtNanSlots) & 1) ^ 1))) break;
             for (int t = s.c0; t < s.c1; ++t, ++u) {
@@ -1108,9 +1253,9 @@ static bool make_tmap_rows(CUtensorMap* map, const void* base, uint64_t rows, in
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool PFX>
+template <int D, bool PFX, bool ONE = false>
 static cudaError_t launch_tile(const PagedArgs& a, const PtParams& p, cudaStream_t stream) {
-    using C = PtCfg<D>;
+    using C = PtCfg<D, ONE>;
     CUtensorMap tk, tv;
     const uint64_t rows = static_cast<uint64_t>(a.num_blocks) * a.Hkv * a.block_size;
     const uint32_t box = a.block_size < 128 ? a.block_size : 128;
@@ -1118,12 +1263,12 @@ static cudaError_t launch_tile(const PagedArgs& a, const PtParams& p, cudaStream
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = once_per_device(done, [] {
-        return cudaFuncSetAttribute(fa_paged_tile_kernel<D, PFX>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        return cudaFuncSetAttribute(fa_paged_tile_kernel<D, PFX, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     });
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute at;
     const cudaLaunchConfig_t cfg = paged_config(512, C::SMEM, stream, PFX && a.chained, &at);
-    return cudaLaunchKernelEx(&cfg, fa_paged_tile_kernel<D, PFX>, tk, tv, p);
+    return cudaLaunchKernelEx(&cfg, fa_paged_tile_kernel<D, PFX, ONE>, tk, tv, p);
 }
 
 cudaError_t launch_paged_tile(const PagedArgs& a, cudaStream_t stream) {
@@ -1157,6 +1302,7 @@ cudaError_t launch_paged_tile(const PagedArgs& a, cudaStream_t stream) {
     p.pl = a.tile_pl;
     p.po = a.tile_po;
     p.join = a.join;
+    if (a.one_tile) return a.d == 64 ? launch_tile<64, true, true>(a, p, stream) : launch_tile<128, true, true>(a, p, stream);
     if (a.join.ml) return a.d == 64 ? launch_tile<64, true>(a, p, stream) : launch_tile<128, true>(a, p, stream);
     return a.d == 64 ? launch_tile<64, false>(a, p, stream) : launch_tile<128, false>(a, p, stream);
 }
