@@ -711,7 +711,7 @@ fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
 // the results of the prefixes' pass, then both passes' partials.
 struct PrefixWs {
     PagedWs prefix, own;
-    size_t cuts, zeroed, ml, o, bytes;
+    size_t cuts, ml, own_ml, o, own_o, bytes;
 };
 
 static PrefixWs prefix_ws(int B, int P, int Hq, int Hkv, int total, int max_new, int d) {
@@ -722,10 +722,11 @@ static PrefixWs prefix_ws(int B, int P, int Hq, int Hkv, int total, int max_new,
     w.prefix = paged_ws_counters(kStatusBytes, P, Hkv, up);
     w.own = paged_ws_counters(w.prefix.zeroed, B, Hkv, uo);
     w.cuts = w.own.zeroed;
-    w.zeroed = w.cuts + align256(2 * fa::kPagedCtas * sizeof(fa::PagedCut));
-    w.ml = w.zeroed;
-    w.o = w.ml + align256(rows * sizeof(float2));
-    paged_ws_partials(w.prefix, w.o + align256(rows * d * sizeof(float)), up, d, 3);
+    w.ml = w.cuts + align256(2 * fa::kPagedCtas * sizeof(fa::PagedCut));
+    w.own_ml = w.ml + align256(rows * sizeof(float2));
+    w.o = w.own_ml + align256(rows * sizeof(float2));
+    w.own_o = w.o + align256(rows * d * sizeof(float));
+    paged_ws_partials(w.prefix, w.own_o + align256(rows * d * sizeof(float)), up, d, 3);
     paged_ws_partials(w.own, w.prefix.bytes, uo, d);
     w.bytes = w.own.bytes;
     return w;
@@ -791,6 +792,7 @@ fa_status fa_fwd_paged_prefix(const void* q, const void* k_cache, const void* v_
     pre.max_blocks = max_prefix_blocks;
     pre.max_new = total;
     pre.join.first = prefix_cu;
+    pre.join.leaves = 1;
     // the split-key kernel where no group can have more rows than it takes, else
     // the row-tile kernel for all (groups of few rows among them: a launch less)
     pre.split_rows = fa::paged_has_tiles(total, group, d) ? 0 : fa::paged_split_rows(total, group, d);
@@ -806,8 +808,12 @@ fa_status fa_fwd_paged_prefix(const void* q, const void* k_cache, const void* v_
     a.join.groups = prefix_cu;
     a.split_rows = fa::paged_split_rows(max_new, group, d);
     paged_place(a, w.own, ws);
+    // Where the prefixes are the row-tile kernel's and the requests' own tokens the
+    // split-key kernel's, both run at once: neither fills the GPU all the time.
+    const bool both = fa::paged_has_tiles(total, group, d) && !fa::paged_has_tiles(max_new, group, d);
+    if (both) fa::paged_run_both(pre, a, reinterpret_cast<float2*>(ws + w.own_ml), reinterpret_cast<float*>(ws + w.own_o));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (cudaMemsetAsync(ws, 0, w.zeroed, s) != cudaSuccess) return FA_ERR_CUDA;
+    if (cudaMemsetAsync(ws, 0, both ? w.o : w.ml, s) != cudaSuccess) return FA_ERR_CUDA;
     int n = 0;
     if (total > 0 && max_new > 0) {
         st = map_cuda(fa::launch_fwd_paged_prefix(pre, a, s, &n));

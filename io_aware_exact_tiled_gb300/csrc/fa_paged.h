@@ -50,13 +50,23 @@ struct PagedCut {
 };
 
 // What a call with shared prefixes adds to its two passes (all zero otherwise).
+// A pass leaves rows in ml and o (maximum and minus the sum, whose sign bit says
+// that the row is there; output, normalised) for the other pass, or for the
+// kernel that merges.
 struct PagedJoin {
     const int32_t* first;   // the prefixes' pass: its request b is requests first[b] .. first[b + 1] - 1
-    const int32_t* groups;  // the other pass: requests groups[0] .. groups[ngroups] - 1 have a prefix
+    const int32_t* groups;  // requests groups[0] .. groups[ngroups] - 1 have a prefix
     int ngroups, requests;
-    float2* ml;             // [total][Hq] of the prefixes' pass: maximum and sum
-    float* o;               // [total][Hq][d] of the prefixes' pass, normalised
+    int leaves;             // this pass leaves the rows that have a prefix
+    float2* ml;             // [total][Hq]; of the other pass where this one does not leave its rows
+    float* o;               // [total][Hq][d]
     PagedCut* cuts;         // [2 * kPagedCtas], prefixes' pass of the row-tile kernel; zero at the start
+    // both passes at once: what the other one reads and how it works, for the
+    // number of CTAs that it gets
+    const int32_t *other_len, *other_cu;
+    int other_n, other_cap;      // its requests, and the longest that one may be
+    int other_rows, other_cost;  // split-key kernel: rows of the row-tile kernel's units, and what one costs
+    float place_us, other_us;  // time of a place on this pass's line and on the other's
 };
 
 struct PagedArgs {
@@ -175,6 +185,27 @@ __device__ __forceinline__ bool paged_members(const PagedJoin& j, int& i0, int& 
 __device__ __forceinline__ bool paged_joins(const PagedJoin& j, int b) {
     return b >= j.groups[0] && b < j.groups[j.ngroups];
 }
+// Places of the row-tile kernel's line that a request of `rows` rows and `len` keys
+// has for each key head, all keys seen by all rows.
+__device__ __forceinline__ long long paged_tile_places(int len, int cap, int rows, int unit, int cost) {
+    const long long tiles = max(1, (min(max(len, 0), cap) + 127) >> 7);
+    return (tiles + cost) * ((rows + unit - 1) / unit);
+}
+// Whether this pass leaves request b's rows to another kernel.
+__device__ __forceinline__ bool paged_leaves(const PagedJoin& j, int b) {
+    return j.leaves && (j.first || paged_joins(j, b));
+}
+// CTAs of this pass where both run at once, each in proportion to its work.
+__device__ __forceinline__ int paged_share(const PagedJoin& j, long long mine, long long other) {
+    const float a = j.place_us * static_cast<float>(mine), b = j.other_us * static_cast<float>(other);
+    if (!j.other_len || mine == 0) return kPagedCtas;
+    return min(max(static_cast<int>(kPagedCtas * (a / (a + b)) + 0.5f), 1), kPagedCtas - 1);
+}
+// Maximum and sum that the other pass left of a row.
+__device__ __forceinline__ float2 paged_left(const PagedJoin& j, size_t row) {
+    const float2 b = __ldcg(&j.ml[row]);
+    return make_float2(b.x, -b.y);
+}
 // Softmax over two sets of keys with maxima m (log2 units) and sums l (both
 // times 2^6, as the kernels keep them): the weights of the own output (not
 // normalised) and of the prefix's (normalised), and L.
@@ -215,6 +246,35 @@ inline FastDiv make_fast_div(int d) {
     while ((1ull << l) < static_cast<uint64_t>(d)) ++l;
     const uint64_t m = ((((1ull << l) - d) << 32) / d) + 1;
     return {static_cast<uint32_t>(d), static_cast<uint32_t>(m), l};
+}
+
+// Key tiles' time that a unit of the row-tile kernel takes beside its tiles', and
+// chunks' time of a split-key unit (see there).
+constexpr int paged_tile_cost(int d) { return d == 64 ? 6 : 8; }
+constexpr int paged_split_cost(int d) { return d == 64 ? 48 : 32; }
+
+// Sets up both passes of a call with shared prefixes to run at once. Times of a
+// place on either line of work, in us: a tile of 128 keys for one or for two row
+// tiles; a chunk of 32 keys for 8, 16, .. rows (SHARE_FIG).
+inline void paged_run_both(PagedArgs& prefix, PagedArgs& own, float2* own_ml, float* own_o) {
+    const int nt = own.split_rows / 8;
+    prefix.join.place_us = prefix.one_tile ? 1.4f : prefix.d == 64 ? 1.65f : 2.6f;
+    prefix.join.other_us = prefix.d == 64 ? 0.115f + 0.038f * (nt - 1) : 0.18f + 0.05f * (nt - 1);
+    prefix.join.other_len = own.cache_len;
+    prefix.join.other_cu = own.cu_seqlens;
+    prefix.join.other_n = own.B;
+    prefix.join.other_cap = own.max_blocks * own.block_size;
+    prefix.join.other_cost = paged_split_cost(own.d);
+    own.join.place_us = prefix.join.other_us;
+    own.join.other_us = prefix.join.place_us;
+    own.join.other_len = prefix.cache_len;
+    own.join.other_n = prefix.B;
+    own.join.other_cap = prefix.max_blocks * prefix.block_size;
+    own.join.other_rows = prefix.one_tile ? 128 : kPagedTileRows;
+    own.join.other_cost = paged_tile_cost(own.d);
+    own.join.leaves = 1;
+    own.join.ml = own_ml;
+    own.join.o = own_o;
 }
 
 cudaError_t launch_cache_plan(const PlanArgs& a, cudaStream_t stream, int* nlaunch);

@@ -89,7 +89,7 @@ struct PgCfg {
     // chunks' time that a long unit's rows, barriers and merge take (64 requests
     // of 1 to 16,384 tokens: d = 128 271 us with 1, 192 with 32, 196 with 48; d = 64
     // 212 with 1, 126 with 48, 129 with 72)
-    static constexpr int COST = D == 64 ? 48 : 32;
+    static constexpr int COST = paged_split_cost(D);
     static constexpr int TILE = kPgChunk * D;             // bytes of a chunk's K (or V)
     static constexpr int SUBS = B16 ? 2 : 1;              // boxes of a tile
     static constexpr int BOX = TILE / SUBS;
@@ -207,6 +207,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
     __shared__ int nan_seen, abort_s;
     __shared__ float row_before[PFX ? RT : 1];
     __shared__ int nmax_s, most_s, scan_u[C::W];
+    __shared__ long long scan_o[2][PFX ? C::W : 1];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     if constexpr (PFX) paged_let_next();
 
@@ -240,16 +241,53 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     if (lane == 0) scan_w[0][warp] = sum;
+    if constexpr (PFX) {
+        if (p.join.other_len) {
+            // places of the row-tile kernel's line, and this pass's units
+            long long tiles = 0, units = 0;
+            for (int b = tid; b < p.join.other_n; b += C::THREADS) {
+                int i0 = b, i1 = b + 1;
+                PagedJoin j = p.join;
+                j.first = j.groups;
+                paged_members(j, i0, i1);
+                const int n = max(min(p.cu_seqlens[i1], p.total) - max(p.cu_seqlens[i0], 0), 0);
+                tiles += paged_tile_places(p.join.other_len[b], p.join.other_cap, n * p.G, p.join.other_rows,
+                                           p.join.other_cost) * p.Hkv;
+            }
+            for (int b = b0; b < b1; ++b) units += p.cu_seqlens[b + 1] > p.cu_seqlens[b] ? p.Hkv : 0;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) {
+                tiles += __shfl_xor_sync(0xffffffffu, tiles, off);
+                units += __shfl_xor_sync(0xffffffffu, units, off);
+            }
+            if (lane == 0) {
+                scan_o[0][warp] = tiles;
+                scan_o[1][warp] = units;
+            }
+        }
+    }
     __syncthreads();
     long long W = 0;
     for (int w = 0; w < C::W; ++w) W += scan_w[0][w];
+    // CTAs that work: all, or where the prefixes' pass runs beside this one its share
+    int ctas = kPagedCtas;
+    if constexpr (PFX) {
+        if (p.join.other_len) {
+            long long tiles = 0, units = 0;
+            for (int w = 0; w < C::W; ++w) {
+                tiles += scan_o[0][w];
+                units += scan_o[1][w];
+            }
+            ctas = paged_share(p.join, W + units * C::COST, tiles);
+        }
+    }
     // A unit of up to a third of a warp's even share of all chunks is short, and
     // one of up to twelve chunks always: a long unit costs its CTA barriers and a
     // merge, a short one keeps a single warp busy, at the end while others have
     // nothing left. d = 128, one token, 8 heads of keys: 1,024 requests of 1 to
     // 600 tokens 197 us (up to a sixth: 251; none short: 302), 256 requests of 1 to
     // 2,000 tokens 143 us (up to a half: 160; to the whole share: 172).
-    const long long share = W / (kPagedCtas * C::W);
+    const long long share = W / (ctas * C::W);
     int T = static_cast<int>(min(max(share / 3, 12ll), 1ll << 30));
     int solo = 0;  // PFX: places that every unit has, one CTA's each; 0: as many as its chunks and COST
     auto places = [&](const PgSeg& s) { return PFX && solo ? solo : s.nchunk + C::COST; };
@@ -332,8 +370,8 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
         // after the other in a lone warp: all units are long ones too where the
         // line of all then ends first (in chunks' time; a unit's own length
         // included; 16 requests of up to 512 tokens, 8 heads of keys: PFX_FIG).
-        const long long lone = (Wl / kPagedCtas) / C::W + max(Ws / (kPagedCtas * C::W), static_cast<long long>(nmax)) + 2;
-        const long long together = max(Wa / kPagedCtas, static_cast<long long>(nmax) + C::COST) / C::W;
+        const long long lone = (Wl / ctas) / C::W + max(Ws / (ctas * C::W), static_cast<long long>(nmax)) + 2;
+        const long long together = max(Wa / ctas, static_cast<long long>(nmax) + C::COST) / C::W;
         all_long |= together < lone;
     }
     if (all_long) {
@@ -347,7 +385,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
     if constexpr (PFX) {
         // Few and short enough, each unit is a CTA's: that costs less than the merge
         // of a unit that was cut (four requests behind 1,000 tokens: SOLO_FIG).
-        if (U <= kPagedCtas && most <= kPgSolo) {
+        if (U <= ctas && most <= kPgSolo) {
             T = 0;
             solo = most + C::COST;
             Wl = static_cast<long long>(U) * solo;
@@ -358,13 +396,14 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
         }
     }
     // equal quotas of the long line, at least one chunk for each warp
-    long long quota = max((Wl + kPagedCtas - 1) / kPagedCtas, static_cast<long long>(C::W));
+    long long quota = max((Wl + ctas - 1) / ctas, static_cast<long long>(C::W));
     if (PFX && solo) quota = solo;
     const long long x0 = quota * blockIdx.x, x1 = min(x0 + quota, Wl);
     // the short units that start in this warp's part of their line; parts that
     // follow one another lie in different CTAs
-    const long long part = (Ws + kPagedCtas * C::W - 1) / (kPagedCtas * C::W);
-    const long long y0 = part * (warp * kPagedCtas + static_cast<int>(blockIdx.x)), y1 = min(y0 + part, Ws);
+    const long long part = (Ws + ctas * C::W - 1) / (ctas * C::W);
+    const bool idle = static_cast<int>(blockIdx.x) >= ctas;
+    const long long y0 = idle ? Ws : part * (warp * ctas + static_cast<int>(blockIdx.x)), y1 = min(y0 + part, Ws);
     short_base[tid] = bs;
     if (tid == C::THREADS - 1) short_base[C::THREADS] = Ws;
     if (x0 < x1 && x0 >= bw && x0 < bw + ml_) {
@@ -851,9 +890,9 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
                     if (r >= nrow) continue;
                     float inv = l[nt][e] == 0.f ? 0.f : 1.f / l[nt][e];
                     const size_t orow = static_cast<size_t>(cs.tok0 + tok) * p.Hq + hq;
-                    float before = 0.f;  // weight of the prefix
+                    float before = -1.f;  // weight of the prefix, if there is one
                     if constexpr (PFX) {
-                        if (p.join.first) {
+                        if (paged_leaves(p.join, cs.b)) {
                             float* dst = p.join.o + orow * D + g * (D / 8);
 #pragma unroll
                             for (int i = 0; i < C::MI; ++i) {
@@ -864,12 +903,12 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
                                 }
                                 *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(a, b);
                             }
-                            if (g == 0) p.join.ml[orow] = make_float2(m[nt][e], l[nt][e]);
+                            if (g == 0) p.join.ml[orow] = make_float2(m[nt][e], -l[nt][e]);
                             continue;
                         }
-                        if (paged_joins(p.join, cs.b)) {
+                        if (!p.join.leaves && paged_joins(p.join, cs.b)) {
                             paged_wait_before();
-                            const PagedWeights w = paged_weights(m[nt][e], l[nt][e], __ldcg(&p.join.ml[orow]));
+                            const PagedWeights w = paged_weights(m[nt][e], l[nt][e], paged_left(p.join, orow));
                             inv = w.own;
                             before = w.prefix;
                             if (g == 0) p.lse[static_cast<size_t>(hq) * p.total + cs.tok0 + tok] = w.lse;
@@ -887,7 +926,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
                             b = nan_at[g * (D / 8) + 2 * i + 1] < lim[nt][e] ? CUDART_NAN_F : b;
                         }
                         if constexpr (PFX) {
-                            if (before != 0.f) {
+                            if (!(before < 0.f)) {
                                 const float2 x = __ldcg(reinterpret_cast<const float2*>(p.join.o + orow * D + g * (D / 8)) + i);
                                 a = fmaf(before, x.x, a);
                                 b = fmaf(before, x.y, b);
@@ -912,7 +951,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
         }
         // ---------------------------------------------------- merge of the warps
         if constexpr (PFX)
-            if (!p.join.first) paged_wait_before();
+            if (!p.join.leaves) paged_wait_before();
         if (nan_bits) nan_seen = 1;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -936,12 +975,12 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
         auto row_end = [&](int r, float M, float L) {
             const int tok = p.by_g.div(r), hq = cs.hk * p.G + r - tok * p.G;
             const size_t orow = static_cast<size_t>(cs.tok0 + tok) * p.Hq + hq;
-            float own = L == 0.f ? 0.f : 1.f / L, before = 0.f, lse = lse_of(M, L);
-            if (p.join.first) {
-                p.join.ml[orow] = make_float2(M, L);
+            float own = L == 0.f ? 0.f : 1.f / L, before = -1.f, lse = lse_of(M, L);
+            if (paged_leaves(p.join, cs.b)) {
+                p.join.ml[orow] = make_float2(M, -L);
             } else {
-                if (paged_joins(p.join, cs.b)) {
-                    const PagedWeights w = paged_weights(M, L, __ldcg(&p.join.ml[orow]));
+                if (!p.join.leaves && paged_joins(p.join, cs.b)) {
+                    const PagedWeights w = paged_weights(M, L, paged_left(p.join, orow));
                     own = w.own;
                     before = w.prefix;
                     lse = w.lse;
@@ -1005,11 +1044,11 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
                     const size_t at = (static_cast<size_t>(cs.tok0 + tok) * p.Hq + hq) * D + col;
                     sum *= ml[C::W * RT + r].y;
                     if constexpr (PFX) {
-                        if (p.join.first) {
+                        if (paged_leaves(p.join, cs.b)) {
                             p.join.o[at] = sum;
                             continue;
                         }
-                        if (row_before[r] != 0.f) sum = fmaf(row_before[r], __ldcg(&p.join.o[at]), sum);
+                        if (!(row_before[r] < 0.f)) sum = fmaf(row_before[r], __ldcg(&p.join.o[at]), sum);
                     }
                     p.o[at] = static_cast<uint16_t>(pack_bf16x2(sum, 0.f) & 0xFFFFu);
                 }
@@ -1082,11 +1121,11 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
                         acc.w *= iL;
                         float4* at = reinterpret_cast<float4*>(
                             p.join.o + (static_cast<size_t>(cs.tok0 + tok) * p.Hq + hq) * D + c4 * 4);
-                        if (p.join.first) {
+                        if (paged_leaves(p.join, cs.b)) {
                             *at = acc;
                             continue;
                         }
-                        if (row_before[r] != 0.f) {
+                        if (!(row_before[r] < 0.f)) {
                             const float4 x = __ldcg(at);
                             acc.x = fmaf(row_before[r], x.x, acc.x);
                             acc.y = fmaf(row_before[r], x.y, acc.y);

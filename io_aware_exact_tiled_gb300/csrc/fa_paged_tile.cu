@@ -60,7 +60,7 @@ constexpr float kPtSpan = 60.0f;    // log2 of the largest ratio of V's block sc
 // to 1,999 tokens, 16 heads: d = 64 105 us with 1, 94 with 6, 99 with 12; d = 128
 // 177, 160 with 6, 155 with 8 and with 12)
 template <int D>
-constexpr int kPtUnitCost = D == 64 ? 6 : 8;
+constexpr int kPtUnitCost = paged_tile_cost(D);
 constexpr int kPtScaleSlots = 8;
 constexpr uint32_t kFmtE5M2 = 1;  // kind::f8f6f4 operand format code
 constexpr int kPtNanSlots = 4;
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(512, 1)
     constexpr int RT = ONE ? 128 : 256, STEP = ONE ? 2 : 1;  // rows of a unit; key tiles from one of a row tile's to the next
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    __shared__ long long scan_w[16], scan_u[16];
+    __shared__ long long scan_w[16], scan_u[16], scan_o[PFX ? 16 : 1];
     __shared__ long long start_line;
     __shared__ int start_b, start_units, abort_s, last_s[2], nan_piece[kPtNanSlots], wide_s[2];
     __shared__ uint32_t tmem_slot;
@@ -369,6 +369,17 @@ __global__ void __launch_bounds__(512, 1)
     if (lane == 31) {
         scan_w[warp] = iw;
         scan_u[warp] = iu;
+    }
+    if constexpr (PFX) {
+        if (p.join.other_len) {  // places of the split-key kernel's line
+            long long other = 0;
+            for (int b = tid; b < p.join.other_n; b += 512)
+                if (p.join.other_cu[b + 1] > p.join.other_cu[b])
+                    other += max(1, (min(max(p.join.other_len[b], 0), p.join.other_cap) + 31) >> 5) + p.join.other_cost;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) other += __shfl_xor_sync(0xffffffffu, other, off);
+            if (lane == 0) scan_o[warp] = other * p.Hkv;
+        }
     }
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::BAR_OFF);
     uint64_t* q_full = bars;                   // [2] Q parts of a row tile stored
@@ -439,7 +450,16 @@ __global__ void __launch_bounds__(512, 1)
         W += scan_w[w];
         U += scan_u[w];
     }
-    const long long quota = max((W + kPagedCtas - 1) / kPagedCtas, 2ll);
+    // CTAs that work: all, or where the requests' own pass runs beside this one its share
+    int ctas = kPagedCtas;
+    if constexpr (PFX) {
+        if (p.join.other_len) {
+            long long other = 0;
+            for (int w = 0; w < 16; ++w) other += scan_o[w];
+            ctas = paged_share(p.join, W, other);
+        }
+    }
+    const long long quota = max((W + ctas - 1) / ctas, 2ll);
     const long long x0 = quota * blockIdx.x, x1 = min(x0 + quota, W);
     if (U > p.max_units || x0 >= x1) {  // uniform over the CTA, before any TMEM use
         // (too many units: overlapping offsets, which the split-key kernel reports)
@@ -528,56 +548,187 @@ __global__ void __launch_bounds__(512, 1)
         // nothing but TMEM to give back
     } else if (warp < 4) {
         regs_dec<96>();
-        // A tile's loads depend on one another (block id, then scales and copies):
-        // ids come four tiles ahead and scales two, by asynchronous copies of a
-        // lane for each group of 16 keys. One warp requests the copies and another
-        // sees to the scales: together they took a warp 2,370 cycles a tile, which
-        // is what a long prefix then took (LOAD_FIG).
-        const int bs = 1 << p.bs_log2, box = min(bs, 128);
-        int* ahead = reinterpret_cast<int*>(sm + C::AHEAD_OFF) + (warp == 0 ? 0 : 8 * kPtAhead);
-        auto has = [&](int t) { return lane < 8 && t < s.c1 && t * 128 + lane * 16 < s.r.len; };
-        auto id_at = [&](int t) { return ahead + (t % kPtAhead) * 8 + lane; };  // lanes 0..7
-        auto fetch_id = [&](int t) {
-            if (has(t))
-                cp_async4(id_at(t), &p.block_table[static_cast<size_t>(s.r.b) * p.max_blocks +
-                                                   ((t * 128 + lane * 16) >> p.bs_log2)]);
-        };
-        auto is_block = [&](int id) { return id >= 0 && id < p.num_blocks; };
-        auto row_of = [&](int id, int t) {
-            return static_cast<int>(((static_cast<long long>(id) * p.Hkv + s.hk) << p.bs_log2) +
-                                    ((t * 128 + lane * 16) & (bs - 1)));
-        };
-        // the first lane of each box of min(block, 128) rows requests it
-        const bool asks = lane < 8 && lane % (box >> 4) == 0;
-        if (warp == 0) {
-            // ------------------------------------------------------ K and V tiles
+        if (ONE && (warp == 0 || warp == 3)) {
+            // A tile's loads depend on one another (block id, then scales and
+            // copies): ids come four tiles ahead and scales two, by asynchronous
+            // copies of a lane for each group of 16 keys. One warp requests the
+            // copies and another sees to the scales: together they took a warp
+            // 2,370 cycles a tile, which is what a prefix of few rows then took
+            // (LOAD_FIG). With two row tiles a tile takes longer than that.
+            const int bs = 1 << p.bs_log2, box = min(bs, 128);
+            int* ahead = reinterpret_cast<int*>(sm + C::AHEAD_OFF) + (warp == 0 ? 0 : 8 * kPtAhead);
+            auto has = [&](int t) { return lane < 8 && t < s.c1 && t * 128 + lane * 16 < s.r.len; };
+            auto id_at = [&](int t) { return ahead + (t % kPtAhead) * 8 + lane; };  // lanes 0..7
+            auto fetch_id = [&](int t) {
+                if (has(t))
+                    cp_async4(id_at(t), &p.block_table[static_cast<size_t>(s.r.b) * p.max_blocks +
+                                                       ((t * 128 + lane * 16) >> p.bs_log2)]);
+            };
+            auto is_block = [&](int id) { return id >= 0 && id < p.num_blocks; };
+            auto row_of = [&](int id, int t) {
+                return static_cast<int>(((static_cast<long long>(id) * p.Hkv + s.hk) << p.bs_log2) +
+                                        ((t * 128 + lane * 16) & (bs - 1)));
+            };
+            // the first lane of each box of min(block, 128) rows requests it
+            const bool asks = lane < 8 && lane % (box >> 4) == 0;
+            if (warp == 0) {
+                // ------------------------------------------------------ K and V tiles
+                int u = 0, klast = -1;
+                bool ok = true;
+                do {
+#pragma unroll 1
+                    for (int t = 0; t < 4; ++t) {
+                        fetch_id(s.c0 + t);
+                        cp_async_commit();
+                    }
+                    for (int t = s.c0; ok && t < s.c1; ++t, ++u) {
+                        const int st = u % C::KS, rs = u % C::RS;
+                        cp_async_wait<3>();
+                        int id = has(t) ? *id_at(t) : 0;
+                        if (!is_block(id)) {
+                            atomicCAS(p.status, 0, FA_DEV_INVALID | (94 << 8));
+                            id = 0;
+                        }
+                        fetch_id(t + 4);
+                        cp_async_commit();
+                        const int row = row_of(id, t);
+                        if (!(ok = wait_warp(&k_empty[st], ((u / C::KS) & 1) ^ 1))) break;
+                        if (lane == 0) {
+                            mbar_arrive(&asked[u % kPtScaleSlots]);
+                            mbar_arrive_expect_tx(&k_full[st], C::K_BYTES);
+                        }
+                        __syncwarp();
+                        if (asks)
+                            tma_load_2d(sm + C::K_OFF + st * C::K_BYTES + lane * 16 * D, &tmK, 0, row, &k_full[st]);
+                        if (!(ok = wait_warp(&r_empty[rs], ((u / C::RS) & 1) ^ 1))) {
+                            klast = u + 1;
+                            break;
+                        }
+                        if (lane == 0) mbar_arrive_expect_tx(&r_full[rs], C::K_BYTES);
+                        __syncwarp();
+                        if (asks)
+                            tma_load_2d(sm + C::R_OFF + rs * C::K_BYTES + lane * 16 * D, &tmV, 0, row, &r_full[rs]);
+                    }
+                    cp_async_wait<0>();
+                } while (ok && next(s));
+                if (!ok) pt_gave_up(&abort_s, p.status, 95);
+                // let every copy in flight land before the CTA can exit
+                if (lane == 0) {
+                    const int nk = max(u, klast);
+                    for (int i = 0; i < C::KS && i < nk; ++i) {
+                        const int last = i + ((nk - 1 - i) / C::KS) * C::KS;
+                        mbar_wait_teardown(&k_full[i], (last / C::KS) & 1, 200000000ull);
+                    }
+                    for (int i = 0; i < C::RS && i < u; ++i) {
+                        const int last = i + ((u - 1 - i) / C::RS) * C::RS;
+                        mbar_wait_teardown(&r_full[i], (last / C::RS) & 1, 200000000ull);
+                    }
+                }
+            } else {
+                // ------------------------------------------------------ scales
+                // A slot is written once K of its tile has been requested: the tile
+                // eight before it, whose slot it was, is then through its softmax.
+                float* raw = reinterpret_cast<float*>(ahead + 8 * kPtAhead);  // {ks, vs} [kPtAhead][8]
+                float* sc = reinterpret_cast<float*>(sm + C::SC_OFF);
+                auto fetch_scales = [&](int t) {
+                    if (!has(t)) return;
+                    const int id = *id_at(t);
+                    if (!is_block(id)) return;
+                    const size_t x = static_cast<size_t>(id) * p.Hkv + s.hk;
+                    cp_async4(raw + ((t % kPtAhead) * 8 + lane) * 2, &p.k_scale[x]);
+                    cp_async4(raw + ((t % kPtAhead) * 8 + lane) * 2 + 1, &p.v_scale[x]);
+                };
+                int u = 0;
+                bool ok = true;
+                do {
+                    float vref = 0.f;  // largest V scale met so far in this piece
+#pragma unroll 1
+                    for (int t = 0; t < 4; ++t) fetch_id(s.c0 + t);
+                    cp_async_commit();
+                    cp_async_wait<0>();
+                    fetch_scales(s.c0);
+                    cp_async_commit();
+                    fetch_scales(s.c0 + 1);
+                    cp_async_commit();
+                    for (int t = s.c0; ok && t < s.c1; ++t, ++u) {
+                        cp_async_wait<1>();
+                        float ks = 0.f, vs = 0.f;
+                        if (has(t) && is_block(*id_at(t))) {
+                            ks = raw[((t % kPtAhead) * 8 + lane) * 2];
+                            vs = raw[((t % kPtAhead) * 8 + lane) * 2 + 1];
+                        }
+                        fetch_scales(t + 2);
+                        fetch_id(t + 4);
+                        cp_async_commit();
+                        float top = vs;
+#pragma unroll
+                        for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        vref = fmaxf(vref, top);
+                        // groups whose scale is below 2^-60 of the largest (blocks of
+                        // zeros have 2^-126) count as if it were that
+                        const float lv = fmaxf(fmaxf(log2f(vs), log2f(vref) - kPtSpan), -100.f), il = exp2f(-lv);
+                        const int slot = u % kPtScaleSlots;
+                        if (!(ok = wait_warp(&asked[slot], (u / kPtScaleSlots) & 1))) break;
+                        if (lane < 8) {
+                            sc[slot * 24 + lane] = ks;
+                            sc[slot * 24 + 8 + lane] = lv;
+                            sc[slot * 24 + 16 + lane] = il;
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sc_full[slot]);
+                    }
+                    cp_async_wait<0>();
+                } while (ok && next(s));
+                if (!ok) pt_gave_up(&abort_s, p.status, 99);
+            }
+        } else if (warp == 0) {
+            // ------------------------------------------------------ K tiles and scales
+            const int bs = 1 << p.bs_log2, box = min(bs, 128);
             int u = 0, klast = -1;
             bool ok = true;
+            float* sc = reinterpret_cast<float*>(sm + C::SC_OFF);
             do {
-#pragma unroll 1
-                for (int t = 0; t < 4; ++t) {
-                    fetch_id(s.c0 + t);
-                    cp_async_commit();
-                }
+                float vref = 0.f;  // largest V scale met so far in this piece
                 for (int t = s.c0; ok && t < s.c1; ++t, ++u) {
-                    const int st = u % C::KS, rs = u % C::RS;
-                    cp_async_wait<3>();
-                    int id = has(t) ? *id_at(t) : 0;
-                    if (!is_block(id)) {
-                        atomicCAS(p.status, 0, FA_DEV_INVALID | (94 << 8));
-                        id = 0;
+                    const int st = u % C::KS, slot = u % kPtScaleSlots;
+                    // lane i < 8: the group of 16 keys from 16 i on
+                    int id = 0;
+                    float ks = 0.f, vs = 0.f;
+                    const int key = t * 128 + lane * 16;
+                    if (lane < 8 && key < s.r.len) {
+                        id = p.block_table[static_cast<size_t>(s.r.b) * p.max_blocks + (key >> p.bs_log2)];
+                        if (id < 0 || id >= p.num_blocks) {
+                            atomicCAS(p.status, 0, FA_DEV_INVALID | (94 << 8));
+                            id = 0;
+                        } else {
+                            ks = p.k_scale[static_cast<size_t>(id) * p.Hkv + s.hk];
+                            vs = p.v_scale[static_cast<size_t>(id) * p.Hkv + s.hk];
+                        }
                     }
-                    fetch_id(t + 4);
-                    cp_async_commit();
-                    const int row = row_of(id, t);
                     if (!(ok = wait_warp(&k_empty[st], ((u / C::KS) & 1) ^ 1))) break;
-                    if (lane == 0) {
-                        mbar_arrive(&asked[u % kPtScaleSlots]);
-                        mbar_arrive_expect_tx(&k_full[st], C::K_BYTES);
-                    }
+                    if (lane == 0) mbar_arrive_expect_tx(&k_full[st], C::K_BYTES);
                     __syncwarp();
+                    // the first lane of each box of min(block, 128) rows requests it
+                    const bool asks = lane < 8 && lane % (box >> 4) == 0;
+                    const int row = static_cast<int>(((static_cast<long long>(id) * p.Hkv + s.hk) << p.bs_log2) +
+                                                     ((t * 128 + lane * 16) & (bs - 1)));
                     if (asks)
                         tma_load_2d(sm + C::K_OFF + st * C::K_BYTES + lane * 16 * D, &tmK, 0, row, &k_full[st]);
+                    float top = vs;
+#pragma unroll
+                    for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    vref = fmaxf(vref, top);
+                    if (lane < 8) {
+                        // groups whose scale is below 2^-60 of the largest (blocks of
+                        // zeros have 2^-126) count as if it were that
+                        const float lv = fmaxf(fmaxf(log2f(vs), log2f(vref) - kPtSpan), -100.f);
+                        sc[slot * 24 + lane] = ks;
+                        sc[slot * 24 + 8 + lane] = lv;
+                        sc[slot * 24 + 16 + lane] = exp2f(-lv);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sc_full[slot]);
+                    const int rs = u % C::RS;
                     if (!(ok = wait_warp(&r_empty[rs], ((u / C::RS) & 1) ^ 1))) {
                         klast = u + 1;
                         break;
@@ -587,7 +738,6 @@ __global__ void __launch_bounds__(512, 1)
                     if (asks)
                         tma_load_2d(sm + C::R_OFF + rs * C::K_BYTES + lane * 16 * D, &tmV, 0, row, &r_full[rs]);
                 }
-                cp_async_wait<0>();
             } while (ok && next(s));
             if (!ok) pt_gave_up(&abort_s, p.status, 95);
             // let every copy in flight land before the CTA can exit
@@ -602,62 +752,6 @@ __global__ void __launch_bounds__(512, 1)
                     mbar_wait_teardown(&r_full[i], (last / C::RS) & 1, 200000000ull);
                 }
             }
-        } else if (warp == 3) {
-            // ------------------------------------------------------ scales
-            // A slot is written once K of its tile has been requested: the tile
-            // eight before it, whose slot it was, is then through its softmax.
-            float* raw = reinterpret_cast<float*>(ahead + 8 * kPtAhead);  // {ks, vs} [kPtAhead][8]
-            float* sc = reinterpret_cast<float*>(sm + C::SC_OFF);
-            auto fetch_scales = [&](int t) {
-                if (!has(t)) return;
-                const int id = *id_at(t);
-                if (!is_block(id)) return;
-                const size_t x = static_cast<size_t>(id) * p.Hkv + s.hk;
-                cp_async4(raw + ((t % kPtAhead) * 8 + lane) * 2, &p.k_scale[x]);
-                cp_async4(raw + ((t % kPtAhead) * 8 + lane) * 2 + 1, &p.v_scale[x]);
-            };
-            int u = 0;
-            bool ok = true;
-            do {
-                float vref = 0.f;  // largest V scale met so far in this piece
-#pragma unroll 1
-                for (int t = 0; t < 4; ++t) fetch_id(s.c0 + t);
-                cp_async_commit();
-                cp_async_wait<0>();
-                fetch_scales(s.c0);
-                cp_async_commit();
-                fetch_scales(s.c0 + 1);
-                cp_async_commit();
-                for (int t = s.c0; ok && t < s.c1; ++t, ++u) {
-                    cp_async_wait<1>();
-                    float ks = 0.f, vs = 0.f;
-                    if (has(t) && is_block(*id_at(t))) {
-                        ks = raw[((t % kPtAhead) * 8 + lane) * 2];
-                        vs = raw[((t % kPtAhead) * 8 + lane) * 2 + 1];
-                    }
-                    fetch_scales(t + 2);
-                    fetch_id(t + 4);
-                    cp_async_commit();
-                    float top = vs;
-#pragma unroll
-                    for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    vref = fmaxf(vref, top);
-                    // groups whose scale is below 2^-60 of the largest (blocks of
-                    // zeros have 2^-126) count as if it were that
-                    const float lv = fmaxf(fmaxf(log2f(vs), log2f(vref) - kPtSpan), -100.f), il = exp2f(-lv);
-                    const int slot = u % kPtScaleSlots;
-                    if (!(ok = wait_warp(&asked[slot], (u / kPtScaleSlots) & 1))) break;
-                    if (lane < 8) {
-                        sc[slot * 24 + lane] = ks;
-                        sc[slot * 24 + 8 + lane] = lv;
-                        sc[slot * 24 + 16 + lane] = il;
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sc_full[slot]);
-                }
-                cp_async_wait<0>();
-            } while (ok && next(s));
-            if (!ok) pt_gave_up(&abort_s, p.status, 99);
         } else if (warp < 3) {
             // ------------------------------------------------------ products of row tile i
             // A key tile's two halves of 64 keys have S columns of their own:
@@ -925,15 +1019,15 @@ __global__ void __launch_bounds__(512, 1)
                                           : 2 * static_cast<int>(blockIdx.x) + (s.line0 <= x0 ? 0 : 1);
             const bool leave = ONE || !whole;
             float inv = leave ? 1.f : l == 0.f ? 0.f : 1.f / l;
-            // PFX: weight of the prefix in the row's output, and L
-            [[maybe_unused]] float before = 0.f, lse_all = 0.f;
+            // PFX: weight of the prefix, if there is one, in the row's output, and L
+            [[maybe_unused]] float before = -1.f, lse_all = 0.f;
             [[maybe_unused]] const size_t orow = qrow / D;
             auto row_weights = [&](float M, float L, float& own) {
                 lse_all = L == 0.f ? -CUDART_INF_F : (M - kPtOffset + log2f(L)) * kPtLn2;
-                if (p.join.first) {
-                    if (row_ok) p.join.ml[orow] = make_float2(M, L);
+                if (p.join.leaves) {
+                    if (row_ok) p.join.ml[orow] = make_float2(M, -L);
                 } else if (row_ok && paged_joins(p.join, s.r.b)) {
-                    const PagedWeights w = paged_weights(M, L, __ldcg(&p.join.ml[orow]));
+                    const PagedWeights w = paged_weights(M, L, paged_left(p.join, orow));
                     own = w.own;
                     before = w.prefix;
                     lse_all = w.lse;
@@ -942,12 +1036,12 @@ __global__ void __launch_bounds__(512, 1)
             // columns c .. c + 7 of the row, normalised
             auto put_row = [&](int c, float (&v)[8]) {
                 float4* at = reinterpret_cast<float4*>(p.join.o + qrow + c);
-                if (p.join.first) {
+                if (p.join.leaves) {
                     at[0] = make_float4(v[0], v[1], v[2], v[3]);
                     at[1] = make_float4(v[4], v[5], v[6], v[7]);
                     return;
                 }
-                if (before != 0.f) {
+                if (!(before < 0.f)) {
                     const float4 x = __ldcg(at), y = __ldcg(at + 1);
                     v[0] = fmaf(before, x.x, v[0]);
                     v[1] = fmaf(before, x.y, v[1]);
@@ -963,7 +1057,7 @@ __global__ void __launch_bounds__(512, 1)
                                pack_bf16x2(v[6], v[7]));
             };
             if constexpr (PFX) {
-                if (!p.join.first) paged_wait_before();
+                if (!p.join.leaves) paged_wait_before();
                 if (!leave) row_weights(mu, l, inv);
             }
             // partial outputs lie as [d / 4][128 rows] float4, coalesced over the rows
@@ -1020,7 +1114,7 @@ __global__ void __launch_bounds__(512, 1)
             const float lse_off = kPtOffset;
             if (!leave) {
                 if constexpr (PFX) {
-                    if (row_ok && !p.join.first) p.lse[static_cast<size_t>(hq) * p.total + s.r.tok0 + tok] = lse_all;
+                    if (row_ok && !p.join.leaves) p.lse[static_cast<size_t>(hq) * p.total + s.r.tok0 + tok] = lse_all;
                 } else if (row_ok)
                     p.lse[static_cast<size_t>(hq) * p.total + s.r.tok0 + tok] =
                         l == 0.f ? -CUDART_INF_F : (mu - lse_off + log2f(l)) * kPtLn2;
@@ -1076,7 +1170,7 @@ __global__ void __launch_bounds__(512, 1)
                     }
                 }
                 if constexpr (PFX) {
-                    if (p.join.first) {  // merged by a kernel of its own, over the whole GPU
+                    if (p.join.leaves) {  // merged by a kernel of its own, over the whole GPU
                         if (r == 0 && i == 0 && s.c0 == 0)
                             p.join.cuts[slot] = {1, s.r.tok0, s.pair * RT, rows, s.hk, f, e, ONE ? (twice ? 4 : 2) : 1, s.line0, quota};
                         continue;
@@ -1139,7 +1233,7 @@ __global__ void __launch_bounds__(512, 1)
                         }
                     }
                     if constexpr (PFX) {
-                        if (row_ok && !p.join.first) p.lse[static_cast<size_t>(hq) * p.total + s.r.tok0 + tok] = lse_all;
+                        if (row_ok && !p.join.leaves) p.lse[static_cast<size_t>(hq) * p.total + s.r.tok0 + tok] = lse_all;
                     } else if (row_ok)
                         p.lse[static_cast<size_t>(hq) * p.total + s.r.tok0 + tok] =
                             L == 0.f ? -CUDART_INF_F : (M - lse_off + log2f(L)) * kPtLn2;
