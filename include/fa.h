@@ -399,7 +399,8 @@ fa_status fa_qk_norm_rope_bwd(const fa_rows* q, const fa_rows* k, const fa_rows*
  * it is. Packed batches of bf16 only ([heads, total] rows; batch strides
  * unused). Tokens of no sequence are skipped, whatever their slots; tokens
  * without a slot have their row of q_out all the same. Arguments as for the two
- * calls, slots and their order included. Runs one kernel; no workspace.
+ * calls, slots and their order included. Runs one kernel, two in large batches; no
+ * workspace.
  */
 fa_status fa_qk_norm_rope_append(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows* q_out,
                                  void* k_cache, void* v_cache, float* k_scale, float* v_scale, const int32_t* slots,

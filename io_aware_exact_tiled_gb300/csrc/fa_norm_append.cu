@@ -124,61 +124,97 @@ __global__ void __launch_bounds__(256)
         *reinterpret_cast<uint2*>(row + ln.b) = append_quantise(raw.w[1], inv);
     };
     if (n <= 2) {
-        // ------------------------------------------------ the CTA takes the runs in turn
+        // ------------------------------------------------ the CTA takes the runs in turn,
+        // HPC heads at a time; a lane's angles stay in shared memory for the next ones
         const int row = tid / LN::TPR;
+        constexpr bool KEEP = L <= 2;
+        ulonglong2* kept = reinterpret_cast<ulonglong2*>(ring) + tid;  // [L][4][256]
         for (int k = 0; k < n; ++k) {
             const int lead = leads[k], end = run_end(lead), first = slot_of[lead] & (bs - 1);
-            NormRaw<uint16_t> raw[L][HPC];
-            uint32_t top[HPC];
-            float old[HPC];
-#pragma unroll
-            for (int h = 0; h < HPC; ++h) {
-                top[h] = 0;
-                old[h] = first > 0 && h < nh ? append_old_scale(scale_at(lead, h0 + h)) : 0.f;
-            }
-#pragma unroll
-            for (int i = 0; i < L; ++i) {
-                const int t = lead + i * ROWS + row;
+            for (int h1 = h0; h1 < h0 + nh; h1 += HPC) {
+                const int mh = min(HPC, h0 + nh - h1);
+                NormRaw<uint16_t> raw[L][HPC];
+                uint32_t top[HPC];
+                float old[HPC];
 #pragma unroll
                 for (int h = 0; h < HPC; ++h) {
-                    raw[i][h].zero();
-                    if (t < end && h < nh) raw[i][h].load(source(h0 + h, t), ln.a, ln.b);
-                }
-                if (!is_v) {
-                    NormTurn turn;
-                    turn_of(min(t, end - 1), turn);
-#pragma unroll
-                    for (int h = 0; h < HPC; ++h) finish(raw[i][h], turn);
+                    top[h] = 0;
+                    old[h] = first > 0 && h < mh ? append_old_scale(scale_at(lead, h1 + h)) : 0.f;
                 }
 #pragma unroll
-                for (int h = 0; h < HPC; ++h) top[h] = append_amax(raw[i][h].w, top[h]);
-            }
+                for (int i = 0; i < L; ++i) {
+                    const int t = lead + i * ROWS + row;
 #pragma unroll
-            for (int h = 0; h < HPC; ++h) {
-                top[h] = __reduce_max_sync(0xffffffffu, top[h]);
-                if (lane == 0) warp_top[h][warp] = top[h];
-            }
-            __syncthreads();  // every thread has read the scales so far, too
-            float inv[HPC];
-#pragma unroll
-            for (int h = 0; h < HPC; ++h) {
-#pragma unroll
-                for (int x = 0; x < 8; ++x) top[h] = max(top[h], warp_top[h][x]);
-                const float s = append_scale(top[h], old[h]);
-                inv[h] = 1.f / s;  // a power of two: exact
-                if (h < nh) {
-                    if (first > 0 && s != old[h]) append_move(cache_at(lead, h0 + h), first * D, old[h] / s, tid, 256);
-                    if (tid == 0) *scale_at(lead, h0 + h) = s;
+                    for (int h = 0; h < HPC; ++h) {
+                        raw[i][h].zero();
+                        if (t < end && h < mh) raw[i][h].load(source(h1 + h, t), ln.a, ln.b);
+                    }
                 }
-            }
-            // the run's own rows, after the moved ones of a slot that it writes again
-            __syncthreads();
+                // the next heads' rows, into L2
 #pragma unroll
-            for (int i = 0; i < L; ++i) {
-                const int t = lead + i * ROWS + row;
+                for (int i = 0; i < L; ++i) {
+                    const int t = lead + i * ROWS + row;
 #pragma unroll
-                for (int h = 0; h < HPC; ++h)
-                    if (t < end && h < nh) store(cache_at(lead, h0 + h) + (slot_of[t] & (bs - 1)) * D, raw[i][h], inv[h]);
+                    for (int h = 0; h < HPC; ++h)
+                        if (ln.j < D / 64 && t < end && h1 + HPC + h < h0 + nh)
+                            asm volatile("prefetch.global.L2 [%0];" ::"l"(source(h1 + HPC + h, t) + ln.j * 64));
+                }
+#pragma unroll
+                for (int i = 0; i < L; ++i) {
+                    const int t = lead + i * ROWS + row;
+                    if (!is_v) {
+                        NormTurn turn;
+                        if (!KEEP || h1 == h0) {
+                            turn_of(min(t, end - 1), turn);
+                            if (KEEP) {
+#pragma unroll
+                                for (int y = 0; y < 4; ++y)
+                                    kept[(i * 4 + y) * 256] = make_ulonglong2(turn.c[y], turn.s[y]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {
+                                const ulonglong2 v = kept[(i * 4 + y) * 256];
+                                turn.c[y] = v.x;
+                                turn.s[y] = v.y;
+                            }
+                        }
+#pragma unroll
+                        for (int h = 0; h < HPC; ++h) finish(raw[i][h], turn);
+                    }
+#pragma unroll
+                    for (int h = 0; h < HPC; ++h) top[h] = append_amax(raw[i][h].w, top[h]);
+                }
+#pragma unroll
+                for (int h = 0; h < HPC; ++h) {
+                    top[h] = __reduce_max_sync(0xffffffffu, top[h]);
+                    if (lane == 0) warp_top[h][warp] = top[h];
+                }
+                __syncthreads();  // every thread has read the scales so far, too
+                float inv[HPC];
+#pragma unroll
+                for (int h = 0; h < HPC; ++h) {
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) top[h] = max(top[h], warp_top[h][x]);
+                    const float s = append_scale(top[h], old[h]);
+                    inv[h] = 1.f / s;  // a power of two: exact
+                    if (h < mh) {
+                        if (first > 0 && s != old[h])
+                            append_move(cache_at(lead, h1 + h), first * D, old[h] / s, tid, 256);
+                        if (tid == 0) *scale_at(lead, h1 + h) = s;
+                    }
+                }
+                // the run's own rows, after the moved ones of a slot that it writes
+                // again; and the maxima have been read
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < L; ++i) {
+                    const int t = lead + i * ROWS + row;
+#pragma unroll
+                    for (int h = 0; h < HPC; ++h)
+                        if (t < end && h < mh)
+                            store(cache_at(lead, h1 + h) + (slot_of[t] & (bs - 1)) * D, raw[i][h], inv[h]);
+                }
             }
         }
         return;
@@ -217,21 +253,28 @@ __global__ void __launch_bounds__(256)
 }
 
 template <int D, bool INTER, int L>
-static cudaError_t launch(const NormAppendArgs& a, cudaStream_t stream) {
+static cudaError_t launch(const NormAppendArgs& a, cudaStream_t stream, int* nlaunch) {
     constexpr int HPC = L >= 8 ? 1 : L == 4 ? 2 : 4;
     const int total = a.a.total, passes = (a.n.Hq * (D / 16) + 31) / 32;
     const int span = total > 8192 && a.a.block_size * D <= 2048 ? 128 : total > 1024 ? 64 : 16;
-    const int hpc = total > 1024 ? HPC : 1;
+    const bool big = total > 1024;
+    const int hpc = big ? 2 * HPC : 1;
     const unsigned kv = static_cast<unsigned>((total + span - 1) / span) * 2u * ((a.a.H + hpc - 1) / hpc);
     int parts = (152 * 16 + total - 1) / total;
     parts = parts > passes ? passes : parts;
     const long long want = (static_cast<long long>(total) * parts + 7) / 8;
-    const unsigned qc = static_cast<unsigned>(want < 152 * 8 ? want : 152 * 8);
+    unsigned qc = static_cast<unsigned>(want < 152 * 8 ? want : 152 * 8);
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = once_per_device(done, [] {
+    cudaError_t e = once_per_device(done, [] {
         return cudaFuncSetAttribute(fa_norm_append_kernel<D, INTER, L, HPC>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, kNormRing<uint16_t>);
     });
+    if (e == cudaSuccess && big) {  // the queries in a kernel with room for more of them on an SM (APPEND_FIG)
+        int n;
+        e = launch_norm(a.n, stream, &n);
+        qc = 0;
+        *nlaunch = 2;
+    }
     if (e != cudaSuccess) return e;
     fa_norm_append_kernel<D, INTER, L, HPC>
         <<<kv + qc, 256, kNormRing<uint16_t>, stream>>>(a, span, hpc, static_cast<int>(kv), parts);
@@ -243,14 +286,14 @@ cudaError_t launch_norm_append(const NormAppendArgs& a, cudaStream_t stream, int
         constexpr bool INTER = decltype(inter)::value;
         const int bs = a.a.block_size;
         if (a.n.d == 64) {
-            if (bs <= 64) return launch<64, INTER, 1>(a, stream);
-            if (bs == 128) return launch<64, INTER, 2>(a, stream);
-            return launch<64, INTER, 4>(a, stream);
+            if (bs <= 64) return launch<64, INTER, 1>(a, stream, nlaunch);
+            if (bs == 128) return launch<64, INTER, 2>(a, stream, nlaunch);
+            return launch<64, INTER, 4>(a, stream, nlaunch);
         } else {
-            if (bs <= 32) return launch<128, INTER, 1>(a, stream);
-            if (bs == 64) return launch<128, INTER, 2>(a, stream);
-            if (bs == 128) return launch<128, INTER, 4>(a, stream);
-            return launch<128, INTER, 8>(a, stream);
+            if (bs <= 32) return launch<128, INTER, 1>(a, stream, nlaunch);
+            if (bs == 64) return launch<128, INTER, 2>(a, stream, nlaunch);
+            if (bs == 128) return launch<128, INTER, 4>(a, stream, nlaunch);
+            return launch<128, INTER, 8>(a, stream, nlaunch);
         }
     };
     *nlaunch = 1;

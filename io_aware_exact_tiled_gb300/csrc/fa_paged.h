@@ -17,6 +17,7 @@ enum : int { FA_DEV_NO_BLOCKS = 5 };
 constexpr int kPlanMaxB = 16384;      // requests of one plan (offsets of all of them sit in shared memory)
 constexpr int kPagedCtas = 152;       // one persistent CTA per SM
 constexpr int kPagedMaxRows = 32;     // tallest row tile of the split-key kernel
+constexpr float kPagedLag = 8.f;      // us that a row-tile CTA's start and end take longer than a split-key CTA's
 constexpr int kPagedTileRows = 256;   // query rows of a unit of the row-tile kernel
 
 struct PlanArgs {
@@ -195,11 +196,16 @@ __device__ __forceinline__ long long paged_tile_places(int len, int cap, int row
 __device__ __forceinline__ bool paged_leaves(const PagedJoin& j, int b) {
     return j.leaves && (j.first || paged_joins(j, b));
 }
-// CTAs of this pass where both run at once, each in proportion to its work.
+// CTAs of this pass where both run at once: n of the prefixes' and the rest of the
+// other such that kPagedLag + a / n = b / (kPagedCtas - n), a and b being the
+// prefixes' work and the other, in us of a CTA.
 __device__ __forceinline__ int paged_share(const PagedJoin& j, long long mine, long long other) {
-    const float a = j.place_us * static_cast<float>(mine), b = j.other_us * static_cast<float>(other);
     if (!j.other_len || mine == 0) return kPagedCtas;
-    return min(max(static_cast<int>(kPagedCtas * (a / (a + b)) + 0.5f), 1), kPagedCtas - 1);
+    const float x = j.place_us * static_cast<float>(mine), y = j.other_us * static_cast<float>(other);
+    const float a = j.first ? x : y, b = j.first ? y : x, c = a + b - kPagedLag * kPagedCtas;
+    const float n = (sqrtf(c * c + 4.f * kPagedLag * kPagedCtas * a) - c) / (2.f * kPagedLag);
+    const int pre = min(max(static_cast<int>(n + 0.5f), 1), kPagedCtas - 1);
+    return j.first ? pre : kPagedCtas - pre;
 }
 // Maximum and sum that the other pass left of a row.
 __device__ __forceinline__ float2 paged_left(const PagedJoin& j, size_t row) {
@@ -258,8 +264,8 @@ constexpr int paged_split_cost(int d) { return d == 64 ? 48 : 32; }
 // tiles; a chunk of 32 keys for 8, 16, .. rows (SHARE_FIG).
 inline void paged_run_both(PagedArgs& prefix, PagedArgs& own, float2* own_ml, float* own_o) {
     const int nt = own.split_rows / 8;
-    prefix.join.place_us = prefix.one_tile ? 1.4f : prefix.d == 64 ? 1.65f : 2.6f;
-    prefix.join.other_us = prefix.d == 64 ? 0.115f + 0.038f * (nt - 1) : 0.18f + 0.05f * (nt - 1);
+    prefix.join.place_us = prefix.d == 64 ? (prefix.one_tile ? 1.15f : 1.65f) : (prefix.one_tile ? 1.3f : 2.3f);
+    prefix.join.other_us = prefix.d == 64 ? 0.20f + 0.05f * (nt - 1) : 0.18f + 0.05f * (nt - 1);
     prefix.join.other_len = own.cache_len;
     prefix.join.other_cu = own.cu_seqlens;
     prefix.join.other_n = own.B;

@@ -165,8 +165,8 @@ cudaError_t launch_fwd_paged_prefix(const PagedArgs& prefix, const PagedArgs& ow
             if (e == cudaSuccess) e = launch_merge(prefix, PagedJoin{}, stream);
             ++*nlaunch;
         }
+        if (own_tiles) run(own, launch_paged_tile);  // first: the longer of the two
         run(own, launch_split<true>);
-        if (own_tiles) run(own, launch_paged_tile);
     }
     if (own.ev_end) cudaEventRecord(own.ev_end, stream);
     return e;

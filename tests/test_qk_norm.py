@@ -303,7 +303,7 @@ def test_append_equals_the_two_calls(cuda_device, which, bs, d, rot, Hq, Hkv, in
     theirs = [x.clone() for x in ours]
     out = torch.full((total, Hq, d), 7.0, dtype=torch.bfloat16, device=cuda_device)
     q_out = fa.qk_norm_rope_append(q, k, v, *ours, ids, **kw, q_out=out)
-    assert q_out is out and fa.last_launch_count() == 1
+    assert q_out is out and fa.last_launch_count() == (2 if total > 1024 else 1)
     qn, kn = fa.qk_norm_rope(q, k, **kw)
     fa.cache_append(kn, v.contiguous(), *theirs, ids)
     assert torch.equal(q_out[:-2], qn[:-2]) and (q_out[-2:] == 7).all()
