@@ -20,7 +20,7 @@ namespace fa {
 constexpr int kNaSeqs = 1024;  // offsets kept in shared memory
 
 template <int D, bool INTER, int L, int HPC>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 2)
     fa_norm_append_kernel(const __grid_constant__ NormAppendArgs args, int span, int hpc, int kv_ctas, int q_parts) {
     using LN = NormLane<D, INTER>;
     constexpr int ROWS = 256 / LN::TPR;  // rows of a CTA-wide load
@@ -128,9 +128,24 @@ __global__ void __launch_bounds__(256)
         // HPC heads at a time; a lane's angles stay in shared memory for the next ones
         const int row = tid / LN::TPR;
         constexpr bool KEEP = L <= 2;
-        ulonglong2* kept = reinterpret_cast<ulonglong2*>(ring) + tid;  // [L][4][256]
+        // rows of the heads to come, on their way; each lane reads what it copied
+        uint4* stage = ring + tid;  // [L][HPC][2][256]
+        ulonglong2* kept = reinterpret_cast<ulonglong2*>(ring + L * HPC * 512) + tid;  // [L][4][256]
         for (int k = 0; k < n; ++k) {
             const int lead = leads[k], end = run_end(lead), first = slot_of[lead] & (bs - 1);
+            auto request = [&](int i, int h1) {  // rows of set i, heads h1 ..
+                const int t = lead + i * ROWS + row;
+#pragma unroll
+                for (int h = 0; h < HPC; ++h) {
+                    if (t >= end || h1 + h >= h0 + nh) continue;
+                    const uint16_t* src = source(h1 + h, t);
+                    cp_async16(stage + ((i * HPC + h) * 2) * 256, src + ln.a);
+                    cp_async16(stage + ((i * HPC + h) * 2 + 1) * 256, src + ln.b);
+                }
+            };
+#pragma unroll
+            for (int i = 0; i < L; ++i) request(i, h0);
+            norm_commit();
             for (int h1 = h0; h1 < h0 + nh; h1 += HPC) {
                 const int mh = min(HPC, h0 + nh - h1);
                 NormRaw<uint16_t> raw[L][HPC];
@@ -141,27 +156,18 @@ __global__ void __launch_bounds__(256)
                     top[h] = 0;
                     old[h] = first > 0 && h < mh ? append_old_scale(scale_at(lead, h1 + h)) : 0.f;
                 }
+                norm_wait<0>();
 #pragma unroll
                 for (int i = 0; i < L; ++i) {
                     const int t = lead + i * ROWS + row;
 #pragma unroll
                     for (int h = 0; h < HPC; ++h) {
                         raw[i][h].zero();
-                        if (t < end && h < mh) raw[i][h].load(source(h1 + h, t), ln.a, ln.b);
+                        if (t < end && h < mh) {
+                            raw[i][h].w[0] = stage[((i * HPC + h) * 2) * 256];
+                            raw[i][h].w[1] = stage[((i * HPC + h) * 2 + 1) * 256];
+                        }
                     }
-                }
-                // the next heads' rows, into L2
-#pragma unroll
-                for (int i = 0; i < L; ++i) {
-                    const int t = lead + i * ROWS + row;
-#pragma unroll
-                    for (int h = 0; h < HPC; ++h)
-                        if (ln.j < D / 64 && t < end && h1 + HPC + h < h0 + nh)
-                            asm volatile("prefetch.global.L2 [%0];" ::"l"(source(h1 + HPC + h, t) + ln.j * 64));
-                }
-#pragma unroll
-                for (int i = 0; i < L; ++i) {
-                    const int t = lead + i * ROWS + row;
                     if (!is_v) {
                         NormTurn turn;
                         if (!KEEP || h1 == h0) {
@@ -184,7 +190,9 @@ __global__ void __launch_bounds__(256)
                     }
 #pragma unroll
                     for (int h = 0; h < HPC; ++h) top[h] = append_amax(raw[i][h].w, top[h]);
+                    request(i, h1 + HPC);  // into the place of the rows just taken
                 }
+                norm_commit();
 #pragma unroll
                 for (int h = 0; h < HPC; ++h) {
                     top[h] = __reduce_max_sync(0xffffffffu, top[h]);
@@ -217,6 +225,7 @@ __global__ void __launch_bounds__(256)
                 }
             }
         }
+        norm_wait<0>();
         return;
     }
     // ---------------------------------------------------- a warp for each run and head
@@ -258,7 +267,9 @@ static cudaError_t launch(const NormAppendArgs& a, cudaStream_t stream, int* nla
     const int total = a.a.total, passes = (a.n.Hq * (D / 16) + 31) / 32;
     const int span = total > 8192 && a.a.block_size * D <= 2048 ? 128 : total > 1024 ? 64 : 16;
     const bool big = total > 1024;
-    const int hpc = big ? 2 * HPC : 1;
+    const int hpc = big ? 4 * HPC : 1;
+    constexpr int kStage = L * HPC * 8192 + (L <= 2 ? L * 16384 : 0);
+    constexpr int kSmem = kStage > kNormRing<uint16_t> ? kStage : kNormRing<uint16_t>;
     const unsigned kv = static_cast<unsigned>((total + span - 1) / span) * 2u * ((a.a.H + hpc - 1) / hpc);
     int parts = (152 * 16 + total - 1) / total;
     parts = parts > passes ? passes : parts;
@@ -267,7 +278,7 @@ static cudaError_t launch(const NormAppendArgs& a, cudaStream_t stream, int* nla
     static std::atomic<uint64_t> done{0};
     cudaError_t e = once_per_device(done, [] {
         return cudaFuncSetAttribute(fa_norm_append_kernel<D, INTER, L, HPC>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kNormRing<uint16_t>);
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     });
     if (e == cudaSuccess && big) {  // the queries in a kernel with room for more of them on an SM (APPEND_FIG)
         int n;
@@ -277,7 +288,7 @@ static cudaError_t launch(const NormAppendArgs& a, cudaStream_t stream, int* nla
     }
     if (e != cudaSuccess) return e;
     fa_norm_append_kernel<D, INTER, L, HPC>
-        <<<kv + qc, 256, kNormRing<uint16_t>, stream>>>(a, span, hpc, static_cast<int>(kv), parts);
+        <<<kv + qc, 256, kSmem, stream>>>(a, span, hpc, static_cast<int>(kv), parts);
     return cudaGetLastError();
 }
 
