@@ -28,34 +28,41 @@ def _like(t, shape, dtype, device, name):
 
 
 def _norm_sizes(q, k, inv_freq, q_weight, k_weight, cu_seqlens, ends):
-    """Checks what the norm calls share; returns (B, N, Hq, Hkv, d, rot, type,
-    shapes of q and k, dtype, device)."""
+    """Checks what the norm calls share (in few steps: a decoding call's host
+    time is these); returns (B, N, Hq, Hkv, d, rot, type, shapes of q and k,
+    dtype, device)."""
     _b._check_device(q)
-    packed = cu_seqlens is not None
     qs, ks, dtype, dev = q.shape, k.shape, q.dtype, q.device
-    if len(qs) != (3 if packed else 4) or len(ks) != len(qs):
-        raise ValueError("expected q, k [B, H, N, d], or [total, H, d] with cu_seqlens")
-    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+    if cu_seqlens is not None:
+        if len(qs) != 3 or len(ks) != 3:
+            raise ValueError("expected packed q, k [total, H, d] with cu_seqlens")
+        N, Hq, d = qs
+        B, Hkv, same = cu_seqlens.numel() - 1, ks[1], ks[0] == N and ks[2] == d
+        if B < 1:
+            raise ValueError("cu_seqlens must be [B + 1]")
+        _b._in(cu_seqlens, (B + 1,), torch.int32, dev, "cu_seqlens")
+    else:
+        if len(qs) != 4 or len(ks) != 4:
+            raise ValueError("expected q, k [B, H, N, d], or [total, H, d] with cu_seqlens")
+        B, Hq, N, d = qs
+        Hkv, same = ks[1], ks[0] == B and ks[2] == N and ks[3] == d
+    if dtype is torch.bfloat16:
+        code = _b.FA_BF16
+    elif dtype is torch.float32:
+        code = _b.FA_FP32
+    else:
         raise ValueError("dtype must be bfloat16 or float32")
-    d = qs[-1]
-    _like(q, qs, dtype, dev, "q")
-    _like(k, (qs[0], ks[1], *qs[2:]), dtype, dev, "k")
+    if not same or k.dtype is not dtype or k.device != dev or q.stride(-1) != 1 or k.stride(-1) != 1:
+        raise ValueError("q and k must share type, device and all sizes but the heads, which must be contiguous")
     half = inv_freq.numel()
     _b._in(inv_freq, (half,), torch.float64, dev, "inv_freq")
     if q_weight is not None:
         _b._in(q_weight, (d,), dtype, dev, "q_weight")
     if k_weight is not None:
         _b._in(k_weight, (d,), dtype, dev, "k_weight")
-    if packed:
-        B, N = cu_seqlens.numel() - 1, qs[0]
-        if B < 1:
-            raise ValueError("cu_seqlens must be [B + 1]")
-        _b._in(cu_seqlens, (B + 1,), torch.int32, dev, "cu_seqlens")
-    else:
-        B, N = qs[0], qs[2]
     if ends is not None:
         _b._in(ends, (B,), torch.int32, dev, "ends")
-    return B, N, qs[1], ks[1], d, 2 * half, _b.FA_BF16 if dtype is torch.bfloat16 else _b.FA_FP32, qs, ks, dtype, dev
+    return B, N, Hq, Hkv, d, 2 * half, code, qs, ks, dtype, dev
 
 
 def _out_like(t, shape, dtype, device, name, stream):
