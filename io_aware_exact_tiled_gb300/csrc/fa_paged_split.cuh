@@ -1152,8 +1152,9 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
         mbar_wait_teardown(&bars[u % C::STAGES], (u / C::STAGES) & 1, 200000000ull);
 }
 
+// (of internal linkage: what is done once for each device is done for each library)
 template <int D, int NT, bool B16, bool PFX>
-cudaError_t launch_split(const PagedArgs& a, const PagedParams& p, cudaStream_t stream) {
+static cudaError_t launch_split(const PagedArgs& a, const PagedParams& p, cudaStream_t stream) {
     using C = PgCfg<D, NT, B16>;
     const uint64_t rows = static_cast<uint64_t>(a.num_blocks) * a.Hkv * a.block_size * D / 128;
     const uint32_t box = C::BOX / 128;
@@ -1173,7 +1174,7 @@ cudaError_t launch_split(const PagedArgs& a, const PagedParams& p, cudaStream_t 
 }
 
 template <int D, bool PFX>
-cudaError_t launch_split_d(const PagedArgs& a, const PagedParams& p, cudaStream_t stream) {
+static cudaError_t launch_split_d(const PagedArgs& a, const PagedParams& p, cudaStream_t stream) {
     const bool b16 = a.block_size == 16;
     const int rows = p.split_rows;
     if (rows <= 8) return b16 ? launch_split<D, 1, true, PFX>(a, p, stream) : launch_split<D, 1, false, PFX>(a, p, stream);
@@ -1217,7 +1218,7 @@ inline PagedParams paged_params(const PagedArgs& a) {
 }
 
 template <bool PFX>
-cudaError_t launch_split(const PagedArgs& a, cudaStream_t stream) {
+static cudaError_t launch_split(const PagedArgs& a, cudaStream_t stream) {
     const PagedParams p = paged_params(a);
     return a.d == 64 ? launch_split_d<64, PFX>(a, p, stream) : launch_split_d<128, PFX>(a, p, stream);
 }
