@@ -7,11 +7,20 @@
 //   u = R(s)^T dz,  xh = x r,  r = 1 / sqrt(mean(x^2) + eps),
 //   dw = sum of u xh over all rows,   dx = r (u w - xh mean(u w xh)).
 //
-// Bound: the heads' bytes, once in and once out.
+// Bound: the heads' bytes, once in and once out. Measured, [2, 16 + 16, 16384,
+// 128] bf16: forward 98 us = 5,480 GB/s (81 % of a copy's rate; 70 % of the issue
+// slots are used), gradient 139 + 4 us = 5,800 GB/s; one token of 16 requests, 32
+// + 8 heads: 6.4 us in a graph, of which a launch alone takes 2.
 //
 // A warp takes one token at a time: four (d = 128) or eight heads in a step,
 // sixteen elements a lane, so that the token's angles are computed once for all
-// its heads.
+// its heads. What has to be hidden is the latency of HBM: each lane's pieces come
+// through a ring of asynchronous copies, five steps ahead (loaded a step ahead
+// into registers: 135 us forward, 224 gradient). Arithmetic is in fp32 pairs.
+// Pointers kept from step to step instead of formed anew cost registers: 112 us
+// with four CTAs on an SM, 99 with three and eight stages. The gradient
+// takes q and then k, so that one set of sixteen sums for the weights stays in
+// registers; CTAs leave their sums to a second kernel, which adds them in order.
 #include <type_traits>
 
 #include "fa_norm.cuh"

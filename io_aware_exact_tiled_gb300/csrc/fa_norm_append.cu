@@ -4,12 +4,19 @@
 //
 // Bound: the tokens' bytes in large batches, latency in small ones.
 //
-// One launch. The first CTAs take the runs (consecutive tokens whose slots lie in
-// one block) that start among `span` tokens, for one group of heads and one of K
-// and V; the others take the queries. One or two runs, as in a prompt, are each
-// the whole CTA's: rows stay in registers from the load to their rounding, which
-// waits for the run's largest value. More runs, as in a decoding batch, go to a
-// warp each, which reads its rows twice.
+// The first CTAs take the runs (consecutive tokens whose slots lie in one block)
+// that start among `span` tokens, for a group of heads and one of K and V; the
+// others take the queries (in large batches the kernel of fa_norm.cu does). One or
+// two runs, as in a prompt, are each the whole CTA's: rows come by asynchronous
+// copies, HPC heads ahead, and stay in registers from their norm to their
+// rounding, which waits for the run's largest value. More runs, as in a decoding
+// batch, go to a warp each, which reads its rows twice.
+//
+// Measured: 128 requests of a token, 32 + 8 heads, 9 us; four prompts of 17,400
+// tokens, 32 heads each, d = 128, blocks of 64: 220 us (874 MB: 129 at the copy
+// rate), 62 of them the queries' kernel and 158 this one, whose sixteen warps on
+// an SM issue in 48 % of the cycles. One head a CTA with its rows loaded directly
+// took 290 us in all, four heads 232, with copies ahead and angles kept 220.
 #include <type_traits>
 
 #include "fa_append.cuh"
@@ -280,7 +287,7 @@ static cudaError_t launch(const NormAppendArgs& a, cudaStream_t stream, int* nla
         return cudaFuncSetAttribute(fa_norm_append_kernel<D, INTER, L, HPC>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     });
-    if (e == cudaSuccess && big) {  // the queries in a kernel with room for more of them on an SM (APPEND_FIG)
+    if (e == cudaSuccess && big) {  // the queries in a kernel of their own, with more warps on an SM
         int n;
         e = launch_norm(a.n, stream, &n);
         qc = 0;

@@ -207,6 +207,13 @@ __device__ __forceinline__ int paged_share(const PagedJoin& j, long long mine, l
     const int pre = min(max(static_cast<int>(n + 0.5f), 1), kPagedCtas - 1);
     return j.first ? pre : kPagedCtas - pre;
 }
+// What a pass leaves of a row: its maximum and minus its sum, a NaN's sign set too
+// (by an instruction that is no arithmetic: that would drop a NaN's sign).
+__device__ __forceinline__ float2 paged_leave(float m, float l) {
+    uint32_t y;
+    asm("or.b32 %0, %1, 0x80000000;" : "=r"(y) : "r"(__float_as_uint(l)));
+    return make_float2(m, __uint_as_float(y));
+}
 // Maximum and sum that the other pass left of a row.
 __device__ __forceinline__ float2 paged_left(const PagedJoin& j, size_t row) {
     const float2 b = __ldcg(&j.ml[row]);
@@ -261,7 +268,8 @@ constexpr int paged_split_cost(int d) { return d == 64 ? 48 : 32; }
 
 // Sets up both passes of a call with shared prefixes to run at once. Times of a
 // place on either line of work, in us: a tile of 128 keys for one or for two row
-// tiles; a chunk of 32 keys for 8, 16, .. rows (SHARE_FIG).
+// tiles; a chunk of 32 keys for 8, 16, .. rows (64 requests behind 32,768 tokens 121
+// us, 143 with one pass after the other; a serving step of 32 behind 4,096: 52 and 62).
 inline void paged_run_both(PagedArgs& prefix, PagedArgs& own, float2* own_ml, float* own_o) {
     const int nt = own.split_rows / 8;
     prefix.join.place_us = prefix.d == 64 ? (prefix.one_tile ? 1.15f : 1.65f) : (prefix.one_tile ? 1.3f : 2.3f);

@@ -1,11 +1,24 @@
 // Attention over the paged 8-bit cache for a batch whose requests share prefixes.
 //
-// Two passes of the kernels of fa_paged_split.cuh and fa_paged_tile.cu. In the
-// first, a group of requests is one request whose new tokens are all of theirs
-// and whose keys are the prefix, so that a prefix is read once for all rows that
-// share it; it leaves each row's maximum and sum and its output, normalised, in
-// fp32. The second is each request over its own tokens, and joins the two. The
-// kernels are chained: one starts on the SMs that the one before leaves idle.
+// Two passes of the kernels of fa_paged_split.cuh and fa_paged_tile.cu. In one, a
+// group of requests is one request whose new tokens are all of theirs and whose
+// keys are the prefix, so that a prefix is read once for all rows that share it;
+// it leaves each row's maximum and sum and its output, normalised, in fp32. The
+// other is each request over its own tokens. Softmax over both sets of keys is
+// then their sum with weights from maxima and sums (paged_weights).
+//
+// The kernels are chained: one starts on the SMs that the one before leaves idle.
+// Where the prefixes are the row-tile kernel's and the own tokens the split-key
+// kernel's (decoding), both work at once on parts of the GPU that the lengths set
+// (paged_share), and a merge joins them. Elsewhere the prefixes' pass comes
+// first and the other one joins what it left as it writes its rows.
+//
+// Bound: the cache's bytes, each prefix once; with many rows the products, in fact
+// the softmax. Measured (d = 128, 32 + 8 heads): 64 requests behind 32,768 tokens
+// with 2,066 of their own on average 121 us (339 MB: 50); 16 behind 262,001 171 us
+// (544 MB: 80; the softmax warps, below); 4 of 30 tokens behind 1,000 27 us, a chain
+// of latencies: scan 5, first chunk 4, merge of the warps 3, own pass and joining
+// 8. d = 64, eight prompts of 9,322 tokens behind 8,192: 584 us.
 #include <math_constants.h>
 
 #include "fa_paged_split.cuh"
@@ -14,10 +27,10 @@ namespace fa {
 
 // Pieces of the prefixes' units that the row-tile kernel cut between CTAs. One
 // long prefix has few units with a piece in every other CTA, so this takes all
-// SMs (where whoever finished last merged, prefixes of 32,768 tokens and 256 rows
-// took MERGE_FIG us longer): a CTA has 128 rows and 8 or 16 of their columns.
-// (a lane of the row tile for a thread) and 8 of their columns, in four groups
-// that take every fourth piece each.
+// SMs: a CTA has 128 rows (a lane of the row tile for a thread) and 8 of their
+// columns, in four groups that take every fourth piece each. (256 rows behind
+// 32,768 tokens: 6 us; merged by whoever finished last 27, by two groups of
+// columns that take all pieces 16.)
 constexpr int kMergeCtas = 2 * kPagedCtas, kMergeGroups = 4, kMergeThreads = 128 * kMergeGroups;
 
 template <int D>
@@ -114,7 +127,7 @@ __global__ void __launch_bounds__(kMergeThreads)
             if (own.ml) {
                 finish(orow, cut.tok0 + tok, cut.hk * G + row - tok * G, make_float2(M, L), c0 + g, sum);
             } else {
-                if (c0 + g == 0) a.join.ml[orow] = make_float2(M, -L);
+                if (c0 + g == 0) a.join.ml[orow] = paged_leave(M, L);
                 reinterpret_cast<float4*>(a.join.o + orow * D)[c0 + g] = sum;
             }
         }

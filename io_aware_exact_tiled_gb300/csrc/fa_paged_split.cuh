@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
     __shared__ long long start_line;
     __shared__ int nan_seen, abort_s;
     __shared__ float row_before[PFX ? RT : 1];
-    __shared__ int nmax_s, most_s, scan_u[C::W];
+    __shared__ int most_s, scan_u[C::W];
     __shared__ long long scan_o[2][PFX ? C::W : 1];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     if constexpr (PFX) paged_let_next();
@@ -230,7 +230,6 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
     if (tid == 0) {
         abort_s = 0;
         nan_seen = 0;
-        nmax_s = 0;
         most_s = 0;
     }
     if (lane < C::STAGES) mbar_init(&bars[lane], 1);
@@ -294,14 +293,13 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
     auto line_long = [&](const PgSeg& s) { return s.nchunk > T ? static_cast<long long>(p.Hkv) * places(s) : 0ll; };
     auto line_short = [&](const PgSeg& s) { return s.nchunk <= T ? static_cast<long long>(p.Hkv) * s.nchunk : 0ll; };
     long long ml_ = 0, ms = 0, ma = 0;  // long, short, all as long ones
-    [[maybe_unused]] int nmax = 0, most = 0, mu = 0;  // the longest of the short ones and of all; units
+    [[maybe_unused]] int most = 0, mu = 0;  // PFX: chunks of the longest; units
     for (int b = b0; b < b1; ++b) {
         PgSeg s;
         pg_request<PFX>(p, b, s);
         ml_ += line_long(s);
         ms += line_short(s);
         if (s.nchunk > 0) ma += static_cast<long long>(p.Hkv) * (s.nchunk + C::COST);
-        if (PFX && s.nchunk <= T) nmax = max(nmax, s.nchunk);
         if (PFX && s.nchunk > 0) {
             mu += p.Hkv;
             most = max(most, s.nchunk);
@@ -309,12 +307,8 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
     }
     [[maybe_unused]] int iu = mu;
     if constexpr (PFX) {
-        nmax = __reduce_max_sync(0xffffffffu, nmax);
         most = __reduce_max_sync(0xffffffffu, most);
-        if (lane == 0) {
-            atomicMax(&nmax_s, nmax);
-            atomicMax(&most_s, most);
-        }
+        if (lane == 0) atomicMax(&most_s, most);
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int a = __shfl_up_sync(0xffffffffu, iu, off);
@@ -354,7 +348,6 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
     }
     [[maybe_unused]] int U = 0, bu = iu - mu;
     if constexpr (PFX) {
-        nmax = nmax_s;
         most = most_s;
         for (int w = 0; w < C::W; ++w) {
             if (w < warp) bu += scan_u[w];
@@ -364,17 +357,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
     // A few short units among long ones would only come after everything else:
     // they are taken as long ones (64 requests of 1 to 16,384 tokens: 192 us, 232
     // with a warp each for the short ones).
-    bool all_long = Ws * 8 < W;
-    if constexpr (PFX) {
-        // A request's own tokens are few beside a prefix, and its keys wait one
-        // after the other in a lone warp: all units are long ones too where the
-        // line of all then ends first (in chunks' time; a unit's own length
-        // included; 16 requests of up to 512 tokens, 8 heads of keys: PFX_FIG).
-        const long long lone = (Wl / ctas) / C::W + max(Ws / (ctas * C::W), static_cast<long long>(nmax)) + 2;
-        const long long together = max(Wa / ctas, static_cast<long long>(nmax) + C::COST) / C::W;
-        all_long |= together < lone;
-    }
-    if (all_long) {
+    if (Ws * 8 < W) {
         T = 0;
         Wl = Wa;
         Ws = 0;
@@ -384,7 +367,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
     }
     if constexpr (PFX) {
         // Few and short enough, each unit is a CTA's: that costs less than the merge
-        // of a unit that was cut (four requests behind 1,000 tokens: SOLO_FIG).
+        // of a unit that was cut (four requests behind 1,000 tokens: 28.2 us a call, 26.8 so).
         if (U <= ctas && most <= kPgSolo) {
             T = 0;
             solo = most + C::COST;
@@ -903,7 +886,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
                                 }
                                 *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(a, b);
                             }
-                            if (g == 0) p.join.ml[orow] = make_float2(m[nt][e], -l[nt][e]);
+                            if (g == 0) p.join.ml[orow] = paged_leave(m[nt][e], l[nt][e]);
                             continue;
                         }
                         if (!p.join.leaves && paged_joins(p.join, cs.b)) {
@@ -977,7 +960,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT, B16>::THREADS, 1)
             const size_t orow = static_cast<size_t>(cs.tok0 + tok) * p.Hq + hq;
             float own = L == 0.f ? 0.f : 1.f / L, before = -1.f, lse = lse_of(M, L);
             if (paged_leaves(p.join, cs.b)) {
-                p.join.ml[orow] = make_float2(M, -L);
+                p.join.ml[orow] = paged_leave(M, L);
             } else {
                 if (!p.join.leaves && paged_joins(p.join, cs.b)) {
                     const PagedWeights w = paged_weights(M, L, paged_left(p.join, orow));

@@ -331,13 +331,17 @@ __device__ __forceinline__ void pt_request(const PtParams& p, int b, PtReq& r) {
 // ONE (a prefix's rows, which see all its keys): a unit is one row tile, and the
 // two softmax groups and product warps, "row tiles" i below, take every other of
 // its key tiles: with few rows the time is the chain of S, softmax and P V, and
-// two chains hide one another (PT_FIG).
+// two chains hide one another (64 rows behind 262,001 tokens, d = 128: 228 us a
+// call with units of two row tiles, 171 so; six groups of 32 to 172 rows, d = 64:
+// 83 and 79). What bounds it is the softmax warps' chain: a half tile takes one
+// 1,980 cycles, with 38 % of the issue slots used.
 template <int D, bool PFX, bool ONE>
 __global__ void __launch_bounds__(512, 1)
     fa_paged_tile_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                          const __grid_constant__ PtParams p) {
     using C = PtCfg<D, ONE>;
-    constexpr int RT = ONE ? 128 : 256, STEP = ONE ? 2 : 1;  // rows of a unit; key tiles from one of a row tile's to the next
+    // rows of a unit; from one key tile of a row tile to its next
+    constexpr int RT = ONE ? 128 : 256, STEP = ONE ? 2 : 1;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ long long scan_w[16], scan_u[16], scan_o[PFX ? 16 : 1];
@@ -356,6 +360,13 @@ __global__ void __launch_bounds__(512, 1)
         pt_request<D, PFX, RT>(p, b, r);
         mu += static_cast<long long>(r.npair) * p.Hkv;
         mw += r.tiles * p.Hkv;
+        if constexpr (PFX) {
+            if (p.join.first && blockIdx.x == 0) {  // the prefixes' pass has no other kernel that would report these
+                int i0 = b, i1 = b + 1;
+                const bool good = paged_members(p.join, i0, i1) && p.cache_len[b] == r.len;
+                if (!good) atomicCAS(p.status, 0, FA_DEV_INVALID | (100 << 8));
+            }
+        }
     }
     long long iw = mw, iu = mu;
 #pragma unroll
@@ -554,7 +565,8 @@ __global__ void __launch_bounds__(512, 1)
             // copies of a lane for each group of 16 keys. One warp requests the
             // copies and another sees to the scales: together they took a warp
             // 2,370 cycles a tile, which is what a prefix of few rows then took
-            // (LOAD_FIG). With two row tiles a tile takes longer than that.
+            // (64 rows behind 262,001 tokens: the kernel 190 us, 168 so). With two row
+            // tiles a tile takes longer than that.
             const int bs = 1 << p.bs_log2, box = min(bs, 128);
             int* ahead = reinterpret_cast<int*>(sm + C::AHEAD_OFF) + (warp == 0 ? 0 : 8 * kPtAhead);
             auto has = [&](int t) { return lane < 8 && t < s.c1 && t * 128 + lane * 16 < s.r.len; };
@@ -1025,7 +1037,7 @@ __global__ void __launch_bounds__(512, 1)
             auto row_weights = [&](float M, float L, float& own) {
                 lse_all = L == 0.f ? -CUDART_INF_F : (M - kPtOffset + log2f(L)) * kPtLn2;
                 if (p.join.leaves) {
-                    if (row_ok) p.join.ml[orow] = make_float2(M, -L);
+                    if (row_ok) p.join.ml[orow] = paged_leave(M, L);
                 } else if (row_ok && paged_joins(p.join, s.r.b)) {
                     const PagedWeights w = paged_weights(M, L, paged_left(p.join, orow));
                     own = w.own;

@@ -133,15 +133,19 @@ def test_scores_of_very_different_parts(cuda_device, d):
 
 
 @pytest.mark.parametrize("d", [64, 128])
-def test_nan_and_infinite_values(cuda_device, d):
-    """A NaN of the prefix reaches all rows of its group and no other; a query
-    with an infinity has no finite row."""
-    b = Batch([(40, 1), (60, 2), (9, 1)], [(0, 90), (2, 50)], 16, 1, 4, d, cuda_device, pad=0)
+@pytest.mark.parametrize("more,new", [(0, 1), (9, 1), (30, 1), (70, 1), (2, 150)])
+def test_nan_and_infinite_values(cuda_device, more, new, d):
+    """A NaN of the prefix reaches all rows of its group and no other, one of a
+    request's own tokens that request's; a query with an infinity has no finite
+    row. With rows for every kernel and way of joining."""
+    b = Batch([(40, 1), (60, 2), (9, 1)] + [(20, new)] * more, [(0, 90), (2, 50)], 16, 1, 4, d, cuda_device, pad=0)
     b.c[1][b.ptable[0, 5], 0, 9, 3] = 127              # token 89, the prefix's last
+    b.c[1][b.table[2, 0], 0, 9, 7] = 127               # the third request's last
     b.q[3, 1, 0] = float("inf")
     o, lse = b.run()
     nan = o.isnan()
-    assert nan[:3, :, 3].all() and nan[3, 1].all() and int(nan.sum()) == 12 + d
+    assert nan[:3, :, 3].all() and nan[3, :, 7].all() and nan[3, 1].all()
+    assert int(nan.sum()) == 12 + 3 + d
     assert lse[1, 3].isnan() and int(lse.isnan().sum()) == 1
 
 
@@ -165,21 +169,27 @@ def test_the_same_bits_each_time(cuda_device, which, d):
         assert torch.equal(o, p) and torch.equal(lse, pl)
 
 
-def test_offsets_and_lengths_out_of_range_are_reported(cuda_device):
+@pytest.mark.parametrize("more", [0, 40])
+def test_offsets_and_lengths_out_of_range_are_reported(cuda_device, more):
+    """In the split-key kernel's prefixes and in the row-tile kernel's."""
     bad = fb.FA_ERR_INVALID_ARG
-    for i, value in ((7, [0, 9, 3]), (7, [0, 2, 1]), (7, [-1, 1, 3]), (8, [1 << 20, 5]), (8, [-3, 5])):
-        b = Batch([(40, 1), (60, 2), (9, 1)], [(0, 90), (2, 50)], 16, 1, 4, 64, cuda_device)
-        t = b.tensors()
+
+    def batch():
+        b = Batch([(40, 1), (60, 2), (9, 1)] + [(5, 1)] * more, [(0, 90), (2, 50)], 16, 1, 4, 64, cuda_device)
+        return b, b.tensors()
+
+    n = 3 + more
+    for i, value in ((7, [0, n + 9, n]), (7, [0, 2, 1]), (7, [-1, 1, n]), (8, [1 << 20, 5]), (8, [-3, 5])):
+        b, t = batch()
         t[i] = dev_i32(value, cuda_device)
         b.run(args=t, status=bad)
     for i, at in ((9, (0, 2)), (6, (1, 1))):          # table entries that are no block
         for value in (-1, 1 << 28):
-            b = Batch([(40, 1), (60, 2), (9, 1)], [(0, 90), (2, 50)], 16, 1, 4, 64, cuda_device)
-            t = b.tensors()
+            b, t = batch()
             t[i][at] = value
             b.run(args=t, status=bad)
     # behind the lengths anything may stand
-    b = Batch([(40, 1), (60, 2), (9, 1)], [(0, 90), (2, 50)], 16, 1, 4, 64, cuda_device)
+    b, _ = batch()
     b.ptable[1, 4:] = 1 << 28
     b.check()
 
