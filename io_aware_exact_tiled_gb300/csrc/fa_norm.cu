@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) fa_norm_bwd_kernel(const __gr
                     more = in.open(p, items, parts, np);
                 }
             }
-            norm_commit();
+            cp_async_commit();
             next = next + 1 == S ? 0 : next + 1;
         };
 #pragma unroll 1
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) fa_norm_bwd_kernel(const __gr
             NormTurn turn;
             warp_turn<D, INTER>(ln, f, pos, turn);
             for (; at.pass < at.end; ++at.pass) {
-                norm_wait<S - 2>();
+                cp_async_wait<S - 2>();
                 const bool mine = there && at.pass * L::RPW + ln.g < H;
                 NormRaw<T> raw;
                 NormVec u, x;
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) fa_norm_bwd_kernel(const __gr
                 if (mine) raw.store(row(rd, at), ln.a, ln.b);
             }
         }
-        norm_wait<0>();
+        cp_async_wait<0>();
         if (!has_w) continue;
         // this CTA's sums, in a fixed order
         float a[16];

@@ -280,11 +280,6 @@ __device__ __forceinline__ void norm_row(NormVec& x, const float* w, const NormL
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
-__device__ __forceinline__ void norm_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>  // all but the newest N groups of this thread have landed
-__device__ __forceinline__ void norm_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 // Where a warp stands among its items: steps [pass, end) of token (b, n).
 struct NormCursor {
@@ -369,7 +364,7 @@ __device__ __forceinline__ void norm_forward(const NormArgs& p, const uint64_t* 
                 more = in.open(p, items, parts, np);
             }
         }
-        norm_commit();
+        cp_async_commit();
         next = next + 1 == S ? 0 : next + 1;
     };
 #pragma unroll 1
@@ -380,7 +375,7 @@ __device__ __forceinline__ void norm_forward(const NormArgs& p, const uint64_t* 
         NormTurn turn;
         warp_turn<D, INTER>(ln, f, pos, turn);
         for (; at.pass < at.end; ++at.pass) {
-            norm_wait<S - 2>();
+            cp_async_wait<S - 2>();
             NormRaw<T> raw;
 #pragma unroll
             for (int i = 0; i < PIECES; ++i) raw.w[i] = ring[(slot * PIECES + i) * 32];
@@ -394,7 +389,7 @@ __device__ __forceinline__ void norm_forward(const NormArgs& p, const uint64_t* 
             if (row(p.q_out, p.k_out, at, dst) && there) raw.store(dst, ln.a, ln.b);
         }
     }
-    norm_wait<0>();
+    cp_async_wait<0>();
 }
 
 // Fractions of a turn and the weights in fp32, into shared memory. The caller synchronises.

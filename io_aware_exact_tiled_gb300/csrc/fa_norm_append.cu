@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(256, 2)
             };
 #pragma unroll
             for (int i = 0; i < L; ++i) request(i, h0);
-            norm_commit();
+            cp_async_commit();
             for (int h1 = h0; h1 < h0 + nh; h1 += HPC) {
                 const int mh = min(HPC, h0 + nh - h1);
                 NormRaw<uint16_t> raw[L][HPC];
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(256, 2)
                     top[h] = 0;
                     old[h] = first > 0 && h < mh ? append_old_scale(scale_at(lead, h1 + h)) : 0.f;
                 }
-                norm_wait<0>();
+                cp_async_wait<0>();
 #pragma unroll
                 for (int i = 0; i < L; ++i) {
                     const int t = lead + i * ROWS + row;
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(256, 2)
                     for (int h = 0; h < HPC; ++h) top[h] = append_amax(raw[i][h].w, top[h]);
                     request(i, h1 + HPC);  // into the place of the rows just taken
                 }
-                norm_commit();
+                cp_async_commit();
 #pragma unroll
                 for (int h = 0; h < HPC; ++h) {
                     top[h] = __reduce_max_sync(0xffffffffu, top[h]);
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(256, 2)
                 }
             }
         }
-        norm_wait<0>();
+        cp_async_wait<0>();
         return;
     }
     // ---------------------------------------------------- a warp for each run and head

@@ -168,6 +168,18 @@ __device__ __forceinline__ long long div_short(long long x, long long d) {
 __device__ __forceinline__ void paged_let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void paged_wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Asynchronous copy of four bytes to shared memory, in groups.
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>  // all but the newest N groups of this thread have landed
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 // Two E4M3 numbers (low 16 bits) to an f16 pair, exactly.
 __device__ __forceinline__ uint32_t f16x2_from_e4m3x2(uint32_t x) {
     uint32_t r;

@@ -18,7 +18,7 @@
 // with 2,066 of their own on average 121 us (339 MB: 50); 16 behind 262,001 171 us
 // (544 MB: 80; the softmax warps, below); 4 of 30 tokens behind 1,000 27 us, a chain
 // of latencies: scan 5, first chunk 4, merge of the warps 3, own pass and joining
-// 8. d = 64, eight prompts of 9,322 tokens behind 8,192: 584 us.
+// 8. d = 64, eight prompts of 9,322 tokens together behind 8,192: 559 us.
 #include <math_constants.h>
 
 #include "fa_paged_split.cuh"
@@ -174,7 +174,7 @@ cudaError_t launch_fwd_paged_prefix(const PagedArgs& prefix, const PagedArgs& ow
         if (e == cudaSuccess) e = launch_merge(prefix, own.join, stream);
         ++*nlaunch;
     } else {
-        if (pre_tiles) {
+        if (pre_tiles && prefix.join.cuts) {
             if (e == cudaSuccess) e = launch_merge(prefix, PagedJoin{}, stream);
             ++*nlaunch;
         }

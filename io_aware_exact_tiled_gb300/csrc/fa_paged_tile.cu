@@ -1182,7 +1182,7 @@ __global__ void __launch_bounds__(512, 1)
                     }
                 }
                 if constexpr (PFX) {
-                    if (p.join.leaves) {  // merged by a kernel of its own, over the whole GPU
+                    if (p.join.cuts) {  // merged by a kernel of its own, over the whole GPU
                         if (r == 0 && i == 0 && s.c0 == 0)
                             p.join.cuts[slot] = {1, s.r.tok0, s.pair * RT, rows, s.hk, f, e, ONE ? (twice ? 4 : 2) : 1, s.line0, quota};
                         continue;
