@@ -783,67 +783,127 @@ __global__ void __launch_bounds__(512, 1)
             // The tiles [c0, c1) of a piece, of which row tile i takes part in
             // those up to `end`; one loop for each form of Q, so that neither
             // tests it between its products.
-            auto walk = [&](auto form, int c0, int c1, int end) {
-                constexpr bool kWide = decltype(form)::value;
-                const int first = ONE ? c0 + i : c0;
-                u += first - c0;
-                for (int t = first; t < c1 + STEP; t += STEP, u += STEP) {
-                    const int st = u % C::KS, vs = (u - STEP) % C::VS;
-                    const bool now = t < c1, before = t > first;  // a tile of K, and one of V, of this row tile's
-                    const uint64_t vd = sdesc_advance(dV, vs * C::V_BYTES), kd = sdesc_advance(dK, st * C::K_BYTES);
-                    if (now && !(ok = wait_warp(&k_full[st], (u / C::KS) & 1))) break;
-                    if (before && !(ok = wait_warp(&v_full[vs], ((u - STEP) / C::VS) & 1))) break;
+            // (ONE: every other tile; apart, as the steps of two cost the other units'
+            // loop 2 % at d = 64.)
+            if constexpr (ONE) {
+                auto walk = [&](auto form, int c0, int c1, int end) {
+                    constexpr bool kWide = decltype(form)::value;
+                    const int first = c0 + i;
+                    u += first - c0;
+                    for (int t = first; t < c1 + STEP; t += STEP, u += STEP) {
+                        const int st = u % C::KS, vs = (u - STEP) % C::VS;
+                        const bool now = t < c1, before = t > first;  // a tile of K, and one of V, of this row tile's
+                        const uint64_t vd = sdesc_advance(dV, vs * C::V_BYTES), kd = sdesc_advance(dK, st * C::K_BYTES);
+                        if (now && !(ok = wait_warp(&k_full[st], (u / C::KS) & 1))) break;
+                        if (before && !(ok = wait_warp(&v_full[vs], ((u - STEP) / C::VS) & 1))) break;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t tS = tm0 + C::COL_S + h * 64, tO = tm0 + C::COL_O;
-                        const uint32_t tP = tm0 + C::COL_P + h * C::P_STRIDE;
-                        if (before && t - STEP < end) {
-                            if (!(ok = wait_warp(&p_full[2 * i + h], np & 1))) break;
-                            tc_fence_after();
-                            const uint32_t more = !(t - STEP == first && h == 0);
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t tS = tm0 + C::COL_S + h * 64, tO = tm0 + C::COL_O;
+                            const uint32_t tP = tm0 + C::COL_P + h * C::P_STRIDE;
+                            if (before && t - STEP < end) {
+                                if (!(ok = wait_warp(&p_full[2 * i + h], np & 1))) break;
+                                tc_fence_after();
+                                const uint32_t more = !(t - STEP == first && h == 0);
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                umma_ts<false>(leader, tO, tP + kk * 8, sdesc_advance(vd, h * 8192 + kk * 2048),
-                                               C::ID_PV, kk > 0 ? 1u : more);
-                            umma_commit(leader, &pv_done[2 * i + h]);
+                                for (int kk = 0; kk < 4; ++kk)
+                                    umma_ts<false>(leader, tO, tP + kk * 8, sdesc_advance(vd, h * 8192 + kk * 2048),
+                                                   C::ID_PV, kk > 0 ? 1u : more);
+                                umma_commit(leader, &pv_done[2 * i + h]);
+                            }
+                            if (t < end) {
+                                // Only products with the same accumulator are bound to
+                                // the order of their issue: where S takes P's place,
+                                // P V has to be done.
+                                if (C::P_OVER_S && before && !(ok = wait_warp(&pv_done[2 * i + h], np & 1))) break;
+                                tc_fence_after();
+#pragma unroll
+                                for (int part = 0; part < (kWide ? 3 : 2); ++part)
+#pragma unroll
+                                    for (int kk = 0; kk < D / 32; ++kk)
+                                        umma_ss_f8(leader, tS, sdesc_advance(dQ, C::q_part(part) + kk * 32),
+                                                   sdesc_advance(kd, h * (C::K_BYTES / 2) + kk * 32),
+                                                   C::id_s(kWide || part == 0), part || kk ? 1u : 0u);
+                                umma_commit(leader, &s_full[2 * i + h]);
+                            }
                         }
-                        if (t < end) {
-                            // Only products with the same accumulator are bound to
-                            // the order of their issue: where S takes P's place,
-                            // P V has to be done.
-                            if (C::P_OVER_S && before && !(ok = wait_warp(&pv_done[2 * i + h], np & 1))) break;
-                            tc_fence_after();
-#pragma unroll
-                            for (int part = 0; part < (kWide ? 3 : 2); ++part)
-#pragma unroll
-                                for (int kk = 0; kk < D / 32; ++kk)
-                                    umma_ss_f8(leader, tS, sdesc_advance(dQ, C::q_part(part) + kk * 32),
-                                               sdesc_advance(kd, h * (C::K_BYTES / 2) + kk * 32),
-                                               C::id_s(kWide || part == 0), part || kk ? 1u : 0u);
-                            umma_commit(leader, &s_full[2 * i + h]);
-                        }
+                        if (!ok) break;
+                        // this row tile has read K of tile t and V of the one before
+                        if (now) umma_commit(leader, &k_empty[st]);
+                        if (before) umma_commit(leader, &v_empty[vs]);
+                        np += before && t - STEP < end;
                     }
+                };
+                int upos = 0;  // tiles of the pieces before
+                do {
+                    // warp-uniform in the compiler's eyes too, so that descriptors and
+                    // TMEM addresses stay in uniform registers
+                    const int c0 = uniform(s.c0), c1 = uniform(s.c1), end = uniform(half_end(s, i));
+                    const bool some = end > c0 + i;
+                    u = upos;
+                    if (some && !(ok = wait_warp(&q_full[i], nseg & 1))) break;
+                    if (some && uniform(wide_s[i])) walk(PtWide{}, c0, c1, end);
+                    else walk(PtNarrow{}, c0, c1, end);
                     if (!ok) break;
-                    // this row tile has read K of tile t and V of the one before
-                    if (now) umma_commit(leader, &k_empty[st]);
-                    if (before) umma_commit(leader, &v_empty[vs]);
-                    np += before && t - STEP < end;
-                }
-            };
-            int upos = 0;  // tiles of the pieces before
-            do {
-                // warp-uniform in the compiler's eyes too, so that descriptors and
-                // TMEM addresses stay in uniform registers
-                const int c0 = uniform(s.c0), c1 = uniform(s.c1), end = uniform(half_end(s, i));
-                const bool some = end > (ONE ? c0 + i : c0);
-                u = upos;
-                if (some && !(ok = wait_warp(&q_full[i], nseg & 1))) break;
-                if (some && uniform(wide_s[i])) walk(PtWide{}, c0, c1, end);
-                else walk(PtNarrow{}, c0, c1, end);
-                if (!ok) break;
-                nseg += some;
-                upos += c1 - c0;
-            } while (__any_sync(0xffffffffu, next(s)));
+                    nseg += some;
+                    upos += c1 - c0;
+                } while (__any_sync(0xffffffffu, next(s)));
+            } else {
+                auto walk = [&](auto form, int c0, int c1, int end) {
+                    constexpr bool kWide = decltype(form)::value;
+                    for (int t = c0; t <= c1; ++t, ++u) {
+                        const int st = u % C::KS, vs = (u - 1) % C::VS;
+                        const uint64_t vd = sdesc_advance(dV, vs * C::V_BYTES), kd = sdesc_advance(dK, st * C::K_BYTES);
+                        if (t < c1 && !(ok = wait_warp(&k_full[st], (u / C::KS) & 1))) break;
+                        if (t > c0 && !(ok = wait_warp(&v_full[vs], ((u - 1) / C::VS) & 1))) break;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t tS = tm0 + C::COL_S + h * 64, tO = tm0 + C::COL_O;
+                            const uint32_t tP = tm0 + C::COL_P + h * C::P_STRIDE;
+                            if (t > c0 && t <= end) {
+                                if (!(ok = wait_warp(&p_full[2 * i + h], np & 1))) break;
+                                tc_fence_after();
+                                const uint32_t more = !(t - 1 == c0 && h == 0);
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk)
+                                    umma_ts<false>(leader, tO, tP + kk * 8, sdesc_advance(vd, h * 8192 + kk * 2048),
+                                                   C::ID_PV, kk > 0 ? 1u : more);
+                                umma_commit(leader, &pv_done[2 * i + h]);
+                            }
+                            if (t < end) {
+                                // Only products with the same accumulator are bound to
+                                // the order of their issue: where S takes P's place,
+                                // P V has to be done.
+                                if (C::P_OVER_S && t > c0 && !(ok = wait_warp(&pv_done[2 * i + h], np & 1))) break;
+                                tc_fence_after();
+#pragma unroll
+                                for (int part = 0; part < (kWide ? 3 : 2); ++part)
+#pragma unroll
+                                    for (int kk = 0; kk < D / 32; ++kk)
+                                        umma_ss_f8(leader, tS, sdesc_advance(dQ, C::q_part(part) + kk * 32),
+                                                   sdesc_advance(kd, h * (C::K_BYTES / 2) + kk * 32),
+                                                   C::id_s(kWide || part == 0), part || kk ? 1u : 0u);
+                                umma_commit(leader, &s_full[2 * i + h]);
+                            }
+                        }
+                        if (!ok) break;
+                        // this row tile has read K of tile t and V of tile t - 1
+                        if (t < c1) umma_commit(leader, &k_empty[st]);
+                        if (t > c0) umma_commit(leader, &v_empty[vs]);
+                        np += t > c0 && t <= end;
+                    }
+                    --u;  // the last round had no tile of its own
+                };
+                do {
+                    // warp-uniform in the compiler's eyes too, so that descriptors and
+                    // TMEM addresses stay in uniform registers
+                    const int c0 = uniform(s.c0), c1 = uniform(s.c1), end = uniform(half_end(s, i));
+                    if (end > c0 && !(ok = wait_warp(&q_full[i], nseg & 1))) break;
+                    if (end > c0 && uniform(wide_s[i])) walk(PtWide{}, c0, c1, end);
+                    else walk(PtNarrow{}, c0, c1, end);
+                    if (!ok) break;
+                    nseg += end > c0;
+                } while (__any_sync(0xffffffffu, next(s)));
+            }
             if (!ok) pt_gave_up(&abort_s, p.status, 96);
             // every MMA issued so far must be complete before TMEM is released
             umma_commit(leader, &drain[i]);
@@ -1139,6 +1199,8 @@ __global__ void __launch_bounds__(512, 1)
                 const int e = static_cast<int>(div_short(s.line0 + s.ntile - 1, quota));
                 if constexpr (ONE) {
                     if (whole) {
+                        // the parts are read past L1: written that far before the barrier
+                        __threadfence();
                         named_sync(3, 256);
                         if (i == 0 && row_ok && !(twice && r >= 64)) {
                             const int n = twice ? 4 : 2;  // parts: row tile k & 1, lanes 64 (k >> 1) + r
