@@ -90,8 +90,8 @@ struct PtCfg {
     static constexpr int V_OFF = R_OFF + RS * K_BYTES;
     static constexpr int SC_OFF = V_OFF + VS * V_BYTES;       // float [slots][24]: ks, log2 vs, 1 / vs of 8 groups
     static constexpr int NAN_OFF = SC_OFF + kPtScaleSlots * 96;  // u64 [slots][D]: {tag, first key with a NaN value}
-    static constexpr int AHEAD_OFF = NAN_OFF + kPtNanSlots * D * 8;  // int ids [2][kPtAhead][8], float {ks, vs} [kPtAhead][8]
-    static constexpr int BAR_OFF = AHEAD_OFF + kPtAhead * 128;
+    static constexpr int AHEAD_OFF = NAN_OFF + kPtNanSlots * D * 8;  // ONE: int ids [2][kPtAhead][8], ..
+    static constexpr int BAR_OFF = AHEAD_OFF + (ONE ? kPtAhead * 128 : 0);  // .. float {ks, vs} [kPtAhead][8]
     static constexpr int USED = BAR_OFF + 512;
     static constexpr int SMEM = USED + 1024;
     // TMEM: S of row tile i and half h of the keys at 128 i + 64 h, O at 256 +
@@ -401,8 +401,8 @@ __global__ void __launch_bounds__(512, 1)
     uint64_t* nan_full = drain + 2;            // [4] a piece's V has been looked over
     uint64_t* nan_empty = nan_full + kPtNanSlots;  // [4] both row tiles' softmax warps are through with that piece
     uint64_t* sc_full = nan_empty + kPtNanSlots;   // [8] scales stored
-    uint64_t* asked = sc_full + kPtScaleSlots;   // [8] K of a tile requested
-    uint64_t* k_full = asked + kPtScaleSlots;    // [KS]
+    [[maybe_unused]] uint64_t* asked = sc_full + kPtScaleSlots;  // ONE: [8] K of a tile requested
+    uint64_t* k_full = sc_full + (ONE ? 2 : 1) * kPtScaleSlots;  // [KS]
     uint64_t* k_empty = k_full + C::KS;        // [KS] both row tiles' S done
     uint64_t* r_full = k_empty + C::KS;        // [RS] V landed
     uint64_t* r_empty = r_full + C::RS;        // [RS] V read
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(512, 1)
         }
         for (int i = 0; i < kPtScaleSlots; ++i) {
             mbar_init(&sc_full[i], 1);
-            mbar_init(&asked[i], 1);
+            if (ONE) mbar_init(&asked[i], 1);
         }
         for (int i = 0; i < C::KS; ++i) {
             mbar_init(&k_full[i], 1);
@@ -1137,7 +1137,7 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t ov[32];
-                if (end > s.c0) {
+                if (end > first) {
                     tmem_ld32(tO + c * 32, ov);
                     tmem_ld_wait(ov);
                 } else {
