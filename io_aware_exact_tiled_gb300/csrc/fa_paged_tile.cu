@@ -783,8 +783,7 @@ __global__ void __launch_bounds__(512, 1)
             // The tiles [c0, c1) of a piece, of which row tile i takes part in
             // those up to `end`; one loop for each form of Q, so that neither
             // tests it between its products.
-            // (ONE: every other tile; apart, as the steps of two cost the other units'
-            // loop 2 % at d = 64.)
+            // (ONE: every other tile.)
             if constexpr (ONE) {
                 auto walk = [&](auto form, int c0, int c1, int end) {
                     constexpr bool kWide = decltype(form)::value;

@@ -149,6 +149,18 @@ def test_nan_and_infinite_values(cuda_device, more, new, d):
     assert lse[1, 3].isnan() and int(lse.isnan().sum()) == 1
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_prefix_of_one_tile_behind_a_call_of_nans(cuda_device, d):
+    """What another call left in tensor memory has no influence: a prefix of one
+    key tile gives the second of a unit's two streams of keys nothing to do."""
+    wild = Batch([(20, 1)] * 40, [(0, 30000)], 64, 4, 4, d, cuda_device, pad=0)
+    wild.q.fill_(float("inf"))
+    b = Batch([(9, 1)] * 20, [(0, 100)], 64, 8, 4, d, cuda_device)
+    assert wild.run()[0].isnan().all()
+    o, lse = b.run()
+    b.check(got=(o, lse))
+
+
 def test_no_prefix_is_forward_paged(cuda_device):
     """Groups without tokens: what forward_paged computes, whose work may be cut
     elsewhere, so that sums run in another order: both within the bounds."""
