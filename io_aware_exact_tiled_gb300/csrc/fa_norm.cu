@@ -46,7 +46,7 @@ template <typename T>
 constexpr int kBwdRing = kNormThreads / 32 * kBwdStages<T> * 2 * NormRaw<T>::PIECES * 32 * 16;
 
 template <typename T, int D, bool INTER>
-__global__ void __launch_bounds__(kNormThreads, 2) fa_norm_bwd_kernel(const __grid_constant__ NormArgs p, int parts) {
+__global__ void __launch_bounds__(kNormThreads, 2) fa_norm_bwd_kernel(const __grid_constant__ NormArgs p, int most) {
     using L = NormLane<D, INTER>;
     constexpr int WARPS = kNormThreads / 32, S = kBwdStages<T>, PIECES = NormRaw<T>::PIECES;
     extern __shared__ __align__(16) uint4 rings[];
@@ -61,11 +61,14 @@ __global__ void __launch_bounds__(kNormThreads, 2) fa_norm_bwd_kernel(const __gr
     uint64_t f[L::OWN];
     lane_turns<D, INTER>(ln, turns, p.rot, f);
     uint4* ring = rings + warp * S * 2 * PIECES * 32 + lane;
-    const long long items = static_cast<long long>(p.tokens) * parts;
     const int w = blockIdx.x * WARPS + warp, nw = gridDim.x * WARPS;
     for (int ten = 0; ten < 2; ++ten) {  // q, then k: one set of sums in registers
         const NormRows rx = ten ? p.k : p.q, ru = ten ? p.k_out : p.q_out, rd = ten ? p.dk : p.dq;
         const int H = ten ? p.Hkv : p.Hq, np = (H + L::RPW - 1) / L::RPW;
+        // of this tensor's own steps: an item without one would stop the ring's
+        // cursor, which moves on behind an item's last step
+        const int parts = min(most, np);
+        const long long items = static_cast<long long>(p.tokens) * parts;
         const bool has_w = ten ? p.k_weight : p.q_weight;
         auto row = [&](const NormRows& r, const NormCursor& c) {
             return static_cast<T*>(r.data) + c.b * r.batch + (c.pass * L::RPW + ln.g) * r.head + c.n * r.token;

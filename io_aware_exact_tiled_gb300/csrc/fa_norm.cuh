@@ -281,7 +281,8 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
-// Where a warp stands among its items: steps [pass, end) of token (b, n).
+// Where a warp stands among its items: steps [pass, end) of token (b, n), one at
+// least (parts <= np, which the callers see to).
 struct NormCursor {
     long long it;
     int t, b, n, pass, end;
