@@ -8,13 +8,16 @@ namespace fa {
 
 // Angles are held as fractions of a turn in 64-bit fixed point: f / (2 pi)
 // modulo 1 once for each frequency, then position * fraction modulo 2^64, which
-// drops whole turns exactly. The fraction's last place is 2^-64, so that an
-// angle is good to 2^-33 of a turn at any 32-bit position; 64-bit floating
-// point would do as well, at a few results a cycle and SM.
+// drops whole turns exactly. The fraction is within 2^-64 (either term's
+// rounding is half of that at most), so that an angle is good to 2^-33 of a turn
+// at any 32-bit position; 64-bit floating point would do as well, at a few
+// results a cycle and SM. A negative frequency has the fraction of its opposite,
+// negated: hi - floor(hi) is exact only where hi is not negative.
 __device__ __forceinline__ uint64_t turn_fraction(double f) {
     constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;  // 1 / (2 pi)
-    const double hi = f * kHi, lo = fma(f, kLo, fma(f, kHi, -hi));
-    return __double2ull_rz((hi - floor(hi)) * 0x1p64) + static_cast<uint64_t>(__double2ll_rn(lo * 0x1p64));
+    const double a = fabs(f), hi = a * kHi, lo = fma(a, kLo, fma(a, kHi, -hi));
+    const uint64_t t = __double2ull_rn((hi - floor(hi)) * 0x1p64) + static_cast<uint64_t>(__double2ll_rn(lo * 0x1p64));
+    return f < 0. ? 0ull - t : t;
 }
 
 // Cosine and sine of `a` turns: the nearest quarter turn, and the Taylor series
