@@ -72,8 +72,12 @@ struct PtCfg {
     // part of Q takes their room: 795 us for pieces of prompts with three and two
     // stages and Q's two parts alone, 793 with these; units of one row tile have
     // one Q)
-    static constexpr int KS = D == 128 ? (ONE ? 3 : 2) : 6;
-    static constexpr int RS = D == 128 ? (ONE ? 3 : 1) : 4;
+    static constexpr int KS = D == 128 ? (ONE ? 4 : 2) : 6;
+    static constexpr int RS = D == 128 ? (ONE ? 2 : 1) : 4;
+    // Of every other tile a product warp waits for K by its stage's parity, which
+    // tells two rounds of a stage apart but not three: the tile in that stage
+    // before has to be one that the warp has waited for, so one of its own.
+    static_assert(!ONE || KS % 2 == 0, "K stages of units of one row tile");
     static constexpr int VS = 2;                  // stages of converted V
     static constexpr int NREG = D / 64;           // 128-byte-wide regions of an f16 row
     // the three parts of a row tile's Q: rows of 128 bytes, d = 64: the first

@@ -1,0 +1,79 @@
+"""CPU check of the stages of K in the row-tile kernel's units of one row tile.
+
+There every other key tile is one product warp's and the rest the other's. A
+warp waits for tile u by the parity of its stage's round, u // stages: that
+says "landed" too early while the round before has not landed yet. A warp knows
+that of its own tiles only, so the tile that had the stage before has to be one
+of its own, or of an earlier piece. All orders in which copies may land and
+warps may move are walked here."""
+
+import os
+import re
+
+import pytest
+
+SOURCE = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "io_aware_exact_tiled_gb300", "csrc",
+                      "fa_paged_tile.cu")
+
+
+def early(stages, pieces):
+    """Whether some order of events lets a wait pass before its tile landed."""
+    tiles, n = [[], []], 0                      # (tile, tiles of the pieces before) of each warp
+    for length in pieces:
+        for t in range(length):
+            tiles[t & 1].append((n + t, n))
+        n += length
+    # requested: a count, in order; landed and done: sets of tiles; at: each warp's place; passed: its wait is over
+    start = (0, frozenset(), frozenset(), (0, 0), (False, False))
+    seen, todo = {start}, [start]
+
+    def go(*state):
+        if state not in seen:
+            seen.add(state)
+            todo.append(state)
+
+    while todo:
+        requested, landed, done, at, passed = todo.pop()
+        if requested < n and (requested < stages or requested - stages in done):
+            go(requested + 1, landed, done, at, passed)
+        for u in range(requested):
+            # a stage's copies follow one another; others may overtake
+            if u not in landed:
+                go(requested, landed | {u}, done, at, passed)
+        for w in range(2):
+            if at[w] == len(tiles[w]):
+                continue
+            u, before = tiles[w][at[w]]
+            if passed[w]:                       # the products, and with them the stage's release
+                go(requested, landed, done | {u}, tuple(x + (i == w) for i, x in enumerate(at)),
+                   tuple(x and i != w for i, x in enumerate(passed)))
+                continue
+            if len([x for x in done if x < before]) < before:
+                continue                        # a piece's Q comes once both warps are through with the piece before
+            rounds = len([x for x in landed if x % stages == u % stages])
+            if rounds % 2 != (u // stages) & 1:
+                if u not in landed:
+                    return True
+                go(requested, landed, done, at, tuple(x or i == w for i, x in enumerate(passed)))
+    return False
+
+
+PIECES = [(9,), (3, 6), (1, 1, 5), (2, 1, 4), (4, 3)]
+
+
+def one_row_tile_stages():
+    with open(SOURCE) as f:
+        m = re.search(r"int KS = D == 128 \? \(ONE \? (\d+) : \d+\) : (\d+);", f.read())
+    return [int(x) for x in m.groups()]
+
+
+@pytest.mark.parametrize("pieces", PIECES)
+def test_no_wait_for_k_passes_early(pieces):
+    for stages in one_row_tile_stages():
+        assert not early(stages, pieces), stages
+
+
+def test_the_walk_finds_early_waits():
+    """With an odd number of stages the tile before in a stage is the other warp's."""
+    assert early(3, (9,)) and early(5, (9,))
+    assert not early(2, (9,)) and not early(4, (9,))
