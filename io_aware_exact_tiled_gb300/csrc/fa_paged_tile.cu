@@ -918,7 +918,7 @@ __global__ void __launch_bounds__(512, 1)
         const int i = (warp - 4) >> 2, wq = warp & 3, r = wq * 32 + lane;
         const uint32_t tl = tm + (static_cast<uint32_t>(wq * 32) << 16);
         const uint32_t tS = tl + C::COL_S + i * 128, tO = tl + C::COL_O + i * 128, tP = tl + C::COL_P + i * 128;
-        uint8_t* qb = sm + C::Q_OFF + (ONE ? 0 : i * C::Q_BYTES);  // ONE: both write the same bytes
+        uint8_t* qb = sm + C::Q_OFF + (ONE ? 0 : i * C::Q_BYTES);
         int u = 0, ns = 0, seg = 0;  // tiles walked, halves of them multiplied, pieces
         bool ok = true;
         do {
@@ -952,15 +952,27 @@ __global__ void __launch_bounds__(512, 1)
                 const int e0 = top >> 7 && !wild ? static_cast<int>(top >> 7) - 138 : 0;
                 int e = min(max(e0, -120), 120);
                 const float f = exp2i(-e);
-                // a row of few small elements leaves out little for certain
-                // (zeros count as small here)
-                const bool few = pt_split_q<D, false>(x, f, qb, r) <= 2.f || top == 0 || wild;
-                const bool fits = few || pt_two_parts_hold<D>(p.q + qrow, f);
+                // ONE: Q is the same for both row tiles. Row tile 0's warps write it,
+                // and where both take part (a piece of one key tile is row tile 0's
+                // alone) neither has its products started before it is whole.
+                const bool writes = !ONE || i == 0, both = ONE && s.c1 - s.c0 > 1;
+                bool fits = true;
+                if (writes) {
+                    // a row of few small elements leaves out little for certain
+                    // (zeros count as small here)
+                    const bool few = pt_split_q<D, false>(x, f, qb, r) <= 2.f || top == 0 || wild;
+                    fits = few || pt_two_parts_hold<D>(p.q + qrow, f);
+                }
+                if (ONE) fence_proxy_async_smem();
                 __syncwarp();
-                const bool wide = !named_all(1 + i, 128, fits);
+                const bool wide = !(both ? named_all(3, 256, fits) : named_all(1 + i, 128, fits));
                 if (wide) {  // [2^14, 2^15), three
                     e = min(max(e0 - 3, -120), 120);
-                    pt_split_q_wide<D>(row_ok ? p.q + qrow : nullptr, exp2i(-e), qb, r);
+                    if (writes) pt_split_q_wide<D>(row_ok ? p.q + qrow : nullptr, exp2i(-e), qb, r);
+                    if (both) {
+                        fence_proxy_async_smem();
+                        named_sync(3, 256);
+                    }
                 }
                 if (r == 0) wide_s[i] = wide;
                 rc = wild ? CUDART_NAN_F : p.scale_log2 * exp2i(e);  // such a row has no finite result
