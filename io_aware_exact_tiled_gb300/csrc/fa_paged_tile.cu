@@ -72,12 +72,14 @@ struct PtCfg {
     // part of Q takes their room: 795 us for pieces of prompts with three and two
     // stages and Q's two parts alone, 793 with these; units of one row tile have
     // one Q)
-    static constexpr int KS = D == 128 ? (ONE ? 4 : 2) : 6;
-    static constexpr int RS = D == 128 ? (ONE ? 2 : 1) : 4;
-    // Of every other tile a product warp waits for K by its stage's parity, which
-    // tells two rounds of a stage apart but not three: the tile in that stage
-    // before has to be one that the warp has waited for, so one of its own.
-    static_assert(!ONE || KS % 2 == 0, "K stages of units of one row tile");
+    static constexpr int KS = D == 128 ? (ONE ? 3 : 2) : 6;
+    static constexpr int RS = D == 128 ? (ONE ? 3 : 1) : 4;
+    // Barriers that tell of K's arrival, tile u's being u % KB. A wait by parity
+    // tells two rounds of a barrier apart but not three, so whoever waits for a
+    // tile has to know that the one before with its barrier has landed. ONE: a
+    // product warp knows that of every other tile, its own.
+    static constexpr int KB = ONE && KS % 2 ? 2 * KS : KS;
+    static_assert(!ONE || KB % 2 == 0, "barriers of K of units of one row tile");
     static constexpr int VS = 2;                  // stages of converted V
     static constexpr int NREG = D / 64;           // 128-byte-wide regions of an f16 row
     // the three parts of a row tile's Q: rows of 128 bytes, d = 64: the first
@@ -406,8 +408,8 @@ __global__ void __launch_bounds__(512, 1)
     uint64_t* nan_empty = nan_full + kPtNanSlots;  // [4] both row tiles' softmax warps are through with that piece
     uint64_t* sc_full = nan_empty + kPtNanSlots;   // [8] scales stored
     [[maybe_unused]] uint64_t* asked = sc_full + kPtScaleSlots;  // ONE: [8] K of a tile requested
-    uint64_t* k_full = sc_full + (ONE ? 2 : 1) * kPtScaleSlots;  // [KS]
-    uint64_t* k_empty = k_full + C::KS;        // [KS] both row tiles' S done
+    uint64_t* k_full = sc_full + (ONE ? 2 : 1) * kPtScaleSlots;  // [KB]
+    uint64_t* k_empty = k_full + C::KB;        // [KS] both row tiles' S done
     uint64_t* r_full = k_empty + C::KS;        // [RS] V landed
     uint64_t* r_empty = r_full + C::RS;        // [RS] V read
     uint64_t* v_full = r_empty + C::RS;        // [VS] V converted
@@ -431,10 +433,8 @@ __global__ void __launch_bounds__(512, 1)
             mbar_init(&sc_full[i], 1);
             if (ONE) mbar_init(&asked[i], 1);
         }
-        for (int i = 0; i < C::KS; ++i) {
-            mbar_init(&k_full[i], 1);
-            mbar_init(&k_empty[i], ONE ? 1 : 2);
-        }
+        for (int i = 0; i < C::KB; ++i) mbar_init(&k_full[i], 1);
+        for (int i = 0; i < C::KS; ++i) mbar_init(&k_empty[i], ONE ? 1 : 2);
         for (int i = 0; i < C::RS; ++i) {
             mbar_init(&r_full[i], 1);
             mbar_init(&r_empty[i], 128);
@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(512, 1)
                         cp_async_commit();
                     }
                     for (int t = s.c0; ok && t < s.c1; ++t, ++u) {
-                        const int st = u % C::KS, rs = u % C::RS;
+                        const int st = u % C::KS, kb = u % C::KB, rs = u % C::RS;
                         cp_async_wait<3>();
                         int id = has(t) ? *id_at(t) : 0;
                         if (!is_block(id)) {
@@ -611,11 +611,11 @@ __global__ void __launch_bounds__(512, 1)
                         if (!(ok = wait_warp(&k_empty[st], ((u / C::KS) & 1) ^ 1))) break;
                         if (lane == 0) {
                             mbar_arrive(&asked[u % kPtScaleSlots]);
-                            mbar_arrive_expect_tx(&k_full[st], C::K_BYTES);
+                            mbar_arrive_expect_tx(&k_full[kb], C::K_BYTES);
                         }
                         __syncwarp();
                         if (asks)
-                            tma_load_2d(sm + C::K_OFF + st * C::K_BYTES + lane * 16 * D, &tmK, 0, row, &k_full[st]);
+                            tma_load_2d(sm + C::K_OFF + st * C::K_BYTES + lane * 16 * D, &tmK, 0, row, &k_full[kb]);
                         if (!(ok = wait_warp(&r_empty[rs], ((u / C::RS) & 1) ^ 1))) {
                             klast = u + 1;
                             break;
@@ -631,9 +631,9 @@ __global__ void __launch_bounds__(512, 1)
                 // let every copy in flight land before the CTA can exit
                 if (lane == 0) {
                     const int nk = max(u, klast);
-                    for (int i = 0; i < C::KS && i < nk; ++i) {
-                        const int last = i + ((nk - 1 - i) / C::KS) * C::KS;
-                        mbar_wait_teardown(&k_full[i], (last / C::KS) & 1, 200000000ull);
+                    for (int i = 0; i < C::KB && i < nk; ++i) {
+                        const int last = i + ((nk - 1 - i) / C::KB) * C::KB;
+                        mbar_wait_teardown(&k_full[i], (last / C::KB) & 1, 200000000ull);
                     }
                     for (int i = 0; i < C::RS && i < u; ++i) {
                         const int last = i + ((u - 1 - i) / C::RS) * C::RS;
@@ -794,10 +794,10 @@ __global__ void __launch_bounds__(512, 1)
                     const int first = c0 + i;
                     u += first - c0;
                     for (int t = first; t < c1 + STEP; t += STEP, u += STEP) {
-                        const int st = u % C::KS, vs = (u - STEP) % C::VS;
+                        const int st = u % C::KS, kb = u % C::KB, vs = (u - STEP) % C::VS;
                         const bool now = t < c1, before = t > first;  // a tile of K, and one of V, of this row tile's
                         const uint64_t vd = sdesc_advance(dV, vs * C::V_BYTES), kd = sdesc_advance(dK, st * C::K_BYTES);
-                        if (now && !(ok = wait_warp(&k_full[st], (u / C::KS) & 1))) break;
+                        if (now && !(ok = wait_warp(&k_full[kb], (u / C::KB) & 1))) break;
                         if (before && !(ok = wait_warp(&v_full[vs], ((u - STEP) / C::VS) & 1))) break;
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {

@@ -1,11 +1,11 @@
 """CPU check of the stages of K in the row-tile kernel's units of one row tile.
 
 There every other key tile is one product warp's and the rest the other's. A
-warp waits for tile u by the parity of its stage's round, u // stages: that
-says "landed" too early while the round before has not landed yet. A warp knows
-that of its own tiles only, so the tile that had the stage before has to be one
-of its own, or of an earlier piece. All orders in which copies may land and
-warps may move are walked here."""
+warp waits for tile u at barrier u % barriers by the parity of its round, u //
+barriers: that says "landed" too early while the round before has not landed
+yet. A warp knows that of its own tiles only, so the tile that had the barrier
+before has to be one of its own, or of an earlier piece. All orders in which
+copies may land and warps may move are walked here."""
 
 import os
 import re
@@ -16,7 +16,7 @@ SOURCE = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))
                       "fa_paged_tile.cu")
 
 
-def early(stages, pieces):
+def early(stages, barriers, pieces):
     """Whether some order of events lets a wait pass before its tile landed."""
     tiles, n = [[], []], 0                      # (tile, tiles of the pieces before) of each warp
     for length in pieces:
@@ -50,8 +50,8 @@ def early(stages, pieces):
                 continue
             if len([x for x in done if x < before]) < before:
                 continue                        # a piece's Q comes once both warps are through with the piece before
-            rounds = len([x for x in landed if x % stages == u % stages])
-            if rounds % 2 != (u // stages) & 1:
+            rounds = len([x for x in landed if x % barriers == u % barriers])
+            if rounds % 2 != (u // barriers) & 1:
                 if u not in landed:
                     return True
                 go(requested, landed, done, at, tuple(x or i == w for i, x in enumerate(passed)))
@@ -63,17 +63,19 @@ PIECES = [(9,), (3, 6), (1, 1, 5), (2, 1, 4), (4, 3)]
 
 def one_row_tile_stages():
     with open(SOURCE) as f:
-        m = re.search(r"int KS = D == 128 \? \(ONE \? (\d+) : \d+\) : (\d+);", f.read())
-    return [int(x) for x in m.groups()]
+        text = f.read()
+    stages = re.search(r"int KS = D == 128 \? \(ONE \? (\d+) : \d+\) : (\d+);", text).groups()
+    assert "int KB = ONE && KS % 2 ? 2 * KS : KS;" in text
+    return [(int(x), int(x) * (1 + int(x) % 2)) for x in stages]
 
 
 @pytest.mark.parametrize("pieces", PIECES)
 def test_no_wait_for_k_passes_early(pieces):
-    for stages in one_row_tile_stages():
-        assert not early(stages, pieces), stages
+    for stages, barriers in one_row_tile_stages():
+        assert not early(stages, barriers, pieces), (stages, barriers)
 
 
 def test_the_walk_finds_early_waits():
-    """With an odd number of stages the tile before in a stage is the other warp's."""
-    assert early(3, (9,)) and early(5, (9,))
-    assert not early(2, (9,)) and not early(4, (9,))
+    """With an odd number of barriers the tile before at a barrier is the other warp's."""
+    assert early(3, 3, (9,)) and early(5, 5, (9,))
+    assert not early(2, 2, (9,)) and not early(4, 4, (9,)) and not early(3, 6, (9,))
