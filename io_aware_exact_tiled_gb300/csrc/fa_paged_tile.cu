@@ -71,7 +71,7 @@ struct PtCfg {
     // K stages, and stages of V as it lies in the cache (d = 128, where the third
     // part of Q takes their room: 795 us for pieces of prompts with three and two
     // stages and Q's two parts alone, 793 with these; units of one row tile have
-    // one Q)
+    // one Q there)
     static constexpr int KS = D == 128 ? (ONE ? 3 : 2) : 6;
     static constexpr int RS = D == 128 ? (ONE ? 3 : 1) : 4;
     // Barriers that tell of K's arrival, tile u's being u % KB. A wait by parity
@@ -90,8 +90,10 @@ struct PtCfg {
     }
     static constexpr int K_BYTES = 128 * D;
     static constexpr int V_BYTES = 128 * D * 2;
+    // one Q for both groups of softmax warps, where there is no room for two
+    static constexpr bool ONE_Q = ONE && D == 128;
     static constexpr int Q_OFF = 0;
-    static constexpr int K_OFF = Q_OFF + (ONE ? 1 : 2) * Q_BYTES;
+    static constexpr int K_OFF = Q_OFF + (ONE_Q ? 1 : 2) * Q_BYTES;
     static constexpr int R_OFF = K_OFF + KS * K_BYTES;
     static constexpr int V_OFF = R_OFF + RS * K_BYTES;
     static constexpr int SC_OFF = V_OFF + VS * V_BYTES;       // float [slots][24]: ks, log2 vs, 1 / vs of 8 groups
@@ -777,7 +779,7 @@ __global__ void __launch_bounds__(512, 1)
             // 450 cycles to issue, which one warp for both could not hide.
             const int i = warp - 1;
             const uint32_t leader = elect_one_sync();
-            const uint64_t dQ = sdesc_sw128(smem_u32(sm + C::Q_OFF) + (ONE ? 0 : i * C::Q_BYTES), 16, 1024);
+            const uint64_t dQ = sdesc_sw128(smem_u32(sm + C::Q_OFF) + (C::ONE_Q ? 0 : i * C::Q_BYTES), 16, 1024);
             const uint64_t dK = D == 128 ? sdesc_sw128(smem_u32(sm + C::K_OFF), 16, 1024)
                                          : sdesc_sw64(smem_u32(sm + C::K_OFF), 512);
             const uint64_t dV = sdesc_sw128(smem_u32(sm + C::V_OFF), 16384, 1024);
@@ -918,7 +920,7 @@ __global__ void __launch_bounds__(512, 1)
         const int i = (warp - 4) >> 2, wq = warp & 3, r = wq * 32 + lane;
         const uint32_t tl = tm + (static_cast<uint32_t>(wq * 32) << 16);
         const uint32_t tS = tl + C::COL_S + i * 128, tO = tl + C::COL_O + i * 128, tP = tl + C::COL_P + i * 128;
-        uint8_t* qb = sm + C::Q_OFF + (ONE ? 0 : i * C::Q_BYTES);
+        uint8_t* qb = sm + C::Q_OFF + (C::ONE_Q ? 0 : i * C::Q_BYTES);
         int u = 0, ns = 0, seg = 0;  // tiles walked, halves of them multiplied, pieces
         bool ok = true;
         do {
@@ -952,10 +954,11 @@ __global__ void __launch_bounds__(512, 1)
                 const int e0 = top >> 7 && !wild ? static_cast<int>(top >> 7) - 138 : 0;
                 int e = min(max(e0, -120), 120);
                 const float f = exp2i(-e);
-                // ONE: Q is the same for both row tiles. Row tile 0's warps write it,
-                // and where both take part (a piece of one key tile is row tile 0's
-                // alone) neither has its products started before it is whole.
-                const bool writes = !ONE || i == 0, both = ONE && s.c1 - s.c0 > 1;
+                // ONE_Q: row tile 0's warps write Q for both, and where both take
+                // part (a piece of one key tile is row tile 0's alone) neither has
+                // its products started before it is whole. (At d = 64 each has its
+                // own: six groups of drafts 85 us a call with one Q, 82 so.)
+                const bool writes = !C::ONE_Q || i == 0, both = C::ONE_Q && s.c1 - s.c0 > 1;
                 bool fits = true;
                 if (writes) {
                     // a row of few small elements leaves out little for certain
@@ -963,7 +966,7 @@ __global__ void __launch_bounds__(512, 1)
                     const bool few = pt_split_q<D, false>(x, f, qb, r) <= 2.f || top == 0 || wild;
                     fits = few || pt_two_parts_hold<D>(p.q + qrow, f);
                 }
-                if (ONE) fence_proxy_async_smem();
+                if (C::ONE_Q) fence_proxy_async_smem();
                 __syncwarp();
                 const bool wide = !(both ? named_all(3, 256, fits) : named_all(1 + i, 128, fits));
                 if (wide) {  // [2^14, 2^15), three
