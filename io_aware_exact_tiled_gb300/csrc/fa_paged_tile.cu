@@ -20,9 +20,10 @@
 //
 // A CTA holds two row tiles so that each V tile is converted once for 256
 // rows. Warps:
-//   0      copies K and V tiles by TMA, E4M3 as they lie
+//   0      copies K and V tiles by TMA, E4M3 as they lie, and their block scales
+//          (units of one row tile: without the scales)
 //   1, 2   issue the products of row tile 0, 1
-//   3      allocates TMEM, then fetches the block scales
+//   3      allocates TMEM (units of one row tile: then fetches the block scales)
 //   4-7    softmax of row tile 0: thread = row
 //   8-11   softmax of row tile 1
 //   12-15  convert V to f16: thread = key
@@ -565,212 +566,11 @@ __global__ void __launch_bounds__(512, 1)
         // nothing but TMEM to give back
     } else if (warp < 4) {
         regs_dec<96>();
-        if (ONE && (warp == 0 || warp == 3)) {
-            // A tile's loads depend on one another (block id, then scales and
-            // copies): ids come four tiles ahead and scales two, by asynchronous
-            // copies of a lane for each group of 16 keys. One warp requests the
-            // copies and another sees to the scales: together they took a warp
-            // 2,370 cycles a tile, which is what a prefix of few rows then took
-            // (64 rows behind 262,001 tokens: the kernel 190 us, 168 so). With two row
-            // tiles a tile takes longer than that.
-            const int bs = 1 << p.bs_log2, box = min(bs, 128);
-            int* ahead = reinterpret_cast<int*>(sm + C::AHEAD_OFF) + (warp == 0 ? 0 : 8 * kPtAhead);
-            auto has = [&](int t) { return lane < 8 && t < s.c1 && t * 128 + lane * 16 < s.r.len; };
-            auto id_at = [&](int t) { return ahead + (t % kPtAhead) * 8 + lane; };  // lanes 0..7
-            auto fetch_id = [&](int t) {
-                if (has(t))
-                    cp_async4(id_at(t), &p.block_table[static_cast<size_t>(s.r.b) * p.max_blocks +
-                                                       ((t * 128 + lane * 16) >> p.bs_log2)]);
-            };
-            auto is_block = [&](int id) { return id >= 0 && id < p.num_blocks; };
-            auto row_of = [&](int id, int t) {
-                return static_cast<int>(((static_cast<long long>(id) * p.Hkv + s.hk) << p.bs_log2) +
-                                        ((t * 128 + lane * 16) & (bs - 1)));
-            };
-            // the first lane of each box of min(block, 128) rows requests it
-            const bool asks = lane < 8 && lane % (box >> 4) == 0;
-            if (warp == 0) {
-                // ------------------------------------------------------ K and V tiles
-                int u = 0, klast = -1;
-                bool ok = true;
-                do {
-#pragma unroll 1
-                    for (int t = 0; t < 4; ++t) {
-                        fetch_id(s.c0 + t);
-                        cp_async_commit();
-                    }
-                    for (int t = s.c0; ok && t < s.c1; ++t, ++u) {
-                        const int st = u % C::KS, kb = u % C::KB, rs = u % C::RS;
-                        cp_async_wait<3>();
-                        int id = has(t) ? *id_at(t) : 0;
-                        if (!is_block(id)) {
-                            atomicCAS(p.status, 0, FA_DEV_INVALID | (94 << 8));
-                            id = 0;
-                        }
-                        fetch_id(t + 4);
-                        cp_async_commit();
-                        const int row = row_of(id, t);
-                        if (!(ok = wait_warp(&k_empty[st], ((u / C::KS) & 1) ^ 1))) break;
-                        if (lane == 0) {
-                            mbar_arrive(&asked[u % kPtScaleSlots]);
-                            mbar_arrive_expect_tx(&k_full[kb], C::K_BYTES);
-                        }
-                        __syncwarp();
-                        if (asks)
-                            tma_load_2d(sm + C::K_OFF + st * C::K_BYTES + lane * 16 * D, &tmK, 0, row, &k_full[kb]);
-                        if (!(ok = wait_warp(&r_empty[rs], ((u / C::RS) & 1) ^ 1))) {
-                            klast = u + 1;
-                            break;
-                        }
-                        if (lane == 0) mbar_arrive_expect_tx(&r_full[rs], C::K_BYTES);
-                        __syncwarp();
-                        if (asks)
-                            tma_load_2d(sm + C::R_OFF + rs * C::K_BYTES + lane * 16 * D, &tmV, 0, row, &r_full[rs]);
-                    }
-                    cp_async_wait<0>();
-                } while (ok && next(s));
-                if (!ok) pt_gave_up(&abort_s, p.status, 95);
-                // let every copy in flight land before the CTA can exit
-                if (lane == 0) {
-                    const int nk = max(u, klast);
-                    for (int i = 0; i < C::KB && i < nk; ++i) {
-                        const int last = i + ((nk - 1 - i) / C::KB) * C::KB;
-                        mbar_wait_teardown(&k_full[i], (last / C::KB) & 1, 200000000ull);
-                    }
-                    for (int i = 0; i < C::RS && i < u; ++i) {
-                        const int last = i + ((u - 1 - i) / C::RS) * C::RS;
-                        mbar_wait_teardown(&r_full[i], (last / C::RS) & 1, 200000000ull);
-                    }
-                }
-            } else {
-                // ------------------------------------------------------ scales
-                // A slot is written once K of its tile has been requested: the tile
-                // eight before it, whose slot it was, is then through its softmax.
-                float* raw = reinterpret_cast<float*>(ahead + 8 * kPtAhead);  // {ks, vs} [kPtAhead][8]
-                float* sc = reinterpret_cast<float*>(sm + C::SC_OFF);
-                auto fetch_scales = [&](int t) {
-                    if (!has(t)) return;
-                    const int id = *id_at(t);
-                    if (!is_block(id)) return;
-                    const size_t x = static_cast<size_t>(id) * p.Hkv + s.hk;
-                    cp_async4(raw + ((t % kPtAhead) * 8 + lane) * 2, &p.k_scale[x]);
-                    cp_async4(raw + ((t % kPtAhead) * 8 + lane) * 2 + 1, &p.v_scale[x]);
-                };
-                int u = 0;
-                bool ok = true;
-                do {
-                    float vref = 0.f;  // largest V scale met so far in this piece
-#pragma unroll 1
-                    for (int t = 0; t < 4; ++t) fetch_id(s.c0 + t);
-                    cp_async_commit();
-                    cp_async_wait<0>();
-                    fetch_scales(s.c0);
-                    cp_async_commit();
-                    fetch_scales(s.c0 + 1);
-                    cp_async_commit();
-                    for (int t = s.c0; ok && t < s.c1; ++t, ++u) {
-                        cp_async_wait<1>();
-                        float ks = 0.f, vs = 0.f;
-                        if (has(t) && is_block(*id_at(t))) {
-                            ks = raw[((t % kPtAhead) * 8 + lane) * 2];
-                            vs = raw[((t % kPtAhead) * 8 + lane) * 2 + 1];
-                        }
-                        fetch_scales(t + 2);
-                        fetch_id(t + 4);
-                        cp_async_commit();
-                        float top = vs;
-#pragma unroll
-                        for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                        vref = fmaxf(vref, top);
-                        // groups whose scale is below 2^-60 of the largest (blocks of
-                        // zeros have 2^-126) count as if it were that
-                        const float lv = fmaxf(fmaxf(log2f(vs), log2f(vref) - kPtSpan), -100.f), il = exp2f(-lv);
-                        const int slot = u % kPtScaleSlots;
-                        if (!(ok = wait_warp(&asked[slot], (u / kPtScaleSlots) & 1))) break;
-                        if (lane < 8) {
-                            sc[slot * 24 + lane] = ks;
-                            sc[slot * 24 + 8 + lane] = lv;
-                            sc[slot * 24 + 16 + lane] = il;
-                        }
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sc_full[slot]);
-                    }
-                    cp_async_wait<0>();
-                } while (ok && next(s));
-                if (!ok) pt_gave_up(&abort_s, p.status, 99);
-            }
-        } else if (warp == 0) {
-            // ------------------------------------------------------ K tiles and scales
-            const int bs = 1 << p.bs_log2, box = min(bs, 128);
-            int u = 0, klast = -1;
-            bool ok = true;
-            float* sc = reinterpret_cast<float*>(sm + C::SC_OFF);
-            do {
-                float vref = 0.f;  // largest V scale met so far in this piece
-                for (int t = s.c0; ok && t < s.c1; ++t, ++u) {
-                    const int st = u % C::KS, slot = u % kPtScaleSlots;
-                    // lane i < 8: the group of 16 keys from 16 i on
-                    int id = 0;
-                    float ks = 0.f, vs = 0.f;
-                    const int key = t * 128 + lane * 16;
-                    if (lane < 8 && key < s.r.len) {
-                        id = p.block_table[static_cast<size_t>(s.r.b) * p.max_blocks + (key >> p.bs_log2)];
-                        if (id < 0 || id >= p.num_blocks) {
-                            atomicCAS(p.status, 0, FA_DEV_INVALID | (94 << 8));
-                            id = 0;
-                        } else {
-                            ks = p.k_scale[static_cast<size_t>(id) * p.Hkv + s.hk];
-                            vs = p.v_scale[static_cast<size_t>(id) * p.Hkv + s.hk];
-                        }
-                    }
-                    if (!(ok = wait_warp(&k_empty[st], ((u / C::KS) & 1) ^ 1))) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&k_full[st], C::K_BYTES);
-                    __syncwarp();
-                    // the first lane of each box of min(block, 128) rows requests it
-                    const bool asks = lane < 8 && lane % (box >> 4) == 0;
-                    const int row = static_cast<int>(((static_cast<long long>(id) * p.Hkv + s.hk) << p.bs_log2) +
-                                                     ((t * 128 + lane * 16) & (bs - 1)));
-                    if (asks)
-                        tma_load_2d(sm + C::K_OFF + st * C::K_BYTES + lane * 16 * D, &tmK, 0, row, &k_full[st]);
-                    float top = vs;
-#pragma unroll
-                    for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    vref = fmaxf(vref, top);
-                    if (lane < 8) {
-                        // groups whose scale is below 2^-60 of the largest (blocks of
-                        // zeros have 2^-126) count as if it were that
-                        const float lv = fmaxf(fmaxf(log2f(vs), log2f(vref) - kPtSpan), -100.f);
-                        sc[slot * 24 + lane] = ks;
-                        sc[slot * 24 + 8 + lane] = lv;
-                        sc[slot * 24 + 16 + lane] = exp2f(-lv);
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sc_full[slot]);
-                    const int rs = u % C::RS;
-                    if (!(ok = wait_warp(&r_empty[rs], ((u / C::RS) & 1) ^ 1))) {
-                        klast = u + 1;
-                        break;
-                    }
-                    if (lane == 0) mbar_arrive_expect_tx(&r_full[rs], C::K_BYTES);
-                    __syncwarp();
-                    if (asks)
-                        tma_load_2d(sm + C::R_OFF + rs * C::K_BYTES + lane * 16 * D, &tmV, 0, row, &r_full[rs]);
-                }
-            } while (ok && next(s));
-            if (!ok) pt_gave_up(&abort_s, p.status, 95);
-            // let every copy in flight land before the CTA can exit
-            if (lane == 0) {
-                const int nk = max(u, klast);
-                for (int i = 0; i < C::KS && i < nk; ++i) {
-                    const int last = i + ((nk - 1 - i) / C::KS) * C::KS;
-                    mbar_wait_teardown(&k_full[i], (last / C::KS) & 1, 200000000ull);
-                }
-                for (int i = 0; i < C::RS && i < u; ++i) {
-                    const int last = i + ((u - 1 - i) / C::RS) * C::RS;
-                    mbar_wait_teardown(&r_full[i], (last / C::RS) & 1, 200000000ull);
-                }
-            }
-        } else if (warp < 3) {
+        // (In this order, and in this form: the roles' code shares the instruction
+        // cache. With the loaders first, told apart by a plain condition, prompts of
+        // 9,322 tokens over 8,192 keys, d = 64, took 443 us, 430 so; six groups of
+        // drafts 82 and 79; pieces of prompts at d = 128 778 and 773.)
+        if (warp == 1 || warp == 2) {
             // ------------------------------------------------------ products of row tile i
             // A key tile's two halves of 64 keys have S columns of their own:
             // while the softmax warps work on one half, P V and the next
@@ -913,6 +713,213 @@ __global__ void __launch_bounds__(512, 1)
             // every MMA issued so far must be complete before TMEM is released
             umma_commit(leader, &drain[i]);
             mbar_wait_teardown(&drain[i], 0, 200000000ull);
+        } else if (warp == 0 || ONE) {
+            if constexpr (ONE) {
+                // A tile's loads depend on one another (block id, then scales and
+                // copies): ids come four tiles ahead and scales two, by asynchronous
+                // copies of a lane for each group of 16 keys. One warp requests the
+                // copies and another sees to the scales: together they took a warp
+                // 2,370 cycles a tile, which is what a prefix of few rows then took
+                // (64 rows behind 262,001 tokens: the kernel 190 us, 168 so). With two row
+                // tiles a tile takes longer than that.
+                const int bs = 1 << p.bs_log2, box = min(bs, 128);
+                int* ahead = reinterpret_cast<int*>(sm + C::AHEAD_OFF) + (warp == 0 ? 0 : 8 * kPtAhead);
+                auto has = [&](int t) { return lane < 8 && t < s.c1 && t * 128 + lane * 16 < s.r.len; };
+                auto id_at = [&](int t) { return ahead + (t % kPtAhead) * 8 + lane; };  // lanes 0..7
+                auto fetch_id = [&](int t) {
+                    if (has(t))
+                        cp_async4(id_at(t), &p.block_table[static_cast<size_t>(s.r.b) * p.max_blocks +
+                                                           ((t * 128 + lane * 16) >> p.bs_log2)]);
+                };
+                auto is_block = [&](int id) { return id >= 0 && id < p.num_blocks; };
+                auto row_of = [&](int id, int t) {
+                    return static_cast<int>(((static_cast<long long>(id) * p.Hkv + s.hk) << p.bs_log2) +
+                                            ((t * 128 + lane * 16) & (bs - 1)));
+                };
+                // the first lane of each box of min(block, 128) rows requests it
+                const bool asks = lane < 8 && lane % (box >> 4) == 0;
+                if (warp == 0) {
+                    // ------------------------------------------------------ K and V tiles
+                    int u = 0, klast = -1;
+                    bool ok = true;
+                    do {
+#pragma unroll 1
+                        for (int t = 0; t < 4; ++t) {
+                            fetch_id(s.c0 + t);
+                            cp_async_commit();
+                        }
+                        for (int t = s.c0; ok && t < s.c1; ++t, ++u) {
+                            const int st = u % C::KS, kb = u % C::KB, rs = u % C::RS;
+                            cp_async_wait<3>();
+                            int id = has(t) ? *id_at(t) : 0;
+                            if (!is_block(id)) {
+                                atomicCAS(p.status, 0, FA_DEV_INVALID | (94 << 8));
+                                id = 0;
+                            }
+                            fetch_id(t + 4);
+                            cp_async_commit();
+                            const int row = row_of(id, t);
+                            if (!(ok = wait_warp(&k_empty[st], ((u / C::KS) & 1) ^ 1))) break;
+                            if (lane == 0) {
+                                mbar_arrive(&asked[u % kPtScaleSlots]);
+                                mbar_arrive_expect_tx(&k_full[kb], C::K_BYTES);
+                            }
+                            __syncwarp();
+                            if (asks)
+                                tma_load_2d(sm + C::K_OFF + st * C::K_BYTES + lane * 16 * D, &tmK, 0, row, &k_full[kb]);
+                            if (!(ok = wait_warp(&r_empty[rs], ((u / C::RS) & 1) ^ 1))) {
+                                klast = u + 1;
+                                break;
+                            }
+                            if (lane == 0) mbar_arrive_expect_tx(&r_full[rs], C::K_BYTES);
+                            __syncwarp();
+                            if (asks)
+                                tma_load_2d(sm + C::R_OFF + rs * C::K_BYTES + lane * 16 * D, &tmV, 0, row, &r_full[rs]);
+                        }
+                        cp_async_wait<0>();
+                    } while (ok && next(s));
+                    if (!ok) pt_gave_up(&abort_s, p.status, 95);
+                    // let every copy in flight land before the CTA can exit
+                    if (lane == 0) {
+                        const int nk = max(u, klast);
+                        for (int i = 0; i < C::KB && i < nk; ++i) {
+                            const int last = i + ((nk - 1 - i) / C::KB) * C::KB;
+                            mbar_wait_teardown(&k_full[i], (last / C::KB) & 1, 200000000ull);
+                        }
+                        for (int i = 0; i < C::RS && i < u; ++i) {
+                            const int last = i + ((u - 1 - i) / C::RS) * C::RS;
+                            mbar_wait_teardown(&r_full[i], (last / C::RS) & 1, 200000000ull);
+                        }
+                    }
+                } else {
+                    // ------------------------------------------------------ scales
+                    // A slot is written once K of its tile has been requested: the tile
+                    // eight before it, whose slot it was, is then through its softmax.
+                    float* raw = reinterpret_cast<float*>(ahead + 8 * kPtAhead);  // {ks, vs} [kPtAhead][8]
+                    float* sc = reinterpret_cast<float*>(sm + C::SC_OFF);
+                    auto fetch_scales = [&](int t) {
+                        if (!has(t)) return;
+                        const int id = *id_at(t);
+                        if (!is_block(id)) return;
+                        const size_t x = static_cast<size_t>(id) * p.Hkv + s.hk;
+                        cp_async4(raw + ((t % kPtAhead) * 8 + lane) * 2, &p.k_scale[x]);
+                        cp_async4(raw + ((t % kPtAhead) * 8 + lane) * 2 + 1, &p.v_scale[x]);
+                    };
+                    int u = 0;
+                    bool ok = true;
+                    do {
+                        float vref = 0.f;  // largest V scale met so far in this piece
+#pragma unroll 1
+                        for (int t = 0; t < 4; ++t) fetch_id(s.c0 + t);
+                        cp_async_commit();
+                        cp_async_wait<0>();
+                        fetch_scales(s.c0);
+                        cp_async_commit();
+                        fetch_scales(s.c0 + 1);
+                        cp_async_commit();
+                        for (int t = s.c0; ok && t < s.c1; ++t, ++u) {
+                            cp_async_wait<1>();
+                            float ks = 0.f, vs = 0.f;
+                            if (has(t) && is_block(*id_at(t))) {
+                                ks = raw[((t % kPtAhead) * 8 + lane) * 2];
+                                vs = raw[((t % kPtAhead) * 8 + lane) * 2 + 1];
+                            }
+                            fetch_scales(t + 2);
+                            fetch_id(t + 4);
+                            cp_async_commit();
+                            float top = vs;
+#pragma unroll
+                            for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                            vref = fmaxf(vref, top);
+                            // groups whose scale is below 2^-60 of the largest (blocks of
+                            // zeros have 2^-126) count as if it were that
+                            const float lv = fmaxf(fmaxf(log2f(vs), log2f(vref) - kPtSpan), -100.f), il = exp2f(-lv);
+                            const int slot = u % kPtScaleSlots;
+                            if (!(ok = wait_warp(&asked[slot], (u / kPtScaleSlots) & 1))) break;
+                            if (lane < 8) {
+                                sc[slot * 24 + lane] = ks;
+                                sc[slot * 24 + 8 + lane] = lv;
+                                sc[slot * 24 + 16 + lane] = il;
+                            }
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&sc_full[slot]);
+                        }
+                        cp_async_wait<0>();
+                    } while (ok && next(s));
+                    if (!ok) pt_gave_up(&abort_s, p.status, 99);
+                }
+            } else {
+                // ------------------------------------------------------ K and V tiles and scales
+                const int bs = 1 << p.bs_log2, box = min(bs, 128);
+                int u = 0, klast = -1;
+                bool ok = true;
+                float* sc = reinterpret_cast<float*>(sm + C::SC_OFF);
+                do {
+                    float vref = 0.f;  // largest V scale met so far in this piece
+                    for (int t = s.c0; ok && t < s.c1; ++t, ++u) {
+                        const int st = u % C::KS, slot = u % kPtScaleSlots;
+                        // lane i < 8: the group of 16 keys from 16 i on
+                        int id = 0;
+                        float ks = 0.f, vs = 0.f;
+                        const int key = t * 128 + lane * 16;
+                        if (lane < 8 && key < s.r.len) {
+                            id = p.block_table[static_cast<size_t>(s.r.b) * p.max_blocks + (key >> p.bs_log2)];
+                            if (id < 0 || id >= p.num_blocks) {
+                                atomicCAS(p.status, 0, FA_DEV_INVALID | (94 << 8));
+                                id = 0;
+                            } else {
+                                ks = p.k_scale[static_cast<size_t>(id) * p.Hkv + s.hk];
+                                vs = p.v_scale[static_cast<size_t>(id) * p.Hkv + s.hk];
+                            }
+                        }
+                        if (!(ok = wait_warp(&k_empty[st], ((u / C::KS) & 1) ^ 1))) break;
+                        if (lane == 0) mbar_arrive_expect_tx(&k_full[st], C::K_BYTES);
+                        __syncwarp();
+                        // the first lane of each box of min(block, 128) rows requests it
+                        const bool asks = lane < 8 && lane % (box >> 4) == 0;
+                        const int row = static_cast<int>(((static_cast<long long>(id) * p.Hkv + s.hk) << p.bs_log2) +
+                                                         ((t * 128 + lane * 16) & (bs - 1)));
+                        if (asks)
+                            tma_load_2d(sm + C::K_OFF + st * C::K_BYTES + lane * 16 * D, &tmK, 0, row, &k_full[st]);
+                        float top = vs;
+#pragma unroll
+                        for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        vref = fmaxf(vref, top);
+                        if (lane < 8) {
+                            // groups whose scale is below 2^-60 of the largest (blocks of
+                            // zeros have 2^-126) count as if it were that
+                            const float lv = fmaxf(fmaxf(log2f(vs), log2f(vref) - kPtSpan), -100.f);
+                            sc[slot * 24 + lane] = ks;
+                            sc[slot * 24 + 8 + lane] = lv;
+                            sc[slot * 24 + 16 + lane] = exp2f(-lv);
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sc_full[slot]);
+                        const int rs = u % C::RS;
+                        if (!(ok = wait_warp(&r_empty[rs], ((u / C::RS) & 1) ^ 1))) {
+                            klast = u + 1;
+                            break;
+                        }
+                        if (lane == 0) mbar_arrive_expect_tx(&r_full[rs], C::K_BYTES);
+                        __syncwarp();
+                        if (asks)
+                            tma_load_2d(sm + C::R_OFF + rs * C::K_BYTES + lane * 16 * D, &tmV, 0, row, &r_full[rs]);
+                    }
+                } while (ok && next(s));
+                if (!ok) pt_gave_up(&abort_s, p.status, 95);
+                // let every copy in flight land before the CTA can exit
+                if (lane == 0) {
+                    const int nk = max(u, klast);
+                    for (int i = 0; i < C::KS && i < nk; ++i) {
+                        const int last = i + ((nk - 1 - i) / C::KS) * C::KS;
+                        mbar_wait_teardown(&k_full[i], (last / C::KS) & 1, 200000000ull);
+                    }
+                    for (int i = 0; i < C::RS && i < u; ++i) {
+                        const int last = i + ((u - 1 - i) / C::RS) * C::RS;
+                        mbar_wait_teardown(&r_full[i], (last / C::RS) & 1, 200000000ull);
+                    }
+                }
+            }
         }
     } else if (warp < 12) {
         // ---------------------------------------------------------- softmax of row tile i
