@@ -707,15 +707,22 @@ fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
     return FA_OK;
 }
 
+// Where the prefixes are the row-tile kernel's and the requests' own tokens the
+// split-key kernel's, both run at once: neither fills the GPU all the time.
+static bool prefix_both(int Hq, int Hkv, int total, int max_new, int d) {
+    return fa::paged_has_tiles(total, Hq / Hkv, d) && !fa::paged_has_tiles(max_new, Hq / Hkv, d);
+}
+
 // Workspace of fa_fwd_paged_prefix: the status word, the counters of both passes,
-// the results of the prefixes' pass, then both passes' partials.
+// the results of the prefixes' pass and, where both run at once, of the own one,
+// then both passes' partials.
 struct PrefixWs {
     PagedWs prefix, own;
     size_t cuts, ml, own_ml, o, own_o, bytes;
 };
 
 static PrefixWs prefix_ws(int B, int P, int Hq, int Hkv, int total, int max_new, int d) {
-    const size_t rows = static_cast<size_t>(total) * Hq;
+    const size_t rows = static_cast<size_t>(total) * Hq, own = prefix_both(Hq, Hkv, total, max_new, d) ? rows : 0;
     const size_t up = static_cast<size_t>(fa::paged_max_tile_units(P, Hq, Hkv, total, total, d, 128));
     const size_t uo = static_cast<size_t>(fa::paged_max_tile_units(B, Hq, Hkv, total, max_new, d));
     PrefixWs w;
@@ -724,9 +731,9 @@ static PrefixWs prefix_ws(int B, int P, int Hq, int Hkv, int total, int max_new,
     w.cuts = w.own.zeroed;
     w.ml = w.cuts + align256(2 * fa::kPagedCtas * sizeof(fa::PagedCut));
     w.own_ml = w.ml + align256(rows * sizeof(float2));
-    w.o = w.own_ml + align256(rows * sizeof(float2));
+    w.o = w.own_ml + align256(own * sizeof(float2));
     w.own_o = w.o + align256(rows * d * sizeof(float));
-    paged_ws_partials(w.prefix, w.own_o + align256(rows * d * sizeof(float)), up, d, 3);
+    paged_ws_partials(w.prefix, w.own_o + align256(own * d * sizeof(float)), up, d, 3);
     paged_ws_partials(w.own, w.prefix.bytes, uo, d);
     w.bytes = w.own.bytes;
     return w;
@@ -808,16 +815,15 @@ fa_status fa_fwd_paged_prefix(const void* q, const void* k_cache, const void* v_
     a.join.groups = prefix_cu;
     a.split_rows = fa::paged_split_rows(max_new, group, d);
     paged_place(a, w.own, ws);
-    // Where the prefixes are the row-tile kernel's and the requests' own tokens the
-    // split-key kernel's, both run at once: neither fills the GPU all the time.
-    const bool both = fa::paged_has_tiles(total, group, d) && !fa::paged_has_tiles(max_new, group, d);
+    const bool both = prefix_both(Hq, Hkv, total, max_new, d);
     // Units enough that one is cut in two or three: whoever finishes last merges it (eight
     // prompts behind 8,192 tokens: 559 us a call, 584 with the merge kernel)
     pre.join.cuts = a.join.cuts;
     const long long units = static_cast<long long>(total) * group / fa::kPagedTileRows * Hkv;
     if (!both && !pre.one_tile && units >= fa::kPagedCtas / 2) pre.join.cuts = nullptr;
     a.join.cuts = nullptr;
-    if (both) fa::paged_run_both(pre, a, reinterpret_cast<float2*>(ws + w.own_ml), reinterpret_cast<float*>(ws + w.own_o));
+    if (both)
+        fa::paged_run_both(pre, a, reinterpret_cast<float2*>(ws + w.own_ml), reinterpret_cast<float*>(ws + w.own_o));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (cudaMemsetAsync(ws, 0, both ? w.o : w.ml, s) != cudaSuccess) return FA_ERR_CUDA;
     int n = 0;
