@@ -816,11 +816,12 @@ fa_status fa_fwd_paged_prefix(const void* q, const void* k_cache, const void* v_
     a.split_rows = fa::paged_split_rows(max_new, group, d);
     paged_place(a, w.own, ws);
     const bool both = prefix_both(Hq, Hkv, total, max_new, d);
-    // Units enough that one is cut in two or three: whoever finishes last merges it (eight
-    // prompts behind 8,192 tokens: 559 us a call, 584 with the merge kernel)
-    pre.join.cuts = a.join.cuts;
-    const long long units = static_cast<long long>(total) * group / fa::kPagedTileRows * Hkv;
-    if (!both && !pre.one_tile && units >= fa::kPagedCtas / 2) pre.join.cuts = nullptr;
+    // Prompts, whose units are of two row tiles and whose rows no merge has to join
+    // with the own pass's: whoever finishes a cut unit last merges it. (Prefix of 8,192
+    // tokens, 16 heads: 9,322 new tokens together 556 us a call and 581 with the merge
+    // kernel at d = 64, 714 and 758 at d = 128; 300 tokens behind 100,000, 16 heads of
+    // two key heads, d = 128: 246 and 253.)
+    pre.join.cuts = both || pre.one_tile ? a.join.cuts : nullptr;
     a.join.cuts = nullptr;
     if (both)
         fa::paged_run_both(pre, a, reinterpret_cast<float2*>(ws + w.own_ml), reinterpret_cast<float*>(ws + w.own_o));
