@@ -314,7 +314,14 @@ fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
  * included, is as for fa_fwd_paged; offsets, lengths and table entries of the
  * prefixes are checked as those of the requests are. A prefix and a request's
  * own tokens are taken apart: the limits on their v_scale are each one's own.
- * Runs up to five kernels.
+ * Where the batch has more rows together (new tokens x heads of a group) than
+ * fa_fwd_paged's limit for one request, all rows meet their prefix as rows of
+ * longer requests do there, single tokens too: v_scale is in their weights, and
+ * of their Q 2^-20 of the row's maximum may be left out in all.
+ * A prefix costs about as much for one request as for many: groups of one or two
+ * requests, or of up to eight behind some 2,000 tokens, run faster through
+ * fa_fwd_paged with the prefix's blocks in each request's table (where they are
+ * full ones). Runs up to four kernels.
  */
 size_t fa_fwd_paged_prefix_workspace_size(int B, int P, int Hq, int Hkv, int total, int max_new, int d);
 fa_status fa_fwd_paged_prefix(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,

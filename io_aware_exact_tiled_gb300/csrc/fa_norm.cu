@@ -9,8 +9,9 @@
 //
 // Bound: the heads' bytes, once in and once out. Measured, [2, 16 + 16, 16384,
 // 128] bf16: forward 98 us = 5,480 GB/s (81 % of a copy's rate; 70 % of the issue
-// slots are used), gradient 139 + 4 us = 5,800 GB/s; one token of 16 requests, 32
-// + 8 heads: 6.4 us in a graph, of which a launch alone takes 2.
+// slots are used), gradient 139 + 4 us = 5,800 GB/s, with 32 + 8 heads 126 and 172;
+// fp32 252 and 408 us = 4,265 and 3,950 GB/s; one token of 16 requests, 32 + 8
+// heads: 6.4 us in a graph, of which a launch alone takes 2.
 //
 // A warp takes one token at a time: four (d = 128) or eight heads in a step,
 // sixteen elements a lane, so that the token's angles are computed once for all

@@ -12,7 +12,7 @@
 // rounding, which waits for the run's largest value. More runs, as in a decoding
 // batch, go to a warp each, which reads its rows twice.
 //
-// Measured: 128 requests of a token, 32 + 8 heads, 9 us; four prompts of 17,400
+// Measured: 128 requests of a token, 32 + 8 heads, 10 us; four prompts of 17,400
 // tokens, 32 heads each, d = 128, blocks of 64: 220 us (874 MB: 129 at the copy
 // rate), 62 of them the queries' kernel and 158 this one, whose sixteen warps on
 // an SM issue in 48 % of the cycles. One head a CTA with its rows loaded directly

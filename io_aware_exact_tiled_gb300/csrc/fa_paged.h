@@ -89,8 +89,9 @@ struct PagedArgs {
     float* po;           // [2 * kPagedCtas][kPagedMaxRows][d]
     int* tile_counters;  // [2 * max_tile_units], of the row-tile kernel's row tiles
     int max_tile_units;
-    float *tile_pm, *tile_pl;  // [2 * kPagedCtas][kPagedTileRows]
-    float* tile_po;            // [2 * kPagedCtas][kPagedTileRows][d]
+    // [2 * kPagedCtas][kPagedTileRows] and the same [d]; the prefixes' pass has kPagedCtas
+    // more, where the two parts of a unit of one row tile lie that is whole in a CTA
+    float *tile_pm, *tile_pl, *tile_po;
     cudaEvent_t ev_begin, ev_end;  // optional, recorded around the attention kernels
     int one_tile;  // units of one row tile (the prefixes' pass)
     int chained;  // launched while the kernel before it may still run (see paged_wait_before)

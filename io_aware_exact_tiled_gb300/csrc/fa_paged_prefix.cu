@@ -15,10 +15,11 @@
 //
 // Bound: the cache's bytes, each prefix once; with many rows the products, in fact
 // the softmax. Measured (d = 128, 32 + 8 heads): 64 requests behind 32,768 tokens
-// with 2,066 of their own on average 121 us (339 MB: 50); 16 behind 262,001 171 us
+// with 2,066 of their own on average 122 us (339 MB: 50); 16 behind 262,001 173 us
 // (544 MB: 80; the softmax warps, below); 4 of 30 tokens behind 1,000 27 us, a chain
 // of latencies: scan 5, first chunk 4, merge of the warps 3, own pass and joining
-// 8. d = 64, eight prompts of 9,322 tokens together behind 8,192: 559 us.
+// 8. Eight prompts of 9,322 tokens together behind 8,192, 16 heads: 558 us at d =
+// 64 (175), 714 at d = 128 (350).
 #include <math_constants.h>
 
 #include "fa_paged_split.cuh"

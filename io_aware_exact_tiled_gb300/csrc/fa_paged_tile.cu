@@ -341,7 +341,7 @@ __device__ __forceinline__ void pt_request(const PtParams& p, int b, PtReq& r) {
 // two softmax groups and product warps, "row tiles" i below, take every other of
 // its key tiles: with few rows the time is the chain of S, softmax and P V, and
 // two chains hide one another (64 rows behind 262,001 tokens, d = 128: 228 us a
-// call with units of two row tiles, 171 so; six groups of 32 to 172 rows, d = 64:
+// call with units of two row tiles, 173 so; six groups of 32 to 172 rows, d = 64:
 // 83 and 79). What bounds it is the softmax warps' chain: a half tile takes one
 // 1,980 cycles, with 38 % of the issue slots used.
 template <int D, bool PFX, bool ONE>
